@@ -31,7 +31,11 @@ EXPORTS = ("kda_status_string", "kda_version", "kda_chunk_fwd_workspace", "kda_c
            "kda_recurrent_bwd_workspace", "kda_recurrent_bwd", "kda_chunk_bwd_workspace", "kda_chunk_bwd",
            "kda_gk_chunk_bwd_workspace", "kda_gk_chunk_bwd",
            "kda_gk_varlen_recurrent_fwd", "kda_gk_decode_step", "kda_query_device_error",
-           "kda_diag_wait_timeout")
+           "kda_diag_wait_timeout",
+           "kda_linear_chunk_fwd_workspace", "kda_linear_chunk_fwd", "kda_linear_varlen_fwd_workspace",
+           "kda_linear_varlen_fwd", "kda_linear_decode_step", "kda_linear_chunk_bwd_workspace", "kda_linear_chunk_bwd",
+           "kda_gated_norm_fwd", "kda_gated_norm_bwd_workspace", "kda_gated_norm_bwd",
+           "kda_residual_norm_fwd", "kda_residual_norm_bwd_workspace", "kda_residual_norm_bwd")
 
 
 class KdaOptions(ctypes.Structure):
@@ -154,6 +158,34 @@ def load(path: str | None = None):
         lib.kda_query_device_error.restype = I
         lib.kda_diag_wait_timeout.argtypes = [P, Z, ctypes.c_uint, P]
         lib.kda_diag_wait_timeout.restype = I
+        L = ctypes.c_long
+        LL = ctypes.c_longlong
+        lib.kda_linear_chunk_fwd_workspace.argtypes = [I] * 7
+        lib.kda_linear_chunk_fwd_workspace.restype = Z
+        lib.kda_linear_chunk_fwd.argtypes = [P, P, P, P, I, P, P, P, P, I, I, I, I, I, I, I, F, P, Z, P]
+        lib.kda_linear_chunk_fwd.restype = I
+        lib.kda_linear_varlen_fwd_workspace.argtypes = [I] * 7
+        lib.kda_linear_varlen_fwd_workspace.restype = Z
+        lib.kda_linear_varlen_fwd.argtypes = [P, P, P, P, I, P, P, P, P, P, P, I, I, I, I, I, I, I, F, P, Z, P]
+        lib.kda_linear_varlen_fwd.restype = I
+        lib.kda_linear_decode_step.argtypes = [P, P, P, P, I, P, P, P, I, I, I, I, I, I, F, P]
+        lib.kda_linear_decode_step.restype = I
+        lib.kda_linear_chunk_bwd_workspace.argtypes = [I] * 7
+        lib.kda_linear_chunk_bwd_workspace.restype = Z
+        lib.kda_linear_chunk_bwd.argtypes = [P, P, P, P, I, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, P, Z, P]
+        lib.kda_linear_chunk_bwd.restype = I
+        lib.kda_gated_norm_fwd.argtypes = [P, P, P, P, P, L, I, I, I, I, F, P]
+        lib.kda_gated_norm_fwd.restype = I
+        lib.kda_gated_norm_bwd_workspace.argtypes = [I]
+        lib.kda_gated_norm_bwd_workspace.restype = Z
+        lib.kda_gated_norm_bwd.argtypes = [P, P, P, P, P, P, P, P, L, I, I, I, I, F, P, Z, P]
+        lib.kda_gated_norm_bwd.restype = I
+        lib.kda_residual_norm_fwd.argtypes = [P, P, P, P, F, P, P, LL, LL, L, I, I, I, F, P]
+        lib.kda_residual_norm_fwd.restype = I
+        lib.kda_residual_norm_bwd_workspace.argtypes = [I]
+        lib.kda_residual_norm_bwd_workspace.restype = Z
+        lib.kda_residual_norm_bwd.argtypes = [P, P, P, P, P, P, F, P, P, P, P, L, I, I, I, F, P, Z, P]
+        lib.kda_residual_norm_bwd.restype = I
         _lib = lib
         return lib
 

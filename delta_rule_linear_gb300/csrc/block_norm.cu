@@ -1,0 +1,474 @@
+// block_norm.cu -- the norms around an attention block, fused with its gate and its residual.
+//
+// After the block, per head row of width D (gated norm):
+//     y = x r w act(g),            r = (mean(x^2) + eps)^(-1/2),   act = silu or sigmoid (or 1)
+//     t = dy act(g) w:  dx = r (t - xn mean(t xn)),  dg = dy xn w act'(g),  dw = sum dy act(g) xn
+// with xn = x r (the bracket is evaluated as eps r^2 t + r^2 (t sum' x^2 - x sum' t x) / D, the sums
+// without the element itself, whose share cancels: in a row that one element dominates the two
+// terms as written would cancel in rounded arithmetic); before the next one, per token row of width D (residual norm):
+//     x' = x + c y,   n = x' r w
+//     t = dn w:  dx = dx' + r (t - xn mean(t xn)),  dy = c dx,  dw = sum dn xn,  dc = sum dx y
+//
+// All are bound by HBM: every element is read once and written once, a row lives in registers
+// between its sum of squares and its output, and everything is computed in fp32 and rounded once.
+// A row belongs to L lanes of a warp (2 to 32, so that narrow rows still fill 16-byte loads) or
+// to a whole CTA; element e of a row is always held by the same thread, so the backward sums
+// of dw and dc stay in that thread's registers over all its rows and meet once at the end: per CTA
+// in shared memory, then over the CTAs by a second small kernel, in a fixed order (no atomics).
+#include <algorithm>
+
+#include "norm_internal.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T, int V> struct Pack;   // V consecutive elements, one or two 16-byte accesses
+template <> struct Pack<float, 8> {
+    static __device__ __forceinline__ void load(const float *p, float (&x)[8]) {
+        const float4 a = *reinterpret_cast<const float4 *>(p), b = *(reinterpret_cast<const float4 *>(p) + 1);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+    static __device__ __forceinline__ void store(float *p, const float (&x)[8]) {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+};
+template <> struct Pack<float, 4> {
+    static __device__ __forceinline__ void load(const float *p, float (&x)[4]) {
+        const float4 a = *reinterpret_cast<const float4 *>(p);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    }
+    static __device__ __forceinline__ void store(float *p, const float (&x)[4]) {
+        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+};
+template <> struct Pack<__nv_bfloat16, 8> {
+    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&x)[8]) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(u[i] << 16);
+            x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&x)[8]) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+};
+template <typename T> struct Pack<T, 1> {
+    static __device__ __forceinline__ void load(const T *p, float (&x)[1]) { x[0] = to_f32(*p); }
+    static __device__ __forceinline__ void store(T *p, const float (&x)[1]) { *p = from_f32<T>(x[0]); }
+};
+
+// Sum over the L threads of a row: lanes of a warp (L <= 32) or the whole CTA (L = blockDim).
+// `s` holds one float per warp; consecutive calls alternate between two of them.
+template <int L>
+__device__ __forceinline__ float row_sum(float x, float *s) {
+#pragma unroll
+    for (int off = (L < 32 ? L : 32) / 2; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    if constexpr (L > 32) {
+        if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
+        __syncthreads();
+        x = s[threadIdx.x & (L / 32 - 1)];
+#pragma unroll
+        for (int off = L / 64; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    }
+    return x;
+}
+
+__device__ __forceinline__ float sigmoid(float a) { return __fdividef(1.f, 1.f + __expf(-a)); }
+
+// act(a) and its derivative.  kind: 0 none, 1 silu, 2 sigmoid.
+__device__ __forceinline__ float act_of(float a, int kind) {
+    const float s = sigmoid(a);
+    return kind == 1 ? a * s : s;
+}
+
+// t - xn mean(t xn) of one element (see above), from the row's sums of x^2 and t x
+__device__ __forceinline__ float norm_back(float t, float x, float ss, float dot, float r2, float eps, float inv_d) {
+    const float ss1 = ss - __fmul_rn(x, x), dot1 = dot - __fmul_rn(t, x);
+    return r2 * fmaf(eps, t, (t * ss1 - x * dot1) * inv_d);
+}
+
+// ------------------------------------------------------------------------------ gated norm
+// L lanes per row (256 / L rows per CTA at a time), NJ packs of V elements per lane.
+template <typename T, int V, int L, int NJ>
+__global__ void __launch_bounds__(kThreads) gated_norm_fwd_kernel(GatedNorm a) {
+    constexpr int RPB = kThreads / L;
+    const int l = threadIdx.x % L;
+    const long row = blockIdx.x * (long)RPB + threadIdx.x / L;
+    const bool live = row < a.rows;
+    const long t = live ? row / a.H : 0;
+    const int h = live ? (int)(row - t * a.H) : 0;
+    const T *xp = static_cast<const T *>(a.x.p) + t * a.x.t + h * a.x.h;
+    const T *gp = static_cast<const T *>(a.g.p) + t * a.g.t + h * a.g.h;
+    T *yp = static_cast<T *>(a.y.p) + t * a.y.t + h * a.y.h;
+    float x[NJ][V], g[NJ][V], ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        const int e = (l + L * j) * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[j][i] = g[j][i] = 0.f;
+        if (live && e < a.D) {
+            Pack<T, V>::load(xp + e, x[j]);
+            if (a.act) Pack<T, V>::load(gp + e, g[j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) ss = fmaf(x[j][i], x[j][i], ss);
+    ss = row_sum<L>(ss, nullptr);
+    const float r = rsqrtf(ss * a.inv_d + a.eps);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        const int e = (l + L * j) * V;
+        if (!live || e >= a.D) continue;
+        float w[V];
+        Pack<float, V>::load(a.w + e, w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float y = x[j][i] * r * w[i];
+            if (a.act) y *= act_of(g[j][i], a.act);
+            x[j][i] = y;
+        }
+        Pack<T, V>::store(yp + e, x[j]);
+    }
+}
+
+template <typename T, int V, int L, int NJ>
+__global__ void __launch_bounds__(kThreads) gated_norm_bwd_kernel(GatedNorm a) {
+    constexpr int RPB = kThreads / L;
+    __shared__ float s_dw[RPB][L * V + 1];
+    const int l = threadIdx.x % L, rg = threadIdx.x / L;
+    float dw[NJ][V], w[NJ][V];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        const int e = (l + L * j) * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) dw[j][i] = w[j][i] = 0.f;
+        if (e < a.D) Pack<float, V>::load(a.w + e, w[j]);
+    }
+    for (long row0 = blockIdx.x * (long)RPB; row0 < a.rows; row0 += gridDim.x * (long)RPB) {
+        const long row = row0 + rg;
+        const bool live = row < a.rows;
+        const long t = live ? row / a.H : 0;
+        const int h = live ? (int)(row - t * a.H) : 0;
+        const T *xp = static_cast<const T *>(a.x.p) + t * a.x.t + h * a.x.h;
+        const T *gp = static_cast<const T *>(a.g.p) + t * a.g.t + h * a.g.h;
+        const T *dyp = static_cast<const T *>(a.dy.p) + t * a.dy.t + h * a.dy.h;
+        float x[NJ][V], g[NJ][V], dy[NJ][V], ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int e = (l + L * j) * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[j][i] = g[j][i] = dy[j][i] = 0.f;
+            if (live && e < a.D) {
+                Pack<T, V>::load(xp + e, x[j]);
+                Pack<T, V>::load(dyp + e, dy[j]);
+                if (a.act) Pack<T, V>::load(gp + e, g[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                ss = fmaf(x[j][i], x[j][i], ss);
+                const float ac = a.act ? act_of(g[j][i], a.act) : 1.f;
+                dot = fmaf(dy[j][i] * ac * w[j][i], x[j][i], dot);
+            }
+        ss = row_sum<L>(ss, nullptr);
+        dot = row_sum<L>(dot, nullptr);
+        const float r = rsqrtf(ss * a.inv_d + a.eps), r2 = r * r;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int e = (l + L * j) * V;
+            if (!live || e >= a.D) continue;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float xn = x[j][i] * r, s = a.act ? sigmoid(g[j][i]) : 1.f;
+                const float ac = a.act == 1 ? g[j][i] * s : s;
+                const float da = a.act == 1 ? s * (1.f + g[j][i] * (1.f - s)) : s * (1.f - s);
+                const float d = dy[j][i];
+                dw[j][i] = fmaf(d * ac, xn, dw[j][i]);
+                x[j][i] = r * norm_back(d * ac * w[j][i], x[j][i], ss, dot, r2, a.eps, a.inv_d);
+                g[j][i] = d * xn * w[j][i] * da;
+            }
+            Pack<T, V>::store(static_cast<T *>(a.dx.p) + t * a.dx.t + h * a.dx.h + e, x[j]);
+            if (a.act) Pack<T, V>::store(static_cast<T *>(a.dg.p) + t * a.dg.t + h * a.dg.h + e, g[j]);
+        }
+    }
+    // this CTA's share of dw, row groups in order
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < V; ++i) s_dw[rg][l * V + i] = dw[j][i];
+        __syncthreads();
+        for (int c = threadIdx.x; c < L * V; c += kThreads) {
+            const int e = L * j * V + c;
+            if (e >= a.D) continue;
+            float sum = 0.f;
+            for (int g = 0; g < RPB; ++g) sum += s_dw[g][c];
+            a.part[(size_t)blockIdx.x * a.D + e] = sum;
+        }
+    }
+}
+
+// out[c] = sum over p of part[p, c], in order: 32 columns x 8 strands of a CTA
+__global__ void __launch_bounds__(256) norm_fold_kernel(const float *part, int np, int D, float *out0, float *out1) {
+    __shared__ float s[8][33];
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
+    const int width = out1 ? 2 * D : D;
+    float sum = 0.f;
+    if (c < width)
+        for (int p = k; p < np; p += 8) sum += part[(size_t)p * width + c];
+    s[k][threadIdx.x & 31] = sum;
+    __syncthreads();
+    if (k == 0 && c < width) {
+        sum = 0.f;
+        for (int i = 0; i < 8; ++i) sum += s[i][threadIdx.x & 31];
+        (c < D ? out0 : out1)[c < D ? c : c - D] = sum;
+    }
+}
+
+// ------------------------------------------------------------------------------ residual norm
+// A row per warp (L = 32, 8 rows per CTA) or per CTA (L = threads).
+template <typename TR, typename T, int V, int L, int NJ>
+__global__ void __launch_bounds__(L > 32 ? L : kThreads) residual_norm_fwd_kernel(ResidualNorm a) {
+    constexpr int RPB = L > 32 ? 1 : kThreads / L;
+    __shared__ float s_red[L > 32 ? L / 32 : 1];
+    const int l = threadIdx.x % L;
+    const long row = blockIdx.x * (long)RPB + threadIdx.x / L;
+    const bool live = row < a.rows;
+    const TR *xp = static_cast<const TR *>(a.x) + (live ? row : 0) * a.xs;
+    const T *yp = static_cast<const T *>(a.y) + (live ? row : 0) * a.ys;
+    float z[NJ][V], ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        const int e = (l + L * j) * V;
+        float y[V], c[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[j][i] = y[i] = 0.f, c[i] = a.c;
+        if (live && e < a.D) {
+            Pack<TR, V>::load(xp + e, z[j]);
+            Pack<T, V>::load(yp + e, y);
+            if (a.cv) Pack<float, V>::load(a.cv + e, c);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[j][i] = fmaf(c[i], y[i], z[j][i]);
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) ss = fmaf(z[j][i], z[j][i], ss);
+    ss = row_sum<L>(ss, s_red);
+    const float r = rsqrtf(ss * a.inv_d + a.eps);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        const int e = (l + L * j) * V;
+        if (!live || e >= a.D) continue;
+        Pack<TR, V>::store(static_cast<TR *>(a.xo) + row * a.D + e, z[j]);
+        float w[V];
+        Pack<float, V>::load(a.w + e, w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[i] *= z[j][i] * r;
+        Pack<T, V>::store(static_cast<T *>(a.n) + row * a.D + e, w);
+    }
+}
+
+template <typename TR, typename T, int V, int L, int NJ>
+__global__ void __launch_bounds__(L > 32 ? L : kThreads) residual_norm_bwd_kernel(ResidualNorm a) {
+    constexpr int RPB = L > 32 ? 1 : kThreads / L;
+    constexpr int SW = L > 32 ? L / 32 : 1;
+    __shared__ float s_red[2][2 * SW];
+    __shared__ float s_dw[L > 32 ? 1 : RPB][L > 32 ? 1 : L * V + 1];
+    const int l = threadIdx.x % L, rg = threadIdx.x / L;
+    float dw[NJ][V], dc[NJ][V];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) dw[j][i] = dc[j][i] = 0.f;
+    int turn = 0;   // the two sums of consecutive rows use two sets of shared floats
+    for (long row0 = blockIdx.x * (long)RPB; row0 < a.rows; row0 += gridDim.x * (long)RPB, turn ^= 1) {
+        const long row = row0 + rg;
+        const bool live = row < a.rows;
+        const long rr = live ? row : 0;
+        float x[NJ][V], dn[NJ][V], dx[NJ][V], ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int e = (l + L * j) * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[j][i] = dn[j][i] = dx[j][i] = 0.f;
+            if (live && e < a.D) {
+                Pack<TR, V>::load(static_cast<const TR *>(a.x) + rr * a.xs + e, x[j]);
+                Pack<T, V>::load(static_cast<const T *>(a.dn) + rr * a.dns + e, dn[j]);
+                if (a.dxo) Pack<TR, V>::load(static_cast<const TR *>(a.dxo) + rr * a.dxs + e, dx[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int e = (l + L * j) * V;
+            float w[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) w[i] = 0.f;
+            if (e < a.D) Pack<float, V>::load(a.w + e, w);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                ss = fmaf(x[j][i], x[j][i], ss);
+                dot = fmaf(dn[j][i] * w[i], x[j][i], dot);
+            }
+        }
+        ss = row_sum<L>(ss, s_red[turn]);
+        dot = row_sum<L>(dot, s_red[turn] + SW);
+        const float r = rsqrtf(ss * a.inv_d + a.eps), r2 = r * r;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int e = (l + L * j) * V;
+            if (!live || e >= a.D) continue;
+            float w[V], c[V], y[V];
+            Pack<float, V>::load(a.w + e, w);
+#pragma unroll
+            for (int i = 0; i < V; ++i) c[i] = a.c;
+            if (a.cv) Pack<float, V>::load(a.cv + e, c);
+            if (a.y) Pack<T, V>::load(static_cast<const T *>(a.y) + rr * a.ys + e, y);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float xn = x[j][i] * r;
+                dw[j][i] = fmaf(dn[j][i], xn, dw[j][i]);
+                dx[j][i] += r * norm_back(dn[j][i] * w[i], x[j][i], ss, dot, r2, a.eps, a.inv_d);
+                if (a.y) dc[j][i] = fmaf(dx[j][i], y[i], dc[j][i]);
+                c[i] *= dx[j][i];
+            }
+            Pack<TR, V>::store(static_cast<TR *>(a.xo) + row * a.D + e, dx[j]);
+            Pack<T, V>::store(static_cast<T *>(a.n) + row * a.D + e, c);
+        }
+    }
+    const int width = a.y ? 2 * a.D : a.D;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        if (which == 1 && !a.y) break;
+        float *part = a.part + (size_t)blockIdx.x * width + which * a.D;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            if constexpr (L > 32) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int e = (l + L * j) * V + i;
+                    if (e < a.D) part[e] = which ? dc[j][i] : dw[j][i];
+                }
+            } else {
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < V; ++i) s_dw[rg][l * V + i] = which ? dc[j][i] : dw[j][i];
+                __syncthreads();
+                for (int c = threadIdx.x; c < L * V; c += kThreads) {
+                    const int e = L * j * V + c;
+                    if (e >= a.D) continue;
+                    float sum = 0.f;
+                    for (int g = 0; g < RPB; ++g) sum += s_dw[g][c];
+                    part[e] = sum;
+                }
+            }
+        }
+    }
+}
+
+template <typename T, int V, int L, int NJ>
+cudaError_t gated_go(const GatedNorm &a, bool bwd, cudaStream_t st) {
+    const long blocks = (a.rows + kThreads / L - 1) / (kThreads / L);
+    if (!bwd) {
+        if (blocks > 0x7fffffffL) return cudaErrorInvalidValue;
+        gated_norm_fwd_kernel<T, V, L, NJ><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+        return cudaGetLastError();
+    }
+    const int grid = (int)std::min(blocks, (long)norm_parts(a.sms));
+    gated_norm_bwd_kernel<T, V, L, NJ><<<grid, kThreads, 0, st>>>(a);
+    norm_fold_kernel<<<(a.D + 31) / 32, 256, 0, st>>>(a.part, grid, a.D, a.dw, nullptr);
+    return cudaGetLastError();
+}
+
+// The narrowest lane group whose 16-byte packs cover the row; whole warps with several packs
+// above that; single elements where a size or an address does not allow 16 bytes.
+template <typename T>
+cudaError_t gated_pick(const GatedNorm &a, bool vec, bool bwd, cudaStream_t st) {
+    constexpr int V = 16 / (int)sizeof(T);
+    if (vec) {
+        const int packs = a.D / V;
+        if (packs <= 4) return gated_go<T, V, 4, 1>(a, bwd, st);
+        if (packs <= 8) return gated_go<T, V, 8, 1>(a, bwd, st);
+        if (packs <= 16) return gated_go<T, V, 16, 1>(a, bwd, st);
+        if (packs <= 32) return gated_go<T, V, 32, 1>(a, bwd, st);
+        if (packs <= 64) return gated_go<T, V, 32, 2>(a, bwd, st);
+        if constexpr (V == 4)   // fp32 rows of more than 512
+            if (packs > 128) return gated_go<T, V, 32, 8>(a, bwd, st);
+        return gated_go<T, V, 32, 4>(a, bwd, st);
+    }
+    if (a.D <= 128) return gated_go<T, 1, 32, 4>(a, bwd, st);
+    if (a.D <= 256) return gated_go<T, 1, 32, 8>(a, bwd, st);
+    return gated_go<T, 1, 32, 32>(a, bwd, st);
+}
+
+template <typename TR, typename T, int V, int L, int NJ>
+cudaError_t residual_go(const ResidualNorm &a, bool bwd, cudaStream_t st) {
+    constexpr int threads = L > 32 ? L : kThreads, rpb = threads / L;
+    const long blocks = (a.rows + rpb - 1) / rpb;
+    if (!bwd) {
+        if (blocks > 0x7fffffffL) return cudaErrorInvalidValue;
+        residual_norm_fwd_kernel<TR, T, V, L, NJ><<<(unsigned)blocks, threads, 0, st>>>(a);
+        return cudaGetLastError();
+    }
+    const int grid = (int)std::min(blocks, (long)norm_parts(a.sms));
+    residual_norm_bwd_kernel<TR, T, V, L, NJ><<<grid, threads, 0, st>>>(a);
+    const int width = a.y ? 2 * a.D : a.D;
+    norm_fold_kernel<<<(width + 31) / 32, 256, 0, st>>>(a.part, grid, a.D, a.dw, a.y ? a.dc : nullptr);
+    return cudaGetLastError();
+}
+
+template <typename TR, typename T>
+cudaError_t residual_pick(const ResidualNorm &a, bool vec, bool bwd, cudaStream_t st) {
+    if (vec) {
+        const int packs = a.D / 8;
+        if (packs <= 32) return residual_go<TR, T, 8, 32, 1>(a, bwd, st);
+        if (packs <= 64) return residual_go<TR, T, 8, 32, 2>(a, bwd, st);
+        if (packs <= 256) return residual_go<TR, T, 8, 256, 1>(a, bwd, st);
+        if (packs <= 512) return residual_go<TR, T, 8, 256, 2>(a, bwd, st);
+        if (packs <= 1024) return residual_go<TR, T, 8, 512, 2>(a, bwd, st);
+        return residual_go<TR, T, 8, 512, 4>(a, bwd, st);
+    }
+    if (a.D <= 256) return residual_go<TR, T, 1, 32, 8>(a, bwd, st);
+    if (a.D <= 2048) return residual_go<TR, T, 1, 256, 8>(a, bwd, st);
+    if (a.D <= 8192) return residual_go<TR, T, 1, 512, 16>(a, bwd, st);
+    return residual_go<TR, T, 1, 512, 32>(a, bwd, st);
+}
+
+}  // namespace
+
+cudaError_t launch_gated_norm(const GatedNorm &a, bool bwd, cudaStream_t st) {
+    const int V = a.dtype == DType::BF16 ? 8 : 4;
+    bool vec = a.D % V == 0;
+    for (const NormView *v : {&a.x, &a.g, &a.y, &a.dy, &a.dx, &a.dg})
+        if (v->p && ((reinterpret_cast<uintptr_t>(v->p) & 15) || v->t % V || v->h % V)) vec = false;
+    if (reinterpret_cast<uintptr_t>(a.w) & 15) vec = false;
+    return a.dtype == DType::BF16 ? gated_pick<__nv_bfloat16>(a, vec, bwd, st) : gated_pick<float>(a, vec, bwd, st);
+}
+
+cudaError_t launch_residual_norm(const ResidualNorm &a, bool bwd, cudaStream_t st) {
+    bool vec = a.D % 8 == 0 && a.xs % 8 == 0 && a.ys % 8 == 0 && a.dns % 8 == 0 && a.dxs % 8 == 0;
+    for (const void *p : {a.x, a.y, a.dn, a.dxo, (const void *)a.xo, (const void *)a.n, (const void *)a.w, (const void *)a.cv})
+        if (reinterpret_cast<uintptr_t>(p) & 15) vec = false;
+    if (a.res == DType::F32 && a.dtype == DType::BF16) return residual_pick<float, __nv_bfloat16>(a, vec, bwd, st);
+    if (a.dtype == DType::BF16) return residual_pick<__nv_bfloat16, __nv_bfloat16>(a, vec, bwd, st);
+    return residual_pick<float, float>(a, vec, bwd, st);
+}
+
+}  // namespace kda

@@ -1,0 +1,629 @@
+// linear_scan.cu -- linear attention with a decay per head, token by token on CUDA cores:
+// the single-token step, the prefill walk for every supported type and shape, and the
+// gradients as three such walks.
+//
+//     h_t = a_t h_{t-1} + k_t v_t^T,     o_t = s h_t^T q_t,      a_t = exp(decay_t)
+//
+// The memory h [dk, dv] stays in fp32 registers: a warp holds 8 value columns of all dk rows
+// (lane l the rows l, l + 32, ...), so the update and the read-out cost 2 dk dv FMAs per token
+// and head plus one 9-shuffle sum over the lanes for 8 outputs.  Four warps share one staged
+// tile of 16 tokens.
+//
+// A walk is sequential over its tokens, so a long sequence with few heads is cut into
+// segments: a first launch leaves every segment's memory as if it started from zero, and the
+// second starts segment p from  sum_{p' < p} (decay of the segments between) local_{p'}, which
+// it adds up itself (at most kMaxSegs - 1 reads).
+//
+// Gradients (D_t = dL/dh_t, collected backwards):
+//     dq_t = s h_t do_t                                 = this walk on (q, k, v) := (do, v, k)
+//     D_t  = a_{t+1} D_{t+1} + s q_t do_t^T
+//     dv_t = D_t^T k_t                                  = the walk backwards on (k, q, do)
+//     dk_t = D_t v_t                                    = the walk backwards on (v, do, q)
+//     ddecay_t = a_t <h_{t-1}, D_t>
+//              = <h_T, dh_T> + sum_{i >= t} (q_i . dq'_i - k_i . dk'_i)
+// where ' leaves out token i's own pair: both dots then hold just what crosses token t (a term
+// of token i's own pair would have to cancel between them, and under a strong decay it is far
+// larger than the result).  The last sum runs in fp64.
+#include <algorithm>
+
+#include "linear_internal.cuh"
+
+namespace kda {
+namespace {
+
+// ------------------------------------------------------------------------------ single token
+constexpr int kStepThreads = 256;
+
+// One CTA per (request, value head): the [DK, DV] memory crosses HBM once in and once out, as
+// 16-byte accesses that are all in flight before the first is used.  Bound by that traffic: 5.8
+// to 6.4 TB/s is the part's measured copy rate, and the arithmetic (3 flops per 4 bytes) is free.
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(kStepThreads) linear_step_kernel(LinDecode a) {
+    constexpr int TPR = DV / 4, RG = kStepThreads / TPR;   // threads per row, rows per pass
+    constexpr int R = (DK + RG - 1) / RG;
+    static_assert(DK % RG == 0, "rows tile the block");
+    __shared__ float s_k[DK], s_q[DK];
+    __shared__ __align__(16) float s_red[RG][DV];
+    const int b = blockIdx.x / a.HV, hv = blockIdx.x % a.HV, hq = hv / (a.HV / a.H);
+    const int tid = threadIdx.x, cg = tid % TPR, rg = tid / TPR;
+    float *st = a.state + (size_t)blockIdx.x * DK * DV + 4 * cg;
+    float4 S[R];
+#pragma unroll
+    for (int m = 0; m < R; ++m) S[m] = __ldcs(reinterpret_cast<const float4 *>(st + (size_t)(rg + RG * m) * DV));
+    for (int i = tid; i < 2 * DK; i += kStepThreads) {
+        if (i < DK)
+            s_k[i] = to_f32(static_cast<const T *>(a.k.p)[b * a.k.b + hq * a.k.h + i]);
+        else
+            s_q[i - DK] = a.scale * to_f32(static_cast<const T *>(a.q.p)[b * a.q.b + hq * a.q.h + i - DK]);
+    }
+    const T *v = static_cast<const T *>(a.v.p) + b * a.v.b + hv * a.v.h + 4 * cg;
+    const float v0 = to_f32(v[0]), v1 = to_f32(v[1]), v2 = to_f32(v[2]), v3 = to_f32(v[3]);
+    const float al = a.g ? expf(a.g[b * a.gb + hv]) : 1.f;
+    __syncthreads();
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int m = 0; m < R; ++m) {
+        const int i = rg + RG * m;
+        const float kk = s_k[i], qq = s_q[i];
+        S[m].x = fmaf(S[m].x, al, kk * v0);
+        S[m].y = fmaf(S[m].y, al, kk * v1);
+        S[m].z = fmaf(S[m].z, al, kk * v2);
+        S[m].w = fmaf(S[m].w, al, kk * v3);
+        o.x = fmaf(S[m].x, qq, o.x);
+        o.y = fmaf(S[m].y, qq, o.y);
+        o.z = fmaf(S[m].z, qq, o.z);
+        o.w = fmaf(S[m].w, qq, o.w);
+        __stcs(reinterpret_cast<float4 *>(st + (size_t)i * DV), S[m]);
+    }
+    *reinterpret_cast<float4 *>(&s_red[rg][4 * cg]) = o;
+    __syncthreads();
+    if (tid < DV) {
+        float sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < RG; ++g) sum += s_red[g][tid];
+        static_cast<T *>(const_cast<void *>(a.o.p))[b * a.o.b + hv * a.o.h + tid] = from_f32<T>(sum);
+    }
+}
+
+// ------------------------------------------------------------------------------ token walk
+constexpr int kTile = 16;        // tokens staged at a time
+constexpr int kWalkThreads = 128;
+constexpr int kCols = 32;        // value columns of a CTA
+constexpr int kMaxSegs = 32;     // segments of a sequence (a start state adds up to 31 memories)
+constexpr int kMinSeg = 64;      // tokens of a segment at least: its launch and its start state cost about that
+
+struct Walk {
+    LinView q, k, v, x;          // roles; x: the vector of the row dots (or p = nullptr)
+    int gq, gk, gv, gx;          // value heads per head of each array
+    void *o;                     // output [.., DV] or nullptr
+    long long ob, ot, oh;
+    int o_f32;                   // the output is fp32 whatever the inputs are
+    LinDecay g;
+    LinSeqs s;
+    int rev;                     // walk the tokens from the last to the first
+    int L;                       // tokens per segment
+    float add_scale, out_scale;
+    const float *h0;
+    float *hT;
+    long long si, sj;            // strides of h0 and hT: row (q/k channel), column
+    int HV, DV;
+    float *loc, *gam;            // per (item, head): local memory [DK, DV] and decay factor
+    float *rd;                   // partial row dots [DV / 32][rows, HV] or nullptr
+    long rows;                   // token rows (stride of rd's slices)
+    WsHeader *hdr;               // no kernel here waits, so the first launch clears the error word
+};
+
+template <typename T> struct Vec;
+template <> struct Vec<float> { static constexpr int N = 4; };
+template <> struct Vec<__nv_bfloat16> { static constexpr int N = 8; };
+template <typename T> __device__ __forceinline__ void put_vec(float *dst, const uint4 &w) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<uint4 *>(dst) = w;
+    } else {
+        float4 lo, hi;
+        lo.x = __uint_as_float(w.x << 16); lo.y = __uint_as_float(w.x & 0xffff0000u);
+        lo.z = __uint_as_float(w.y << 16); lo.w = __uint_as_float(w.y & 0xffff0000u);
+        hi.x = __uint_as_float(w.z << 16); hi.y = __uint_as_float(w.z & 0xffff0000u);
+        hi.z = __uint_as_float(w.w << 16); hi.w = __uint_as_float(w.w & 0xffff0000u);
+        reinterpret_cast<float4 *>(dst)[0] = lo;
+        reinterpret_cast<float4 *>(dst)[1] = hi;
+    }
+}
+
+// OUT: the second launch (outputs, final memory); otherwise a segment's local memory.
+template <typename T, int DK, bool OUT, bool RD>
+__global__ void __launch_bounds__(kWalkThreads) linear_walk_kernel(Walk w) {
+    constexpr int R = DK / 32, VN = Vec<T>::N;
+    constexpr int QV = kTile * DK / VN;                      // 16-byte pieces of a q or k tile
+    constexpr int NQ = (QV + kWalkThreads - 1) / kWalkThreads;
+    constexpr int VV = kTile * kCols / VN;
+    static_assert(VV <= kWalkThreads, "one piece of v per thread");
+    __shared__ __align__(16) float s_q[kTile][DK], s_k[kTile][DK], s_v[kTile][kCols], s_o[kTile][kCols];
+    __shared__ float s_a[kTile], s_qk[kTile];
+
+    const int nsl = w.DV / kCols, sl = blockIdx.x % nsl, item = blockIdx.x / nsl, hv = blockIdx.y;
+    if (blockIdx.x == 0 && hv == 0 && threadIdx.x == 0) w.hdr->error = 0;
+    LinItem it;
+    if (!lin_item(w.s, w.L, item, it)) return;
+    if (!OUT && it.p == it.nseg - 1) return;                 // nobody reads the last segment's memory
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int col0 = sl * kCols, c0 = col0 + 8 * warp;
+    const int u0 = it.p * w.L, u1 = min(it.len, u0 + w.L);
+    const int b = w.s.cu ? 0 : it.n;
+    const long t_base = w.s.cu ? it.start : 0;               // token index inside batch entry b
+    auto tok = [&](int u) { return t_base + (w.rev ? it.len - 1 - u : u); };
+    const T *qp = static_cast<const T *>(w.q.p) + b * w.q.b + (hv / w.gq) * w.q.h;
+    const T *kp = static_cast<const T *>(w.k.p) + b * w.k.b + (hv / w.gk) * w.k.h;
+    const T *vp = static_cast<const T *>(w.v.p) + b * w.v.b + (hv / w.gv) * w.v.h + col0;
+    const float *gp = w.g.p ? w.g.p + b * w.g.b + hv : nullptr;
+
+    float h[R][8];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) h[r][c] = 0.f;
+    if constexpr (OUT) {
+        if (w.h0) {
+            const float *p = w.h0 + ((size_t)it.n * w.HV + hv) * DK * w.DV;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) h[r][c] = p[(lane + 32 * r) * w.si + (c0 + c) * w.sj];
+        }
+        for (int pp = 0; pp < it.p; ++pp) {                  // start state of this segment
+            const size_t slot = (size_t)(it.first + pp) * w.HV + hv;
+            const float ga = w.gam[slot];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float4 *l = reinterpret_cast<const float4 *>(w.loc + (slot * DK + lane + 32 * r) * w.DV + c0);
+                const float4 x = l[0], y = l[1];
+                h[r][0] = fmaf(h[r][0], ga, x.x); h[r][1] = fmaf(h[r][1], ga, x.y);
+                h[r][2] = fmaf(h[r][2], ga, x.z); h[r][3] = fmaf(h[r][3], ga, x.w);
+                h[r][4] = fmaf(h[r][4], ga, y.x); h[r][5] = fmaf(h[r][5], ga, y.y);
+                h[r][6] = fmaf(h[r][6], ga, y.z); h[r][7] = fmaf(h[r][7], ga, y.w);
+            }
+        }
+    }
+    // the tile after the current one, in flight
+    uint4 rq[NQ], rk[NQ], rv;
+    float ra = 0.f;
+    auto fetch = [&](int u) {
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+            const int i = tid + j * kWalkThreads, t = i / (DK / VN), e = (i % (DK / VN)) * VN;
+            rq[j] = rk[j] = make_uint4(0, 0, 0, 0);
+            if (i < QV && u + t < u1) {
+                const long row = tok(u + t);
+                if (OUT) rq[j] = *reinterpret_cast<const uint4 *>(qp + row * w.q.t + e);
+                rk[j] = *reinterpret_cast<const uint4 *>(kp + row * w.k.t + e);
+            }
+        }
+        rv = make_uint4(0, 0, 0, 0);
+        if (tid < VV) {
+            const int t = tid / (kCols / VN), e = (tid % (kCols / VN)) * VN;
+            if (u + t < u1) rv = *reinterpret_cast<const uint4 *>(vp + tok(u + t) * w.v.t + e);
+        }
+        if (tid < kTile) {
+            // the factor before token u's update: its own decay, or (backwards) that of the
+            // token visited before it
+            const int ud = w.rev ? u + tid - 1 : u + tid;
+            ra = (gp && u + tid < u1 && ud >= 0) ? gp[tok(ud) * w.g.t] : 0.f;
+        }
+    };
+    float gsum = 0.f;
+    if (u0 < u1) fetch(u0);
+    for (int u = u0; u < u1; u += kTile) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+            const int i = tid + j * kWalkThreads;
+            if (i < QV) {
+                if (OUT) put_vec<T>(&s_q[0][0] + i * VN, rq[j]);
+                put_vec<T>(&s_k[0][0] + i * VN, rk[j]);
+            }
+        }
+        if (tid < VV) put_vec<T>(&s_v[0][0] + tid * VN, rv);
+        if (tid < kTile) {
+            s_a[tid] = expf(ra);
+            gsum += ra;
+        }
+        __syncthreads();
+        if (u + kTile < u1) fetch(u + kTile);
+        const int nt = min(kTile, u1 - u);
+#pragma unroll 2
+        for (int t = 0; t < nt; ++t) {
+            const float a = s_a[t];
+            float vv[8], kk[R], acc[8];
+            *reinterpret_cast<float4 *>(vv) = *reinterpret_cast<const float4 *>(&s_v[t][8 * warp]);
+            *reinterpret_cast<float4 *>(vv + 4) = *reinterpret_cast<const float4 *>(&s_v[t][8 * warp + 4]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) kk[r] = w.add_scale * s_k[t][lane + 32 * r];
+            if constexpr (!OUT) {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) h[r][c] = fmaf(h[r][c], a, kk[r] * vv[c]);
+                continue;
+            }
+            float qq[R], qk = 0.f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) qq[r] = s_q[t][lane + 32 * r];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) acc[c] = 0.f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if constexpr (RD) qk = fmaf(qq[r], kk[r], qk);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    if constexpr (RD) {
+                        h[r][c] *= a;
+                        acc[c] = fmaf(h[r][c], qq[r], acc[c]);
+                        h[r][c] = fmaf(kk[r], vv[c], h[r][c]);
+                    } else {
+                        h[r][c] = fmaf(h[r][c], a, kk[r] * vv[c]);
+                        acc[c] = fmaf(h[r][c], qq[r], acc[c]);
+                    }
+                }
+            }
+            // sum over the lanes; lane l ends with column 4 l4 + 2 l3 + l2 (its bits)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const bool up = lane & 16;
+                const float keep = up ? acc[c + 4] : acc[c], send = up ? acc[c] : acc[c + 4];
+                acc[c] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const bool up = lane & 8;
+                const float keep = up ? acc[c + 2] : acc[c], send = up ? acc[c] : acc[c + 2];
+                acc[c] = keep + __shfl_xor_sync(0xffffffffu, send, 8);
+            }
+            {
+                const bool up = lane & 4;
+                const float keep = up ? acc[1] : acc[0], send = up ? acc[0] : acc[1];
+                acc[0] = keep + __shfl_xor_sync(0xffffffffu, send, 4);
+            }
+            acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 2);
+            acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 1);
+            if ((lane & 3) == 0)
+                s_o[t][8 * warp + ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1)] =
+                    acc[0] * w.out_scale;
+            if constexpr (RD) {
+#pragma unroll
+                for (int off = 16; off; off >>= 1) qk += __shfl_xor_sync(0xffffffffu, qk, off);
+                if (warp == 0 && lane == 0) s_qk[t] = qk * w.out_scale;
+            }
+        }
+        if constexpr (OUT) {
+            __syncthreads();
+            if constexpr (RD) {
+                // x . (output without the token's own pair), this CTA's 32 columns
+                const int t = tid >> 3, e = (tid & 7) * 4;
+                float d = 0.f;
+                if (t < nt) {
+                    const T *xp = static_cast<const T *>(w.x.p) + b * w.x.b + (hv / w.gx) * w.x.h +
+                                  tok(u + t) * w.x.t + col0 + e;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) d = fmaf(to_f32(xp[j]), s_o[t][e + j], d);
+                }
+#pragma unroll
+                for (int off = 4; off; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+                if (t < nt && (tid & 7) == 0)
+                    w.rd[(size_t)sl * w.rows * w.HV + ((size_t)(w.s.cu ? 0 : (long)it.n * w.s.T) + tok(u + t)) * w.HV +
+                         hv] = d;
+            }
+            for (int i = tid; i < nt * kCols; i += kWalkThreads) {
+                const int t = i / kCols, c = i % kCols;
+                float val = s_o[t][c];
+                if constexpr (RD) val = fmaf(s_qk[t], s_v[t][c], val);
+                const long long off = b * w.ob + tok(u + t) * w.ot + hv * w.oh + col0 + c;
+                if (w.o_f32)
+                    static_cast<float *>(w.o)[off] = val;
+                else
+                    static_cast<T *>(w.o)[off] = from_f32<T>(val);
+            }
+        }
+    }
+    if constexpr (OUT) {
+        if (w.hT && it.p == it.nseg - 1) {
+            // backwards, the first token's own decay is still due
+            const float a = (w.rev && gp && it.len > 0) ? expf(gp[tok(it.len - 1) * w.g.t]) : 1.f;
+            float *p = w.hT + ((size_t)it.n * w.HV + hv) * DK * w.DV;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) p[(lane + 32 * r) * w.si + (c0 + c) * w.sj] = a * h[r][c];
+        }
+    } else {
+        const size_t slot = (size_t)item * w.HV + hv;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float4 *l = reinterpret_cast<float4 *>(w.loc + (slot * DK + lane + 32 * r) * w.DV + c0);
+            l[0] = make_float4(h[r][0], h[r][1], h[r][2], h[r][3]);
+            l[1] = make_float4(h[r][4], h[r][5], h[r][6], h[r][7]);
+        }
+        if (sl == 0 && warp == 0) {
+#pragma unroll
+            for (int off = 16; off; off >>= 1) gsum += __shfl_xor_sync(0xffffffffu, gsum, off);
+            if (lane == 0) w.gam[slot] = expf(gsum);
+        }
+    }
+}
+
+// Tokens per segment.  Whole sequences as long as they give every SM six CTAs (what hides the
+// walk's latency); otherwise as many segments as get there, none below kMinSeg tokens.
+int walk_segment(int nseq, int HV, int nsl, long total, int max_len, bool varlen, int sms) {
+    const long ctas = (long)nseq * HV * nsl, want = 6L * sms;
+    if (max_len <= 2 * kMinSeg || ctas >= want) return std::max(max_len, 1);
+    const long tokens = varlen ? total : (long)nseq * max_len;
+    const long segs = std::max(1L, want / ((long)HV * nsl));
+    long L = (tokens + segs - 1) / segs;
+    L = std::max(L, (long)(max_len + kMaxSegs - 1) / kMaxSegs);
+    L = std::max(L, (long)kMinSeg);
+    return (int)((L + kTile - 1) / kTile * kTile);
+}
+
+template <typename T, int DK>
+cudaError_t run_walk_t(const Walk &w, long items, int max_len, cudaStream_t st) {
+    const int nsl = w.DV / kCols;
+    if (items * nsl > 0x7fffffffL) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)(items * nsl), (unsigned)w.HV);
+    if (max_len > w.L) linear_walk_kernel<T, DK, false, false><<<grid, kWalkThreads, 0, st>>>(w);
+    if (w.rd)
+        linear_walk_kernel<T, DK, true, true><<<grid, kWalkThreads, 0, st>>>(w);
+    else
+        linear_walk_kernel<T, DK, true, false><<<grid, kWalkThreads, 0, st>>>(w);
+    return cudaGetLastError();
+}
+
+cudaError_t run_walk(const Walk &w, DType dt, int DK, long items, int max_len, cudaStream_t st) {
+    if (dt == DType::BF16) {
+        switch (DK) {
+            case 32: return run_walk_t<__nv_bfloat16, 32>(w, items, max_len, st);
+            case 64: return run_walk_t<__nv_bfloat16, 64>(w, items, max_len, st);
+            default: return run_walk_t<__nv_bfloat16, 128>(w, items, max_len, st);
+        }
+    }
+    switch (DK) {
+        case 32: return run_walk_t<float, 32>(w, items, max_len, st);
+        case 64: return run_walk_t<float, 64>(w, items, max_len, st);
+        default: return run_walk_t<float, 128>(w, items, max_len, st);
+    }
+}
+
+// ------------------------------------------------------------------------------ reductions
+// ddecay from the row dots: one CTA per (batch entry, value head); every thread sums a run of
+// tokens, the runs' sums are scanned from the end, and the runs are walked again.
+constexpr int kGradThreads = 256;
+__global__ void __launch_bounds__(kGradThreads)
+linear_dgate_kernel(const float *rq, int nq, const float *rk, int nk, const float *hT, const float *dhT, float *dg,
+                    int T, int HV, int cells, long rows) {
+    __shared__ double s[kGradThreads];
+    const int b = blockIdx.x / HV, hv = blockIdx.x % HV, tid = threadIdx.x;
+    const size_t slice = (size_t)rows * HV;
+    auto at = [&](int t) {
+        const size_t i = ((size_t)b * T + t) * HV + hv;
+        double d = 0.0;
+        for (int j = 0; j < nq; ++j) d += rq[j * slice + i];
+        for (int j = 0; j < nk; ++j) d -= rk[j * slice + i];
+        return d;
+    };
+    double anchor = 0.0;
+    if (dhT)
+        for (int i = tid; i < cells; i += kGradThreads)
+            anchor += (double)hT[(size_t)blockIdx.x * cells + i] * dhT[(size_t)blockIdx.x * cells + i];
+    s[tid] = anchor;
+    __syncthreads();
+    for (int off = kGradThreads / 2; off; off >>= 1) {
+        if (tid < off) s[tid] += s[tid + off];
+        __syncthreads();
+    }
+    anchor = s[0];
+    __syncthreads();
+    const int run = (T + kGradThreads - 1) / kGradThreads, t0 = min(T, tid * run), t1 = min(T, t0 + run);
+    double mine = 0.0;
+    for (int t = t0; t < t1; ++t) mine += at(t);
+    s[tid] = mine;
+    __syncthreads();
+    for (int off = 1; off < kGradThreads; off <<= 1) {       // sums over this and the later runs
+        const double up = tid + off < kGradThreads ? s[tid + off] : 0.0;
+        __syncthreads();
+        s[tid] += up;
+        __syncthreads();
+    }
+    double acc = anchor + s[tid] - mine;
+    for (int t = t1 - 1; t >= t0; --t) {
+        acc += at(t);
+        dg[((size_t)b * T + t) * HV + hv] = (float)acc;
+    }
+}
+
+template <typename T>
+__global__ void fold_heads_kernel(const float *src, LinView dst, long n, int Tlen, int H, int m, int D) {
+    for (long i = blockIdx.x * (long)blockDim.x + threadIdx.x; i < n; i += (long)gridDim.x * blockDim.x) {
+        const int c = (int)(i % D);
+        const long rh = i / D;
+        const int h = (int)(rh % H);
+        const long row = rh / H;
+        float sum = 0.f;
+        for (int j = 0; j < m; ++j) sum += src[((row * H + h) * m + j) * D + c];
+        static_cast<T *>(const_cast<void *>(dst.p))[(row / Tlen) * dst.b + (row % Tlen) * dst.t + h * dst.h + c] =
+            from_f32<T>(sum);
+    }
+}
+
+// dst[c] = sum over the rows of src[r, c]: one CTA per column, a fixed order, fp64 sums (a
+// fixed decay's gradient adds up every token of the batch).
+__global__ void __launch_bounds__(256) sum_rows_kernel(const float *src, float *dst, long rows, int cols) {
+    __shared__ double s[256];
+    double d = 0.0;
+    for (long r = threadIdx.x; r < rows; r += 256) d += src[r * cols + blockIdx.x];
+    s[threadIdx.x] = d;
+    __syncthreads();
+    for (int off = 128; off; off >>= 1) {
+        if (threadIdx.x < off) s[threadIdx.x] += s[threadIdx.x + off];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) dst[blockIdx.x] = (float)s[0];
+}
+
+size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// bytes of the segment memories (and their decay factors) of one walk
+size_t walk_scratch(int nseq, int HV, int dk, int dv, long total, int max_len, bool varlen, int L) {
+    if (max_len <= L) return 0;
+    const size_t slots = (size_t)lin_items(nseq, total, max_len, varlen, L) * HV;
+    return round256(slots * dk * dv * 4) + round256(slots * 4);
+}
+
+}  // namespace
+
+size_t linear_scan_scratch_bytes(int nseq, int HV, int dk, int dv, long total, int max_len, bool varlen, int sms) {
+    if (varlen) {   // whatever the lengths turn out to be: the shortest segments the total allows
+        const long ctas = (long)nseq * HV * (dv / kCols), want = 6L * sms;
+        if (total <= 2 * kMinSeg || ctas >= want) return 0;
+        const long L = walk_segment(nseq, HV, dv / kCols, total, 2 * kMinSeg + 1, true, sms);
+        const size_t slots = (size_t)(total / L + nseq) * HV;
+        return round256(slots * dk * dv * 4) + round256(slots * 4);
+    }
+    return walk_scratch(nseq, HV, dk, dv, total, max_len, varlen,
+                        walk_segment(nseq, HV, dv / kCols, total, max_len, varlen, sms));
+}
+
+cudaError_t launch_linear_scan(const LinFwd &a, cudaStream_t st) {
+    Walk w{};
+    const bool varlen = a.s.cu != nullptr;
+    const int m = a.HV / a.H;
+    w.q = a.q; w.k = a.k; w.v = a.v;
+    w.gq = w.gk = m; w.gv = w.gx = 1;
+    w.o = const_cast<void *>(a.o.p); w.ob = a.o.b; w.ot = a.o.t; w.oh = a.o.h;
+    w.g = a.g; w.s = a.s; w.hdr = a.hdr;
+    w.add_scale = 1.f; w.out_scale = a.scale;
+    w.h0 = a.h0; w.hT = a.hT; w.si = a.dv; w.sj = 1;
+    w.HV = a.HV; w.DV = a.dv;
+    // in place (h_T over h_0) every CTA must own its memory: no segments
+    w.L = a.h0 && a.h0 == a.hT ? std::max(a.max_len, 1)
+                                : walk_segment(a.s.nseq, a.HV, a.dv / kCols, a.total, a.max_len, varlen, a.sms);
+    const long items = lin_items(a.s.nseq, a.total, a.max_len, varlen, w.L);
+    w.loc = static_cast<float *>(a.ws);
+    w.gam = reinterpret_cast<float *>(static_cast<char *>(a.ws) + round256((size_t)items * a.HV * a.dk * a.dv * 4));
+    return run_walk(w, a.dtype, a.dk, items, a.max_len, st);
+}
+
+cudaError_t launch_fold_heads(const float *src, const LinView &dst, DType dt, int B, int T, int H, int m, int D,
+                              cudaStream_t st) {
+    const long n = (long)B * T * H * D;
+    const int grid = (int)std::min(4096L, (n + 255) / 256);
+    if (dt == DType::BF16)
+        fold_heads_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(src, dst, n, T, H, m, D);
+    else
+        fold_heads_kernel<float><<<grid, 256, 0, st>>>(src, dst, n, T, H, m, D);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_sum_rows(const float *src, float *dst, long rows, int cols, cudaStream_t st) {
+    sum_rows_kernel<<<cols, 256, 0, st>>>(src, dst, rows, cols);
+    return cudaGetLastError();
+}
+
+// Scratch of the gradients: [segment memories of the largest walk][h_T][row dots of dq and
+// dk][per-value-head dq, dk when heads are shared][per-token ddecay when it is summed]
+size_t linear_scan_bwd_scratch_bytes(int B, int T, int H, int HV, int dk, int dv, int sms) {
+    size_t seg = 0;
+    const int dims[3][2] = {{dv, dk}, {dk, dv}, {dv, dk}};
+    for (auto &d : dims)
+        seg = std::max(seg, walk_scratch(B, HV, d[0], d[1], T, T, false,
+                                         walk_segment(B, HV, d[1] / kCols, T, T, false, sms)));
+    const size_t rows = (size_t)B * T * HV;
+    size_t n = seg + round256((size_t)B * HV * dk * dv * 4) + 2 * round256(rows * (dk / kCols) * 4) + round256(rows * 4);
+    if (HV > H) n += 2 * round256(rows * dk * 4);
+    return n;
+}
+
+cudaError_t launch_linear_scan_bwd(const LinBwd &a, cudaStream_t st) {
+    const int m = a.HV / a.H;
+    const size_t rows = (size_t)a.B * a.T * a.HV;
+    char *p = static_cast<char *>(a.ws);
+    auto carve = [&](size_t n) { char *r = p; p += round256(n); return reinterpret_cast<float *>(r); };
+    float *hT = carve((size_t)a.B * a.HV * a.dk * a.dv * 4);
+    float *rq = carve(rows * (a.dk / kCols) * 4), *rk = carve(rows * (a.dk / kCols) * 4);
+    float *dgt = carve(rows * 4);
+    float *fq = nullptr, *fk = nullptr;
+    if (m > 1) {
+        fq = carve(rows * a.dk * 4);
+        fk = carve(rows * a.dk * 4);
+    }
+    Walk w{};
+    w.hdr = a.hdr;
+    w.g = a.g; w.s.nseq = a.B; w.s.T = a.T; w.HV = a.HV;
+    w.rows = (long)a.B * a.T;
+    const bool want_g = a.g.p && a.dg;
+    auto go = [&](int DK, int DV, const LinView &out, float *f32out) {
+        w.DV = DV;
+        w.L = walk_segment(a.B, a.HV, DV / kCols, a.T, a.T, false, a.sms);
+        const long items = lin_items(a.B, a.T, a.T, false, w.L);
+        w.loc = reinterpret_cast<float *>(p);
+        w.gam = reinterpret_cast<float *>(p + round256((size_t)items * a.HV * DK * DV * 4));
+        w.o_f32 = f32out != nullptr;
+        w.o = f32out ? static_cast<void *>(f32out) : const_cast<void *>(out.p);
+        w.ob = f32out ? (long long)a.T * a.HV * DV : out.b;
+        w.ot = f32out ? (long long)a.HV * DV : out.t;
+        w.oh = f32out ? DV : out.h;
+        return run_walk(w, a.dtype, DK, items, a.T, st);
+    };
+    // dq: forwards on (do, v, k); memory transposed, [dv, dk]
+    w.q = a.d_o; w.gq = 1; w.k = a.v; w.gk = 1; w.v = a.k; w.gv = m;
+    w.x = a.q; w.gx = m; w.rd = want_g ? rq : nullptr;
+    w.add_scale = 1.f; w.out_scale = a.scale;
+    w.h0 = a.h0; w.hT = want_g && a.dhT ? hT : nullptr; w.si = 1; w.sj = a.dv;
+    cudaError_t e = go(a.dv, a.dk, a.dq, fq);
+    if (e != cudaSuccess) return e;
+    // dk: backwards on (v, do, q), memory [dv, dk]
+    w.rev = 1;
+    w.q = a.v; w.gq = 1; w.k = a.d_o; w.gk = 1; w.v = a.q; w.gv = m;
+    w.x = a.k; w.gx = m; w.rd = want_g ? rk : nullptr;
+    w.add_scale = a.scale; w.out_scale = 1.f;
+    w.h0 = a.dhT; w.hT = nullptr; w.si = 1; w.sj = a.dv;
+    if ((e = go(a.dv, a.dk, a.dk_, fk)) != cudaSuccess) return e;
+    // dv: backwards on (k, q, do), memory [dk, dv]; its final memory is the initial one's gradient
+    w.q = a.k; w.gq = m; w.k = a.q; w.gk = m; w.v = a.d_o; w.gv = 1;
+    w.x = LinView{}; w.rd = nullptr;
+    w.hT = a.dh0; w.si = a.dv; w.sj = 1;
+    if ((e = go(a.dk, a.dv, a.dv_, nullptr)) != cudaSuccess) return e;
+    if (m > 1) {
+        if ((e = launch_fold_heads(fq, a.dq, a.dtype, a.B, a.T, a.H, m, a.dk, st)) != cudaSuccess) return e;
+        if ((e = launch_fold_heads(fk, a.dk_, a.dtype, a.B, a.T, a.H, m, a.dk, st)) != cudaSuccess) return e;
+    }
+    if (want_g) {
+        const bool fixed = a.g.t == 0;
+        linear_dgate_kernel<<<a.B * a.HV, kGradThreads, 0, st>>>(rq, a.dk / kCols, rk, a.dk / kCols, hT, a.dhT,
+                                                               fixed ? dgt : a.dg, a.T, a.HV, a.dk * a.dv,
+                                                               (long)a.B * a.T);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if (fixed) e = launch_sum_rows(dgt, a.dg, (long)a.B * a.T, a.HV, st);
+    }
+    return e;
+}
+
+namespace {
+template <typename T, int DK>
+cudaError_t step_dv(const LinDecode &a, cudaStream_t st) {
+    const unsigned grid = (unsigned)(a.B * a.HV);
+    switch (a.dv) {
+        case 32: linear_step_kernel<T, DK, 32><<<grid, kStepThreads, 0, st>>>(a); break;
+        case 64: linear_step_kernel<T, DK, 64><<<grid, kStepThreads, 0, st>>>(a); break;
+        default: linear_step_kernel<T, DK, 128><<<grid, kStepThreads, 0, st>>>(a); break;
+    }
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t step_dk(const LinDecode &a, cudaStream_t st) {
+    return a.dk == 32 ? step_dv<T, 32>(a, st) : a.dk == 64 ? step_dv<T, 64>(a, st) : step_dv<T, 128>(a, st);
+}
+}  // namespace
+
+cudaError_t launch_linear_decode(const LinDecode &a, cudaStream_t st) {
+    return a.dtype == DType::BF16 ? step_dk<__nv_bfloat16>(a, st) : step_dk<float>(a, st);
+}
+
+}  // namespace kda

@@ -434,6 +434,117 @@ kda_status kda_gk_chunk_bwd(const void *q, const void *k, const void *v,
                             void *ws, size_t ws_bytes, kda_stream_t stream);
 
 /*
+ * Linear attention with a decay for each head: the recurrence above without the delta term,
+ *
+ *     h_t = exp(decay_t) h_{t-1} + k_t v_t^T,      o_t = h_t^T (scale q_t),
+ *
+ * for the layers of a model that keep a plain decayed memory.  q and k are used as given (no L2
+ * normalisation) and there is no beta.  Grouped value heads: q and k have H heads, v, o, the
+ * decay and the memories HV = m H, and value head hv reads q/k head hv / m.
+ *
+ *   q, k    [B,T,H,dk], v, o [B,T,HV,dv], KDA_F32 or KDA_BF16; dk, dv in {32, 64, 128}.
+ *   strides NULL: contiguous arrays.  Otherwise twelve element strides (batch, token, head) of
+ *           q, k, v, o in that order, each a multiple of 16 bytes (KDA_ERR_ALIGN), the last
+ *           dimension contiguous: q, k and v may be slices of one projection's output.  The
+ *           stride of a dimension of size 1 is not looked at; packed calls ignore batch strides.
+ *   decay   float32 log decays, or NULL for none: [B,T,HV], contiguous, or with decay_fixed
+ *           [HV], the same at every token.  -inf (any value below -104) forgets the memory:
+ *           a token so marked starts a new document in the same row.
+ *   initial_state, final_state   [B,HV,dk,dv] float32 (packed: [N,HV,dk,dv]) or NULL.  They may
+ *           be the same array (a long sequence is then not split over the GPU), and must not
+ *           overlap otherwise.
+ *   scale   <= 0 selects dk^-0.5.
+ *   ws      at least the query's bytes, 16-byte aligned; a kernel's bounded wait that runs out
+ *           is recorded in its header (kda_query_device_error).
+ * bf16 with dk, dv in {64, 128} runs by chunks of 128 tokens on the tensor cores (sequences of
+ * more than 32 tokens); everything else runs token by token on CUDA cores.  The results do not
+ * depend on which beyond rounding: memories and their sums are fp32 in both.  In the chunked form
+ * an infinite or NaN v or k reaches the outputs of its whole chunk.
+ * B, N, T == 0 are allowed (final_state = initial_state, or zeros).
+ */
+size_t kda_linear_chunk_fwd_workspace(int B, int T, int H, int HV, int dk, int dv, kda_dtype dtype);
+kda_status kda_linear_chunk_fwd(const void *q, const void *k, const void *v, const float *decay,
+                                int decay_fixed, const float *initial_state, void *o,
+                                float *final_state, const long long *strides, int B, int T, int H,
+                                int HV, int dk, int dv, kda_dtype dtype, float scale, void *ws,
+                                size_t ws_bytes, kda_stream_t stream);
+
+/* Packed sequences: token arrays [1,total_T,..], cu_seqlens / cu_seqlens_host as kda_varlen_fwd
+ * (the host copy also tells how to split the work), one memory per sequence. */
+size_t kda_linear_varlen_fwd_workspace(int N, int total_T, int H, int HV, int dk, int dv,
+                                       kda_dtype dtype);
+kda_status kda_linear_varlen_fwd(const void *q, const void *k, const void *v, const float *decay,
+                                 int decay_fixed, const int *cu_seqlens,
+                                 const int *cu_seqlens_host, const float *initial_state, void *o,
+                                 float *final_state, const long long *strides, int N, int total_T,
+                                 int H, int HV, int dk, int dv, kda_dtype dtype, float scale,
+                                 void *ws, size_t ws_bytes, kda_stream_t stream);
+
+/* One token for each of B requests: q, k [B,H,dk], v, o [B,HV,dv] (contiguous, or with eight
+ * strides (batch, head) of q, k, v, o: elements, any alignment of the element type), decay
+ * [B,HV], [HV] with decay_fixed, or NULL; state [B,HV,dk,dv] float32, updated in place. */
+kda_status kda_linear_decode_step(const void *q, const void *k, const void *v, const float *decay,
+                                  int decay_fixed, float *state, void *o, const long long *strides,
+                                  int B, int H, int HV, int dk, int dv, kda_dtype dtype,
+                                  float scale, kda_stream_t stream);
+
+/*
+ * Gradients of kda_linear_chunk_fwd for equal-length batches, given d_o = dL/do (dtype of q) and
+ * dfinal_state (float32 or NULL: zeros): dq, dk, dv in q's dtype (those of a shared q/k head
+ * summed over its value heads in fp32), ddecay float32 ([B,T,HV]; with decay_fixed [HV], summed over
+ * all tokens; NULL allowed; not written when decay is NULL) and dinitial_state float32 (NULL
+ * allowed).  strides: NULL or twenty-one element strides (batch, token, head) of q, k, v, d_o, dq,
+ * dk, dv, with the rules above.
+ */
+size_t kda_linear_chunk_bwd_workspace(int B, int T, int H, int HV, int dk, int dv, kda_dtype dtype);
+kda_status kda_linear_chunk_bwd(const void *q, const void *k, const void *v, const float *decay,
+                                int decay_fixed, const float *initial_state, const void *d_o,
+                                const float *dfinal_state, void *dq, void *dk_out, void *dv_out,
+                                float *ddecay, float *dinitial_state, const long long *strides,
+                                int B, int T, int H, int HV, int dk, int dv, kda_dtype dtype,
+                                float scale, void *ws, size_t ws_bytes, kda_stream_t stream);
+
+/*
+ * The norm behind an attention block, fused with its gate, per head row of width D <= 1024:
+ *     y = x (mean(x^2) + eps)^(-1/2) weight act(gate)
+ * x, gate, y [N,H,D] (N tokens; contiguous, or with six element strides (token, head) of x, gate,
+ * y), KDA_F32 or KDA_BF16; weight [D] float32.  activation 0: no gate (gate NULL), 1: silu,
+ * 2: sigmoid.  y may be x or gate (same strides).
+ * The backward writes dx, dgate (dtype of x; strides: ten, of x, gate, d_y, dx, dgate) and
+ * dweight [D] float32.  ws: at least the query's bytes.
+ */
+kda_status kda_gated_norm_fwd(const void *x, const void *gate, const float *weight, void *y,
+                              const long long *strides, long N, int H, int D, kda_dtype dtype,
+                              int activation, float eps, kda_stream_t stream);
+size_t kda_gated_norm_bwd_workspace(int D);
+kda_status kda_gated_norm_bwd(const void *d_y, const void *x, const void *gate, const float *weight,
+                              void *dx, void *dgate, float *dweight, const long long *strides,
+                              long N, int H, int D, kda_dtype dtype, int activation, float eps,
+                              void *ws, size_t ws_bytes, kda_stream_t stream);
+
+/*
+ * The residual connection fused with the norm before the next block, rows of width D <= 16384:
+ *     x_out = x + scale y,      n = x_out (mean(x_out^2) + eps)^(-1/2) weight
+ * x, x_out have dtype `res`, y, n dtype `dtype` (equal, or an fp32 residual stream around bf16
+ * blocks); weight [D] float32; the scale is scale_vec [D] float32, or the number `scale` when that
+ * is NULL.  xs, ys: row strides of x and y in elements (x_out, n contiguous).  n is computed from
+ * the unrounded sum.  x_out may be x (with xs == D).
+ * The backward takes the gradients d_n and d_x_out (NULL: zeros), x_out itself, and y where
+ * dscale [D] is wanted (else y and dscale NULL); it writes dx (dtype res), dy = scale dx (dtype) and
+ * dweight [D] (float32).  All rows contiguous.
+ */
+kda_status kda_residual_norm_fwd(const void *x, const void *y, const float *weight,
+                                 const float *scale_vec, float scale, void *x_out, void *n,
+                                 long long xs, long long ys, long N, int D, kda_dtype res,
+                                 kda_dtype dtype, float eps, kda_stream_t stream);
+size_t kda_residual_norm_bwd_workspace(int D);
+kda_status kda_residual_norm_bwd(const void *d_n, const void *d_x_out, const void *x_out,
+                                 const void *y, const float *weight, const float *scale_vec,
+                                 float scale, void *dx, void *dy, float *dweight, float *dscale,
+                                 long N, int D, kda_dtype res, kda_dtype dtype, float eps, void *ws,
+                                 size_t ws_bytes, kda_stream_t stream);
+
+/*
  * Read the device error word that the kernels of the most recent kda_chunk_fwd /
  * kda_varlen_fwd call on `ws` recorded (KDA_OK if none), then clear it.  Each of
  * those calls clears the word on its stream before its kernels run.  ws == NULL reads

@@ -1,0 +1,252 @@
+"""Linear attention with a decay per head on the GPU against the fp64 token recurrence."""
+import numpy as np
+import pytest
+
+import _linear_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def kda():
+    import delta_rule_linear_gb300 as m
+    m.load()
+    return m
+
+
+def _t(x, dt):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(x)).to("cuda", dt)
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _dt(name):
+    import torch
+    return torch.bfloat16 if name == "bf16" else torch.float32
+
+
+def _make(B, T, H, m, dk, dv, dtype, decay="mild", h0=True, seed=0):
+    """Inputs on the GPU and as the fp64 values they hold."""
+    import torch
+    r = np.random.default_rng(seed)
+    dt = _dt(dtype)
+    d = dict(q=_t(r.normal(size=(B, T, H, dk)), dt), k=_t(r.normal(size=(B, T, H, dk)), dt),
+             v=_t(r.normal(size=(B, T, H * m, dv)), dt), d_o=_t(r.normal(size=(B, T, H * m, dv)), dt))
+    z = np.abs(r.normal(size=(B, T, H * m)))
+    g = dict(mild=-0.05 * z, strong=-3.0 * z, none=None, fixed=-0.03 * z[0, 0] if T and B else -0.03 * np.ones(H * m),
+             grow=0.02 * (z - 1.0))[decay if decay != "reset" else "mild"]
+    if decay == "reset":
+        g = np.where(r.random(g.shape) < 0.1, -np.inf, g)
+    d["decay"] = None if g is None else _t(g, torch.float32)
+    d["h0"] = _t(r.normal(size=(B, H * m, dk, dv)), torch.float32) if h0 else None
+    d["dhT"] = _t(r.normal(size=(B, H * m, dk, dv)), torch.float32)
+    return d, {n: None if t is None else _np(t) for n, t in d.items()}
+
+
+def _tc(dtype, dk, dv, T):
+    return dtype == "bf16" and dk >= 64 and dv >= 64 and T > 32
+
+
+def _check_fwd(o, h, n, dtype, dk, dv, T):
+    ro, rh = ref.forward(n["q"], n["k"], n["v"], n["decay"], n["h0"])
+    assert ref.frob(_np(o), ro) <= (ref.F32 if dtype == "f32" else ref.BF16_O)
+    assert ref.frob(_np(h), rh) <= (ref.TC_STATE if _tc(dtype, dk, dv, T) else ref.F32)
+
+
+SHAPES = [
+    (1, 1, 1, 1, 32, 32), (2, 5, 3, 1, 32, 64), (1, 45, 2, 1, 32, 32), (1, 33, 2, 1, 64, 64), (2, 127, 1, 2, 64, 128),
+    (1, 128, 2, 1, 128, 128), (1, 129, 1, 3, 128, 64), (3, 300, 2, 1, 64, 64), (1, 517, 1, 1, 128, 128), (1, 600, 1, 1, 64, 32),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_chunk_fwd(kda, shape, dtype):
+    B, T, H, m, dk, dv = shape
+    d, n = _make(*shape, dtype)
+    o, h = kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], check_device=True)
+    assert o.dtype == d["q"].dtype
+    _check_fwd(o, h, n, dtype, dk, dv, T)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("decay", ["none", "fixed", "strong", "reset", "grow"])
+def test_chunk_fwd_decays(kda, decay, dtype):
+    shape = (2, 261, 1, 2, 64, 64)
+    d, n = _make(*shape, dtype, decay=decay, h0=decay != "none")
+    o, h = kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], check_device=True)
+    _check_fwd(o, h, n, dtype, 64, 64, 261)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [700, 3000])
+def test_chunk_fwd_split_sequences(kda, T, dtype):
+    """One head alone: the sequence is split into segments."""
+    d, n = _make(1, T, 1, 1, 64, 64, dtype, decay="mild")
+    o, h = kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], check_device=True)
+    _check_fwd(o, h, n, dtype, 64, 64, T)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_in_place_memory_gives_the_same(kda, dtype):
+    d, n = _make(1, 900, 1, 1, 128, 128, dtype)
+    st = d["h0"].clone()
+    o, h = kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["decay"], st, final_state=st, check_device=True)
+    assert h is st
+    _check_fwd(o, h, n, dtype, 128, 128, 900)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [20, 200])
+def test_strided_views_equal_contiguous(kda, T, dtype):
+    """q, k, v as slices of one projection, the output as a slice, heads before tokens."""
+    import torch
+    d, _ = _make(2, T, 2, 1, 64, 64, dtype)
+    z = torch.cat([d[x].flatten(2) for x in ("q", "k", "v")], -1)
+    q, k, v = (z[..., i * 128:(i + 1) * 128].unflatten(-1, (2, 64)) for i in range(3))
+    assert not q.is_contiguous()
+    o0, h0 = kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["decay"], d["h0"])
+    big = torch.zeros(2, T, 3, 64, dtype=d["q"].dtype, device="cuda")
+    o1, h1 = kda.linear_chunk_fwd(q, k, v, d["decay"], d["h0"], out=big[:, :, :2])
+    assert torch.equal(o0, o1) and torch.equal(h0, h1) and not big[:, :, 2].any()
+    kt = d["k"].transpose(1, 2).contiguous().transpose(1, 2)
+    o2, _ = kda.linear_chunk_fwd(q, kt, v, d["decay"], d["h0"])
+    assert torch.equal(o0, o2)
+    g0 = kda.linear_chunk_bwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], d["d_o"], d["dhT"])
+    g1 = kda.linear_chunk_bwd(q, kt, v, d["decay"], d["h0"], d["d_o"], d["dhT"])
+    assert all(torch.equal(g0[x], g1[x]) for x in g0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("host", [False, True])
+@pytest.mark.parametrize("lens", [[5], [0, 40, 1, 0, 130], [300, 17, 64, 128, 129], [1000, 3], [2] * 70 + [400]], ids=str)
+def test_varlen_equals_separate_sequences(kda, lens, host, dtype):
+    import torch
+    total = sum(lens)
+    d, n = _make(1, total, 1, 2, 64, 64, dtype, h0=False, seed=4)
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    h0 = np.random.default_rng(5).normal(size=(len(lens), 2, 64, 64))
+    h0t = _t(h0, torch.float32)
+    # what lies behind a sequence's end belongs to another one: it may hold anything
+    o, h = kda.linear_varlen_fwd(d["q"], d["k"], d["v"], _t(cu, torch.int32), d["decay"], h0t,
+                                 cu_seqlens_cpu=torch.from_numpy(cu) if host else None, check_device=True)
+    ro, rh = np.zeros(o.shape), np.zeros(h.shape)
+    for i, (a, b) in enumerate(zip(cu, cu[1:])):
+        oo, hh = ref.forward(n["q"][:, a:b], n["k"][:, a:b], n["v"][:, a:b], n["decay"][:, a:b], _np(h0t[i:i + 1]))
+        ro[:, a:b], rh[i] = oo, hh[0]
+    assert ref.frob(_np(o), ro) <= (ref.F32 if dtype == "f32" else ref.BF16_O)
+    assert ref.frob(_np(h), rh) <= (ref.TC_STATE if dtype == "bf16" else ref.F32)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_varlen_neighbours_do_not_leak(kda, dtype):
+    """NaN and infinities in one packed sequence leave the others finite and unchanged."""
+    import torch
+    lens = [150, 70, 200]
+    cu = _t(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32), torch.int32)
+    d, _ = _make(1, 420, 1, 1, 64, 64, dtype, h0=False)
+    o0, h0 = kda.linear_varlen_fwd(d["q"], d["k"], d["v"], cu, d["decay"])
+    for x, bad in (("q", float("inf")), ("k", float("nan")), ("v", float("nan"))):
+        d[x][:, 150:220] = bad
+    o1, h1 = kda.linear_varlen_fwd(d["q"], d["k"], d["v"], cu, d["decay"])
+    keep = [slice(0, 150), slice(220, 420)]
+    assert all(torch.equal(o0[:, s], o1[:, s]) for s in keep)
+    assert torch.equal(h0[0], h1[0]) and torch.equal(h0[2], h1[2])
+    assert not torch.isfinite(o1[:, 150:220]).all()
+
+
+def test_empty_calls(kda):
+    import torch
+    d, _ = _make(2, 0, 2, 1, 64, 64, "bf16")
+    o, h = kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["decay"], d["h0"])
+    assert o.shape == (2, 0, 2, 64) and torch.equal(h, d["h0"])
+    g = kda.linear_chunk_bwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], d["d_o"], d["dhT"])
+    assert torch.equal(g["dh0"], d["dhT"])
+    o, h = kda.linear_chunk_fwd(d["q"][:0], d["k"][:0], d["v"][:0], d["decay"][:0])
+    assert h.shape == (0, 2, 64, 64)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,m,dk,dv", [(1, 1, 1, 32, 32), (3, 2, 2, 128, 64), (5, 1, 3, 64, 128), (2, 3, 1, 32, 128),
+                                         (4, 2, 1, 128, 32)])
+def test_decode_steps_equal_prefill(kda, B, H, m, dk, dv, dtype):
+    d, n = _make(B, 6, H, m, dk, dv, dtype)
+    st = d["h0"].clone()
+    ro, rh = ref.forward(n["q"], n["k"], n["v"], n["decay"], n["h0"])
+    got = [kda.linear_decode_step(d["q"][:, t:t + 1], d["k"][:, t:t + 1], d["v"][:, t:t + 1],
+                                  d["decay"][:, t].contiguous(), st) for t in range(6)]
+    o = np.concatenate([_np(x) for x in got], 1)
+    assert ref.frob(o, ro) <= (ref.F32 if dtype == "f32" else ref.U8 + ref.F32)
+    assert ref.frob(_np(st), rh) <= ref.F32
+
+
+def test_decode_without_and_with_fixed_decay(kda):
+    import torch
+    d, n = _make(2, 1, 2, 1, 64, 64, "f32")
+    fixed = _t(np.array([-0.5, -np.inf]), torch.float32)
+    for dec in (None, fixed):
+        st = d["h0"].clone()
+        o = kda.linear_decode_step(d["q"][:, 0], d["k"][:, 0], d["v"][:, 0], dec, st)
+        ro, rh = ref.forward(n["q"], n["k"], n["v"], None if dec is None else _np(dec), n["h0"])
+        assert ref.frob(_np(o), ro[:, 0]) <= ref.F32 and ref.frob(_np(st), rh) <= ref.F32
+
+
+def _check_bwd(got, n, dtype, dk, dv, T, h0, fixed=False):
+    want = ref.backward(n["q"], n["k"], n["v"], n["decay"], n["h0"] if h0 else None, n["d_o"], n["dhT"])
+    tc = _tc(dtype, dk, dv, T)
+    for x in ("dq", "dk", "dv"):
+        assert ref.frob(_np(got[x]), want[x]) <= (ref.F32 if dtype == "f32" else ref.BF16_GRAD), x
+    if n["decay"] is not None:
+        w = want["ddecay"].sum((0, 1)) if fixed else want["ddecay"]
+        assert ref.frob(_np(got["ddecay"]), w) <= (ref.TC_DDECAY if tc else ref.F32)
+    else:
+        assert "ddecay" not in got
+    if h0:
+        assert ref.frob(_np(got["dh0"]), want["dh0"]) <= (ref.TC_STATE if tc else ref.F32)
+    else:
+        assert "dh0" not in got
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_chunk_bwd(kda, shape, dtype):
+    B, T, H, m, dk, dv = shape
+    d, n = _make(*shape, dtype, seed=2)
+    got = kda.linear_chunk_bwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], d["d_o"], d["dhT"], check_device=True)
+    assert got["dq"].dtype == d["q"].dtype and got["ddecay"].shape == d["decay"].shape
+    _check_bwd(got, n, dtype, dk, dv, T, True)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("decay", ["none", "fixed", "strong", "reset", "grow"])
+def test_chunk_bwd_decays(kda, decay, dtype):
+    d, n = _make(2, 261, 1, 2, 64, 64, dtype, decay=decay, h0=False, seed=3)
+    got = kda.linear_chunk_bwd(d["q"], d["k"], d["v"], d["decay"], None, d["d_o"], d["dhT"], check_device=True)
+    _check_bwd(got, n, dtype, 64, 64, 261, False, fixed=decay == "fixed")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_chunk_bwd_long_and_without_final_gradient(kda, dtype):
+    d, n = _make(1, 1500, 1, 1, 128, 128, dtype, seed=6)
+    n["dhT"] = None
+    got = kda.linear_chunk_bwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], d["d_o"], check_device=True)
+    _check_bwd(got, n, dtype, 128, 128, 1500, True)
+
+
+def test_other_stream_and_repeat(kda):
+    """Calls on a side stream give the same bits, run after run."""
+    import torch
+    d, _ = _make(1, 700, 2, 1, 128, 128, "bf16")
+    o0, h0 = kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["decay"], d["h0"])
+    g0 = kda.linear_chunk_bwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], d["d_o"], d["dhT"])
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        o1, h1 = kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], stream=s)
+        g1 = kda.linear_chunk_bwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], d["d_o"], d["dhT"], stream=s)
+        s.synchronize()
+        assert torch.equal(o0, o1) and torch.equal(h0, h1)
+        assert all(torch.equal(g0[x], g1[x]) for x in g0)
