@@ -1,8 +1,958 @@
+// linear_tc.cu -- linear attention with a decay per head on the tcgen05 tensor cores: bf16,
+// dk, dv in {64, 128}, chunks of C = 128 tokens.
+//
+// With G the running sum of the chunk's log decays (G_C its total), per (sequence, value head):
+//
+//     O = diag(e^G) Q S  +  P V,         P[i][j] = (q_i . k_j) e^{G_i - G_j}   (j <= i)
+//     S_next = e^{G_C} S + K^T (diag(e^{G_C - G}) V)
+//
+// One CTA walks the chunks of one (sequence, head) or of one segment of it; the memory stays in TMEM in
+// fp32 as S^T [dv, dk].  Per chunk four products of M = 128 rows (tokens, or value channels):
+//
+//     1  scores = Q K^T                     (operands as TMA writes them)
+//     2  O = Q S_bf16                       (S rounded to a bf16 operand in shared memory)
+//     3  O += P V                           (P written back to TMEM as the A operand)
+//     4  S^T += Vw^T K,  Vw = hi + mid + lo (three products; Vw^T written to TMEM as the A operand)
+//
+// What is rounded: P and the operand copy of S to bf16, each once, so O errs by three bf16
+// roundings with its own (2.3e-3 of it, against 1.7e-3 for the last one alone); the memory itself
+// must not, since a model carries it over tens of thousands of tokens and reads it back in fp32: the
+// decayed values w v go in as the sum of three bf16s, which is w v as fp32 has it (two parts, 16
+// bits, leave 2.4e-6 in the memory), k is exact, and S accumulates in fp32.
+//
+// Bound: 2 (2 dk + 2 dv) bytes per token and head through HBM; per chunk of d = 128 that is 128 KB,
+// 5900 clocks of an SM's share at the measured 6.8 TB/s.  What the CTA itself is short of is shared-memory
+// bandwidth (a product with both operands there reads 8 KB per 16 of K) and instruction
+// fetch: so the two products that can take their A operand from TMEM do, and every role's loop is kept
+// to a few hundred instructions (fully unrolled, the roles evicted each other's code and the walk took
+// 1.5 times as long).
+//
+// Warps 0-3: scores -> P.  4-7: outputs.  8-11: the memory's operand copy and its decay.  12-19: Vw.
+// 20: decays and TMA.  21: issues the products.  The groups and the tensor pipe work on different
+// stages of neighbouring chunks, so that none of their latencies adds up.
+//
+// Few heads and long sequences: a sequence is cut into segments.  A first launch (local kernel)
+// leaves, for all but the last, the memory it adds from zero; the walk starts segment p from
+// sum_{p'} (decay of the segments between) local_{p'}.  It reads k and v a second time, so the cut is
+// chosen by a cost model (plan below).  The local kernel walks backwards, so that every weight is
+// the product of the decays behind it and nothing needs rescaling, it leaves the segment's first
+// tokens in L2, where the walk begins, and it stops once the weights are 0 in fp32.
+//
+// Every wait is bounded (2 s); a time-out is recorded in the workspace header and the CTA unwinds.
+#include <algorithm>
+#include <initializer_list>
+
 #include "linear_internal.cuh"
+#include "tc_ptx.cuh"
+#include "tma_host.cuh"
+
 namespace kda {
-bool linear_tc_supported(int, int, DType) { return false; }
-size_t linear_tc_scratch_bytes(int, int, int, int, long, int, bool, int) { return 0; }
-cudaError_t launch_linear_tc(const LinFwd &, cudaStream_t) { return cudaErrorNotSupported; }
-size_t linear_tc_bwd_scratch_bytes(int, int, int, int, int, int, int) { return 0; }
-cudaError_t launch_linear_tc_bwd(const LinBwd &, cudaStream_t) { return cudaErrorNotSupported; }
+namespace {
+
+using namespace ptx;
+
+constexpr int kC = 128;                        // tokens per chunk
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kStatusDeviceTimeout = 8;        // KDA_ERR_DEVICE_TIMEOUT
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kZeroWeight = -150.f;          // 2^x is 0 in fp32 below this
+// A chunk whose running log2 decays stay within +-kMildSpan is attended with e^{G_i - G_C} taken out of the
+// row: O_i = e^{G_i - G_C} (q_i (e^{G_C} S) + sum_j s_ij w_j v_j), w_j = e^{G_C - G_j} the weights that the
+// memory takes too: one accumulator and one factor per column, none beyond 2^124.  Stronger decays (a
+// restart among them) get every weight e^{G_i - G_j} from its own exponent and the first term
+// rescaled in between.
+constexpr float kMildSpan = 62.f;
+constexpr int kMaxSegs = 64;                   // segments of a sequence at most (equal lengths)
+constexpr int kSortSeqs = 128;                 // packed sequences ranked by length up to this many
+
+struct TcWalk {
+    LinSeqs s;
+    LinDecay g;
+    int L;                  // tokens per segment (a multiple of kC)
+    int HV, m;              // value heads, value heads per q/k head
+    int sorted;             // packed, one segment each: take the sequences longest first
+    float scale;
+    const float *h0;
+    float *hT;
+    __nv_bfloat16 *o;
+    long long ob, ot, oh;
+    float *loc, *gam;       // per (item, head): [DK, DV], decay factor
+    WsHeader *hdr;
+};
+
+// 2^x (ex2.approx: 2 ulp; results below 2^-126 are 0)
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
+__device__ __forceinline__ void named_sync(int id, int count) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+__device__ __forceinline__ void named_arrive(int id, int count) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+// A CTA's failure flag and its bounded waits: once one has run out, the others return at once.
+struct Waits {
+    volatile int *fail;
+    WsHeader *hdr;
+    __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, int where) const {
+        return mbar_try_wait(bar, parity) || slow(bar, parity, where);
+    }
+    // out of line: the roles' loops have to stay in the instruction caches
+    __device__ __noinline__ bool slow(uint64_t *bar, uint32_t parity, int where) const {
+        if (*fail) return false;
+        const uint64_t t0 = globaltimer_ns();
+        while (true) {
+#pragma unroll 1
+            for (int i = 0; i < 64; ++i)
+                if (mbar_try_wait(bar, parity)) return true;
+            if (*fail) return false;
+            if (globaltimer_ns() - t0 > kWaitNs) break;
+        }
+        *fail = 1;
+        if (atomicCAS(&hdr->error, 0, kStatusDeviceTimeout) == 0) hdr->where = where;
+        return false;
+    }
+    // for a whole warp, which goes on or leaves together
+    __device__ __forceinline__ bool warp(uint64_t *bar, uint32_t parity, int where) const {
+        return __all_sync(0xffffffffu, wait(bar, parity, where));
+    }
+};
+
+// The sequence of rank r by decreasing length (ties: lower index first); whole warp.
+__device__ __forceinline__ int seq_by_rank(const LinSeqs &s, int r) {
+    const int lane = threadIdx.x & 31;
+    int found = -1;
+    for (int n = lane; n < s.nseq; n += 32) {
+        const int len = s.cu[n + 1] - s.cu[n];
+        int rank = 0;
+        for (int k = 0; k < s.nseq; ++k) {
+            const int lk = s.cu[k + 1] - s.cu[k];
+            rank += (lk > len || (lk == len && k < n)) ? 1 : 0;
+        }
+        if (rank == r) found = n;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, found >= 0);
+    return __shfl_sync(0xffffffffu, found, __ffs(hit) - 1);
+}
+
+__device__ __forceinline__ bool walk_item(const TcWalk &w, int item, LinItem &it) {
+    if (w.sorted) {
+        if (item >= w.s.nseq) return false;
+        item = seq_by_rank(w.s, item);   // one segment each: item = sequence
+    }
+    return lin_item(w.s, w.L, item, it);
+}
+
+// A decayed value x = w v in fp32 goes in as the sum of three bf16s: each takes the top 8 bits of what is
+// left (a truncation, so the rest is exact), together x's 24.
+__device__ __forceinline__ uint32_t top2(float a, float b) {
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ float rest(float a) { return a - __uint_as_float(__float_as_uint(a) & 0xffff0000u); }
+// byte offset of 16-byte piece c of row r in a bf16 tile [rows][D] (blocks of 64 channels, 128-byte swizzle)
+__device__ __forceinline__ uint32_t piece(int rows, int r, int c) {
+    return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+// The decayed values of channel `ch`, tokens t0 .. t0 + 63, as A-operand words (two tokens each): 8 columns
+// a step into column t0 / 2 of each part.  PARTS: bit 0 hi and mid, bit 1 lo.
+template <int PARTS>
+__device__ __forceinline__ void put_values(const uint8_t *v, const float *wa, int ch, int t0, uint32_t hi, uint32_t mid,
+                                           uint32_t lo) {
+    const uint8_t *col = v + (ch >> 6) * kC * 128 + (ch & 7) * 2;
+    const int c = (ch >> 3) & 7;
+#pragma unroll 1
+    for (int t = t0; t < t0 + 64; t += 16) {
+        uint32_t h[8], m[8], l[8];
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+            const uint32_t b0 = *reinterpret_cast<const uint16_t *>(col + (t + j) * 128 + ((c ^ (j & 7)) << 4));
+            const uint32_t b1 = *reinterpret_cast<const uint16_t *>(col + (t + j + 1) * 128 + ((c ^ ((j + 1) & 7)) << 4));
+            const float2 w = *reinterpret_cast<const float2 *>(wa + t + j);
+            const float x = w.x * __uint_as_float(b0 << 16), y = w.y * __uint_as_float(b1 << 16);
+            h[j / 2] = top2(x, y);
+            const float rx = rest(x), ry = rest(y);
+            m[j / 2] = top2(rx, ry);
+            l[j / 2] = top2(rest(rx), rest(ry));
+        }
+        if constexpr (PARTS & 1) {
+            tmem_st8(hi + t / 2, h);
+            tmem_st8(mid + t / 2, m);
+        }
+        if constexpr (PARTS & 2) tmem_st8(lo + t / 2, l);
+    }
+    tmem_st_wait();
+}
+
+// One product: sums over K in steps of 16, issued by the lane with `on`.  A step moves a descriptor's start
+// address, in 16-byte units: a K-major tile of `rows` rows by 32 bytes inside a block of 64 channels; an
+// MN-major one by 16 rows of 128 bytes.
+constexpr uint64_t kmajor_step(int ks, int rows) { return (uint64_t)((ks >> 2) * rows * 8 + (ks & 3) * 2); }
+constexpr uint64_t mn_step(int ks) { return (uint64_t)ks * 128; }
+
+// Lane t of a group of four starts with four pieces of its own row and ends with piece t of the
+// four rows.
+__device__ __forceinline__ void trade4(uint4 (&r)[4], int lane) {
+#pragma unroll
+    for (int b = 1; b < 4; b <<= 1) {
+        const bool up = lane & b;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j & b) continue;
+            uint32_t *lo = &r[j].x, *hi = &r[j | b].x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo[i] : hi[i], b);
+                if (up) lo[i] = got; else hi[i] = got;
+            }
+        }
+    }
+}
+
+// log2 decays of tokens u .. u + 3 of the sequence (u >= limit: 0)
+__device__ __forceinline__ float4 load_decay(const LinDecay &g, const float *gp, int u, int limit) {
+    float4 d;
+    float *p = &d.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = (gp && u + i < limit) ? clamp_decay(gp[(long long)(u + i) * g.t]) * kLog2e : 0.f;
+    return d;
+}
+
+// ------------------------------------------------------------------------------ the walk
+template <int DK, int DV>
+struct WalkCfg {
+    static constexpr int QB = kC * DK * 2, VB = kC * DV * 2;    // bytes of a q or k tile, of a v tile
+    static constexpr int STAGE = 2 * QB + VB;                   // Q, K, V; two stages
+    static constexpr int SB = 2 * STAGE;                        // the memory's operand copy
+    static constexpr int ARR = SB + DK * DV * 2;                // per chunk parity: G [128], w [128]
+    static constexpr int CTL = ARR + 2 * 2 * kC * 4;
+    static constexpr int SMEM = CTL + 256;
+    // TMEM columns: the memory [dv][dk], scores / P, O, hi and mid of the decayed values; lo lies in the
+    // upper half of the scores, which P leaves free
+    static constexpr int T_S = 0, T_P = DK, T_O = DK + 128, T_V = DK + 128 + DV, T_LO = T_P + 64;
+    static_assert(T_V + 128 <= 512, "TMEM");
+    static_assert(SMEM <= 232448, "shared memory");
+};
+
+struct WalkCtl {
+    uint64_t full[2], done[2], s_full, q_free, p_ready, r_ready, o_full, o_free, s_ready, v_ready, lo_ready, kv_done, cleared, last;
+    uint32_t tmem;
+    int fail;
+    int strong[2];   // the chunk's decays exceed kMildSpan
+};
+static_assert(sizeof(WalkCtl) <= 256, "control block");
+
+constexpr int kWalkThreads = 22 * 32;
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kWalkThreads, 1)
+linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv, TcWalk w) {
+    using Cf = WalkCfg<DK, DV>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    WalkCtl *ctl = reinterpret_cast<WalkCtl *>(smem + Cf::CTL);
+    if ((smem_u32(smem) & 1023) || blockDim.x != kWalkThreads) {   // what follows is laid out for these
+        if (threadIdx.x == 0) atomicCAS(&w.hdr->error, 0, kStatusDeviceTimeout);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int hv = blockIdx.x % w.HV;
+    LinItem it;
+    if (!walk_item(w, blockIdx.x / w.HV, it)) return;
+    const int t0 = it.p * w.L, t1 = min(it.len, t0 + w.L);      // tokens of the sequence
+    const int nch = (t1 - t0 + kC - 1) / kC;
+    const int b = w.s.cu ? 0 : it.n;
+    const long tb = w.s.cu ? it.start : 0;                      // token of batch entry b
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->full[i], 1);
+            mbar_init(&ctl->done[i], 1);
+        }
+        for (uint64_t *x : {&ctl->s_full, &ctl->q_free, &ctl->o_full, &ctl->kv_done, &ctl->last}) mbar_init(x, 1);
+        for (uint64_t *x : {&ctl->p_ready, &ctl->r_ready, &ctl->o_free, &ctl->s_ready}) mbar_init(x, 128);
+        for (uint64_t *x : {&ctl->v_ready, &ctl->lo_ready, &ctl->cleared}) mbar_init(x, 256);
+        ctl->fail = 0;
+        fence_mbar_init();
+    }
+    if (warp == 21) {
+        tmem_alloc(&ctl->tmem, 512);
+        tmem_relinquish();
+    }
+    if (warp == 20 && lane == 0) {
+        tma_prefetch_desc(&mq);
+        tma_prefetch_desc(&mk);
+        tma_prefetch_desc(&mv);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = ctl->tmem;
+    const Waits wt{&ctl->fail, w.hdr};
+    const uint32_t tlane = tm + ((uint32_t)(32 * (warp & 3)) << 16);   // this warp's 32 TMEM lanes
+    auto arr_g = [&](int c) { return reinterpret_cast<float *>(smem + Cf::ARR) + (c & 1) * 2 * kC; };
+    auto stage = [&](int c) { return smem + (c & 1) * Cf::STAGE; };
+
+    if (warp == 20) {
+        // ---- decays and loads
+        const float *gp = w.g.p ? w.g.p + b * w.g.b + tb * w.g.t + hv : nullptr;
+        float4 d = load_decay(w.g, gp, t0 + 4 * lane, t1);
+        for (int c = 0; c < nch; ++c) {
+            const int s = c & 1, u = t0 + c * kC;
+            float4 x = d;                       // running sums
+            x.y += x.x; x.z += x.y; x.w += x.z;
+            // sums of the decays behind a token (its weight in the memory)
+            float4 e = make_float4(d.y + (d.z + d.w), d.z + d.w, d.w, 0.f);
+            float up = x.w, down = d.x + e.x;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float y = __shfl_up_sync(0xffffffffu, up, off), z = __shfl_down_sync(0xffffffffu, down, off);
+                if (lane >= off) up += y;
+                if (lane + off < 32) down += z;
+            }
+            float before = __shfl_up_sync(0xffffffffu, up, 1), behind = __shfl_down_sync(0xffffffffu, down, 1);
+            if (lane == 0) before = 0.f;
+            if (lane == 31) behind = 0.f;
+            x.x += before; x.y += before; x.z += before; x.w += before;
+            e = make_float4(ex2(e.x + behind), ex2(e.y + behind), ex2(e.z + behind), ex2(behind));
+            const bool mild = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))) <= kMildSpan;
+            const int strong = !__all_sync(0xffffffffu, mild);
+            if (c >= 2 && !wt.warp(&ctl->done[s], ((c >> 1) - 1) & 1, 1)) break;
+            float *ga = arr_g(c);
+            *reinterpret_cast<float4 *>(ga + 4 * lane) = x;
+            *reinterpret_cast<float4 *>(ga + kC + 4 * lane) = e;
+            __syncwarp();
+            if (lane == 0) {
+                uint8_t *st = stage(c);
+                uint64_t *bar = &ctl->full[s];
+                ctl->strong[s] = strong;
+                mbar_expect_tx(bar, Cf::STAGE);
+                const int row = (int)(tb + u), hq = hv / w.m;
+#pragma unroll
+                for (int i = 0; i < DK / 64; ++i) tma_load_4d(st + i * kC * 128, &mq, bar, 64 * i, hq, row, b);
+#pragma unroll
+                for (int i = 0; i < DK / 64; ++i) tma_load_4d(st + Cf::QB + i * kC * 128, &mk, bar, 64 * i, hq, row, b);
+#pragma unroll
+                for (int i = 0; i < DV / 64; ++i) tma_load_4d(st + 2 * Cf::QB + i * kC * 128, &mv, bar, 64 * i, hv, row, b);
+            }
+            if (c + 1 < nch) d = load_decay(w.g, gp, u + kC + 4 * lane, t1);
+        }
+    } else if (warp == 21) {
+        // ---- products
+        constexpr uint32_t id1 = idesc_bf16_f32(128, 128, false, false);
+        constexpr uint32_t id2 = idesc_bf16_f32(128, DV, false, false);
+        constexpr uint32_t id3 = idesc_bf16_f32(128, DV, false, true);
+        constexpr uint32_t id4 = idesc_bf16_f32(128, DK, false, true);   // dv = 64: rows 64.. are nobody's
+        const uint32_t on = lane == 0;
+        const uint64_t ds = desc_kmajor_sw128(smem_u32(smem + Cf::SB), DV, 0);
+        // product 1 of chunk c: its scores lie where P(c - 1) did
+        auto scores = [&](int c) {
+            if (!wt.warp(&ctl->full[c & 1], (c >> 1) & 1, 3)) return false;
+            tc_fence_after();
+            const uint32_t q = smem_u32(stage(c));
+            const uint64_t dq = desc_kmajor_sw128(q, kC, 0), dk = desc_kmajor_sw128(q + Cf::QB, kC, 0);
+#pragma unroll
+            for (int ks = 0; ks < DK / 16; ++ks)
+                mma_bf16_ss_on(on, tm + Cf::T_P, dq + kmajor_step(ks, kC), dk + kmajor_step(ks, kC), id1, ks > 0);
+            mma_commit_on(on, &ctl->s_full);
+            return true;
+        };
+        // Products 3 and 1 of the next chunk come after 4: they fill the pipe while the memory
+        // (waiting for 4) is turned into the next operand
+        bool ok = nch > 0 && scores(0);
+        uint32_t ph_r = 0;
+        for (int c = 0; ok && c < nch; ++c) {
+            const uint32_t ph = c & 1;
+            const uint32_t q = smem_u32(stage(c));
+            const uint64_t dq = desc_kmajor_sw128(q, kC, 0), dk = desc_mnmajor_sw128(q + Cf::QB, kC, 0),
+                           dv = desc_mnmajor_sw128(q + 2 * Cf::QB, kC, 0);
+            if (!wt.warp(&ctl->s_ready, ph, 4) || !wt.warp(&ctl->o_free, ph, 5)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < DK / 16; ++ks)
+                mma_bf16_ss_on(on, tm + Cf::T_O, dq + kmajor_step(ks, kC), ds + kmajor_step(ks, DV), id2, ks > 0);
+            mma_commit_on(on, &ctl->q_free);
+            if (!wt.warp(&ctl->v_ready, ph, 6)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int ks = 0; ks < kC / 16; ++ks)
+                    mma_bf16_ts_on(on, tm + Cf::T_S, tm + Cf::T_V + 64 * i + 8 * ks, dk + mn_step(ks), id4, 1u);
+            if (!wt.warp(&ctl->lo_ready, ph, 7)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < kC / 16; ++ks)
+                mma_bf16_ts_on(on, tm + Cf::T_S, tm + Cf::T_LO + 8 * ks, dk + mn_step(ks), id4, 1u);
+            mma_commit_on(on, &ctl->kv_done);
+            if (!wt.warp(&ctl->p_ready, ph, 8)) break;
+            if (ctl->strong[ph]) {
+                if (!wt.warp(&ctl->r_ready, ph_r, 9)) break;
+                ph_r ^= 1;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < kC / 16; ++ks)
+                mma_bf16_ts_on(on, tm + Cf::T_O, tm + Cf::T_P + 8 * ks, dv + mn_step(ks), id3, 1u);
+            mma_commit_on(on, &ctl->o_full);
+            mma_commit_on(on, &ctl->done[ph]);
+            if (c + 1 < nch) ok = scores(c + 1);
+        }
+    } else if (warp < 4) {
+        // ---- scores -> P (thread = token row)
+        const int row = tid;
+        for (int c = 0; c < nch; ++c) {
+            const float *ga = arr_g(c), *wa = ga + kC;
+            if (!wt.warp(&ctl->full[c & 1], (c >> 1) & 1, 10)) break;
+            if (!wt.warp(&ctl->s_full, c & 1, 11)) break;
+            tc_fence_after();
+            const float gi = ga[row];
+            const bool strong = ctl->strong[c & 1];
+            // 16 columns at a time, written as 8 columns of packed pairs over scores read already
+#pragma unroll 1
+            for (int j0 = 0; j0 < 32 * (warp + 1); j0 += 16) {
+                uint32_t x[16], p[8];
+                tmem_ld16(tlane + Cf::T_P + j0, x);
+                tmem_ld_wait();
+                if (!strong) {
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 e = *reinterpret_cast<const float4 *>(wa + j0 + j);
+                        x[j] = __float_as_uint(__uint_as_float(x[j]) * e.x);
+                        x[j + 1] = __float_as_uint(__uint_as_float(x[j + 1]) * e.y);
+                        x[j + 2] = __float_as_uint(__uint_as_float(x[j + 2]) * e.z);
+                        x[j + 3] = __float_as_uint(__uint_as_float(x[j + 3]) * e.w);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        x[j] = __float_as_uint(__uint_as_float(x[j]) * (w.scale * ex2(gi - ga[j0 + j])));
+                }
+                // nothing after the row's own token (only the last 32 columns hold any)
+                const int keep = j0 >= 32 * warp ? row - j0 : 16;
+#pragma unroll
+                for (int j = 0; j < 16; j += 2)
+                    p[j / 2] = pack_bf16(j <= keep ? __uint_as_float(x[j]) : 0.f, j + 1 <= keep ? __uint_as_float(x[j + 1]) : 0.f);
+                tmem_st8(tlane + Cf::T_P + j0 / 2, p);
+            }
+#pragma unroll 1
+            for (int j0 = 16 * (warp + 1); j0 < 64; j0 += 8) {  // tokens after the row
+                const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                tmem_st8(tlane + Cf::T_P + j0, zero);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&ctl->p_ready);
+        }
+    } else if (warp < 8) {
+        // ---- outputs (thread = token row)
+        const int row = tid - 128;
+        float gi = 0.f, gc = 0.f;              // G of the row and of the chunk and the chunk's kind, read a
+        bool next_strong = false;              // chunk ahead (their places are reused)
+        if (nch > 0 && wt.warp(&ctl->full[0], 0, 12)) {
+            gi = arr_g(0)[row];
+            gc = arr_g(0)[kC - 1];
+            next_strong = ctl->strong[0];
+            mbar_arrive(&ctl->o_free);         // nothing to read yet
+        }
+        for (int c = 0; c < nch; ++c) {
+            const bool strong = next_strong;
+            float gs = w.scale * ex2(strong ? gi : gi - gc);
+            const int u0 = t0 + c * kC + (row & ~3);       // first row of the four lanes that trade pieces
+            __nv_bfloat16 *op = w.o + b * w.ob + (tb + u0) * w.ot + hv * w.oh + 8 * (lane & 3);
+            if (c + 1 < nch) {
+                if (!wt.warp(&ctl->full[(c + 1) & 1], ((c + 1) >> 1) & 1, 13)) break;
+                gi = arr_g(c + 1)[row];
+                gc = arr_g(c + 1)[kC - 1];
+                next_strong = ctl->strong[(c + 1) & 1];
+            }
+            if (strong) {                                   // the first term takes its factor before P V is added
+                if (!wt.warp(&ctl->q_free, c & 1, 14)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int cb = 0; cb < DV; cb += 32) {
+                    uint32_t x[32];
+                    tmem_ld32(tlane + Cf::T_O + cb, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(gs * __uint_as_float(x[j]));
+                    tmem_st32(tlane + Cf::T_O + cb, x);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&ctl->r_ready);
+                gs = 1.f;
+            }
+            if (!wt.warp(&ctl->o_full, c & 1, 15)) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int cb = 0; cb < DV; cb += 32) {
+                uint32_t x[32];
+                tmem_ld32(tlane + Cf::T_O + cb, x);
+                tmem_ld_wait();
+                if (cb + 32 == DV) {       // the accumulator is free before the last stores go out
+                    tc_fence_before();
+                    mbar_arrive(&ctl->o_free);
+                }
+                // Stored as they lie, a row to a thread, 16-byte stores would touch 32 lines each and stall
+                // for thousands of clocks; four lanes trade 16-byte pieces, so that they hold 64
+                // bytes of one row at a time.
+                uint4 r[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t *pr = &r[j].x;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        pr[i] = pack_bf16(gs * __uint_as_float(x[8 * j + 2 * i]), gs * __uint_as_float(x[8 * j + 2 * i + 1]));
+                }
+                trade4(r, lane);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (u0 + j < t1) *reinterpret_cast<uint4 *>(op + (long long)j * w.ot + cb) = r[j];
+            }
+        }
+    } else if (warp < 12) {
+        // ---- the memory (thread = value channel i, TMEM lane i; dv = 64: warps 8 and 9)
+        const int i = tid - 256;
+        uint8_t *sb = smem + Cf::SB;
+        const size_t pair = (size_t)it.n * w.HV + hv;
+        for (int c = 0; c < nch; ++c) {
+            if (!wt.warp(&ctl->full[c & 1], (c >> 1) & 1, 16)) break;
+            const float alpha = ex2(arr_g(c)[kC - 1]), beta = ctl->strong[c & 1] ? 1.f : alpha;
+            if (c > 0 && (!wt.warp(&ctl->q_free, (c - 1) & 1, 17) || !wt.warp(&ctl->kv_done, (c - 1) & 1, 18))) break;
+            tc_fence_after();
+            if (warp - 8 < DV / 32) {
+#pragma unroll 1
+                for (int cb = 0; cb < DK; cb += 32) {
+                    uint32_t x[32];
+                    if (c > 0) {
+                        tmem_ld32(tlane + Cf::T_S + cb, x);
+                        tmem_ld_wait();
+                    } else {                       // the segment's start
+                        float acc[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) acc[j] = w.h0 ? w.h0[(pair * DK + cb + j) * DV + i] : 0.f;
+                        for (int pp = 0; pp < it.p; ++pp) {
+                            const size_t slot = (size_t)(it.first + pp) * w.HV + hv;
+                            const float ga2 = w.gam[slot];
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) acc[j] = fmaf(acc[j], ga2, w.loc[(slot * DK + cb + j) * DV + i]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(acc[j]);
+                    }
+                    // operand: row i, 32 key channels
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        uint4 p;
+                        uint32_t *pp = &p.x;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            pp[k] = pack_bf16(beta * __uint_as_float(x[j + 2 * k]), beta * __uint_as_float(x[j + 2 * k + 1]));
+                        *reinterpret_cast<uint4 *>(sb + piece(DV, i, (cb + j) / 8)) = p;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(alpha * __uint_as_float(x[j]));
+                    tmem_st32(tlane + Cf::T_S + cb, x);
+                }
+                tmem_st_wait();
+                fence_proxy_async();
+                tc_fence_before();
+            }
+            mbar_arrive(&ctl->s_ready);
+        }
+        // the final memory
+        if (w.hT && it.p == it.nseg - 1 && warp - 8 < DV / 32) {
+            float *hp = w.hT + pair * DK * DV + i;
+            if (nch == 0) {                    // an empty sequence keeps its memory
+                for (int j = 0; j < DK; ++j) hp[j * DV] = w.h0 ? w.h0[(pair * DK + j) * DV + i] : 0.f;
+            } else if (wt.warp(&ctl->kv_done, (nch - 1) & 1, 19)) {
+                tc_fence_after();
+#pragma unroll 1
+                for (int cb = 0; cb < DK; cb += 32) {
+                    uint32_t x[32];
+                    tmem_ld32(tlane + Cf::T_S + cb, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) hp[(cb + j) * DV] = __uint_as_float(x[j]);
+                }
+            }
+        }
+    } else {
+        // ---- decayed values (thread = value channel, half of the tokens)
+        const int ch = (tid - 384) & 127, half = (tid - 384) >> 7;
+        const bool mine = (ch & ~31) < DV;
+        for (int c = 0; c < nch; ++c) {
+            if (!wt.warp(&ctl->full[c & 1], (c >> 1) & 1, 20)) break;
+            const float *wa = arr_g(c) + kC;
+            uint8_t *k = stage(c) + Cf::QB, *v = stage(c) + 2 * Cf::QB;
+            if (c > 0 && !wt.warp(&ctl->kv_done, (c - 1) & 1, 21)) break;   // the last chunk's are used
+            const int live = t1 - t0 - c * kC;
+            if (live < kC) {
+                // rows past the sequence may hold anything: cleared in K and V by the 256 threads, each half of
+                // one row (of both tiles' own widths), before any of them reads V
+                if (!wt.warp(&ctl->s_full, c & 1, 22)) break;               // product 1 reads K
+                if (ch >= live) {
+#pragma unroll 1
+                    for (int p = half * (DK / 16); p < (half + 1) * (DK / 16); ++p)
+                        *reinterpret_cast<uint4 *>(k + piece(kC, ch, p)) = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+                    for (int p = half * (DV / 16); p < (half + 1) * (DV / 16); ++p)
+                        *reinterpret_cast<uint4 *>(v + piece(kC, ch, p)) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async();
+                mbar_arrive(&ctl->cleared);                                 // only a sequence's last chunk comes here
+                if (!wt.warp(&ctl->cleared, 0, 24)) break;
+            }
+            tc_fence_after();
+            if (mine) put_values<1>(v, wa, ch, 64 * half, tlane + Cf::T_V, tlane + Cf::T_V + 64, 0);
+            tc_fence_before();
+            mbar_arrive(&ctl->v_ready);
+            if (!wt.warp(&ctl->p_ready, c & 1, 23)) break;                  // the scores have been read
+            tc_fence_after();
+            if (mine) put_values<2>(v, wa, ch, 64 * half, 0, 0, tlane + Cf::T_LO);
+            tc_fence_before();
+            mbar_arrive(&ctl->lo_ready);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 21) {
+        // nothing of this CTA's is in flight once its last product and loads have landed (a bounded
+        // wait: after a time-out they may not have)
+        mma_commit_on(lane == 0, &ctl->last);
+        (void)mbar_wait(&ctl->last, 0, kWaitNs);
+        if (ctl->fail) {
+            const uint64_t t = globaltimer_ns();
+            while (globaltimer_ns() - t < 1000000ull) {
+            }
+        }
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tm, 512);
+    }
+}
+
+// ------------------------------------------------------------------------------ local memories
+template <int DK, int DV>
+struct LocalCfg {
+    static constexpr int KB = kC * DK * 2, VB = kC * DV * 2;
+    static constexpr int STAGE = KB + VB;                      // K, V
+    static constexpr int NST = STAGE > 48 * 1024 ? 3 : 4;
+    static constexpr int ARR = NST * STAGE;                    // per stage: w [128]
+    static constexpr int CTL = ARR + NST * kC * 4;
+    static constexpr int SMEM = CTL + 256;
+    static constexpr int T_V = DK;                             // two sets of hi, mid, lo
+    static_assert(T_V + 384 <= 512 && SMEM <= 232448, "TMEM, shared memory");
+};
+struct LocalCtl {
+    uint64_t full[4], empty[4], ready[2], used[2], last;
+    uint32_t tmem;
+    int fail;
+    int cmd[4];        // 1: a chunk, 0: no more
+    float red[8], top[8];
+};
+static_assert(sizeof(LocalCtl) <= 256, "control block");
+
+// The memory one segment adds from zero.  Warps 0-7: weighted values (thread = channel, half of the
+// tokens), the segment's total decay, the result; 8: decays and TMA, from the segment's last chunk to its
+// first; 9: products.
+constexpr int kLocalThreads = 10 * 32;
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kLocalThreads, 1)
+linear_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, TcWalk w) {
+    using Cf = LocalCfg<DK, DV>;
+    constexpr int NST = Cf::NST;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    LocalCtl *ctl = reinterpret_cast<LocalCtl *>(smem + Cf::CTL);
+    if ((smem_u32(smem) & 1023) || blockDim.x != kLocalThreads) {
+        if (threadIdx.x == 0) atomicCAS(&w.hdr->error, 0, kStatusDeviceTimeout);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int hv = blockIdx.x % w.HV, item = blockIdx.x / w.HV;
+    LinItem it;
+    if (!lin_item(w.s, w.L, item, it) || it.p == it.nseg - 1) return;   // nobody reads the last segment's
+    const int t0 = it.p * w.L, nch = w.L / kC;                          // whole chunks: not the last segment
+    const int b = w.s.cu ? 0 : it.n;
+    const long tb = w.s.cu ? it.start : 0;
+    const float *gp = w.g.p ? w.g.p + b * w.g.b + tb * w.g.t + hv : nullptr;
+    if (tid == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&ctl->full[i], 1);
+            mbar_init(&ctl->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->ready[i], 256);
+            mbar_init(&ctl->used[i], 1);
+        }
+        mbar_init(&ctl->last, 1);
+        ctl->fail = 0;
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(&ctl->tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = ctl->tmem;
+    const Waits wt{&ctl->fail, w.hdr};
+    float *wa = reinterpret_cast<float *>(smem + Cf::ARR);
+
+    if (warp == 8) {
+        float tail = 0.f;                       // decays behind the chunk
+        float4 d = load_decay(w.g, gp, t0 + (nch - 1) * kC + 4 * lane, 0x7fffffff);
+        int n = 0, c = nch - 1;
+        bool known = false, never_up = false;
+        for (; c >= 0; --c, ++n) {
+            const int s = n % NST, u = t0 + c * kC;
+            // sums of the decays behind each token: a suffix sum without the token's own
+            float4 x = make_float4(d.y + (d.z + d.w), d.z + d.w, d.w, 0.f);
+            float down = x.x + d.x;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float y = __shfl_down_sync(0xffffffffu, down, off);
+                if (lane + off < 32) down += y;
+            }
+            const float all = __shfl_sync(0xffffffffu, down, 0);
+            float behind = __shfl_down_sync(0xffffffffu, down, 1);
+            if (lane == 31) behind = 0.f;
+            behind += tail;
+            // with no positive decay in the segment the weights only fall from here on
+            if (tail < kZeroWeight) {
+                if (!known) {
+                    named_sync(1, 288);         // the totals are in
+                    known = true;
+                    never_up = true;
+                    for (int i = 0; i < 8; ++i) never_up = never_up && ctl->top[i] <= 0.f;
+                }
+                if (never_up) break;
+            }
+            if (n >= NST && !wt.warp(&ctl->empty[s], (n / NST - 1) & 1, 31)) break;
+            *reinterpret_cast<float4 *>(wa + s * kC + 4 * lane) =
+                make_float4(ex2(x.x + behind), ex2(x.y + behind), ex2(x.z + behind), ex2(x.w + behind));
+            __syncwarp();
+            if (lane == 0) {
+                ctl->cmd[s] = 1;
+                uint8_t *st = smem + s * Cf::STAGE;
+                mbar_expect_tx(&ctl->full[s], Cf::STAGE);
+                const int row = (int)(tb + u), hq = hv / w.m;
+#pragma unroll
+                for (int i = 0; i < DK / 64; ++i) tma_load_4d(st + i * kC * 128, &mk, &ctl->full[s], 64 * i, hq, row, b);
+#pragma unroll
+                for (int i = 0; i < DV / 64; ++i)
+                    tma_load_4d(st + Cf::KB + i * kC * 128, &mv, &ctl->full[s], 64 * i, hv, row, b);
+            }
+            tail += all;
+            if (c > 0) d = load_decay(w.g, gp, u - kC + 4 * lane, 0x7fffffff);
+        }
+        if (!known) named_sync(1, 288);
+        // tell the others
+        const int s = n % NST;
+        if (n < NST || wt.warp(&ctl->empty[s], (n / NST - 1) & 1, 32)) {
+            if (lane == 0) {
+                ctl->cmd[s] = 0;
+                mbar_arrive(&ctl->full[s]);
+            }
+        }
+    } else if (warp == 9) {
+        constexpr uint32_t id = idesc_bf16_f32(128, DK, false, true);
+        const uint32_t on = lane == 0;
+        for (int n = 0;; ++n) {
+            const int s = n % NST;
+            if (!wt.warp(&ctl->full[s], (n / NST) & 1, 33)) break;
+            if (!ctl->cmd[s]) break;
+            if (!wt.warp(&ctl->ready[n & 1], (n >> 1) & 1, 34)) break;
+            tc_fence_after();
+            const uint64_t dk = desc_mnmajor_sw128(smem_u32(smem + s * Cf::STAGE), kC, 0);
+            const uint32_t a = tm + Cf::T_V + (n & 1) * 192;
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int ks = 0; ks < kC / 16; ++ks)
+                    mma_bf16_ts_on(on, tm, a + 64 * i + 8 * ks, dk + mn_step(ks), id, (uint32_t)n | (uint32_t)(i + ks));
+            mma_commit_on(on, &ctl->used[n & 1]);
+            mma_commit_on(on, &ctl->empty[s]);
+        }
+        mma_commit_on(on, &ctl->last);
+    } else {
+        // total decay of the segment, in a fixed order; its largest decay
+        float sum = 0.f, top = -INFINITY;
+        for (int u = tid; u < w.L; u += 256) {
+            const float x = gp ? clamp_decay(gp[(long long)(t0 + u) * w.g.t]) * kLog2e : 0.f;
+            sum += x;
+            top = x > top || x != x ? x : top;
+        }
+#pragma unroll
+        for (int off = 16; off; off >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            const float y = __shfl_xor_sync(0xffffffffu, top, off);
+            top = y > top || y != y ? y : top;
+        }
+        if (lane == 0) {
+            ctl->red[warp] = sum;
+            ctl->top[warp] = top;
+        }
+        named_sync(2, 256);
+        named_arrive(1, 288);                   // the producer warp may look at them
+        const size_t slot = (size_t)item * w.HV + hv;
+        if (tid == 0) {
+            float all = 0.f;
+            for (int i = 0; i < 8; ++i) all += ctl->red[i];
+            w.gam[slot] = ex2(all);
+        }
+        const int ch = tid & 127, half = tid >> 7;
+        const bool mine = (ch & ~31) < DV;
+        const uint32_t tlane = tm + ((uint32_t)(32 * (warp & 3)) << 16);
+        for (int n = 0;; ++n) {
+            const int s = n % NST;
+            if (!wt.warp(&ctl->full[s], (n / NST) & 1, 35)) break;
+            if (!ctl->cmd[s]) break;
+            if (n >= 2 && !wt.warp(&ctl->used[n & 1], ((n >> 1) - 1) & 1, 36)) break;
+            tc_fence_after();
+            const uint32_t a = tlane + Cf::T_V + (n & 1) * 192;
+            if (mine) put_values<3>(smem + s * Cf::STAGE + Cf::KB, wa + s * kC, ch, 64 * half, a, a + 64, a + 128);
+            tc_fence_before();
+            mbar_arrive(&ctl->ready[n & 1]);
+        }
+        if (wt.warp(&ctl->last, 0, 37)) {
+            tc_fence_after();
+            if (mine) {                         // half of the key channels
+                float *lp = w.loc + slot * DK * DV + ch;
+#pragma unroll 1
+                for (int cb = half * (DK / 2); cb < (half + 1) * (DK / 2); cb += 32) {
+                    uint32_t x[32];
+                    tmem_ld32(tlane + cb, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) lp[(cb + j) * DV] = __uint_as_float(x[j]);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        if (ctl->fail) {                        // let what is in flight land
+            const uint64_t t = globaltimer_ns();
+            while (globaltimer_ns() - t < 1000000ull) {
+            }
+        }
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tm, 512);
+    }
+}
+
+// ------------------------------------------------------------------------------ host
+bool token_map(CUtensorMap *map, const LinView &v, int D, int heads, long T, long B, int rows = kC) {
+    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)heads, (uint64_t)T, (uint64_t)B};
+    const uint64_t st[3] = {(uint64_t)v.h * 2, (uint64_t)v.t * 2, (uint64_t)v.b * 2};
+    const uint32_t box[4] = {64, 1, (uint32_t)rows, 1};
+    return make_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.p, dims, st, box, true);
+}
+
+size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// Chunks per segment.  In units of one chunk of the walk (0.85 us), a CTA costs about 3 to set up and
+// fill, a chunk of the local kernel 0.55, its launch 3, a start state's segment 0.6; every (sequence, head)
+// that finds no SM waits for the next wave.  Equal lengths: the cut with the least of it.  Packed
+// sequences: whole ones while the longest is no more than an SM's share of the work (taken longest
+// first they then fill the SMs evenly), else segments of half an SM's share.
+int plan_chunks(int nseq, int HV, long total, int max_len, bool varlen, int sms) {
+    const int nch = std::max(1, (max_len + kC - 1) / kC);
+    const long pairs = (long)nseq * HV;
+    if (varlen) {
+        const double share = (double)(total / kC + nseq) * HV / sms;
+        if (nch <= share + 2.0 || nch <= 8) return nch;
+        return std::min(nch, std::max(4, (int)(share / 2 + 0.5)));
+    }
+    int best = nch;
+    double cost = 1e30;
+    for (int p = 1; p <= std::min(nch, kMaxSegs); ++p) {
+        const int lc = (nch + p - 1) / p, segs = (nch + lc - 1) / lc;
+        double t = (double)((pairs * segs + sms - 1) / sms) * (lc + 3.0);
+        if (segs > 1) t += (double)((pairs * (segs - 1) + sms - 1) / sms) * (0.55 * lc + 3.0) + 3.0 + 0.6 * (segs - 1);
+        if (t < cost) {
+            cost = t;
+            best = lc;
+        }
+    }
+    return best;
+}
+
+template <int DK, int DV>
+cudaError_t go(const LinFwd &a, const TcWalk &w, long items, bool split, const CUtensorMap &mq, const CUtensorMap &mk,
+               const CUtensorMap &mv, cudaStream_t st) {
+    using WC = WalkCfg<DK, DV>;
+    using LC = LocalCfg<DK, DV>;
+    if (items * a.HV > 0x7fffffffL) return cudaErrorInvalidValue;
+    const unsigned grid = (unsigned)(items * a.HV);
+    cudaError_t e;
+    if (split) {
+        e = cudaFuncSetAttribute(linear_local_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, LC::SMEM);
+        if (e != cudaSuccess) return e;
+        linear_local_kernel<DK, DV><<<grid, kLocalThreads, LC::SMEM, st>>>(mk, mv, w);
+    }
+    e = cudaFuncSetAttribute(linear_chunk_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, WC::SMEM);
+    if (e != cudaSuccess) return e;
+    linear_chunk_kernel<DK, DV><<<grid, kWalkThreads, WC::SMEM, st>>>(mq, mk, mv, w);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool linear_tc_supported(int dk, int dv, DType dt) {
+    return dt == DType::BF16 && (dk == 64 || dk == 128) && (dv == 64 || dv == 128);
+}
+
+size_t linear_tc_scratch_bytes(int nseq, int HV, int dk, int dv, long total, int max_len, bool varlen, int sms) {
+    size_t slots;
+    if (varlen) {   // whatever the lengths turn out to be: the shortest segments plan_chunks cuts
+        const double share = (double)(total / kC + nseq) * HV / sms;
+        const long lc = std::max(4, (int)(share / 2 + 0.5));
+        slots = (size_t)(total / (lc * kC) + nseq) * HV;
+    } else {
+        const int lc = plan_chunks(nseq, HV, total, max_len, false, sms);
+        if ((long)lc * kC >= max_len) return 0;
+        slots = (size_t)lin_items(nseq, total, max_len, false, lc * kC) * HV;
+    }
+    return round256(slots * dk * dv * 4) + round256(slots * 4);
+}
+
+cudaError_t launch_linear_tc(const LinFwd &a, cudaStream_t st) {
+    const bool varlen = a.s.cu != nullptr;
+    int lc = plan_chunks(a.s.nseq, a.HV, a.total, a.max_len, varlen, a.sms);
+    if (a.h0 && a.h0 == a.hT) lc = (a.max_len + kC - 1) / kC;   // in place: every CTA owns its memory
+    TcWalk w{};
+    w.s = a.s; w.g = a.g; w.L = lc * kC; w.HV = a.HV; w.m = a.HV / a.H;
+    w.scale = a.scale; w.h0 = a.h0; w.hT = a.hT;
+    w.o = static_cast<__nv_bfloat16 *>(const_cast<void *>(a.o.p));
+    w.ob = a.o.b; w.ot = a.o.t; w.oh = a.o.h; w.hdr = a.hdr;
+    const bool split = a.max_len > w.L;
+    w.sorted = varlen && !split && a.s.nseq > 1 && a.s.nseq <= kSortSeqs;
+    const long items = lin_items(a.s.nseq, a.total, a.max_len, varlen, w.L);
+    w.loc = static_cast<float *>(a.ws);
+    w.gam = reinterpret_cast<float *>(static_cast<char *>(a.ws) + round256((size_t)items * a.HV * a.dk * a.dv * 4));
+    const long B = varlen ? 1 : a.s.nseq;
+    CUtensorMap mq, mk, mv;
+    if (!token_map(&mq, a.q, a.dk, a.H, a.total, B) || !token_map(&mk, a.k, a.dk, a.H, a.total, B) ||
+        !token_map(&mv, a.v, a.dv, a.HV, a.total, B))
+        return cudaErrorInvalidValue;
+    if (a.dk == 128 && a.dv == 128) return go<128, 128>(a, w, items, split, mq, mk, mv, st);
+    if (a.dk == 128) return go<128, 64>(a, w, items, split, mq, mk, mv, st);
+    if (a.dv == 128) return go<64, 128>(a, w, items, split, mq, mk, mv, st);
+    return go<64, 64>(a, w, items, split, mq, mk, mv, st);
+}
+
+size_t linear_tc_bwd_scratch_bytes(int B, int T, int H, int HV, int dk, int dv, int sms) {
+    return linear_scan_bwd_scratch_bytes(B, T, H, HV, dk, dv, sms);
+}
+cudaError_t launch_linear_tc_bwd(const LinBwd &a, cudaStream_t st) { return launch_linear_scan_bwd(a, st); }
+
+}  // namespace kda
