@@ -1,0 +1,145 @@
+// linear_tc.cuh -- what the tensor-core kernels of linear attention (linear_tc.cu, linear_tc_bwd.cu) share:
+// chunk constants, bounded waits, operand layouts, the three-part operand, tensor maps.
+#pragma once
+
+#include "linear_internal.cuh"
+#include "tc_ptx.cuh"
+#include "tma_host.cuh"
+
+namespace kda {
+namespace lin {
+
+using namespace ptx;
+
+constexpr int kC = 128;                        // tokens per chunk
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kStatusDeviceTimeout = 8;        // KDA_ERR_DEVICE_TIMEOUT
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 2^x (ex2.approx: 2 ulp; results below 2^-126 are 0)
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void named_sync(int id, int count) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+__device__ __forceinline__ void named_arrive(int id, int count) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+// A CTA's failure flag and its bounded waits: once one has run out, the others return at once.
+struct Waits {
+    volatile int *fail;
+    WsHeader *hdr;
+    __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, int where) const {
+        return mbar_try_wait(bar, parity) || slow(bar, parity, where);
+    }
+    // out of line: the roles' loops have to stay in the instruction caches
+    __device__ __noinline__ bool slow(uint64_t *bar, uint32_t parity, int where) const {
+        if (*fail) return false;
+        const uint64_t t0 = globaltimer_ns();
+        while (true) {
+#pragma unroll 1
+            for (int i = 0; i < 64; ++i)
+                if (mbar_try_wait(bar, parity)) return true;
+            if (*fail) return false;
+            if (globaltimer_ns() - t0 > kWaitNs) break;
+        }
+        *fail = 1;
+        if (atomicCAS(&hdr->error, 0, kStatusDeviceTimeout) == 0) hdr->where = where;
+        return false;
+    }
+    // for a whole warp, which goes on or leaves together
+    __device__ __forceinline__ bool warp(uint64_t *bar, uint32_t parity, int where) const {
+        return __all_sync(0xffffffffu, wait(bar, parity, where));
+    }
+};
+
+// A decayed value x = w v in fp32 goes in as the sum of three bf16s: each takes the top 8 bits of what is
+// left (a truncation, so the rest is exact), together x's 24.
+__device__ __forceinline__ uint32_t top2(float a, float b) {
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ float rest(float a) { return a - __uint_as_float(__float_as_uint(a) & 0xffff0000u); }
+// byte offset of 16-byte piece c of row r in a bf16 tile [rows][D] (blocks of 64 channels, 128-byte swizzle)
+__device__ __forceinline__ uint32_t piece(int rows, int r, int c) {
+    return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+// The decayed values of channel `ch`, tokens t0 .. t0 + 63, as A-operand words (two tokens each): 8 columns
+// a step into column t0 / 2 of each part.  PARTS: bit 0 hi and mid, bit 1 lo.
+template <int PARTS>
+__device__ __forceinline__ void put_values(const uint8_t *v, const float *wa, int ch, int t0, uint32_t hi, uint32_t mid,
+                                           uint32_t lo) {
+    const uint8_t *col = v + (ch >> 6) * kC * 128 + (ch & 7) * 2;
+    const int c = (ch >> 3) & 7;
+#pragma unroll 1
+    for (int t = t0; t < t0 + 64; t += 16) {
+        uint32_t h[8], m[8], l[8];
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+            const uint32_t b0 = *reinterpret_cast<const uint16_t *>(col + (t + j) * 128 + ((c ^ (j & 7)) << 4));
+            const uint32_t b1 = *reinterpret_cast<const uint16_t *>(col + (t + j + 1) * 128 + ((c ^ ((j + 1) & 7)) << 4));
+            const float2 w = *reinterpret_cast<const float2 *>(wa + t + j);
+            const float x = w.x * __uint_as_float(b0 << 16), y = w.y * __uint_as_float(b1 << 16);
+            h[j / 2] = top2(x, y);
+            const float rx = rest(x), ry = rest(y);
+            m[j / 2] = top2(rx, ry);
+            l[j / 2] = top2(rest(rx), rest(ry));
+        }
+        if constexpr (PARTS & 1) {
+            tmem_st8(hi + t / 2, h);
+            tmem_st8(mid + t / 2, m);
+        }
+        if constexpr (PARTS & 2) tmem_st8(lo + t / 2, l);
+    }
+    tmem_st_wait();
+}
+
+// One product: sums over K in steps of 16, issued by the lane with `on`.  A step moves a descriptor's start
+// address, in 16-byte units: a K-major tile of `rows` rows by 32 bytes inside a block of 64 channels; an
+// MN-major one by 16 rows of 128 bytes.
+constexpr uint64_t kmajor_step(int ks, int rows) { return (uint64_t)((ks >> 2) * rows * 8 + (ks & 3) * 2); }
+constexpr uint64_t mn_step(int ks) { return (uint64_t)ks * 128; }
+
+// Lane t of a group of four starts with four pieces of its own row and ends with piece t of the
+// four rows.
+__device__ __forceinline__ void trade4(uint4 (&r)[4], int lane) {
+#pragma unroll
+    for (int b = 1; b < 4; b <<= 1) {
+        const bool up = lane & b;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j & b) continue;
+            uint32_t *lo = &r[j].x, *hi = &r[j | b].x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo[i] : hi[i], b);
+                if (up) lo[i] = got; else hi[i] = got;
+            }
+        }
+    }
+}
+
+// log2 decays of tokens u .. u + 3 of the sequence (u >= limit: 0)
+__device__ __forceinline__ float4 load_decay(const LinDecay &g, const float *gp, int u, int limit) {
+    float4 d;
+    float *p = &d.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = (gp && u + i < limit) ? clamp_decay(gp[(long long)(u + i) * g.t]) * kLog2e : 0.f;
+    return d;
+}
+
+// ---- host
+inline bool token_map(CUtensorMap *map, const LinView &v, int D, int heads, long T, long B, int rows = kC) {
+    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)heads, (uint64_t)T, (uint64_t)B};
+    const uint64_t st[3] = {(uint64_t)v.h * 2, (uint64_t)v.t * 2, (uint64_t)v.b * 2};
+    const uint32_t box[4] = {64, 1, (uint32_t)rows, 1};
+    return make_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.p, dims, st, box, true);
+}
+
+inline size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+
+}  // namespace lin
+}  // namespace kda

@@ -1,0 +1,803 @@
+// linear_tc_bwd.cu -- gradients of linear attention with a decay per head on the tcgen05 tensor cores:
+// bf16, dk, dv in {64, 128}, chunks of C = 128 tokens.
+//
+// With S the memory entering a chunk, R the gradient of the memory leaving it, G the chunk's running log
+// decays, D_ij = e^{G_i - G_j} (j <= i), s = Q K^T, m = dO V^T and c the query scale:
+//
+//     dQ = diag(c e^G) dO S^T       + M K,          M_ij = c m_ij D_ij
+//     dK = diag(e^{G_C - G}) V R^T  + M^T Q
+//     dV = diag(e^{G_C - G}) K R    + P^T dO,       P_ij = c s_ij D_ij
+//     S' = e^{G_C} S + K^T diag(e^{G_C - G}) V,     R' = e^{G_C} R + Q^T diag(c e^G) dO   (R': into the chunk)
+//     ddecay_t = e^{G_C} <S, R> + sum_{i >= t} q_i . (first term of dQ)_i + sum_{j < t} k_j . (first term of dK)_j
+//                + sum_{j < t <= i} W_ij,           W_ij = c s_ij m_ij D_ij
+//
+// (what crosses token t: the memory through the whole chunk, into a later token, from an earlier token
+// out, or from an earlier to a later token; a sum over j < t <= i is a suffix sum of W's row sums less its
+// column sums, j < i only).  Every term of ddecay comes from fp32 products of exact or two-part operands
+// and is anchored in its own chunk, so nothing drifts along the sequence.
+//
+// Three launches for a group of (sequence, head) pairs:
+//   1  every chunk's own contribution to S' and to R', all chunks at once (the two are one kernel on other
+//      operands: the weighted values go in as three bf16 parts, as in the forward);
+//   2  the two chains over the chunks, elementwise and in place: each slot then holds S (or R);
+//   3  everything else, all chunks at once.
+// The memories of a group (2 x 4 dk dv bytes per chunk) stay within L2: 64 KB + 64 KB at d = 128 and at most
+// kGroupChunks chunks; a larger problem is taken group by group through the same scratch.
+//
+// Every wait is bounded; a time-out is recorded in the workspace header and the CTA unwinds.
+#include <algorithm>
+#include <initializer_list>
+
+#include "linear_tc.cuh"
+
+namespace kda {
+namespace {
+
+using namespace lin;
+
+// Chunks of a group: six for every SM, and 117 MB of memories at d = 128 (L2 is 129 MB)
+constexpr long kGroupChunks = 912;
+
+struct BwdParams {
+    LinDecay g;
+    int HV, m, T, nch;
+    long pair0;                 // first (sequence, head) pair of the group
+    int pairs;
+    float scale;
+    const float *h0, *dhT;      // whole arrays
+    float *dh0;
+    float *S, *R, *alpha;       // [pairs * nch][DK, DV] twice, [pairs * nch]
+    __nv_bfloat16 *dq, *dk, *dv;
+    long long qs[3], ks[3], vs[3];   // strides of dq, dk, dv: batch, token, head
+    float *fq, *fk;             // per-value-head fp32 dq, dk [B, T, HV, DK] when heads are shared
+    float *dg;                  // per-token ddecay [B, T, HV] or nullptr
+    WsHeader *hdr;
+};
+
+// ------------------------------------------------------------------------------ 1: contributions
+// Warps 0-7: weighted values (thread = value channel, half of the tokens); 8-11: results; 12: decays
+// and TMA; 13: products.  Items (direction, pair, chunk) go round the CTAs.
+constexpr int kPartThreads = 14 * 32;
+
+template <int DK, int DV>
+struct PartCfg {
+    static constexpr int KB = kC * DK * 2, VB = kC * DV * 2, STAGE = KB + VB;
+    static constexpr int NST = STAGE > 48 * 1024 ? 3 : 4;
+    static constexpr int ARR = NST * STAGE, CTL = ARR + NST * kC * 4, SMEM = CTL + 256;
+    static constexpr int T_V = 128;             // result [128], then two sets of hi, mid, lo
+    static_assert(T_V + 384 <= 512 && SMEM <= 232448, "TMEM, shared memory");
+};
+struct PartCtl {
+    uint64_t full[4], empty[4], ready[2], used[2], d_full, d_free, last;
+    uint32_t tmem;
+    int fail;
+};
+static_assert(sizeof(PartCtl) <= 256, "control block");
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kPartThreads, 1)
+linear_part_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, BwdParams w) {
+    using Cf = PartCfg<DK, DV>;
+    constexpr int NST = Cf::NST;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    PartCtl *ctl = reinterpret_cast<PartCtl *>(smem + Cf::CTL);
+    if ((smem_u32(smem) & 1023) || blockDim.x != kPartThreads) {
+        if (threadIdx.x == 0) atomicCAS(&w.hdr->error, 0, kStatusDeviceTimeout);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int slots = w.pairs * w.nch, items = 2 * slots;
+    const int mine = ((int)blockIdx.x < items) ? (items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+    if (tid == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&ctl->full[i], 1);
+            mbar_init(&ctl->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->ready[i], 256);
+            mbar_init(&ctl->used[i], 1);
+        }
+        mbar_init(&ctl->d_full, 1);
+        mbar_init(&ctl->d_free, 128);
+        mbar_init(&ctl->last, 1);
+        ctl->fail = 0;
+        fence_mbar_init();
+    }
+    if (warp == 13) {
+        tmem_alloc(&ctl->tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = ctl->tmem;
+    const Waits wt{&ctl->fail, w.hdr};
+    const uint32_t tlane = tm + ((uint32_t)(32 * (warp & 3)) << 16);
+    float *wa = reinterpret_cast<float *>(smem + Cf::ARR);
+    auto item_of = [&](int n) { return (int)blockIdx.x + n * (int)gridDim.x; };
+
+    if (warp == 12) {
+        for (int n = 0; n < mine; ++n) {
+            const int s = n % NST, item = item_of(n), dir = item >= slots, slot = item - dir * slots;
+            const int pi = slot / w.nch, c = slot - pi * w.nch, u = c * kC;
+            const long pair = w.pair0 + pi;
+            const int b = (int)(pair / w.HV), hv = (int)(pair % w.HV);
+            const float *gp = w.g.p ? w.g.p + b * w.g.b + hv : nullptr;
+            const float4 d = load_decay(w.g, gp, u + 4 * lane, w.T);
+            // sums behind a token (direction 0), up to and with it (direction 1)
+            float4 x = d, y = make_float4(d.y + (d.z + d.w), d.z + d.w, d.w, 0.f);
+            x.y += x.x; x.z += x.y; x.w += x.z;
+            float up = x.w, down = d.x + y.x;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float p = __shfl_up_sync(0xffffffffu, up, off), q = __shfl_down_sync(0xffffffffu, down, off);
+                if (lane >= off) up += p;
+                if (lane + off < 32) down += q;
+            }
+            float before = __shfl_up_sync(0xffffffffu, up, 1), behind = __shfl_down_sync(0xffffffffu, down, 1);
+            if (lane == 0) before = 0.f;
+            if (lane == 31) {
+                behind = 0.f;
+                if (!dir) w.alpha[slot] = ex2(up);
+            }
+            if (n >= NST && !wt.warp(&ctl->empty[s], (n / NST - 1) & 1, 41)) break;
+            *reinterpret_cast<float4 *>(wa + s * kC + 4 * lane) =
+                dir ? make_float4(w.scale * ex2(x.x + before), w.scale * ex2(x.y + before), w.scale * ex2(x.z + before),
+                                  w.scale * ex2(x.w + before))
+                    : make_float4(ex2(y.x + behind), ex2(y.y + behind), ex2(y.z + behind), ex2(behind));
+            __syncwarp();
+            if (lane == 0) {
+                uint8_t *st = smem + s * Cf::STAGE;
+                mbar_expect_tx(&ctl->full[s], Cf::STAGE);
+#pragma unroll
+                for (int i = 0; i < DK / 64; ++i)
+                    tma_load_4d(st + i * kC * 128, dir ? &mq : &mk, &ctl->full[s], 64 * i, hv / w.m, u, b);
+#pragma unroll
+                for (int i = 0; i < DV / 64; ++i)
+                    tma_load_4d(st + Cf::KB + i * kC * 128, dir ? &mo : &mv, &ctl->full[s], 64 * i, hv, u, b);
+            }
+        }
+    } else if (warp == 13) {
+        constexpr uint32_t id = idesc_bf16_f32(128, DK, false, true);
+        const uint32_t on = lane == 0;
+        for (int n = 0; n < mine; ++n) {
+            const int s = n % NST;
+            if (!wt.warp(&ctl->full[s], (n / NST) & 1, 42) || !wt.warp(&ctl->ready[n & 1], (n >> 1) & 1, 43)) break;
+            if (n > 0 && !wt.warp(&ctl->d_free, (n - 1) & 1, 44)) break;
+            tc_fence_after();
+            const uint64_t dk = desc_mnmajor_sw128(smem_u32(smem + s * Cf::STAGE), kC, 0);
+            const uint32_t a = tm + Cf::T_V + (n & 1) * 192;
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int ks = 0; ks < kC / 16; ++ks)
+                    mma_bf16_ts_on(on, tm, a + 64 * i + 8 * ks, dk + mn_step(ks), id, (uint32_t)(i + ks));
+            mma_commit_on(on, &ctl->used[n & 1]);
+            mma_commit_on(on, &ctl->empty[s]);
+            mma_commit_on(on, &ctl->d_full);
+        }
+    } else if (warp < 8) {
+        const int ch = tid & 127, half = tid >> 7;
+        const bool has = (ch & ~31) < DV;
+        for (int n = 0; n < mine; ++n) {
+            const int s = n % NST;
+            if (!wt.warp(&ctl->full[s], (n / NST) & 1, 45)) break;
+            if (n >= 2 && !wt.warp(&ctl->used[n & 1], ((n >> 1) - 1) & 1, 46)) break;
+            tc_fence_after();
+            const uint32_t a = tlane + Cf::T_V + (n & 1) * 192;
+            if (has) put_values<3>(smem + s * Cf::STAGE + Cf::KB, wa + s * kC, ch, 64 * half, a, a + 64, a + 128);
+            tc_fence_before();
+            mbar_arrive(&ctl->ready[n & 1]);
+        }
+    } else {
+        const int i = tid - 256;                // value channel
+        for (int n = 0; n < mine; ++n) {
+            const int item = item_of(n), dir = item >= slots, slot = item - dir * slots;
+            float *p = (dir ? w.R : w.S) + (size_t)slot * DK * DV + i;
+            if (!wt.warp(&ctl->d_full, n & 1, 47)) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int cb = 0; cb < DK; cb += 32) {
+                uint32_t x[32];
+                tmem_ld32(tlane + cb, x);
+                tmem_ld_wait();
+                if (cb + 32 == DK) {
+                    tc_fence_before();
+                    mbar_arrive(&ctl->d_free);
+                }
+                if (i < DV)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) p[(cb + j) * DV] = __uint_as_float(x[j]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 13) {
+        mma_commit_on(lane == 0, &ctl->last);
+        (void)mbar_wait(&ctl->last, 0, kWaitNs);
+        if (ctl->fail) {                        // let what is in flight land
+            const uint64_t t = globaltimer_ns();
+            while (globaltimer_ns() - t < 1000000ull) {
+            }
+        }
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tm, 512);
+    }
+}
+
+// ------------------------------------------------------------------------------ 2: the chains
+// In place: a slot's contribution becomes the memory entering its chunk (S), or the gradient of the one
+// leaving it (R).  Bound by L2: eight slots' loads are in flight per thread.
+__global__ void __launch_bounds__(256) linear_chain_kernel(BwdParams w, int cells) {
+    const int per = cells / 4, e = blockIdx.x * 256 + threadIdx.x;
+    if (e >= per * w.pairs) return;
+    const int pi = e / per, at = (e - pi * per) * 4;
+    const bool rev = blockIdx.y;
+    const size_t pc = (size_t)(w.pair0 + pi) * cells + at;
+    const float *init = rev ? w.dhT : w.h0;
+    float4 s = init ? *reinterpret_cast<const float4 *>(init + pc) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float *base = (rev ? w.R : w.S) + (size_t)pi * w.nch * cells + at;
+    const float *al = w.alpha + (size_t)pi * w.nch;
+    constexpr int U = 8;
+    for (int c0 = 0; c0 < w.nch; c0 += U) {
+        float4 x[U];
+        float a[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int c = rev ? w.nch - 1 - (c0 + i) : c0 + i;
+            if (c0 + i < w.nch) {
+                x[i] = *reinterpret_cast<const float4 *>(base + (size_t)c * cells);
+                a[i] = al[c];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int c = rev ? w.nch - 1 - (c0 + i) : c0 + i;
+            if (c0 + i < w.nch) {
+                *reinterpret_cast<float4 *>(base + (size_t)c * cells) = s;
+                s.x = fmaf(a[i], s.x, x[i].x); s.y = fmaf(a[i], s.y, x[i].y);
+                s.z = fmaf(a[i], s.z, x[i].z); s.w = fmaf(a[i], s.w, x[i].w);
+            }
+        }
+    }
+    if (rev && w.dh0) *reinterpret_cast<float4 *>(w.dh0 + pc) = s;
+}
+
+// ------------------------------------------------------------------------------ 3: gradients
+// One chunk at a time per CTA.  Warps 0-7 compute (thread = token row of the TMEM lanes, half of the
+// columns), warp 8 loads and issues.  TMEM: K Q^T, V dO^T, Q K^T, dO V^T in four blocks of 128 columns; then P^T
+// over the first, M^T over the second, M over the fourth; dQ gathers in the third, dK in the fourth
+// once M is used, dV in the second once M^T is.
+// The first terms of dQ and dK are read back before their second terms are added: they take their row factor
+// there, and their dots with q and k (S and R go in as two bf16 parts for those dots).
+constexpr int kGradThreads = 9 * 32;
+
+template <int DK, int DV>
+struct GradCfg {
+    static constexpr int QB = kC * DK * 2, VB = kC * DV * 2, XB = DK * DV * 2;
+    static constexpr int Q = 0, K = QB, V = 2 * QB, O = 2 * QB + VB, XH = 2 * QB + 2 * VB, XL = XH + XB;
+    static constexpr int ARR = XL + XB;         // G, then halves of: r, c, q dots, k dots
+    static constexpr int CTL = ARR + 9 * kC * 4, SMEM = CTL + 256;
+    static_assert(SMEM <= 232448, "shared memory");
+};
+struct GradCtl {
+    uint64_t full, m, go, sync, last;
+    uint32_t tmem;
+    int fail;
+    float dot[8];
+};
+static_assert(sizeof(GradCtl) <= 256, "control block");
+
+// 64 (or 32) columns of a row of results, bf16, four lanes trading 16-byte pieces (rows u0 .. u0 + 3)
+template <int N>
+__device__ __forceinline__ void store_rows(uint32_t taddr, __nv_bfloat16 *p, long long ts, int rows, int lane) {
+#pragma unroll 1
+    for (int cb = 0; cb < N; cb += 32) {
+        uint32_t x[32];
+        tmem_ld32(taddr + cb, x);
+        tmem_ld_wait();
+        uint4 r[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t *pr = &r[j].x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                pr[i] = pack_bf16(__uint_as_float(x[8 * j + 2 * i]), __uint_as_float(x[8 * j + 2 * i + 1]));
+        }
+        trade4(r, lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < rows) *reinterpret_cast<uint4 *>(p + (long long)j * ts + cb) = r[j];
+    }
+}
+// the same in fp32, a row to a thread (only where q/k heads are shared)
+template <int N>
+__device__ __forceinline__ void store_row_f32(uint32_t taddr, float *p, bool live) {
+#pragma unroll 1
+    for (int cb = 0; cb < N; cb += 32) {
+        uint32_t x[32];
+        tmem_ld32(taddr + cb, x);
+        tmem_ld_wait();
+        if (live)
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+                *reinterpret_cast<uint4 *>(p + cb + j) = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+    }
+}
+// Row factor f on N columns in place; the dot of the scaled row with columns c0 .. of row r of a bf16 tile
+template <int N, bool DOT>
+__device__ __forceinline__ float scale_row(uint32_t taddr, float f, const uint8_t *tile, int r, int c0) {
+    float dot = 0.f;
+#pragma unroll 1
+    for (int cb = 0; cb < N; cb += 32) {
+        uint32_t x[32];
+        tmem_ld32(taddr + cb, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+            uint4 t;
+            if constexpr (DOT) t = *reinterpret_cast<const uint4 *>(tile + piece(kC, r, (c0 + cb + j) / 8));
+            const uint32_t *pt = &t.x;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float v = f * __uint_as_float(x[j + i]);
+                x[j + i] = __float_as_uint(v);
+                if constexpr (DOT)
+                    dot = fmaf(v, __uint_as_float((i & 1) ? (pt[i / 2] & 0xffff0000u) : (pt[i / 2] << 16)), dot);
+            }
+        }
+        tmem_st32(taddr + cb, x);
+    }
+    tmem_st_wait();
+    return dot;
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kGradThreads, 1)
+linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, BwdParams w) {
+    using Cf = GradCfg<DK, DV>;
+    constexpr uint32_t R0 = 0, R1 = 128, R2 = 256, R3 = 384;
+    constexpr int NX = DK * DV / 8 / 256;       // 8-value pieces of a memory per thread
+    extern __shared__ __align__(1024) uint8_t smem[];
+    GradCtl *ctl = reinterpret_cast<GradCtl *>(smem + Cf::CTL);
+    if ((smem_u32(smem) & 1023) || blockDim.x != kGradThreads) {
+        if (threadIdx.x == 0) atomicCAS(&w.hdr->error, 0, kStatusDeviceTimeout);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int slots = w.pairs * w.nch;
+    if (tid == 0) {
+        mbar_init(&ctl->full, 1);
+        mbar_init(&ctl->m, 1);
+        mbar_init(&ctl->go, 256);
+        mbar_init(&ctl->sync, 256);
+        mbar_init(&ctl->last, 1);
+        ctl->fail = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(&ctl->tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = ctl->tmem;
+    const Waits wt{&ctl->fail, w.hdr};
+
+    if (warp == 8) {
+        constexpr uint32_t ida = idesc_bf16_f32(128, 128, false, false);
+        constexpr uint32_t idx = idesc_bf16_f32(128, DK, false, false);
+        constexpr uint32_t idk = idesc_bf16_f32(128, DK, false, true);
+        constexpr uint32_t idv = idesc_bf16_f32(128, DV, false, true);
+        const uint32_t on = lane == 0;
+        const uint32_t sb = smem_u32(smem);
+        const uint64_t q = desc_kmajor_sw128(sb + Cf::Q, kC, 0), k = desc_kmajor_sw128(sb + Cf::K, kC, 0),
+                       v = desc_kmajor_sw128(sb + Cf::V, kC, 0), o = desc_kmajor_sw128(sb + Cf::O, kC, 0);
+        const uint64_t qn = desc_mnmajor_sw128(sb + Cf::Q, kC, 0), kn = desc_mnmajor_sw128(sb + Cf::K, kC, 0),
+                       on_ = desc_mnmajor_sw128(sb + Cf::O, kC, 0);
+        const uint64_t xh = desc_kmajor_sw128(sb + Cf::XH, DK, 0), xl = desc_kmajor_sw128(sb + Cf::XL, DK, 0),
+                       xn = desc_mnmajor_sw128(sb + Cf::XH, DK, 0);
+        auto load = [&](int slot) {
+            const int pi = slot / w.nch, u = (slot - pi * w.nch) * kC;
+            const long pair = w.pair0 + pi;
+            const int b = (int)(pair / w.HV), hv = (int)(pair % w.HV);
+            if (lane == 0) {
+                mbar_expect_tx(&ctl->full, 2 * Cf::QB + 2 * Cf::VB);
+#pragma unroll
+                for (int i = 0; i < DK / 64; ++i) {
+                    tma_load_4d(smem + Cf::Q + i * kC * 128, &mq, &ctl->full, 64 * i, hv / w.m, u, b);
+                    tma_load_4d(smem + Cf::K + i * kC * 128, &mk, &ctl->full, 64 * i, hv / w.m, u, b);
+                }
+#pragma unroll
+                for (int i = 0; i < DV / 64; ++i) {
+                    tma_load_4d(smem + Cf::V + i * kC * 128, &mv, &ctl->full, 64 * i, hv, u, b);
+                    tma_load_4d(smem + Cf::O + i * kC * 128, &mo, &ctl->full, 64 * i, hv, u, b);
+                }
+            }
+            __syncwarp();
+        };
+        // token tile times token tile, both K-major
+        auto gram = [&](uint32_t d, uint64_t a, uint64_t bb, int D) {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+                if (ks < D / 16) mma_bf16_ss_on(on, tm + d, a + kmajor_step(ks, kC), bb + kmajor_step(ks, kC), ida, ks > 0);
+        };
+        // token tile [., dv] times X^T
+        auto into = [&](uint64_t a) {
+            return [&, a](uint32_t d) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int ks = 0; ks < DV / 16; ++ks)
+                        mma_bf16_ss_on(on, tm + d, a + kmajor_step(ks, kC), (i ? xl : xh) + kmajor_step(ks, DK), idx, i + ks > 0);
+            };
+        };
+        // A in TMEM times a token tile
+        auto spread = [&](uint32_t d, uint32_t a, uint64_t bb, uint32_t id) {
+#pragma unroll
+            for (int ks = 0; ks < kC / 16; ++ks) mma_bf16_ts_on(on, tm + d, tm + a + 8 * ks, bb + mn_step(ks), id, 1u);
+        };
+        int n = 0, ph = 0;                       // items; phases of `go` seen
+        auto next = [&]() {
+            const bool ok = wt.warp(&ctl->go, ph & 1, 52);
+            ++ph;
+            tc_fence_after();
+            return ok;
+        };
+        if ((int)blockIdx.x < slots) load(blockIdx.x);
+        for (int slot = blockIdx.x; slot < slots; slot += gridDim.x, ++n) {
+            if (!wt.warp(&ctl->full, n & 1, 51)) break;
+            tc_fence_after();
+            gram(R0, k, q, DK);
+            gram(R1, v, o, DV);
+            gram(R2, q, k, DK);
+            gram(R3, o, v, DV);
+            mma_commit_on(on, &ctl->m);
+            if (!next()) break;
+            into(o)(R2);                         // dO S^T
+            mma_commit_on(on, &ctl->m);
+            if (!next()) break;
+            spread(R2, R3, kn, idk);             // + M K
+            into(v)(R3);                         // V R^T
+            mma_commit_on(on, &ctl->m);
+            if (!next()) break;
+            spread(R3, R1, qn, idk);             // + M^T Q
+#pragma unroll
+            for (int ks = 0; ks < DK / 16; ++ks)  // K R
+                mma_bf16_ss_on(on, tm + R1, k + kmajor_step(ks, kC), xn + mn_step(ks), idv, ks > 0);
+            mma_commit_on(on, &ctl->m);
+            if (!next()) break;
+            spread(R1, R0, on_, idv);            // + P^T dO
+            mma_commit_on(on, &ctl->m);
+            if (!next()) break;                  // the last results are read, so the tiles are dead too
+            if (slot + (int)gridDim.x < slots) load(slot + gridDim.x);
+        }
+    } else {
+        const int quad = warp & 3, half = warp >> 2, row = 32 * quad + lane;
+        const uint32_t tl = tm + ((uint32_t)(32 * quad) << 16);
+        float *ga = reinterpret_cast<float *>(smem + Cf::ARR);
+        float *ar = ga + kC + half * kC, *ac = ar + 2 * kC, *aq = ac + 2 * kC, *ak = aq + 2 * kC;   // this half's
+        int ph = 0, sp = 0;                      // phases of `m` and `sync` seen
+        auto done = [&](int where) {
+            const bool ok = wt.warp(&ctl->m, ph & 1, where);
+            ++ph;
+            tc_fence_after();
+            return ok;
+        };
+        auto meet = [&]() {
+            mbar_arrive(&ctl->sync);
+            const bool ok = wt.warp(&ctl->sync, sp & 1, 60);
+            ++sp;
+            return ok;
+        };
+        auto go = [&]() {
+            fence_proxy_async();
+            tc_fence_before();
+            mbar_arrive(&ctl->go);
+        };
+        // a memory's pieces of this thread, as two bf16 parts (16 bits) into the operand tiles
+        auto put_x = [&](const float4 (&x)[2 * NX]) {
+#pragma unroll
+            for (int p = 0; p < NX; ++p) {
+                const int e = tid + 256 * p, r = e / (DV / 8), c = e % (DV / 8);
+                const float f[8] = {x[2 * p].x, x[2 * p].y, x[2 * p].z, x[2 * p].w,
+                                    x[2 * p + 1].x, x[2 * p + 1].y, x[2 * p + 1].z, x[2 * p + 1].w};
+                uint4 h, l;
+                uint32_t *ph_ = &h.x, *pl = &l.x;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    ph_[i] = pack_bf16(f[2 * i], f[2 * i + 1]);   // rounded: dV takes this part alone
+                    pl[i] = pack_bf16(f[2 * i] - __uint_as_float(ph_[i] << 16),
+                                      f[2 * i + 1] - __uint_as_float(ph_[i] & 0xffff0000u));
+                }
+                *reinterpret_cast<uint4 *>(smem + Cf::XH + piece(DK, r, c)) = h;
+                *reinterpret_cast<uint4 *>(smem + Cf::XL + piece(DK, r, c)) = l;
+            }
+        };
+        int it = 0;
+        for (int slot = blockIdx.x; slot < slots; slot += gridDim.x, ++it) {
+            const int pi = slot / w.nch, u = (slot - pi * w.nch) * kC;
+            const long pair = w.pair0 + pi;
+            const int b = (int)(pair / w.HV), hv = (int)(pair % w.HV);
+            const int live = w.T - u;            // tokens of the chunk (more: all 128)
+            // ---- S, the decays
+            float4 xs[2 * NX];
+            const float4 *ps = reinterpret_cast<const float4 *>(w.S + (size_t)slot * DK * DV);
+#pragma unroll
+            for (int p = 0; p < NX; ++p) {
+                xs[2 * p] = ps[2 * (tid + 256 * p)];
+                xs[2 * p + 1] = ps[2 * (tid + 256 * p) + 1];
+            }
+            if (warp == 0) {
+                const float *gp = w.g.p ? w.g.p + b * w.g.b + hv : nullptr;
+                float4 x = load_decay(w.g, gp, u + 4 * lane, w.T);
+                x.y += x.x; x.z += x.y; x.w += x.z;
+                float up = x.w;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const float y = __shfl_up_sync(0xffffffffu, up, off);
+                    if (lane >= off) up += y;
+                }
+                float before = __shfl_up_sync(0xffffffffu, up, 1);
+                if (lane == 0) before = 0.f;
+                *reinterpret_cast<float4 *>(ga + 4 * lane) = make_float4(x.x + before, x.y + before, x.z + before, x.w + before);
+            }
+            put_x(xs);
+            if (!meet()) break;
+            const float gr = ga[row], gc = ga[kC - 1];
+            if (!wt.warp(&ctl->full, it & 1, 58) || !done(53)) break;
+            // ---- P^T, M^T of this row j and its half of the i; M of this row i and its half of the j; sums of W
+            uint32_t pt[32], mt[32], mm[32];
+            float cs = 0.f, rs = 0.f;
+#pragma unroll
+            for (int blk = 0; blk < 4; ++blk) {
+                const int i0 = 64 * half + 16 * blk;
+                if (i0 + 15 < 32 * quad) {       // all before the row's tokens
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) pt[8 * blk + j] = mt[8 * blk + j] = 0u;
+                } else {
+                    uint32_t x[16], y[16];
+                    tmem_ld16(tl + R0 + i0, x);
+                    tmem_ld16(tl + R1 + i0, y);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        float a[2], c[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int i = i0 + j + e;
+                            const float d = i >= row ? w.scale * ex2(ga[i] - gr) : 0.f;
+                            const float sx = __uint_as_float(x[j + e]), mx = __uint_as_float(y[j + e]);
+                            a[e] = i >= row ? sx * d : 0.f;
+                            c[e] = i >= row ? mx * d : 0.f;
+                            if (i > row) cs = fmaf(sx, c[e], cs);
+                        }
+                        pt[8 * blk + j / 2] = pack_bf16(a[0], a[1]);
+                        mt[8 * blk + j / 2] = pack_bf16(c[0], c[1]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int blk = 0; blk < 4; ++blk) {
+                const int j0 = 64 * half + 16 * blk;
+                if (j0 > 32 * quad + 31) {       // all after the row's tokens
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) mm[8 * blk + j] = 0u;
+                } else {
+                    uint32_t x[16], y[16];
+                    tmem_ld16(tl + R2 + j0, x);
+                    tmem_ld16(tl + R3 + j0, y);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        float c[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int jj = j0 + j + e;
+                            const float d = jj <= row ? w.scale * ex2(gr - ga[jj]) : 0.f;
+                            c[e] = jj <= row ? __uint_as_float(y[j + e]) * d : 0.f;
+                            if (jj < row) rs = fmaf(__uint_as_float(x[j + e]), c[e], rs);
+                        }
+                        mm[8 * blk + j / 2] = pack_bf16(c[0], c[1]);
+                    }
+                }
+            }
+            ar[row] = rs;
+            ac[row] = cs;
+            tc_fence_before();
+            if (!meet()) break;                  // both halves have read their columns
+            tc_fence_after();
+            tmem_st32(tl + R0 + 32 * half, pt);
+            tmem_st32(tl + R1 + 32 * half, mt);
+            tmem_st32(tl + R3 + 32 * half, mm);
+            tmem_st_wait();
+            go();
+            // ---- R; first term of dQ
+            float4 xr[2 * NX];
+            const float4 *pr = reinterpret_cast<const float4 *>(w.R + (size_t)slot * DK * DV);
+#pragma unroll
+            for (int p = 0; p < NX; ++p) {
+                xr[2 * p] = pr[2 * (tid + 256 * p)];
+                xr[2 * p + 1] = pr[2 * (tid + 256 * p) + 1];
+            }
+            float dot = 0.f;
+#pragma unroll
+            for (int p = 0; p < 2 * NX; ++p)
+                dot = fmaf(xs[p].x, xr[p].x, fmaf(xs[p].y, xr[p].y, fmaf(xs[p].z, xr[p].z, fmaf(xs[p].w, xr[p].w, dot))));
+#pragma unroll
+            for (int off = 16; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+            if (lane == 0) ctl->dot[warp] = dot;
+            if (!done(54)) break;
+            put_x(xr);
+            const float eg = w.scale * ex2(gr), ew = ex2(gc - gr);
+            aq[row] = scale_row<DK / 2, true>(tl + R2 + half * (DK / 2), eg, smem + Cf::Q, row, half * (DK / 2));
+            go();
+            // ---- dQ out; first term of dK
+            const int u0 = u + (row & ~3), rows = min(4, w.T - u0), l8 = 8 * (lane & 3);
+            const long long tok = (long long)b * w.T + u + row;
+            if (!done(55)) break;
+            if (w.fq)
+                store_row_f32<DK / 2>(tl + R2 + half * (DK / 2), w.fq + (tok * w.HV + hv) * DK + half * (DK / 2), row < live);
+            else
+                store_rows<DK / 2>(tl + R2 + half * (DK / 2),
+                                   w.dq + b * w.qs[0] + (long long)u0 * w.qs[1] + hv * w.qs[2] + half * (DK / 2) + l8,
+                                   w.qs[1], rows, lane);
+            ak[row] = scale_row<DK / 2, true>(tl + R3 + half * (DK / 2), ew, smem + Cf::K, row, half * (DK / 2));
+            go();
+            // ---- dK out; first term of dV
+            if (!done(56)) break;
+            if (w.fk)
+                store_row_f32<DK / 2>(tl + R3 + half * (DK / 2), w.fk + (tok * w.HV + hv) * DK + half * (DK / 2), row < live);
+            else
+                store_rows<DK / 2>(tl + R3 + half * (DK / 2),
+                                   w.dk + b * w.ks[0] + (long long)u0 * w.ks[1] + hv * w.ks[2] + half * (DK / 2) + l8,
+                                   w.ks[1], rows, lane);
+            scale_row<DV / 2, false>(tl + R1 + half * (DV / 2), ew, nullptr, 0, 0);
+            go();
+            // ---- ddecay (the dots and sums of both halves are in); dV out
+            if (w.dg) {
+                if (!meet()) break;
+                if (warp == 0) {
+                    const float *a0 = ga + kC;
+                    float f[4], kd[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int t = 4 * lane + i;
+                        f[i] = (a0[t] + a0[kC + t]) - (a0[2 * kC + t] + a0[3 * kC + t]) + (a0[4 * kC + t] + a0[5 * kC + t]);
+                        kd[i] = a0[6 * kC + t] + a0[7 * kC + t];
+                    }
+                    float fs = (f[0] + f[1]) + (f[2] + f[3]), kk = (kd[0] + kd[1]) + (kd[2] + kd[3]);
+                    float down = fs, up = kk;    // over this and the later lanes; this and the earlier
+#pragma unroll
+                    for (int off = 1; off < 32; off <<= 1) {
+                        const float x = __shfl_down_sync(0xffffffffu, down, off), y = __shfl_up_sync(0xffffffffu, up, off);
+                        if (lane + off < 32) down += x;
+                        if (lane >= off) up += y;
+                    }
+                    float all = 0.f;
+                    for (int i = 0; i < 8; ++i) all += ctl->dot[i];
+                    float behind = __shfl_down_sync(0xffffffffu, down, 1), before = __shfl_up_sync(0xffffffffu, up, 1);
+                    if (lane == 31) behind = 0.f;
+                    if (lane == 0) before = 0.f;
+                    all *= ex2(gc);
+                    float suf[4];
+                    suf[3] = behind + f[3]; suf[2] = suf[3] + f[2]; suf[1] = suf[2] + f[1]; suf[0] = suf[1] + f[0];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int t = u + 4 * lane + i;
+                        if (t < w.T) w.dg[((long long)b * w.T + t) * w.HV + hv] = all + suf[i] + before;
+                        before += kd[i];
+                    }
+                }
+            }
+            if (!done(57)) break;
+            store_rows<DV / 2>(tl + R1 + half * (DV / 2),
+                               w.dv + b * w.vs[0] + (long long)u0 * w.vs[1] + hv * w.vs[2] + half * (DV / 2) + l8, w.vs[1],
+                               rows, lane);
+            go();
+            if (!meet()) break;                  // the shared sums are free for the next chunk
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        mma_commit_on(lane == 0, &ctl->last);
+        (void)mbar_wait(&ctl->last, 0, kWaitNs);
+        if (ctl->fail) {                         // let what is in flight land
+            const uint64_t t = globaltimer_ns();
+            while (globaltimer_ns() - t < 1000000ull) {
+            }
+        }
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tm, 512);
+    }
+}
+
+// ------------------------------------------------------------------------------ host
+long group_pairs(long pairs, int nch) { return std::max(1L, std::min(pairs, kGroupChunks / nch)); }
+
+template <int DK, int DV>
+cudaError_t run_groups(const LinBwd &a, BwdParams w, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                       const CUtensorMap &mo, cudaStream_t st) {
+    using PC = PartCfg<DK, DV>;
+    using GC = GradCfg<DK, DV>;
+    cudaError_t e = cudaFuncSetAttribute(linear_part_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, PC::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(linear_grad_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, GC::SMEM);
+    if (e != cudaSuccess) return e;
+    const long pairs = (long)a.B * a.HV, np = group_pairs(pairs, w.nch);
+    constexpr int cells = DK * DV;
+    for (long p0 = 0; p0 < pairs; p0 += np) {
+        w.pair0 = p0;
+        w.pairs = (int)std::min(np, pairs - p0);
+        const int slots = w.pairs * w.nch;
+        linear_part_kernel<DK, DV><<<std::min(2 * slots, a.sms), kPartThreads, PC::SMEM, st>>>(mq, mk, mv, mo, w);
+        const dim3 grid((unsigned)(((long)w.pairs * (cells / 4) + 255) / 256), 2);
+        linear_chain_kernel<<<grid, 256, 0, st>>>(w, cells);
+        linear_grad_kernel<DK, DV><<<std::min(slots, a.sms), kGradThreads, GC::SMEM, st>>>(mq, mk, mv, mo, w);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+// Scratch: [S][R][chunk decays] of a group, [per-value-head dq, dk] when heads are shared, [per-token ddecay]
+size_t linear_tc_bwd_scratch_bytes(int B, int T, int H, int HV, int dk, int dv, int sms) {
+    (void)sms;
+    const int nch = (T + kC - 1) / kC;
+    const size_t slots = (size_t)group_pairs((long)B * HV, nch) * nch, rows = (size_t)B * T * HV;
+    size_t n = 2 * round256(slots * dk * dv * 4) + round256(slots * 4) + round256(rows * 4);
+    if (HV > H) n += 2 * round256(rows * dk * 4);
+    return n;
+}
+
+cudaError_t launch_linear_tc_bwd(const LinBwd &a, cudaStream_t st) {
+    BwdParams w{};
+    const int m = a.HV / a.H;
+    w.g = a.g; w.HV = a.HV; w.m = m; w.T = a.T; w.nch = (a.T + kC - 1) / kC; w.scale = a.scale;
+    w.h0 = a.h0; w.dhT = a.dhT; w.dh0 = a.dh0; w.hdr = a.hdr;
+    const size_t slots = (size_t)group_pairs((long)a.B * a.HV, w.nch) * w.nch, rows = (size_t)a.B * a.T * a.HV;
+    char *p = static_cast<char *>(a.ws);
+    auto carve = [&](size_t n) { char *r = p; p += round256(n); return reinterpret_cast<float *>(r); };
+    w.S = carve(slots * a.dk * a.dv * 4);
+    w.R = carve(slots * a.dk * a.dv * 4);
+    w.alpha = carve(slots * 4);
+    float *dgt = carve(rows * 4);
+    if (m > 1) {
+        w.fq = carve(rows * a.dk * 4);
+        w.fk = carve(rows * a.dk * 4);
+    }
+    const bool want_g = a.g.p && a.dg, fixed = want_g && a.g.t == 0;
+    w.dg = want_g ? (fixed ? dgt : a.dg) : nullptr;
+    auto out = [](const LinView &v, __nv_bfloat16 *&q, long long (&s)[3]) {
+        q = static_cast<__nv_bfloat16 *>(const_cast<void *>(v.p));
+        s[0] = v.b; s[1] = v.t; s[2] = v.h;
+    };
+    out(a.dq, w.dq, w.qs);
+    out(a.dk_, w.dk, w.ks);
+    out(a.dv_, w.dv, w.vs);
+    CUtensorMap mq, mk, mv, mo;
+    if (!token_map(&mq, a.q, a.dk, a.H, a.T, a.B) || !token_map(&mk, a.k, a.dk, a.H, a.T, a.B) ||
+        !token_map(&mv, a.v, a.dv, a.HV, a.T, a.B) || !token_map(&mo, a.d_o, a.dv, a.HV, a.T, a.B))
+        return cudaErrorInvalidValue;
+    cudaError_t e;
+    if (a.dk == 128 && a.dv == 128) e = run_groups<128, 128>(a, w, mq, mk, mv, mo, st);
+    else if (a.dk == 128) e = run_groups<128, 64>(a, w, mq, mk, mv, mo, st);
+    else if (a.dv == 128) e = run_groups<64, 128>(a, w, mq, mk, mv, mo, st);
+    else e = run_groups<64, 64>(a, w, mq, mk, mv, mo, st);
+    if (e != cudaSuccess) return e;
+    if (m > 1) {
+        if ((e = launch_fold_heads(w.fq, a.dq, a.dtype, a.B, a.T, a.H, m, a.dk, st)) != cudaSuccess) return e;
+        if ((e = launch_fold_heads(w.fk, a.dk_, a.dtype, a.B, a.T, a.H, m, a.dk, st)) != cudaSuccess) return e;
+    }
+    return fixed ? launch_sum_rows(dgt, a.dg, (long)a.B * a.T, a.HV, st) : cudaSuccess;
+}
+
+}  // namespace kda
