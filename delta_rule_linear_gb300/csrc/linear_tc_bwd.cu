@@ -267,89 +267,80 @@ __global__ void __launch_bounds__(256) linear_chain_kernel(BwdParams w, int cell
 }
 
 // ------------------------------------------------------------------------------ 3: gradients
-// One chunk at a time per CTA.  Warps 0-7 compute (thread = token row of the TMEM lanes, half of the
-// columns), warp 8 loads and issues.  TMEM: K Q^T, V dO^T, Q K^T, dO V^T in four blocks of 128 columns; then P^T
-// over the first, M^T over the second, M over the fourth; dQ gathers in the third, dK in the fourth
-// once M is used, dV in the second once M^T is.
+// One chunk at a time per CTA.  Warps 0-15 compute (thread = token row of the TMEM lanes, a quarter of the
+// columns), warp 16 loads and issues.  TMEM: K Q^T, V dO^T, Q K^T, dO V^T in four blocks of 128 columns; then P^T
+// over the first, M^T over the second, M over the fourth, every quarter's packed pairs in the lower half
+// of its own columns; dQ gathers in the third, dK in the fourth once M is used, dV in the second once
+// M^T is.  Loops are kept rolled and what is used three times out of line: the chunk's code runs once per
+// chunk, and instruction fetch is what a longer one waits for (8 warps and unrolled passes: 0.109 ms at
+// the training shape instead of 0.067).
 // The first terms of dQ and dK are read back before their second terms are added: they take their row factor
 // there, and their dots with q and k (S and R go in as two bf16 parts for those dots).
-constexpr int kGradThreads = 9 * 32;
+constexpr int kGradThreads = 17 * 32;
 
 template <int DK, int DV>
 struct GradCfg {
     static constexpr int QB = kC * DK * 2, VB = kC * DV * 2, XB = DK * DV * 2;
     static constexpr int Q = 0, K = QB, V = 2 * QB, O = 2 * QB + VB, XH = 2 * QB + 2 * VB, XL = XH + XB;
-    static constexpr int ARR = XL + XB;         // G, then halves of: r, c, q dots, k dots
-    static constexpr int CTL = ARR + 9 * kC * 4, SMEM = CTL + 256;
+    static constexpr int ARR = XL + XB;         // G, then quarters of: r, c, q dots, k dots
+    static constexpr int CTL = ARR + 17 * kC * 4, SMEM = CTL + 256;
     static_assert(SMEM <= 232448, "shared memory");
 };
 struct GradCtl {
     uint64_t full, m, go, sync, last;
     uint32_t tmem;
     int fail;
-    float dot[8];
+    float dot[16];
 };
 static_assert(sizeof(GradCtl) <= 256, "control block");
 
-// 64 (or 32) columns of a row of results, bf16, four lanes trading 16-byte pieces (rows u0 .. u0 + 3)
-template <int N>
-__device__ __forceinline__ void store_rows(uint32_t taddr, __nv_bfloat16 *p, long long ts, int rows, int lane) {
-#pragma unroll 1
-    for (int cb = 0; cb < N; cb += 32) {
-        uint32_t x[32];
-        tmem_ld32(taddr + cb, x);
-        tmem_ld_wait();
-        uint4 r[4];
+// 32 columns of a row of results, bf16, four lanes trading 16-byte pieces (rows u0 .. u0 + 3)
+__device__ __noinline__ void store_rows(uint32_t taddr, __nv_bfloat16 *p, long long ts, int rows, int lane) {
+    uint32_t x[32];
+    tmem_ld32(taddr, x);
+    tmem_ld_wait();
+    uint4 r[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t *pr = &r[j].x;
+    for (int j = 0; j < 4; ++j) {
+        uint32_t *pr = &r[j].x;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                pr[i] = pack_bf16(__uint_as_float(x[8 * j + 2 * i]), __uint_as_float(x[8 * j + 2 * i + 1]));
-        }
-        trade4(r, lane);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j < rows) *reinterpret_cast<uint4 *>(p + (long long)j * ts + cb) = r[j];
+        for (int i = 0; i < 4; ++i)
+            pr[i] = pack_bf16(__uint_as_float(x[8 * j + 2 * i]), __uint_as_float(x[8 * j + 2 * i + 1]));
     }
+    trade4(r, lane);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (j < rows) *reinterpret_cast<uint4 *>(p + (long long)j * ts) = r[j];
 }
 // the same in fp32, a row to a thread (only where q/k heads are shared)
-template <int N>
-__device__ __forceinline__ void store_row_f32(uint32_t taddr, float *p, bool live) {
-#pragma unroll 1
-    for (int cb = 0; cb < N; cb += 32) {
-        uint32_t x[32];
-        tmem_ld32(taddr + cb, x);
-        tmem_ld_wait();
-        if (live)
+__device__ __noinline__ void store_row_f32(uint32_t taddr, float *p, bool live) {
+    uint32_t x[32];
+    tmem_ld32(taddr, x);
+    tmem_ld_wait();
+    if (live)
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-                *reinterpret_cast<uint4 *>(p + cb + j) = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-    }
+        for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<uint4 *>(p + j) = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
 }
-// Row factor f on N columns in place; the dot of the scaled row with columns c0 .. of row r of a bf16 tile
-template <int N, bool DOT>
-__device__ __forceinline__ float scale_row(uint32_t taddr, float f, const uint8_t *tile, int r, int c0) {
+// Row factor f on 32 columns in place; the dot of the scaled row with columns c0 .. of row r of a bf16 tile
+// (nullptr: 0)
+__device__ __noinline__ float scale_row(uint32_t taddr, float f, const uint8_t *tile, int r, int c0) {
     float dot = 0.f;
-#pragma unroll 1
-    for (int cb = 0; cb < N; cb += 32) {
-        uint32_t x[32];
-        tmem_ld32(taddr + cb, x);
-        tmem_ld_wait();
+    uint32_t x[32];
+    tmem_ld32(taddr, x);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(f * __uint_as_float(x[i]));
+    tmem_st32(taddr, x);
+    if (tile) {
 #pragma unroll
         for (int j = 0; j < 32; j += 8) {
-            uint4 t;
-            if constexpr (DOT) t = *reinterpret_cast<const uint4 *>(tile + piece(kC, r, (c0 + cb + j) / 8));
+            const uint4 t = *reinterpret_cast<const uint4 *>(tile + piece(kC, r, (c0 + j) / 8));
             const uint32_t *pt = &t.x;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float v = f * __uint_as_float(x[j + i]);
-                x[j + i] = __float_as_uint(v);
-                if constexpr (DOT)
-                    dot = fmaf(v, __uint_as_float((i & 1) ? (pt[i / 2] & 0xffff0000u) : (pt[i / 2] << 16)), dot);
-            }
+            for (int i = 0; i < 8; ++i)
+                dot = fmaf(__uint_as_float(x[j + i]), __uint_as_float((i & 1) ? (pt[i / 2] & 0xffff0000u) : (pt[i / 2] << 16)), dot);
         }
-        tmem_st32(taddr + cb, x);
     }
     tmem_st_wait();
     return dot;
@@ -361,7 +352,7 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, BwdParams w) {
     using Cf = GradCfg<DK, DV>;
     constexpr uint32_t R0 = 0, R1 = 128, R2 = 256, R3 = 384;
-    constexpr int NX = DK * DV / 8 / 256;       // 8-value pieces of a memory per thread
+    constexpr int NX = DK * DV / 8 / 512;       // 8-value pieces of a memory per thread
     extern __shared__ __align__(1024) uint8_t smem[];
     GradCtl *ctl = reinterpret_cast<GradCtl *>(smem + Cf::CTL);
     if ((smem_u32(smem) & 1023) || blockDim.x != kGradThreads) {
@@ -373,13 +364,13 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     if (tid == 0) {
         mbar_init(&ctl->full, 1);
         mbar_init(&ctl->m, 1);
-        mbar_init(&ctl->go, 256);
-        mbar_init(&ctl->sync, 256);
+        mbar_init(&ctl->go, 512);
+        mbar_init(&ctl->sync, 512);
         mbar_init(&ctl->last, 1);
         ctl->fail = 0;
         fence_mbar_init();
     }
-    if (warp == 8) {
+    if (warp == 16) {
         tmem_alloc(&ctl->tmem, 512);
         tmem_relinquish();
     }
@@ -389,7 +380,7 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     const uint32_t tm = ctl->tmem;
     const Waits wt{&ctl->fail, w.hdr};
 
-    if (warp == 8) {
+    if (warp == 16) {
         constexpr uint32_t ida = idesc_bf16_f32(128, 128, false, false);
         constexpr uint32_t idx = idesc_bf16_f32(128, DK, false, false);
         constexpr uint32_t idk = idesc_bf16_f32(128, DK, false, true);
@@ -402,22 +393,24 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                        on_ = desc_mnmajor_sw128(sb + Cf::O, kC, 0);
         const uint64_t xh = desc_kmajor_sw128(sb + Cf::XH, DK, 0), xl = desc_kmajor_sw128(sb + Cf::XL, DK, 0),
                        xn = desc_mnmajor_sw128(sb + Cf::XH, DK, 0);
-        auto load = [&](int slot) {
+        // tiles of the item at `slot`, as they become free: V, then Q and K, then dO (one barrier for all)
+        auto load = [&](int slot, int what) {
             const int pi = slot / w.nch, u = (slot - pi * w.nch) * kC;
             const long pair = w.pair0 + pi;
             const int b = (int)(pair / w.HV), hv = (int)(pair % w.HV);
-            if (lane == 0) {
-                mbar_expect_tx(&ctl->full, 2 * Cf::QB + 2 * Cf::VB);
-#pragma unroll
-                for (int i = 0; i < DK / 64; ++i) {
-                    tma_load_4d(smem + Cf::Q + i * kC * 128, &mq, &ctl->full, 64 * i, hv / w.m, u, b);
-                    tma_load_4d(smem + Cf::K + i * kC * 128, &mk, &ctl->full, 64 * i, hv / w.m, u, b);
-                }
+            if (lane == 0 && slot < slots) {
+                if (what == 0) mbar_expect_tx(&ctl->full, 2 * Cf::QB + 2 * Cf::VB);
 #pragma unroll
                 for (int i = 0; i < DV / 64; ++i) {
-                    tma_load_4d(smem + Cf::V + i * kC * 128, &mv, &ctl->full, 64 * i, hv, u, b);
-                    tma_load_4d(smem + Cf::O + i * kC * 128, &mo, &ctl->full, 64 * i, hv, u, b);
+                    if (what == 0) tma_load_4d(smem + Cf::V + i * kC * 128, &mv, &ctl->full, 64 * i, hv, u, b);
+                    if (what == 2) tma_load_4d(smem + Cf::O + i * kC * 128, &mo, &ctl->full, 64 * i, hv, u, b);
                 }
+#pragma unroll
+                for (int i = 0; i < DK / 64; ++i)
+                    if (what == 1) {
+                        tma_load_4d(smem + Cf::Q + i * kC * 128, &mq, &ctl->full, 64 * i, hv / w.m, u, b);
+                        tma_load_4d(smem + Cf::K + i * kC * 128, &mk, &ctl->full, 64 * i, hv / w.m, u, b);
+                    }
             }
             __syncwarp();
         };
@@ -440,7 +433,8 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         // A in TMEM times a token tile
         auto spread = [&](uint32_t d, uint32_t a, uint64_t bb, uint32_t id) {
 #pragma unroll
-            for (int ks = 0; ks < kC / 16; ++ks) mma_bf16_ts_on(on, tm + d, tm + a + 8 * ks, bb + mn_step(ks), id, 1u);
+            for (int ks = 0; ks < kC / 16; ++ks)
+                mma_bf16_ts_on(on, tm + d, tm + a + 32 * (ks >> 1) + 8 * (ks & 1), bb + mn_step(ks), id, 1u);
         };
         int n = 0, ph = 0;                       // items; phases of `go` seen
         auto next = [&]() {
@@ -449,7 +443,7 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             tc_fence_after();
             return ok;
         };
-        if ((int)blockIdx.x < slots) load(blockIdx.x);
+        for (int i = 0; i < 3; ++i) load(blockIdx.x, i);
         for (int slot = blockIdx.x; slot < slots; slot += gridDim.x, ++n) {
             if (!wt.warp(&ctl->full, n & 1, 51)) break;
             tc_fence_after();
@@ -466,22 +460,24 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             into(v)(R3);                         // V R^T
             mma_commit_on(on, &ctl->m);
             if (!next()) break;
+            load(slot + gridDim.x, 0);           // products with V are done
             spread(R3, R1, qn, idk);             // + M^T Q
 #pragma unroll
             for (int ks = 0; ks < DK / 16; ++ks)  // K R
                 mma_bf16_ss_on(on, tm + R1, k + kmajor_step(ks, kC), xn + mn_step(ks), idv, ks > 0);
             mma_commit_on(on, &ctl->m);
             if (!next()) break;
+            load(slot + gridDim.x, 1);           // and with Q and K
             spread(R1, R0, on_, idv);            // + P^T dO
             mma_commit_on(on, &ctl->m);
-            if (!next()) break;                  // the last results are read, so the tiles are dead too
-            if (slot + (int)gridDim.x < slots) load(slot + gridDim.x);
+            if (!next()) break;
+            load(slot + gridDim.x, 2);
         }
     } else {
-        const int quad = warp & 3, half = warp >> 2, row = 32 * quad + lane;
+        const int quad = warp & 3, part = warp >> 2, row = 32 * quad + lane;
         const uint32_t tl = tm + ((uint32_t)(32 * quad) << 16);
         float *ga = reinterpret_cast<float *>(smem + Cf::ARR);
-        float *ar = ga + kC + half * kC, *ac = ar + 2 * kC, *aq = ac + 2 * kC, *ak = aq + 2 * kC;   // this half's
+        float *ar = ga + kC + part * kC, *ac = ar + 4 * kC, *aq = ac + 4 * kC, *ak = aq + 4 * kC;   // this quarter's
         int ph = 0, sp = 0;                      // phases of `m` and `sync` seen
         auto done = [&](int where) {
             const bool ok = wt.warp(&ctl->m, ph & 1, where);
@@ -504,7 +500,7 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         auto put_x = [&](const float4 (&x)[2 * NX]) {
 #pragma unroll
             for (int p = 0; p < NX; ++p) {
-                const int e = tid + 256 * p, r = e / (DV / 8), c = e % (DV / 8);
+                const int e = tid + 512 * p, r = e / (DV / 8), c = e % (DV / 8);
                 const float f[8] = {x[2 * p].x, x[2 * p].y, x[2 * p].z, x[2 * p].w,
                                     x[2 * p + 1].x, x[2 * p + 1].y, x[2 * p + 1].z, x[2 * p + 1].w};
                 uint4 h, l;
@@ -530,8 +526,8 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             const float4 *ps = reinterpret_cast<const float4 *>(w.S + (size_t)slot * DK * DV);
 #pragma unroll
             for (int p = 0; p < NX; ++p) {
-                xs[2 * p] = ps[2 * (tid + 256 * p)];
-                xs[2 * p + 1] = ps[2 * (tid + 256 * p) + 1];
+                xs[2 * p] = ps[2 * (tid + 512 * p)];
+                xs[2 * p + 1] = ps[2 * (tid + 512 * p) + 1];
             }
             if (warp == 0) {
                 const float *gp = w.g.p ? w.g.p + b * w.g.b + hv : nullptr;
@@ -551,17 +547,16 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             if (!meet()) break;
             const float gr = ga[row], gc = ga[kC - 1];
             if (!wt.warp(&ctl->full, it & 1, 58) || !done(53)) break;
-            // ---- P^T, M^T of this row j and its half of the i; M of this row i and its half of the j; sums of W
-            uint32_t pt[32], mt[32], mm[32];
+            // ---- P^T, M^T of this row j and its quarter of the i; M of this row i and its quarter of the j; sums of W
             float cs = 0.f, rs = 0.f;
+#pragma unroll 1
+            for (int i0 = 32 * part; i0 < 32 * part + 32; i0 += 16) {
+                const uint32_t to = 32 * part + (i0 & 16) / 2;
+                uint32_t x[16], y[16], p[8], q[8];
+                if (part < quad) {               // all before the row's tokens
 #pragma unroll
-            for (int blk = 0; blk < 4; ++blk) {
-                const int i0 = 64 * half + 16 * blk;
-                if (i0 + 15 < 32 * quad) {       // all before the row's tokens
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) pt[8 * blk + j] = mt[8 * blk + j] = 0u;
+                    for (int j = 0; j < 8; ++j) p[j] = q[j] = 0u;
                 } else {
-                    uint32_t x[16], y[16];
                     tmem_ld16(tl + R0 + i0, x);
                     tmem_ld16(tl + R1 + i0, y);
                     tmem_ld_wait();
@@ -571,25 +566,26 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int i = i0 + j + e;
-                            const float d = i >= row ? w.scale * ex2(ga[i] - gr) : 0.f;
-                            const float sx = __uint_as_float(x[j + e]), mx = __uint_as_float(y[j + e]);
+                            const float d = w.scale * ex2(ga[i] - gr), sx = __uint_as_float(x[j + e]);
                             a[e] = i >= row ? sx * d : 0.f;
-                            c[e] = i >= row ? mx * d : 0.f;
-                            if (i > row) cs = fmaf(sx, c[e], cs);
+                            c[e] = i >= row ? __uint_as_float(y[j + e]) * d : 0.f;
+                            cs += i > row ? sx * c[e] : 0.f;
                         }
-                        pt[8 * blk + j / 2] = pack_bf16(a[0], a[1]);
-                        mt[8 * blk + j / 2] = pack_bf16(c[0], c[1]);
+                        p[j / 2] = pack_bf16(a[0], a[1]);
+                        q[j / 2] = pack_bf16(c[0], c[1]);
                     }
                 }
+                tmem_st8(tl + R0 + to, p);
+                tmem_st8(tl + R1 + to, q);
             }
+#pragma unroll 1
+            for (int j0 = 32 * part; j0 < 32 * part + 32; j0 += 16) {
+                const uint32_t to = 32 * part + (j0 & 16) / 2;
+                uint32_t x[16], y[16], p[8];
+                if (part > quad) {               // all after the row's tokens
 #pragma unroll
-            for (int blk = 0; blk < 4; ++blk) {
-                const int j0 = 64 * half + 16 * blk;
-                if (j0 > 32 * quad + 31) {       // all after the row's tokens
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) mm[8 * blk + j] = 0u;
+                    for (int j = 0; j < 8; ++j) p[j] = 0u;
                 } else {
-                    uint32_t x[16], y[16];
                     tmem_ld16(tl + R2 + j0, x);
                     tmem_ld16(tl + R3 + j0, y);
                     tmem_ld_wait();
@@ -599,22 +595,16 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int jj = j0 + j + e;
-                            const float d = jj <= row ? w.scale * ex2(gr - ga[jj]) : 0.f;
-                            c[e] = jj <= row ? __uint_as_float(y[j + e]) * d : 0.f;
-                            if (jj < row) rs = fmaf(__uint_as_float(x[j + e]), c[e], rs);
+                            c[e] = jj <= row ? __uint_as_float(y[j + e]) * (w.scale * ex2(gr - ga[jj])) : 0.f;
+                            rs += jj < row ? __uint_as_float(x[j + e]) * c[e] : 0.f;
                         }
-                        mm[8 * blk + j / 2] = pack_bf16(c[0], c[1]);
+                        p[j / 2] = pack_bf16(c[0], c[1]);
                     }
                 }
+                tmem_st8(tl + R3 + to, p);
             }
             ar[row] = rs;
             ac[row] = cs;
-            tc_fence_before();
-            if (!meet()) break;                  // both halves have read their columns
-            tc_fence_after();
-            tmem_st32(tl + R0 + 32 * half, pt);
-            tmem_st32(tl + R1 + 32 * half, mt);
-            tmem_st32(tl + R3 + 32 * half, mm);
             tmem_st_wait();
             go();
             // ---- R; first term of dQ
@@ -622,8 +612,8 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             const float4 *pr = reinterpret_cast<const float4 *>(w.R + (size_t)slot * DK * DV);
 #pragma unroll
             for (int p = 0; p < NX; ++p) {
-                xr[2 * p] = pr[2 * (tid + 256 * p)];
-                xr[2 * p + 1] = pr[2 * (tid + 256 * p) + 1];
+                xr[2 * p] = pr[2 * (tid + 512 * p)];
+                xr[2 * p + 1] = pr[2 * (tid + 512 * p) + 1];
             }
             float dot = 0.f;
 #pragma unroll
@@ -635,30 +625,34 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             if (!done(54)) break;
             put_x(xr);
             const float eg = w.scale * ex2(gr), ew = ex2(gc - gr);
-            aq[row] = scale_row<DK / 2, true>(tl + R2 + half * (DK / 2), eg, smem + Cf::Q, row, half * (DK / 2));
+            const bool onk = 32 * part < DK, onv = 32 * part < DV;   // this warp's 32 columns exist
+            aq[row] = onk ? scale_row(tl + R2 + 32 * part, eg, smem + Cf::Q, row, 32 * part) : 0.f;
             go();
             // ---- dQ out; first term of dK
             const int u0 = u + (row & ~3), rows = min(4, w.T - u0), l8 = 8 * (lane & 3);
             const long long tok = (long long)b * w.T + u + row;
             if (!done(55)) break;
-            if (w.fq)
-                store_row_f32<DK / 2>(tl + R2 + half * (DK / 2), w.fq + (tok * w.HV + hv) * DK + half * (DK / 2), row < live);
-            else
-                store_rows<DK / 2>(tl + R2 + half * (DK / 2),
-                                   w.dq + b * w.qs[0] + (long long)u0 * w.qs[1] + hv * w.qs[2] + half * (DK / 2) + l8,
-                                   w.qs[1], rows, lane);
-            ak[row] = scale_row<DK / 2, true>(tl + R3 + half * (DK / 2), ew, smem + Cf::K, row, half * (DK / 2));
+            // dK's first term first: products 4 wait for it, nobody for dQ's stores
+            ak[row] = onk ? scale_row(tl + R3 + 32 * part, ew, smem + Cf::K, row, 32 * part) : 0.f;
             go();
+            if (onk) {
+                if (w.fq)
+                    store_row_f32(tl + R2 + 32 * part, w.fq + (tok * w.HV + hv) * DK + 32 * part, row < live);
+                else
+                    store_rows(tl + R2 + 32 * part,
+                               w.dq + b * w.qs[0] + (long long)u0 * w.qs[1] + hv * w.qs[2] + 32 * part + l8, w.qs[1], rows, lane);
+            }
             // ---- dK out; first term of dV
             if (!done(56)) break;
-            if (w.fk)
-                store_row_f32<DK / 2>(tl + R3 + half * (DK / 2), w.fk + (tok * w.HV + hv) * DK + half * (DK / 2), row < live);
-            else
-                store_rows<DK / 2>(tl + R3 + half * (DK / 2),
-                                   w.dk + b * w.ks[0] + (long long)u0 * w.ks[1] + hv * w.ks[2] + half * (DK / 2) + l8,
-                                   w.ks[1], rows, lane);
-            scale_row<DV / 2, false>(tl + R1 + half * (DV / 2), ew, nullptr, 0, 0);
+            if (onv) scale_row(tl + R1 + 32 * part, ew, nullptr, 0, 0);
             go();
+            if (onk) {
+                if (w.fk)
+                    store_row_f32(tl + R3 + 32 * part, w.fk + (tok * w.HV + hv) * DK + 32 * part, row < live);
+                else
+                    store_rows(tl + R3 + 32 * part,
+                               w.dk + b * w.ks[0] + (long long)u0 * w.ks[1] + hv * w.ks[2] + 32 * part + l8, w.ks[1], rows, lane);
+            }
             // ---- ddecay (the dots and sums of both halves are in); dV out
             if (w.dg) {
                 if (!meet()) break;
@@ -668,8 +662,12 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int t = 4 * lane + i;
-                        f[i] = (a0[t] + a0[kC + t]) - (a0[2 * kC + t] + a0[3 * kC + t]) + (a0[4 * kC + t] + a0[5 * kC + t]);
-                        kd[i] = a0[6 * kC + t] + a0[7 * kC + t];
+                        auto sum4 = [&](int which) {
+                            const float *a = a0 + 4 * which * kC + t;
+                            return (a[0] + a[kC]) + (a[2 * kC] + a[3 * kC]);
+                        };
+                        f[i] = sum4(0) - sum4(1) + sum4(2);
+                        kd[i] = sum4(3);
                     }
                     float fs = (f[0] + f[1]) + (f[2] + f[3]), kk = (kd[0] + kd[1]) + (kd[2] + kd[3]);
                     float down = fs, up = kk;    // over this and the later lanes; this and the earlier
@@ -680,7 +678,7 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                         if (lane >= off) up += y;
                     }
                     float all = 0.f;
-                    for (int i = 0; i < 8; ++i) all += ctl->dot[i];
+                    for (int i = 0; i < 16; ++i) all += ctl->dot[i];
                     float behind = __shfl_down_sync(0xffffffffu, down, 1), before = __shfl_up_sync(0xffffffffu, up, 1);
                     if (lane == 31) behind = 0.f;
                     if (lane == 0) before = 0.f;
@@ -696,16 +694,17 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                 }
             }
             if (!done(57)) break;
-            store_rows<DV / 2>(tl + R1 + half * (DV / 2),
-                               w.dv + b * w.vs[0] + (long long)u0 * w.vs[1] + hv * w.vs[2] + half * (DV / 2) + l8, w.vs[1],
-                               rows, lane);
+            if (onv)
+                store_rows(tl + R1 + 32 * part,
+                           w.dv + b * w.vs[0] + (long long)u0 * w.vs[1] + hv * w.vs[2] + 32 * part + l8, w.vs[1], rows, lane);
+            tc_fence_before();
             go();
             if (!meet()) break;                  // the shared sums are free for the next chunk
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 16) {
         mma_commit_on(lane == 0, &ctl->last);
         (void)mbar_wait(&ctl->last, 0, kWaitNs);
         if (ctl->fail) {                         // let what is in flight land
