@@ -6,7 +6,6 @@ call runs on.  q, k, v and the other token arrays may be views with any batch, t
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -15,8 +14,10 @@ from ._lib import KDA_BF16, KDA_F32, KdaError, load, query_device_error
 
 _DT = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
 _ACT = {None: 0, "silu": 1, "sigmoid": 2}
-_NONE = contextlib.nullcontext()
-_on = torch.cuda.stream
+_F32 = torch.float32
+_empty = torch.empty
+# The calls below cost a few microseconds on the GPU for small inputs, so their checks are a handful of
+# comparisons; what fails one goes through _need, which finds the words.
 
 
 def _code(t, what="q/k/v"):
@@ -37,24 +38,44 @@ def _need(t, name, dtype, shape, dense=True):
     if dense:
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-    elif t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
+    elif t.shape[-1] > 1 and t.numel() and t.stride(-1) != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
 
 
+def _view(t, name, dtype, shape):
+    """Checks a strided view; True when it is contiguous."""
+    if t.is_contiguous() and t.dtype is dtype and t.is_cuda and t.shape == shape:
+        return True
+    _need(t, name, dtype, shape, False)
+    return t.is_contiguous()
+
+
+def _dense(t, name, dtype, shape):
+    if not (t.is_contiguous() and t.dtype is dtype and t.is_cuda and t.shape == shape):
+        _need(t, name, dtype, shape)
+
+
 def _strides(*ts):
-    """None when every array is contiguous, else their strides without the last dimension."""
-    if all(t.is_contiguous() for t in ts):
-        return None
     s = [x for t in ts for x in t.stride()[:-1]]
     return (ctypes.c_longlong * len(s))(*s)
 
 
-def _p(t):
+def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw(stream):
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+# The current stream's handle; the short way where this torch has it.
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw(t):
+    return _current(t.get_device()) if _current is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _on(stream, call, *args, **kw):
+    """Runs a call on another stream than the current one: what it allocates belongs there too."""
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
 
 
 def _ok(code, where, lib):
@@ -63,13 +84,12 @@ def _ok(code, where, lib):
 
 
 def _ws(need, where, lib, device, workspace):
-    if need == 0:
-        raise KdaError(4, where, lib)
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    if workspace.numel() * workspace.element_size() < need:
-        raise ValueError("workspace too small")
-    return workspace
+        if need == 0:
+            raise KdaError(4, where, lib)
+        workspace = _empty(need, dtype=torch.uint8, device=device)
+        return workspace, need
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _heads(H, HV):
@@ -82,10 +102,18 @@ def _decay(decay, shape):
     if decay is None:
         return 0
     if decay.dim() == 1:
-        _need(decay, "decay", torch.float32, shape[-1:])
+        _dense(decay, "decay", _F32, shape[-1:])
         return 1
-    _need(decay, "decay", torch.float32, shape)
+    _dense(decay, "decay", _F32, shape)
     return 0
+
+
+def _qkv(q, k, v, B, T, H, HV, dk, dv):
+    """Checks q, k and v; True when all are contiguous."""
+    if HV != H:
+        _heads(H, HV)
+    dt = q.dtype
+    return _view(q, "q", dt, q.shape) & _view(k, "k", dt, (B, T, H, dk)) & _view(v, "v", dt, (B, T, HV, dv))
 
 
 def linear_chunk_fwd(q, k, v, decay=None, initial_state=None, *, scale=None, out=None, final_state=None,
@@ -97,34 +125,33 @@ def linear_chunk_fwd(q, k, v, decay=None, initial_state=None, *, scale=None, out
     [B,T,HV] fp32, [HV] (the same at every token) or None; initial_state [B,HV,dk,dv] fp32 or None.
     Returns (o [B,T,HV,dv], final_state [B,HV,dk,dv] fp32).  check_device as in chunk_fwd.
     """
+    if stream is not None:
+        return _on(stream, linear_chunk_fwd, q, k, v, decay, initial_state, scale=scale, out=out,
+                   final_state=final_state, workspace=workspace, check_device=check_device)
     lib = load()
     B, T, H, dk = q.shape
     HV, dv = v.shape[-2:]
-    _heads(H, HV)
     dt = _code(q)
-    _need(q, "q", q.dtype, q.shape, False)
-    _need(k, "k", q.dtype, q.shape, False)
-    _need(v, "v", q.dtype, (B, T, HV, dv), False)
+    plain = _qkv(q, k, v, B, T, H, HV, dk, dv)
     fixed = _decay(decay, (B, T, HV))
     if initial_state is not None:
-        _need(initial_state, "initial_state", torch.float32, (B, HV, dk, dv))
-    with _NONE if stream is None else _on(stream):
-        if out is None:
-            out = torch.empty((B, T, HV, dv), dtype=q.dtype, device=q.device)
-        else:
-            _need(out, "out", q.dtype, (B, T, HV, dv), False)
-        if final_state is None:
-            final_state = torch.empty((B, HV, dk, dv), dtype=torch.float32, device=q.device)
-        else:
-            _need(final_state, "final_state", torch.float32, (B, HV, dk, dv))
-        need = lib.kda_linear_chunk_fwd_workspace(B, T, H, HV, dk, dv, dt)
-        ws = _ws(need, "kda_linear_chunk_fwd_workspace", lib, q.device, workspace)
-        _ok(lib.kda_linear_chunk_fwd(_p(q), _p(k), _p(v), _p(decay), fixed, _p(initial_state), _p(out),
-                                     _p(final_state), _strides(q, k, v, out), B, T, H, HV, dk, dv, dt, scale or 0.0,
-                                     _p(ws), ws.numel() * ws.element_size(), _raw(stream)),
-            "kda_linear_chunk_fwd", lib)
-        if check_device:
-            _ok(query_device_error(ws, stream), "kda_linear_chunk_fwd (device)", lib)
+        _dense(initial_state, "initial_state", _F32, (B, HV, dk, dv))
+    dev = q.device
+    if out is None:
+        out = _empty((B, T, HV, dv), dtype=q.dtype, device=dev)
+    else:
+        plain &= _view(out, "out", q.dtype, (B, T, HV, dv))
+    if final_state is None:
+        final_state = _empty((B, HV, dk, dv), dtype=_F32, device=dev)
+    else:
+        _dense(final_state, "final_state", _F32, (B, HV, dk, dv))
+    ws, n = _ws(lib.kda_linear_chunk_fwd_workspace(B, T, H, HV, dk, dv, dt), "kda_linear_chunk_fwd_workspace", lib, dev,
+                workspace)
+    _ok(lib.kda_linear_chunk_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(decay), fixed, _ptr(initial_state),
+                                 out.data_ptr(), final_state.data_ptr(), None if plain else _strides(q, k, v, out), B, T, H,
+                                 HV, dk, dv, dt, scale or 0.0, ws.data_ptr(), n, _raw(q)), "kda_linear_chunk_fwd", lib)
+    if check_device:
+        _ok(query_device_error(ws), "kda_linear_chunk_fwd (device)", lib)
     return out, final_state
 
 
@@ -133,44 +160,43 @@ def linear_varlen_fwd(q, k, v, cu_seqlens, decay=None, initial_state=None, *, cu
     """kda_linear_varlen_fwd: packed sequences [1,total,H,D] split by cu_seqlens [N+1] (int32, device);
     cu_seqlens_cpu, its host copy where there is one, is checked and tells how to split the work.
     Returns (o [1,total,HV,dv], final_state [N,HV,dk,dv] fp32)."""
+    if stream is not None:
+        return _on(stream, linear_varlen_fwd, q, k, v, cu_seqlens, decay, initial_state, cu_seqlens_cpu=cu_seqlens_cpu,
+                   scale=scale, out=out, final_state=final_state, workspace=workspace, check_device=check_device)
     lib = load()
     one, total, H, dk = q.shape
     HV, dv = v.shape[-2:]
-    _heads(H, HV)
     if one != 1:
         raise ValueError("packed sequences need token arrays with B == 1")
     dt = _code(q)
     N = cu_seqlens.numel() - 1
-    _need(q, "q", q.dtype, q.shape, False)
-    _need(k, "k", q.dtype, q.shape, False)
-    _need(v, "v", q.dtype, (1, total, HV, dv), False)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,))
+    plain = _qkv(q, k, v, 1, total, H, HV, dk, dv)
+    _dense(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,))
     fixed = _decay(decay, (1, total, HV))
     if initial_state is not None:
-        _need(initial_state, "initial_state", torch.float32, (N, HV, dk, dv))
+        _dense(initial_state, "initial_state", _F32, (N, HV, dk, dv))
     host = None
     if cu_seqlens_cpu is not None:
         host = cu_seqlens_cpu.to(torch.int32).contiguous()
         if host.is_cuda or host.numel() != N + 1:
             raise ValueError("cu_seqlens_cpu must be a host tensor of cu_seqlens' length")
-    with _NONE if stream is None else _on(stream):
-        if out is None:
-            out = torch.empty((1, total, HV, dv), dtype=q.dtype, device=q.device)
-        else:
-            _need(out, "out", q.dtype, (1, total, HV, dv), False)
-        if final_state is None:
-            final_state = torch.empty((N, HV, dk, dv), dtype=torch.float32, device=q.device)
-        else:
-            _need(final_state, "final_state", torch.float32, (N, HV, dk, dv))
-        need = lib.kda_linear_varlen_fwd_workspace(N, total, H, HV, dk, dv, dt)
-        ws = _ws(need, "kda_linear_varlen_fwd_workspace", lib, q.device, workspace)
-        _ok(lib.kda_linear_varlen_fwd(_p(q), _p(k), _p(v), _p(decay), fixed, _p(cu_seqlens), _p(host),
-                                      _p(initial_state), _p(out), _p(final_state), _strides(q, k, v, out), N, total, H,
-                                      HV, dk, dv, dt, scale or 0.0, _p(ws), ws.numel() * ws.element_size(),
-                                      _raw(stream)),
-            "kda_linear_varlen_fwd", lib)
-        if check_device:
-            _ok(query_device_error(ws, stream), "kda_linear_varlen_fwd (device)", lib)
+    dev = q.device
+    if out is None:
+        out = _empty((1, total, HV, dv), dtype=q.dtype, device=dev)
+    else:
+        plain &= _view(out, "out", q.dtype, (1, total, HV, dv))
+    if final_state is None:
+        final_state = _empty((N, HV, dk, dv), dtype=_F32, device=dev)
+    else:
+        _dense(final_state, "final_state", _F32, (N, HV, dk, dv))
+    ws, n = _ws(lib.kda_linear_varlen_fwd_workspace(N, total, H, HV, dk, dv, dt), "kda_linear_varlen_fwd_workspace", lib,
+                dev, workspace)
+    _ok(lib.kda_linear_varlen_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(decay), fixed, cu_seqlens.data_ptr(),
+                                  _ptr(host), _ptr(initial_state), out.data_ptr(), final_state.data_ptr(),
+                                  None if plain else _strides(q, k, v, out), N, total, H, HV, dk, dv, dt, scale or 0.0,
+                                  ws.data_ptr(), n, _raw(q)), "kda_linear_varlen_fwd", lib)
+    if check_device:
+        _ok(query_device_error(ws), "kda_linear_varlen_fwd (device)", lib)
     return out, final_state
 
 
@@ -178,30 +204,37 @@ def linear_decode_step(q, k, v, decay, state, *, scale=None, out=None, stream=No
     """kda_linear_decode_step: one token per sequence; ``state`` [B,HV,dk,dv] fp32 is updated in place.
     q, k [B,1,H,dk] or [B,H,dk]; v [B,1,HV,dv] or [B,HV,dv]; decay [B,1,HV] or [B,HV] fp32, [HV] or None.
     Returns o with v's shape."""
+    if stream is not None:
+        return _on(stream, linear_decode_step, q, k, v, decay, state, scale=scale, out=out)
     lib = load()
     B, HV, dk, dv = state.shape
     H = q.shape[-2]
-    _heads(H, HV)
-    dt = _code(q)
-    mid = (1,) if q.dim() == 4 else ()
-    _need(q, "q", q.dtype, (B, *mid, H, dk), False)
-    _need(k, "k", q.dtype, (B, *mid, H, dk), False)
-    _need(v, "v", q.dtype, (B, *mid, HV, dv), False)
-    _need(state, "state", torch.float32, state.shape)
+    if HV != H:
+        _heads(H, HV)
+    dt, dtype = _code(q), q.dtype
+    if q.dim() == 4:
+        qs, vs = (B, 1, H, dk), (B, 1, HV, dv)
+    else:
+        qs, vs = (B, H, dk), (B, HV, dv)
+    plain = _view(q, "q", dtype, qs) & _view(k, "k", dtype, qs) & _view(v, "v", dtype, vs)
+    _dense(state, "state", _F32, state.shape)
     fixed = 0
     if decay is not None:
-        fixed = int(decay.dim() == 1)
-        _need(decay, "decay", torch.float32, (HV,) if fixed else (B, *mid[:decay.dim() - 2], HV))
-    with _NONE if stream is None else _on(stream):
-        if out is None:
-            out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        if decay.dim() == 1:
+            fixed = 1
+            _dense(decay, "decay", _F32, (HV,))
         else:
-            _need(out, "out", v.dtype, v.shape, False)
-        s = None
-        if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous()):
-            s = (ctypes.c_longlong * 8)(*(x for t in (q, k, v, out) for x in (t.stride(0), t.stride(-2))))
-        _ok(lib.kda_linear_decode_step(_p(q), _p(k), _p(v), _p(decay), fixed, _p(state), _p(out), s, B, H, HV, dk, dv,
-                                       dt, scale or 0.0, _raw(stream)), "kda_linear_decode_step", lib)
+            _dense(decay, "decay", _F32, (B, 1, HV) if decay.dim() == 3 else (B, HV))
+    if out is None:
+        out = _empty(vs, dtype=dtype, device=q.device)
+    else:
+        plain &= _view(out, "out", dtype, vs)
+    s = None
+    if not plain:
+        s = (ctypes.c_longlong * 8)(*(x for t in (q, k, v, out) for x in (t.stride(0), t.stride(-2))))
+    _ok(lib.kda_linear_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(decay), fixed, state.data_ptr(),
+                                   out.data_ptr(), s, B, H, HV, dk, dv, dt, scale or 0.0, _raw(q)),
+        "kda_linear_decode_step", lib)
     return out
 
 
@@ -210,39 +243,37 @@ def linear_chunk_bwd(q, k, v, decay, initial_state, d_o, dfinal_state=None, *, s
     """kda_linear_chunk_bwd: gradients of linear_chunk_fwd given dL/do (dtype of q) and dL/dfinal_state
     (fp32 or None).  Returns a dict dq, dk, dv (q's dtype), ddecay (fp32, decay's shape; absent without a
     decay) and dh0 (fp32; absent without an initial state)."""
+    if stream is not None:
+        return _on(stream, linear_chunk_bwd, q, k, v, decay, initial_state, d_o, dfinal_state, scale=scale,
+                   workspace=workspace, check_device=check_device)
     lib = load()
     B, T, H, dk = q.shape
     HV, dv = v.shape[-2:]
-    _heads(H, HV)
-    dt = _code(q)
-    _need(q, "q", q.dtype, q.shape, False)
-    _need(k, "k", q.dtype, q.shape, False)
-    _need(v, "v", q.dtype, (B, T, HV, dv), False)
-    _need(d_o, "d_o", q.dtype, (B, T, HV, dv), False)
+    dt, dtype = _code(q), q.dtype
+    plain = _qkv(q, k, v, B, T, H, HV, dk, dv) & _view(d_o, "d_o", dtype, (B, T, HV, dv))
     fixed = _decay(decay, (B, T, HV))
-    for t, name in ((initial_state, "initial_state"), (dfinal_state, "dfinal_state")):
-        if t is not None:
-            _need(t, name, torch.float32, (B, HV, dk, dv))
-    with _NONE if stream is None else _on(stream):
-        dev = q.device
-        dq = torch.empty((B, T, H, dk), dtype=q.dtype, device=dev)
-        dkk = torch.empty((B, T, H, dk), dtype=q.dtype, device=dev)
-        dvv = torch.empty((B, T, HV, dv), dtype=q.dtype, device=dev)
-        out = dict(dq=dq, dk=dkk, dv=dvv)
-        dg = dh0 = None
-        if decay is not None:
-            dg = out["ddecay"] = torch.empty(decay.shape, dtype=torch.float32, device=dev)
-        if initial_state is not None:
-            dh0 = out["dh0"] = torch.empty((B, HV, dk, dv), dtype=torch.float32, device=dev)
-        need = lib.kda_linear_chunk_bwd_workspace(B, T, H, HV, dk, dv, dt)
-        ws = _ws(need, "kda_linear_chunk_bwd_workspace", lib, dev, workspace)
-        _ok(lib.kda_linear_chunk_bwd(_p(q), _p(k), _p(v), _p(decay), fixed, _p(initial_state), _p(d_o),
-                                     _p(dfinal_state), _p(dq), _p(dkk), _p(dvv), _p(dg), _p(dh0),
-                                     _strides(q, k, v, d_o, dq, dkk, dvv), B, T, H, HV, dk, dv, dt, scale or 0.0,
-                                     _p(ws), ws.numel() * ws.element_size(), _raw(stream)),
-            "kda_linear_chunk_bwd", lib)
-        if check_device:
-            _ok(query_device_error(ws, stream), "kda_linear_chunk_bwd (device)", lib)
+    if initial_state is not None:
+        _dense(initial_state, "initial_state", _F32, (B, HV, dk, dv))
+    if dfinal_state is not None:
+        _dense(dfinal_state, "dfinal_state", _F32, (B, HV, dk, dv))
+    dev = q.device
+    dq = _empty((B, T, H, dk), dtype=dtype, device=dev)
+    dkk = _empty((B, T, H, dk), dtype=dtype, device=dev)
+    dvv = _empty((B, T, HV, dv), dtype=dtype, device=dev)
+    out = dict(dq=dq, dk=dkk, dv=dvv)
+    dg = dh0 = None
+    if decay is not None:
+        dg = out["ddecay"] = _empty(decay.shape, dtype=_F32, device=dev)
+    if initial_state is not None:
+        dh0 = out["dh0"] = _empty((B, HV, dk, dv), dtype=_F32, device=dev)
+    ws, n = _ws(lib.kda_linear_chunk_bwd_workspace(B, T, H, HV, dk, dv, dt), "kda_linear_chunk_bwd_workspace", lib, dev,
+                workspace)
+    _ok(lib.kda_linear_chunk_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(decay), fixed, _ptr(initial_state),
+                                 d_o.data_ptr(), _ptr(dfinal_state), dq.data_ptr(), dkk.data_ptr(), dvv.data_ptr(),
+                                 _ptr(dg), _ptr(dh0), None if plain else _strides(q, k, v, d_o, dq, dkk, dvv), B, T, H, HV,
+                                 dk, dv, dt, scale or 0.0, ws.data_ptr(), n, _raw(q)), "kda_linear_chunk_bwd", lib)
+    if check_device:
+        _ok(query_device_error(ws), "kda_linear_chunk_bwd (device)", lib)
     return out
 
 
@@ -257,7 +288,7 @@ def _token_strides(t):
     return t.stride(lead - 1), t.stride(-2)
 
 
-def _norm_args(x, gate, weight, activation, *more):
+def _norm_args(x, gate, weight, activation):
     act = _ACT.get(activation if gate is not None else None)
     if act is None:
         raise ValueError("activation must be 'silu' or 'sigmoid'")
@@ -265,53 +296,62 @@ def _norm_args(x, gate, weight, activation, *more):
         raise ValueError("x must be [..., H, D]")
     H, D = x.shape[-2:]
     dt = _code(x, "x")
-    _need(weight, "weight", torch.float32, (D,))
-    ts = [x, gate, *more]
-    for t, name in zip(ts, ("x", "gate", "d_y")):
-        if t is not None:
-            _need(t, name, x.dtype, x.shape, False)
-    return act, dt, H, D, x.numel() // max(1, H * D)
+    _dense(weight, "weight", _F32, (D,))
+    plain = _view(x, "x", x.dtype, x.shape)
+    if gate is not None:
+        plain &= _view(gate, "gate", x.dtype, x.shape)
+    return act, dt, H, D, x.numel() // max(1, H * D), plain
 
 
 def gated_norm_fwd(x, gate, weight, *, eps=1e-6, activation="silu", out=None, stream=None):
     """kda_gated_norm_fwd: y = x (mean(x^2) + eps)^(-1/2) weight act(gate) over the last dimension.
     x, gate [..., H, D] (gate None: no gate), weight [D] fp32, activation "silu" or "sigmoid"."""
+    if stream is not None:
+        return _on(stream, gated_norm_fwd, x, gate, weight, eps=eps, activation=activation, out=out)
     lib = load()
-    act, dt, H, D, N = _norm_args(x, gate, weight, activation)
-    with _NONE if stream is None else _on(stream):
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        else:
-            _need(out, "out", x.dtype, x.shape, False)
-        s = None
-        if not (x.is_contiguous() and out.is_contiguous() and (gate is None or gate.is_contiguous())):
-            s = (ctypes.c_longlong * 6)(*_token_strides(x), *_token_strides(gate if gate is not None else x),
-                                        *_token_strides(out))
-        _ok(lib.kda_gated_norm_fwd(_p(x), _p(gate), _p(weight), _p(out), s, N, H, D, dt, act, eps, _raw(stream)),
-            "kda_gated_norm_fwd", lib)
+    act, dt, H, D, N, plain = _norm_args(x, gate, weight, activation)
+    if out is None:
+        out = _empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        plain &= _view(out, "out", x.dtype, x.shape)
+    s = None
+    if not plain:
+        s = (ctypes.c_longlong * 6)(*_token_strides(x), *_token_strides(gate if gate is not None else x),
+                                    *_token_strides(out))
+    _ok(lib.kda_gated_norm_fwd(x.data_ptr(), _ptr(gate), weight.data_ptr(), out.data_ptr(), s, N, H, D, dt, act, eps,
+                               _raw(x)), "kda_gated_norm_fwd", lib)
     return out
 
 
 def gated_norm_bwd(d_y, x, gate, weight, *, eps=1e-6, activation="silu", workspace=None, stream=None):
     """kda_gated_norm_bwd: a dict dx, dgate (x's dtype; dgate absent without a gate) and dw [D] fp32."""
+    if stream is not None:
+        return _on(stream, gated_norm_bwd, d_y, x, gate, weight, eps=eps, activation=activation, workspace=workspace)
     lib = load()
-    act, dt, H, D, N = _norm_args(x, gate, weight, activation, d_y)
-    with _NONE if stream is None else _on(stream):
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dg = torch.empty(x.shape, dtype=x.dtype, device=x.device) if gate is not None else None
-        dw = torch.empty(D, dtype=torch.float32, device=x.device)
-        ws = _ws(lib.kda_gated_norm_bwd_workspace(D), "kda_gated_norm_bwd_workspace", lib, x.device, workspace)
-        s = None
-        if not (x.is_contiguous() and d_y.is_contiguous() and (gate is None or gate.is_contiguous())):
-            s = (ctypes.c_longlong * 10)(*_token_strides(x), *_token_strides(gate if gate is not None else x),
-                                         *_token_strides(d_y), H * D, D, H * D, D)
-        _ok(lib.kda_gated_norm_bwd(_p(d_y), _p(x), _p(gate), _p(weight), _p(dx), _p(dg), _p(dw), s, N, H, D, dt, act, eps,
-                                   _p(ws), ws.numel() * ws.element_size(), _raw(stream)), "kda_gated_norm_bwd", lib)
-    return dict(dx=dx, dgate=dg, dw=dw) if dg is not None else dict(dx=dx, dw=dw)
+    act, dt, H, D, N, plain = _norm_args(x, gate, weight, activation)
+    plain &= _view(d_y, "d_y", x.dtype, x.shape)
+    dev = x.device
+    dx = _empty(x.shape, dtype=x.dtype, device=dev)
+    dw = _empty(D, dtype=_F32, device=dev)
+    out = dict(dx=dx, dw=dw)
+    dg = None
+    if gate is not None:
+        dg = out["dgate"] = _empty(x.shape, dtype=x.dtype, device=dev)
+    ws, n = _ws(lib.kda_gated_norm_bwd_workspace(D), "kda_gated_norm_bwd_workspace", lib, dev, workspace)
+    s = None
+    if not plain:
+        s = (ctypes.c_longlong * 10)(*_token_strides(x), *_token_strides(gate if gate is not None else x),
+                                     *_token_strides(d_y), H * D, D, H * D, D)
+    _ok(lib.kda_gated_norm_bwd(d_y.data_ptr(), x.data_ptr(), _ptr(gate), weight.data_ptr(), dx.data_ptr(), _ptr(dg),
+                               dw.data_ptr(), s, N, H, D, dt, act, eps, ws.data_ptr(), n, _raw(x)),
+        "kda_gated_norm_bwd", lib)
+    return out
 
 
 def _rows(t, D):
     """Row stride of [..., D] whose leading dimensions step evenly."""
+    if t.is_contiguous():
+        return D
     lead = t.dim() - 1
     for i in range(lead - 1):
         if t.shape[i] > 1 and t.stride(i) != t.stride(i + 1) * t.shape[i + 1]:
@@ -321,7 +361,7 @@ def _rows(t, D):
 
 def _scale(scale, D):
     if isinstance(scale, torch.Tensor):
-        _need(scale, "scale", torch.float32, (D,))
+        _dense(scale, "scale", _F32, (D,))
         return scale.data_ptr(), 0.0
     return None, float(scale)
 
@@ -331,23 +371,28 @@ def residual_norm_fwd(x, y, weight, *, scale=1.0, eps=1e-6, out=None, out_norm=N
     dimension.  x [..., D] is the residual stream (bf16, or fp32 around bf16 blocks), y [..., D] the
     block's output, weight [D] fp32, scale a number or a [D] fp32 tensor.  Returns (x' in x's dtype, n in
     y's); out may be x."""
+    if stream is not None:
+        return _on(stream, residual_norm_fwd, x, y, weight, scale=scale, eps=eps, out=out, out_norm=out_norm)
     lib = load()
-    D = x.shape[-1]
-    _need(x, "x", x.dtype, x.shape, False)
-    _need(y, "y", y.dtype, x.shape, False)
-    _need(weight, "weight", torch.float32, (D,))
+    shape = x.shape
+    D = shape[-1]
+    res, dt = _code(x, "x"), _code(y, "y")
+    _view(x, "x", x.dtype, shape)
+    _view(y, "y", y.dtype, shape)
+    _dense(weight, "weight", _F32, (D,))
     cv, c = _scale(scale, D)
-    with _NONE if stream is None else _on(stream):
-        for t, name, like in ((out, "out", x), (out_norm, "out_norm", y)):
-            if t is not None:
-                _need(t, name, like.dtype, x.shape)
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if out_norm is None:
-            out_norm = torch.empty(x.shape, dtype=y.dtype, device=x.device)
-        _ok(lib.kda_residual_norm_fwd(_p(x), _p(y), _p(weight), cv, c, _p(out), _p(out_norm), _rows(x, D), _rows(y, D),
-                                      x.numel() // max(1, D), D, _code(x, "x"), _code(y, "y"), eps, _raw(stream)),
-            "kda_residual_norm_fwd", lib)
+    dev = x.device
+    if out is None:
+        out = _empty(shape, dtype=x.dtype, device=dev)
+    else:
+        _dense(out, "out", x.dtype, shape)
+    if out_norm is None:
+        out_norm = _empty(shape, dtype=y.dtype, device=dev)
+    else:
+        _dense(out_norm, "out_norm", y.dtype, shape)
+    _ok(lib.kda_residual_norm_fwd(x.data_ptr(), y.data_ptr(), weight.data_ptr(), cv, c, out.data_ptr(), out_norm.data_ptr(),
+                                  _rows(x, D), _rows(y, D), x.numel() // max(1, D), D, res, dt, eps, _raw(x)),
+        "kda_residual_norm_fwd", lib)
     return out, out_norm
 
 
@@ -355,25 +400,29 @@ def residual_norm_bwd(d_n, d_x, x, weight, y=None, *, scale=1.0, eps=1e-6, works
     """kda_residual_norm_bwd: gradients of residual_norm_fwd at its output x (= x'), given those of n and
     x' (d_x None: zeros).  Returns a dict dx (x's dtype; the gradient of the incoming residual), dy = scale
     dx (d_n's dtype), dw [D] fp32, and dscale [D] fp32 when y is given."""
+    if stream is not None:
+        return _on(stream, residual_norm_bwd, d_n, d_x, x, weight, y, scale=scale, eps=eps, workspace=workspace)
     lib = load()
-    D = x.shape[-1]
-    _need(x, "x", x.dtype, x.shape)
-    _need(d_n, "d_n", d_n.dtype, x.shape)
-    _need(weight, "weight", torch.float32, (D,))
+    shape = x.shape
+    D = shape[-1]
+    res, dt = _code(x, "x"), _code(d_n, "d_n")
+    _dense(x, "x", x.dtype, shape)
+    _dense(d_n, "d_n", d_n.dtype, shape)
+    _dense(weight, "weight", _F32, (D,))
     if d_x is not None:
-        _need(d_x, "d_x", x.dtype, x.shape)
-    if y is not None:
-        _need(y, "y", d_n.dtype, x.shape)
+        _dense(d_x, "d_x", x.dtype, shape)
     cv, c = _scale(scale, D)
-    with _NONE if stream is None else _on(stream):
-        out = dict(dx=torch.empty(x.shape, dtype=x.dtype, device=x.device),
-                   dy=torch.empty(x.shape, dtype=d_n.dtype, device=x.device),
-                   dw=torch.empty(D, dtype=torch.float32, device=x.device))
-        if y is not None:
-            out["dscale"] = torch.empty(D, dtype=torch.float32, device=x.device)
-        ws = _ws(lib.kda_residual_norm_bwd_workspace(D), "kda_residual_norm_bwd_workspace", lib, x.device, workspace)
-        _ok(lib.kda_residual_norm_bwd(_p(d_n), _p(d_x), _p(x), _p(y), _p(weight), cv, c, _p(out["dx"]), _p(out["dy"]),
-                                      _p(out["dw"]), _p(out.get("dscale")), x.numel() // max(1, D), D, _code(x, "x"),
-                                      _code(d_n, "d_n"), eps, _p(ws), ws.numel() * ws.element_size(), _raw(stream)),
-            "kda_residual_norm_bwd", lib)
+    dev = x.device
+    dx = _empty(shape, dtype=x.dtype, device=dev)
+    dy = _empty(shape, dtype=d_n.dtype, device=dev)
+    dw = _empty(D, dtype=_F32, device=dev)
+    out = dict(dx=dx, dy=dy, dw=dw)
+    ds = None
+    if y is not None:
+        _dense(y, "y", d_n.dtype, shape)
+        ds = out["dscale"] = _empty(D, dtype=_F32, device=dev)
+    ws, n = _ws(lib.kda_residual_norm_bwd_workspace(D), "kda_residual_norm_bwd_workspace", lib, dev, workspace)
+    _ok(lib.kda_residual_norm_bwd(d_n.data_ptr(), _ptr(d_x), x.data_ptr(), _ptr(y), weight.data_ptr(), cv, c, dx.data_ptr(),
+                                  dy.data_ptr(), dw.data_ptr(), _ptr(ds), x.numel() // max(1, D), D, res, dt, eps,
+                                  ws.data_ptr(), n, _raw(x)), "kda_residual_norm_bwd", lib)
     return out

@@ -101,47 +101,60 @@ __device__ __forceinline__ float norm_back(float t, float x, float ss, float dot
 
 // ------------------------------------------------------------------------------ gated norm
 // L lanes per row (256 / L rows per CTA at a time), NJ packs of V elements per lane.
-template <typename T, int V, int L, int NJ>
+// NR rows are loaded before the first is reduced: one row's two 16-byte loads per thread do not keep
+// enough bytes in flight (32768 x 32 rows of 128 bf16: 0.175 ms with one).
+template <typename T, int V, int L, int NJ, int NR>
 __global__ void __launch_bounds__(kThreads) gated_norm_fwd_kernel(GatedNorm a) {
     constexpr int RPB = kThreads / L;
     const int l = threadIdx.x % L;
-    const long row = blockIdx.x * (long)RPB + threadIdx.x / L;
-    const bool live = row < a.rows;
-    const long t = live ? row / a.H : 0;
-    const int h = live ? (int)(row - t * a.H) : 0;
-    const T *xp = static_cast<const T *>(a.x.p) + t * a.x.t + h * a.x.h;
-    const T *gp = static_cast<const T *>(a.g.p) + t * a.g.t + h * a.g.h;
-    T *yp = static_cast<T *>(a.y.p) + t * a.y.t + h * a.y.h;
-    float x[NJ][V], g[NJ][V], ss = 0.f;
+    const long row0 = blockIdx.x * (long)(RPB * NR) + threadIdx.x / L;
+    float x[NR][NJ][V], g[NR][NJ][V];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-        const int e = (l + L * j) * V;
+    for (int n = 0; n < NR; ++n) {
+        const long row = row0 + n * RPB;
+        const bool live = row < a.rows;
+        const long t = live ? row / a.H : 0;
+        const int h = live ? (int)(row - t * a.H) : 0;
+        const T *xp = static_cast<const T *>(a.x.p) + t * a.x.t + h * a.x.h;
+        const T *gp = static_cast<const T *>(a.g.p) + t * a.g.t + h * a.g.h;
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[j][i] = g[j][i] = 0.f;
-        if (live && e < a.D) {
-            Pack<T, V>::load(xp + e, x[j]);
-            if (a.act) Pack<T, V>::load(gp + e, g[j]);
+        for (int j = 0; j < NJ; ++j) {
+            const int e = (l + L * j) * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[n][j][i] = g[n][j][i] = 0.f;
+            if (live && e < a.D) {
+                Pack<T, V>::load(xp + e, x[n][j]);
+                if (a.act) Pack<T, V>::load(gp + e, g[n][j]);
+            }
         }
     }
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+    for (int n = 0; n < NR; ++n) {
+        const long row = row0 + n * RPB;
+        const bool live = row < a.rows;
+        float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) ss = fmaf(x[j][i], x[j][i], ss);
-    ss = row_sum<L>(ss, nullptr);
-    const float r = rsqrtf(ss * a.inv_d + a.eps);
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-        const int e = (l + L * j) * V;
-        if (!live || e >= a.D) continue;
-        float w[V];
-        Pack<float, V>::load(a.w + e, w);
+            for (int i = 0; i < V; ++i) ss = fmaf(x[n][j][i], x[n][j][i], ss);
+        ss = row_sum<L>(ss, nullptr);
+        const float r = rsqrtf(ss * a.inv_d + a.eps);
+        const long t = live ? row / a.H : 0;
+        T *yp = static_cast<T *>(a.y.p) + t * a.y.t + (live ? (int)(row - t * a.H) : 0) * a.y.h;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float y = x[j][i] * r * w[i];
-            if (a.act) y *= act_of(g[j][i], a.act);
-            x[j][i] = y;
+        for (int j = 0; j < NJ; ++j) {
+            const int e = (l + L * j) * V;
+            if (!live || e >= a.D) continue;
+            float w[V];
+            Pack<float, V>::load(a.w + e, w);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float y = x[n][j][i] * r * w[i];
+                if (a.act) y *= act_of(g[n][j][i], a.act);
+                x[n][j][i] = y;
+            }
+            Pack<T, V>::store(yp + e, x[n][j]);
         }
-        Pack<T, V>::store(yp + e, x[j]);
     }
 }
 
@@ -224,21 +237,23 @@ __global__ void __launch_bounds__(kThreads) gated_norm_bwd_kernel(GatedNorm a) {
     }
 }
 
-// out[c] = sum over p of part[p, c], in order: 32 columns x 8 strands of a CTA
-__global__ void __launch_bounds__(256) norm_fold_kernel(const float *part, int np, int D, float *out0, float *out1) {
-    __shared__ float s[8][33];
+// out[c] = sum over p of part[p, c] in a fixed order: 32 columns x 32 strands of a CTA
+__global__ void __launch_bounds__(1024) norm_fold_kernel(const float *part, int np, int D, float *out0, float *out1) {
+    __shared__ float s[32][33];
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
     const int width = out1 ? 2 * D : D;
     float sum = 0.f;
-    if (c < width)
-        for (int p = k; p < np; p += 8) sum += part[(size_t)p * width + c];
+    if (c < width) {
+#pragma unroll 8
+        for (int p = k; p < np; p += 32) sum += part[(size_t)p * width + c];
+    }
     s[k][threadIdx.x & 31] = sum;
     __syncthreads();
-    if (k == 0 && c < width) {
-        sum = 0.f;
-        for (int i = 0; i < 8; ++i) sum += s[i][threadIdx.x & 31];
-        (c < D ? out0 : out1)[c < D ? c : c - D] = sum;
-    }
+    sum = s[threadIdx.x & 31][k];               // column k's strands, one per lane
+#pragma unroll
+    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    const int cc = blockIdx.x * 32 + k;
+    if ((threadIdx.x & 31) == 0 && cc < width) (cc < D ? out0 : out1)[cc < D ? cc : cc - D] = sum;
 }
 
 // ------------------------------------------------------------------------------ residual norm
@@ -298,23 +313,40 @@ __global__ void __launch_bounds__(L > 32 ? L : kThreads) residual_norm_bwd_kerne
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int i = 0; i < V; ++i) dw[j][i] = dc[j][i] = 0.f;
-    int turn = 0;   // the two sums of consecutive rows use two sets of shared floats
-    for (long row0 = blockIdx.x * (long)RPB; row0 < a.rows; row0 += gridDim.x * (long)RPB, turn ^= 1) {
-        const long row = row0 + rg;
+    // the next row's loads go out before this row is summed
+    float nx[NJ][V], nn[NJ][V], nd[NJ][V], ny[NJ][V];
+    auto fetch = [&](long row) {
         const bool live = row < a.rows;
         const long rr = live ? row : 0;
-        float x[NJ][V], dn[NJ][V], dx[NJ][V], ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             const int e = (l + L * j) * V;
 #pragma unroll
-            for (int i = 0; i < V; ++i) x[j][i] = dn[j][i] = dx[j][i] = 0.f;
+            for (int i = 0; i < V; ++i) nx[j][i] = nn[j][i] = nd[j][i] = ny[j][i] = 0.f;
             if (live && e < a.D) {
-                Pack<TR, V>::load(static_cast<const TR *>(a.x) + rr * a.xs + e, x[j]);
-                Pack<T, V>::load(static_cast<const T *>(a.dn) + rr * a.dns + e, dn[j]);
-                if (a.dxo) Pack<TR, V>::load(static_cast<const TR *>(a.dxo) + rr * a.dxs + e, dx[j]);
+                Pack<TR, V>::load(static_cast<const TR *>(a.x) + rr * a.xs + e, nx[j]);
+                Pack<T, V>::load(static_cast<const T *>(a.dn) + rr * a.dns + e, nn[j]);
+                if (a.dxo) Pack<TR, V>::load(static_cast<const TR *>(a.dxo) + rr * a.dxs + e, nd[j]);
+                if (a.y) Pack<T, V>::load(static_cast<const T *>(a.y) + rr * a.ys + e, ny[j]);
             }
         }
+    };
+    fetch(blockIdx.x * (long)RPB + rg);
+    int turn = 0;   // the two sums of consecutive rows use two sets of shared floats
+    for (long row0 = blockIdx.x * (long)RPB; row0 < a.rows; row0 += gridDim.x * (long)RPB, turn ^= 1) {
+        const long row = row0 + rg;
+        const bool live = row < a.rows;
+        float x[NJ][V], dn[NJ][V], dx[NJ][V], y[NJ][V], ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                x[j][i] = nx[j][i];
+                dn[j][i] = nn[j][i];
+                dx[j][i] = nd[j][i];
+                y[j][i] = ny[j][i];
+            }
+        if (NJ * V <= 16) fetch(row + gridDim.x * (long)RPB);   // wider rows have no registers for it
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             const int e = (l + L * j) * V;
@@ -335,23 +367,23 @@ __global__ void __launch_bounds__(L > 32 ? L : kThreads) residual_norm_bwd_kerne
         for (int j = 0; j < NJ; ++j) {
             const int e = (l + L * j) * V;
             if (!live || e >= a.D) continue;
-            float w[V], c[V], y[V];
+            float w[V], c[V];
             Pack<float, V>::load(a.w + e, w);
 #pragma unroll
             for (int i = 0; i < V; ++i) c[i] = a.c;
             if (a.cv) Pack<float, V>::load(a.cv + e, c);
-            if (a.y) Pack<T, V>::load(static_cast<const T *>(a.y) + rr * a.ys + e, y);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float xn = x[j][i] * r;
                 dw[j][i] = fmaf(dn[j][i], xn, dw[j][i]);
                 dx[j][i] += r * norm_back(dn[j][i] * w[i], x[j][i], ss, dot, r2, a.eps, a.inv_d);
-                if (a.y) dc[j][i] = fmaf(dx[j][i], y[i], dc[j][i]);
+                dc[j][i] = fmaf(dx[j][i], y[j][i], dc[j][i]);
                 c[i] *= dx[j][i];
             }
             Pack<TR, V>::store(static_cast<TR *>(a.xo) + row * a.D + e, dx[j]);
             Pack<T, V>::store(static_cast<T *>(a.n) + row * a.D + e, c);
         }
+        if (NJ * V > 16) fetch(row + gridDim.x * (long)RPB);
     }
     const int width = a.y ? 2 * a.D : a.D;
 #pragma unroll
@@ -388,12 +420,17 @@ cudaError_t gated_go(const GatedNorm &a, bool bwd, cudaStream_t st) {
     const long blocks = (a.rows + kThreads / L - 1) / (kThreads / L);
     if (!bwd) {
         if (blocks > 0x7fffffffL) return cudaErrorInvalidValue;
-        gated_norm_fwd_kernel<T, V, L, NJ><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+        // four rows per thread once that still leaves every SM two CTAs; else one, for latency
+        constexpr int kRows = NJ == 1 && V != 1 ? 4 : 1;
+        if (blocks >= 2L * kRows * a.sms)
+            gated_norm_fwd_kernel<T, V, L, NJ, kRows><<<(unsigned)((blocks + kRows - 1) / kRows), kThreads, 0, st>>>(a);
+        else
+            gated_norm_fwd_kernel<T, V, L, NJ, 1><<<(unsigned)blocks, kThreads, 0, st>>>(a);
         return cudaGetLastError();
     }
     const int grid = (int)std::min(blocks, (long)norm_parts(a.sms));
     gated_norm_bwd_kernel<T, V, L, NJ><<<grid, kThreads, 0, st>>>(a);
-    norm_fold_kernel<<<(a.D + 31) / 32, 256, 0, st>>>(a.part, grid, a.D, a.dw, nullptr);
+    norm_fold_kernel<<<(a.D + 31) / 32, 1024, 0, st>>>(a.part, grid, a.D, a.dw, nullptr);
     return cudaGetLastError();
 }
 
@@ -427,10 +464,12 @@ cudaError_t residual_go(const ResidualNorm &a, bool bwd, cudaStream_t st) {
         residual_norm_fwd_kernel<TR, T, V, L, NJ><<<(unsigned)blocks, threads, 0, st>>>(a);
         return cudaGetLastError();
     }
-    const int grid = (int)std::min(blocks, (long)norm_parts(a.sms));
+    // a partial sum of dw (and dc) per CTA costs as much traffic as rows do: two CTAs of a row per SM, which the
+    // prefetched row keeps busy; narrow rows (a warp each) have narrow partial sums
+    const int grid = (int)std::min(blocks, (long)(L > 32 ? 2 : 4) * a.sms);
     residual_norm_bwd_kernel<TR, T, V, L, NJ><<<grid, threads, 0, st>>>(a);
     const int width = a.y ? 2 * a.D : a.D;
-    norm_fold_kernel<<<(width + 31) / 32, 256, 0, st>>>(a.part, grid, a.D, a.dw, a.y ? a.dc : nullptr);
+    norm_fold_kernel<<<(width + 31) / 32, 1024, 0, st>>>(a.part, grid, a.D, a.dw, a.y ? a.dc : nullptr);
     return cudaGetLastError();
 }
 

@@ -73,7 +73,6 @@ kda_status run_fwd(LinFwd &a, void *ws, kda_dtype dt, cudaStream_t st) {
         return done(launch_state_passthrough(p, st));
     }
     if (!use_tc(a.dk, a.dv, dt, a.max_len)) return done(launch_linear_scan(a, st));
-    if (cudaMemsetAsync(ws, 0, 2 * sizeof(int), st) != cudaSuccess) return KDA_ERR_CUDA;
     return done(launch_linear_tc(a, st));
 }
 
@@ -224,7 +223,6 @@ kda_status kda_linear_chunk_bwd(const void *q, const void *k, const void *v, con
     a.hdr = static_cast<WsHeader *>(ws);
     a.ws = static_cast<char *>(ws) + kWsHeader;
     if (!use_tc(dk, dv, dtype, T)) return done(launch_linear_scan_bwd(a, st));
-    if (cudaMemsetAsync(ws, 0, 2 * sizeof(int), st) != cudaSuccess) return KDA_ERR_CUDA;
     return done(launch_linear_tc_bwd(a, st));
 }
 

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kWalkThreads) linear_walk_kernel(Walk w) {
     __shared__ float s_a[kTile], s_qk[kTile];
 
     const int nsl = w.DV / kCols, sl = blockIdx.x % nsl, item = blockIdx.x / nsl, hv = blockIdx.y;
-    if (blockIdx.x == 0 && hv == 0 && threadIdx.x == 0) w.hdr->error = 0;
+    if (blockIdx.x == 0 && hv == 0 && threadIdx.x == 0 && w.hdr) w.hdr->error = 0;
     LinItem it;
     if (!lin_item(w.s, w.L, item, it)) return;
     if (!OUT && it.p == it.nseg - 1) return;                 // nobody reads the last segment's memory

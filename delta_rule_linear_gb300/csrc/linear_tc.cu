@@ -72,6 +72,7 @@ struct TcWalk {
     long long ob, ot, oh;
     float *loc, *gam;       // per (item, head): [DK, DV], decay factor
     WsHeader *hdr;
+    int clear;              // this launch is the call's first: it clears the error word
 };
 
 // The sequence of rank r by decreasing length (ties: lower index first); whole warp.
@@ -137,6 +138,8 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         return;
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (no wait can run out before the first CTA has got here)
+    if (w.clear && blockIdx.x == 0 && tid == 0) w.hdr->error = 0;
     const int hv = blockIdx.x % w.HV;
     LinItem it;
     if (!walk_item(w, blockIdx.x / w.HV, it)) return;
@@ -552,6 +555,7 @@ linear_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
         return;
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (w.clear && blockIdx.x == 0 && tid == 0) w.hdr->error = 0;
     const int hv = blockIdx.x % w.HV, item = blockIdx.x / w.HV;
     LinItem it;
     if (!lin_item(w.s, w.L, item, it) || it.p == it.nseg - 1) return;   // nobody reads the last segment's
@@ -763,15 +767,16 @@ cudaError_t go(const LinFwd &a, const TcWalk &w, long items, bool split, const C
     using LC = LocalCfg<DK, DV>;
     if (items * a.HV > 0x7fffffffL) return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)(items * a.HV);
+    static SmemOnce local_once, walk_once;
     cudaError_t e;
+    TcWalk first = w;
+    first.clear = 1;
     if (split) {
-        e = cudaFuncSetAttribute(linear_local_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, LC::SMEM);
-        if (e != cudaSuccess) return e;
-        linear_local_kernel<DK, DV><<<grid, kLocalThreads, LC::SMEM, st>>>(mk, mv, w);
+        if ((e = local_once(linear_local_kernel<DK, DV>, LC::SMEM)) != cudaSuccess) return e;
+        linear_local_kernel<DK, DV><<<grid, kLocalThreads, LC::SMEM, st>>>(mk, mv, first);
     }
-    e = cudaFuncSetAttribute(linear_chunk_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, WC::SMEM);
-    if (e != cudaSuccess) return e;
-    linear_chunk_kernel<DK, DV><<<grid, kWalkThreads, WC::SMEM, st>>>(mq, mk, mv, w);
+    if ((e = walk_once(linear_chunk_kernel<DK, DV>, WC::SMEM)) != cudaSuccess) return e;
+    linear_chunk_kernel<DK, DV><<<grid, kWalkThreads, WC::SMEM, st>>>(mq, mk, mv, split ? w : first);
     return cudaGetLastError();
 }
 

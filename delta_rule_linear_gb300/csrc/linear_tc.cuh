@@ -2,6 +2,8 @@
 // chunk constants, bounded waits, operand layouts, the three-part operand, tensor maps.
 #pragma once
 
+#include <atomic>
+
 #include "linear_internal.cuh"
 #include "tc_ptx.cuh"
 #include "tma_host.cuh"
@@ -138,6 +140,21 @@ inline bool token_map(CUtensorMap *map, const LinView &v, int D, int heads, long
     const uint32_t box[4] = {64, 1, (uint32_t)rows, 1};
     return make_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.p, dims, st, box, true);
 }
+
+// A kernel's dynamic shared memory limit, raised once per device.
+struct SmemOnce {
+    std::atomic<unsigned long long> done{0};
+    template <typename K> cudaError_t operator()(K *kernel, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const unsigned long long bit = 1ull << (dev & 63);
+        if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
 
 inline size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 

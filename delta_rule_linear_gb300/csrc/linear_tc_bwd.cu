@@ -52,6 +52,7 @@ struct BwdParams {
     float *fq, *fk;             // per-value-head fp32 dq, dk [B, T, HV, DK] when heads are shared
     float *dg;                  // per-token ddecay [B, T, HV] or nullptr
     WsHeader *hdr;
+    int clear;                  // the call's first launch: clears the error word
 };
 
 // ------------------------------------------------------------------------------ 1: contributions
@@ -87,6 +88,7 @@ linear_part_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         return;
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (w.clear && blockIdx.x == 0 && tid == 0) w.hdr->error = 0;
     const int slots = w.pairs * w.nch, items = 2 * slots;
     const int mine = ((int)blockIdx.x < items) ? (items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
     if (tid == 0) {
@@ -726,14 +728,15 @@ cudaError_t run_groups(const LinBwd &a, BwdParams w, const CUtensorMap &mq, cons
                        const CUtensorMap &mo, cudaStream_t st) {
     using PC = PartCfg<DK, DV>;
     using GC = GradCfg<DK, DV>;
-    cudaError_t e = cudaFuncSetAttribute(linear_part_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, PC::SMEM);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(linear_grad_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, GC::SMEM);
+    static SmemOnce part_once, grad_once;
+    cudaError_t e = part_once(linear_part_kernel<DK, DV>, PC::SMEM);
+    if (e == cudaSuccess) e = grad_once(linear_grad_kernel<DK, DV>, GC::SMEM);
     if (e != cudaSuccess) return e;
     const long pairs = (long)a.B * a.HV, np = group_pairs(pairs, w.nch);
     constexpr int cells = DK * DV;
     for (long p0 = 0; p0 < pairs; p0 += np) {
         w.pair0 = p0;
+        w.clear = p0 == 0;
         w.pairs = (int)std::min(np, pairs - p0);
         const int slots = w.pairs * w.nch;
         linear_part_kernel<DK, DV><<<std::min(2 * slots, a.sms), kPartThreads, PC::SMEM, st>>>(mq, mk, mv, mo, w);

@@ -39,8 +39,8 @@ struct ResidualNorm {
     int sms;
 };
 
-// CTAs of a backward at most (each leaves one partial row of dw): eight per SM keep HBM busy.
-inline int norm_parts(int sms) { return 8 * sms; }
+// CTAs of a backward at most (each leaves one partial row of dw).
+inline int norm_parts(int sms) { return 4 * sms; }
 
 cudaError_t launch_gated_norm(const GatedNorm &a, bool bwd, cudaStream_t st);
 cudaError_t launch_residual_norm(const ResidualNorm &a, bool bwd, cudaStream_t st);
