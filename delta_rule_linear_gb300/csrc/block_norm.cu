@@ -24,50 +24,67 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename T, int V> struct Pack;   // V consecutive elements, one or two 16-byte accesses
-template <> struct Pack<float, 8> {
-    static __device__ __forceinline__ void load(const float *p, float (&x)[8]) {
-        const float4 a = *reinterpret_cast<const float4 *>(p), b = *(reinterpret_cast<const float4 *>(p) + 1);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    }
-    static __device__ __forceinline__ void store(float *p, const float (&x)[8]) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-    }
-};
-template <> struct Pack<float, 4> {
-    static __device__ __forceinline__ void load(const float *p, float (&x)[4]) {
-        const float4 a = *reinterpret_cast<const float4 *>(p);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    }
-    static __device__ __forceinline__ void store(float *p, const float (&x)[4]) {
-        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    }
-};
-template <> struct Pack<__nv_bfloat16, 8> {
-    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&x)[8]) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// V consecutive elements as they lie in memory (16-byte pieces), their values, and back.
+template <typename T, int V> struct Pack {
+    static constexpr int N = V * (int)sizeof(T) / 16;
+    struct Raw {
+        uint4 w[N];
+    };
+    static __device__ __forceinline__ Raw zero() {
+        Raw r;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(u[i] << 16);
-            x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        for (int i = 0; i < N; ++i) r.w[i] = make_uint4(0, 0, 0, 0);
+        return r;
+    }
+    static __device__ __forceinline__ Raw get(const T *p) {
+        Raw r;
+#pragma unroll
+        for (int i = 0; i < N; ++i) r.w[i] = reinterpret_cast<const uint4 *>(p)[i];
+        return r;
+    }
+    static __device__ __forceinline__ void open(const Raw &r, float (&x)[V]) {
+        const uint32_t *u = &r.w[0].x;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if constexpr (sizeof(T) == 4)
+                x[i] = __uint_as_float(u[i]);
+            else
+                x[i] = __uint_as_float((i & 1) ? (u[i / 2] & 0xffff0000u) : (u[i / 2] << 16));
         }
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&x)[8]) {
-        uint32_t u[4];
+    static __device__ __forceinline__ void load(const T *p, float (&x)[V]) { open(get(p), x); }
+    static __device__ __forceinline__ void store(T *p, const float (&x)[V]) {
+        Raw r;
+        uint32_t *u = &r.w[0].x;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t *>(&h);
+        for (int i = 0; i < V; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                u[i] = __float_as_uint(x[i]);
+            } else if (!(i & 1)) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x[i], x[i + 1]);
+                u[i / 2] = *reinterpret_cast<const uint32_t *>(&h);
+            }
         }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) reinterpret_cast<uint4 *>(p)[i] = r.w[i];
     }
 };
 template <typename T> struct Pack<T, 1> {
+    using Raw = T;
+    static __device__ __forceinline__ Raw zero() { return from_f32<T>(0.f); }
+    static __device__ __forceinline__ Raw get(const T *p) { return *p; }
+    static __device__ __forceinline__ void open(const Raw &r, float (&x)[1]) { x[0] = to_f32(r); }
     static __device__ __forceinline__ void load(const T *p, float (&x)[1]) { x[0] = to_f32(*p); }
     static __device__ __forceinline__ void store(T *p, const float (&x)[1]) { *p = from_f32<T>(x[0]); }
 };
+
+// Offset of a head row in an array of strides (t, h); contiguous arrays need no division, which would
+// cost more than the row's arithmetic.
+__device__ __forceinline__ long row_at(const NormView &v, long row, int H, int D, bool flat) {
+    if (flat) return row * D;
+    const long t = row / H;
+    return t * v.t + (row - t * H) * v.h;
+}
 
 // Sum over the L threads of a row: lanes of a warp (L <= 32) or the whole CTA (L = blockDim).
 // `s` holds one float per warp; consecutive calls alternate between two of them.
@@ -101,59 +118,70 @@ __device__ __forceinline__ float norm_back(float t, float x, float ss, float dot
 
 // ------------------------------------------------------------------------------ gated norm
 // L lanes per row (256 / L rows per CTA at a time), NJ packs of V elements per lane.
-// NR rows are loaded before the first is reduced: one row's two 16-byte loads per thread do not keep
-// enough bytes in flight (32768 x 32 rows of 128 bf16: 0.175 ms with one).
-template <typename T, int V, int L, int NJ, int NR>
+// The CTAs go round the rows; a thread's next two rows are in flight, unopened, while it works on one.
+template <typename T, int V, int L, int NJ>
 __global__ void __launch_bounds__(kThreads) gated_norm_fwd_kernel(GatedNorm a) {
-    constexpr int RPB = kThreads / L;
+    constexpr int RPB = kThreads / L, AH = NJ == 1 ? 2 : 1;
+    using Pk = Pack<T, V>;
     const int l = threadIdx.x % L;
-    const long row0 = blockIdx.x * (long)(RPB * NR) + threadIdx.x / L;
-    float x[NR][NJ][V], g[NR][NJ][V];
-#pragma unroll
-    for (int n = 0; n < NR; ++n) {
-        const long row = row0 + n * RPB;
+    typename Pk::Raw x[AH][NJ], g[AH][NJ];
+    float w[NJ][V];
+    auto fetch = [&](int k, long row) {
         const bool live = row < a.rows;
-        const long t = live ? row / a.H : 0;
-        const int h = live ? (int)(row - t * a.H) : 0;
-        const T *xp = static_cast<const T *>(a.x.p) + t * a.x.t + h * a.x.h;
-        const T *gp = static_cast<const T *>(a.g.p) + t * a.g.t + h * a.g.h;
+        const T *xp = static_cast<const T *>(a.x.p) + row_at(a.x, live ? row : 0, a.H, a.D, a.flat);
+        const T *gp = static_cast<const T *>(a.g.p) + row_at(a.g, live ? row : 0, a.H, a.D, a.flat);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             const int e = (l + L * j) * V;
-#pragma unroll
-            for (int i = 0; i < V; ++i) x[n][j][i] = g[n][j][i] = 0.f;
+            x[k][j] = g[k][j] = Pk::zero();
             if (live && e < a.D) {
-                Pack<T, V>::load(xp + e, x[n][j]);
-                if (a.act) Pack<T, V>::load(gp + e, g[n][j]);
+                x[k][j] = Pk::get(xp + e);
+                if (a.act) g[k][j] = Pk::get(gp + e);
             }
         }
+    };
+    const long step = gridDim.x * (long)RPB, first = blockIdx.x * (long)RPB + threadIdx.x / L;
+#pragma unroll
+    for (int k = 0; k < AH; ++k) fetch(k, first + k * step);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        const int e = (l + L * j) * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[j][i] = 0.f;
+        if (e < a.D) Pack<float, V>::load(a.w + e, w[j]);
     }
+    // whole CTAs go on together (the sums use every lane of a warp)
+    for (long row0 = first; row0 - threadIdx.x / L < a.rows; row0 += AH * step) {
 #pragma unroll
-    for (int n = 0; n < NR; ++n) {
-        const long row = row0 + n * RPB;
-        const bool live = row < a.rows;
-        float ss = 0.f;
+        for (int k = 0; k < AH; ++k) {
+            const long row = row0 + k * step;
+            float v[NJ][V], ga[NJ][V], ss = 0.f;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) ss = fmaf(x[n][j][i], x[n][j][i], ss);
-        ss = row_sum<L>(ss, nullptr);
-        const float r = rsqrtf(ss * a.inv_d + a.eps);
-        const long t = live ? row / a.H : 0;
-        T *yp = static_cast<T *>(a.y.p) + t * a.y.t + (live ? (int)(row - t * a.H) : 0) * a.y.h;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int e = (l + L * j) * V;
-            if (!live || e >= a.D) continue;
-            float w[V];
-            Pack<float, V>::load(a.w + e, w);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float y = x[n][j][i] * r * w[i];
-                if (a.act) y *= act_of(g[n][j][i], a.act);
-                x[n][j][i] = y;
+            for (int j = 0; j < NJ; ++j) {
+                Pk::open(x[k][j], v[j]);
+                Pk::open(g[k][j], ga[j]);
             }
-            Pack<T, V>::store(yp + e, x[n][j]);
+            fetch(k, row + AH * step);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) ss = fmaf(v[j][i], v[j][i], ss);
+            ss = row_sum<L>(ss, nullptr);
+            const float r = rsqrtf(ss * a.inv_d + a.eps);
+            if (row >= a.rows) continue;
+            T *yp = static_cast<T *>(a.y.p) + row_at(a.y, row, a.H, a.D, a.flat);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const int e = (l + L * j) * V;
+                if (e >= a.D) continue;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float y = v[j][i] * r * w[j][i];
+                    if (a.act) y *= act_of(ga[j][i], a.act);
+                    v[j][i] = y;
+                }
+                Pk::store(yp + e, v[j]);
+            }
         }
     }
 }
@@ -171,32 +199,46 @@ __global__ void __launch_bounds__(kThreads) gated_norm_bwd_kernel(GatedNorm a) {
         for (int i = 0; i < V; ++i) dw[j][i] = w[j][i] = 0.f;
         if (e < a.D) Pack<float, V>::load(a.w + e, w[j]);
     }
-    for (long row0 = blockIdx.x * (long)RPB; row0 < a.rows; row0 += gridDim.x * (long)RPB) {
-        const long row = row0 + rg;
+    using Pk = Pack<T, V>;
+    typename Pk::Raw ax[NJ], ag[NJ], ad[NJ];    // the next row, in flight
+    auto fetch = [&](long row) {
         const bool live = row < a.rows;
-        const long t = live ? row / a.H : 0;
-        const int h = live ? (int)(row - t * a.H) : 0;
-        const T *xp = static_cast<const T *>(a.x.p) + t * a.x.t + h * a.x.h;
-        const T *gp = static_cast<const T *>(a.g.p) + t * a.g.t + h * a.g.h;
-        const T *dyp = static_cast<const T *>(a.dy.p) + t * a.dy.t + h * a.dy.h;
-        float x[NJ][V], g[NJ][V], dy[NJ][V], ss = 0.f, dot = 0.f;
+        const long rr = live ? row : 0;
+        const T *xp = static_cast<const T *>(a.x.p) + row_at(a.x, rr, a.H, a.D, a.flat);
+        const T *gp = static_cast<const T *>(a.g.p) + row_at(a.g, rr, a.H, a.D, a.flat);
+        const T *dyp = static_cast<const T *>(a.dy.p) + row_at(a.dy, rr, a.H, a.D, a.flat);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             const int e = (l + L * j) * V;
-#pragma unroll
-            for (int i = 0; i < V; ++i) x[j][i] = g[j][i] = dy[j][i] = 0.f;
+            ax[j] = ag[j] = ad[j] = Pk::zero();
             if (live && e < a.D) {
-                Pack<T, V>::load(xp + e, x[j]);
-                Pack<T, V>::load(dyp + e, dy[j]);
-                if (a.act) Pack<T, V>::load(gp + e, g[j]);
+                ax[j] = Pk::get(xp + e);
+                ad[j] = Pk::get(dyp + e);
+                if (a.act) ag[j] = Pk::get(gp + e);
             }
         }
+    };
+    fetch(blockIdx.x * (long)RPB + rg);
+    for (long row0 = blockIdx.x * (long)RPB; row0 < a.rows; row0 += gridDim.x * (long)RPB) {
+        const long row = row0 + rg;
+        const bool live = row < a.rows;
+        const long rr = live ? row : 0;
+        float x[NJ][V], g[NJ][V], dy[NJ][V], ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            Pk::open(ax[j], x[j]);
+            Pk::open(ag[j], g[j]);
+            Pk::open(ad[j], dy[j]);
+        }
+        fetch(row + gridDim.x * (long)RPB);
+        float sg[NJ][V];                        // sigmoid of the gate: its two special-function operations once
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
+                sg[j][i] = a.act ? sigmoid(g[j][i]) : 1.f;
                 ss = fmaf(x[j][i], x[j][i], ss);
-                const float ac = a.act ? act_of(g[j][i], a.act) : 1.f;
+                const float ac = a.act == 1 ? g[j][i] * sg[j][i] : sg[j][i];
                 dot = fmaf(dy[j][i] * ac * w[j][i], x[j][i], dot);
             }
         ss = row_sum<L>(ss, nullptr);
@@ -208,16 +250,15 @@ __global__ void __launch_bounds__(kThreads) gated_norm_bwd_kernel(GatedNorm a) {
             if (!live || e >= a.D) continue;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float xn = x[j][i] * r, s = a.act ? sigmoid(g[j][i]) : 1.f;
+                const float s = sg[j][i], xn = x[j][i] * r, d = dy[j][i];
                 const float ac = a.act == 1 ? g[j][i] * s : s;
-                const float da = a.act == 1 ? s * (1.f + g[j][i] * (1.f - s)) : s * (1.f - s);
-                const float d = dy[j][i];
+                const float da = a.act == 1 ? fmaf(ac, 1.f - s, s) : s * (1.f - s);
                 dw[j][i] = fmaf(d * ac, xn, dw[j][i]);
-                x[j][i] = r * norm_back(d * ac * w[j][i], x[j][i], ss, dot, r2, a.eps, a.inv_d);
                 g[j][i] = d * xn * w[j][i] * da;
+                x[j][i] = r * norm_back(d * ac * w[j][i], x[j][i], ss, dot, r2, a.eps, a.inv_d);
             }
-            Pack<T, V>::store(static_cast<T *>(a.dx.p) + t * a.dx.t + h * a.dx.h + e, x[j]);
-            if (a.act) Pack<T, V>::store(static_cast<T *>(a.dg.p) + t * a.dg.t + h * a.dg.h + e, g[j]);
+            Pack<T, V>::store(static_cast<T *>(a.dx.p) + row_at(a.dx, rr, a.H, a.D, a.flat) + e, x[j]);
+            if (a.act) Pack<T, V>::store(static_cast<T *>(a.dg.p) + row_at(a.dg, rr, a.H, a.D, a.flat) + e, g[j]);
         }
     }
     // this CTA's share of dw, row groups in order
@@ -313,40 +354,50 @@ __global__ void __launch_bounds__(L > 32 ? L : kThreads) residual_norm_bwd_kerne
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int i = 0; i < V; ++i) dw[j][i] = dc[j][i] = 0.f;
-    // the next row's loads go out before this row is summed
-    float nx[NJ][V], nn[NJ][V], nd[NJ][V], ny[NJ][V];
-    auto fetch = [&](long row) {
+    // the next row's loads go out before this row is summed, where the registers hold two rows
+    constexpr bool kAhead = NJ * V <= 16 && L <= 256;
+    struct Row {
+        typename Pack<TR, V>::Raw x[NJ], dx[NJ];
+        typename Pack<T, V>::Raw dn[NJ], y[NJ];
+    };
+    auto fetch = [&](Row &r, long row) {
         const bool live = row < a.rows;
         const long rr = live ? row : 0;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             const int e = (l + L * j) * V;
-#pragma unroll
-            for (int i = 0; i < V; ++i) nx[j][i] = nn[j][i] = nd[j][i] = ny[j][i] = 0.f;
+            r.x[j] = r.dx[j] = Pack<TR, V>::zero();
+            r.dn[j] = r.y[j] = Pack<T, V>::zero();
             if (live && e < a.D) {
-                Pack<TR, V>::load(static_cast<const TR *>(a.x) + rr * a.xs + e, nx[j]);
-                Pack<T, V>::load(static_cast<const T *>(a.dn) + rr * a.dns + e, nn[j]);
-                if (a.dxo) Pack<TR, V>::load(static_cast<const TR *>(a.dxo) + rr * a.dxs + e, nd[j]);
-                if (a.y) Pack<T, V>::load(static_cast<const T *>(a.y) + rr * a.ys + e, ny[j]);
+                r.x[j] = Pack<TR, V>::get(static_cast<const TR *>(a.x) + rr * a.xs + e);
+                r.dn[j] = Pack<T, V>::get(static_cast<const T *>(a.dn) + rr * a.dns + e);
+                if (a.dxo) r.dx[j] = Pack<TR, V>::get(static_cast<const TR *>(a.dxo) + rr * a.dxs + e);
+                if (a.y) r.y[j] = Pack<T, V>::get(static_cast<const T *>(a.y) + rr * a.ys + e);
             }
         }
     };
-    fetch(blockIdx.x * (long)RPB + rg);
+    Row ahead;
+    if constexpr (kAhead) fetch(ahead, blockIdx.x * (long)RPB + rg);
     int turn = 0;   // the two sums of consecutive rows use two sets of shared floats
     for (long row0 = blockIdx.x * (long)RPB; row0 < a.rows; row0 += gridDim.x * (long)RPB, turn ^= 1) {
         const long row = row0 + rg;
         const bool live = row < a.rows;
-        float x[NJ][V], dn[NJ][V], dx[NJ][V], y[NJ][V], ss = 0.f, dot = 0.f;
+        float ss = 0.f, dot = 0.f;
+        Row r0;
+        if constexpr (kAhead) {
+            r0 = ahead;
+            fetch(ahead, row + gridDim.x * (long)RPB);
+        } else {
+            fetch(r0, row);
+        }
+        float x[NJ][V], dn[NJ][V], dx[NJ][V], y[NJ][V];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                x[j][i] = nx[j][i];
-                dn[j][i] = nn[j][i];
-                dx[j][i] = nd[j][i];
-                y[j][i] = ny[j][i];
-            }
-        if (NJ * V <= 16) fetch(row + gridDim.x * (long)RPB);   // wider rows have no registers for it
+        for (int j = 0; j < NJ; ++j) {
+            Pack<TR, V>::open(r0.x[j], x[j]);
+            Pack<T, V>::open(r0.dn[j], dn[j]);
+            Pack<TR, V>::open(r0.dx[j], dx[j]);
+            Pack<T, V>::open(r0.y[j], y[j]);
+        }
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             const int e = (l + L * j) * V;
@@ -383,7 +434,6 @@ __global__ void __launch_bounds__(L > 32 ? L : kThreads) residual_norm_bwd_kerne
             Pack<TR, V>::store(static_cast<TR *>(a.xo) + row * a.D + e, dx[j]);
             Pack<T, V>::store(static_cast<T *>(a.n) + row * a.D + e, c);
         }
-        if (NJ * V > 16) fetch(row + gridDim.x * (long)RPB);
     }
     const int width = a.y ? 2 * a.D : a.D;
 #pragma unroll
@@ -420,12 +470,7 @@ cudaError_t gated_go(const GatedNorm &a, bool bwd, cudaStream_t st) {
     const long blocks = (a.rows + kThreads / L - 1) / (kThreads / L);
     if (!bwd) {
         if (blocks > 0x7fffffffL) return cudaErrorInvalidValue;
-        // four rows per thread once that still leaves every SM two CTAs; else one, for latency
-        constexpr int kRows = NJ == 1 && V != 1 ? 4 : 1;
-        if (blocks >= 2L * kRows * a.sms)
-            gated_norm_fwd_kernel<T, V, L, NJ, kRows><<<(unsigned)((blocks + kRows - 1) / kRows), kThreads, 0, st>>>(a);
-        else
-            gated_norm_fwd_kernel<T, V, L, NJ, 1><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+        gated_norm_fwd_kernel<T, V, L, NJ><<<(unsigned)std::min(blocks, 8L * a.sms), kThreads, 0, st>>>(a);
         return cudaGetLastError();
     }
     const int grid = (int)std::min(blocks, (long)norm_parts(a.sms));
@@ -466,7 +511,7 @@ cudaError_t residual_go(const ResidualNorm &a, bool bwd, cudaStream_t st) {
     }
     // a partial sum of dw (and dc) per CTA costs as much traffic as rows do: two CTAs of a row per SM, which the
     // prefetched row keeps busy; narrow rows (a warp each) have narrow partial sums
-    const int grid = (int)std::min(blocks, (long)(L > 32 ? 2 : 4) * a.sms);
+    const int grid = (int)std::min(blocks, (long)(L > 32 ? 2 : 8) * a.sms);
     residual_norm_bwd_kernel<TR, T, V, L, NJ><<<grid, threads, 0, st>>>(a);
     const int width = a.y ? 2 * a.D : a.D;
     norm_fold_kernel<<<(width + 31) / 32, 1024, 0, st>>>(a.part, grid, a.D, a.dw, a.y ? a.dc : nullptr);
@@ -492,9 +537,13 @@ cudaError_t residual_pick(const ResidualNorm &a, bool vec, bool bwd, cudaStream_
 
 }  // namespace
 
-cudaError_t launch_gated_norm(const GatedNorm &a, bool bwd, cudaStream_t st) {
-    const int V = a.dtype == DType::BF16 ? 8 : 4;
+cudaError_t launch_gated_norm(const GatedNorm &a0, bool bwd, cudaStream_t st) {
+    const int V = a0.dtype == DType::BF16 ? 8 : 4;
+    GatedNorm a = a0;
     bool vec = a.D % V == 0;
+    a.flat = 1;
+    for (const NormView *v : {&a.x, &a.g, &a.y, &a.dy, &a.dx, &a.dg})
+        if (v->p && (v->t != (long long)a.H * a.D || (a.H > 1 && v->h != a.D))) a.flat = 0;
     for (const NormView *v : {&a.x, &a.g, &a.y, &a.dy, &a.dx, &a.dg})
         if (v->p && ((reinterpret_cast<uintptr_t>(v->p) & 15) || v->t % V || v->h % V)) vec = false;
     if (reinterpret_cast<uintptr_t>(a.w) & 15) vec = false;

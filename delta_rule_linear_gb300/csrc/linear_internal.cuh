@@ -146,10 +146,10 @@ size_t linear_tc_bwd_scratch_bytes(int B, int T, int H, int HV, int dk, int dv, 
 cudaError_t launch_linear_tc_bwd(const LinBwd &a, cudaStream_t st);
 
 // Reductions the backwards share (linear_scan.cu): the value heads of a shared q/k head added
-// up (fp32 [rows, HV, D] -> out[rows, H, D] of the input type), and a fixed decay's gradient
-// (per-token [B * T, HV] -> [HV]).
-cudaError_t launch_fold_heads(const float *src, const LinView &dst, DType dt, int B, int T, int H, int m, int D,
-                              cudaStream_t st);
+// up, dq and dk at once (fp32 [rows, HV, D] -> out[rows, H, D] of the input type), and a fixed decay's
+// gradient (per-token [B * T, HV] -> [HV]).
+cudaError_t launch_fold_heads(const float *src0, const LinView &dst0, const float *src1, const LinView &dst1, DType dt,
+                              int B, int T, int H, int m, int D, cudaStream_t st);
 cudaError_t launch_sum_rows(const float *src, float *dst, long rows, int cols, cudaStream_t st);
 
 }  // namespace kda

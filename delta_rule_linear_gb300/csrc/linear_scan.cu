@@ -131,8 +131,14 @@ template <typename T> __device__ __forceinline__ void put_vec(float *dst, const 
 }
 
 // OUT: the second launch (outputs, final memory); otherwise a segment's local memory.
+// Up to three walks of the same role dimensions in one launch (a gradient's are as short as its launches).
+struct Walks {
+    Walk w[3];
+};
+
 template <typename T, int DK, bool OUT, bool RD>
-__global__ void __launch_bounds__(kWalkThreads) linear_walk_kernel(Walk w) {
+__global__ void __launch_bounds__(kWalkThreads) linear_walk_kernel(const __grid_constant__ Walks ws) {
+    const Walk &w = ws.w[blockIdx.z];
     constexpr int R = DK / 32, VN = Vec<T>::N;
     constexpr int QV = kTile * DK / VN;                      // 16-byte pieces of a q or k tile
     constexpr int NQ = (QV + kWalkThreads - 1) / kWalkThreads;
@@ -300,7 +306,7 @@ __global__ void __launch_bounds__(kWalkThreads) linear_walk_kernel(Walk w) {
                 // x . (output without the token's own pair), this CTA's 32 columns
                 const int t = tid >> 3, e = (tid & 7) * 4;
                 float d = 0.f;
-                if (t < nt) {
+                if (w.rd && t < nt) {
                     const T *xp = static_cast<const T *>(w.x.p) + b * w.x.b + (hv / w.gx) * w.x.h +
                                   tok(u + t) * w.x.t + col0 + e;
 #pragma unroll
@@ -308,7 +314,7 @@ __global__ void __launch_bounds__(kWalkThreads) linear_walk_kernel(Walk w) {
                 }
 #pragma unroll
                 for (int off = 4; off; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-                if (t < nt && (tid & 7) == 0)
+                if (w.rd && t < nt && (tid & 7) == 0)
                     w.rd[(size_t)sl * w.rows * w.HV + ((size_t)(w.s.cu ? 0 : (long)it.n * w.s.T) + tok(u + t)) * w.HV +
                          hv] = d;
             }
@@ -363,31 +369,31 @@ int walk_segment(int nseq, int HV, int nsl, long total, int max_len, bool varlen
     return (int)((L + kTile - 1) / kTile * kTile);
 }
 
-template <typename T, int DK>
-cudaError_t run_walk_t(const Walk &w, long items, int max_len, cudaStream_t st) {
+template <typename T, int DK, bool RD>
+cudaError_t run_walk_t(const Walks &ws, int n, long items, int max_len, cudaStream_t st) {
+    const Walk &w = ws.w[0];
     const int nsl = w.DV / kCols;
     if (items * nsl > 0x7fffffffL) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)(items * nsl), (unsigned)w.HV);
-    if (max_len > w.L) linear_walk_kernel<T, DK, false, false><<<grid, kWalkThreads, 0, st>>>(w);
-    if (w.rd)
-        linear_walk_kernel<T, DK, true, true><<<grid, kWalkThreads, 0, st>>>(w);
-    else
-        linear_walk_kernel<T, DK, true, false><<<grid, kWalkThreads, 0, st>>>(w);
+    const dim3 grid((unsigned)(items * nsl), (unsigned)w.HV, n);
+    if (max_len > w.L) linear_walk_kernel<T, DK, false, false><<<grid, kWalkThreads, 0, st>>>(ws);
+    linear_walk_kernel<T, DK, true, RD><<<grid, kWalkThreads, 0, st>>>(ws);
     return cudaGetLastError();
 }
 
-cudaError_t run_walk(const Walk &w, DType dt, int DK, long items, int max_len, cudaStream_t st) {
+// n walks alike but for their arrays (same role dimensions, segments, heads); RD: some have row dots
+template <bool RD>
+cudaError_t run_walk(const Walks &ws, int n, DType dt, int DK, long items, int max_len, cudaStream_t st) {
     if (dt == DType::BF16) {
         switch (DK) {
-            case 32: return run_walk_t<__nv_bfloat16, 32>(w, items, max_len, st);
-            case 64: return run_walk_t<__nv_bfloat16, 64>(w, items, max_len, st);
-            default: return run_walk_t<__nv_bfloat16, 128>(w, items, max_len, st);
+            case 32: return run_walk_t<__nv_bfloat16, 32, RD>(ws, n, items, max_len, st);
+            case 64: return run_walk_t<__nv_bfloat16, 64, RD>(ws, n, items, max_len, st);
+            default: return run_walk_t<__nv_bfloat16, 128, RD>(ws, n, items, max_len, st);
         }
     }
     switch (DK) {
-        case 32: return run_walk_t<float, 32>(w, items, max_len, st);
-        case 64: return run_walk_t<float, 64>(w, items, max_len, st);
-        default: return run_walk_t<float, 128>(w, items, max_len, st);
+        case 32: return run_walk_t<float, 32, RD>(ws, n, items, max_len, st);
+        case 64: return run_walk_t<float, 64, RD>(ws, n, items, max_len, st);
+        default: return run_walk_t<float, 128, RD>(ws, n, items, max_len, st);
     }
 }
 
@@ -439,7 +445,10 @@ linear_dgate_kernel(const float *rq, int nq, const float *rk, int nk, const floa
 }
 
 template <typename T>
-__global__ void fold_heads_kernel(const float *src, LinView dst, long n, int Tlen, int H, int m, int D) {
+__global__ void fold_heads_kernel(const float *src0, LinView dst0, const float *src1, LinView dst1, long n, int Tlen, int H,
+                                  int m, int D) {
+    const float *src = blockIdx.y ? src1 : src0;
+    const LinView &dst = blockIdx.y ? dst1 : dst0;
     for (long i = blockIdx.x * (long)blockDim.x + threadIdx.x; i < n; i += (long)gridDim.x * blockDim.x) {
         const int c = (int)(i % D);
         const long rh = i / D;
@@ -507,17 +516,19 @@ cudaError_t launch_linear_scan(const LinFwd &a, cudaStream_t st) {
     const long items = lin_items(a.s.nseq, a.total, a.max_len, varlen, w.L);
     w.loc = static_cast<float *>(a.ws);
     w.gam = reinterpret_cast<float *>(static_cast<char *>(a.ws) + round256((size_t)items * a.HV * a.dk * a.dv * 4));
-    return run_walk(w, a.dtype, a.dk, items, a.max_len, st);
+    Walks ws{};
+    ws.w[0] = w;
+    return run_walk<false>(ws, 1, a.dtype, a.dk, items, a.max_len, st);
 }
 
-cudaError_t launch_fold_heads(const float *src, const LinView &dst, DType dt, int B, int T, int H, int m, int D,
-                              cudaStream_t st) {
+cudaError_t launch_fold_heads(const float *src0, const LinView &dst0, const float *src1, const LinView &dst1, DType dt,
+                              int B, int T, int H, int m, int D, cudaStream_t st) {
     const long n = (long)B * T * H * D;
-    const int grid = (int)std::min(4096L, (n + 255) / 256);
+    const dim3 grid((unsigned)std::min(4096L, (n + 255) / 256), 2);
     if (dt == DType::BF16)
-        fold_heads_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(src, dst, n, T, H, m, D);
+        fold_heads_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(src0, dst0, src1, dst1, n, T, H, m, D);
     else
-        fold_heads_kernel<float><<<grid, 256, 0, st>>>(src, dst, n, T, H, m, D);
+        fold_heads_kernel<float><<<grid, 256, 0, st>>>(src0, dst0, src1, dst1, n, T, H, m, D);
     return cudaGetLastError();
 }
 
@@ -526,16 +537,15 @@ cudaError_t launch_sum_rows(const float *src, float *dst, long rows, int cols, c
     return cudaGetLastError();
 }
 
-// Scratch of the gradients: [segment memories of the largest walk][h_T][row dots of dq and
-// dk][per-value-head dq, dk when heads are shared][per-token ddecay when it is summed]
+// Scratch of the gradients: [h_T][row dots of dq and dk][per-token ddecay when it is summed]
+// [per-value-head dq, dk when heads are shared][segment memories of the three walks]
 size_t linear_scan_bwd_scratch_bytes(int B, int T, int H, int HV, int dk, int dv, int sms) {
-    size_t seg = 0;
-    const int dims[3][2] = {{dv, dk}, {dk, dv}, {dv, dk}};
+    size_t n = 0;
+    const int dims[3][2] = {{dv, dk}, {dv, dk}, {dk, dv}};
     for (auto &d : dims)
-        seg = std::max(seg, walk_scratch(B, HV, d[0], d[1], T, T, false,
-                                         walk_segment(B, HV, d[1] / kCols, T, T, false, sms)));
+        n += walk_scratch(B, HV, d[0], d[1], T, T, false, walk_segment(B, HV, d[1] / kCols, T, T, false, sms));
     const size_t rows = (size_t)B * T * HV;
-    size_t n = seg + round256((size_t)B * HV * dk * dv * 4) + 2 * round256(rows * (dk / kCols) * 4) + round256(rows * 4);
+    n += round256((size_t)B * HV * dk * dv * 4) + 2 * round256(rows * (dk / kCols) * 4) + round256(rows * 4);
     if (HV > H) n += 2 * round256(rows * dk * 4);
     return n;
 }
@@ -553,47 +563,60 @@ cudaError_t launch_linear_scan_bwd(const LinBwd &a, cudaStream_t st) {
         fq = carve(rows * a.dk * 4);
         fk = carve(rows * a.dk * 4);
     }
-    Walk w{};
-    w.hdr = a.hdr;
-    w.g = a.g; w.s.nseq = a.B; w.s.T = a.T; w.HV = a.HV;
-    w.rows = (long)a.B * a.T;
     const bool want_g = a.g.p && a.dg;
-    auto go = [&](int DK, int DV, const LinView &out, float *f32out) {
+    auto walk = [&](int DK, int DV, const LinView &out, float *f32out) {
+        Walk w{};
+        w.hdr = a.hdr;
+        w.g = a.g; w.s.nseq = a.B; w.s.T = a.T; w.HV = a.HV;
+        w.rows = (long)a.B * a.T;
         w.DV = DV;
         w.L = walk_segment(a.B, a.HV, DV / kCols, a.T, a.T, false, a.sms);
-        const long items = lin_items(a.B, a.T, a.T, false, w.L);
-        w.loc = reinterpret_cast<float *>(p);
-        w.gam = reinterpret_cast<float *>(p + round256((size_t)items * a.HV * DK * DV * 4));
+        const size_t need = walk_scratch(a.B, a.HV, DK, DV, a.T, a.T, false, w.L);
+        if (need) {
+            const size_t slots = (size_t)lin_items(a.B, a.T, a.T, false, w.L) * a.HV;
+            w.loc = carve(slots * DK * DV * 4);
+            w.gam = carve(slots * 4);
+        }
         w.o_f32 = f32out != nullptr;
         w.o = f32out ? static_cast<void *>(f32out) : const_cast<void *>(out.p);
         w.ob = f32out ? (long long)a.T * a.HV * DV : out.b;
         w.ot = f32out ? (long long)a.HV * DV : out.t;
         w.oh = f32out ? DV : out.h;
-        return run_walk(w, a.dtype, DK, items, a.T, st);
+        return w;
     };
+    Walks qk{}, v{};
     // dq: forwards on (do, v, k); memory transposed, [dv, dk]
-    w.q = a.d_o; w.gq = 1; w.k = a.v; w.gk = 1; w.v = a.k; w.gv = m;
-    w.x = a.q; w.gx = m; w.rd = want_g ? rq : nullptr;
-    w.add_scale = 1.f; w.out_scale = a.scale;
-    w.h0 = a.h0; w.hT = want_g && a.dhT ? hT : nullptr; w.si = 1; w.sj = a.dv;
-    cudaError_t e = go(a.dv, a.dk, a.dq, fq);
-    if (e != cudaSuccess) return e;
+    Walk &wq = qk.w[0] = walk(a.dv, a.dk, a.dq, fq);
+    wq.q = a.d_o; wq.gq = 1; wq.k = a.v; wq.gk = 1; wq.v = a.k; wq.gv = m;
+    wq.x = a.q; wq.gx = m; wq.rd = want_g ? rq : nullptr;
+    wq.add_scale = 1.f; wq.out_scale = a.scale;
+    wq.h0 = a.h0; wq.hT = want_g && a.dhT ? hT : nullptr; wq.si = 1; wq.sj = a.dv;
     // dk: backwards on (v, do, q), memory [dv, dk]
-    w.rev = 1;
-    w.q = a.v; w.gq = 1; w.k = a.d_o; w.gk = 1; w.v = a.q; w.gv = m;
-    w.x = a.k; w.gx = m; w.rd = want_g ? rk : nullptr;
-    w.add_scale = a.scale; w.out_scale = 1.f;
-    w.h0 = a.dhT; w.hT = nullptr; w.si = 1; w.sj = a.dv;
-    if ((e = go(a.dv, a.dk, a.dk_, fk)) != cudaSuccess) return e;
+    Walk &wk = qk.w[1] = walk(a.dv, a.dk, a.dk_, fk);
+    wk.rev = 1;
+    wk.q = a.v; wk.gq = 1; wk.k = a.d_o; wk.gk = 1; wk.v = a.q; wk.gv = m;
+    wk.x = a.k; wk.gx = m; wk.rd = want_g ? rk : nullptr;
+    wk.add_scale = a.scale; wk.out_scale = 1.f;
+    wk.h0 = a.dhT; wk.si = 1; wk.sj = a.dv;
     // dv: backwards on (k, q, do), memory [dk, dv]; its final memory is the initial one's gradient
-    w.q = a.k; w.gq = m; w.k = a.q; w.gk = m; w.v = a.d_o; w.gv = 1;
-    w.x = LinView{}; w.rd = nullptr;
-    w.hT = a.dh0; w.si = a.dv; w.sj = 1;
-    if ((e = go(a.dk, a.dv, a.dv_, nullptr)) != cudaSuccess) return e;
-    if (m > 1) {
-        if ((e = launch_fold_heads(fq, a.dq, a.dtype, a.B, a.T, a.H, m, a.dk, st)) != cudaSuccess) return e;
-        if ((e = launch_fold_heads(fk, a.dk_, a.dtype, a.B, a.T, a.H, m, a.dk, st)) != cudaSuccess) return e;
+    Walk wv = walk(a.dk, a.dv, a.dv_, nullptr);
+    wv.rev = 1;
+    wv.q = a.k; wv.gq = m; wv.k = a.q; wv.gk = m; wv.v = a.d_o; wv.gv = wv.gx = 1;
+    wv.add_scale = a.scale; wv.out_scale = 1.f;
+    wv.h0 = a.dhT; wv.hT = a.dh0; wv.si = a.dv; wv.sj = 1;
+    const long items = lin_items(a.B, a.T, a.T, false, wq.L);
+    cudaError_t e;
+    if (a.dk == a.dv) {
+        qk.w[2] = wv;
+        e = run_walk<true>(qk, 3, a.dtype, a.dv, items, a.T, st);
+    } else {
+        v.w[0] = wv;
+        e = run_walk<true>(qk, 2, a.dtype, a.dv, items, a.T, st);
+        if (e == cudaSuccess)
+            e = run_walk<false>(v, 1, a.dtype, a.dk, lin_items(a.B, a.T, a.T, false, wv.L), a.T, st);
     }
+    if (e != cudaSuccess) return e;
+    if (m > 1 && (e = launch_fold_heads(fq, a.dq, fk, a.dk_, a.dtype, a.B, a.T, a.H, m, a.dk, st)) != cudaSuccess) return e;
     if (want_g) {
         const bool fixed = a.g.t == 0;
         linear_dgate_kernel<<<a.B * a.HV, kGradThreads, 0, st>>>(rq, a.dk / kCols, rk, a.dk / kCols, hT, a.dhT,

@@ -117,7 +117,7 @@ struct WalkCfg {
 };
 
 struct WalkCtl {
-    uint64_t full[2], done[2], s_full, q_free, p_ready, r_ready, o_full, o_free, s_ready, v_ready, lo_ready, kv_done, cleared, last;
+    uint64_t full[2], done[2], s_full, q_free, p_ready, r_ready, o_full, o_free, s_ready, v_ready, lo_ready, kv_done, cleared, start, last;
     uint32_t tmem;
     int fail;
     int strong[2];   // the chunk's decays exceed kMildSpan
@@ -156,6 +156,7 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         for (uint64_t *x : {&ctl->s_full, &ctl->q_free, &ctl->o_full, &ctl->kv_done, &ctl->last}) mbar_init(x, 1);
         for (uint64_t *x : {&ctl->p_ready, &ctl->r_ready, &ctl->o_free, &ctl->s_ready}) mbar_init(x, 128);
         for (uint64_t *x : {&ctl->v_ready, &ctl->lo_ready, &ctl->cleared}) mbar_init(x, 256);
+        mbar_init(&ctl->start, 512);
         ctl->fail = 0;
         fence_mbar_init();
     }
@@ -176,6 +177,38 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     const uint32_t tlane = tm + ((uint32_t)(32 * (warp & 3)) << 16);   // this warp's 32 TMEM lanes
     auto arr_g = [&](int c) { return reinterpret_cast<float *>(smem + Cf::ARR) + (c & 1) * 2 * kC; };
     auto stage = [&](int c) { return smem + (c & 1) * Cf::STAGE; };
+
+    // The segment's start state, 32 key channels to each of four warp groups (one group alone spent
+    // 1 us per 32 channels and earlier segment, all of it latency).
+    const size_t pair = (size_t)it.n * w.HV + hv;
+    if (warp < 16) {
+        const int i = tid & 127, cb = 32 * (warp >> 2);
+        if (nch > 0 && cb < DK && (i & ~31) < DV) {
+            float acc[32];
+            if (w.h0) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) acc[j] = w.h0[(pair * DK + cb + j) * DV + i];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) acc[j] = 0.f;
+            }
+#pragma unroll 1
+            for (int pp = 0; pp < it.p; ++pp) {
+                const size_t slot = (size_t)(it.first + pp) * w.HV + hv;
+                const float ga = w.gam[slot];
+                const float *l = w.loc + (slot * DK + cb) * DV + i;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) acc[j] = fmaf(acc[j], ga, l[j * DV]);
+            }
+            uint32_t x[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(acc[j]);
+            tmem_st32(tlane + Cf::T_S + cb, x);
+            tmem_st_wait();
+        }
+        tc_fence_before();
+        mbar_arrive(&ctl->start);
+    }
 
     if (warp == 20) {
         // ---- decays and loads
@@ -399,32 +432,18 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         // ---- the memory (thread = value channel i, TMEM lane i; dv = 64: warps 8 and 9)
         const int i = tid - 256;
         uint8_t *sb = smem + Cf::SB;
-        const size_t pair = (size_t)it.n * w.HV + hv;
         for (int c = 0; c < nch; ++c) {
             if (!wt.warp(&ctl->full[c & 1], (c >> 1) & 1, 16)) break;
             const float alpha = ex2(arr_g(c)[kC - 1]), beta = ctl->strong[c & 1] ? 1.f : alpha;
-            if (c > 0 && (!wt.warp(&ctl->q_free, (c - 1) & 1, 17) || !wt.warp(&ctl->kv_done, (c - 1) & 1, 18))) break;
+            if (c == 0 ? !wt.warp(&ctl->start, 0, 25)
+                       : !wt.warp(&ctl->q_free, (c - 1) & 1, 17) || !wt.warp(&ctl->kv_done, (c - 1) & 1, 18)) break;
             tc_fence_after();
             if (warp - 8 < DV / 32) {
 #pragma unroll 1
                 for (int cb = 0; cb < DK; cb += 32) {
                     uint32_t x[32];
-                    if (c > 0) {
-                        tmem_ld32(tlane + Cf::T_S + cb, x);
-                        tmem_ld_wait();
-                    } else {                       // the segment's start
-                        float acc[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) acc[j] = w.h0 ? w.h0[(pair * DK + cb + j) * DV + i] : 0.f;
-                        for (int pp = 0; pp < it.p; ++pp) {
-                            const size_t slot = (size_t)(it.first + pp) * w.HV + hv;
-                            const float ga2 = w.gam[slot];
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) acc[j] = fmaf(acc[j], ga2, w.loc[(slot * DK + cb + j) * DV + i]);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(acc[j]);
-                    }
+                    tmem_ld32(tlane + Cf::T_S + cb, x);
+                    tmem_ld_wait();
                     // operand: row i, 32 key channels
 #pragma unroll
                     for (int j = 0; j < 32; j += 8) {
@@ -733,11 +752,13 @@ linear_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
 }
 
 // ------------------------------------------------------------------------------ host
-// Chunks per segment.  In units of one chunk of the walk (0.85 us), a CTA costs about 3 to set up and
-// fill, a chunk of the local kernel 0.55, its launch 3, a start state's segment 0.6; every (sequence, head)
-// that finds no SM waits for the next wave.  Equal lengths: the cut with the least of it.  Packed
-// sequences: whole ones while the longest is no more than an SM's share of the work (taken longest
-// first they then fill the SMs evenly), else segments of half an SM's share.
+// Chunks per segment.  In units of one chunk of the walk (4.5 us at d = 128), a CTA costs about 3 to set up,
+// fill and drain, a chunk of the local kernel 0.5, its launch 1, a start state 0.2 per earlier segment; every
+// (sequence, head) that finds no SM waits for the next wave.  Equal lengths: the cut with the least of it, and
+// of cuts within 5 % the coarsest (a long segment's local memory stops early where decays are strong: B=1 T=32768
+// H=32 with softplus decays, 4 segments 0.35 ms, 9 segments 0.39 ms).  Packed sequences: whole ones while the
+// longest is no more than an SM's share of the work (taken longest first they then fill the SMs evenly),
+// else segments of half an SM's share.
 int plan_chunks(int nseq, int HV, long total, int max_len, bool varlen, int sms) {
     const int nch = std::max(1, (max_len + kC - 1) / kC);
     const long pairs = (long)nseq * HV;
@@ -751,8 +772,8 @@ int plan_chunks(int nseq, int HV, long total, int max_len, bool varlen, int sms)
     for (int p = 1; p <= std::min(nch, kMaxSegs); ++p) {
         const int lc = (nch + p - 1) / p, segs = (nch + lc - 1) / lc;
         double t = (double)((pairs * segs + sms - 1) / sms) * (lc + 3.0);
-        if (segs > 1) t += (double)((pairs * (segs - 1) + sms - 1) / sms) * (0.55 * lc + 3.0) + 3.0 + 0.6 * (segs - 1);
-        if (t < cost) {
+        if (segs > 1) t += (double)((pairs * (segs - 1) + sms - 1) / sms) * (0.5 * lc + 3.0) + 1.0 + 0.2 * (segs - 1);
+        if (t < 0.95 * cost) {
             cost = t;
             best = lc;
         }

@@ -795,10 +795,7 @@ cudaError_t launch_linear_tc_bwd(const LinBwd &a, cudaStream_t st) {
     else if (a.dv == 128) e = run_groups<64, 128>(a, w, mq, mk, mv, mo, st);
     else e = run_groups<64, 64>(a, w, mq, mk, mv, mo, st);
     if (e != cudaSuccess) return e;
-    if (m > 1) {
-        if ((e = launch_fold_heads(w.fq, a.dq, a.dtype, a.B, a.T, a.H, m, a.dk, st)) != cudaSuccess) return e;
-        if ((e = launch_fold_heads(w.fk, a.dk_, a.dtype, a.B, a.T, a.H, m, a.dk, st)) != cudaSuccess) return e;
-    }
+    if (m > 1 && (e = launch_fold_heads(w.fq, a.dq, w.fk, a.dk_, a.dtype, a.B, a.T, a.H, m, a.dk, st)) != cudaSuccess) return e;
     return fixed ? launch_sum_rows(dgt, a.dg, (long)a.B * a.T, a.HV, st) : cudaSuccess;
 }
 

@@ -20,6 +20,7 @@ struct GatedNorm {
     float *dw, *part;        // [D]; [norm_parts, D] scratch
     long rows;               // tokens * heads
     int H, D, act;           // act: 0 none, 1 silu, 2 sigmoid
+    int flat;                // every array is contiguous (set by the launcher)
     float eps, inv_d;
     DType dtype;
     int sms;
@@ -40,7 +41,7 @@ struct ResidualNorm {
 };
 
 // CTAs of a backward at most (each leaves one partial row of dw).
-inline int norm_parts(int sms) { return 4 * sms; }
+inline int norm_parts(int sms) { return 8 * sms; }
 
 cudaError_t launch_gated_norm(const GatedNorm &a, bool bwd, cudaStream_t st);
 cudaError_t launch_residual_norm(const ResidualNorm &a, bool bwd, cudaStream_t st);
