@@ -55,7 +55,6 @@ constexpr float kZeroWeight = -150.f;          // 2^x is 0 in fp32 below this
 // memory takes too: one accumulator and one factor per column, none beyond 2^124.  Stronger decays (a
 // restart among them) get every weight e^{G_i - G_j} from its own exponent and the first term
 // rescaled in between.
-constexpr float kMildSpan = 62.f;
 constexpr int kMaxSegs = 64;                   // segments of a sequence at most (equal lengths)
 constexpr int kSortSeqs = 128;                 // packed sequences ranked by length up to this many
 

@@ -17,6 +17,7 @@ constexpr int kC = 128;                        // tokens per chunk
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kStatusDeviceTimeout = 8;        // KDA_ERR_DEVICE_TIMEOUT
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMildSpan = 62.f;              // running log2 decays of a chunk that factors over rows and columns
 
 // 2^x (ex2.approx: 2 ulp; results below 2^-126 are 0)
 __device__ __forceinline__ float ex2(float x) {

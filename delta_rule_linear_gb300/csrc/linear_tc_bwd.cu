@@ -276,28 +276,33 @@ __global__ void __launch_bounds__(256) linear_chain_kernel(BwdParams w, int cell
 // M^T is.  Loops are kept rolled and what is used three times out of line: the chunk's code runs once per
 // chunk, and instruction fetch is what a longer one waits for (8 warps and unrolled passes: 0.109 ms at
 // the training shape instead of 0.067).
-// The first terms of dQ and dK are read back before their second terms are added: they take their row factor
-// there, and their dots with q and k (S and R go in as two bf16 parts for those dots).
+// The first terms of dQ and dK are read back before their second terms are added, for their dots with q and k
+// (S and R go in as two bf16 parts for those dots).  Row factors are left to the stores,
+//     dQ_i = E_i [dO (e^{G_C} S)^T + sum_j m_ij w_j k_j],   E_i = c e^{G_i - G_C},
+//     dK_j = w_j [V R^T + sum_i m_ij E_i q_i],   dV_j = w_j [K R + sum_i s_ij E_i do_i],   w_j = e^{G_C - G_j},
+// which takes one multiplication per element and no exponential, as long as the chunk's log2 decays stay within
+// +-kMildSpan; beyond that every weight has its own exponent and the first terms are rescaled in place.
 constexpr int kGradThreads = 17 * 32;
 
 template <int DK, int DV>
 struct GradCfg {
     static constexpr int QB = kC * DK * 2, VB = kC * DV * 2, XB = DK * DV * 2;
     static constexpr int Q = 0, K = QB, V = 2 * QB, O = 2 * QB + VB, XH = 2 * QB + 2 * VB, XL = XH + XB;
-    static constexpr int ARR = XL + XB;         // G, then quarters of: r, c, q dots, k dots
-    static constexpr int CTL = ARR + 17 * kC * 4, SMEM = CTL + 256;
+    static constexpr int ARR = XL + XB;         // G, E, w, then quarters of: r, c, q dots, k dots
+    static constexpr int CTL = ARR + 19 * kC * 4, SMEM = CTL + 256;
     static_assert(SMEM <= 232448, "shared memory");
 };
 struct GradCtl {
-    uint64_t full, m, go, sync, last;
+    uint64_t full_qk, full_vo, m, go, sync, last;
     uint32_t tmem;
     int fail;
+    int strong;
     float dot[16];
 };
 static_assert(sizeof(GradCtl) <= 256, "control block");
 
-// 32 columns of a row of results, bf16, four lanes trading 16-byte pieces (rows u0 .. u0 + 3)
-__device__ __noinline__ void store_rows(uint32_t taddr, __nv_bfloat16 *p, long long ts, int rows, int lane) {
+// 32 columns of a row of results times f, bf16, four lanes trading 16-byte pieces (rows u0 .. u0 + 3)
+__device__ __noinline__ void store_rows(uint32_t taddr, float f, __nv_bfloat16 *p, long long ts, int rows, int lane) {
     uint32_t x[32];
     tmem_ld32(taddr, x);
     tmem_ld_wait();
@@ -307,7 +312,7 @@ __device__ __noinline__ void store_rows(uint32_t taddr, __nv_bfloat16 *p, long l
         uint32_t *pr = &r[j].x;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            pr[i] = pack_bf16(__uint_as_float(x[8 * j + 2 * i]), __uint_as_float(x[8 * j + 2 * i + 1]));
+            pr[i] = pack_bf16(f * __uint_as_float(x[8 * j + 2 * i]), f * __uint_as_float(x[8 * j + 2 * i + 1]));
     }
     trade4(r, lane);
 #pragma unroll
@@ -315,37 +320,43 @@ __device__ __noinline__ void store_rows(uint32_t taddr, __nv_bfloat16 *p, long l
         if (j < rows) *reinterpret_cast<uint4 *>(p + (long long)j * ts) = r[j];
 }
 // the same in fp32, a row to a thread (only where q/k heads are shared)
-__device__ __noinline__ void store_row_f32(uint32_t taddr, float *p, bool live) {
+__device__ __noinline__ void store_row_f32(uint32_t taddr, float f, float *p, bool live) {
     uint32_t x[32];
     tmem_ld32(taddr, x);
     tmem_ld_wait();
     if (live)
 #pragma unroll
         for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<uint4 *>(p + j) = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+            *reinterpret_cast<float4 *>(p + j) = make_float4(f * __uint_as_float(x[j]), f * __uint_as_float(x[j + 1]),
+                                                             f * __uint_as_float(x[j + 2]), f * __uint_as_float(x[j + 3]));
 }
-// Row factor f on 32 columns in place; the dot of the scaled row with columns c0 .. of row r of a bf16 tile
-// (nullptr: 0)
-__device__ __noinline__ float scale_row(uint32_t taddr, float f, const uint8_t *tile, int r, int c0) {
-    float dot = 0.f;
+// dot of 32 columns with columns c0 .. of row r of a bf16 tile
+__device__ __noinline__ float dot_row(uint32_t taddr, const uint8_t *tile, int r, int c0) {
+    float d0 = 0.f, d1 = 0.f;
+    uint32_t x[32];
+    tmem_ld32(taddr, x);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 32; j += 8) {
+        const uint4 t = *reinterpret_cast<const uint4 *>(tile + piece(kC, r, (c0 + j) / 8));
+        const uint32_t *pt = &t.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            d0 = fmaf(__uint_as_float(x[j + 2 * i]), __uint_as_float(pt[i] << 16), d0);
+            d1 = fmaf(__uint_as_float(x[j + 2 * i + 1]), __uint_as_float(pt[i] & 0xffff0000u), d1);
+        }
+    }
+    return d0 + d1;
+}
+// row factor on 32 columns in place
+__device__ __noinline__ void scale_row(uint32_t taddr, float f) {
     uint32_t x[32];
     tmem_ld32(taddr, x);
     tmem_ld_wait();
 #pragma unroll
     for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(f * __uint_as_float(x[i]));
     tmem_st32(taddr, x);
-    if (tile) {
-#pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-            const uint4 t = *reinterpret_cast<const uint4 *>(tile + piece(kC, r, (c0 + j) / 8));
-            const uint32_t *pt = &t.x;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                dot = fmaf(__uint_as_float(x[j + i]), __uint_as_float((i & 1) ? (pt[i / 2] & 0xffff0000u) : (pt[i / 2] << 16)), dot);
-        }
-    }
     tmem_st_wait();
-    return dot;
 }
 
 template <int DK, int DV>
@@ -364,7 +375,8 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int slots = w.pairs * w.nch;
     if (tid == 0) {
-        mbar_init(&ctl->full, 1);
+        mbar_init(&ctl->full_qk, 1);
+        mbar_init(&ctl->full_vo, 1);
         mbar_init(&ctl->m, 1);
         mbar_init(&ctl->go, 512);
         mbar_init(&ctl->sync, 512);
@@ -395,23 +407,24 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                        on_ = desc_mnmajor_sw128(sb + Cf::O, kC, 0);
         const uint64_t xh = desc_kmajor_sw128(sb + Cf::XH, DK, 0), xl = desc_kmajor_sw128(sb + Cf::XL, DK, 0),
                        xn = desc_mnmajor_sw128(sb + Cf::XH, DK, 0);
-        // tiles of the item at `slot`, as they become free: V, then Q and K, then dO (one barrier for all)
+        // tiles of the item at `slot`, as they become free: V, then Q and K, then dO
         auto load = [&](int slot, int what) {
             const int pi = slot / w.nch, u = (slot - pi * w.nch) * kC;
             const long pair = w.pair0 + pi;
             const int b = (int)(pair / w.HV), hv = (int)(pair % w.HV);
             if (lane == 0 && slot < slots) {
-                if (what == 0) mbar_expect_tx(&ctl->full, 2 * Cf::QB + 2 * Cf::VB);
+                if (what == 0) mbar_expect_tx(&ctl->full_vo, 2 * Cf::VB);
+                if (what == 1) mbar_expect_tx(&ctl->full_qk, 2 * Cf::QB);
 #pragma unroll
                 for (int i = 0; i < DV / 64; ++i) {
-                    if (what == 0) tma_load_4d(smem + Cf::V + i * kC * 128, &mv, &ctl->full, 64 * i, hv, u, b);
-                    if (what == 2) tma_load_4d(smem + Cf::O + i * kC * 128, &mo, &ctl->full, 64 * i, hv, u, b);
+                    if (what == 0) tma_load_4d(smem + Cf::V + i * kC * 128, &mv, &ctl->full_vo, 64 * i, hv, u, b);
+                    if (what == 2) tma_load_4d(smem + Cf::O + i * kC * 128, &mo, &ctl->full_vo, 64 * i, hv, u, b);
                 }
 #pragma unroll
                 for (int i = 0; i < DK / 64; ++i)
                     if (what == 1) {
-                        tma_load_4d(smem + Cf::Q + i * kC * 128, &mq, &ctl->full, 64 * i, hv / w.m, u, b);
-                        tma_load_4d(smem + Cf::K + i * kC * 128, &mk, &ctl->full, 64 * i, hv / w.m, u, b);
+                        tma_load_4d(smem + Cf::Q + i * kC * 128, &mq, &ctl->full_qk, 64 * i, hv / w.m, u, b);
+                        tma_load_4d(smem + Cf::K + i * kC * 128, &mk, &ctl->full_qk, 64 * i, hv / w.m, u, b);
                     }
             }
             __syncwarp();
@@ -447,11 +460,12 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         };
         for (int i = 0; i < 3; ++i) load(blockIdx.x, i);
         for (int slot = blockIdx.x; slot < slots; slot += gridDim.x, ++n) {
-            if (!wt.warp(&ctl->full, n & 1, 51)) break;
+            if (!wt.warp(&ctl->full_qk, n & 1, 51)) break;
             tc_fence_after();
             gram(R0, k, q, DK);
-            gram(R1, v, o, DV);
             gram(R2, q, k, DK);
+            if (!wt.warp(&ctl->full_vo, n & 1, 50)) break;   // dO comes last
+            gram(R1, v, o, DV);
             gram(R3, o, v, DV);
             mma_commit_on(on, &ctl->m);
             if (!next()) break;
@@ -479,7 +493,8 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         const int quad = warp & 3, part = warp >> 2, row = 32 * quad + lane;
         const uint32_t tl = tm + ((uint32_t)(32 * quad) << 16);
         float *ga = reinterpret_cast<float *>(smem + Cf::ARR);
-        float *ar = ga + kC + part * kC, *ac = ar + 4 * kC, *aq = ac + 4 * kC, *ak = aq + 4 * kC;   // this quarter's
+        float *ae = ga + kC, *aw = ae + kC;
+        float *ar = aw + kC + part * kC, *ac = ar + 4 * kC, *aq = ac + 4 * kC, *ak = aq + 4 * kC;   // this quarter's
         int ph = 0, sp = 0;                      // phases of `m` and `sync` seen
         auto done = [&](int where) {
             const bool ok = wt.warp(&ctl->m, ph & 1, where);
@@ -499,12 +514,12 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             mbar_arrive(&ctl->go);
         };
         // a memory's pieces of this thread, as two bf16 parts (16 bits) into the operand tiles
-        auto put_x = [&](const float4 (&x)[2 * NX]) {
+        auto put_x = [&](const float4 (&x)[2 * NX], float f0) {
 #pragma unroll
             for (int p = 0; p < NX; ++p) {
                 const int e = tid + 512 * p, r = e / (DV / 8), c = e % (DV / 8);
-                const float f[8] = {x[2 * p].x, x[2 * p].y, x[2 * p].z, x[2 * p].w,
-                                    x[2 * p + 1].x, x[2 * p + 1].y, x[2 * p + 1].z, x[2 * p + 1].w};
+                const float f[8] = {f0 * x[2 * p].x, f0 * x[2 * p].y, f0 * x[2 * p].z, f0 * x[2 * p].w,
+                                    f0 * x[2 * p + 1].x, f0 * x[2 * p + 1].y, f0 * x[2 * p + 1].z, f0 * x[2 * p + 1].w};
                 uint4 h, l;
                 uint32_t *ph_ = &h.x, *pl = &l.x;
 #pragma unroll
@@ -517,20 +532,23 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                 *reinterpret_cast<uint4 *>(smem + Cf::XL + piece(DK, r, c)) = l;
             }
         };
-        int it = 0;
-        for (int slot = blockIdx.x; slot < slots; slot += gridDim.x, ++it) {
-            const int pi = slot / w.nch, u = (slot - pi * w.nch) * kC;
-            const long pair = w.pair0 + pi;
-            const int b = (int)(pair / w.HV), hv = (int)(pair % w.HV);
-            const int live = w.T - u;            // tokens of the chunk (more: all 128)
-            // ---- S, the decays
-            float4 xs[2 * NX];
+        float4 xs[2 * NX];
+        auto get_s = [&](int slot) {
             const float4 *ps = reinterpret_cast<const float4 *>(w.S + (size_t)slot * DK * DV);
 #pragma unroll
             for (int p = 0; p < NX; ++p) {
                 xs[2 * p] = ps[2 * (tid + 512 * p)];
                 xs[2 * p + 1] = ps[2 * (tid + 512 * p) + 1];
             }
+        };
+        if ((int)blockIdx.x < slots) get_s(blockIdx.x);
+        int it = 0;
+        for (int slot = blockIdx.x; slot < slots; slot += gridDim.x, ++it) {
+            const int pi = slot / w.nch, u = (slot - pi * w.nch) * kC;
+            const long pair = w.pair0 + pi;
+            const int b = (int)(pair / w.HV), hv = (int)(pair % w.HV);
+            const int live = w.T - u;            // tokens of the chunk (more: all 128)
+            // ---- S (loaded an item ahead), the decays
             if (warp == 0) {
                 const float *gp = w.g.p ? w.g.p + b * w.g.b + hv : nullptr;
                 float4 x = load_decay(w.g, gp, u + 4 * lane, w.T);
@@ -543,38 +561,63 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                 }
                 float before = __shfl_up_sync(0xffffffffu, up, 1);
                 if (lane == 0) before = 0.f;
-                *reinterpret_cast<float4 *>(ga + 4 * lane) = make_float4(x.x + before, x.y + before, x.z + before, x.w + before);
+                x = make_float4(x.x + before, x.y + before, x.z + before, x.w + before);
+                const float end = __shfl_sync(0xffffffffu, x.w, 31);
+                const bool mild = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))) <= kMildSpan;
+                const int strong = !__all_sync(0xffffffffu, mild);
+                if (lane == 0) ctl->strong = strong;
+                *reinterpret_cast<float4 *>(ga + 4 * lane) = x;
+                *reinterpret_cast<float4 *>(ae + 4 * lane) = make_float4(w.scale * ex2(x.x - end), w.scale * ex2(x.y - end),
+                                                                         w.scale * ex2(x.z - end), w.scale * ex2(x.w - end));
+                *reinterpret_cast<float4 *>(aw + 4 * lane) = make_float4(ex2(end - x.x), ex2(end - x.y), ex2(end - x.z), ex2(end - x.w));
             }
-            put_x(xs);
             if (!meet()) break;
             const float gr = ga[row], gc = ga[kC - 1];
-            if (!wt.warp(&ctl->full, it & 1, 58) || !done(53)) break;
+            const bool strong = ctl->strong;
+            // row factors of dQ and of dK, dV at the end; of the first terms in place
+            const float fq = strong ? 1.f : ae[row], fk = strong ? 1.f : aw[row];
+            const float iq = w.scale * ex2(gr), ik = ex2(gc - gr);
+            put_x(xs, strong ? 1.f : ex2(gc));
+            if (!wt.warp(&ctl->full_qk, it & 1, 58) || !done(53)) break;   // Q and K are read here too
             // ---- P^T, M^T of this row j and its quarter of the i; M of this row i and its quarter of the j; sums of W
             float cs = 0.f, rs = 0.f;
 #pragma unroll 1
             for (int i0 = 32 * part; i0 < 32 * part + 32; i0 += 16) {
                 const uint32_t to = 32 * part + (i0 & 16) / 2;
-                uint32_t x[16], y[16], p[8], q[8];
+                uint32_t p[8], q[8];
                 if (part < quad) {               // all before the row's tokens
 #pragma unroll
                     for (int j = 0; j < 8; ++j) p[j] = q[j] = 0u;
                 } else {
+                    uint32_t x[16], y[16];
                     tmem_ld16(tl + R0 + i0, x);
                     tmem_ld16(tl + R1 + i0, y);
+                    float e[16];
+                    if (!strong) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4)
+                            *reinterpret_cast<float4 *>(e + j) = *reinterpret_cast<const float4 *>(ae + i0 + j);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) e[j] = w.scale * ex2(ga[i0 + j] - gr);
+                    }
+                    if (part == quad) {          // nothing from before the row's own token, W not from it either
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (i0 + j < row) e[j] = 0.f;
+                    }
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        float a[2], c[2];
+                    for (int j = 0; j < 16; ++j) {
+                        const float sx = __uint_as_float(x[j]), c = __uint_as_float(y[j]) * e[j];
+                        cs = fmaf(sx, part == quad && i0 + j == row ? 0.f : c, cs);
+                        x[j] = __float_as_uint(sx * e[j]);
+                        y[j] = __float_as_uint(c);
+                    }
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int i = i0 + j + e;
-                            const float d = w.scale * ex2(ga[i] - gr), sx = __uint_as_float(x[j + e]);
-                            a[e] = i >= row ? sx * d : 0.f;
-                            c[e] = i >= row ? __uint_as_float(y[j + e]) * d : 0.f;
-                            cs += i > row ? sx * c[e] : 0.f;
-                        }
-                        p[j / 2] = pack_bf16(a[0], a[1]);
-                        q[j / 2] = pack_bf16(c[0], c[1]);
+                    for (int j = 0; j < 8; ++j) {
+                        p[j] = pack_bf16(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
+                        q[j] = pack_bf16(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1]));
                     }
                 }
                 tmem_st8(tl + R0 + to, p);
@@ -583,30 +626,42 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
 #pragma unroll 1
             for (int j0 = 32 * part; j0 < 32 * part + 32; j0 += 16) {
                 const uint32_t to = 32 * part + (j0 & 16) / 2;
-                uint32_t x[16], y[16], p[8];
+                uint32_t p[8];
                 if (part > quad) {               // all after the row's tokens
 #pragma unroll
                     for (int j = 0; j < 8; ++j) p[j] = 0u;
                 } else {
+                    uint32_t x[16], y[16];
                     tmem_ld16(tl + R2 + j0, x);
                     tmem_ld16(tl + R3 + j0, y);
+                    float e[16];
+                    if (!strong) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4)
+                            *reinterpret_cast<float4 *>(e + j) = *reinterpret_cast<const float4 *>(aw + j0 + j);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) e[j] = w.scale * ex2(gr - ga[j0 + j]);
+                    }
+                    if (part == quad) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (j0 + j > row) e[j] = 0.f;
+                    }
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        float c[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int jj = j0 + j + e;
-                            c[e] = jj <= row ? __uint_as_float(y[j + e]) * (w.scale * ex2(gr - ga[jj])) : 0.f;
-                            rs += jj < row ? __uint_as_float(x[j + e]) * c[e] : 0.f;
-                        }
-                        p[j / 2] = pack_bf16(c[0], c[1]);
+                    for (int j = 0; j < 16; ++j) {
+                        const float c = __uint_as_float(y[j]) * e[j];
+                        rs = fmaf(__uint_as_float(x[j]), part == quad && j0 + j == row ? 0.f : c, rs);
+                        y[j] = __float_as_uint(c);
                     }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) p[j] = pack_bf16(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1]));
                 }
                 tmem_st8(tl + R3 + to, p);
             }
-            ar[row] = rs;
-            ac[row] = cs;
+            ar[row] = fq * rs;
+            ac[row] = fk * cs;
             tmem_st_wait();
             go();
             // ---- R; first term of dQ
@@ -625,83 +680,83 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             for (int off = 16; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
             if (lane == 0) ctl->dot[warp] = dot;
             if (!done(54)) break;
-            put_x(xr);
-            const float eg = w.scale * ex2(gr), ew = ex2(gc - gr);
+            put_x(xr, 1.f);
+            if (slot + (int)gridDim.x < slots) get_s(slot + gridDim.x);
             const bool onk = 32 * part < DK, onv = 32 * part < DV;   // this warp's 32 columns exist
-            aq[row] = onk ? scale_row(tl + R2 + 32 * part, eg, smem + Cf::Q, row, 32 * part) : 0.f;
+            if (strong && onk) scale_row(tl + R2 + 32 * part, iq);
+            aq[row] = onk ? fq * dot_row(tl + R2 + 32 * part, smem + Cf::Q, row, 32 * part) : 0.f;
             go();
             // ---- dQ out; first term of dK
             const int u0 = u + (row & ~3), rows = min(4, w.T - u0), l8 = 8 * (lane & 3);
             const long long tok = (long long)b * w.T + u + row;
             if (!done(55)) break;
             // dK's first term first: products 4 wait for it, nobody for dQ's stores
-            ak[row] = onk ? scale_row(tl + R3 + 32 * part, ew, smem + Cf::K, row, 32 * part) : 0.f;
+            if (strong && onk) scale_row(tl + R3 + 32 * part, ik);
+            ak[row] = onk ? fk * dot_row(tl + R3 + 32 * part, smem + Cf::K, row, 32 * part) : 0.f;
             go();
             if (onk) {
                 if (w.fq)
-                    store_row_f32(tl + R2 + 32 * part, w.fq + (tok * w.HV + hv) * DK + 32 * part, row < live);
+                    store_row_f32(tl + R2 + 32 * part, fq, w.fq + (tok * w.HV + hv) * DK + 32 * part, row < live);
                 else
-                    store_rows(tl + R2 + 32 * part,
+                    store_rows(tl + R2 + 32 * part, fq,
                                w.dq + b * w.qs[0] + (long long)u0 * w.qs[1] + hv * w.qs[2] + 32 * part + l8, w.qs[1], rows, lane);
             }
             // ---- dK out; first term of dV
             if (!done(56)) break;
-            if (onv) scale_row(tl + R1 + 32 * part, ew, nullptr, 0, 0);
+            if (strong && onv) scale_row(tl + R1 + 32 * part, ik);
             go();
             if (onk) {
                 if (w.fk)
-                    store_row_f32(tl + R3 + 32 * part, w.fk + (tok * w.HV + hv) * DK + 32 * part, row < live);
+                    store_row_f32(tl + R3 + 32 * part, fk, w.fk + (tok * w.HV + hv) * DK + 32 * part, row < live);
                 else
-                    store_rows(tl + R3 + 32 * part,
+                    store_rows(tl + R3 + 32 * part, fk,
                                w.dk + b * w.ks[0] + (long long)u0 * w.ks[1] + hv * w.ks[2] + 32 * part + l8, w.ks[1], rows, lane);
             }
-            // ---- ddecay (the dots and sums of both halves are in); dV out
-            if (w.dg) {
-                if (!meet()) break;
-                if (warp == 0) {
-                    const float *a0 = ga + kC;
-                    float f[4], kd[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int t = 4 * lane + i;
-                        auto sum4 = [&](int which) {
-                            const float *a = a0 + 4 * which * kC + t;
-                            return (a[0] + a[kC]) + (a[2 * kC] + a[3 * kC]);
-                        };
-                        f[i] = sum4(0) - sum4(1) + sum4(2);
-                        kd[i] = sum4(3);
-                    }
-                    float fs = (f[0] + f[1]) + (f[2] + f[3]), kk = (kd[0] + kd[1]) + (kd[2] + kd[3]);
-                    float down = fs, up = kk;    // over this and the later lanes; this and the earlier
-#pragma unroll
-                    for (int off = 1; off < 32; off <<= 1) {
-                        const float x = __shfl_down_sync(0xffffffffu, down, off), y = __shfl_up_sync(0xffffffffu, up, off);
-                        if (lane + off < 32) down += x;
-                        if (lane >= off) up += y;
-                    }
-                    float all = 0.f;
-                    for (int i = 0; i < 16; ++i) all += ctl->dot[i];
-                    float behind = __shfl_down_sync(0xffffffffu, down, 1), before = __shfl_up_sync(0xffffffffu, up, 1);
-                    if (lane == 31) behind = 0.f;
-                    if (lane == 0) before = 0.f;
-                    all *= ex2(gc);
-                    float suf[4];
-                    suf[3] = behind + f[3]; suf[2] = suf[3] + f[2]; suf[1] = suf[2] + f[1]; suf[0] = suf[1] + f[0];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int t = u + 4 * lane + i;
-                        if (t < w.T) w.dg[((long long)b * w.T + t) * w.HV + hv] = all + suf[i] + before;
-                        before += kd[i];
-                    }
-                }
-            }
+            // ---- dV out
             if (!done(57)) break;
             if (onv)
-                store_rows(tl + R1 + 32 * part,
+                store_rows(tl + R1 + 32 * part, fk,
                            w.dv + b * w.vs[0] + (long long)u0 * w.vs[1] + hv * w.vs[2] + 32 * part + l8, w.vs[1], rows, lane);
             tc_fence_before();
             go();
-            if (!meet()) break;                  // the shared sums are free for the next chunk
+            // ---- ddecay, while the next chunk's first products run (every warp's sums and dots came before `done`;
+            // they are written again after the next meeting, which this warp joins when it is through)
+            if (w.dg && warp == 0) {
+                const float *a0 = aw + kC;
+                float f[4], kd[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = 4 * lane + i;
+                    auto sum4 = [&](int which) {
+                        const float *a = a0 + 4 * which * kC + t;
+                        return (a[0] + a[kC]) + (a[2 * kC] + a[3 * kC]);
+                    };
+                    f[i] = sum4(0) - sum4(1) + sum4(2);
+                    kd[i] = sum4(3);
+                }
+                float fs = (f[0] + f[1]) + (f[2] + f[3]), kk = (kd[0] + kd[1]) + (kd[2] + kd[3]);
+                float down = fs, up = kk;    // over this and the later lanes; this and the earlier
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const float x = __shfl_down_sync(0xffffffffu, down, off), y = __shfl_up_sync(0xffffffffu, up, off);
+                    if (lane + off < 32) down += x;
+                    if (lane >= off) up += y;
+                }
+                float all = 0.f;
+                for (int i = 0; i < 16; ++i) all += ctl->dot[i];
+                float behind = __shfl_down_sync(0xffffffffu, down, 1), before = __shfl_up_sync(0xffffffffu, up, 1);
+                if (lane == 31) behind = 0.f;
+                if (lane == 0) before = 0.f;
+                all *= ex2(gc);
+                float suf[4];
+                suf[3] = behind + f[3]; suf[2] = suf[3] + f[2]; suf[1] = suf[2] + f[1]; suf[0] = suf[1] + f[0];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = u + 4 * lane + i;
+                    if (t < w.T) w.dg[((long long)b * w.T + t) * w.HV + hv] = all + suf[i] + before;
+                    before += kd[i];
+                }
+            }
         }
     }
     tc_fence_before();
