@@ -108,10 +108,12 @@ struct WalkCfg {
     static constexpr int ARR = SB + DK * DV * 2;                // per chunk parity: G [128], w [128]
     static constexpr int CTL = ARR + 2 * 2 * kC * 4;
     static constexpr int SMEM = CTL + 256;
-    // TMEM columns: the memory [dv][dk], scores / P, O, hi and mid of the decayed values; lo lies in the
-    // upper half of the scores, which P leaves free
-    static constexpr int T_S = 0, T_P = DK, T_O = DK + 128, T_V = DK + 128 + DV, T_LO = T_P + 64;
-    static_assert(T_V + 128 <= 512, "TMEM");
+    // TMEM columns: the memory [dv][dk], scores / P, O, the three parts of the decayed values.  At d = 128 there is
+    // room for two of them, and lo lies in the upper half of the scores, which P leaves free: it waits for P
+    // (where it need not, dk + dv <= 192, that wait was half of the chunk's chain)
+    static constexpr bool OWN_LO = DK + DV <= 192;
+    static constexpr int T_S = 0, T_P = DK, T_O = DK + 128, T_V = DK + 128 + DV, T_LO = OWN_LO ? T_V + 128 : T_P + 64;
+    static_assert(T_V + (OWN_LO ? 192 : 128) <= 512, "TMEM");
     static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -259,7 +261,6 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         constexpr uint32_t id2 = idesc_bf16_f32(128, DV, false, false);
         constexpr uint32_t id3 = idesc_bf16_f32(128, DV, false, true);
         constexpr uint32_t id4 = idesc_bf16_f32(128, DK, false, true);   // dv = 64: rows 64.. are nobody's
-        const uint32_t on = lane == 0;
         const uint64_t ds = desc_kmajor_sw128(smem_u32(smem + Cf::SB), DV, 0);
         // product 1 of chunk c: its scores lie where P(c - 1) did
         auto scores = [&](int c) {
@@ -267,10 +268,11 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             tc_fence_after();
             const uint32_t q = smem_u32(stage(c));
             const uint64_t dq = desc_kmajor_sw128(q, kC, 0), dk = desc_kmajor_sw128(q + Cf::QB, kC, 0);
-#pragma unroll
-            for (int ks = 0; ks < DK / 16; ++ks)
-                mma_bf16_ss_on(on, tm + Cf::T_P, dq + kmajor_step(ks, kC), dk + kmajor_step(ks, kC), id1, ks > 0);
-            mma_commit_on(on, &ctl->s_full);
+            if (lane == 0) {
+                product_ss<DK / 16, kC, kC, false>(tm + Cf::T_P, dq, dk, id1);
+                mma_commit(&ctl->s_full);
+            }
+            __syncwarp();
             return true;
         };
         // Products 3 and 1 of the next chunk come after 4: they fill the pipe while the memory
@@ -284,34 +286,39 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
                            dv = desc_mnmajor_sw128(q + 2 * Cf::QB, kC, 0);
             if (!wt.warp(&ctl->s_ready, ph, 4) || !wt.warp(&ctl->o_free, ph, 5)) break;
             tc_fence_after();
-#pragma unroll
-            for (int ks = 0; ks < DK / 16; ++ks)
-                mma_bf16_ss_on(on, tm + Cf::T_O, dq + kmajor_step(ks, kC), ds + kmajor_step(ks, DV), id2, ks > 0);
-            mma_commit_on(on, &ctl->q_free);
+            if (lane == 0) {
+                product_ss<DK / 16, kC, DV, false>(tm + Cf::T_O, dq, ds, id2);
+                mma_commit(&ctl->q_free);
+            }
+            __syncwarp();
             if (!wt.warp(&ctl->v_ready, ph, 6)) break;
             tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int ks = 0; ks < kC / 16; ++ks)
-                    mma_bf16_ts_on(on, tm + Cf::T_S, tm + Cf::T_V + 64 * i + 8 * ks, dk + mn_step(ks), id4, 1u);
-            if (!wt.warp(&ctl->lo_ready, ph, 7)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int ks = 0; ks < kC / 16; ++ks)
-                mma_bf16_ts_on(on, tm + Cf::T_S, tm + Cf::T_LO + 8 * ks, dk + mn_step(ks), id4, 1u);
-            mma_commit_on(on, &ctl->kv_done);
+            if (lane == 0) {
+                product_ts<true>(tm + Cf::T_S, tm + Cf::T_V, dk, id4);
+                product_ts<true>(tm + Cf::T_S, tm + Cf::T_V + 64, dk, id4);
+            }
+            __syncwarp();
+            if (!Cf::OWN_LO) {
+                if (!wt.warp(&ctl->lo_ready, ph, 7)) break;
+                tc_fence_after();
+            }
+            if (lane == 0) {
+                product_ts<true>(tm + Cf::T_S, tm + Cf::T_LO, dk, id4);
+                mma_commit(&ctl->kv_done);
+            }
+            __syncwarp();
             if (!wt.warp(&ctl->p_ready, ph, 8)) break;
             if (ctl->strong[ph]) {
                 if (!wt.warp(&ctl->r_ready, ph_r, 9)) break;
                 ph_r ^= 1;
             }
             tc_fence_after();
-#pragma unroll
-            for (int ks = 0; ks < kC / 16; ++ks)
-                mma_bf16_ts_on(on, tm + Cf::T_O, tm + Cf::T_P + 8 * ks, dv + mn_step(ks), id3, 1u);
-            mma_commit_on(on, &ctl->o_full);
-            mma_commit_on(on, &ctl->done[ph]);
+            if (lane == 0) {
+                product_ts<true>(tm + Cf::T_O, tm + Cf::T_P, dv, id3);
+                mma_commit(&ctl->o_full);
+                mma_commit(&ctl->done[ph]);
+            }
+            __syncwarp();
             if (c + 1 < nch) ok = scores(c + 1);
         }
     } else if (warp < 4) {
@@ -507,9 +514,10 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
                 if (!wt.warp(&ctl->cleared, 0, 24)) break;
             }
             tc_fence_after();
-            if (mine) put_values<1>(v, wa, ch, 64 * half, tlane + Cf::T_V, tlane + Cf::T_V + 64, 0);
+            if (mine) put_values<Cf::OWN_LO ? 3 : 1>(v, wa, ch, 64 * half, tlane + Cf::T_V, tlane + Cf::T_V + 64, tlane + Cf::T_LO);
             tc_fence_before();
             mbar_arrive(&ctl->v_ready);
+            if constexpr (Cf::OWN_LO) continue;
             if (!wt.warp(&ctl->p_ready, c & 1, 23)) break;                  // the scores have been read
             tc_fence_after();
             if (mine) put_values<2>(v, wa, ch, 64 * half, 0, 0, tlane + Cf::T_LO);
@@ -522,7 +530,8 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     if (warp == 21) {
         // nothing of this CTA's is in flight once its last product and loads have landed (a bounded
         // wait: after a time-out they may not have)
-        mma_commit_on(lane == 0, &ctl->last);
+        if (lane == 0) mma_commit(&ctl->last);
+        __syncwarp();
         (void)mbar_wait(&ctl->last, 0, kWaitNs);
         if (ctl->fail) {
             const uint64_t t = globaltimer_ns();
@@ -663,7 +672,6 @@ linear_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
         }
     } else if (warp == 9) {
         constexpr uint32_t id = idesc_bf16_f32(128, DK, false, true);
-        const uint32_t on = lane == 0;
         for (int n = 0;; ++n) {
             const int s = n % NST;
             if (!wt.warp(&ctl->full[s], (n / NST) & 1, 33)) break;
@@ -672,15 +680,20 @@ linear_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
             tc_fence_after();
             const uint64_t dk = desc_mnmajor_sw128(smem_u32(smem + s * Cf::STAGE), kC, 0);
             const uint32_t a = tm + Cf::T_V + (n & 1) * 192;
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-#pragma unroll
-                for (int ks = 0; ks < kC / 16; ++ks)
-                    mma_bf16_ts_on(on, tm, a + 64 * i + 8 * ks, dk + mn_step(ks), id, (uint32_t)n | (uint32_t)(i + ks));
-            mma_commit_on(on, &ctl->used[n & 1]);
-            mma_commit_on(on, &ctl->empty[s]);
+            if (lane == 0) {
+                if (n)
+                    product_ts<true>(tm, a, dk, id);
+                else
+                    product_ts<false>(tm, a, dk, id);
+                product_ts<true>(tm, a + 64, dk, id);
+                product_ts<true>(tm, a + 128, dk, id);
+                mma_commit(&ctl->used[n & 1]);
+                mma_commit(&ctl->empty[s]);
+            }
+            __syncwarp();
         }
-        mma_commit_on(on, &ctl->last);
+        if (lane == 0) mma_commit(&ctl->last);
+        __syncwarp();
     } else {
         // total decay of the segment, in a fixed order; its largest decay
         float sum = 0.f, top = -INFINITY;

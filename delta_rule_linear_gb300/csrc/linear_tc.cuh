@@ -100,11 +100,32 @@ __device__ __forceinline__ void put_values(const uint8_t *v, const float *wa, in
     tmem_st_wait();
 }
 
-// One product: sums over K in steps of 16, issued by the lane with `on`.  A step moves a descriptor's start
-// address, in 16-byte units: a K-major tile of `rows` rows by 32 bytes inside a block of 64 channels; an
-// MN-major one by 16 rows of 128 bytes.
-constexpr uint64_t kmajor_step(int ks, int rows) { return (uint64_t)((ks >> 2) * rows * 8 + (ks & 3) * 2); }
-constexpr uint64_t mn_step(int ks) { return (uint64_t)ks * 128; }
+// One product: a sum over K in steps of 16, issued by one lane.  A step moves a descriptor's start address, in
+// 16-byte units: a K-major tile of ROWS rows by 32 bytes inside a block of 64 channels, an MN-major one (ROWS = 0)
+// by 16 rows of 128 bytes.
+constexpr uint64_t op_step(int ks, int rows) {
+    return rows ? (uint64_t)((ks >> 2) * rows * 8 + (ks & 3) * 2) : (uint64_t)ks * 128;
+}
+template <int STEPS, int RA, int RB, bool ADD>
+__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id) {
+    if constexpr (ADD)
+        mma_ss<1>(d, a, b, id);
+    else
+        mma_ss<0>(d, a, b, id);
+#pragma unroll
+    for (int ks = 1; ks < STEPS; ++ks) mma_ss<1>(d, a + op_step(ks, RA), b + op_step(ks, RB), id);
+}
+// A in TMEM, 8 columns a step (QUARTERS: of every 32 columns the first 16), B MN-major, 128 tokens
+template <bool ADD, bool QUARTERS = false>
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id) {
+    if constexpr (ADD)
+        mma_ts<1>(d, a, b, id);
+    else
+        mma_ts<0>(d, a, b, id);
+#pragma unroll
+    for (int ks = 1; ks < kC / 16; ++ks)
+        mma_ts<1>(d, a + (QUARTERS ? 32 * (ks >> 1) + 8 * (ks & 1) : 8 * ks), b + op_step(ks, 0), id);
+}
 
 // Lane t of a group of four starts with four pieces of its own row and ends with piece t of the
 // four rows.

@@ -162,7 +162,6 @@ linear_part_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         }
     } else if (warp == 13) {
         constexpr uint32_t id = idesc_bf16_f32(128, DK, false, true);
-        const uint32_t on = lane == 0;
         for (int n = 0; n < mine; ++n) {
             const int s = n % NST;
             if (!wt.warp(&ctl->full[s], (n / NST) & 1, 42) || !wt.warp(&ctl->ready[n & 1], (n >> 1) & 1, 43)) break;
@@ -170,14 +169,15 @@ linear_part_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             tc_fence_after();
             const uint64_t dk = desc_mnmajor_sw128(smem_u32(smem + s * Cf::STAGE), kC, 0);
             const uint32_t a = tm + Cf::T_V + (n & 1) * 192;
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-#pragma unroll
-                for (int ks = 0; ks < kC / 16; ++ks)
-                    mma_bf16_ts_on(on, tm, a + 64 * i + 8 * ks, dk + mn_step(ks), id, (uint32_t)(i + ks));
-            mma_commit_on(on, &ctl->used[n & 1]);
-            mma_commit_on(on, &ctl->empty[s]);
-            mma_commit_on(on, &ctl->d_full);
+            if (lane == 0) {
+                product_ts<false>(tm, a, dk, id);
+                product_ts<true>(tm, a + 64, dk, id);
+                product_ts<true>(tm, a + 128, dk, id);
+                mma_commit(&ctl->used[n & 1]);
+                mma_commit(&ctl->empty[s]);
+                mma_commit(&ctl->d_full);
+            }
+            __syncwarp();
         }
     } else if (warp < 8) {
         const int ch = tid & 127, half = tid >> 7;
@@ -217,7 +217,8 @@ linear_part_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     tc_fence_before();
     __syncthreads();
     if (warp == 13) {
-        mma_commit_on(lane == 0, &ctl->last);
+        if (lane == 0) mma_commit(&ctl->last);
+        __syncwarp();
         (void)mbar_wait(&ctl->last, 0, kWaitNs);
         if (ctl->fail) {                        // let what is in flight land
             const uint64_t t = globaltimer_ns();
@@ -399,12 +400,11 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         constexpr uint32_t idx = idesc_bf16_f32(128, DK, false, false);
         constexpr uint32_t idk = idesc_bf16_f32(128, DK, false, true);
         constexpr uint32_t idv = idesc_bf16_f32(128, DV, false, true);
-        const uint32_t on = lane == 0;
         const uint32_t sb = smem_u32(smem);
         const uint64_t q = desc_kmajor_sw128(sb + Cf::Q, kC, 0), k = desc_kmajor_sw128(sb + Cf::K, kC, 0),
                        v = desc_kmajor_sw128(sb + Cf::V, kC, 0), o = desc_kmajor_sw128(sb + Cf::O, kC, 0);
         const uint64_t qn = desc_mnmajor_sw128(sb + Cf::Q, kC, 0), kn = desc_mnmajor_sw128(sb + Cf::K, kC, 0),
-                       on_ = desc_mnmajor_sw128(sb + Cf::O, kC, 0);
+                       on = desc_mnmajor_sw128(sb + Cf::O, kC, 0);
         const uint64_t xh = desc_kmajor_sw128(sb + Cf::XH, DK, 0), xl = desc_kmajor_sw128(sb + Cf::XL, DK, 0),
                        xn = desc_mnmajor_sw128(sb + Cf::XH, DK, 0);
         // tiles of the item at `slot`, as they become free: V, then Q and K, then dO
@@ -429,28 +429,17 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             }
             __syncwarp();
         };
-        // token tile times token tile, both K-major
-        auto gram = [&](uint32_t d, uint64_t a, uint64_t bb, int D) {
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-                if (ks < D / 16) mma_bf16_ss_on(on, tm + d, a + kmajor_step(ks, kC), bb + kmajor_step(ks, kC), ida, ks > 0);
-        };
+        // token tile times token tile over D channels, both K-major
+        auto gram_k = [&](uint32_t d, uint64_t a, uint64_t bb) { product_ss<DK / 16, kC, kC, false>(tm + d, a, bb, ida); };
+        auto gram_v = [&](uint32_t d, uint64_t a, uint64_t bb) { product_ss<DV / 16, kC, kC, false>(tm + d, a, bb, ida); };
         // token tile [., dv] times X^T
-        auto into = [&](uint64_t a) {
-            return [&, a](uint32_t d) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int ks = 0; ks < DV / 16; ++ks)
-                        mma_bf16_ss_on(on, tm + d, a + kmajor_step(ks, kC), (i ? xl : xh) + kmajor_step(ks, DK), idx, i + ks > 0);
-            };
+        auto into = [&](uint64_t a, uint32_t d) {
+            product_ss<DV / 16, kC, DK, false>(tm + d, a, xh, idx);
+            product_ss<DV / 16, kC, DK, true>(tm + d, a, xl, idx);
         };
         // A in TMEM times a token tile
-        auto spread = [&](uint32_t d, uint32_t a, uint64_t bb, uint32_t id) {
-#pragma unroll
-            for (int ks = 0; ks < kC / 16; ++ks)
-                mma_bf16_ts_on(on, tm + d, tm + a + 32 * (ks >> 1) + 8 * (ks & 1), bb + mn_step(ks), id, 1u);
-        };
+        auto spread = [&](uint32_t d, uint32_t a, uint64_t bb, uint32_t id) { product_ts<true, true>(tm + d, tm + a, bb, id); };
+        auto done = [&]() { mma_commit(&ctl->m); };
         int n = 0, ph = 0;                       // items; phases of `go` seen
         auto next = [&]() {
             const bool ok = wt.warp(&ctl->go, ph & 1, 52);
@@ -462,30 +451,46 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         for (int slot = blockIdx.x; slot < slots; slot += gridDim.x, ++n) {
             if (!wt.warp(&ctl->full_qk, n & 1, 51)) break;
             tc_fence_after();
-            gram(R0, k, q, DK);
-            gram(R2, q, k, DK);
+            if (lane == 0) {
+                gram_k(R0, k, q);
+                gram_k(R2, q, k);
+            }
+            __syncwarp();
             if (!wt.warp(&ctl->full_vo, n & 1, 50)) break;   // dO comes last
-            gram(R1, v, o, DV);
-            gram(R3, o, v, DV);
-            mma_commit_on(on, &ctl->m);
+            if (lane == 0) {
+                gram_v(R1, v, o);
+                gram_v(R3, o, v);
+                done();
+            }
+            __syncwarp();
             if (!next()) break;
-            into(o)(R2);                         // dO S^T
-            mma_commit_on(on, &ctl->m);
+            if (lane == 0) {
+                into(o, R2);                     // dO S^T
+                done();
+            }
+            __syncwarp();
             if (!next()) break;
-            spread(R2, R3, kn, idk);             // + M K
-            into(v)(R3);                         // V R^T
-            mma_commit_on(on, &ctl->m);
+            if (lane == 0) {
+                spread(R2, R3, kn, idk);         // + M K
+                into(v, R3);                     // V R^T
+                done();
+            }
+            __syncwarp();
             if (!next()) break;
             load(slot + gridDim.x, 0);           // products with V are done
-            spread(R3, R1, qn, idk);             // + M^T Q
-#pragma unroll
-            for (int ks = 0; ks < DK / 16; ++ks)  // K R
-                mma_bf16_ss_on(on, tm + R1, k + kmajor_step(ks, kC), xn + mn_step(ks), idv, ks > 0);
-            mma_commit_on(on, &ctl->m);
+            if (lane == 0) {
+                spread(R3, R1, qn, idk);         // + M^T Q
+                product_ss<DK / 16, kC, 0, false>(tm + R1, k, xn, idv);   // K R
+                done();
+            }
+            __syncwarp();
             if (!next()) break;
             load(slot + gridDim.x, 1);           // and with Q and K
-            spread(R1, R0, on_, idv);            // + P^T dO
-            mma_commit_on(on, &ctl->m);
+            if (lane == 0) {
+                spread(R1, R0, on, idv);         // + P^T dO
+                done();
+            }
+            __syncwarp();
             if (!next()) break;
             load(slot + gridDim.x, 2);
         }
@@ -762,7 +767,8 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     tc_fence_before();
     __syncthreads();
     if (warp == 16) {
-        mma_commit_on(lane == 0, &ctl->last);
+        if (lane == 0) mma_commit(&ctl->last);
+        __syncwarp();
         (void)mbar_wait(&ctl->last, 0, kWaitNs);
         if (ctl->fail) {                         // let what is in flight land
             const uint64_t t = globaltimer_ns();
