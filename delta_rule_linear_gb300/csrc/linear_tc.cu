@@ -109,16 +109,15 @@ struct WalkCfg {
     static constexpr int CTL = ARR + 2 * 2 * kC * 4;
     static constexpr int SMEM = CTL + 256;
     // TMEM columns: the memory [dv][dk], scores / P, O, the three parts of the decayed values.  At d = 128 there is
-    // room for two of them, and lo lies in the upper half of the scores, which P leaves free: it waits for P
-    // (where it need not, dk + dv <= 192, that wait was half of the chunk's chain)
+    // room for two of them, and lo follows hi once that is used
     static constexpr bool OWN_LO = DK + DV <= 192;
-    static constexpr int T_S = 0, T_P = DK, T_O = DK + 128, T_V = DK + 128 + DV, T_LO = OWN_LO ? T_V + 128 : T_P + 64;
+    static constexpr int T_S = 0, T_P = DK, T_O = DK + 128, T_V = DK + 128 + DV, T_LO = OWN_LO ? T_V + 128 : T_V;
     static_assert(T_V + (OWN_LO ? 192 : 128) <= 512, "TMEM");
     static_assert(SMEM <= 232448, "shared memory");
 };
 
 struct WalkCtl {
-    uint64_t full[2], done[2], s_full, q_free, p_ready, r_ready, o_full, o_free, s_ready, v_ready, lo_ready, kv_done, cleared, start, last;
+    uint64_t full[2], done[2], s_full, q_free, p_ready, r_ready, o_full, o_free, s_ready, v_ready, lo_ready, hi_done, kv_done, cleared, start, last;
     uint32_t tmem;
     int fail;
     int strong[2];   // the chunk's decays exceed kMildSpan
@@ -154,7 +153,7 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             mbar_init(&ctl->full[i], 1);
             mbar_init(&ctl->done[i], 1);
         }
-        for (uint64_t *x : {&ctl->s_full, &ctl->q_free, &ctl->o_full, &ctl->kv_done, &ctl->last}) mbar_init(x, 1);
+        for (uint64_t *x : {&ctl->s_full, &ctl->q_free, &ctl->o_full, &ctl->hi_done, &ctl->kv_done, &ctl->last}) mbar_init(x, 1);
         for (uint64_t *x : {&ctl->p_ready, &ctl->r_ready, &ctl->o_free, &ctl->s_ready}) mbar_init(x, 128);
         for (uint64_t *x : {&ctl->v_ready, &ctl->lo_ready, &ctl->cleared}) mbar_init(x, 256);
         mbar_init(&ctl->start, 512);
@@ -275,8 +274,8 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             __syncwarp();
             return true;
         };
-        // Products 3 and 1 of the next chunk come after 4: they fill the pipe while the memory
-        // (waiting for 4) is turned into the next operand
+        // Product 1 of the next chunk comes after 4 (where it can, product 3 too): they fill the pipe while
+        // the memory (waiting for 4) is turned into the next operand
         bool ok = nch > 0 && scores(0);
         uint32_t ph_r = 0;
         for (int c = 0; ok && c < nch; ++c) {
@@ -291,14 +290,31 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
                 mma_commit(&ctl->q_free);
             }
             __syncwarp();
+            // product 3, once P is there
+            auto outputs = [&]() {
+                if (!wt.warp(&ctl->p_ready, ph, 8)) return false;
+                if (ctl->strong[ph]) {
+                    if (!wt.warp(&ctl->r_ready, ph_r, 9)) return false;
+                    ph_r ^= 1;
+                }
+                tc_fence_after();
+                if (lane == 0) {
+                    product_ts<true>(tm + Cf::T_O, tm + Cf::T_P, dv, id3);
+                    mma_commit(&ctl->o_full);
+                }
+                __syncwarp();
+                return true;
+            };
             if (!wt.warp(&ctl->v_ready, ph, 6)) break;
             tc_fence_after();
             if (lane == 0) {
                 product_ts<true>(tm + Cf::T_S, tm + Cf::T_V, dk, id4);
+                if (!Cf::OWN_LO) mma_commit(&ctl->hi_done);
                 product_ts<true>(tm + Cf::T_S, tm + Cf::T_V + 64, dk, id4);
             }
             __syncwarp();
-            if (!Cf::OWN_LO) {
+            if (!Cf::OWN_LO) {                   // while lo is written over hi
+                if (!outputs()) break;
                 if (!wt.warp(&ctl->lo_ready, ph, 7)) break;
                 tc_fence_after();
             }
@@ -307,17 +323,8 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
                 mma_commit(&ctl->kv_done);
             }
             __syncwarp();
-            if (!wt.warp(&ctl->p_ready, ph, 8)) break;
-            if (ctl->strong[ph]) {
-                if (!wt.warp(&ctl->r_ready, ph_r, 9)) break;
-                ph_r ^= 1;
-            }
-            tc_fence_after();
-            if (lane == 0) {
-                product_ts<true>(tm + Cf::T_O, tm + Cf::T_P, dv, id3);
-                mma_commit(&ctl->o_full);
-                mma_commit(&ctl->done[ph]);
-            }
+            if (Cf::OWN_LO && !outputs()) break;
+            if (lane == 0) mma_commit(&ctl->done[ph]);
             __syncwarp();
             if (c + 1 < nch) ok = scores(c + 1);
         }
@@ -518,7 +525,7 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             tc_fence_before();
             mbar_arrive(&ctl->v_ready);
             if constexpr (Cf::OWN_LO) continue;
-            if (!wt.warp(&ctl->p_ready, c & 1, 23)) break;                  // the scores have been read
+            if (!wt.warp(&ctl->hi_done, c & 1, 23)) break;
             tc_fence_after();
             if (mine) put_values<2>(v, wa, ch, 64 * half, 0, 0, tlane + Cf::T_LO);
             tc_fence_before();
