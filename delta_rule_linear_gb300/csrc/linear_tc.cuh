@@ -70,32 +70,39 @@ __device__ __forceinline__ float rest(float a) { return a - __uint_as_float(__fl
 __device__ __forceinline__ uint32_t piece(int rows, int r, int c) {
     return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
-// The decayed values of channel `ch`, tokens t0 .. t0 + 63, as A-operand words (two tokens each): 8 columns
-// a step into column t0 / 2 of each part.  PARTS: bit 0 hi and mid, bit 1 lo.
+// The decayed values of the warp's 32 channels (from `ch`, its TMEM lanes), tokens t0 .. t0 + 63, as A-operand
+// words (two tokens each) into column t0 / 2 of each part.  PARTS: bit 0 hi and mid, bit 1 lo.  The tile is
+// token-major: ldmatrix transposes it into the layout that a 16x128b store takes (lane l holds channel l / 4,
+// tokens 2 (l % 4) and the next of each 8), 16 channels by 32 tokens a step.
 template <int PARTS>
 __device__ __forceinline__ void put_values(const uint8_t *v, const float *wa, int ch, int t0, uint32_t hi, uint32_t mid,
                                            uint32_t lo) {
-    const uint8_t *col = v + (ch >> 6) * kC * 128 + (ch & 7) * 2;
-    const int c = (ch >> 3) & 7;
+    const int lane = threadIdx.x & 31, row = ((lane >> 4) << 3) | (lane & 7);
+    const uint32_t base = smem_u32(v) + (ch >> 6) * kC * 128 + row * 128;
+    const int c = ((ch >> 3) & 4) + ((lane >> 3) & 1);        // 16-byte piece of the row
+    wa += 2 * (lane & 3);
 #pragma unroll 1
-    for (int t = t0; t < t0 + 64; t += 16) {
-        uint32_t h[8], m[8], l[8];
+    for (int u = 0; u < 4; ++u) {
+        const int t = t0 + (u >> 1) * 32;
+        const uint32_t at = base + t * 128 + (((c + 2 * (u & 1)) ^ (lane & 7)) << 4);
+        uint32_t r[8], h[8], m[8], l[8];
+        ldsm4t(at, r);
+        ldsm4t(at + 16 * 128, r + 4);
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            const uint32_t b0 = *reinterpret_cast<const uint16_t *>(col + (t + j) * 128 + ((c ^ (j & 7)) << 4));
-            const uint32_t b1 = *reinterpret_cast<const uint16_t *>(col + (t + j + 1) * 128 + ((c ^ ((j + 1) & 7)) << 4));
-            const float2 w = *reinterpret_cast<const float2 *>(wa + t + j);
-            const float x = w.x * __uint_as_float(b0 << 16), y = w.y * __uint_as_float(b1 << 16);
-            h[j / 2] = top2(x, y);
+        for (int j = 0; j < 8; ++j) {
+            const float2 w = *reinterpret_cast<const float2 *>(wa + t + (j >> 1) * 8);
+            const float x = w.x * __uint_as_float(r[j] << 16), y = w.y * __uint_as_float(r[j] & 0xffff0000u);
+            h[j] = top2(x, y);
             const float rx = rest(x), ry = rest(y);
-            m[j / 2] = top2(rx, ry);
-            l[j / 2] = top2(rest(rx), rest(ry));
+            m[j] = top2(rx, ry);
+            l[j] = top2(rest(rx), rest(ry));
         }
+        const uint32_t to = ((uint32_t)(u & 1) << 20) + t / 2;  // 16 lanes on
         if constexpr (PARTS & 1) {
-            tmem_st8(hi + t / 2, h);
-            tmem_st8(mid + t / 2, m);
+            tmem_st_16x128(hi + to, h);
+            tmem_st_16x128(mid + to, m);
         }
-        if constexpr (PARTS & 2) tmem_st8(lo + t / 2, l);
+        if constexpr (PARTS & 2) tmem_st_16x128(lo + to, l);
     }
     tmem_st_wait();
 }
