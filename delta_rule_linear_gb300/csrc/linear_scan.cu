@@ -6,8 +6,8 @@
 //
 // The memory h [dk, dv] stays in fp32 registers: a warp holds 8 value columns of all dk rows
 // (lane l the rows l, l + 32, ...), so the update and the read-out cost 2 dk dv FMAs per token
-// and head plus one 9-shuffle sum over the lanes for 8 outputs.  Four warps share one staged
-// tile of 16 tokens.
+// and head; the sums over the lanes for the 32 outputs of four tokens are 31 shuffles.  Four warps share
+// one staged tile of 16 tokens.
 //
 // A walk is sequential over its tokens, so a long sequence with few heads is cut into
 // segments: a first launch leaves every segment's memory as if it started from zero, and the
@@ -35,8 +35,8 @@ namespace {
 constexpr int kStepThreads = 256;
 
 // One CTA per (request, value head): the [DK, DV] memory crosses HBM once in and once out, as
-// 16-byte accesses that are all in flight before the first is used.  Bound by that traffic: 5.8
-// to 6.4 TB/s is the part's measured copy rate, and the arithmetic (3 flops per 4 bytes) is free.
+// 16-byte accesses that are all in flight before the first is used.  Bound by that traffic: 256 requests of
+// 32 heads of 128 x 128 take 157 us, 6.9 TB/s, what a plain copy reaches; the arithmetic (3 flops per 4 bytes) is free.
 template <typename T, int DK, int DV>
 __global__ void __launch_bounds__(kStepThreads) linear_step_kernel(LinDecode a) {
     constexpr int TPR = DV / 4, RG = kStepThreads / TPR;   // threads per row, rows per pass
@@ -90,7 +90,7 @@ constexpr int kTile = 16;        // tokens staged at a time
 constexpr int kWalkThreads = 128;
 constexpr int kCols = 32;        // value columns of a CTA
 constexpr int kMaxSegs = 32;     // segments of a sequence (a start state adds up to 31 memories)
-constexpr int kMinSeg = 64;      // tokens of a segment at least: its launch and its start state cost about that
+constexpr int kMinSeg = 32;      // tokens of a segment at least: 300 tokens, 4 heads of 32 x 64, fp32: 10.3 us, 13.7 with 64
 
 struct Walk {
     LinView q, k, v, x;          // roles; x: the vector of the row dots (or p = nullptr)
@@ -130,21 +130,41 @@ template <typename T> __device__ __forceinline__ void put_vec(float *dst, const 
     }
 }
 
+// Sums over the warp of x[0 .. N - 1]: half of the values go to the other half of the lanes, and so on; lane l ends with
+// that of index l N / 32 in x[0].
+template <int N, int LANES>
+__device__ __forceinline__ void lane_sums(float *x, int lane) {
+    if constexpr (LANES > 1) {
+        constexpr int half = LANES / 2, keep = N > 1 ? N / 2 : 1;
+        if constexpr (N > 1) {
+            const bool up = lane & half;
+#pragma unroll
+            for (int i = 0; i < keep; ++i) {
+                const float mine = up ? x[i + keep] : x[i], send = up ? x[i] : x[i + keep];
+                x[i] = mine + __shfl_xor_sync(0xffffffffu, send, half);
+            }
+        } else {
+            x[0] += __shfl_xor_sync(0xffffffffu, x[0], half);
+        }
+        lane_sums<keep, half>(x, lane);
+    }
+}
+
 // OUT: the second launch (outputs, final memory); otherwise a segment's local memory.
-// Up to three walks of the same role dimensions in one launch (a gradient's are as short as its launches).
+// A gradient's three walks, in one launch (they are as short as their launches).
 struct Walks {
     Walk w[3];
 };
 
 template <typename T, int DK, bool OUT, bool RD>
-__global__ void __launch_bounds__(kWalkThreads) linear_walk_kernel(const __grid_constant__ Walks ws) {
-    const Walk &w = ws.w[blockIdx.z];
+__device__ __forceinline__ void walk_tokens(const Walk &w) {
     constexpr int R = DK / 32, VN = Vec<T>::N;
     constexpr int QV = kTile * DK / VN;                      // 16-byte pieces of a q or k tile
     constexpr int NQ = (QV + kWalkThreads - 1) / kWalkThreads;
     constexpr int VV = kTile * kCols / VN;
     static_assert(VV <= kWalkThreads, "one piece of v per thread");
-    __shared__ __align__(16) float s_q[kTile][DK], s_k[kTile][DK], s_v[kTile][kCols], s_o[kTile][kCols];
+    __shared__ __align__(16) float s_q[kTile][DK], s_k[kTile][DK], s_v[kTile][kCols],
+        s_o[kTile][kCols + 8];                               // rows apart in the banks
     __shared__ float s_a[kTile], s_qk[kTile];
 
     const int nsl = w.DV / kCols, sl = blockIdx.x % nsl, item = blockIdx.x / nsl, hv = blockIdx.y;
@@ -176,6 +196,7 @@ __global__ void __launch_bounds__(kWalkThreads) linear_walk_kernel(const __grid_
 #pragma unroll
                 for (int c = 0; c < 8; ++c) h[r][c] = p[(lane + 32 * r) * w.si + (c0 + c) * w.sj];
         }
+#pragma unroll 4
         for (int pp = 0; pp < it.p; ++pp) {                  // start state of this segment
             const size_t slot = (size_t)(it.first + pp) * w.HV + hv;
             const float ga = w.gam[slot];
@@ -236,68 +257,56 @@ __global__ void __launch_bounds__(kWalkThreads) linear_walk_kernel(const __grid_
         __syncthreads();
         if (u + kTile < u1) fetch(u + kTile);
         const int nt = min(kTile, u1 - u);
-#pragma unroll 2
-        for (int t = 0; t < nt; ++t) {
-            const float a = s_a[t];
-            float vv[8], kk[R], acc[8];
-            *reinterpret_cast<float4 *>(vv) = *reinterpret_cast<const float4 *>(&s_v[t][8 * warp]);
-            *reinterpret_cast<float4 *>(vv + 4) = *reinterpret_cast<const float4 *>(&s_v[t][8 * warp + 4]);
+        // four tokens at a time (rows past the segment are staged as zeros): their updates are a chain of one FMA
+        // each, and their 32 outputs are summed over the lanes together, a shuffle for each
+#pragma unroll 1
+        for (int t0 = 0; t0 < nt; t0 += 4) {
+            float acc[32], qk[4];
 #pragma unroll
-            for (int r = 0; r < R; ++r) kk[r] = w.add_scale * s_k[t][lane + 32 * r];
-            if constexpr (!OUT) {
+            for (int j = 0; j < 4; ++j) {
+                const int t = t0 + j;
+                const float a = s_a[t];
+                float vv[8], kk[R];
+                *reinterpret_cast<float4 *>(vv) = *reinterpret_cast<const float4 *>(&s_v[t][8 * warp]);
+                *reinterpret_cast<float4 *>(vv + 4) = *reinterpret_cast<const float4 *>(&s_v[t][8 * warp + 4]);
 #pragma unroll
-                for (int r = 0; r < R; ++r)
+                for (int r = 0; r < R; ++r) kk[r] = w.add_scale * s_k[t][lane + 32 * r];
+                if constexpr (!OUT) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) h[r][c] = fmaf(h[r][c], a, kk[r] * vv[c]);
-                continue;
-            }
-            float qq[R], qk = 0.f;
+                    for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int r = 0; r < R; ++r) qq[r] = s_q[t][lane + 32 * r];
+                        for (int c = 0; c < 8; ++c) h[r][c] = fmaf(h[r][c], a, kk[r] * vv[c]);
+                } else {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) acc[c] = 0.f;
+                    for (int c = 0; c < 8; ++c) acc[8 * j + c] = 0.f;
+                    qk[j] = 0.f;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                if constexpr (RD) qk = fmaf(qq[r], kk[r], qk);
+                    for (int r = 0; r < R; ++r) {
+                        const float qq = s_q[t][lane + 32 * r];
+                        if constexpr (RD) qk[j] = fmaf(qq, kk[r], qk[j]);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    if constexpr (RD) {
-                        h[r][c] *= a;
-                        acc[c] = fmaf(h[r][c], qq[r], acc[c]);
-                        h[r][c] = fmaf(kk[r], vv[c], h[r][c]);
-                    } else {
-                        h[r][c] = fmaf(h[r][c], a, kk[r] * vv[c]);
-                        acc[c] = fmaf(h[r][c], qq[r], acc[c]);
+                        for (int c = 0; c < 8; ++c) {
+                            if constexpr (RD) {
+                                h[r][c] *= a;
+                                acc[8 * j + c] = fmaf(h[r][c], qq, acc[8 * j + c]);
+                                h[r][c] = fmaf(kk[r], vv[c], h[r][c]);
+                            } else {
+                                h[r][c] = fmaf(h[r][c], a, kk[r] * vv[c]);
+                                acc[8 * j + c] = fmaf(h[r][c], qq, acc[8 * j + c]);
+                            }
+                        }
                     }
                 }
             }
-            // sum over the lanes; lane l ends with column 4 l4 + 2 l3 + l2 (its bits)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const bool up = lane & 16;
-                const float keep = up ? acc[c + 4] : acc[c], send = up ? acc[c] : acc[c + 4];
-                acc[c] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
-            }
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const bool up = lane & 8;
-                const float keep = up ? acc[c + 2] : acc[c], send = up ? acc[c] : acc[c + 2];
-                acc[c] = keep + __shfl_xor_sync(0xffffffffu, send, 8);
-            }
-            {
-                const bool up = lane & 4;
-                const float keep = up ? acc[1] : acc[0], send = up ? acc[0] : acc[1];
-                acc[0] = keep + __shfl_xor_sync(0xffffffffu, send, 4);
-            }
-            acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 2);
-            acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 1);
-            if ((lane & 3) == 0)
-                s_o[t][8 * warp + ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1)] =
-                    acc[0] * w.out_scale;
-            if constexpr (RD) {
-#pragma unroll
-                for (int off = 16; off; off >>= 1) qk += __shfl_xor_sync(0xffffffffu, qk, off);
-                if (warp == 0 && lane == 0) s_qk[t] = qk * w.out_scale;
+            if constexpr (OUT) {
+                lane_sums<32, 32>(acc, lane);                // lane l: token l / 8, column l % 8
+                s_o[t0 + (lane >> 3)][8 * warp + (lane & 7)] = acc[0] * w.out_scale;
+                if constexpr (RD) {
+                    if (((t0 >> 2) & 3) == warp) {           // all warps hold q and k: they take turns
+                        lane_sums<4, 32>(qk, lane);          // lanes 8 j and on: token j
+                        if ((lane & 7) == 0) s_qk[t0 + (lane >> 3)] = qk[0] * w.out_scale;
+                    }
+                }
             }
         }
         if constexpr (OUT) {
@@ -318,15 +327,22 @@ __global__ void __launch_bounds__(kWalkThreads) linear_walk_kernel(const __grid_
                     w.rd[(size_t)sl * w.rows * w.HV + ((size_t)(w.s.cu ? 0 : (long)it.n * w.s.T) + tok(u + t)) * w.HV +
                          hv] = d;
             }
-            for (int i = tid; i < nt * kCols; i += kWalkThreads) {
-                const int t = i / kCols, c = i % kCols;
-                float val = s_o[t][c];
-                if constexpr (RD) val = fmaf(s_qk[t], s_v[t][c], val);
+            static_assert(kTile * kCols == 4 * kWalkThreads, "four columns to a thread");
+            if (const int t = tid >> 3, c = (tid & 7) * 4; t < nt) {
+                float4 val = *reinterpret_cast<const float4 *>(&s_o[t][c]);
+                if constexpr (RD) {
+                    const float4 vv = *reinterpret_cast<const float4 *>(&s_v[t][c]);
+                    const float d = s_qk[t];
+                    val.x = fmaf(d, vv.x, val.x); val.y = fmaf(d, vv.y, val.y);
+                    val.z = fmaf(d, vv.z, val.z); val.w = fmaf(d, vv.w, val.w);
+                }
                 const long long off = b * w.ob + tok(u + t) * w.ot + hv * w.oh + col0 + c;
-                if (w.o_f32)
-                    static_cast<float *>(w.o)[off] = val;
-                else
-                    static_cast<T *>(w.o)[off] = from_f32<T>(val);
+                if (sizeof(T) == 4 || w.o_f32)
+                    *reinterpret_cast<float4 *>(static_cast<float *>(w.o) + off) = val;
+                else {
+                    const __nv_bfloat162 p[2] = {__floats2bfloat162_rn(val.x, val.y), __floats2bfloat162_rn(val.z, val.w)};
+                    *reinterpret_cast<uint2 *>(static_cast<T *>(w.o) + off) = *reinterpret_cast<const uint2 *>(p);
+                }
             }
         }
     }
@@ -356,11 +372,27 @@ __global__ void __launch_bounds__(kWalkThreads) linear_walk_kernel(const __grid_
     }
 }
 
+template <typename T, int DK, bool OUT, bool RD>
+__global__ void __launch_bounds__(kWalkThreads) linear_walk_kernel(const __grid_constant__ Walks ws) {
+    walk_tokens<T, DK, OUT, RD>(ws.w[blockIdx.z]);
+}
+// A gradient's walks where dk and dv differ: two with rows of DKA channels, the third with DKB.  One launch of these,
+// whose CTAs run side by side: apart, with 301 tokens and 4 heads in fp32, each pair of launches takes 26 us.
+template <typename T, int DKA, int DKB, bool OUT>
+__global__ void __launch_bounds__(kWalkThreads) linear_walk3_kernel(const __grid_constant__ Walks ws) {
+    if (blockIdx.z < 2)
+        walk_tokens<T, DKA, OUT, OUT>(ws.w[blockIdx.z]);
+    else
+        walk_tokens<T, DKB, OUT, false>(ws.w[2]);
+}
+
 // Tokens per segment.  Whole sequences as long as they give every SM six CTAs (what hides the
-// walk's latency); otherwise as many segments as get there, none below kMinSeg tokens.
+// walk's latency); otherwise as many segments as get there, none below kMinSeg tokens.  A sequence of up to
+// four of those is not cut: the second launch costs the host more than it saves (128 tokens, 4 heads
+// of 64, fp32: a call takes 20.8 us, cut 24.5; replayed in a graph 17.3 and 13.3).
 int walk_segment(int nseq, int HV, int nsl, long total, int max_len, bool varlen, int sms) {
     const long ctas = (long)nseq * HV * nsl, want = 6L * sms;
-    if (max_len <= 2 * kMinSeg || ctas >= want) return std::max(max_len, 1);
+    if (max_len <= 4 * kMinSeg || ctas >= want) return std::max(max_len, 1);
     const long tokens = varlen ? total : (long)nseq * max_len;
     const long segs = std::max(1L, want / ((long)HV * nsl));
     long L = (tokens + segs - 1) / segs;
@@ -369,31 +401,61 @@ int walk_segment(int nseq, int HV, int nsl, long total, int max_len, bool varlen
     return (int)((L + kTile - 1) / kTile * kTile);
 }
 
-template <typename T, int DK, bool RD>
-cudaError_t run_walk_t(const Walks &ws, int n, long items, int max_len, cudaStream_t st) {
-    const Walk &w = ws.w[0];
+template <typename T, int DK>
+cudaError_t run_walk_t(const Walk &w, long items, int max_len, cudaStream_t st) {
     const int nsl = w.DV / kCols;
     if (items * nsl > 0x7fffffffL) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)(items * nsl), (unsigned)w.HV, n);
+    const dim3 grid((unsigned)(items * nsl), (unsigned)w.HV);
+    Walks ws{};
+    ws.w[0] = w;
     if (max_len > w.L) linear_walk_kernel<T, DK, false, false><<<grid, kWalkThreads, 0, st>>>(ws);
-    linear_walk_kernel<T, DK, true, RD><<<grid, kWalkThreads, 0, st>>>(ws);
+    linear_walk_kernel<T, DK, true, false><<<grid, kWalkThreads, 0, st>>>(ws);
     return cudaGetLastError();
 }
-
-// n walks alike but for their arrays (same role dimensions, segments, heads); RD: some have row dots
-template <bool RD>
-cudaError_t run_walk(const Walks &ws, int n, DType dt, int DK, long items, int max_len, cudaStream_t st) {
-    if (dt == DType::BF16) {
-        switch (DK) {
-            case 32: return run_walk_t<__nv_bfloat16, 32, RD>(ws, n, items, max_len, st);
-            case 64: return run_walk_t<__nv_bfloat16, 64, RD>(ws, n, items, max_len, st);
-            default: return run_walk_t<__nv_bfloat16, 128, RD>(ws, n, items, max_len, st);
-        }
-    }
+template <typename T>
+cudaError_t run_walk(const Walk &w, int DK, long items, int max_len, cudaStream_t st) {
     switch (DK) {
-        case 32: return run_walk_t<float, 32, RD>(ws, n, items, max_len, st);
-        case 64: return run_walk_t<float, 64, RD>(ws, n, items, max_len, st);
-        default: return run_walk_t<float, 128, RD>(ws, n, items, max_len, st);
+        case 32: return run_walk_t<T, 32>(w, items, max_len, st);
+        case 64: return run_walk_t<T, 64>(w, items, max_len, st);
+        default: return run_walk_t<T, 128>(w, items, max_len, st);
+    }
+}
+
+// The walks of a gradient, equal lengths: ws.w[0] and [1] with rows of DKA channels, [2] with DKB.  Where the
+// three share one kernel, the one without row dots has a null pointer for them.
+template <typename T, int DKA, int DKB>
+cudaError_t run_walks_t(const Walks &ws, int T_len, cudaStream_t st) {
+    long x = 0;
+    bool cut = false;
+    for (const Walk &w : ws.w) {
+        x = std::max(x, lin_items(w.s.nseq, T_len, T_len, false, w.L) * (w.DV / kCols));
+        cut = cut || T_len > w.L;
+    }
+    if (x > 0x7fffffffL) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)x, (unsigned)ws.w[0].HV, 3);
+    if constexpr (DKA == DKB) {
+        if (cut) linear_walk_kernel<T, DKA, false, false><<<grid, kWalkThreads, 0, st>>>(ws);
+        linear_walk_kernel<T, DKA, true, true><<<grid, kWalkThreads, 0, st>>>(ws);
+    } else {
+        if (cut) linear_walk3_kernel<T, DKA, DKB, false><<<grid, kWalkThreads, 0, st>>>(ws);
+        linear_walk3_kernel<T, DKA, DKB, true><<<grid, kWalkThreads, 0, st>>>(ws);
+    }
+    return cudaGetLastError();
+}
+template <typename T, int DKA>
+cudaError_t run_walks_b(const Walks &ws, int DKB, int T_len, cudaStream_t st) {
+    switch (DKB) {
+        case 32: return run_walks_t<T, DKA, 32>(ws, T_len, st);
+        case 64: return run_walks_t<T, DKA, 64>(ws, T_len, st);
+        default: return run_walks_t<T, DKA, 128>(ws, T_len, st);
+    }
+}
+template <typename T>
+cudaError_t run_walks(const Walks &ws, int DKA, int DKB, int T_len, cudaStream_t st) {
+    switch (DKA) {
+        case 32: return run_walks_b<T, 32>(ws, DKB, T_len, st);
+        case 64: return run_walks_b<T, 64>(ws, DKB, T_len, st);
+        default: return run_walks_b<T, 128>(ws, DKB, T_len, st);
     }
 }
 
@@ -401,64 +463,97 @@ cudaError_t run_walk(const Walks &ws, int n, DType dt, int DK, long items, int m
 // ddecay from the row dots: one CTA per (batch entry, value head); every thread sums a run of
 // tokens, the runs' sums are scanned from the end, and the runs are walked again.
 constexpr int kGradThreads = 256;
-__global__ void __launch_bounds__(kGradThreads)
-linear_dgate_kernel(const float *rq, int nq, const float *rk, int nk, const float *hT, const float *dhT, float *dg,
-                    int T, int HV, int cells, long rows) {
-    __shared__ double s[kGradThreads];
-    const int b = blockIdx.x / HV, hv = blockIdx.x % HV, tid = threadIdx.x;
-    const size_t slice = (size_t)rows * HV;
+struct Dgate {
+    const float *rq, *rk;        // row dots, n slices each
+    int n;
+    const float *hT, *dhT;       // final memory and its gradient (or nullptr)
+    float *dg;
+    int T, HV, cells;
+    long rows;
+};
+__device__ __forceinline__ void sum_dgate(const Dgate &d, int pair) {
+    __shared__ double s_run[kGradThreads / 32], s_anchor[kGradThreads / 32];
+    const int b = pair / d.HV, hv = pair % d.HV, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const size_t slice = (size_t)d.rows * d.HV;
     auto at = [&](int t) {
-        const size_t i = ((size_t)b * T + t) * HV + hv;
-        double d = 0.0;
-        for (int j = 0; j < nq; ++j) d += rq[j * slice + i];
-        for (int j = 0; j < nk; ++j) d -= rk[j * slice + i];
-        return d;
+        const size_t i = ((size_t)b * d.T + t) * d.HV + hv;
+        double x = 0.0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < d.n) x += (double)__ldg(d.rq + j * slice + i) - (double)__ldg(d.rk + j * slice + i);
+        return x;
     };
-    double anchor = 0.0;
-    if (dhT)
-        for (int i = tid; i < cells; i += kGradThreads)
-            anchor += (double)hT[(size_t)blockIdx.x * cells + i] * dhT[(size_t)blockIdx.x * cells + i];
-    s[tid] = anchor;
-    __syncthreads();
-    for (int off = kGradThreads / 2; off; off >>= 1) {
-        if (tid < off) s[tid] += s[tid + off];
-        __syncthreads();
-    }
-    anchor = s[0];
-    __syncthreads();
-    const int run = (T + kGradThreads - 1) / kGradThreads, t0 = min(T, tid * run), t1 = min(T, t0 + run);
-    double mine = 0.0;
+    const int run = (d.T + kGradThreads - 1) / kGradThreads, t0 = min(d.T, tid * run), t1 = min(d.T, t0 + run);
+    double mine = 0.0, anchor = 0.0;
+#pragma unroll 2
     for (int t = t0; t < t1; ++t) mine += at(t);
-    s[tid] = mine;
-    __syncthreads();
-    for (int off = 1; off < kGradThreads; off <<= 1) {       // sums over this and the later runs
-        const double up = tid + off < kGradThreads ? s[tid + off] : 0.0;
-        __syncthreads();
-        s[tid] += up;
-        __syncthreads();
+    if (d.dhT) {
+        const float *p = d.hT + (size_t)pair * d.cells, *q = d.dhT + (size_t)pair * d.cells;
+#pragma unroll 8
+        for (int i = tid; i < d.cells; i += kGradThreads) anchor += (double)__ldg(p + i) * __ldg(q + i);
+#pragma unroll
+        for (int off = 16; off; off >>= 1) anchor += __shfl_xor_sync(0xffffffffu, anchor, off);
     }
-    double acc = anchor + s[tid] - mine;
+    double sum = mine;                                       // over this and the warp's later runs
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const double x = __shfl_down_sync(0xffffffffu, sum, off);
+        if (lane + off < 32) sum += x;
+    }
+    if (lane == 0) {
+        s_run[warp] = sum;
+        s_anchor[warp] = anchor;
+    }
+    __syncthreads();
+    double acc = sum - mine;
+#pragma unroll
+    for (int i = 0; i < kGradThreads / 32; ++i) acc += s_anchor[i] + (i > warp ? s_run[i] : 0.0);
     for (int t = t1 - 1; t >= t0; --t) {
         acc += at(t);
-        dg[((size_t)b * T + t) * HV + hv] = (float)acc;
+        d.dg[((size_t)b * d.T + t) * d.HV + hv] = (float)acc;
     }
 }
 
+// The value heads of a shared q/k head added up: two arrays
+struct Fold {
+    const float *src[2];         // [rows, H, m, D]
+    LinView dst[2];
+    long n;                      // elements of a result
+    int T, H, m, D;
+};
 template <typename T>
-__global__ void fold_heads_kernel(const float *src0, LinView dst0, const float *src1, LinView dst1, long n, int Tlen, int H,
-                                  int m, int D) {
-    const float *src = blockIdx.y ? src1 : src0;
-    const LinView &dst = blockIdx.y ? dst1 : dst0;
-    for (long i = blockIdx.x * (long)blockDim.x + threadIdx.x; i < n; i += (long)gridDim.x * blockDim.x) {
-        const int c = (int)(i % D);
-        const long rh = i / D;
-        const int h = (int)(rh % H);
-        const long row = rh / H;
+__device__ __forceinline__ void fold_heads(const Fold &f, int which, long first, long step) {
+    const float *src = f.src[which];
+    const LinView &dst = f.dst[which];
+    for (long i = first; i < f.n; i += step) {
+        const int c = (int)(i % f.D);
+        const long rh = i / f.D;
+        const int h = (int)(rh % f.H);
+        const long row = rh / f.H;
         float sum = 0.f;
-        for (int j = 0; j < m; ++j) sum += src[((row * H + h) * m + j) * D + c];
-        static_cast<T *>(const_cast<void *>(dst.p))[(row / Tlen) * dst.b + (row % Tlen) * dst.t + h * dst.h + c] =
+        for (int j = 0; j < f.m; ++j) sum += src[((row * f.H + h) * f.m + j) * f.D + c];
+        static_cast<T *>(const_cast<void *>(dst.p))[(row / f.T) * dst.b + (row % f.T) * dst.t + h * dst.h + c] =
             from_f32<T>(sum);
     }
+}
+// What follows a gradient's walks, in one launch: the first CTAs take ddecay, the others the shared heads.
+template <typename T>
+__global__ void __launch_bounds__(kGradThreads) linear_tail_kernel(Dgate d, int pairs, Fold f) {
+    if ((int)blockIdx.x < pairs) {
+        sum_dgate(d, blockIdx.x);
+        return;
+    }
+    const int at = blockIdx.x - pairs, per = (gridDim.x - pairs) / 2;
+    fold_heads<T>(f, at >= per, (long)(at % per) * kGradThreads + threadIdx.x, (long)per * kGradThreads);
+}
+cudaError_t run_tail(const Dgate &d, int pairs, const Fold &f, DType dt, cudaStream_t st) {
+    const long grid = pairs + 2 * std::min(2048L, (f.n + kGradThreads - 1) / kGradThreads);
+    if (grid == 0) return cudaSuccess;
+    if (dt == DType::BF16)
+        linear_tail_kernel<__nv_bfloat16><<<(unsigned)grid, kGradThreads, 0, st>>>(d, pairs, f);
+    else
+        linear_tail_kernel<float><<<(unsigned)grid, kGradThreads, 0, st>>>(d, pairs, f);
+    return cudaGetLastError();
 }
 
 // dst[c] = sum over the rows of src[r, c]: one CTA per column, a fixed order, fp64 sums (a
@@ -490,8 +585,8 @@ size_t walk_scratch(int nseq, int HV, int dk, int dv, long total, int max_len, b
 size_t linear_scan_scratch_bytes(int nseq, int HV, int dk, int dv, long total, int max_len, bool varlen, int sms) {
     if (varlen) {   // whatever the lengths turn out to be: the shortest segments the total allows
         const long ctas = (long)nseq * HV * (dv / kCols), want = 6L * sms;
-        if (total <= 2 * kMinSeg || ctas >= want) return 0;
-        const long L = walk_segment(nseq, HV, dv / kCols, total, 2 * kMinSeg + 1, true, sms);
+        if (total <= 4 * kMinSeg || ctas >= want) return 0;
+        const long L = walk_segment(nseq, HV, dv / kCols, total, 4 * kMinSeg + 1, true, sms);
         const size_t slots = (size_t)(total / L + nseq) * HV;
         return round256(slots * dk * dv * 4) + round256(slots * 4);
     }
@@ -516,20 +611,13 @@ cudaError_t launch_linear_scan(const LinFwd &a, cudaStream_t st) {
     const long items = lin_items(a.s.nseq, a.total, a.max_len, varlen, w.L);
     w.loc = static_cast<float *>(a.ws);
     w.gam = reinterpret_cast<float *>(static_cast<char *>(a.ws) + round256((size_t)items * a.HV * a.dk * a.dv * 4));
-    Walks ws{};
-    ws.w[0] = w;
-    return run_walk<false>(ws, 1, a.dtype, a.dk, items, a.max_len, st);
+    return a.dtype == DType::BF16 ? run_walk<__nv_bfloat16>(w, a.dk, items, a.max_len, st)
+                                  : run_walk<float>(w, a.dk, items, a.max_len, st);
 }
 
 cudaError_t launch_fold_heads(const float *src0, const LinView &dst0, const float *src1, const LinView &dst1, DType dt,
                               int B, int T, int H, int m, int D, cudaStream_t st) {
-    const long n = (long)B * T * H * D;
-    const dim3 grid((unsigned)std::min(4096L, (n + 255) / 256), 2);
-    if (dt == DType::BF16)
-        fold_heads_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(src0, dst0, src1, dst1, n, T, H, m, D);
-    else
-        fold_heads_kernel<float><<<grid, 256, 0, st>>>(src0, dst0, src1, dst1, n, T, H, m, D);
-    return cudaGetLastError();
+    return run_tail(Dgate{}, 0, Fold{{src0, src1}, {dst0, dst1}, (long)B * T * H * D, T, H, m, D}, dt, st);
 }
 
 cudaError_t launch_sum_rows(const float *src, float *dst, long rows, int cols, cudaStream_t st) {
@@ -584,47 +672,35 @@ cudaError_t launch_linear_scan_bwd(const LinBwd &a, cudaStream_t st) {
         w.oh = f32out ? DV : out.h;
         return w;
     };
-    Walks qk{}, v{};
+    Walks ws{};
     // dq: forwards on (do, v, k); memory transposed, [dv, dk]
-    Walk &wq = qk.w[0] = walk(a.dv, a.dk, a.dq, fq);
+    Walk &wq = ws.w[0] = walk(a.dv, a.dk, a.dq, fq);
     wq.q = a.d_o; wq.gq = 1; wq.k = a.v; wq.gk = 1; wq.v = a.k; wq.gv = m;
     wq.x = a.q; wq.gx = m; wq.rd = want_g ? rq : nullptr;
     wq.add_scale = 1.f; wq.out_scale = a.scale;
     wq.h0 = a.h0; wq.hT = want_g && a.dhT ? hT : nullptr; wq.si = 1; wq.sj = a.dv;
     // dk: backwards on (v, do, q), memory [dv, dk]
-    Walk &wk = qk.w[1] = walk(a.dv, a.dk, a.dk_, fk);
+    Walk &wk = ws.w[1] = walk(a.dv, a.dk, a.dk_, fk);
     wk.rev = 1;
     wk.q = a.v; wk.gq = 1; wk.k = a.d_o; wk.gk = 1; wk.v = a.q; wk.gv = m;
     wk.x = a.k; wk.gx = m; wk.rd = want_g ? rk : nullptr;
     wk.add_scale = a.scale; wk.out_scale = 1.f;
     wk.h0 = a.dhT; wk.si = 1; wk.sj = a.dv;
     // dv: backwards on (k, q, do), memory [dk, dv]; its final memory is the initial one's gradient
-    Walk wv = walk(a.dk, a.dv, a.dv_, nullptr);
+    Walk &wv = ws.w[2] = walk(a.dk, a.dv, a.dv_, nullptr);
     wv.rev = 1;
     wv.q = a.k; wv.gq = m; wv.k = a.q; wv.gk = m; wv.v = a.d_o; wv.gv = wv.gx = 1;
     wv.add_scale = a.scale; wv.out_scale = 1.f;
     wv.h0 = a.dhT; wv.hT = a.dh0; wv.si = a.dv; wv.sj = 1;
-    const long items = lin_items(a.B, a.T, a.T, false, wq.L);
-    cudaError_t e;
-    if (a.dk == a.dv) {
-        qk.w[2] = wv;
-        e = run_walk<true>(qk, 3, a.dtype, a.dv, items, a.T, st);
-    } else {
-        v.w[0] = wv;
-        e = run_walk<true>(qk, 2, a.dtype, a.dv, items, a.T, st);
-        if (e == cudaSuccess)
-            e = run_walk<false>(v, 1, a.dtype, a.dk, lin_items(a.B, a.T, a.T, false, wv.L), a.T, st);
-    }
+    cudaError_t e = a.dtype == DType::BF16 ? run_walks<__nv_bfloat16>(ws, a.dv, a.dk, a.T, st)
+                                           : run_walks<float>(ws, a.dv, a.dk, a.T, st);
     if (e != cudaSuccess) return e;
-    if (m > 1 && (e = launch_fold_heads(fq, a.dq, fk, a.dk_, a.dtype, a.B, a.T, a.H, m, a.dk, st)) != cudaSuccess) return e;
-    if (want_g) {
-        const bool fixed = a.g.t == 0;
-        linear_dgate_kernel<<<a.B * a.HV, kGradThreads, 0, st>>>(rq, a.dk / kCols, rk, a.dk / kCols, hT, a.dhT,
-                                                               fixed ? dgt : a.dg, a.T, a.HV, a.dk * a.dv,
-                                                               (long)a.B * a.T);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        if (fixed) e = launch_sum_rows(dgt, a.dg, (long)a.B * a.T, a.HV, st);
-    }
+    const bool fixed = a.g.t == 0;
+    Dgate d{rq, rk, a.dk / kCols, hT, a.dhT, fixed ? dgt : a.dg, a.T, a.HV, a.dk * a.dv, (long)a.B * a.T};
+    Fold f{};
+    if (m > 1) f = Fold{{fq, fk}, {a.dq, a.dk_}, (long)a.B * a.T * a.H * a.dk, a.T, a.H, m, a.dk};
+    e = run_tail(d, want_g ? a.B * a.HV : 0, f, a.dtype, st);
+    if (e == cudaSuccess && want_g && fixed) e = launch_sum_rows(dgt, a.dg, (long)a.B * a.T, a.HV, st);
     return e;
 }
 
