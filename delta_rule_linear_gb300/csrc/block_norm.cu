@@ -278,23 +278,28 @@ __global__ void __launch_bounds__(kThreads) gated_norm_bwd_kernel(GatedNorm a) {
     }
 }
 
-// out[c] = sum over p of part[p, c] in a fixed order: 32 columns x 32 strands of a CTA
-__global__ void __launch_bounds__(1024) norm_fold_kernel(const float *part, int np, int D, float *out0, float *out1) {
-    __shared__ float s[32][33];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
+// out[c] = sum over p of part[p, c] in a fixed order: 8 columns (a sector) x 32 strands of a CTA (32 columns to
+// a CTA leave narrow rows too few of them: 3 us more with 608 partial sums of 128 columns)
+__global__ void __launch_bounds__(kThreads) norm_fold_kernel(const float *part, int np, int D, float *out0, float *out1) {
+    __shared__ float s[8][33];
+    const int c = blockIdx.x * 8 + (threadIdx.x & 7), k = threadIdx.x >> 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int width = out1 ? 2 * D : D;
     float sum = 0.f;
     if (c < width) {
 #pragma unroll 8
         for (int p = k; p < np; p += 32) sum += part[(size_t)p * width + c];
     }
-    s[k][threadIdx.x & 31] = sum;
+    s[threadIdx.x & 7][k] = sum;
     __syncthreads();
-    sum = s[threadIdx.x & 31][k];               // column k's strands, one per lane
+    sum = s[warp][lane];                        // column `warp`, a strand per lane
 #pragma unroll
     for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    const int cc = blockIdx.x * 32 + k;
-    if ((threadIdx.x & 31) == 0 && cc < width) (cc < D ? out0 : out1)[cc < D ? cc : cc - D] = sum;
+    const int cc = blockIdx.x * 8 + warp;
+    if (lane == 0 && cc < width) (cc < D ? out0 : out1)[cc < D ? cc : cc - D] = sum;
+}
+cudaError_t norm_fold(const float *part, int np, int D, float *out0, float *out1, cudaStream_t st) {
+    norm_fold_kernel<<<((out1 ? 2 * D : D) + 7) / 8, kThreads, 0, st>>>(part, np, D, out0, out1);
+    return cudaGetLastError();
 }
 
 // ------------------------------------------------------------------------------ residual norm
@@ -473,10 +478,10 @@ cudaError_t gated_go(const GatedNorm &a, bool bwd, cudaStream_t st) {
         gated_norm_fwd_kernel<T, V, L, NJ><<<(unsigned)std::min(blocks, 8L * a.sms), kThreads, 0, st>>>(a);
         return cudaGetLastError();
     }
-    const int grid = (int)std::min(blocks, (long)norm_parts(a.sms));
+    // what its registers let an SM hold (8 of them, in two rounds, 24.1 us instead of 22.3 with 65,536 rows of 128)
+    const int grid = (int)std::min(blocks, 4L * a.sms);
     gated_norm_bwd_kernel<T, V, L, NJ><<<grid, kThreads, 0, st>>>(a);
-    norm_fold_kernel<<<(a.D + 31) / 32, 1024, 0, st>>>(a.part, grid, a.D, a.dw, nullptr);
-    return cudaGetLastError();
+    return norm_fold(a.part, grid, a.D, a.dw, nullptr, st);
 }
 
 // The narrowest lane group whose 16-byte packs cover the row; whole warps with several packs
@@ -513,9 +518,7 @@ cudaError_t residual_go(const ResidualNorm &a, bool bwd, cudaStream_t st) {
     // prefetched row keeps busy; narrow rows (a warp each) have narrow partial sums
     const int grid = (int)std::min(blocks, (long)(L > 32 ? 2 : 8) * a.sms);
     residual_norm_bwd_kernel<TR, T, V, L, NJ><<<grid, threads, 0, st>>>(a);
-    const int width = a.y ? 2 * a.D : a.D;
-    norm_fold_kernel<<<(width + 31) / 32, 1024, 0, st>>>(a.part, grid, a.D, a.dw, a.y ? a.dc : nullptr);
-    return cudaGetLastError();
+    return norm_fold(a.part, grid, a.D, a.dw, a.y ? a.dc : nullptr, st);
 }
 
 template <typename TR, typename T>
