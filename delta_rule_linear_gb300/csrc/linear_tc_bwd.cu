@@ -37,6 +37,7 @@ using namespace lin;
 
 // Chunks of a group: six for every SM, and 117 MB of memories at d = 128 (L2 is 129 MB)
 constexpr long kGroupChunks = 912;
+constexpr long kWalkCtas = 56, kWalkChunks = 4864;
 
 struct BwdParams {
     LinDecay g;
@@ -54,6 +55,28 @@ struct BwdParams {
     WsHeader *hdr;
     int clear;                  // the call's first launch: clears the error word
 };
+
+// Weights of a lane's four tokens from their log2 decays: of their values in the memory that leaves the chunk
+// (direction 0: the decays behind a token), of their output gradients in the one that enters it (direction 1: up to and
+// with it, times the query scale).  `all` (lane 31): the chunk's factor.
+__device__ __forceinline__ float4 chunk_weights(const float4 &d, int dir, float scale, int lane, float &all) {
+    float4 x = d, y = make_float4(d.y + (d.z + d.w), d.z + d.w, d.w, 0.f);
+    x.y += x.x; x.z += x.y; x.w += x.z;
+    float up = x.w, down = d.x + y.x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const float p = __shfl_up_sync(0xffffffffu, up, off), q = __shfl_down_sync(0xffffffffu, down, off);
+        if (lane >= off) up += p;
+        if (lane + off < 32) down += q;
+    }
+    float before = __shfl_up_sync(0xffffffffu, up, 1), behind = __shfl_down_sync(0xffffffffu, down, 1);
+    if (lane == 0) before = 0.f;
+    if (lane == 31) behind = 0.f;
+    all = ex2(up);
+    return dir ? make_float4(scale * ex2(x.x + before), scale * ex2(x.y + before), scale * ex2(x.z + before),
+                             scale * ex2(x.w + before))
+               : make_float4(ex2(y.x + behind), ex2(y.y + behind), ex2(y.z + behind), ex2(behind));
+}
 
 // ------------------------------------------------------------------------------ 1: contributions
 // Warps 0-7: weighted values (thread = value channel, half of the tokens); 8-11: results; 12: decays
@@ -127,27 +150,11 @@ linear_part_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             const int b = (int)(pair / w.HV), hv = (int)(pair % w.HV);
             const float *gp = w.g.p ? w.g.p + b * w.g.b + hv : nullptr;
             const float4 d = load_decay(w.g, gp, u + 4 * lane, w.T);
-            // sums behind a token (direction 0), up to and with it (direction 1)
-            float4 x = d, y = make_float4(d.y + (d.z + d.w), d.z + d.w, d.w, 0.f);
-            x.y += x.x; x.z += x.y; x.w += x.z;
-            float up = x.w, down = d.x + y.x;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const float p = __shfl_up_sync(0xffffffffu, up, off), q = __shfl_down_sync(0xffffffffu, down, off);
-                if (lane >= off) up += p;
-                if (lane + off < 32) down += q;
-            }
-            float before = __shfl_up_sync(0xffffffffu, up, 1), behind = __shfl_down_sync(0xffffffffu, down, 1);
-            if (lane == 0) before = 0.f;
-            if (lane == 31) {
-                behind = 0.f;
-                if (!dir) w.alpha[slot] = ex2(up);
-            }
+            float all;
+            const float4 f = chunk_weights(d, dir, w.scale, lane, all);
+            if (lane == 31 && !dir) w.alpha[slot] = all;
             if (n >= NST && !wt.warp(&ctl->empty[s], (n / NST - 1) & 1, 41)) break;
-            *reinterpret_cast<float4 *>(wa + s * kC + 4 * lane) =
-                dir ? make_float4(w.scale * ex2(x.x + before), w.scale * ex2(x.y + before), w.scale * ex2(x.z + before),
-                                  w.scale * ex2(x.w + before))
-                    : make_float4(ex2(y.x + behind), ex2(y.y + behind), ex2(y.z + behind), ex2(behind));
+            *reinterpret_cast<float4 *>(wa + s * kC + 4 * lane) = f;
             __syncwarp();
             if (lane == 0) {
                 uint8_t *st = smem + s * Cf::STAGE;
@@ -267,6 +274,191 @@ __global__ void __launch_bounds__(256) linear_chain_kernel(BwdParams w, int cell
         }
     }
     if (rev && w.dh0) *reinterpret_cast<float4 *>(w.dh0 + pc) = s;
+}
+
+// ------------------------------------------------------------------------------ 1 and 2 at once: the walk
+// A CTA walks the chunks of one (direction, pair) for 64 key channels: the memory stays in TMEM in fp32, is stored
+// to each chunk's slot, decayed, and takes the chunk's product.  A chunk's chain is the product (24 steps of N = 64)
+// and the memory's way through registers; loads, weighted values and stores run beside it.
+// Warps 0-7: weighted values; 8-11: the memory; 12: decays and TMA; 13: products.
+template <int DV>
+struct StateCfg {
+    static constexpr int KB = kC * 128, VB = kC * DV * 2, STAGE = KB + VB, NST = 4;
+    static constexpr int ARR = NST * STAGE, CTL = ARR + NST * kC * 4, SMEM = CTL + 256;
+    static constexpr int T_V = 128;             // the memory [64], then two sets of hi, mid, lo
+    static_assert(SMEM <= 232448, "shared memory");
+};
+struct StateCtl {
+    uint64_t full[4], empty[4], ready[2], used[2], s_ready, d_full, last;
+    float alpha[4];
+    uint32_t tmem;
+    int fail;
+};
+static_assert(sizeof(StateCtl) <= 256, "control block");
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kPartThreads, 1)
+linear_state_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, BwdParams w) {
+    using Cf = StateCfg<DV>;
+    constexpr int NST = Cf::NST, KS = DK / 64;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    StateCtl *ctl = reinterpret_cast<StateCtl *>(smem + Cf::CTL);
+    if ((smem_u32(smem) & 1023) || blockDim.x != kPartThreads) {
+        if (threadIdx.x == 0) atomicCAS(&w.hdr->error, 0, kStatusDeviceTimeout);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (w.clear && blockIdx.x == 0 && tid == 0) w.hdr->error = 0;
+    const int part = blockIdx.x % KS, dir = blockIdx.x / KS % 2, pi = blockIdx.x / (2 * KS), nch = w.nch;
+    const long pair = w.pair0 + pi;
+    const int b = (int)(pair / w.HV), hv = (int)(pair % w.HV);
+    if (tid == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&ctl->full[i], 1);
+            mbar_init(&ctl->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->ready[i], 256);
+            mbar_init(&ctl->used[i], 1);
+        }
+        mbar_init(&ctl->s_ready, 128);
+        mbar_init(&ctl->d_full, 1);
+        mbar_init(&ctl->last, 1);
+        ctl->fail = 0;
+        fence_mbar_init();
+    }
+    if (warp == 13) {
+        tmem_alloc(&ctl->tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = ctl->tmem;
+    const Waits wt{&ctl->fail, w.hdr};
+    const uint32_t tlane = tm + ((uint32_t)(32 * (warp & 3)) << 16);
+    float *wa = reinterpret_cast<float *>(smem + Cf::ARR);
+    auto chunk_of = [&](int n) { return dir ? nch - 1 - n : n; };
+
+    if (warp == 12) {
+        const float *gp = w.g.p ? w.g.p + b * w.g.b + hv : nullptr;
+        for (int n = 0; n < nch; ++n) {
+            const int s = n % NST, u = chunk_of(n) * kC;
+            float all;
+            const float4 f = chunk_weights(load_decay(w.g, gp, u + 4 * lane, w.T), dir, w.scale, lane, all);
+            if (n >= NST && !wt.warp(&ctl->empty[s], (n / NST - 1) & 1, 61)) break;
+            *reinterpret_cast<float4 *>(wa + s * kC + 4 * lane) = f;
+            if (lane == 31) ctl->alpha[s] = all;
+            __syncwarp();
+            if (lane == 0) {
+                uint8_t *st = smem + s * Cf::STAGE;
+                mbar_expect_tx(&ctl->full[s], Cf::STAGE);
+                tma_load_4d(st, dir ? &mq : &mk, &ctl->full[s], 64 * part, hv / w.m, u, b);
+#pragma unroll
+                for (int i = 0; i < DV / 64; ++i)
+                    tma_load_4d(st + Cf::KB + i * kC * 128, dir ? &mo : &mv, &ctl->full[s], 64 * i, hv, u, b);
+            }
+        }
+    } else if (warp == 13) {
+        constexpr uint32_t id = idesc_bf16_f32(128, 64, false, true);
+        for (int n = 0; n < nch; ++n) {
+            const int s = n % NST;
+            if (!wt.warp(&ctl->full[s], (n / NST) & 1, 62) || !wt.warp(&ctl->ready[n & 1], (n >> 1) & 1, 63) ||
+                !wt.warp(&ctl->s_ready, n & 1, 64)) break;
+            tc_fence_after();
+            const uint64_t dk = desc_mnmajor_sw128(smem_u32(smem + s * Cf::STAGE), kC, 0);
+            const uint32_t a = tm + Cf::T_V + (n & 1) * 192;
+            if (lane == 0) {
+                product_ts<true>(tm, a, dk, id);
+                product_ts<true>(tm, a + 64, dk, id);
+                product_ts<true>(tm, a + 128, dk, id);
+                mma_commit(&ctl->used[n & 1]);
+                mma_commit(&ctl->empty[s]);
+                mma_commit(&ctl->d_full);
+            }
+            __syncwarp();
+        }
+    } else if (warp < 8) {
+        const int ch = tid & 127, half = tid >> 7;
+        const bool has = (ch & ~31) < DV;
+        for (int n = 0; n < nch; ++n) {
+            const int s = n % NST;
+            if (!wt.warp(&ctl->full[s], (n / NST) & 1, 65)) break;
+            if (n >= 2 && !wt.warp(&ctl->used[n & 1], ((n >> 1) - 1) & 1, 66)) break;
+            tc_fence_after();
+            const uint32_t a = tlane + Cf::T_V + (n & 1) * 192;
+            if (has) put_values<3>(smem + s * Cf::STAGE + Cf::KB, wa + s * kC, ch, 64 * half, a, a + 64, a + 128);
+            tc_fence_before();
+            mbar_arrive(&ctl->ready[n & 1]);
+        }
+    } else {
+        const int i = tid - 256;                // value channel
+        const float *init = dir ? w.dhT : w.h0;
+        const size_t own = (size_t)64 * part * DV + i;
+        uint32_t x[2][32];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                x[k][j] = init && i < DV ? __float_as_uint(init[(size_t)pair * DK * DV + own + (32 * k + j) * DV]) : 0u;
+        bool ok = true;
+        for (int n = 0; n < nch; ++n) {
+            const int s = n % NST;
+            ok = wt.warp(&ctl->full[s], (n / NST) & 1, 67) && (n == 0 || wt.warp(&ctl->d_full, (n - 1) & 1, 68));
+            if (!ok) break;
+            tc_fence_after();
+            if (n > 0) {
+                tmem_ld32(tlane, x[0]);
+                tmem_ld32(tlane + 32, x[1]);
+                tmem_ld_wait();
+            }
+            const float al = ctl->alpha[s];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t y[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(al * __uint_as_float(x[k][j]));
+                tmem_st32(tlane + 32 * k, y);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&ctl->s_ready);
+            float *p = (dir ? w.R : w.S) + ((size_t)pi * nch + chunk_of(n)) * DK * DV + own;
+            if (i < DV)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) p[(32 * k + j) * DV] = __uint_as_float(x[k][j]);
+        }
+        if (dir && w.dh0 && ok && wt.warp(&ctl->d_full, (nch - 1) & 1, 69)) {
+            tc_fence_after();
+            tmem_ld32(tlane, x[0]);
+            tmem_ld32(tlane + 32, x[1]);
+            tmem_ld_wait();
+            float *p = w.dh0 + (size_t)pair * DK * DV + own;
+            if (i < DV)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) p[(32 * k + j) * DV] = __uint_as_float(x[k][j]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 13) {
+        if (lane == 0) mma_commit(&ctl->last);
+        __syncwarp();
+        (void)mbar_wait(&ctl->last, 0, kWaitNs);
+        if (ctl->fail) {                        // let what is in flight land
+            const uint64_t t = globaltimer_ns();
+            while (globaltimer_ns() - t < 1000000ull) {
+            }
+        }
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tm, 512);
+    }
 }
 
 // ------------------------------------------------------------------------------ 3: gradients
@@ -782,27 +974,36 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
 }
 
 // ------------------------------------------------------------------------------ host
-long group_pairs(long pairs, int nch) { return std::max(1L, std::min(pairs, kGroupChunks / nch)); }
+bool walks(long pairs, int dk) { return pairs * (dk / 64) * 2 >= kWalkCtas; }
+long group_pairs(long pairs, int nch, int dk) {
+    return std::max(1L, std::min(pairs, (walks(pairs, dk) ? kWalkChunks : kGroupChunks) / nch));
+}
 
 template <int DK, int DV>
 cudaError_t run_groups(const LinBwd &a, BwdParams w, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                        const CUtensorMap &mo, cudaStream_t st) {
     using PC = PartCfg<DK, DV>;
     using GC = GradCfg<DK, DV>;
-    static SmemOnce part_once, grad_once;
+    using SC = StateCfg<DV>;
+    static SmemOnce part_once, state_once, grad_once;
     cudaError_t e = part_once(linear_part_kernel<DK, DV>, PC::SMEM);
+    if (e == cudaSuccess) e = state_once(linear_state_kernel<DK, DV>, SC::SMEM);
     if (e == cudaSuccess) e = grad_once(linear_grad_kernel<DK, DV>, GC::SMEM);
     if (e != cudaSuccess) return e;
-    const long pairs = (long)a.B * a.HV, np = group_pairs(pairs, w.nch);
+    const long pairs = (long)a.B * a.HV, np = group_pairs(pairs, w.nch, DK);
     constexpr int cells = DK * DV;
     for (long p0 = 0; p0 < pairs; p0 += np) {
         w.pair0 = p0;
         w.clear = p0 == 0;
         w.pairs = (int)std::min(np, pairs - p0);
         const int slots = w.pairs * w.nch;
-        linear_part_kernel<DK, DV><<<std::min(2 * slots, a.sms), kPartThreads, PC::SMEM, st>>>(mq, mk, mv, mo, w);
-        const dim3 grid((unsigned)(((long)w.pairs * (cells / 4) + 255) / 256), 2);
-        linear_chain_kernel<<<grid, 256, 0, st>>>(w, cells);
+        if (walks(pairs, DK)) {
+            linear_state_kernel<DK, DV><<<w.pairs * 2 * (DK / 64), kPartThreads, SC::SMEM, st>>>(mq, mk, mv, mo, w);
+        } else {
+            linear_part_kernel<DK, DV><<<std::min(2 * slots, a.sms), kPartThreads, PC::SMEM, st>>>(mq, mk, mv, mo, w);
+            const dim3 grid((unsigned)(((long)w.pairs * (cells / 4) + 255) / 256), 2);
+            linear_chain_kernel<<<grid, 256, 0, st>>>(w, cells);
+        }
         linear_grad_kernel<DK, DV><<<std::min(slots, a.sms), kGradThreads, GC::SMEM, st>>>(mq, mk, mv, mo, w);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
@@ -815,7 +1016,7 @@ cudaError_t run_groups(const LinBwd &a, BwdParams w, const CUtensorMap &mq, cons
 size_t linear_tc_bwd_scratch_bytes(int B, int T, int H, int HV, int dk, int dv, int sms) {
     (void)sms;
     const int nch = (T + kC - 1) / kC;
-    const size_t slots = (size_t)group_pairs((long)B * HV, nch) * nch, rows = (size_t)B * T * HV;
+    const size_t slots = (size_t)group_pairs((long)B * HV, nch, dk) * nch, rows = (size_t)B * T * HV;
     size_t n = 2 * round256(slots * dk * dv * 4) + round256(slots * 4) + round256(rows * 4);
     if (HV > H) n += 2 * round256(rows * dk * 4);
     return n;
@@ -826,7 +1027,7 @@ cudaError_t launch_linear_tc_bwd(const LinBwd &a, cudaStream_t st) {
     const int m = a.HV / a.H;
     w.g = a.g; w.HV = a.HV; w.m = m; w.T = a.T; w.nch = (a.T + kC - 1) / kC; w.scale = a.scale;
     w.h0 = a.h0; w.dhT = a.dhT; w.dh0 = a.dh0; w.hdr = a.hdr;
-    const size_t slots = (size_t)group_pairs((long)a.B * a.HV, w.nch) * w.nch, rows = (size_t)a.B * a.T * a.HV;
+    const size_t slots = (size_t)group_pairs((long)a.B * a.HV, w.nch, a.dk) * w.nch, rows = (size_t)a.B * a.T * a.HV;
     char *p = static_cast<char *>(a.ws);
     auto carve = [&](size_t n) { char *r = p; p += round256(n); return reinterpret_cast<float *>(r); };
     w.S = carve(slots * a.dk * a.dv * 4);
