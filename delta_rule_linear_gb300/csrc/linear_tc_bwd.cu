@@ -16,13 +16,20 @@
 // column sums, j < i only).  Every term of ddecay comes from fp32 products of exact or two-part operands
 // and is anchored in its own chunk, so nothing drifts along the sequence.
 //
-// Three launches for a group of (sequence, head) pairs:
-//   1  every chunk's own contribution to S' and to R', all chunks at once (the two are one kernel on other
-//      operands: the weighted values go in as three bf16 parts, as in the forward);
-//   2  the two chains over the chunks, elementwise and in place: each slot then holds S (or R);
-//   3  everything else, all chunks at once.
-// The memories of a group (2 x 4 dk dv bytes per chunk) stay within L2: 64 KB + 64 KB at d = 128 and at most
-// kGroupChunks chunks; a larger problem is taken group by group through the same scratch.
+// For a group of (sequence, head) pairs, first every chunk's S and R (the two are one kernel on other
+// operands: the weighted values go in as three bf16 parts, as in the forward), then everything else, all chunks
+// at once.  S and R come
+//   of enough pairs from one launch that walks the chunks, the memory in TMEM;
+//   of few pairs from two: every chunk's own contribution, all chunks at once, then the two chains over
+//   the chunks, elementwise and in place.
+// A walk takes 1.4 to 2.1 us a chunk of d = 128 however many pairs fit the machine, the other way 0.11 us a
+// chunk and pair or, where a group has room for few pairs, the latency of the chains (costs in `walks` below).  All
+// gradients of 2 x 2048 tokens, 16 heads of 128: 101 us walked, 118 the other way; of 2048 tokens, 14 heads:
+// 63 and 55; of 2 x 2048 tokens, 16 heads of 64: 65 and 61; of 32,768 tokens, 16 heads of 128: 814 and 1280.
+// The contributions of a group stay within L2, where the chains read them: 2 x 64 KB a chunk at d = 128 and
+// at most kGroupChunks chunks.  A walk's memories are read back once, and a wider group fills the machine: kWalkChunks
+// of them (32,768 tokens, 16 heads: 814 us, with half as many 1187).  A larger problem is taken group by
+// group through the same scratch.
 //
 // Every wait is bounded; a time-out is recorded in the workspace header and the CTA unwinds.
 #include <algorithm>
@@ -37,7 +44,7 @@ using namespace lin;
 
 // Chunks of a group: six for every SM, and 117 MB of memories at d = 128 (L2 is 129 MB)
 constexpr long kGroupChunks = 912;
-constexpr long kWalkCtas = 56, kWalkChunks = 4864;
+constexpr long kWalkChunks = 4864;     // 0.6 GB of memories at d = 128
 
 struct BwdParams {
     LinDecay g;
@@ -279,7 +286,8 @@ __global__ void __launch_bounds__(256) linear_chain_kernel(BwdParams w, int cell
 // ------------------------------------------------------------------------------ 1 and 2 at once: the walk
 // A CTA walks the chunks of one (direction, pair) for 64 key channels: the memory stays in TMEM in fp32, is stored
 // to each chunk's slot, decayed, and takes the chunk's product.  A chunk's chain is the product (24 steps of N = 64)
-// and the memory's way through registers; loads, weighted values and stores run beside it.
+// and the memory's way through registers, 2000 to 2400 clocks; loads and stores run beside it.  The weighted
+// values of the next chunk do too, and take as long: 14 instructions a pair of them, in either half of a memory's CTAs.
 // Warps 0-7: weighted values; 8-11: the memory; 12: decays and TMA; 13: products.
 template <int DV>
 struct StateCfg {
@@ -974,9 +982,16 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
 }
 
 // ------------------------------------------------------------------------------ host
-bool walks(long pairs, int dk) { return pairs * (dk / 64) * 2 >= kWalkCtas; }
-long group_pairs(long pairs, int nch, int dk) {
-    return std::max(1L, std::min(pairs, (walks(pairs, dk) ? kWalkChunks : kGroupChunks) / nch));
+// Whether the memories are walked: the time of either way, in us per chunk of a sequence (as measured).
+bool walks(long pairs, int nch, int dk, int sms) {
+    auto group = [&](long chunks) { return std::max(1L, std::min(pairs, chunks / nch)); };
+    auto count = [&](long g) { return (double)((pairs + g - 1) / g); };
+    const long gw = group(kWalkChunks), gc = group(kGroupChunks), ctas = gw * (dk / 64) * 2;
+    const double each = gc * dk / 128.0;
+    return count(gw) * (double)((ctas + sms - 1) / sms) * 2.0 < count(gc) * std::max(0.11 * each, 0.045 * each + 0.4);
+}
+long group_pairs(long pairs, int nch, int dk, int sms) {
+    return std::max(1L, std::min(pairs, (walks(pairs, nch, dk, sms) ? kWalkChunks : kGroupChunks) / nch));
 }
 
 template <int DK, int DV>
@@ -990,14 +1005,14 @@ cudaError_t run_groups(const LinBwd &a, BwdParams w, const CUtensorMap &mq, cons
     if (e == cudaSuccess) e = state_once(linear_state_kernel<DK, DV>, SC::SMEM);
     if (e == cudaSuccess) e = grad_once(linear_grad_kernel<DK, DV>, GC::SMEM);
     if (e != cudaSuccess) return e;
-    const long pairs = (long)a.B * a.HV, np = group_pairs(pairs, w.nch, DK);
+    const long pairs = (long)a.B * a.HV, np = group_pairs(pairs, w.nch, DK, a.sms);
     constexpr int cells = DK * DV;
     for (long p0 = 0; p0 < pairs; p0 += np) {
         w.pair0 = p0;
         w.clear = p0 == 0;
         w.pairs = (int)std::min(np, pairs - p0);
         const int slots = w.pairs * w.nch;
-        if (walks(pairs, DK)) {
+        if (walks(pairs, w.nch, DK, a.sms)) {
             linear_state_kernel<DK, DV><<<w.pairs * 2 * (DK / 64), kPartThreads, SC::SMEM, st>>>(mq, mk, mv, mo, w);
         } else {
             linear_part_kernel<DK, DV><<<std::min(2 * slots, a.sms), kPartThreads, PC::SMEM, st>>>(mq, mk, mv, mo, w);
@@ -1014,9 +1029,8 @@ cudaError_t run_groups(const LinBwd &a, BwdParams w, const CUtensorMap &mq, cons
 
 // Scratch: [S][R][chunk decays] of a group, [per-value-head dq, dk] when heads are shared, [per-token ddecay]
 size_t linear_tc_bwd_scratch_bytes(int B, int T, int H, int HV, int dk, int dv, int sms) {
-    (void)sms;
     const int nch = (T + kC - 1) / kC;
-    const size_t slots = (size_t)group_pairs((long)B * HV, nch, dk) * nch, rows = (size_t)B * T * HV;
+    const size_t slots = (size_t)group_pairs((long)B * HV, nch, dk, sms) * nch, rows = (size_t)B * T * HV;
     size_t n = 2 * round256(slots * dk * dv * 4) + round256(slots * 4) + round256(rows * 4);
     if (HV > H) n += 2 * round256(rows * dk * 4);
     return n;
@@ -1027,7 +1041,7 @@ cudaError_t launch_linear_tc_bwd(const LinBwd &a, cudaStream_t st) {
     const int m = a.HV / a.H;
     w.g = a.g; w.HV = a.HV; w.m = m; w.T = a.T; w.nch = (a.T + kC - 1) / kC; w.scale = a.scale;
     w.h0 = a.h0; w.dhT = a.dhT; w.dh0 = a.dh0; w.hdr = a.hdr;
-    const size_t slots = (size_t)group_pairs((long)a.B * a.HV, w.nch, a.dk) * w.nch, rows = (size_t)a.B * a.T * a.HV;
+    const size_t slots = (size_t)group_pairs((long)a.B * a.HV, w.nch, a.dk, a.sms) * w.nch, rows = (size_t)a.B * a.T * a.HV;
     char *p = static_cast<char *>(a.ws);
     auto carve = [&](size_t n) { char *r = p; p += round256(n); return reinterpret_cast<float *>(r); };
     w.S = carve(slots * a.dk * a.dv * 4);

@@ -236,6 +236,33 @@ def test_chunk_bwd_long_and_without_final_gradient(kda, dtype):
     _check_bwd(got, n, dtype, 128, 128, 1500, True)
 
 
+@pytest.mark.parametrize("decay", ["mild", "strong", "none"])
+@pytest.mark.parametrize("shape", [(1, 300, 20, 1, 128, 128), (2, 260, 10, 2, 64, 128), (1, 129, 10, 2, 128, 64),
+                                   (2, 128, 20, 1, 64, 64)], ids=str)
+def test_chunk_bwd_many_heads(kda, shape, decay):
+    """Enough heads for the memories to be walked chunk after chunk."""
+    B, T, H, m, dk, dv = shape
+    d, n = _make(*shape, "bf16", decay=decay, seed=11)
+    got = kda.linear_chunk_bwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], d["d_o"], d["dhT"], check_device=True)
+    _check_bwd(got, n, "bf16", dk, dv, T, True)
+
+
+@pytest.mark.parametrize("B,T,H,D", [(50, 129, 50, 64), (1, 16384, 8, 128)])
+def test_chunk_bwd_groups_do_not_meet(kda, B, T, H, D):
+    """More memories than the scratch holds at a time: the same bits as for either half of the heads alone."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(12)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    q, k, v, d_o = (r(B, T, H, D).bfloat16() for _ in range(4))
+    decay, dhT = -0.05 * r(B, T, H).abs(), r(B, H, D, D)
+    whole = kda.linear_chunk_bwd(q, k, v, decay, None, d_o, dhT, check_device=True)
+    for part in (slice(0, H // 2), slice(H // 2, H)):
+        half = kda.linear_chunk_bwd(q[:, :, part], k[:, :, part], v[:, :, part], decay[:, :, part].contiguous(), None,
+                                    d_o[:, :, part], dhT[:, part].contiguous(), check_device=True)
+        for x in half:
+            assert torch.equal(half[x], whole[x][:, :, part]), x
+
+
 def test_other_stream_and_repeat(kda):
     """Calls on a side stream give the same bits, run after run."""
     import torch
