@@ -190,6 +190,7 @@ template <typename T, int V, int L, int NJ>
 __global__ void __launch_bounds__(kThreads) gated_norm_bwd_kernel(GatedNorm a) {
     constexpr int RPB = kThreads / L;
     __shared__ float s_dw[RPB][L * V + 1];
+    next_may_start();
     const int l = threadIdx.x % L, rg = threadIdx.x / L;
     float dw[NJ][V], w[NJ][V];
 #pragma unroll
@@ -284,6 +285,7 @@ __global__ void __launch_bounds__(kThreads) norm_fold_kernel(const float *part, 
     __shared__ float s[8][33];
     const int c = blockIdx.x * 8 + (threadIdx.x & 7), k = threadIdx.x >> 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int width = out1 ? 2 * D : D;
+    wait_for_previous();
     float sum = 0.f;
     if (c < width) {
 #pragma unroll 8
@@ -298,8 +300,7 @@ __global__ void __launch_bounds__(kThreads) norm_fold_kernel(const float *part, 
     if (lane == 0 && cc < width) (cc < D ? out0 : out1)[cc < D ? cc : cc - D] = sum;
 }
 cudaError_t norm_fold(const float *part, int np, int D, float *out0, float *out1, cudaStream_t st) {
-    norm_fold_kernel<<<((out1 ? 2 * D : D) + 7) / 8, kThreads, 0, st>>>(part, np, D, out0, out1);
-    return cudaGetLastError();
+    return launch_after(norm_fold_kernel, ((out1 ? 2 * D : D) + 7) / 8, kThreads, 0, st, part, np, D, out0, out1);
 }
 
 // ------------------------------------------------------------------------------ residual norm
@@ -353,6 +354,7 @@ __global__ void __launch_bounds__(L > 32 ? L : kThreads) residual_norm_bwd_kerne
     constexpr int SW = L > 32 ? L / 32 : 1;
     __shared__ float s_red[2][2 * SW];
     __shared__ float s_dw[L > 32 ? 1 : RPB][L > 32 ? 1 : L * V + 1];
+    next_may_start();
     const int l = threadIdx.x % L, rg = threadIdx.x / L;
     float dw[NJ][V], dc[NJ][V];
 #pragma unroll
@@ -481,6 +483,7 @@ cudaError_t gated_go(const GatedNorm &a, bool bwd, cudaStream_t st) {
     // what its registers let an SM hold (8 of them, in two rounds, 24.1 us instead of 22.3 with 65,536 rows of 128)
     const int grid = (int)std::min(blocks, 4L * a.sms);
     gated_norm_bwd_kernel<T, V, L, NJ><<<grid, kThreads, 0, st>>>(a);
+    if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     return norm_fold(a.part, grid, a.D, a.dw, nullptr, st);
 }
 
@@ -518,6 +521,7 @@ cudaError_t residual_go(const ResidualNorm &a, bool bwd, cudaStream_t st) {
     // prefetched row keeps busy; narrow rows (a warp each) have narrow partial sums
     const int grid = (int)std::min(blocks, (long)(L > 32 ? 2 : 8) * a.sms);
     residual_norm_bwd_kernel<TR, T, V, L, NJ><<<grid, threads, 0, st>>>(a);
+    if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     return norm_fold(a.part, grid, a.D, a.dw, a.y ? a.dc : nullptr, st);
 }
 

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "kda_internal.cuh"
+#include "launch_after.cuh"
 
 namespace kda {
 

@@ -167,6 +167,7 @@ __device__ __forceinline__ void walk_tokens(const Walk &w) {
         s_o[kTile][kCols + 8];                               // rows apart in the banks
     __shared__ float s_a[kTile], s_qk[kTile];
 
+    if constexpr (OUT) wait_for_previous();
     const int nsl = w.DV / kCols, sl = blockIdx.x % nsl, item = blockIdx.x / nsl, hv = blockIdx.y;
     if (blockIdx.x == 0 && hv == 0 && threadIdx.x == 0 && w.hdr) w.hdr->error = 0;
     LinItem it;
@@ -401,6 +402,17 @@ int walk_segment(int nseq, int HV, int nsl, long total, int max_len, bool varlen
     return (int)((L + kTile - 1) / kTile * kTile);
 }
 
+// The segments' memories where there are several, and the outputs
+cudaError_t run_pair(void (*local)(Walks), void (*out)(Walks), bool cut, dim3 grid, const Walks &ws, cudaStream_t st) {
+    if (!cut) {
+        out<<<grid, kWalkThreads, 0, st>>>(ws);
+        return cudaGetLastError();
+    }
+    local<<<grid, kWalkThreads, 0, st>>>(ws);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? launch_after(out, grid, kWalkThreads, 0, st, ws) : e;
+}
+
 template <typename T, int DK>
 cudaError_t run_walk_t(const Walk &w, long items, int max_len, cudaStream_t st) {
     const int nsl = w.DV / kCols;
@@ -408,9 +420,8 @@ cudaError_t run_walk_t(const Walk &w, long items, int max_len, cudaStream_t st) 
     const dim3 grid((unsigned)(items * nsl), (unsigned)w.HV);
     Walks ws{};
     ws.w[0] = w;
-    if (max_len > w.L) linear_walk_kernel<T, DK, false, false><<<grid, kWalkThreads, 0, st>>>(ws);
-    linear_walk_kernel<T, DK, true, false><<<grid, kWalkThreads, 0, st>>>(ws);
-    return cudaGetLastError();
+    return run_pair(linear_walk_kernel<T, DK, false, false>, linear_walk_kernel<T, DK, true, false>, max_len > w.L, grid,
+                    ws, st);
 }
 template <typename T>
 cudaError_t run_walk(const Walk &w, int DK, long items, int max_len, cudaStream_t st) {
@@ -433,14 +444,10 @@ cudaError_t run_walks_t(const Walks &ws, int T_len, cudaStream_t st) {
     }
     if (x > 0x7fffffffL) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)x, (unsigned)ws.w[0].HV, 3);
-    if constexpr (DKA == DKB) {
-        if (cut) linear_walk_kernel<T, DKA, false, false><<<grid, kWalkThreads, 0, st>>>(ws);
-        linear_walk_kernel<T, DKA, true, true><<<grid, kWalkThreads, 0, st>>>(ws);
-    } else {
-        if (cut) linear_walk3_kernel<T, DKA, DKB, false><<<grid, kWalkThreads, 0, st>>>(ws);
-        linear_walk3_kernel<T, DKA, DKB, true><<<grid, kWalkThreads, 0, st>>>(ws);
-    }
-    return cudaGetLastError();
+    if constexpr (DKA == DKB)
+        return run_pair(linear_walk_kernel<T, DKA, false, false>, linear_walk_kernel<T, DKA, true, true>, cut, grid, ws, st);
+    else
+        return run_pair(linear_walk3_kernel<T, DKA, DKB, false>, linear_walk3_kernel<T, DKA, DKB, true>, cut, grid, ws, st);
 }
 template <typename T, int DKA>
 cudaError_t run_walks_b(const Walks &ws, int DKB, int T_len, cudaStream_t st) {
@@ -539,6 +546,8 @@ __device__ __forceinline__ void fold_heads(const Fold &f, int which, long first,
 // What follows a gradient's walks, in one launch: the first CTAs take ddecay, the others the shared heads.
 template <typename T>
 __global__ void __launch_bounds__(kGradThreads) linear_tail_kernel(Dgate d, int pairs, Fold f) {
+    next_may_start();
+    wait_for_previous();
     if ((int)blockIdx.x < pairs) {
         sum_dgate(d, blockIdx.x);
         return;
@@ -549,17 +558,15 @@ __global__ void __launch_bounds__(kGradThreads) linear_tail_kernel(Dgate d, int 
 cudaError_t run_tail(const Dgate &d, int pairs, const Fold &f, DType dt, cudaStream_t st) {
     const long grid = pairs + 2 * std::min(2048L, (f.n + kGradThreads - 1) / kGradThreads);
     if (grid == 0) return cudaSuccess;
-    if (dt == DType::BF16)
-        linear_tail_kernel<__nv_bfloat16><<<(unsigned)grid, kGradThreads, 0, st>>>(d, pairs, f);
-    else
-        linear_tail_kernel<float><<<(unsigned)grid, kGradThreads, 0, st>>>(d, pairs, f);
-    return cudaGetLastError();
+    return launch_after(dt == DType::BF16 ? linear_tail_kernel<__nv_bfloat16> : linear_tail_kernel<float>, (unsigned)grid,
+                        kGradThreads, 0, st, d, pairs, f);
 }
 
 // dst[c] = sum over the rows of src[r, c]: one CTA per column, a fixed order, fp64 sums (a
 // fixed decay's gradient adds up every token of the batch).
 __global__ void __launch_bounds__(256) sum_rows_kernel(const float *src, float *dst, long rows, int cols) {
     __shared__ double s[256];
+    wait_for_previous();
     double d = 0.0;
     for (long r = threadIdx.x; r < rows; r += 256) d += src[r * cols + blockIdx.x];
     s[threadIdx.x] = d;
@@ -621,8 +628,7 @@ cudaError_t launch_fold_heads(const float *src0, const LinView &dst0, const floa
 }
 
 cudaError_t launch_sum_rows(const float *src, float *dst, long rows, int cols, cudaStream_t st) {
-    sum_rows_kernel<<<cols, 256, 0, st>>>(src, dst, rows, cols);
-    return cudaGetLastError();
+    return launch_after(sum_rows_kernel, cols, 256, 0, st, src, dst, rows, cols);
 }
 
 // Scratch of the gradients: [h_T][row dots of dq and dk][per-token ddecay when it is summed]

@@ -182,6 +182,7 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     // 1 us per 32 channels and earlier segment, all of it latency).
     const size_t pair = (size_t)it.n * w.HV + hv;
     if (warp < 16) {
+        wait_for_previous();
         const int i = tid & 127, cb = 32 * (warp >> 2);
         if (nch > 0 && cb < DK && (i & ~31) < DV) {
             float acc[32];
@@ -590,6 +591,7 @@ linear_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (w.clear && blockIdx.x == 0 && tid == 0) w.hdr->error = 0;
+    next_may_start();
     const int hv = blockIdx.x % w.HV, item = blockIdx.x / w.HV;
     LinItem it;
     if (!lin_item(w.s, w.L, item, it) || it.p == it.nseg - 1) return;   // nobody reads the last segment's
@@ -814,9 +816,11 @@ cudaError_t go(const LinFwd &a, const TcWalk &w, long items, bool split, const C
     if (split) {
         if ((e = local_once(linear_local_kernel<DK, DV>, LC::SMEM)) != cudaSuccess) return e;
         linear_local_kernel<DK, DV><<<grid, kLocalThreads, LC::SMEM, st>>>(mk, mv, first);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if ((e = walk_once(linear_chunk_kernel<DK, DV>, WC::SMEM)) != cudaSuccess) return e;
-    linear_chunk_kernel<DK, DV><<<grid, kWalkThreads, WC::SMEM, st>>>(mq, mk, mv, split ? w : first);
+    if (split) return launch_after(linear_chunk_kernel<DK, DV>, grid, kWalkThreads, WC::SMEM, st, mq, mk, mv, w);
+    linear_chunk_kernel<DK, DV><<<grid, kWalkThreads, WC::SMEM, st>>>(mq, mk, mv, first);
     return cudaGetLastError();
 }
 

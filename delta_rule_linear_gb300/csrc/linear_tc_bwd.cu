@@ -119,6 +119,7 @@ linear_part_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (w.clear && blockIdx.x == 0 && tid == 0) w.hdr->error = 0;
+    next_may_start();
     const int slots = w.pairs * w.nch, items = 2 * slots;
     const int mine = ((int)blockIdx.x < items) ? (items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
     if (tid == 0) {
@@ -249,6 +250,8 @@ linear_part_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
 // In place: a slot's contribution becomes the memory entering its chunk (S), or the gradient of the one
 // leaving it (R).  Bound by L2: eight slots' loads are in flight per thread.
 __global__ void __launch_bounds__(256) linear_chain_kernel(BwdParams w, int cells) {
+    next_may_start();
+    wait_for_previous();
     const int per = cells / 4, e = blockIdx.x * 256 + threadIdx.x;
     if (e >= per * w.pairs) return;
     const int pi = e / per, at = (e - pi * per) * 4;
@@ -318,6 +321,7 @@ linear_state_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (w.clear && blockIdx.x == 0 && tid == 0) w.hdr->error = 0;
+    next_may_start();
     const int part = blockIdx.x % KS, dir = blockIdx.x / KS % 2, pi = blockIdx.x / (2 * KS), nch = w.nch;
     const long pair = w.pair0 + pi;
     const int b = (int)(pair / w.HV), hv = (int)(pair % w.HV);
@@ -574,6 +578,7 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         return;
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    next_may_start();
     const int slots = w.pairs * w.nch;
     if (tid == 0) {
         mbar_init(&ctl->full_qk, 1);
@@ -746,6 +751,7 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                 xs[2 * p + 1] = ps[2 * (tid + 512 * p) + 1];
             }
         };
+        wait_for_previous();                     // S and R (the other warp loads the call's inputs)
         if ((int)blockIdx.x < slots) get_s(blockIdx.x);
         int it = 0;
         for (int slot = blockIdx.x; slot < slots; slot += gridDim.x, ++it) {
@@ -1014,13 +1020,16 @@ cudaError_t run_groups(const LinBwd &a, BwdParams w, const CUtensorMap &mq, cons
         const int slots = w.pairs * w.nch;
         if (walks(pairs, w.nch, DK, a.sms)) {
             linear_state_kernel<DK, DV><<<w.pairs * 2 * (DK / 64), kPartThreads, SC::SMEM, st>>>(mq, mk, mv, mo, w);
+            e = cudaGetLastError();
         } else {
             linear_part_kernel<DK, DV><<<std::min(2 * slots, a.sms), kPartThreads, PC::SMEM, st>>>(mq, mk, mv, mo, w);
             const dim3 grid((unsigned)(((long)w.pairs * (cells / 4) + 255) / 256), 2);
-            linear_chain_kernel<<<grid, 256, 0, st>>>(w, cells);
+            e = cudaGetLastError();
+            if (e == cudaSuccess) e = launch_after(linear_chain_kernel, grid, 256, 0, st, w, cells);
         }
-        linear_grad_kernel<DK, DV><<<std::min(slots, a.sms), kGradThreads, GC::SMEM, st>>>(mq, mk, mv, mo, w);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if (e == cudaSuccess)
+            e = launch_after(linear_grad_kernel<DK, DV>, std::min(slots, a.sms), kGradThreads, GC::SMEM, st, mq, mk, mv, mo, w);
+        if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "kda_internal.cuh"
+#include "launch_after.cuh"
 
 namespace kda {
 
