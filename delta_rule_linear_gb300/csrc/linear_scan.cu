@@ -546,7 +546,6 @@ __device__ __forceinline__ void fold_heads(const Fold &f, int which, long first,
 // What follows a gradient's walks, in one launch: the first CTAs take ddecay, the others the shared heads.
 template <typename T>
 __global__ void __launch_bounds__(kGradThreads) linear_tail_kernel(Dgate d, int pairs, Fold f) {
-    next_may_start();
     wait_for_previous();
     if ((int)blockIdx.x < pairs) {
         sum_dgate(d, blockIdx.x);

@@ -578,7 +578,6 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         return;
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    next_may_start();
     const int slots = w.pairs * w.nch;
     if (tid == 0) {
         mbar_init(&ctl->full_qk, 1);
