@@ -46,9 +46,11 @@ bool view(LinView &v, const void *p, const long long *strides, int i, long B, lo
 }
 
 // Whether the chunked tensor-core form takes this problem.  A chunk costs the same whatever it
-// holds, and the token walk of a chunk's first 32 tokens costs less than a chunk does.
+// holds; the token walk costs less for a few tokens.  Prefill on the device, walk and chunk: one sequence,
+// 4 heads of 64, 16 tokens 5.6 and 7.1 us, 32 tokens 7.5 and 7.1; 4 heads of 128, 16 tokens 8.5 and 8.9, 32 tokens
+// 11.2 and 8.9 (gradients 26 and 21, 29 and 21); 16 x 32 heads of 128 gain from 8 tokens on (76 and 33).
 bool use_tc(int dk, int dv, kda_dtype dt, int max_len) {
-    return linear_tc_supported(dk, dv, to_dtype(dt)) && max_len > 32;
+    return linear_tc_supported(dk, dv, to_dtype(dt)) && max_len > 16;
 }
 
 size_t fwd_scratch(int n, long total, int max_len, bool varlen, int HV, int dk, int dv, kda_dtype dt) {

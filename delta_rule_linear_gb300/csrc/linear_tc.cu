@@ -21,11 +21,13 @@
 // bits, leave 2.4e-6 in the memory), k is exact, and S accumulates in fp32.
 //
 // Bound: 2 (2 dk + 2 dv) bytes per token and head through HBM; per chunk of d = 128 that is 128 KB,
-// 5900 clocks of an SM's share at the measured 6.8 TB/s.  What the CTA itself is short of is shared-memory
-// bandwidth (a product with both operands there reads 8 KB per 16 of K) and instruction
-// fetch: so the two products that can take their A operand from TMEM do, and every role's loop is kept
-// to a few hundred instructions (fully unrolled, the roles evicted each other's code and the walk took
-// 1.5 times as long).
+// 5900 clocks of an SM's share at the measured 6.8 TB/s.  A chunk takes 6700 (8 x 4096 tokens, 19 heads: one CTA
+// per SM, 127 us, 5.0 TB/s), of d = 64 5100 (half the bytes).  What the CTA itself is short of is TMEM and
+// shared-memory bandwidth: beside the passes over values, memory and outputs a product's step of 16 takes 130 to
+// 230 clocks (64 alone), and the passes take longer beside the products; and instruction fetch.  So the two
+// products that can take their A operand from TMEM do, values are transposed by ldmatrix, products are issued from
+// one-lane branches, and every role's loop is kept to a few hundred instructions (fully unrolled, the roles
+// evicted each other's code and the walk took 1.5 times as long).
 //
 // Warps 0-3: scores -> P.  4-7: outputs.  8-11: the memory's operand copy and its decay.  12-19: Vw.
 // 20: decays and TMA.  21: issues the products.  The groups and the tensor pipe work on different
@@ -773,11 +775,12 @@ linear_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
 }
 
 // ------------------------------------------------------------------------------ host
-// Chunks per segment.  In units of one chunk of the walk (4.5 us at d = 128), a CTA costs about 3 to set up,
+// Chunks per segment.  In units of one chunk of the walk (3.6 us at d = 128, 2.6 at 64), a CTA costs about 3 to set up,
 // fill and drain, a chunk of the local kernel 0.5, its launch 1, a start state 0.2 per earlier segment; every
 // (sequence, head) that finds no SM waits for the next wave.  Equal lengths: the cut with the least of it, and
 // of cuts within 5 % the coarsest (a long segment's local memory stops early where decays are strong: B=1 T=32768
-// H=32 with softplus decays, 4 segments 0.35 ms, 9 segments 0.39 ms).  Packed sequences: whole ones while the
+// H=32 with softplus decays, 4 segments 0.31 ms, 9 segments 0.36 ms).  Of all cuts of nine shapes, 2048 to
+// 32,768 tokens, 1 to 128 heads, it picks the fastest or one within 2 %.  Packed sequences: whole ones while the
 // longest is no more than an SM's share of the work (taken longest first they then fill the SMs evenly),
 // else segments of half an SM's share.
 int plan_chunks(int nseq, int HV, long total, int max_len, bool varlen, int sms) {

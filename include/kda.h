@@ -457,7 +457,7 @@ kda_status kda_gk_chunk_bwd(const void *q, const void *k, const void *v,
  *   ws      at least the query's bytes, 16-byte aligned; a kernel's bounded wait that runs out
  *           is recorded in its header (kda_query_device_error).
  * bf16 with dk, dv in {64, 128} runs by chunks of 128 tokens on the tensor cores (sequences of
- * more than 32 tokens); everything else runs token by token on CUDA cores.  The results do not
+ * more than 16 tokens); everything else runs token by token on CUDA cores.  The results do not
  * depend on which beyond rounding: memories and their sums are fp32 in both.  In the chunked form
  * an infinite or NaN v or k reaches the outputs of its whole chunk.
  * B, N, T == 0 are allowed (final_state = initial_state, or zeros).
