@@ -5,7 +5,7 @@
 #include <atomic>
 
 #include "linear_internal.cuh"
-#include "tc_ptx.cuh"
+#include "linear_ptx.cuh"
 #include "tma_host.cuh"
 
 namespace kda {
