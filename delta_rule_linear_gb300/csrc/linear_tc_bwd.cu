@@ -119,7 +119,6 @@ linear_part_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (w.clear && blockIdx.x == 0 && tid == 0) w.hdr->error = 0;
-    next_may_start();
     const int slots = w.pairs * w.nch, items = 2 * slots;
     const int mine = ((int)blockIdx.x < items) ? (items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
     if (tid == 0) {
@@ -718,7 +717,6 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             return ok;
         };
         auto go = [&]() {
-            fence_proxy_async();
             tc_fence_before();
             mbar_arrive(&ctl->go);
         };
@@ -758,7 +756,7 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             const long pair = w.pair0 + pi;
             const int b = (int)(pair / w.HV), hv = (int)(pair % w.HV);
             const int live = w.T - u;            // tokens of the chunk (more: all 128)
-            // ---- S (loaded an item ahead), the decays
+            // ---- S (asked for at the end of the item before), the decays
             if (warp == 0) {
                 const float *gp = w.g.p ? w.g.p + b * w.g.b + hv : nullptr;
                 float4 x = load_decay(w.g, gp, u + 4 * lane, w.T);
@@ -788,6 +786,7 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             const float fq = strong ? 1.f : ae[row], fk = strong ? 1.f : aw[row];
             const float iq = w.scale * ex2(gr), ik = ex2(gc - gr);
             put_x(xs, strong ? 1.f : ex2(gc));
+            fence_proxy_async();                 // here, where the products are waited for (1500 clocks before `go`)
             if (!wt.warp(&ctl->full_qk, it & 1, 58) || !done(53)) break;   // Q and K are read here too
             // ---- P^T, M^T of this row j and its quarter of the i; M of this row i and its quarter of the j; sums of W
             float cs = 0.f, rs = 0.f;
@@ -891,10 +890,10 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             if (lane == 0) ctl->dot[warp] = dot;
             if (!done(54)) break;
             put_x(xr, 1.f);
-            if (slot + (int)gridDim.x < slots) get_s(slot + gridDim.x);
             const bool onk = 32 * part < DK, onv = 32 * part < DV;   // this warp's 32 columns exist
             if (strong && onk) scale_row(tl + R2 + 32 * part, iq);
             aq[row] = onk ? fq * dot_row(tl + R2 + 32 * part, smem + Cf::Q, row, 32 * part) : 0.f;
+            fence_proxy_async();                 // R's parts
             go();
             // ---- dQ out; first term of dK
             const int u0 = u + (row & ~3), rows = min(4, w.T - u0), l8 = 8 * (lane & 3);
@@ -927,8 +926,9 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             if (onv)
                 store_rows(tl + R1 + 32 * part, fk,
                            w.dv + b * w.vs[0] + (long long)u0 * w.vs[1] + hv * w.vs[2] + 32 * part + l8, w.vs[1], rows, lane);
-            tc_fence_before();
             go();
+            // the next item's S: 32 registers of it would not live through the calls above, which would wait for it
+            if (slot + (int)gridDim.x < slots) get_s(slot + gridDim.x);
             // ---- ddecay, while the next chunk's first products run (every warp's sums and dots came before `done`;
             // they are written again after the next meeting, which this warp joins when it is through)
             if (w.dg && warp == 0) {
