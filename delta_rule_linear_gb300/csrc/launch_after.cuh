@@ -9,11 +9,10 @@
 namespace kda {
 
 // In the kernel before (never a call's last one): from here on, once all of its CTAs have come here, the next
-// one's may be placed.  For
-// kernels whose CTAs fill the machine once (linear attention of 2 x 2048 tokens, 16 heads of 128: 38.5 -> 35.8 us, its
-// gradients 100.7 -> 97.7, the norms' 2 us less); before kernels of many small CTAs it loses, since those are
-// then placed unevenly (gradients of 8192 tokens: token walks, 4 heads of 64, fp32, 445 -> 499 us; chains, 16 heads of
-// 64, 117 -> 146 us), and the kernels before them leave it to their end.
+// one's may be placed.  For kernels whose CTAs fill the machine once (linear attention of 2 x 2048 tokens, 16
+// heads of 128: 38.5 -> 35.8 us, its gradients 100.7 -> 97.7, the norms' 2 us less).  Before kernels of many small
+// CTAs it loses, since those are then placed unevenly (gradients of 8192 tokens: token walks, 4 heads of 64, fp32,
+// 445 -> 499 us; chains, 16 heads of 64, 117 -> 146 us): the kernels before them leave it to their end.
 __device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 // In the kernel after: every kernel before it in the call has ended and its writes are visible.  At least one
 // thread of the grid has to come here even where it reads nothing of theirs, since what follows the call in the

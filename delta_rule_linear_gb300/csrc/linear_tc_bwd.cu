@@ -24,8 +24,9 @@
 //   the chunks, elementwise and in place.
 // A walk takes 1.4 to 2.1 us a chunk of d = 128 however many pairs fit the machine, the other way 0.11 us a
 // chunk and pair or, where a group has room for few pairs, the latency of the chains (costs in `walks` below).  All
-// gradients of 2 x 2048 tokens, 16 heads of 128: 101 us walked, 118 the other way; of 2048 tokens, 14 heads:
-// 63 and 55; of 2 x 2048 tokens, 16 heads of 64: 65 and 61; of 32,768 tokens, 16 heads of 128: 814 and 1280.
+// gradients of 2 x 2048 tokens, 16 heads of 128: 96 us walked, 112 the other way; of 2048 tokens, 14 heads:
+// 60 and 50; of 2 x 2048 tokens, 16 heads of 64: 63 and 57; of 32,768 tokens, 16 heads of 128: 815 and 1209.  Of 22
+// shapes the choice is the faster one or within 6 % of it.
 // The contributions of a group stay within L2, where the chains read them: 2 x 64 KB a chunk at d = 128 and
 // at most kGroupChunks chunks.  A walk's memories are read back once, and a wider group fills the machine: kWalkChunks
 // of them (32,768 tokens, 16 heads: 814 us, with half as many 1187).  A larger problem is taken group by
@@ -478,8 +479,8 @@ linear_state_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
 // over the first, M^T over the second, M over the fourth, every quarter's packed pairs in the lower half
 // of its own columns; dQ gathers in the third, dK in the fourth once M is used, dV in the second once
 // M^T is.  Loops are kept rolled and what is used three times out of line: the chunk's code runs once per
-// chunk, and instruction fetch is what a longer one waits for (8 warps and unrolled passes: 0.109 ms at
-// the training shape instead of 0.067).
+// chunk, and instruction fetch is what a longer one waits for (8 warps and unrolled passes: 0.109 ms with
+// 2 x 2048 tokens, 16 heads of 128, instead of 0.065).
 // The first terms of dQ and dK are read back before their second terms are added, for their dots with q and k
 // (S and R go in as two bf16 parts for those dots).  Row factors are left to the stores,
 //     dQ_i = E_i [dO (e^{G_C} S)^T + sum_j m_ij w_j k_j],   E_i = c e^{G_i - G_C},
