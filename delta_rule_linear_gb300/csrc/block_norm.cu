@@ -15,6 +15,11 @@
 // to a whole CTA; element e of a row is always held by the same thread, so the backward sums
 // of dw and dc stay in that thread's registers over all its rows and meet once at the end: per CTA
 // in shared memory, then over the CTAs by a second small kernel, in a fixed order (no atomics).
+//
+// Measured, bf16: gated norm of 32,768 x 32 rows of 128: 126 us, 6.4 TB/s; its gradient, 4096 x 16 rows of 128: 20 us
+// (84 MB, 12.4 us at the copy rate: some 45 instructions an element are the other bound); residual norm of 256
+// rows of 4096: 3.2 us; its gradient, 4096 rows of 2048, fp32 stream, learned scale: 32 us (151 MB, 22.3 us at the
+// copy rate; the two launches' ends are the rest).
 #include <algorithm>
 
 #include "norm_internal.cuh"
@@ -102,7 +107,14 @@ __device__ __forceinline__ float row_sum(float x, float *s) {
     return x;
 }
 
-__device__ __forceinline__ float sigmoid(float a) { return __fdividef(1.f, 1.f + __expf(-a)); }
+// 1 / (1 + 2^(-a log2 e)): approximate operations that flush what is below 2^-126 (a sigmoid of -88 or less), without
+// the scaling that keeps subnormals, which every element would pay for
+__device__ __forceinline__ float sigmoid(float a) {
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * a));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+    return s;
+}
 
 // act(a) and its derivative.  kind: 0 none, 1 silu, 2 sigmoid.
 __device__ __forceinline__ float act_of(float a, int kind) {
@@ -480,7 +492,7 @@ cudaError_t gated_go(const GatedNorm &a, bool bwd, cudaStream_t st) {
         gated_norm_fwd_kernel<T, V, L, NJ><<<(unsigned)std::min(blocks, 8L * a.sms), kThreads, 0, st>>>(a);
         return cudaGetLastError();
     }
-    // what its registers let an SM hold (8 of them, in two rounds, 24.1 us instead of 22.3 with 65,536 rows of 128)
+    // what its registers let an SM hold (8, in two rounds, cost 8 % more with 65,536 rows of 128)
     const int grid = (int)std::min(blocks, 4L * a.sms);
     gated_norm_bwd_kernel<T, V, L, NJ><<<grid, kThreads, 0, st>>>(a);
     if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
