@@ -277,3 +277,52 @@ def test_other_stream_and_repeat(kda):
         s.synchronize()
         assert torch.equal(o0, o1) and torch.equal(h0, h1)
         assert all(torch.equal(g0[x], g1[x]) for x in g0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("heads", [2, 24])
+def test_graph_replays_follow_their_inputs(kda, dtype, heads):
+    """A captured call and its gradients, replayed with other inputs, give those inputs' bits (shared heads, several
+    segments: every launch of a call is in the graph, one after another)."""
+    import torch
+    shape = (1, 700, heads, 2, 64, 128)
+    d, _ = _make(*shape, dtype, seed=21)
+    run = lambda x: (kda.linear_chunk_fwd(x["q"], x["k"], x["v"], x["decay"], x["h0"]),  # noqa: E731
+                     kda.linear_chunk_bwd(x["q"], x["k"], x["v"], x["decay"], x["h0"], x["d_o"], x["dhT"]))
+    run(d)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        (o, h), grads = run(d)
+    for seed in (22, 23):
+        n, _ = _make(*shape, dtype, seed=seed)
+        for x in n:
+            d[x].copy_(n[x])
+        g.replay()
+        (o1, h1), grads1 = run(n)
+        assert torch.equal(o, o1) and torch.equal(h, h1)
+        assert all(torch.equal(grads[x], grads1[x]) for x in grads1)
+
+
+def test_calls_back_to_back_do_not_overtake(kda):
+    """Calls that feed one another without a pause, each of several overlapping launches, as one after another."""
+    import torch
+    d, _ = _make(1, 600, 3, 1, 128, 128, "bf16", decay="mild", seed=24)
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+
+    def chain(pause):
+        v, h, out = d["v"], d["h0"], []
+        for _ in range(4):
+            o, h = kda.linear_chunk_fwd(d["q"], d["k"], v, d["decay"], h, workspace=ws)
+            pause()
+            g = kda.linear_chunk_bwd(d["q"], d["k"], v, d["decay"], h, o, h, workspace=ws)
+            pause()
+            v = (g["dv"].float() / g["dv"].float().abs().amax().clamp_min(1e-3)).bfloat16()
+            h = h / h.abs().amax()
+            out += [o, h, *g.values()]
+        return out
+
+    slow = chain(torch.cuda.synchronize)
+    for _ in range(3):
+        fast = chain(lambda: None)
+        assert all(torch.equal(a, b) for a, b in zip(slow, fast))
