@@ -7,6 +7,7 @@ call runs on.  q, k, v and the other token arrays may be views with any batch, t
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -16,6 +17,7 @@ _DT = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
 _ACT = {None: 0, "silu": 1, "sigmoid": 2}
 _F32 = torch.float32
 _empty = torch.empty
+_like = torch.empty_like      # of contiguous tensors: cheaper than naming shape, type and device
 # The calls below cost a few microseconds on the GPU for small inputs, so their checks are a handful of
 # comparisons; what fails one goes through _need, which finds the words.
 
@@ -83,13 +85,30 @@ def _ok(code, where, lib):
         raise KdaError(code, where, lib)
 
 
-def _ws(need, where, lib, device, workspace):
-    if workspace is None:
-        if need == 0:
-            raise KdaError(4, where, lib)
-        workspace = _empty(need, dtype=torch.uint8, device=device)
-        return workspace, need
-    return workspace, workspace.numel() * workspace.element_size()
+@functools.lru_cache(maxsize=1024)
+def _bytes(query, *sizes):
+    return getattr(load(), query)(*sizes)
+
+
+_HEADER = 256       # bytes of a workspace that is its header alone (the error word)
+_headers = {}
+
+
+def _ws(query, sizes, t, stream, workspace, asked=False):
+    """(workspace, its bytes) of a call on t's device.  A call that needs the header alone takes one that is kept per
+    stream, whose calls follow one another; where its error word is asked for, a fresh one."""
+    if workspace is not None:
+        return workspace, workspace.numel() * workspace.element_size()
+    need = _bytes(query, *sizes)
+    if need == 0:
+        raise KdaError(4, query, load())
+    if need > _HEADER or asked:
+        return _empty(need, dtype=torch.uint8, device=t.device), need
+    key = (t.get_device(), stream)
+    ws = _headers.get(key)
+    if ws is None:
+        ws = _headers[key] = _empty(_HEADER, dtype=torch.uint8, device=t.device)
+    return ws, _HEADER
 
 
 def _heads(H, HV):
@@ -138,18 +157,18 @@ def linear_chunk_fwd(q, k, v, decay=None, initial_state=None, *, scale=None, out
         _dense(initial_state, "initial_state", _F32, (B, HV, dk, dv))
     dev = q.device
     if out is None:
-        out = _empty((B, T, HV, dv), dtype=q.dtype, device=dev)
+        out = _like(v) if plain else _empty((B, T, HV, dv), dtype=q.dtype, device=dev)
     else:
         plain &= _view(out, "out", q.dtype, (B, T, HV, dv))
     if final_state is None:
         final_state = _empty((B, HV, dk, dv), dtype=_F32, device=dev)
     else:
         _dense(final_state, "final_state", _F32, (B, HV, dk, dv))
-    ws, n = _ws(lib.kda_linear_chunk_fwd_workspace(B, T, H, HV, dk, dv, dt), "kda_linear_chunk_fwd_workspace", lib, dev,
-                workspace)
+    st = _raw(q)
+    ws, n = _ws("kda_linear_chunk_fwd_workspace", (B, T, H, HV, dk, dv, dt), q, st, workspace, check_device)
     _ok(lib.kda_linear_chunk_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(decay), fixed, _ptr(initial_state),
                                  out.data_ptr(), final_state.data_ptr(), None if plain else _strides(q, k, v, out), B, T, H,
-                                 HV, dk, dv, dt, scale or 0.0, ws.data_ptr(), n, _raw(q)), "kda_linear_chunk_fwd", lib)
+                                 HV, dk, dv, dt, scale or 0.0, ws.data_ptr(), n, st), "kda_linear_chunk_fwd", lib)
     if check_device:
         _ok(query_device_error(ws), "kda_linear_chunk_fwd (device)", lib)
     return out, final_state
@@ -182,19 +201,19 @@ def linear_varlen_fwd(q, k, v, cu_seqlens, decay=None, initial_state=None, *, cu
             raise ValueError("cu_seqlens_cpu must be a host tensor of cu_seqlens' length")
     dev = q.device
     if out is None:
-        out = _empty((1, total, HV, dv), dtype=q.dtype, device=dev)
+        out = _like(v) if plain else _empty((1, total, HV, dv), dtype=q.dtype, device=dev)
     else:
         plain &= _view(out, "out", q.dtype, (1, total, HV, dv))
     if final_state is None:
         final_state = _empty((N, HV, dk, dv), dtype=_F32, device=dev)
     else:
         _dense(final_state, "final_state", _F32, (N, HV, dk, dv))
-    ws, n = _ws(lib.kda_linear_varlen_fwd_workspace(N, total, H, HV, dk, dv, dt), "kda_linear_varlen_fwd_workspace", lib,
-                dev, workspace)
+    st = _raw(q)
+    ws, n = _ws("kda_linear_varlen_fwd_workspace", (N, total, H, HV, dk, dv, dt), q, st, workspace, check_device)
     _ok(lib.kda_linear_varlen_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(decay), fixed, cu_seqlens.data_ptr(),
                                   _ptr(host), _ptr(initial_state), out.data_ptr(), final_state.data_ptr(),
                                   None if plain else _strides(q, k, v, out), N, total, H, HV, dk, dv, dt, scale or 0.0,
-                                  ws.data_ptr(), n, _raw(q)), "kda_linear_varlen_fwd", lib)
+                                  ws.data_ptr(), n, st), "kda_linear_varlen_fwd", lib)
     if check_device:
         _ok(query_device_error(ws), "kda_linear_varlen_fwd (device)", lib)
     return out, final_state
@@ -226,7 +245,7 @@ def linear_decode_step(q, k, v, decay, state, *, scale=None, out=None, stream=No
         else:
             _dense(decay, "decay", _F32, (B, 1, HV) if decay.dim() == 3 else (B, HV))
     if out is None:
-        out = _empty(vs, dtype=dtype, device=q.device)
+        out = _like(v) if plain else _empty(vs, dtype=dtype, device=q.device)
     else:
         plain &= _view(out, "out", dtype, vs)
     s = None
@@ -257,21 +276,24 @@ def linear_chunk_bwd(q, k, v, decay, initial_state, d_o, dfinal_state=None, *, s
     if dfinal_state is not None:
         _dense(dfinal_state, "dfinal_state", _F32, (B, HV, dk, dv))
     dev = q.device
-    dq = _empty((B, T, H, dk), dtype=dtype, device=dev)
-    dkk = _empty((B, T, H, dk), dtype=dtype, device=dev)
-    dvv = _empty((B, T, HV, dv), dtype=dtype, device=dev)
+    if plain:
+        dq, dkk, dvv = _like(q), _like(k), _like(v)
+    else:
+        dq = _empty((B, T, H, dk), dtype=dtype, device=dev)
+        dkk = _empty((B, T, H, dk), dtype=dtype, device=dev)
+        dvv = _empty((B, T, HV, dv), dtype=dtype, device=dev)
     out = dict(dq=dq, dk=dkk, dv=dvv)
     dg = dh0 = None
     if decay is not None:
-        dg = out["ddecay"] = _empty(decay.shape, dtype=_F32, device=dev)
+        dg = out["ddecay"] = _like(decay)
     if initial_state is not None:
-        dh0 = out["dh0"] = _empty((B, HV, dk, dv), dtype=_F32, device=dev)
-    ws, n = _ws(lib.kda_linear_chunk_bwd_workspace(B, T, H, HV, dk, dv, dt), "kda_linear_chunk_bwd_workspace", lib, dev,
-                workspace)
+        dh0 = out["dh0"] = _like(initial_state)
+    st = _raw(q)
+    ws, n = _ws("kda_linear_chunk_bwd_workspace", (B, T, H, HV, dk, dv, dt), q, st, workspace, check_device)
     _ok(lib.kda_linear_chunk_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(decay), fixed, _ptr(initial_state),
                                  d_o.data_ptr(), _ptr(dfinal_state), dq.data_ptr(), dkk.data_ptr(), dvv.data_ptr(),
                                  _ptr(dg), _ptr(dh0), None if plain else _strides(q, k, v, d_o, dq, dkk, dvv), B, T, H, HV,
-                                 dk, dv, dt, scale or 0.0, ws.data_ptr(), n, _raw(q)), "kda_linear_chunk_bwd", lib)
+                                 dk, dv, dt, scale or 0.0, ws.data_ptr(), n, st), "kda_linear_chunk_bwd", lib)
     if check_device:
         _ok(query_device_error(ws), "kda_linear_chunk_bwd (device)", lib)
     return out
@@ -311,7 +333,7 @@ def gated_norm_fwd(x, gate, weight, *, eps=1e-6, activation="silu", out=None, st
     lib = load()
     act, dt, H, D, N, plain = _norm_args(x, gate, weight, activation)
     if out is None:
-        out = _empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _like(x) if plain else _empty(x.shape, dtype=x.dtype, device=x.device)
     else:
         plain &= _view(out, "out", x.dtype, x.shape)
     s = None
@@ -330,20 +352,20 @@ def gated_norm_bwd(d_y, x, gate, weight, *, eps=1e-6, activation="silu", workspa
     lib = load()
     act, dt, H, D, N, plain = _norm_args(x, gate, weight, activation)
     plain &= _view(d_y, "d_y", x.dtype, x.shape)
-    dev = x.device
-    dx = _empty(x.shape, dtype=x.dtype, device=dev)
-    dw = _empty(D, dtype=_F32, device=dev)
+    dx = _like(x) if plain else _empty(x.shape, dtype=x.dtype, device=x.device)
+    dw = _like(weight)
     out = dict(dx=dx, dw=dw)
     dg = None
     if gate is not None:
-        dg = out["dgate"] = _empty(x.shape, dtype=x.dtype, device=dev)
-    ws, n = _ws(lib.kda_gated_norm_bwd_workspace(D), "kda_gated_norm_bwd_workspace", lib, dev, workspace)
+        dg = out["dgate"] = _like(dx)
+    st = _raw(x)
+    ws, n = _ws("kda_gated_norm_bwd_workspace", (D,), x, st, workspace)
     s = None
     if not plain:
         s = (ctypes.c_longlong * 10)(*_token_strides(x), *_token_strides(gate if gate is not None else x),
                                      *_token_strides(d_y), H * D, D, H * D, D)
     _ok(lib.kda_gated_norm_bwd(d_y.data_ptr(), x.data_ptr(), _ptr(gate), weight.data_ptr(), dx.data_ptr(), _ptr(dg),
-                               dw.data_ptr(), s, N, H, D, dt, act, eps, ws.data_ptr(), n, _raw(x)),
+                               dw.data_ptr(), s, N, H, D, dt, act, eps, ws.data_ptr(), n, st),
         "kda_gated_norm_bwd", lib)
     return out
 
@@ -377,17 +399,15 @@ def residual_norm_fwd(x, y, weight, *, scale=1.0, eps=1e-6, out=None, out_norm=N
     shape = x.shape
     D = shape[-1]
     res, dt = _code(x, "x"), _code(y, "y")
-    _view(x, "x", x.dtype, shape)
-    _view(y, "y", y.dtype, shape)
+    x_dense, y_dense = _view(x, "x", x.dtype, shape), _view(y, "y", y.dtype, shape)
     _dense(weight, "weight", _F32, (D,))
     cv, c = _scale(scale, D)
-    dev = x.device
     if out is None:
-        out = _empty(shape, dtype=x.dtype, device=dev)
+        out = _like(x) if x_dense else _empty(shape, dtype=x.dtype, device=x.device)
     else:
         _dense(out, "out", x.dtype, shape)
     if out_norm is None:
-        out_norm = _empty(shape, dtype=y.dtype, device=dev)
+        out_norm = _like(y) if y_dense else _empty(shape, dtype=y.dtype, device=x.device)
     else:
         _dense(out_norm, "out_norm", y.dtype, shape)
     _ok(lib.kda_residual_norm_fwd(x.data_ptr(), y.data_ptr(), weight.data_ptr(), cv, c, out.data_ptr(), out_norm.data_ptr(),
@@ -412,17 +432,15 @@ def residual_norm_bwd(d_n, d_x, x, weight, y=None, *, scale=1.0, eps=1e-6, works
     if d_x is not None:
         _dense(d_x, "d_x", x.dtype, shape)
     cv, c = _scale(scale, D)
-    dev = x.device
-    dx = _empty(shape, dtype=x.dtype, device=dev)
-    dy = _empty(shape, dtype=d_n.dtype, device=dev)
-    dw = _empty(D, dtype=_F32, device=dev)
+    dx, dy, dw = _like(x), _like(d_n), _like(weight)
     out = dict(dx=dx, dy=dy, dw=dw)
     ds = None
     if y is not None:
         _dense(y, "y", d_n.dtype, shape)
-        ds = out["dscale"] = _empty(D, dtype=_F32, device=dev)
-    ws, n = _ws(lib.kda_residual_norm_bwd_workspace(D), "kda_residual_norm_bwd_workspace", lib, dev, workspace)
+        ds = out["dscale"] = _like(weight)
+    st = _raw(x)
+    ws, n = _ws("kda_residual_norm_bwd_workspace", (D,), x, st, workspace)
     _ok(lib.kda_residual_norm_bwd(d_n.data_ptr(), _ptr(d_x), x.data_ptr(), _ptr(y), weight.data_ptr(), cv, c, dx.data_ptr(),
                                   dy.data_ptr(), dw.data_ptr(), _ptr(ds), x.numel() // max(1, D), D, res, dt, eps,
-                                  ws.data_ptr(), n, _raw(x)), "kda_residual_norm_bwd", lib)
+                                  ws.data_ptr(), n, st), "kda_residual_norm_bwd", lib)
     return out
