@@ -16,7 +16,7 @@
 // of dw and dc stay in that thread's registers over all its rows and meet once at the end: per CTA
 // in shared memory, then over the CTAs by a second small kernel, in a fixed order (no atomics).
 //
-// Measured, bf16: gated norm of 32,768 x 32 rows of 128: 126 us, 6.4 TB/s; its gradient, 4096 x 16 rows of 128: 20 us
+// Measured, bf16: gated norm of 32,768 x 32 rows of 128: 123 us, 6.6 TB/s; its gradient, 4096 x 16 rows of 128: 19 us
 // (84 MB, 12.4 us at the copy rate: some 45 instructions an element are the other bound); residual norm of 256
 // rows of 4096: 3.2 us; its gradient, 4096 rows of 2048, fp32 stream, learned scale: 32 us (151 MB, 22.3 us at the
 // copy rate; the two launches' ends are the rest).
@@ -198,7 +198,8 @@ __global__ void __launch_bounds__(kThreads) gated_norm_fwd_kernel(GatedNorm a) {
     }
 }
 
-template <typename T, int V, int L, int NJ>
+// ACT, the gate's function, is a constant here: selecting it per element cost 6 % (65,536 rows of 128: 20.2 us).
+template <typename T, int V, int L, int NJ, int ACT>
 __global__ void __launch_bounds__(kThreads) gated_norm_bwd_kernel(GatedNorm a) {
     constexpr int RPB = kThreads / L;
     __shared__ float s_dw[RPB][L * V + 1];
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) gated_norm_bwd_kernel(GatedNorm a) {
             if (live && e < a.D) {
                 ax[j] = Pk::get(xp + e);
                 ad[j] = Pk::get(dyp + e);
-                if (a.act) ag[j] = Pk::get(gp + e);
+                if (ACT) ag[j] = Pk::get(gp + e);
             }
         }
     };
@@ -249,9 +250,9 @@ __global__ void __launch_bounds__(kThreads) gated_norm_bwd_kernel(GatedNorm a) {
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                sg[j][i] = a.act ? sigmoid(g[j][i]) : 1.f;
+                sg[j][i] = ACT ? sigmoid(g[j][i]) : 1.f;
                 ss = fmaf(x[j][i], x[j][i], ss);
-                const float ac = a.act == 1 ? g[j][i] * sg[j][i] : sg[j][i];
+                const float ac = ACT == 1 ? g[j][i] * sg[j][i] : sg[j][i];
                 dot = fmaf(dy[j][i] * ac * w[j][i], x[j][i], dot);
             }
         ss = row_sum<L>(ss, nullptr);
@@ -264,14 +265,14 @@ __global__ void __launch_bounds__(kThreads) gated_norm_bwd_kernel(GatedNorm a) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float s = sg[j][i], xn = x[j][i] * r, d = dy[j][i];
-                const float ac = a.act == 1 ? g[j][i] * s : s;
-                const float da = a.act == 1 ? fmaf(ac, 1.f - s, s) : s * (1.f - s);
+                const float ac = ACT == 1 ? g[j][i] * s : s;
+                const float da = ACT == 1 ? fmaf(ac, 1.f - s, s) : s * (1.f - s);
                 dw[j][i] = fmaf(d * ac, xn, dw[j][i]);
                 g[j][i] = d * xn * w[j][i] * da;
                 x[j][i] = r * norm_back(d * ac * w[j][i], x[j][i], ss, dot, r2, a.eps, a.inv_d);
             }
             Pack<T, V>::store(static_cast<T *>(a.dx.p) + row_at(a.dx, rr, a.H, a.D, a.flat) + e, x[j]);
-            if (a.act) Pack<T, V>::store(static_cast<T *>(a.dg.p) + row_at(a.dg, rr, a.H, a.D, a.flat) + e, g[j]);
+            if (ACT) Pack<T, V>::store(static_cast<T *>(a.dg.p) + row_at(a.dg, rr, a.H, a.D, a.flat) + e, g[j]);
         }
     }
     // this CTA's share of dw, row groups in order
@@ -494,7 +495,12 @@ cudaError_t gated_go(const GatedNorm &a, bool bwd, cudaStream_t st) {
     }
     // what its registers let an SM hold (8, in two rounds, cost 8 % more with 65,536 rows of 128)
     const int grid = (int)std::min(blocks, 4L * a.sms);
-    gated_norm_bwd_kernel<T, V, L, NJ><<<grid, kThreads, 0, st>>>(a);
+    if (a.act == 0)
+        gated_norm_bwd_kernel<T, V, L, NJ, 0><<<grid, kThreads, 0, st>>>(a);
+    else if (a.act == 1)
+        gated_norm_bwd_kernel<T, V, L, NJ, 1><<<grid, kThreads, 0, st>>>(a);
+    else
+        gated_norm_bwd_kernel<T, V, L, NJ, 2><<<grid, kThreads, 0, st>>>(a);
     if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     return norm_fold(a.part, grid, a.D, a.dw, nullptr, st);
 }
