@@ -494,7 +494,9 @@ kda_status kda_linear_decode_step(const void *q, const void *k, const void *v, c
  * summed over its value heads in fp32), ddecay float32 ([B,T,HV]; with decay_fixed [HV], summed over
  * all tokens; NULL allowed; not written when decay is NULL) and dinitial_state float32 (NULL
  * allowed).  strides: NULL or twenty-one element strides (batch, token, head) of q, k, v, d_o, dq,
- * dk, dv, with the rules above.
+ * dk, dv, with the rules above.  The chunked form's workspace holds the memories of up to 4864 chunks
+ * of 128 tokens and their gradients, 8 dk dv bytes each (0.64 GB at 128 x 128; one sequence's, where
+ * that alone is more); a larger problem goes through it in parts.
  */
 size_t kda_linear_chunk_bwd_workspace(int B, int T, int H, int HV, int dk, int dv, kda_dtype dtype);
 kda_status kda_linear_chunk_bwd(const void *q, const void *k, const void *v, const float *decay,
