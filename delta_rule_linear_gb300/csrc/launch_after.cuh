@@ -9,7 +9,10 @@
 namespace kda {
 
 // In the kernel before (never a call's last one): from here on, once all of its CTAs have come here, the next
-// one's may be placed.  For kernels whose CTAs fill the machine once (linear attention of 2 x 2048 tokens, 16
+// one's may be placed.  A kernel that takes TMEM calls it behind the barrier that follows its allocation: a CTA of
+// the next one on the same SM could otherwise take the columns first and wait for this kernel, which waits for them
+// (an allocation has no limit); only the two kernels' registers and shared memory would keep that from happening.
+// For kernels whose CTAs fill the machine once (linear attention of 2 x 2048 tokens, 16
 // heads of 128: 38.5 -> 35.8 us, its gradients 100.7 -> 97.7, the norms' 2 us less).  Before kernels of many small
 // CTAs it loses, since those are then placed unevenly (gradients of 8192 tokens: token walks, 4 heads of 64, fp32,
 // 445 -> 499 us; chains, 16 heads of 64, 117 -> 146 us): the kernels before them leave it to their end.

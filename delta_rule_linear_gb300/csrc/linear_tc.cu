@@ -593,7 +593,6 @@ linear_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (w.clear && blockIdx.x == 0 && tid == 0) w.hdr->error = 0;
-    next_may_start();
     const int hv = blockIdx.x % w.HV, item = blockIdx.x / w.HV;
     LinItem it;
     if (!lin_item(w.s, w.L, item, it) || it.p == it.nseg - 1) return;   // nobody reads the last segment's
@@ -620,6 +619,7 @@ linear_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
+    next_may_start();                       // the TMEM is this CTA's by now (one that returned above has its say too)
     tc_fence_after();
     const uint32_t tm = ctl->tmem;
     const Waits wt{&ctl->fail, w.hdr};

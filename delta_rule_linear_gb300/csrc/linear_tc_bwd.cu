@@ -321,7 +321,6 @@ linear_state_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (w.clear && blockIdx.x == 0 && tid == 0) w.hdr->error = 0;
-    next_may_start();
     const int part = blockIdx.x % KS, dir = blockIdx.x / KS % 2, pi = blockIdx.x / (2 * KS), nch = w.nch;
     const long pair = w.pair0 + pi;
     const int b = (int)(pair / w.HV), hv = (int)(pair % w.HV);
@@ -346,6 +345,7 @@ linear_state_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
+    next_may_start();                           // the TMEM is this CTA's by now
     tc_fence_after();
     const uint32_t tm = ctl->tmem;
     const Waits wt{&ctl->fail, w.hdr};
