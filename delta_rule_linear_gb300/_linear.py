@@ -299,15 +299,26 @@ def linear_chunk_bwd(q, k, v, decay, initial_state, d_o, dfinal_state=None, *, s
     return out
 
 
+def _step(t, lead, what, none):
+    """The stride from one place of the first ``lead`` dimensions to the next, in order (``none``: there is one place
+    or none).  Dimensions of size 1 are left out: their strides say nothing."""
+    step = span = None
+    for i in range(lead - 1, -1, -1):
+        n, s = t.shape[i], t.stride(i)
+        if n == 1:
+            continue
+        if step is None:
+            step = s
+        elif s != span:
+            raise ValueError(f"the leading dimensions must step evenly (one stride from {what} to {what})")
+        span = s * n
+    return none if step is None else step
+
+
 def _token_strides(t):
     """(token, head) strides of [..., H, D] whose leading dimensions step evenly."""
-    lead = t.dim() - 2
-    if lead == 0:
-        return 0, t.stride(-2)
-    for i in range(lead - 1):
-        if t.shape[i] > 1 and t.stride(i) != t.stride(i + 1) * t.shape[i + 1]:
-            raise ValueError("the leading dimensions must step evenly (one stride from token to token)")
-    return t.stride(lead - 1), t.stride(-2)
+    H, D = t.shape[-2:]
+    return _step(t, t.dim() - 2, "token", H * D), t.stride(-2) if H > 1 else D
 
 
 def _norm_args(x, gate, weight, activation):
@@ -372,13 +383,7 @@ def gated_norm_bwd(d_y, x, gate, weight, *, eps=1e-6, activation="silu", workspa
 
 def _rows(t, D):
     """Row stride of [..., D] whose leading dimensions step evenly."""
-    if t.is_contiguous():
-        return D
-    lead = t.dim() - 1
-    for i in range(lead - 1):
-        if t.shape[i] > 1 and t.stride(i) != t.stride(i + 1) * t.shape[i + 1]:
-            raise ValueError("the leading dimensions must step evenly (one stride from row to row)")
-    return t.stride(lead - 1) if lead else D
+    return D if t.is_contiguous() else _step(t, t.dim() - 1, "row", D)
 
 
 def _scale(scale, D):

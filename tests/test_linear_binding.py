@@ -1,0 +1,58 @@
+"""The binding of linear attention and the block norms on the host: which rows a view's strides name, and what is refused
+before a launch (the library and the device of the tensors are stood in for: nothing is launched)."""
+import itertools
+
+import pytest
+import torch
+
+import delta_rule_linear_gb300 as kda
+from delta_rule_linear_gb300 import _linear
+
+
+# ------------------------------------------------------------------------------ strides
+def _views():
+    """Views whose leading dimensions may be of size 1 and may be slices, named by how they are made."""
+    for sizes in itertools.product((1, 2, 3), repeat=3):
+        for cut in range(4):
+            for axis in range(3):
+                big = [s + (2 if cut & 1 and i == axis else 0) for i, s in enumerate(sizes)]
+                x = torch.empty(*big, 2, 8 if cut & 2 else 5)
+                yield f"{sizes} {axis} {cut}", x.narrow(axis, 1 if cut & 1 else 0, sizes[axis])[..., :5]
+    x = torch.empty(4, 6, 2, 5)
+    yield "last token", x[:, -1:]
+    yield "one request", x[:1, 1:4]
+    yield "heads first", x.transpose(1, 2)
+    yield "every other", x[::2, ::2]
+    yield "broadcast", torch.empty(1, 1, 2, 5).expand(3, 4, 2, 5)
+    yield "two rows", torch.empty(2, 1, 8, 2, 8)[:, :, :5, :, :5]
+
+
+def _offsets(t, lead):
+    """Offsets of the places of the first `lead` dimensions, in order."""
+    return [sum(i * s for i, s in zip(at, t.stride())) for at in itertools.product(*(range(n) for n in t.shape[:lead]))]
+
+
+def _even(offs):
+    return all(o == i * (offs[1] if len(offs) > 1 else 0) for i, o in enumerate(offs))
+
+
+@pytest.mark.parametrize("name,t", list(_views()), ids=lambda x: x if isinstance(x, str) else "")
+def test_one_stride_reaches_every_row_or_the_view_is_refused(name, t):
+    """Rows [..., D] and tokens [..., H, D]: row i lies at i times the stride, or no stride says where."""
+    rows = t.flatten(-2) if t.is_contiguous() else t[..., 0, :]
+    for x, lead, get in ((rows, rows.dim() - 1, lambda x: _linear._rows(x, x.shape[-1])),
+                         (t, t.dim() - 2, lambda x: _linear._token_strides(x)[0])):
+        offs = _offsets(x, lead)
+        if _even(offs):
+            step = get(x)
+            assert offs == [i * step for i in range(len(offs))]
+        else:
+            with pytest.raises(ValueError, match="step evenly"):
+                get(x)
+
+
+def test_the_head_stride_of_one_head_is_its_width():
+    """One head: no other head is looked for, and an odd stride must not cost the wide loads."""
+    t = torch.empty(7, 3, 64)[:, :1].transpose(0, 1)[:, :1]
+    assert t.shape == (1, 1, 64) and _linear._token_strides(torch.empty(5, 9, 64)[:, 3:4])[1] == 64
+    assert _linear._token_strides(t)[1] == 64
