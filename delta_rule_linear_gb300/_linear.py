@@ -14,7 +14,7 @@ import torch
 from ._lib import KDA_BF16, KDA_F32, KdaError, load, query_device_error
 
 _DT = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
-_ACT = {None: 0, "silu": 1, "sigmoid": 2}
+_ACT = {"silu": 1, "sigmoid": 2}
 _F32 = torch.float32
 _empty = torch.empty
 _like = torch.empty_like      # of contiguous tensors: cheaper than naming shape, type and device
@@ -322,9 +322,9 @@ def _token_strides(t):
 
 
 def _norm_args(x, gate, weight, activation):
-    act = _ACT.get(activation if gate is not None else None)
+    act = 0 if gate is None else _ACT.get(activation)
     if act is None:
-        raise ValueError("activation must be 'silu' or 'sigmoid'")
+        raise ValueError("a gate's activation must be 'silu' or 'sigmoid'")
     if x.dim() < 2:
         raise ValueError("x must be [..., H, D]")
     H, D = x.shape[-2:]
@@ -338,7 +338,7 @@ def _norm_args(x, gate, weight, activation):
 
 def gated_norm_fwd(x, gate, weight, *, eps=1e-6, activation="silu", out=None, stream=None):
     """kda_gated_norm_fwd: y = x (mean(x^2) + eps)^(-1/2) weight act(gate) over the last dimension.
-    x, gate [..., H, D] (gate None: no gate), weight [D] fp32, activation "silu" or "sigmoid"."""
+    x, gate [..., H, D] (gate None: no gate, whatever the activation), weight [D] fp32, activation "silu" or "sigmoid"."""
     if stream is not None:
         return _on(stream, gated_norm_fwd, x, gate, weight, eps=eps, activation=activation, out=out)
     lib = load()

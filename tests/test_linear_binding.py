@@ -56,3 +56,14 @@ def test_the_head_stride_of_one_head_is_its_width():
     t = torch.empty(7, 3, 64)[:, :1].transpose(0, 1)[:, :1]
     assert t.shape == (1, 1, 64) and _linear._token_strides(torch.empty(5, 9, 64)[:, 3:4])[1] == 64
     assert _linear._token_strides(t)[1] == 64
+
+
+# ------------------------------------------------------------------------------ refusals
+@pytest.mark.parametrize("activation", [None, "tanh", "SiLU", 1])
+def test_a_gate_needs_one_of_the_two_activations(activation):
+    """Without one the kernels would take no gate: the forward would drop it, and its gradient would never be written."""
+    x, w = torch.zeros(2, 3, 8), torch.ones(8)
+    for call in (lambda: kda.gated_norm_fwd(x, x, w, activation=activation),
+                 lambda: kda.gated_norm_bwd(x, x, x, w, activation=activation)):
+        with pytest.raises(ValueError, match="activation"):
+            call()
