@@ -169,7 +169,7 @@ def linear_chunk_fwd(q, k, v, decay=None, initial_state=None, *, scale=None, out
     _ok(lib.kda_linear_chunk_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(decay), fixed, _ptr(initial_state),
                                  out.data_ptr(), final_state.data_ptr(), None if plain else _strides(q, k, v, out), B, T, H,
                                  HV, dk, dv, dt, scale or 0.0, ws.data_ptr(), n, st), "kda_linear_chunk_fwd", lib)
-    if check_device:
+    if check_device and B:        # an empty batch launches nothing and leaves the header as it is
         _ok(query_device_error(ws), "kda_linear_chunk_fwd (device)", lib)
     return out, final_state
 
@@ -214,7 +214,7 @@ def linear_varlen_fwd(q, k, v, cu_seqlens, decay=None, initial_state=None, *, cu
                                   _ptr(host), _ptr(initial_state), out.data_ptr(), final_state.data_ptr(),
                                   None if plain else _strides(q, k, v, out), N, total, H, HV, dk, dv, dt, scale or 0.0,
                                   ws.data_ptr(), n, st), "kda_linear_varlen_fwd", lib)
-    if check_device:
+    if check_device and N:        # an empty batch launches nothing and leaves the header as it is
         _ok(query_device_error(ws), "kda_linear_varlen_fwd (device)", lib)
     return out, final_state
 
@@ -294,7 +294,7 @@ def linear_chunk_bwd(q, k, v, decay, initial_state, d_o, dfinal_state=None, *, s
                                  d_o.data_ptr(), _ptr(dfinal_state), dq.data_ptr(), dkk.data_ptr(), dvv.data_ptr(),
                                  _ptr(dg), _ptr(dh0), None if plain else _strides(q, k, v, d_o, dq, dkk, dvv), B, T, H, HV,
                                  dk, dv, dt, scale or 0.0, ws.data_ptr(), n, st), "kda_linear_chunk_bwd", lib)
-    if check_device:
+    if check_device and B:        # an empty batch launches nothing and leaves the header as it is
         _ok(query_device_error(ws), "kda_linear_chunk_bwd (device)", lib)
     return out
 

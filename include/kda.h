@@ -460,7 +460,8 @@ kda_status kda_gk_chunk_bwd(const void *q, const void *k, const void *v,
  * more than 16 tokens); everything else runs token by token on CUDA cores.  The results do not
  * depend on which beyond rounding: memories and their sums are fp32 in both.  In the chunked form
  * an infinite or NaN v or k reaches the outputs of its whole chunk.
- * B, N, T == 0 are allowed (final_state = initial_state, or zeros).
+ * B, N, T == 0 are allowed (final_state = initial_state, or zeros).  Without a sequence (B or N == 0)
+ * nothing is touched, the workspace's header included: there is no error word to ask for.
  */
 size_t kda_linear_chunk_fwd_workspace(int B, int T, int H, int HV, int dk, int dv, kda_dtype dtype);
 kda_status kda_linear_chunk_fwd(const void *q, const void *k, const void *v, const float *decay,

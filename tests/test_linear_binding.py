@@ -1,5 +1,5 @@
-"""The binding of linear attention and the block norms on the host: which rows a view's strides name, and what is refused
-before a launch (the library and the device of the tensors are stood in for: nothing is launched)."""
+"""The binding of linear attention and the block norms on the host: which rows a view's strides name, what is refused
+before a launch and what is asked after it (the library and the tensors' device are stood in for: nothing is launched)."""
 import itertools
 
 import pytest
@@ -67,3 +67,66 @@ def test_a_gate_needs_one_of_the_two_activations(activation):
                  lambda: kda.gated_norm_bwd(x, x, x, w, activation=activation)):
         with pytest.raises(ValueError, match="activation"):
             call()
+
+
+# ------------------------------------------------------------------------------ calls of a library that is stood in for
+class _Cuda(torch.Tensor):
+    """Host memory that calls itself a CUDA tensor of device ``index``."""
+    index = 0
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return self.index
+
+
+def _on_device(t, index=0):
+    t = t.as_subclass(_Cuda)
+    t.index = index
+    return t
+
+
+class _Lib:
+    """Every call succeeds and is counted; the error word of every workspace says that a wait ran out."""
+
+    def __init__(self):
+        self.launched = []
+
+    def __getattr__(self, name):
+        if name.endswith("_workspace"):
+            return lambda *a: 512
+        if name == "kda_status_string":
+            return lambda code: b"status"
+
+        def call(*a):
+            self.launched.append(name)
+            return 0
+        return call
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    lib = _Lib()
+    _linear._bytes.cache_clear()
+    monkeypatch.setattr(_linear, "load", lambda: lib)
+    monkeypatch.setattr(_linear, "_raw", lambda t: 0)
+    monkeypatch.setattr(_linear, "query_device_error", lambda ws: 8)
+    yield lib
+    _linear._bytes.cache_clear()
+
+
+def _zeros(*s, dtype=torch.float32, index=0):
+    return _on_device(torch.zeros(*s, dtype=dtype), index)
+
+
+def test_an_empty_batch_has_no_error_word(lib):
+    """No kernel runs and none clears the header, so what a fresh workspace holds must not be read as an error."""
+    x, cu = _zeros(0, 4, 1, 32), _zeros(1, dtype=torch.int32)
+    p = _zeros(1, 0, 1, 32)
+    for call in (lambda x: kda.linear_chunk_fwd(x, x, x, check_device=True),
+                 lambda x: kda.linear_chunk_bwd(x, x, x, None, None, x, check_device=True)):
+        call(x)
+        with pytest.raises(kda.KdaError):          # with sequences, the word is asked for
+            call(_zeros(2, 4, 1, 32))
+    kda.linear_varlen_fwd(p, p, p, cu, check_device=True)
+    with pytest.raises(kda.KdaError):
+        kda.linear_varlen_fwd(p, p, p, _zeros(3, dtype=torch.int32), check_device=True)
