@@ -1,7 +1,7 @@
 """Binding of linear attention with a decay per head and of the block norms (include/kda.h).
 
 Argument marshalling only, as ``_lib``: outputs and workspaces are torch tensors of the stream the
-call runs on.  q, k, v and the other token arrays may be views with any batch, token and head strides
+call runs on, and the tensors of a call are all on the current device.  q, k, v and the other token arrays may be views with any batch, token and head strides
 (16-byte multiples, last dimension contiguous), e.g. slices of one projection's output.
 """
 from __future__ import annotations
@@ -29,10 +29,12 @@ def _code(t, what="q/k/v"):
     return c
 
 
-def _need(t, name, dtype, shape, dense=True):
-    """Refuses a tensor that the call cannot take (dense: contiguous; else a strided view)."""
+def _need(t, name, dtype, shape, dev, dense=True):
+    """Refuses a tensor that the call on device `dev` cannot take (dense: contiguous; else a strided view)."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on CUDA device {t.get_device()}, the call's other tensors on device {dev}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -44,17 +46,32 @@ def _need(t, name, dtype, shape, dense=True):
         raise ValueError(f"{name}'s last dimension must be contiguous")
 
 
-def _view(t, name, dtype, shape):
+def _view(t, name, dtype, shape, dev):
     """Checks a strided view; True when it is contiguous."""
-    if t.is_contiguous() and t.dtype is dtype and t.is_cuda and t.shape == shape:
+    if t.is_contiguous() and t.dtype is dtype and t.get_device() == dev and t.shape == shape:
         return True
-    _need(t, name, dtype, shape, False)
+    _need(t, name, dtype, shape, dev, False)
     return t.is_contiguous()
 
 
-def _dense(t, name, dtype, shape):
-    if not (t.is_contiguous() and t.dtype is dtype and t.is_cuda and t.shape == shape):
-        _need(t, name, dtype, shape)
+def _dense(t, name, dtype, shape, dev):
+    if not (t.is_contiguous() and t.dtype is dtype and t.get_device() == dev and t.shape == shape):
+        _need(t, name, dtype, shape, dev)
+
+
+# The current device, on which a call launches; the short way where this torch has it.
+_here = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _device(t, name):
+    """The device of a call, named by its first tensor: the kernels run on the current one, so it has to be that."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev, here = t.get_device(), _here()
+    if dev != here:
+        raise ValueError(f"{name} is on CUDA device {dev}, but the current device is {here}: make the call under "
+                         f"torch.cuda.device({dev})")
+    return dev
 
 
 def _strides(*ts):
@@ -70,8 +87,8 @@ def _ptr(t):
 _current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _raw(t):
-    return _current(t.get_device()) if _current is not None else torch.cuda.current_stream().cuda_stream
+def _raw(dev):
+    return _current(dev) if _current is not None else torch.cuda.current_stream().cuda_stream
 
 
 def _on(stream, call, *args, **kw):
@@ -116,23 +133,24 @@ def _heads(H, HV):
         raise ValueError(f"the value heads ({HV}) must be a multiple of the q/k heads ({H})")
 
 
-def _decay(decay, shape):
+def _decay(decay, shape, dev):
     """1 for a fixed decay per head ([HV]), 0 for one per token and head (or none)."""
     if decay is None:
         return 0
     if decay.dim() == 1:
-        _dense(decay, "decay", _F32, shape[-1:])
+        _dense(decay, "decay", _F32, shape[-1:], dev)
         return 1
-    _dense(decay, "decay", _F32, shape)
+    _dense(decay, "decay", _F32, shape, dev)
     return 0
 
 
-def _qkv(q, k, v, B, T, H, HV, dk, dv):
+def _qkv(q, k, v, B, T, H, HV, dk, dv, dev):
     """Checks q, k and v; True when all are contiguous."""
     if HV != H:
         _heads(H, HV)
     dt = q.dtype
-    return _view(q, "q", dt, q.shape) & _view(k, "k", dt, (B, T, H, dk)) & _view(v, "v", dt, (B, T, HV, dv))
+    return (_view(q, "q", dt, q.shape, dev) & _view(k, "k", dt, (B, T, H, dk), dev) &
+            _view(v, "v", dt, (B, T, HV, dv), dev))
 
 
 def linear_chunk_fwd(q, k, v, decay=None, initial_state=None, *, scale=None, out=None, final_state=None,
@@ -150,21 +168,20 @@ def linear_chunk_fwd(q, k, v, decay=None, initial_state=None, *, scale=None, out
     lib = load()
     B, T, H, dk = q.shape
     HV, dv = v.shape[-2:]
-    dt = _code(q)
-    plain = _qkv(q, k, v, B, T, H, HV, dk, dv)
-    fixed = _decay(decay, (B, T, HV))
+    dt, dev = _code(q), _device(q, "q")
+    plain = _qkv(q, k, v, B, T, H, HV, dk, dv, dev)
+    fixed = _decay(decay, (B, T, HV), dev)
     if initial_state is not None:
-        _dense(initial_state, "initial_state", _F32, (B, HV, dk, dv))
-    dev = q.device
+        _dense(initial_state, "initial_state", _F32, (B, HV, dk, dv), dev)
     if out is None:
-        out = _like(v) if plain else _empty((B, T, HV, dv), dtype=q.dtype, device=dev)
+        out = _like(v) if plain else _empty((B, T, HV, dv), dtype=q.dtype, device=q.device)
     else:
-        plain &= _view(out, "out", q.dtype, (B, T, HV, dv))
+        plain &= _view(out, "out", q.dtype, (B, T, HV, dv), dev)
     if final_state is None:
-        final_state = _empty((B, HV, dk, dv), dtype=_F32, device=dev)
+        final_state = _empty((B, HV, dk, dv), dtype=_F32, device=q.device)
     else:
-        _dense(final_state, "final_state", _F32, (B, HV, dk, dv))
-    st = _raw(q)
+        _dense(final_state, "final_state", _F32, (B, HV, dk, dv), dev)
+    st = _raw(dev)
     ws, n = _ws("kda_linear_chunk_fwd_workspace", (B, T, H, HV, dk, dv, dt), q, st, workspace, check_device)
     _ok(lib.kda_linear_chunk_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(decay), fixed, _ptr(initial_state),
                                  out.data_ptr(), final_state.data_ptr(), None if plain else _strides(q, k, v, out), B, T, H,
@@ -187,28 +204,27 @@ def linear_varlen_fwd(q, k, v, cu_seqlens, decay=None, initial_state=None, *, cu
     HV, dv = v.shape[-2:]
     if one != 1:
         raise ValueError("packed sequences need token arrays with B == 1")
-    dt = _code(q)
+    dt, dev = _code(q), _device(q, "q")
     N = cu_seqlens.numel() - 1
-    plain = _qkv(q, k, v, 1, total, H, HV, dk, dv)
-    _dense(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,))
-    fixed = _decay(decay, (1, total, HV))
+    plain = _qkv(q, k, v, 1, total, H, HV, dk, dv, dev)
+    _dense(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
+    fixed = _decay(decay, (1, total, HV), dev)
     if initial_state is not None:
-        _dense(initial_state, "initial_state", _F32, (N, HV, dk, dv))
+        _dense(initial_state, "initial_state", _F32, (N, HV, dk, dv), dev)
     host = None
     if cu_seqlens_cpu is not None:
         host = cu_seqlens_cpu.to(torch.int32).contiguous()
         if host.is_cuda or host.numel() != N + 1:
             raise ValueError("cu_seqlens_cpu must be a host tensor of cu_seqlens' length")
-    dev = q.device
     if out is None:
-        out = _like(v) if plain else _empty((1, total, HV, dv), dtype=q.dtype, device=dev)
+        out = _like(v) if plain else _empty((1, total, HV, dv), dtype=q.dtype, device=q.device)
     else:
-        plain &= _view(out, "out", q.dtype, (1, total, HV, dv))
+        plain &= _view(out, "out", q.dtype, (1, total, HV, dv), dev)
     if final_state is None:
-        final_state = _empty((N, HV, dk, dv), dtype=_F32, device=dev)
+        final_state = _empty((N, HV, dk, dv), dtype=_F32, device=q.device)
     else:
-        _dense(final_state, "final_state", _F32, (N, HV, dk, dv))
-    st = _raw(q)
+        _dense(final_state, "final_state", _F32, (N, HV, dk, dv), dev)
+    st = _raw(dev)
     ws, n = _ws("kda_linear_varlen_fwd_workspace", (N, total, H, HV, dk, dv, dt), q, st, workspace, check_device)
     _ok(lib.kda_linear_varlen_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(decay), fixed, cu_seqlens.data_ptr(),
                                   _ptr(host), _ptr(initial_state), out.data_ptr(), final_state.data_ptr(),
@@ -230,29 +246,29 @@ def linear_decode_step(q, k, v, decay, state, *, scale=None, out=None, stream=No
     H = q.shape[-2]
     if HV != H:
         _heads(H, HV)
-    dt, dtype = _code(q), q.dtype
+    dt, dtype, dev = _code(q), q.dtype, _device(q, "q")
     if q.dim() == 4:
         qs, vs = (B, 1, H, dk), (B, 1, HV, dv)
     else:
         qs, vs = (B, H, dk), (B, HV, dv)
-    plain = _view(q, "q", dtype, qs) & _view(k, "k", dtype, qs) & _view(v, "v", dtype, vs)
-    _dense(state, "state", _F32, state.shape)
+    plain = _view(q, "q", dtype, qs, dev) & _view(k, "k", dtype, qs, dev) & _view(v, "v", dtype, vs, dev)
+    _dense(state, "state", _F32, state.shape, dev)
     fixed = 0
     if decay is not None:
         if decay.dim() == 1:
             fixed = 1
-            _dense(decay, "decay", _F32, (HV,))
+            _dense(decay, "decay", _F32, (HV,), dev)
         else:
-            _dense(decay, "decay", _F32, (B, 1, HV) if decay.dim() == 3 else (B, HV))
+            _dense(decay, "decay", _F32, (B, 1, HV) if decay.dim() == 3 else (B, HV), dev)
     if out is None:
         out = _like(v) if plain else _empty(vs, dtype=dtype, device=q.device)
     else:
-        plain &= _view(out, "out", dtype, vs)
+        plain &= _view(out, "out", dtype, vs, dev)
     s = None
     if not plain:
         s = (ctypes.c_longlong * 8)(*(x for t in (q, k, v, out) for x in (t.stride(0), t.stride(-2))))
     _ok(lib.kda_linear_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(decay), fixed, state.data_ptr(),
-                                   out.data_ptr(), s, B, H, HV, dk, dv, dt, scale or 0.0, _raw(q)),
+                                   out.data_ptr(), s, B, H, HV, dk, dv, dt, scale or 0.0, _raw(dev)),
         "kda_linear_decode_step", lib)
     return out
 
@@ -268,27 +284,26 @@ def linear_chunk_bwd(q, k, v, decay, initial_state, d_o, dfinal_state=None, *, s
     lib = load()
     B, T, H, dk = q.shape
     HV, dv = v.shape[-2:]
-    dt, dtype = _code(q), q.dtype
-    plain = _qkv(q, k, v, B, T, H, HV, dk, dv) & _view(d_o, "d_o", dtype, (B, T, HV, dv))
-    fixed = _decay(decay, (B, T, HV))
+    dt, dtype, dev = _code(q), q.dtype, _device(q, "q")
+    plain = _qkv(q, k, v, B, T, H, HV, dk, dv, dev) & _view(d_o, "d_o", dtype, (B, T, HV, dv), dev)
+    fixed = _decay(decay, (B, T, HV), dev)
     if initial_state is not None:
-        _dense(initial_state, "initial_state", _F32, (B, HV, dk, dv))
+        _dense(initial_state, "initial_state", _F32, (B, HV, dk, dv), dev)
     if dfinal_state is not None:
-        _dense(dfinal_state, "dfinal_state", _F32, (B, HV, dk, dv))
-    dev = q.device
+        _dense(dfinal_state, "dfinal_state", _F32, (B, HV, dk, dv), dev)
     if plain:
         dq, dkk, dvv = _like(q), _like(k), _like(v)
     else:
-        dq = _empty((B, T, H, dk), dtype=dtype, device=dev)
-        dkk = _empty((B, T, H, dk), dtype=dtype, device=dev)
-        dvv = _empty((B, T, HV, dv), dtype=dtype, device=dev)
+        dq = _empty((B, T, H, dk), dtype=dtype, device=q.device)
+        dkk = _empty((B, T, H, dk), dtype=dtype, device=q.device)
+        dvv = _empty((B, T, HV, dv), dtype=dtype, device=q.device)
     out = dict(dq=dq, dk=dkk, dv=dvv)
     dg = dh0 = None
     if decay is not None:
         dg = out["ddecay"] = _like(decay)
     if initial_state is not None:
         dh0 = out["dh0"] = _like(initial_state)
-    st = _raw(q)
+    st = _raw(dev)
     ws, n = _ws("kda_linear_chunk_bwd_workspace", (B, T, H, HV, dk, dv, dt), q, st, workspace, check_device)
     _ok(lib.kda_linear_chunk_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(decay), fixed, _ptr(initial_state),
                                  d_o.data_ptr(), _ptr(dfinal_state), dq.data_ptr(), dkk.data_ptr(), dvv.data_ptr(),
@@ -328,12 +343,12 @@ def _norm_args(x, gate, weight, activation):
     if x.dim() < 2:
         raise ValueError("x must be [..., H, D]")
     H, D = x.shape[-2:]
-    dt = _code(x, "x")
-    _dense(weight, "weight", _F32, (D,))
-    plain = _view(x, "x", x.dtype, x.shape)
+    dt, dev = _code(x, "x"), _device(x, "x")
+    _dense(weight, "weight", _F32, (D,), dev)
+    plain = _view(x, "x", x.dtype, x.shape, dev)
     if gate is not None:
-        plain &= _view(gate, "gate", x.dtype, x.shape)
-    return act, dt, H, D, x.numel() // max(1, H * D), plain
+        plain &= _view(gate, "gate", x.dtype, x.shape, dev)
+    return act, dt, H, D, x.numel() // max(1, H * D), plain, dev
 
 
 def gated_norm_fwd(x, gate, weight, *, eps=1e-6, activation="silu", out=None, stream=None):
@@ -342,17 +357,17 @@ def gated_norm_fwd(x, gate, weight, *, eps=1e-6, activation="silu", out=None, st
     if stream is not None:
         return _on(stream, gated_norm_fwd, x, gate, weight, eps=eps, activation=activation, out=out)
     lib = load()
-    act, dt, H, D, N, plain = _norm_args(x, gate, weight, activation)
+    act, dt, H, D, N, plain, dev = _norm_args(x, gate, weight, activation)
     if out is None:
         out = _like(x) if plain else _empty(x.shape, dtype=x.dtype, device=x.device)
     else:
-        plain &= _view(out, "out", x.dtype, x.shape)
+        plain &= _view(out, "out", x.dtype, x.shape, dev)
     s = None
     if not plain:
         s = (ctypes.c_longlong * 6)(*_token_strides(x), *_token_strides(gate if gate is not None else x),
                                     *_token_strides(out))
     _ok(lib.kda_gated_norm_fwd(x.data_ptr(), _ptr(gate), weight.data_ptr(), out.data_ptr(), s, N, H, D, dt, act, eps,
-                               _raw(x)), "kda_gated_norm_fwd", lib)
+                               _raw(dev)), "kda_gated_norm_fwd", lib)
     return out
 
 
@@ -361,15 +376,15 @@ def gated_norm_bwd(d_y, x, gate, weight, *, eps=1e-6, activation="silu", workspa
     if stream is not None:
         return _on(stream, gated_norm_bwd, d_y, x, gate, weight, eps=eps, activation=activation, workspace=workspace)
     lib = load()
-    act, dt, H, D, N, plain = _norm_args(x, gate, weight, activation)
-    plain &= _view(d_y, "d_y", x.dtype, x.shape)
+    act, dt, H, D, N, plain, dev = _norm_args(x, gate, weight, activation)
+    plain &= _view(d_y, "d_y", x.dtype, x.shape, dev)
     dx = _like(x) if plain else _empty(x.shape, dtype=x.dtype, device=x.device)
     dw = _like(weight)
     out = dict(dx=dx, dw=dw)
     dg = None
     if gate is not None:
         dg = out["dgate"] = _like(dx)
-    st = _raw(x)
+    st = _raw(dev)
     ws, n = _ws("kda_gated_norm_bwd_workspace", (D,), x, st, workspace)
     s = None
     if not plain:
@@ -386,9 +401,9 @@ def _rows(t, D):
     return D if t.is_contiguous() else _step(t, t.dim() - 1, "row", D)
 
 
-def _scale(scale, D):
+def _scale(scale, D, dev):
     if isinstance(scale, torch.Tensor):
-        _dense(scale, "scale", _F32, (D,))
+        _dense(scale, "scale", _F32, (D,), dev)
         return scale.data_ptr(), 0.0
     return None, float(scale)
 
@@ -403,20 +418,20 @@ def residual_norm_fwd(x, y, weight, *, scale=1.0, eps=1e-6, out=None, out_norm=N
     lib = load()
     shape = x.shape
     D = shape[-1]
-    res, dt = _code(x, "x"), _code(y, "y")
-    x_dense, y_dense = _view(x, "x", x.dtype, shape), _view(y, "y", y.dtype, shape)
-    _dense(weight, "weight", _F32, (D,))
-    cv, c = _scale(scale, D)
+    res, dt, dev = _code(x, "x"), _code(y, "y"), _device(x, "x")
+    x_dense, y_dense = _view(x, "x", x.dtype, shape, dev), _view(y, "y", y.dtype, shape, dev)
+    _dense(weight, "weight", _F32, (D,), dev)
+    cv, c = _scale(scale, D, dev)
     if out is None:
         out = _like(x) if x_dense else _empty(shape, dtype=x.dtype, device=x.device)
     else:
-        _dense(out, "out", x.dtype, shape)
+        _dense(out, "out", x.dtype, shape, dev)
     if out_norm is None:
         out_norm = _like(y) if y_dense else _empty(shape, dtype=y.dtype, device=x.device)
     else:
-        _dense(out_norm, "out_norm", y.dtype, shape)
+        _dense(out_norm, "out_norm", y.dtype, shape, dev)
     _ok(lib.kda_residual_norm_fwd(x.data_ptr(), y.data_ptr(), weight.data_ptr(), cv, c, out.data_ptr(), out_norm.data_ptr(),
-                                  _rows(x, D), _rows(y, D), x.numel() // max(1, D), D, res, dt, eps, _raw(x)),
+                                  _rows(x, D), _rows(y, D), x.numel() // max(1, D), D, res, dt, eps, _raw(dev)),
         "kda_residual_norm_fwd", lib)
     return out, out_norm
 
@@ -430,20 +445,20 @@ def residual_norm_bwd(d_n, d_x, x, weight, y=None, *, scale=1.0, eps=1e-6, works
     lib = load()
     shape = x.shape
     D = shape[-1]
-    res, dt = _code(x, "x"), _code(d_n, "d_n")
-    _dense(x, "x", x.dtype, shape)
-    _dense(d_n, "d_n", d_n.dtype, shape)
-    _dense(weight, "weight", _F32, (D,))
+    res, dt, dev = _code(x, "x"), _code(d_n, "d_n"), _device(x, "x")
+    _dense(x, "x", x.dtype, shape, dev)
+    _dense(d_n, "d_n", d_n.dtype, shape, dev)
+    _dense(weight, "weight", _F32, (D,), dev)
     if d_x is not None:
-        _dense(d_x, "d_x", x.dtype, shape)
-    cv, c = _scale(scale, D)
+        _dense(d_x, "d_x", x.dtype, shape, dev)
+    cv, c = _scale(scale, D, dev)
     dx, dy, dw = _like(x), _like(d_n), _like(weight)
     out = dict(dx=dx, dy=dy, dw=dw)
     ds = None
     if y is not None:
-        _dense(y, "y", d_n.dtype, shape)
+        _dense(y, "y", d_n.dtype, shape, dev)
         ds = out["dscale"] = _like(weight)
-    st = _raw(x)
+    st = _raw(dev)
     ws, n = _ws("kda_residual_norm_bwd_workspace", (D,), x, st, workspace)
     _ok(lib.kda_residual_norm_bwd(d_n.data_ptr(), _ptr(d_x), x.data_ptr(), _ptr(y), weight.data_ptr(), cv, c, dx.data_ptr(),
                                   dy.data_ptr(), dw.data_ptr(), _ptr(ds), x.numel() // max(1, D), D, res, dt, eps,

@@ -109,6 +109,7 @@ def lib(monkeypatch):
     _linear._bytes.cache_clear()
     monkeypatch.setattr(_linear, "load", lambda: lib)
     monkeypatch.setattr(_linear, "_raw", lambda t: 0)
+    monkeypatch.setattr(_linear, "_here", lambda: 0, raising=False)
     monkeypatch.setattr(_linear, "query_device_error", lambda ws: 8)
     yield lib
     _linear._bytes.cache_clear()
@@ -130,3 +131,37 @@ def test_an_empty_batch_has_no_error_word(lib):
     kda.linear_varlen_fwd(p, p, p, cu, check_device=True)
     with pytest.raises(kda.KdaError):
         kda.linear_varlen_fwd(p, p, p, _zeros(3, dtype=torch.int32), check_device=True)
+
+
+_CU = lambda i: _zeros(2, dtype=torch.int32, index=i)  # noqa: E731
+# each call of tensors of which the last is on device j, the others on device i
+_CALLS = {
+    "chunk_fwd": lambda i, j: kda.linear_chunk_fwd(*(_zeros(1, 4, 1, 32, index=i) for _ in range(3)),
+                                                   _zeros(1, 4, 1, index=i), _zeros(1, 1, 32, 32, index=j)),
+    "chunk_fwd out": lambda i, j: kda.linear_chunk_fwd(*(_zeros(1, 4, 1, 32, index=i) for _ in range(3)),
+                                                       out=_zeros(1, 4, 1, 32, index=j)),
+    "varlen_fwd": lambda i, j: kda.linear_varlen_fwd(*(_zeros(1, 4, 1, 32, index=i) for _ in range(3)), _CU(j)),
+    "decode_step": lambda i, j: kda.linear_decode_step(*(_zeros(1, 1, 1, 32, index=i) for _ in range(3)), None,
+                                                       _zeros(1, 1, 32, 32, index=j)),
+    "chunk_bwd": lambda i, j: kda.linear_chunk_bwd(*(_zeros(1, 4, 1, 32, index=i) for _ in range(3)), None, None,
+                                                   _zeros(1, 4, 1, 32, index=j)),
+    "gated_norm_fwd": lambda i, j: kda.gated_norm_fwd(_zeros(2, 3, 8, index=i), _zeros(2, 3, 8, index=i), _zeros(8, index=j)),
+    "gated_norm_bwd": lambda i, j: kda.gated_norm_bwd(_zeros(2, 3, 8, index=j), _zeros(2, 3, 8, index=i),
+                                                      _zeros(2, 3, 8, index=i), _zeros(8, index=i)),
+    "residual_norm_fwd": lambda i, j: kda.residual_norm_fwd(_zeros(2, 8, index=i), _zeros(2, 8, index=i), _zeros(8, index=i),
+                                                            scale=_zeros(8, index=j)),
+    "residual_norm_bwd": lambda i, j: kda.residual_norm_bwd(_zeros(2, 8, index=i), None, _zeros(2, 8, index=i),
+                                                            _zeros(8, index=i), _zeros(2, 8, index=j)),
+}
+
+
+@pytest.mark.parametrize("name", list(_CALLS))
+def test_tensors_of_another_device_are_refused(lib, name):
+    """The kernels run on the current device, on the stream of that number there: tensors of another device would be
+    reached through the wrong stream, or not at all."""
+    _CALLS[name](0, 0)
+    assert len(lib.launched) == 1
+    for devices in ((0, 1), (1, 0), (1, 1)):
+        with pytest.raises(ValueError, match="device"):
+            _CALLS[name](*devices)
+    assert len(lib.launched) == 1
