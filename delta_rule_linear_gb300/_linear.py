@@ -115,6 +115,9 @@ def _ws(query, sizes, t, stream, workspace, asked=False):
     """(workspace, its bytes) of a call on t's device.  A call that needs the header alone takes one that is kept per
     stream, whose calls follow one another; where its error word is asked for, a fresh one."""
     if workspace is not None:
+        # its bytes are counted from here on: a cut or broadcast view has fewer of its own
+        if workspace.get_device() != t.get_device() or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor on the call's device")
         return workspace, workspace.numel() * workspace.element_size()
     need = _bytes(query, *sizes)
     if need == 0:

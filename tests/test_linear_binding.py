@@ -165,3 +165,21 @@ def test_tensors_of_another_device_are_refused(lib, name):
         with pytest.raises(ValueError, match="device"):
             _CALLS[name](*devices)
     assert len(lib.launched) == 1
+
+
+@pytest.mark.parametrize("name", ["chunk_fwd", "varlen_fwd", "chunk_bwd", "gated_norm_bwd", "residual_norm_bwd"])
+def test_a_workspace_is_whole_and_on_the_device(lib, name):
+    """Kernels write to all the bytes a workspace is said to have, so those have to be its own and the device's."""
+    x, n, w = _zeros(1, 4, 1, 32), _zeros(2, 8), _zeros(8)
+    call = {"chunk_fwd": lambda ws: kda.linear_chunk_fwd(x, x, x, workspace=ws),
+            "varlen_fwd": lambda ws: kda.linear_varlen_fwd(x, x, x, _CU(0), workspace=ws),
+            "chunk_bwd": lambda ws: kda.linear_chunk_bwd(x, x, x, None, None, x, workspace=ws),
+            "gated_norm_bwd": lambda ws: kda.gated_norm_bwd(x, x, x, _zeros(32), workspace=ws),
+            "residual_norm_bwd": lambda ws: kda.residual_norm_bwd(n, None, n, w, workspace=ws)}[name]
+    call(_zeros(4096))
+    assert len(lib.launched) == 1
+    for ws in (torch.zeros(4096), _zeros(4096, index=1), _on_device(torch.zeros(4096)[::2]),
+               _on_device(torch.zeros(1).expand(4096)), _on_device(torch.zeros(64, 64).t())):
+        with pytest.raises(ValueError, match="workspace"):
+            call(ws)
+    assert len(lib.launched) == 1
