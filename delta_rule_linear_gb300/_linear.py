@@ -109,6 +109,7 @@ def _bytes(query, *sizes):
 
 _HEADER = 256       # bytes of a workspace that is its header alone (the error word)
 _headers = {}
+_capturing = torch.cuda.is_current_stream_capturing
 
 
 def _ws(query, sizes, t, stream, workspace, asked=False):
@@ -127,7 +128,9 @@ def _ws(query, sizes, t, stream, workspace, asked=False):
     key = (t.get_device(), stream)
     ws = _headers.get(key)
     if ws is None:
-        ws = _headers[key] = _empty(_HEADER, dtype=torch.uint8, device=t.device)
+        ws = _empty(_HEADER, dtype=torch.uint8, device=t.device)
+        if not _capturing():        # a capture's memory is its graph's: kept, it would be used beside and after the graph
+            _headers[key] = ws
     return ws, _HEADER
 
 

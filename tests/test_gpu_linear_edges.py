@@ -36,3 +36,29 @@ def test_empty_batches_raise_no_device_error(kda, dtype):
         o, h = kda.linear_chunk_fwd(d["q"][:, :0], d["k"][:, :0], d["v"][:, :0], d["decay"][:, :0].contiguous(), d["h0"],
                                     check_device=True)
         assert torch.equal(h, d["h0"])
+
+
+def test_a_first_call_in_a_capture_leaves_nothing_of_the_graph_behind(kda):
+    """A call that needs no more than a header, captured on a stream that made none before, replayed, and called again on
+    that stream after the graph has gone."""
+    import torch
+    from delta_rule_linear_gb300 import _linear
+    d, n = _make(1, 20, 2, 1, 32, 32, "f32")
+    ro, _ = ref.forward(n["q"], n["k"], n["v"], n["decay"], n["h0"])
+    call = lambda: kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["decay"], d["h0"])[0]  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    before = set(_linear._headers)
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        o = call()
+    assert set(_linear._headers) == before
+    g.replay()
+    torch.cuda.synchronize()
+    assert ref.frob(_np(o), ro) <= ref.F32
+    del g, o
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(s):
+        o = call()
+    s.synchronize()
+    assert ref.frob(_np(o), ro) <= ref.F32

@@ -105,14 +105,14 @@ class _Lib:
 
 @pytest.fixture
 def lib(monkeypatch):
-    lib = _Lib()
-    _linear._bytes.cache_clear()
+    lib, sizes = _Lib(), _linear._bytes
+    sizes.cache_clear()
     monkeypatch.setattr(_linear, "load", lambda: lib)
     monkeypatch.setattr(_linear, "_raw", lambda t: 0)
     monkeypatch.setattr(_linear, "_here", lambda: 0, raising=False)
     monkeypatch.setattr(_linear, "query_device_error", lambda ws: 8)
     yield lib
-    _linear._bytes.cache_clear()
+    sizes.cache_clear()
 
 
 def _zeros(*s, dtype=torch.float32, index=0):
@@ -183,3 +183,22 @@ def test_a_workspace_is_whole_and_on_the_device(lib, name):
         with pytest.raises(ValueError, match="workspace"):
             call(ws)
     assert len(lib.launched) == 1
+
+
+def test_a_header_taken_in_a_capture_is_not_kept(lib, monkeypatch):
+    """Memory that is first asked for while a graph is captured belongs to that graph."""
+    x = _zeros(1, 4, 1, 32)
+    monkeypatch.setattr(_linear, "_headers", {})
+    monkeypatch.setattr(_linear, "_bytes", lambda *a: _linear._HEADER)
+    capturing = [True]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    monkeypatch.setattr(_linear, "_capturing", lambda: capturing[0], raising=False)
+    kda.linear_chunk_fwd(x, x, x)
+    assert not _linear._headers
+    capturing[0] = False
+    kda.linear_chunk_fwd(x, x, x)
+    kept = dict(_linear._headers)
+    assert len(kept) == 1
+    capturing[0] = True                     # what is kept already is nobody's but this process's
+    kda.linear_chunk_fwd(x, x, x)
+    assert _linear._headers == kept and len(lib.launched) == 3
