@@ -54,6 +54,15 @@ def _view(t, name, dtype, shape, dev):
     return t.is_contiguous()
 
 
+def _into(t, name, dtype, shape, dev):
+    """_view of an output, whose elements have to be apart: through a broadcast dimension CTAs write over one another."""
+    if _view(t, name, dtype, shape, dev):
+        return True
+    if any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)) and t.numel():
+        raise ValueError(f"{name} must not be a broadcast view")
+    return False
+
+
 def _dense(t, name, dtype, shape, dev):
     if not (t.is_contiguous() and t.dtype is dtype and t.get_device() == dev and t.shape == shape):
         _need(t, name, dtype, shape, dev)
@@ -182,7 +191,7 @@ def linear_chunk_fwd(q, k, v, decay=None, initial_state=None, *, scale=None, out
     if out is None:
         out = _like(v) if plain else _empty((B, T, HV, dv), dtype=q.dtype, device=q.device)
     else:
-        plain &= _view(out, "out", q.dtype, (B, T, HV, dv), dev)
+        plain &= _into(out, "out", q.dtype, (B, T, HV, dv), dev)
     if final_state is None:
         final_state = _empty((B, HV, dk, dv), dtype=_F32, device=q.device)
     else:
@@ -225,7 +234,7 @@ def linear_varlen_fwd(q, k, v, cu_seqlens, decay=None, initial_state=None, *, cu
     if out is None:
         out = _like(v) if plain else _empty((1, total, HV, dv), dtype=q.dtype, device=q.device)
     else:
-        plain &= _view(out, "out", q.dtype, (1, total, HV, dv), dev)
+        plain &= _into(out, "out", q.dtype, (1, total, HV, dv), dev)
     if final_state is None:
         final_state = _empty((N, HV, dk, dv), dtype=_F32, device=q.device)
     else:
@@ -269,7 +278,7 @@ def linear_decode_step(q, k, v, decay, state, *, scale=None, out=None, stream=No
     if out is None:
         out = _like(v) if plain else _empty(vs, dtype=dtype, device=q.device)
     else:
-        plain &= _view(out, "out", dtype, vs, dev)
+        plain &= _into(out, "out", dtype, vs, dev)
     s = None
     if not plain:
         s = (ctypes.c_longlong * 8)(*(x for t in (q, k, v, out) for x in (t.stride(0), t.stride(-2))))
@@ -367,7 +376,7 @@ def gated_norm_fwd(x, gate, weight, *, eps=1e-6, activation="silu", out=None, st
     if out is None:
         out = _like(x) if plain else _empty(x.shape, dtype=x.dtype, device=x.device)
     else:
-        plain &= _view(out, "out", x.dtype, x.shape, dev)
+        plain &= _into(out, "out", x.dtype, x.shape, dev)
     s = None
     if not plain:
         s = (ctypes.c_longlong * 6)(*_token_strides(x), *_token_strides(gate if gate is not None else x),

@@ -202,3 +202,18 @@ def test_a_header_taken_in_a_capture_is_not_kept(lib, monkeypatch):
     capturing[0] = True                     # what is kept already is nobody's but this process's
     kda.linear_chunk_fwd(x, x, x)
     assert _linear._headers == kept and len(lib.launched) == 3
+
+
+def test_outputs_are_no_broadcast_views(lib):
+    """Rows that share memory would be written by several CTAs at once."""
+    x, cu, st = _zeros(2, 4, 2, 32), _zeros(2, dtype=torch.int32), _zeros(2, 2, 32, 32)
+    into = lambda *s: _on_device(torch.zeros(s[-1]).expand(*s))  # noqa: E731
+    for call in (lambda: kda.linear_chunk_fwd(x, x, x, out=into(2, 4, 2, 32)),
+                 lambda: kda.linear_varlen_fwd(x[:1], x[:1], x[:1], cu, out=into(1, 4, 2, 32)),
+                 lambda: kda.linear_decode_step(x[:, 0], x[:, 0], x[:, 0], None, st, out=into(2, 2, 32)),
+                 lambda: kda.gated_norm_fwd(x, x, _zeros(32), out=into(2, 4, 2, 32))):
+        with pytest.raises(ValueError, match="broadcast"):
+            call()
+    assert not lib.launched
+    kda.linear_chunk_fwd(x, x, x, out=_on_device(torch.zeros(2, 4, 3, 32)[:, :, :2]))
+    assert len(lib.launched) == 1
