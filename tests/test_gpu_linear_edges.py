@@ -62,3 +62,25 @@ def test_a_first_call_in_a_capture_leaves_nothing_of_the_graph_behind(kda):
         o = call()
     s.synchronize()
     assert ref.frob(_np(o), ro) <= ref.F32
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [5, 150])
+def test_broadcast_inputs_equal_copies(kda, T, dtype):
+    """q, k, v and d_o expanded over requests, tokens or heads (strides of 0), in both forms and the single step."""
+    import torch
+    d, _ = _make(2, T, 2, 1, 64, 64, dtype)
+    names = ("q", "k", "v", "d_o")
+    for name, cut in ((n, c) for n in names for c in (slice(0, 1), (slice(None), slice(0, 1)), (slice(None), slice(None), slice(0, 1)))):
+        x = dict(d)
+        x[name] = d[name][cut].expand(2, T, 2, 64)
+        c = dict(d)
+        c[name] = x[name].contiguous()
+        run = lambda a: (*kda.linear_chunk_fwd(a["q"], a["k"], a["v"], a["decay"], a["h0"]),  # noqa: E731
+                         *kda.linear_chunk_bwd(a["q"], a["k"], a["v"], a["decay"], a["h0"], a["d_o"], a["dhT"]).values())
+        assert all(torch.equal(p, q) for p, q in zip(run(x), run(c))), (name, cut)
+        if name != "d_o":
+            s0, s1 = d["h0"].clone(), d["h0"].clone()
+            o0 = kda.linear_decode_step(*(x[n][:, 0] for n in names[:3]), d["decay"][:, 0].contiguous(), s0)
+            o1 = kda.linear_decode_step(*(c[n][:, 0] for n in names[:3]), d["decay"][:, 0].contiguous(), s1)
+            assert torch.equal(o0, o1) and torch.equal(s0, s1)
