@@ -3,11 +3,14 @@
 // After the block, per head row of width D (gated norm):
 //     y = x r w act(g),            r = (mean(x^2) + eps)^(-1/2),   act = silu or sigmoid (or 1)
 //     t = dy act(g) w:  dx = r (t - xn mean(t xn)),  dg = dy xn w act'(g),  dw = sum dy act(g) xn
-// with xn = x r (the bracket is evaluated as eps r^2 t + r^2 (t sum' x^2 - x sum' t x) / D, the sums
-// without the element itself, whose share cancels: in a row that one element dominates the two
-// terms as written would cancel in rounded arithmetic); before the next one, per token row of width D (residual norm):
+// with xn = x r; before the next one, per token row of width D (residual norm):
 //     x' = x + c y,   n = x' r w
 //     t = dn w:  dx = dx' + r (t - xn mean(t xn)),  dy = c dx,  dw = sum dn xn,  dc = sum dx y
+// The bracket cancels at an element that carries its row (D = 1: all but eps r^2 t is lost).  With ' for sums without
+// the element it is also t u - xn w, u = r^2 (eps + sum' x^2 / D), w = r sum' t x / D, which does not cancel.  An element
+// of more than half of the row's squares takes this form.  There is at most one, and only rows that have one form their
+// two sums again, without it (taken from the sums with it they would have lost it already).  What it costs is the
+// search: 2 % of the gradient of 4096 fp32 rows of 2048, 12 % at 16,384, where registers spill.
 //
 // All are bound by HBM: every element is read once and written once, a row lives in registers
 // between its sum of squares and its output, and everything is computed in fp32 and rounded once.
@@ -16,9 +19,9 @@
 // of dw and dc stay in that thread's registers over all its rows and meet once at the end: per CTA
 // in shared memory, then over the CTAs by a second small kernel, in a fixed order (no atomics).
 //
-// Measured, bf16: gated norm of 32,768 x 32 rows of 128: 123 us, 6.6 TB/s; its gradient, 4096 x 16 rows of 128: 19 us
-// (84 MB, 12.4 us at the copy rate: some 45 instructions an element are the other bound); residual norm of 256
-// rows of 4096: 3.2 us; its gradient, 4096 rows of 2048, fp32 stream, learned scale: 32 us (151 MB, 22.3 us at the
+// Measured, bf16: gated norm of 32,768 x 32 rows of 128: 123 us, 6.6 TB/s; its gradient, 4096 x 16 rows of 128: 18 us
+// (84 MB, 12.4 us at the copy rate: some 40 instructions an element are the other bound); residual norm of 256
+// rows of 4096: 3.2 us; its gradient, 4096 rows of 2048, fp32 stream, learned scale: 33 us (151 MB, 22.3 us at the
 // copy rate; the two launches' ends are the rest).
 #include <algorithm>
 
@@ -93,13 +96,21 @@ __device__ __forceinline__ long row_at(const NormView &v, long row, int H, int D
 
 // Sum over the L threads of a row: lanes of a warp (L <= 32) or the whole CTA (L = blockDim).
 // `s` holds one float per warp; consecutive calls alternate between two of them.
+// `any`: whether a thread of the warp (L <= 32) or of the CTA brings it (`s` then holds twice as many floats).
 template <int L>
-__device__ __forceinline__ float row_sum(float x, float *s) {
+__device__ __forceinline__ float row_sum(float x, float *s, bool *any = nullptr) {
 #pragma unroll
     for (int off = (L < 32 ? L : 32) / 2; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    if constexpr (L > 32) {
+    if constexpr (L <= 32) {
+        if (any) *any = __any_sync(0xffffffffu, *any);
+    } else {
         if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
+        if (any) {
+            const bool mine = __any_sync(0xffffffffu, *any);
+            if ((threadIdx.x & 31) == 0) s[L / 32 + (threadIdx.x >> 5)] = mine ? 1.f : 0.f;
+        }
         __syncthreads();
+        if (any) *any = __any_sync(0xffffffffu, s[L / 32 + (threadIdx.x & (L / 32 - 1))] != 0.f);
         x = s[threadIdx.x & (L / 32 - 1)];
 #pragma unroll
         for (int off = L / 64; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
@@ -122,10 +133,9 @@ __device__ __forceinline__ float act_of(float a, int kind) {
     return kind == 1 ? a * s : s;
 }
 
-// t - xn mean(t xn) of one element (see above), from the row's sums of x^2 and t x
-__device__ __forceinline__ float norm_back(float t, float x, float ss, float dot, float r2, float eps, float inv_d) {
-    const float ss1 = ss - __fmul_rn(x, x), dot1 = dot - __fmul_rn(t, x);
-    return r2 * fmaf(eps, t, (t * ss1 - x * dot1) * inv_d);
+// t - xn mean(t xn) of the element that carries the row (see above), from the row's sums without it
+__device__ __forceinline__ float carrier_back(float t, float x, float r, float ss1, float dot1, float eps, float inv_d) {
+    return t * (r * r * fmaf(ss1, inv_d, eps)) - x * r * (r * dot1 * inv_d);
 }
 
 // ------------------------------------------------------------------------------ gated norm
@@ -198,9 +208,10 @@ __global__ void __launch_bounds__(kThreads) gated_norm_fwd_kernel(GatedNorm a) {
     }
 }
 
-// ACT, the gate's function, is a constant here: selecting it per element cost 6 % (65,536 rows of 128: 20.2 us).
+// ACT, the gate's function, is a constant here: selecting it per element cost 6 %.  fp32 rows of up to 128 are held to 64
+// registers, the four CTAs per SM that are launched (72 without: 37.0 us for 65,536 rows of 128 instead of 29.4).
 template <typename T, int V, int L, int NJ, int ACT>
-__global__ void __launch_bounds__(kThreads) gated_norm_bwd_kernel(GatedNorm a) {
+__global__ void __launch_bounds__(kThreads, V == 4 && NJ == 1 ? 4 : 1) gated_norm_bwd_kernel(GatedNorm a) {
     constexpr int RPB = kThreads / L;
     __shared__ float s_dw[RPB][L * V + 1];
     next_may_start();
@@ -245,19 +256,53 @@ __global__ void __launch_bounds__(kThreads) gated_norm_bwd_kernel(GatedNorm a) {
             Pk::open(ad[j], dy[j]);
         }
         fetch(row + gridDim.x * (long)RPB);
-        float sg[NJ][V];                        // sigmoid of the gate: its two special-function operations once
+        float sg[NJ][V], top = 0.f;             // sigmoid of the gate: its two special-function operations once
+        auto t_of = [&](int j, int i) { return dy[j][i] * (ACT == 1 ? g[j][i] * sg[j][i] : sg[j][i]) * w[j][i]; };
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 sg[j][i] = ACT ? sigmoid(g[j][i]) : 1.f;
                 ss = fmaf(x[j][i], x[j][i], ss);
-                const float ac = ACT == 1 ? g[j][i] * sg[j][i] : sg[j][i];
-                dot = fmaf(dy[j][i] * ac * w[j][i], x[j][i], dot);
+                dot = fmaf(t_of(j, i), x[j][i], dot);
+                top = fmaxf(top, fabsf(x[j][i]));
             }
         ss = row_sum<L>(ss, nullptr);
-        dot = row_sum<L>(dot, nullptr);
-        const float r = rsqrtf(ss * a.inv_d + a.eps), r2 = r * r;
+        bool carried = top * top > 0.5f * ss;
+        dot = row_sum<L>(dot, nullptr, &carried);
+        const float r = rsqrtf(ss * a.inv_d + a.eps), mean = r * dot * a.inv_d;
+        float carrier = 0.f;
+        int at = -1;                            // the carrier's place, in the lane that holds it
+        if (carried) {                          // a row of the warp has an element of more than half of its squares
+            float ss1 = 0.f, dot1 = 0.f, t = 0.f, v = 0.f;
+            auto take = [&](float xe, float te, int e) {
+                const bool is = xe * xe > 0.5f * ss;
+                ss1 += is ? 0.f : xe * xe;
+                dot1 += is ? 0.f : te * xe;
+                t = is ? te : t;
+                v = is ? xe : v;
+                at = is ? e : at;
+            };
+            if constexpr (NJ * V <= 16) {
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) take(x[j][i], t_of(j, i), (l + L * j) * V + i);
+            } else {                            // wide rows have no registers to spare: read again, one by one
+#pragma unroll 1
+                for (int k = 0; k < NJ * V; ++k) {
+                    const int e = (l + L * (k / V)) * V + k % V;
+                    if (!live || e >= a.D) continue;
+                    const float ge = ACT ? to_f32(static_cast<const T *>(a.g.p)[row_at(a.g, rr, a.H, a.D, a.flat) + e]) : 0.f;
+                    const float act = ACT ? act_of(ge, ACT) : 1.f;
+                    take(to_f32(static_cast<const T *>(a.x.p)[row_at(a.x, rr, a.H, a.D, a.flat) + e]),
+                         to_f32(static_cast<const T *>(a.dy.p)[row_at(a.dy, rr, a.H, a.D, a.flat) + e]) * act * a.w[e], e);
+                }
+            }
+            ss1 = row_sum<L>(ss1, nullptr);
+            dot1 = row_sum<L>(dot1, nullptr);
+            carrier = r * carrier_back(t, v, r, ss1, dot1, a.eps, a.inv_d);
+        }
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             const int e = (l + L * j) * V;
@@ -269,11 +314,13 @@ __global__ void __launch_bounds__(kThreads) gated_norm_bwd_kernel(GatedNorm a) {
                 const float da = ACT == 1 ? fmaf(ac, 1.f - s, s) : s * (1.f - s);
                 dw[j][i] = fmaf(d * ac, xn, dw[j][i]);
                 g[j][i] = d * xn * w[j][i] * da;
-                x[j][i] = r * norm_back(d * ac * w[j][i], x[j][i], ss, dot, r2, a.eps, a.inv_d);
+                x[j][i] = r * fmaf(-xn, mean, d * ac * w[j][i]);
             }
             Pack<T, V>::store(static_cast<T *>(a.dx.p) + row_at(a.dx, rr, a.H, a.D, a.flat) + e, x[j]);
             if (ACT) Pack<T, V>::store(static_cast<T *>(a.dg.p) + row_at(a.dg, rr, a.H, a.D, a.flat) + e, g[j]);
         }
+        if (at >= 0)                            // over what this thread has just stored
+            static_cast<T *>(a.dx.p)[row_at(a.dx, rr, a.H, a.D, a.flat) + at] = from_f32<T>(carrier);
     }
     // this CTA's share of dw, row groups in order
 #pragma unroll
@@ -365,7 +412,7 @@ template <typename TR, typename T, int V, int L, int NJ>
 __global__ void __launch_bounds__(L > 32 ? L : kThreads) residual_norm_bwd_kernel(ResidualNorm a) {
     constexpr int RPB = L > 32 ? 1 : kThreads / L;
     constexpr int SW = L > 32 ? L / 32 : 1;
-    __shared__ float s_red[2][2 * SW];
+    __shared__ float s_red[2][5 * SW];
     __shared__ float s_dw[L > 32 ? 1 : RPB][L > 32 ? 1 : L * V + 1];
     next_may_start();
     const int l = threadIdx.x % L, rg = threadIdx.x / L;
@@ -380,15 +427,18 @@ __global__ void __launch_bounds__(L > 32 ? L : kThreads) residual_norm_bwd_kerne
         typename Pack<TR, V>::Raw x[NJ], dx[NJ];
         typename Pack<T, V>::Raw dn[NJ], y[NJ];
     };
+    // Fetched ahead in packs the loads have no branches, past the end the last places are read again: they go out together
+    // and none is waited for early (4096 rows of 2048 fp32: 32.6 us, with branches 39.6)
+    constexpr bool kClamp = kAhead && V > 1;
     auto fetch = [&](Row &r, long row) {
         const bool live = row < a.rows;
-        const long rr = live ? row : 0;
+        const long rr = live ? row : kClamp ? a.rows - 1 : 0;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            const int e = (l + L * j) * V;
+            const int e0 = (l + L * j) * V, e = kClamp ? min(e0, a.D - V) : e0;
             r.x[j] = r.dx[j] = Pack<TR, V>::zero();
             r.dn[j] = r.y[j] = Pack<T, V>::zero();
-            if (live && e < a.D) {
+            if (kClamp || (live && e < a.D)) {
                 r.x[j] = Pack<TR, V>::get(static_cast<const TR *>(a.x) + rr * a.xs + e);
                 r.dn[j] = Pack<T, V>::get(static_cast<const T *>(a.dn) + rr * a.dns + e);
                 if (a.dxo) r.dx[j] = Pack<TR, V>::get(static_cast<const TR *>(a.dxo) + rr * a.dxs + e);
@@ -398,11 +448,11 @@ __global__ void __launch_bounds__(L > 32 ? L : kThreads) residual_norm_bwd_kerne
     };
     Row ahead;
     if constexpr (kAhead) fetch(ahead, blockIdx.x * (long)RPB + rg);
-    int turn = 0;   // the two sums of consecutive rows use two sets of shared floats
+    int turn = 0;   // the sums of consecutive rows use two sets of shared floats
     for (long row0 = blockIdx.x * (long)RPB; row0 < a.rows; row0 += gridDim.x * (long)RPB, turn ^= 1) {
         const long row = row0 + rg;
         const bool live = row < a.rows;
-        float ss = 0.f, dot = 0.f;
+        float ss = 0.f, dot = 0.f, top = 0.f;
         Row r0;
         if constexpr (kAhead) {
             r0 = ahead;
@@ -421,19 +471,55 @@ __global__ void __launch_bounds__(L > 32 ? L : kThreads) residual_norm_bwd_kerne
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             const int e = (l + L * j) * V;
+            if (e >= a.D) continue;
             float w[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) w[i] = 0.f;
-            if (e < a.D) Pack<float, V>::load(a.w + e, w);
+            Pack<float, V>::load(a.w + e, w);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 ss = fmaf(x[j][i], x[j][i], ss);
                 dot = fmaf(dn[j][i] * w[i], x[j][i], dot);
+                top = fmaxf(top, fabsf(x[j][i]));
             }
         }
         ss = row_sum<L>(ss, s_red[turn]);
-        dot = row_sum<L>(dot, s_red[turn] + SW);
-        const float r = rsqrtf(ss * a.inv_d + a.eps), r2 = r * r;
+        bool carried = top * top > 0.5f * ss;
+        dot = row_sum<L>(dot, s_red[turn] + SW, &carried);
+        const float r = rsqrtf(ss * a.inv_d + a.eps), mean = r * dot * a.inv_d;
+        float carrier = 0.f;
+        int at = -1;                            // the carrier's place among this thread's elements
+        if (carried) {                          // an element has more than half of its row's squares
+            float ss1 = 0.f, dot1 = 0.f, t = 0.f, v = 0.f;
+            auto take = [&](float xe, float te, int k) {
+                const bool is = xe * xe > 0.5f * ss;
+                ss1 += is ? 0.f : xe * xe;
+                dot1 += is ? 0.f : te * xe;
+                t = is ? te : t;
+                v = is ? xe : v;
+                at = is ? k : at;
+            };
+            if constexpr (kAhead) {
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    const int e = (l + L * j) * V;
+                    if (e >= a.D) continue;
+                    float w[V];
+                    Pack<float, V>::load(a.w + e, w);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) take(x[j][i], dn[j][i] * w[i], j * V + i);
+                }
+            } else {                            // wide rows have no registers to spare: read again, one by one
+#pragma unroll 1
+                for (int k = 0; k < NJ * V; ++k) {
+                    const int e = (l + L * (k / V)) * V + k % V;
+                    if (live && e < a.D)
+                        take(to_f32(static_cast<const TR *>(a.x)[row * a.xs + e]),
+                             to_f32(static_cast<const T *>(a.dn)[row * a.dns + e]) * a.w[e], k);
+                }
+            }
+            ss1 = row_sum<L>(ss1, s_red[turn] + 3 * SW);
+            dot1 = row_sum<L>(dot1, s_red[turn] + 4 * SW);
+            carrier = carrier_back(t, v, r, ss1, dot1, a.eps, a.inv_d);
+        }
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             const int e = (l + L * j) * V;
@@ -447,7 +533,9 @@ __global__ void __launch_bounds__(L > 32 ? L : kThreads) residual_norm_bwd_kerne
             for (int i = 0; i < V; ++i) {
                 const float xn = x[j][i] * r;
                 dw[j][i] = fmaf(dn[j][i], xn, dw[j][i]);
-                dx[j][i] += r * norm_back(dn[j][i] * w[i], x[j][i], ss, dot, r2, a.eps, a.inv_d);
+                float b = fmaf(-xn, mean, dn[j][i] * w[i]);
+                b = at == j * V + i ? carrier : b;
+                dx[j][i] += r * b;
                 dc[j][i] = fmaf(dx[j][i], y[j][i], dc[j][i]);
                 c[i] *= dx[j][i];
             }
