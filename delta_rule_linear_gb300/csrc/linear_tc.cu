@@ -52,9 +52,9 @@ namespace {
 using namespace lin;
 
 constexpr float kZeroWeight = -150.f;          // 2^x is 0 in fp32 below this
-// A chunk whose running log2 decays stay within +-kMildSpan is attended with e^{G_i - G_C} taken out of the
-// row: O_i = e^{G_i - G_C} (q_i (e^{G_C} S) + sum_j s_ij w_j v_j), w_j = e^{G_C - G_j} the weights that the
-// memory takes too: one accumulator and one factor per column, none beyond 2^124.  Stronger decays (a
+// A mild chunk (is_mild) is attended with e^{G_i - G_C} taken out of the row:
+// O_i = e^{G_i - G_C} (q_i (e^{G_C} S) + sum_j s_ij w_j v_j), w_j = e^{G_C - G_j} the weights that the
+// memory takes too: one accumulator and one factor per column, none beyond 2^62.  Stronger decays (a
 // restart among them) get every weight e^{G_i - G_j} from its own exponent and the first term
 // rescaled in between.
 constexpr int kMaxSegs = 64;                   // segments of a sequence at most (equal lengths)
@@ -122,7 +122,7 @@ struct WalkCtl {
     uint64_t full[2], done[2], s_full, q_free, p_ready, r_ready, o_full, o_free, s_ready, v_ready, lo_ready, hi_done, kv_done, cleared, start, last;
     uint32_t tmem;
     int fail;
-    int strong[2];   // the chunk's decays exceed kMildSpan
+    int strong[2];   // the chunk is not mild
 };
 static_assert(sizeof(WalkCtl) <= 256, "control block");
 
@@ -235,8 +235,7 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             if (lane == 31) behind = 0.f;
             x.x += before; x.y += before; x.z += before; x.w += before;
             e = make_float4(ex2(e.x + behind), ex2(e.y + behind), ex2(e.z + behind), ex2(behind));
-            const bool mild = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))) <= kMildSpan;
-            const int strong = !__all_sync(0xffffffffu, mild);
+            const int strong = !__all_sync(0xffffffffu, is_mild(x, __shfl_sync(0xffffffffu, x.w, 31)));
             if (c >= 2 && !wt.warp(&ctl->done[s], ((c >> 1) - 1) & 1, 1)) break;
             float *ga = arr_g(c);
             *reinterpret_cast<float4 *>(ga + 4 * lane) = x;

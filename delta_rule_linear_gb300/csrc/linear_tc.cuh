@@ -17,13 +17,21 @@ constexpr int kC = 128;                        // tokens per chunk
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kStatusDeviceTimeout = 8;        // KDA_ERR_DEVICE_TIMEOUT
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMildSpan = 62.f;              // running log2 decays of a chunk that factors over rows and columns
+constexpr float kMildSpan = 62.f;
 
 // 2^x (ex2.approx: 2 ulp; results below 2^-126 are 0)
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// Whether a chunk's weights e^{G_i - G_j} factor over rows and columns, e^{G_i - G_C} e^{G_C - G_j}: its running log2
+// decays (a lane's four, `end` the last of all) lie within kMildSpan of the chunk's start and of its end, so that no
+// factor passes 2^62.  Decays that only fall are mild by the first alone; ones that fall and grow again would have
+// columns of up to 2^124, which times a score passes fp32 where no result does.
+__device__ __forceinline__ bool is_mild(const float4 &x, float end) {
+    const float top = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)), low = fminf(fminf(x.x, x.y), fminf(x.z, x.w));
+    return fmaxf(top, top - end) <= kMildSpan && fminf(low, low - end) >= -kMildSpan;
 }
 __device__ __forceinline__ void named_sync(int id, int count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");

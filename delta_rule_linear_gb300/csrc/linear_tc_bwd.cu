@@ -485,8 +485,8 @@ linear_state_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
 // (S and R go in as two bf16 parts for those dots).  Row factors are left to the stores,
 //     dQ_i = E_i [dO (e^{G_C} S)^T + sum_j m_ij w_j k_j],   E_i = c e^{G_i - G_C},
 //     dK_j = w_j [V R^T + sum_i m_ij E_i q_i],   dV_j = w_j [K R + sum_i s_ij E_i do_i],   w_j = e^{G_C - G_j},
-// which takes one multiplication per element and no exponential, as long as the chunk's log2 decays stay within
-// +-kMildSpan; beyond that every weight has its own exponent and the first terms are rescaled in place.
+// which takes one multiplication per element and no exponential, as long as the chunk is mild (is_mild); otherwise
+// every weight has its own exponent and the first terms are rescaled in place.
 constexpr int kGradThreads = 17 * 32;
 
 template <int DK, int DV>
@@ -772,8 +772,7 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                 if (lane == 0) before = 0.f;
                 x = make_float4(x.x + before, x.y + before, x.z + before, x.w + before);
                 const float end = __shfl_sync(0xffffffffu, x.w, 31);
-                const bool mild = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))) <= kMildSpan;
-                const int strong = !__all_sync(0xffffffffu, mild);
+                const int strong = !__all_sync(0xffffffffu, is_mild(x, end));
                 if (lane == 0) ctl->strong = strong;
                 *reinterpret_cast<float4 *>(ga + 4 * lane) = x;
                 *reinterpret_cast<float4 *>(ae + 4 * lane) = make_float4(w.scale * ex2(x.x - end), w.scale * ex2(x.y - end),

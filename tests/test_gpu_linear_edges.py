@@ -84,3 +84,53 @@ def test_broadcast_inputs_equal_copies(kda, T, dtype):
             o0 = kda.linear_decode_step(*(x[n][:, 0] for n in names[:3]), d["decay"][:, 0].contiguous(), s0)
             o1 = kda.linear_decode_step(*(c[n][:, 0] for n in names[:3]), d["decay"][:, 0].contiguous(), s1)
             assert torch.equal(o0, o1) and torch.equal(s0, s1)
+
+
+def _terms(q, k, v, decay, h0, d_o, dhT):
+    """Root sum of squares of the terms of each row of o, dq, dk and dv of one chunk (one head per q/k head): what the
+    roundings of the weights and of the memories' elements are relative to, where the terms cancel too."""
+    G = np.cumsum(decay, 1).transpose(0, 2, 1)                                     # [B, H, T]
+    w = np.exp(G[..., :, None] - G[..., None, :]) * np.tril(np.ones(G.shape[-1:] * 2))
+    c = q.shape[-1] ** -0.5
+    t = lambda x: x.transpose(0, 2, 1, 3)  # noqa: E731
+    q, k, v, d_o = t(q), t(k), t(v), t(d_o)
+    P, M = c * w * (q @ np.swapaxes(k, -1, -2)), c * w * (d_o @ np.swapaxes(v, -1, -2))
+    into, out = np.exp(G)[..., None], np.exp(G[..., -1:] - G)[..., None]
+    norm2 = lambda x: (x * x).sum(-1, keepdims=True)  # noqa: E731
+    T = lambda x: np.swapaxes(x, -1, -2)  # noqa: E731
+    rows = dict(o=(P ** 2 @ norm2(v), c * into, q, h0), dq=(M ** 2 @ norm2(k), c * into, d_o, T(h0)),
+                dk=(T(M) ** 2 @ norm2(q), out, v, T(dhT)), dv=(T(P) ** 2 @ norm2(d_o), out, k, dhT))
+    return {n: np.sqrt(a + f ** 2 * (x ** 2 @ m ** 2).sum(-1, keepdims=True))[..., 0].transpose(0, 2, 1)
+            for n, (a, f, x, m) in rows.items()}
+
+
+@pytest.mark.parametrize("heads", [2, 24])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("first,size", [("fall", 4), ("grow", 32)])
+def test_decays_that_fall_and_grow_in_a_chunk(kda, first, size, D, heads):
+    """Log decays that sum to -60 (base 2) and then to +60 within a chunk, or the other way round: weights of 2^120 between
+    its tokens or the inverse of them, times scores of some 2^8 (fall) or 2^14 (grow), and finite results in every row (v
+    and d_o are small enough).  A row may hang on one weight, rounded to bf16 (2^-8 = 2 U8 of its term), beside its own
+    rounding and, before the growth, that of the memory's operand (U8 each): 4 U8 of the row's terms.  (ddecay adds
+    products of all four inputs and may pass fp32.)"""
+    import torch
+    T = 128
+    d, _ = _make(1, T, heads, 1, D, D, "bf16", seed=31)
+    for x, f in (("q", size), ("k", size), ("v", 2.0 ** -10), ("d_o", 2.0 ** -10), ("h0", 2.0 ** -10), ("dhT", 2.0 ** -10)):
+        d[x] = f * d[x]
+    g = np.zeros(T)
+    g[:40], g[40:120] = -60 / 40 * np.log(2), 120 / 80 * np.log(2)
+    d["decay"] = _t(np.repeat((g if first == "fall" else -g)[None, :, None], heads, 2), torch.float32)
+    n = {x: None if t is None else _np(t) for x, t in d.items()}
+    ro, rh = ref.forward(n["q"], n["k"], n["v"], n["decay"], n["h0"])
+    want = dict(ref.backward(n["q"], n["k"], n["v"], n["decay"], n["h0"], n["d_o"], n["dhT"]), o=ro)
+    terms = _terms(**n)
+    assert max(np.abs(x).max() for x in (rh, *want.values())) < 2.0 ** 124 or first == "grow"
+    o, h = kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], check_device=True)
+    got = dict(kda.linear_chunk_bwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], d["d_o"], d["dhT"], check_device=True), o=o)
+    for x in ("o", "dq", "dk", "dv"):
+        assert torch.isfinite(got[x]).all(), x
+        err = np.linalg.norm(_np(got[x]) - want[x], axis=-1) / np.maximum(terms[x], np.linalg.norm(want[x], axis=-1))
+        assert err.max() <= 4 * ref.U8, (x, err.max())
+    assert ref.frob(_np(h), rh) <= ref.TC_STATE
+    assert ref.frob(_np(got["dh0"]), want["dh0"]) <= ref.TC_STATE
