@@ -118,18 +118,21 @@ __device__ __forceinline__ float row_sum(float x, float *s, bool *any = nullptr)
     return x;
 }
 
-// 1 / (1 + 2^(-a log2 e)): approximate operations that flush what is below 2^-126 (a sigmoid of -88 or less), without
-// the scaling that keeps subnormals, which every element would pay for
-__device__ __forceinline__ float sigmoid(float a) {
+// s = 1 / (1 + e), e = 2^(-a log2 e): approximate operations that flush what is below 2^-126 (a sigmoid of -88 or
+// less), without the scaling that keeps subnormals, which every element would pay for.  `rest`: 1 - s = e s, with all its
+// bits where s is next to 1 (and 1 where e is infinite).
+__device__ __forceinline__ float sigmoid(float a, float &rest) {
     float e, s;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * a));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+    rest = fminf(e * s, 1.f);
     return s;
 }
 
-// act(a) and its derivative.  kind: 0 none, 1 silu, 2 sigmoid.
+// act(a).  kind: 1 silu, 2 sigmoid.
 __device__ __forceinline__ float act_of(float a, int kind) {
-    const float s = sigmoid(a);
+    float rest;
+    const float s = sigmoid(a, rest);
     return kind == 1 ? a * s : s;
 }
 
@@ -262,7 +265,9 @@ __global__ void __launch_bounds__(kThreads, V == 4 && NJ == 1 ? 4 : 1) gated_nor
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                sg[j][i] = ACT ? sigmoid(g[j][i]) : 1.f;
+                float rest = 0.f;
+                sg[j][i] = ACT ? sigmoid(g[j][i], rest) : 1.f;
+                if (ACT == 2) g[j][i] = rest;   // a sigmoid's gate is not looked at again
                 ss = fmaf(x[j][i], x[j][i], ss);
                 dot = fmaf(t_of(j, i), x[j][i], dot);
                 top = fmaxf(top, fabsf(x[j][i]));
@@ -311,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, V == 4 && NJ == 1 ? 4 : 1) gated_nor
             for (int i = 0; i < V; ++i) {
                 const float s = sg[j][i], xn = x[j][i] * r, d = dy[j][i];
                 const float ac = ACT == 1 ? g[j][i] * s : s;
-                const float da = ACT == 1 ? fmaf(ac, 1.f - s, s) : s * (1.f - s);
+                const float da = ACT == 1 ? fmaf(ac, 1.f - s, s) : s * g[j][i];
                 dw[j][i] = fmaf(d * ac, xn, dw[j][i]);
                 g[j][i] = d * xn * w[j][i] * da;
                 x[j][i] = r * fmaf(-xn, mean, d * ac * w[j][i]);

@@ -97,3 +97,45 @@ def test_rows_at_the_end_of_the_range_have_finite_gradients(kda, large):
     plain = [i for i in range(len(x)) if i != 7]
     for dx in (kda.gated_norm_bwd(DY[:, None], X[:, None], None, W, eps=EPS)["dx"][:, 0], kda.residual_norm_bwd(DY, None, X, W, eps=EPS)["dx"]):
         assert torch.isfinite(dx).all() and float(dx[plain].abs().max()) <= 1e5 / large
+
+
+def _gates(rows, D):
+    """Every row the same x, so that y / act(gate) is one value, and gates over the whole range of a sigmoid."""
+    return np.linspace(-80.0, 80.0, rows * D).astype(np.float32).reshape(rows, 1, D)
+
+
+@pytest.mark.parametrize("D", [64, 77])
+def test_the_gradient_of_a_closed_or_open_sigmoid_gate(kda, D):
+    """Element by element: s (1 - s) has as many bits for a gate of 80 as for one of -80 (a difference taken from 1 has
+    three digits at 10 and none above 17).  An exponential with an exponent rounded at 80 and some ten operations: ref.F32."""
+    import torch
+    a = _gates(300, D)
+    x = np.broadcast_to(np.random.default_rng(3).normal(size=D).astype(np.float32), a.shape)
+    w, dy = np.ones(D, np.float32), np.random.default_rng(4).normal(size=a.shape).astype(np.float32)
+    f = a.astype(np.float64)
+    r = 1 / np.sqrt((x.astype(np.float64) ** 2).mean(-1, keepdims=True) + EPS)
+    want = dy * x * r / (1.0 + np.exp(-f)) / (1.0 + np.exp(f))
+    got = kda.gated_norm_bwd(*(_t(z, torch.float32) for z in (dy, x, a, w)), eps=EPS, activation="sigmoid")["dgate"]
+    err = np.abs(_np(got) - want) / np.abs(want)
+    assert err.max() <= ref.F32, (err.max(), a.reshape(-1)[err.argmax()])
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_infinite_and_nan_gates(kda, dtype):
+    """The limits where there are any, NaN where the formula has one, and other elements unharmed."""
+    import torch
+    dt = getattr(torch, dtype)
+    x, w = torch.ones(2, 1, 64, device="cuda", dtype=dt), torch.ones(64, device="cuda")
+    a = torch.zeros_like(x)
+    inf = float("inf")
+    a[0, 0, :5] = torch.tensor([inf, -inf, float("nan"), 1e30, -1e30], device="cuda", dtype=dt)
+    y = {act: kda.gated_norm_fwd(x, a, w, eps=0.0, activation=act)[0, 0].float() for act in ("silu", "sigmoid")}
+    assert y["sigmoid"][0] == 1 and y["sigmoid"][1] == 0 and y["sigmoid"][2].isnan() and y["sigmoid"][3] == 1 and y["sigmoid"][4] == 0
+    assert y["silu"][0] == inf and y["silu"][1].isnan() and y["silu"][2].isnan() and y["silu"][3] > 9e29 and y["silu"][4] == 0
+    assert (y["sigmoid"][5:] == 0.5).all() and (y["silu"][5:] == 0).all()
+    a[0, 0, :3] = 0
+    for act, half in (("sigmoid", 0.25), ("silu", 0.5)):
+        g = kda.gated_norm_bwd(x, x, a, w, eps=0.0, activation=act)
+        d = g["dgate"][0, 0].float()
+        assert d[3] == (0 if act == "sigmoid" else 1) and d[4] == 0 and (d[5:] == half).all()
+        assert torch.isfinite(g["dx"][1]).all()
