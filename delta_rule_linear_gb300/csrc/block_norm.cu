@@ -119,20 +119,30 @@ __device__ __forceinline__ float row_sum(float x, float *s, bool *any = nullptr)
 }
 
 // s = 1 / (1 + e), e = 2^(-a log2 e): approximate operations that flush what is below 2^-126 (a sigmoid of -88 or
-// less), without the scaling that keeps subnormals, which every element would pay for.  `rest`: 1 - s = e s, with all its
-// bits where s is next to 1 (and 1 where e is infinite).
+// less), without the scaling that keeps subnormals, which every element would pay for.  An exponent p = a log2 e rounded
+// to fp32 is off by up to 2^-24 |p|, 3e-6 of e at |a| = 80: a bf16 result does not show that; for fp32 (T) what p lost,
+// which an FMA gives exactly, and what the constant lost, go in to the first order, 2^-d = 1 - d ln 2.  `rest`: 1 - s = e s, with all its bits where s is next to 1 (and 1
+// where e is infinite).
+template <typename T>
 __device__ __forceinline__ float sigmoid(float a, float &rest) {
+    constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = 1.925963033e-8f, kLn2 = 0.6931471805599453f;
+    const float p = kLog2e * a;
     float e, s;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * a));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-p));
+    if constexpr (sizeof(T) == 4) {
+        const float low = fmaf(kLog2eLow, a, fmaf(kLog2e, a, -p));
+        e = fabsf(p) < 126.f ? fmaf(e, -kLn2 * low, e) : e;     // beyond it e is 0 or infinite, or a NaN
+    }
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
     rest = fminf(e * s, 1.f);
     return s;
 }
 
 // act(a).  kind: 1 silu, 2 sigmoid.
+template <typename T>
 __device__ __forceinline__ float act_of(float a, int kind) {
     float rest;
-    const float s = sigmoid(a, rest);
+    const float s = sigmoid<T>(a, rest);
     return kind == 1 ? a * s : s;
 }
 
@@ -202,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) gated_norm_fwd_kernel(GatedNorm a) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     float y = v[j][i] * r * w[j][i];
-                    if (a.act) y *= act_of(ga[j][i], a.act);
+                    if (a.act) y *= act_of<T>(ga[j][i], a.act);
                     v[j][i] = y;
                 }
                 Pk::store(yp + e, v[j]);
@@ -266,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, V == 4 && NJ == 1 ? 4 : 1) gated_nor
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 float rest = 0.f;
-                sg[j][i] = ACT ? sigmoid(g[j][i], rest) : 1.f;
+                sg[j][i] = ACT ? sigmoid<T>(g[j][i], rest) : 1.f;
                 if (ACT == 2) g[j][i] = rest;   // a sigmoid's gate is not looked at again
                 ss = fmaf(x[j][i], x[j][i], ss);
                 dot = fmaf(t_of(j, i), x[j][i], dot);
@@ -299,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, V == 4 && NJ == 1 ? 4 : 1) gated_nor
                     const int e = (l + L * (k / V)) * V + k % V;
                     if (!live || e >= a.D) continue;
                     const float ge = ACT ? to_f32(static_cast<const T *>(a.g.p)[row_at(a.g, rr, a.H, a.D, a.flat) + e]) : 0.f;
-                    const float act = ACT ? act_of(ge, ACT) : 1.f;
+                    const float act = ACT ? act_of<T>(ge, ACT) : 1.f;
                     take(to_f32(static_cast<const T *>(a.x.p)[row_at(a.x, rr, a.H, a.D, a.flat) + e]),
                          to_f32(static_cast<const T *>(a.dy.p)[row_at(a.dy, rr, a.H, a.D, a.flat) + e]) * act * a.w[e], e);
                 }

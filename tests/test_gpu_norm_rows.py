@@ -139,3 +139,25 @@ def test_infinite_and_nan_gates(kda, dtype):
         d = g["dgate"][0, 0].float()
         assert d[3] == (0 if act == "sigmoid" else 1) and d[4] == 0 and (d[5:] == half).all()
         assert torch.isfinite(g["dx"][1]).all()
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+@pytest.mark.parametrize("D", [64, 77])
+def test_fp32_gates_over_the_whole_range(kda, D, act):
+    """Element by element: an exponential of 2^-22, a reciprocal and a reciprocal root of 2^-22.4 and 2^-23, a sum of squares
+    of up to eight terms a lane and some six roundings of 2^-24 are 1.2e-6 together; 1.5e-6 with what the exponent's own
+    rounding leaves once its rest is taken along (left out, that alone is 2.6e-6 at 80)."""
+    import torch
+    a = _gates(300, D)
+    x = np.broadcast_to(np.random.default_rng(3).normal(size=D).astype(np.float32), a.shape)
+    w, dy = np.ones(D, np.float32), np.random.default_rng(4).normal(size=a.shape).astype(np.float32)
+    X, A, W, DY = (_t(z, torch.float32) for z in (x, a, w, dy))
+    want = ref.gated_norm(x, a, w, EPS, act)
+    err = np.abs(_np(kda.gated_norm_fwd(X, A, W, eps=EPS, activation=act)) - want) / np.abs(want).clip(1e-300)
+    assert err[a != 0].max() <= 1.5e-6, (err[a != 0].max(), a[a != 0][err[a != 0].argmax()])
+    if act == "sigmoid":
+        f = a.astype(np.float64)
+        r = 1 / np.sqrt((x.astype(np.float64) ** 2).mean(-1, keepdims=True) + EPS)
+        want = dy * x * r / (1.0 + np.exp(-f)) / (1.0 + np.exp(f))
+        err = np.abs(_np(kda.gated_norm_bwd(DY, X, A, W, eps=EPS, activation=act)["dgate"]) - want) / np.abs(want)
+        assert err.max() <= 2e-6, (err.max(), a.reshape(-1)[err.argmax()])
