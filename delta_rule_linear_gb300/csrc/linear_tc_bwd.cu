@@ -19,7 +19,7 @@
 // For a group of (sequence, head) pairs, first every chunk's S and R (the two are one kernel on other
 // operands: the weighted values go in as three bf16 parts, as in the forward), then everything else, all chunks
 // at once.  S and R come
-//   of enough pairs from one launch that walks the chunks, the memory in TMEM;
+//   of enough pairs from one launch that walks the chunks, the memory in registers;
 //   of few pairs from two: every chunk's own contribution, all chunks at once, then the two chains over
 //   the chunks, elementwise and in place.
 // A walk takes 1.4 to 2.1 us a chunk of d = 128 however many pairs fit the machine, the other way 0.11 us a
@@ -287,20 +287,22 @@ __global__ void __launch_bounds__(256) linear_chain_kernel(BwdParams w, int cell
 }
 
 // ------------------------------------------------------------------------------ 1 and 2 at once: the walk
-// A CTA walks the chunks of one (direction, pair) for 64 key channels: the memory stays in TMEM in fp32, is stored
-// to each chunk's slot, decayed, and takes the chunk's product.  A chunk's chain is the product (24 steps of N = 64)
-// and the memory's way through registers, 2000 to 2400 clocks; loads and stores run beside it.  The weighted
-// values of the next chunk do too, and take as long: 14 instructions a pair of them, in either half of a memory's CTAs.
+// A CTA walks the chunks of one (direction, pair) for 64 key channels: the memory stays in fp32 registers, is stored
+// to each chunk's slot, decayed, and takes the chunk's contribution, a product of its own (24 steps of N = 64) in one of
+// two TMEM accumulators, rounded to nearest.  Added up in the accumulator itself it would be cut 24 times a chunk, always
+// towards 0: without decays that came to 1.2e-4 of the memory over 32,768 tokens.  The products wait for nothing of the
+// memory's, so what a chunk takes is the conversion of its weighted values: 14 instructions a pair of them, in either half
+// of a memory's CTAs.
 // Warps 0-7: weighted values; 8-11: the memory; 12: decays and TMA; 13: products.
 template <int DV>
 struct StateCfg {
     static constexpr int KB = kC * 128, VB = kC * DV * 2, STAGE = KB + VB, NST = 4;
     static constexpr int ARR = NST * STAGE, CTL = ARR + NST * kC * 4, SMEM = CTL + 256;
-    static constexpr int T_V = 128;             // the memory [64], then two sets of hi, mid, lo
+    static constexpr int T_V = 128;             // two accumulators [64], then two sets of hi, mid, lo
     static_assert(SMEM <= 232448, "shared memory");
 };
 struct StateCtl {
-    uint64_t full[4], empty[4], ready[2], used[2], s_ready, d_full, last;
+    uint64_t full[4], empty[4], ready[2], used[2], d_full[2], d_free[2], last;
     float alpha[4];
     uint32_t tmem;
     int fail;
@@ -327,14 +329,14 @@ linear_state_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&ctl->full[i], 1);
-            mbar_init(&ctl->empty[i], 1);
+            mbar_init(&ctl->empty[i], 1 + 128);   // the product has read the tiles, the memory's threads the factor
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->ready[i], 256);
             mbar_init(&ctl->used[i], 1);
+            mbar_init(&ctl->d_full[i], 1);
+            mbar_init(&ctl->d_free[i], 128);
         }
-        mbar_init(&ctl->s_ready, 128);
-        mbar_init(&ctl->d_full, 1);
         mbar_init(&ctl->last, 1);
         ctl->fail = 0;
         fence_mbar_init();
@@ -376,18 +378,18 @@ linear_state_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         constexpr uint32_t id = idesc_bf16_f32(128, 64, false, true);
         for (int n = 0; n < nch; ++n) {
             const int s = n % NST;
-            if (!wt.warp(&ctl->full[s], (n / NST) & 1, 62) || !wt.warp(&ctl->ready[n & 1], (n >> 1) & 1, 63) ||
-                !wt.warp(&ctl->s_ready, n & 1, 64)) break;
+            if (!wt.warp(&ctl->full[s], (n / NST) & 1, 62) || !wt.warp(&ctl->ready[n & 1], (n >> 1) & 1, 63)) break;
+            if (n >= 2 && !wt.warp(&ctl->d_free[n & 1], ((n >> 1) - 1) & 1, 64)) break;
             tc_fence_after();
             const uint64_t dk = desc_mnmajor_sw128(smem_u32(smem + s * Cf::STAGE), kC, 0);
-            const uint32_t a = tm + Cf::T_V + (n & 1) * 192;
+            const uint32_t a = tm + Cf::T_V + (n & 1) * 192, d = tm + (n & 1) * 64;
             if (lane == 0) {
-                product_ts<true>(tm, a, dk, id);
-                product_ts<true>(tm, a + 64, dk, id);
-                product_ts<true>(tm, a + 128, dk, id);
+                product_ts<false>(d, a, dk, id);
+                product_ts<true>(d, a + 64, dk, id);
+                product_ts<true>(d, a + 128, dk, id);
                 mma_commit(&ctl->used[n & 1]);
                 mma_commit(&ctl->empty[s]);
-                mma_commit(&ctl->d_full);
+                mma_commit(&ctl->d_full[n & 1]);
             }
             __syncwarp();
         }
@@ -408,52 +410,42 @@ linear_state_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         const int i = tid - 256;                // value channel
         const float *init = dir ? w.dhT : w.h0;
         const size_t own = (size_t)64 * part * DV + i;
-        uint32_t x[2][32];
+        float x[2][32];
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                x[k][j] = init && i < DV ? __float_as_uint(init[(size_t)pair * DK * DV + own + (32 * k + j) * DV]) : 0u;
+            for (int j = 0; j < 32; ++j) x[k][j] = init && i < DV ? init[(size_t)pair * DK * DV + own + (32 * k + j) * DV] : 0.f;
         bool ok = true;
         for (int n = 0; n < nch; ++n) {
             const int s = n % NST;
-            ok = wt.warp(&ctl->full[s], (n / NST) & 1, 67) && (n == 0 || wt.warp(&ctl->d_full, (n - 1) & 1, 68));
-            if (!ok) break;
-            tc_fence_after();
-            if (n > 0) {
-                tmem_ld32(tlane, x[0]);
-                tmem_ld32(tlane + 32, x[1]);
-                tmem_ld_wait();
-            }
+            if (!(ok = wt.warp(&ctl->full[s], (n / NST) & 1, 67))) break;
             const float al = ctl->alpha[s];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t y[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(al * __uint_as_float(x[k][j]));
-                tmem_st32(tlane + 32 * k, y);
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&ctl->s_ready);
+            mbar_arrive(&ctl->empty[s]);
             float *p = (dir ? w.R : w.S) + ((size_t)pi * nch + chunk_of(n)) * DK * DV + own;
             if (i < DV)
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) p[(32 * k + j) * DV] = __uint_as_float(x[k][j]);
-        }
-        if (dir && w.dh0 && ok && wt.warp(&ctl->d_full, (nch - 1) & 1, 69)) {
+                    for (int j = 0; j < 32; ++j) p[(32 * k + j) * DV] = x[k][j];
+            if (!(ok = wt.warp(&ctl->d_full[n & 1], (n >> 1) & 1, 68))) break;
             tc_fence_after();
-            tmem_ld32(tlane, x[0]);
-            tmem_ld32(tlane + 32, x[1]);
-            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t y[32];
+                tmem_ld32(tlane + (n & 1) * 64 + 32 * k, y);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[k][j] = fmaf(al, x[k][j], __uint_as_float(y[j]));
+            }
+            tc_fence_before();
+            mbar_arrive(&ctl->d_free[n & 1]);
+        }
+        if (dir && w.dh0 && ok && i < DV) {
             float *p = w.dh0 + (size_t)pair * DK * DV + own;
-            if (i < DV)
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) p[(32 * k + j) * DV] = __uint_as_float(x[k][j]);
+                for (int j = 0; j < 32; ++j) p[(32 * k + j) * DV] = x[k][j];
         }
     }
     tc_fence_before();

@@ -1,0 +1,41 @@
+"""Memories of linear attention that are kept over thousands of tokens.
+
+Without decays a memory and its gradient are plain sums, h_T = h_0 + sum k_t v_t^T and dh_0 = dh_T + c sum q_t do_t^T.
+Tensor-core accumulators cut each addition, always towards 0, so a chunk's contribution (24 steps of 16 tokens and parts)
+loses some 24 2^-25 = 7e-7 of itself however long the sequence is, as long as it is not added to the memory in there, which
+would lose as much of the whole every chunk: 64 chunks would be 1.5e-5 or more.  Added in fp32, rounded to nearest, 64
+chunks err by sqrt(64) 2^-25 = 2.4e-7 beside it: 2^-19 together, with a margin of two.
+"""
+import pytest
+
+pytestmark = pytest.mark.gpu
+MEMORY = 2.0 ** -19
+
+
+@pytest.fixture(scope="module")
+def kda():
+    import delta_rule_linear_gb300 as m
+    m.load()
+    return m
+
+
+def _inputs(T, H, dk, dv):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(17)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    q, k, v, d_o = (r(1, T, H, d).bfloat16() for d in (dk, dk, dv, dv))
+    return q, k, v, d_o, r(1, H, dk, dv), r(1, H, dk, dv)
+
+
+def _rel(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("heads", [2, 40])
+@pytest.mark.parametrize("dims", [(64, 64), (64, 128), (128, 64), (128, 128)], ids=str)
+def test_gradient_of_a_memory_kept_throughout(kda, dims, heads):
+    import torch
+    q, k, v, d_o, h0, dhT = _inputs(8192, heads, *dims)
+    got = kda.linear_chunk_bwd(q, k, v, None, h0, d_o, dhT, check_device=True)["dh0"]
+    want = dhT.double() + dims[0] ** -0.5 * torch.einsum("bthi,bthj->bhij", q.double(), d_o.double())
+    assert _rel(got, want) <= MEMORY
