@@ -73,5 +73,15 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t *r) {
                  : "memory");
 }
 
+// A warp group's registers a thread from here on: fewer, which others may then take, or more, which waits for them.
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 }  // namespace ptx
 }  // namespace kda

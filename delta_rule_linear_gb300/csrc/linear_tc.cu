@@ -6,32 +6,34 @@
 //     O = diag(e^G) Q S  +  P V,         P[i][j] = (q_i . k_j) e^{G_i - G_j}   (j <= i)
 //     S_next = e^{G_C} S + K^T (diag(e^{G_C - G}) V)
 //
-// One CTA walks the chunks of one (sequence, head) or of one segment of it; the memory stays in TMEM in
+// One CTA walks the chunks of one (sequence, head) or of one segment of it; the memory stays in registers in
 // fp32 as S^T [dv, dk].  Per chunk four products of M = 128 rows (tokens, or value channels):
 //
 //     1  scores = Q K^T                     (operands as TMA writes them)
 //     2  O = Q S_bf16                       (S rounded to a bf16 operand in shared memory)
 //     3  O += P V                           (P written back to TMEM as the A operand)
-//     4  S^T += Vw^T K,  Vw = hi + mid + lo (three products; Vw^T written to TMEM as the A operand)
+//     4  Vw^T K,  Vw = hi + mid + lo        (three products; Vw^T written to TMEM as the A operand)
 //
 // What is rounded: P and the operand copy of S to bf16, each once, so O errs by three bf16
 // roundings with its own (2.3e-3 of it, against 1.7e-3 for the last one alone); the memory itself
 // must not, since a model carries it over tens of thousands of tokens and reads it back in fp32: the
 // decayed values w v go in as the sum of three bf16s, which is w v as fp32 has it (two parts, 16
-// bits, leave 2.4e-6 in the memory), k is exact, and S accumulates in fp32.
+// bits, leave 2.4e-6 in the memory), k is exact, and a chunk's product is added to S in fp32 registers, rounded to
+// nearest.  (Added up in the tensor cores' accumulator, S would be cut at each of the 24 steps of a chunk, always towards
+// 0: 3.8e-5 of a memory kept over 32,768 tokens, against 3e-7.  It costs 3 % at dk = 128, nothing at 64.)
 //
 // Bound: 2 (2 dk + 2 dv) bytes per token and head through HBM; per chunk of d = 128 that is 128 KB,
-// 5900 clocks of an SM's share at the measured 6.8 TB/s.  A chunk takes 6700 (8 x 4096 tokens, 19 heads: one CTA
-// per SM, 127 us, 5.0 TB/s), of d = 64 5100 (half the bytes).  What the CTA itself is short of is TMEM and
+// 5900 clocks of an SM's share at the measured 6.8 TB/s.  A chunk takes 6900 (8 x 4096 tokens, 19 heads: one CTA
+// per SM, 131 us, 4.8 TB/s), of d = 64 5100 (half the bytes).  What the CTA itself is short of is TMEM and
 // shared-memory bandwidth: beside the passes over values, memory and outputs a product's step of 16 takes 130 to
 // 230 clocks (64 alone), and the passes take longer beside the products; and instruction fetch.  So the two
 // products that can take their A operand from TMEM do, values are transposed by ldmatrix, products are issued from
 // one-lane branches, and every role's loop is kept to a few hundred instructions (fully unrolled, the roles
 // evicted each other's code and the walk took 1.5 times as long).
 //
-// Warps 0-3: scores -> P.  4-7: outputs.  8-11: the memory's operand copy and its decay.  12-19: Vw.
-// 20: decays and TMA.  21: issues the products.  The groups and the tensor pipe work on different
-// stages of neighbouring chunks, so that none of their latencies adds up.
+// Warps 0-3: scores -> P.  4-7: outputs.  8-15: the memory and its operand copy.  16-23: Vw.
+// 24: decays and TMA.  25: issues the products.  (26 and 27 fill their warp group.)  The groups and the tensor pipe
+// work on different stages of neighbouring chunks, so that none of their latencies adds up.
 //
 // Few heads and long sequences: a sequence is cut into segments.  A first launch (local kernel)
 // leaves, for all but the last, the memory it adds from zero; the walk starts segment p from
@@ -43,6 +45,7 @@
 // Every wait is bounded (2 s); a time-out is recorded in the workspace header and the CTA unwinds.
 #include <algorithm>
 #include <initializer_list>
+#include <type_traits>
 
 #include "linear_tc.cuh"
 
@@ -50,6 +53,14 @@ namespace kda {
 namespace {
 
 using namespace lin;
+
+// The registers that warp groups trade have to be what the launch holds, or the trade never ends.
+template <typename K>
+cudaError_t check_regs(K *kernel, int regs) {
+    cudaFuncAttributes f;
+    const cudaError_t e = cudaFuncGetAttributes(&f, kernel);
+    return e != cudaSuccess ? e : f.numRegs == regs ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
 
 constexpr float kZeroWeight = -150.f;          // 2^x is 0 in fp32 below this
 // A mild chunk (is_mild) is attended with e^{G_i - G_C} taken out of the row:
@@ -110,7 +121,7 @@ struct WalkCfg {
     static constexpr int ARR = SB + DK * DV * 2;                // per chunk parity: G [128], w [128]
     static constexpr int CTL = ARR + 2 * 2 * kC * 4;
     static constexpr int SMEM = CTL + 256;
-    // TMEM columns: the memory [dv][dk], scores / P, O, the three parts of the decayed values.  At d = 128 there is
+    // TMEM columns: a chunk's product 4 [dv][dk] (first the start state), scores / P, O, the three parts of the decayed values.  At d = 128 there is
     // room for two of them, and lo follows hi once that is used
     static constexpr bool OWN_LO = DK + DV <= 192;
     static constexpr int T_S = 0, T_P = DK, T_O = DK + 128, T_V = DK + 128 + DV, T_LO = OWN_LO ? T_V + 128 : T_V;
@@ -126,7 +137,19 @@ struct WalkCtl {
 };
 static_assert(sizeof(WalkCtl) <= 256, "control block");
 
-constexpr int kWalkThreads = 22 * 32;
+constexpr int kWalkThreads = 28 * 32;
+// dk = 128: a thread of the memory holds 64 of its channels, and registers are split by warp groups (four warps: P, outputs,
+// twice the memory, twice the values, the rest).  What one gives up another takes; all there is, is what the launch holds.
+// Calls do not go with that, so the waits are short ones, which cost 3 %; dk = 64 needs neither.
+constexpr int kWalkRegs = 72, kRegsP = 48, kRegsO = 64, kRegsM = 96, kRegsV = 64, kRegsC = 72;
+static_assert(kRegsP + kRegsO + 2 * kRegsM + 2 * kRegsV + kRegsC <= 7 * kWalkRegs, "more than the launch holds: an endless wait");
+template <int DK, int N>
+__device__ __forceinline__ void reg_split() {
+    if constexpr (DK == 128 && N < kWalkRegs) reg_dec<N>();
+    if constexpr (DK == 128 && N > kWalkRegs) reg_inc<N>();
+}
+__device__ __forceinline__ Waits walk_waits(WalkCtl *ctl, WsHeader *hdr, std::false_type) { return {&ctl->fail, hdr}; }
+__device__ __forceinline__ ShortWaits walk_waits(WalkCtl *ctl, WsHeader *, std::true_type) { return {&ctl->fail}; }
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kWalkThreads, 1)
@@ -156,17 +179,17 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             mbar_init(&ctl->done[i], 1);
         }
         for (uint64_t *x : {&ctl->s_full, &ctl->q_free, &ctl->o_full, &ctl->hi_done, &ctl->kv_done, &ctl->last}) mbar_init(x, 1);
-        for (uint64_t *x : {&ctl->p_ready, &ctl->r_ready, &ctl->o_free, &ctl->s_ready}) mbar_init(x, 128);
-        for (uint64_t *x : {&ctl->v_ready, &ctl->lo_ready, &ctl->cleared}) mbar_init(x, 256);
+        for (uint64_t *x : {&ctl->p_ready, &ctl->r_ready, &ctl->o_free}) mbar_init(x, 128);
+        for (uint64_t *x : {&ctl->s_ready, &ctl->v_ready, &ctl->lo_ready, &ctl->cleared}) mbar_init(x, 256);
         mbar_init(&ctl->start, 512);
         ctl->fail = 0;
         fence_mbar_init();
     }
-    if (warp == 21) {
+    if (warp == 25) {
         tmem_alloc(&ctl->tmem, 512);
         tmem_relinquish();
     }
-    if (warp == 20 && lane == 0) {
+    if (warp == 24 && lane == 0) {
         tma_prefetch_desc(&mq);
         tma_prefetch_desc(&mk);
         tma_prefetch_desc(&mv);
@@ -175,7 +198,7 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = ctl->tmem;
-    const Waits wt{&ctl->fail, w.hdr};
+    const auto wt = walk_waits(ctl, w.hdr, std::integral_constant<bool, DK == 128>());
     const uint32_t tlane = tm + ((uint32_t)(32 * (warp & 3)) << 16);   // this warp's 32 TMEM lanes
     auto arr_g = [&](int c) { return reinterpret_cast<float *>(smem + Cf::ARR) + (c & 1) * 2 * kC; };
     auto stage = [&](int c) { return smem + (c & 1) * Cf::STAGE; };
@@ -213,7 +236,8 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         mbar_arrive(&ctl->start);
     }
 
-    if (warp == 20) {
+    if (warp >= 24) reg_split<DK, kRegsC>();
+    if (warp == 24) {
         // ---- decays and loads
         const float *gp = w.g.p ? w.g.p + b * w.g.b + tb * w.g.t + hv : nullptr;
         float4 d = load_decay(w.g, gp, t0 + 4 * lane, t1);
@@ -256,7 +280,7 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             }
             if (c + 1 < nch) d = load_decay(w.g, gp, u + kC + 4 * lane, t1);
         }
-    } else if (warp == 21) {
+    } else if (warp == 25) {
         // ---- products
         constexpr uint32_t id1 = idesc_bf16_f32(128, 128, false, false);
         constexpr uint32_t id2 = idesc_bf16_f32(128, DV, false, false);
@@ -310,7 +334,7 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             if (!wt.warp(&ctl->v_ready, ph, 6)) break;
             tc_fence_after();
             if (lane == 0) {
-                product_ts<true>(tm + Cf::T_S, tm + Cf::T_V, dk, id4);
+                product_ts<false>(tm + Cf::T_S, tm + Cf::T_V, dk, id4);
                 if (!Cf::OWN_LO) mma_commit(&ctl->hi_done);
                 product_ts<true>(tm + Cf::T_S, tm + Cf::T_V + 64, dk, id4);
             }
@@ -332,6 +356,7 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         }
     } else if (warp < 4) {
         // ---- scores -> P (thread = token row)
+        reg_split<DK, kRegsP>();
         const int row = tid;
         for (int c = 0; c < nch; ++c) {
             const float *ga = arr_g(c), *wa = ga + kC;
@@ -378,6 +403,7 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         }
     } else if (warp < 8) {
         // ---- outputs (thread = token row)
+        reg_split<DK, kRegsO>();
         const int row = tid - 128;
         float gi = 0.f, gc = 0.f;              // G of the row and of the chunk and the chunk's kind, read a
         bool next_strong = false;              // chunk ahead (their places are reused)
@@ -443,62 +469,74 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
                     if (u0 + j < t1) *reinterpret_cast<uint4 *>(op + (long long)j * w.ot + cb) = r[j];
             }
         }
-    } else if (warp < 12) {
-        // ---- the memory (thread = value channel i, TMEM lane i; dv = 64: warps 8 and 9)
-        const int i = tid - 256;
+    } else if (warp < 16) {
+        // ---- the memory (thread = value channel i, TMEM lane i, half of the key channels; dv = 64: half of the warps)
+        reg_split<DK, kRegsM>();
+        constexpr int NB = DK / 64;                // blocks of 32 key channels
+        const int i = tid & 127, k0 = (warp >> 2 & 1) * (DK / 2);
+        const bool mine = (i & ~31) < DV;
         uint8_t *sb = smem + Cf::SB;
+        float S[NB][32], alpha = 0.f;
+        // what the start, or the last chunk's products, left in TMEM is added
+        auto add = [&]() {
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int h = 0; h < 32; h += 16) {
+                    uint32_t x[16];
+                    tmem_ld16(tlane + Cf::T_S + k0 + 32 * n + h, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) S[n][h + j] = fmaf(alpha, S[n][h + j], __uint_as_float(x[j]));
+                }
+        };
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) S[n][j] = 0.f;
         for (int c = 0; c < nch; ++c) {
             if (!wt.warp(&ctl->full[c & 1], (c >> 1) & 1, 16)) break;
-            const float alpha = ex2(arr_g(c)[kC - 1]), beta = ctl->strong[c & 1] ? 1.f : alpha;
+            const float next = ex2(arr_g(c)[kC - 1]), beta = ctl->strong[c & 1] ? 1.f : next;
             if (c == 0 ? !wt.warp(&ctl->start, 0, 25)
                        : !wt.warp(&ctl->q_free, (c - 1) & 1, 17) || !wt.warp(&ctl->kv_done, (c - 1) & 1, 18)) break;
             tc_fence_after();
-            if (warp - 8 < DV / 32) {
-#pragma unroll 1
-                for (int cb = 0; cb < DK; cb += 32) {
-                    uint32_t x[32];
-                    tmem_ld32(tlane + Cf::T_S + cb, x);
-                    tmem_ld_wait();
-                    // operand: row i, 32 key channels
+            if (mine) {
+                add();
+                // operand: row i, 32 key channels at a time
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
 #pragma unroll
                     for (int j = 0; j < 32; j += 8) {
                         uint4 p;
                         uint32_t *pp = &p.x;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            pp[k] = pack_bf16(beta * __uint_as_float(x[j + 2 * k]), beta * __uint_as_float(x[j + 2 * k + 1]));
-                        *reinterpret_cast<uint4 *>(sb + piece(DV, i, (cb + j) / 8)) = p;
+                        for (int k = 0; k < 4; ++k) pp[k] = pack_bf16(beta * S[n][j + 2 * k], beta * S[n][j + 2 * k + 1]);
+                        *reinterpret_cast<uint4 *>(sb + piece(DV, i, (k0 + 32 * n + j) / 8)) = p;
                     }
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(alpha * __uint_as_float(x[j]));
-                    tmem_st32(tlane + Cf::T_S + cb, x);
-                }
-                tmem_st_wait();
                 fence_proxy_async();
                 tc_fence_before();
             }
+            alpha = next;
             mbar_arrive(&ctl->s_ready);
         }
         // the final memory
-        if (w.hT && it.p == it.nseg - 1 && warp - 8 < DV / 32) {
-            float *hp = w.hT + pair * DK * DV + i;
+        if (w.hT && it.p == it.nseg - 1 && mine) {
+            float *hp = w.hT + (pair * DK + k0) * DV + i;
             if (nch == 0) {                    // an empty sequence keeps its memory
-                for (int j = 0; j < DK; ++j) hp[j * DV] = w.h0 ? w.h0[(pair * DK + j) * DV + i] : 0.f;
+                for (int j = 0; j < DK / 2; ++j) hp[j * DV] = w.h0 ? w.h0[(pair * DK + k0 + j) * DV + i] : 0.f;
             } else if (wt.warp(&ctl->kv_done, (nch - 1) & 1, 19)) {
                 tc_fence_after();
-#pragma unroll 1
-                for (int cb = 0; cb < DK; cb += 32) {
-                    uint32_t x[32];
-                    tmem_ld32(tlane + Cf::T_S + cb, x);
-                    tmem_ld_wait();
+                add();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) hp[(cb + j) * DV] = __uint_as_float(x[j]);
-                }
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) hp[(32 * n + j) * DV] = S[n][j];
             }
         }
-    } else {
+    } else if (warp < 24) {
         // ---- decayed values (thread = value channel, half of the tokens)
-        const int ch = (tid - 384) & 127, half = (tid - 384) >> 7;
+        reg_split<DK, kRegsV>();
+        const int ch = tid & 127, half = (tid - 512) >> 7;
         const bool mine = (ch & ~31) < DV;
         for (int c = 0; c < nch; ++c) {
             if (!wt.warp(&ctl->full[c & 1], (c >> 1) & 1, 20)) break;
@@ -536,13 +574,14 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 21) {
+    if (warp == 25) {
         // nothing of this CTA's is in flight once its last product and loads have landed (a bounded
         // wait: after a time-out they may not have)
         if (lane == 0) mma_commit(&ctl->last);
         __syncwarp();
         (void)mbar_wait(&ctl->last, 0, kWaitNs);
-        if (ctl->fail) {
+        if (const int where = ctl->fail) {
+            if (DK == 128 && lane == 0 && atomicCAS(&w.hdr->error, 0, kStatusDeviceTimeout) == 0) w.hdr->where = where;
             const uint64_t t = globaltimer_ns();
             while (globaltimer_ns() - t < 1000000ull) {
             }
@@ -821,6 +860,10 @@ cudaError_t go(const LinFwd &a, const TcWalk &w, long items, bool split, const C
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if ((e = walk_once(linear_chunk_kernel<DK, DV>, WC::SMEM)) != cudaSuccess) return e;
+    if constexpr (DK == 128) {
+        static const cudaError_t held = check_regs(linear_chunk_kernel<DK, DV>, kWalkRegs);
+        if (held != cudaSuccess) return held;
+    }
     if (split) return launch_after(linear_chunk_kernel<DK, DV>, grid, kWalkThreads, WC::SMEM, st, mq, mk, mv, w);
     linear_chunk_kernel<DK, DV><<<grid, kWalkThreads, WC::SMEM, st>>>(mq, mk, mv, first);
     return cudaGetLastError();

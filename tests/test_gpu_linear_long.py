@@ -39,3 +39,29 @@ def test_gradient_of_a_memory_kept_throughout(kda, dims, heads):
     got = kda.linear_chunk_bwd(q, k, v, None, h0, d_o, dhT, check_device=True)["dh0"]
     want = dhT.double() + dims[0] ** -0.5 * torch.einsum("bthi,bthj->bhij", q.double(), d_o.double())
     assert _rel(got, want) <= MEMORY
+
+
+@pytest.mark.parametrize("heads", [2, 40])
+@pytest.mark.parametrize("dims", [(64, 64), (64, 128), (128, 64), (128, 128)], ids=str)
+def test_a_memory_kept_throughout_a_whole_walk(kda, dims, heads):
+    """In place, a sequence is not cut: one walk over all its chunks."""
+    import torch
+    q, k, v, _, h0, _ = _inputs(8192, heads, *dims)
+    want = h0.double() + torch.einsum("bthi,bthj->bhij", k.double(), v.double())
+    st = h0.clone()
+    kda.linear_chunk_fwd(q, k, v, None, st, final_state=st, check_device=True)
+    assert _rel(st, want) <= MEMORY
+
+
+def test_a_memory_kept_over_calls(kda):
+    """The memory handed on from call to call, decays between: as the fp64 sum of all its tokens."""
+    import torch
+    q, k, v, _, h0, _ = _inputs(8192, 4, 128, 128)
+    g = torch.full((1, 8192, 4), -2.0 ** -13, device="cuda")
+    w = ((8191 - torch.arange(8192, device="cuda")).double() * -2.0 ** -13).exp()
+    want = h0.double() * float(torch.tensor(-1.0).exp()) + torch.einsum("t,bthi,bthj->bhij", w, k.double(), v.double())
+    h = h0
+    for t in range(0, 8192, 1024):
+        s = slice(t, t + 1024)
+        h = kda.linear_chunk_fwd(q[:, s], k[:, s], v[:, s], g[:, s].contiguous(), h, check_device=True)[1]
+    assert _rel(h, want) <= MEMORY
