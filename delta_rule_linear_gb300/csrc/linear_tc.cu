@@ -601,11 +601,11 @@ struct LocalCfg {
     static constexpr int ARR = NST * STAGE;                    // per stage: w [128]
     static constexpr int CTL = ARR + NST * kC * 4;
     static constexpr int SMEM = CTL + 256;
-    static constexpr int T_V = DK;                             // two sets of hi, mid, lo
+    static constexpr int T_V = DK;                             // a chunk's product [DK], two sets of hi, mid, lo
     static_assert(T_V + 384 <= 512 && SMEM <= 232448, "TMEM, shared memory");
 };
 struct LocalCtl {
-    uint64_t full[4], empty[4], ready[2], used[2], last;
+    uint64_t full[4], empty[4], ready[2], used[2], d_full, d_free;
     uint32_t tmem;
     int fail;
     int cmd[4];        // 1: a chunk, 0: no more
@@ -613,10 +613,10 @@ struct LocalCtl {
 };
 static_assert(sizeof(LocalCtl) <= 256, "control block");
 
-// The memory one segment adds from zero.  Warps 0-7: weighted values (thread = channel, half of the
-// tokens), the segment's total decay, the result; 8: decays and TMA, from the segment's last chunk to its
-// first; 9: products.
-constexpr int kLocalThreads = 10 * 32;
+// The memory one segment adds from zero, in registers as in the walk.  Warps 0-7: weighted values (thread = channel,
+// half of the tokens), the segment's total decay; 8: decays and TMA, from the segment's last chunk to its first; 9:
+// products; 12-19: the memory (thread = channel, half of the key channels); 10 and 11 bring these to their TMEM lanes.
+constexpr int kLocalThreads = 20 * 32;
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kLocalThreads, 1)
@@ -641,13 +641,14 @@ linear_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&ctl->full[i], 1);
-            mbar_init(&ctl->empty[i], 1);
+            mbar_init(&ctl->empty[i], 1 + 256);     // the product has read the tiles, the memory's threads the command
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->ready[i], 256);
             mbar_init(&ctl->used[i], 1);
         }
-        mbar_init(&ctl->last, 1);
+        mbar_init(&ctl->d_full, 1);
+        mbar_init(&ctl->d_free, 256);
         ctl->fail = 0;
         fence_mbar_init();
     }
@@ -726,24 +727,60 @@ linear_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
             if (!wt.warp(&ctl->full[s], (n / NST) & 1, 33)) break;
             if (!ctl->cmd[s]) break;
             if (!wt.warp(&ctl->ready[n & 1], (n >> 1) & 1, 34)) break;
+            if (n > 0 && !wt.warp(&ctl->d_free, (n - 1) & 1, 37)) break;
             tc_fence_after();
             const uint64_t dk = desc_mnmajor_sw128(smem_u32(smem + s * Cf::STAGE), kC, 0);
             const uint32_t a = tm + Cf::T_V + (n & 1) * 192;
             if (lane == 0) {
-                if (n)
-                    product_ts<true>(tm, a, dk, id);
-                else
-                    product_ts<false>(tm, a, dk, id);
+                product_ts<false>(tm, a, dk, id);
                 product_ts<true>(tm, a + 64, dk, id);
                 product_ts<true>(tm, a + 128, dk, id);
                 mma_commit(&ctl->used[n & 1]);
                 mma_commit(&ctl->empty[s]);
+                mma_commit(&ctl->d_full);
             }
             __syncwarp();
         }
-        if (lane == 0) mma_commit(&ctl->last);
-        __syncwarp();
-    } else {
+    } else if (warp >= 12) {
+        constexpr int NB = DK / 64;             // blocks of 32 key channels
+        const int ch = tid & 127, k0 = ((warp >> 2) & 1) * (DK / 2);
+        const bool mine = (ch & ~31) < DV;
+        const uint32_t tlane = tm + ((uint32_t)(32 * (warp & 3)) << 16);
+        float S[NB][32];
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) S[i][j] = 0.f;
+        bool ok;
+        for (int n = 0;; ++n) {
+            const int s = n % NST;
+            ok = wt.warp(&ctl->full[s], (n / NST) & 1, 38);
+            if (!ok || !ctl->cmd[s]) break;
+            mbar_arrive(&ctl->empty[s]);
+            ok = wt.warp(&ctl->d_full, n & 1, 39);
+            if (!ok) break;
+            tc_fence_after();
+            if (mine) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    uint32_t x[32];
+                    tmem_ld32(tlane + k0 + 32 * i, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) S[i][j] += __uint_as_float(x[j]);
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&ctl->d_free);
+        }
+        if (ok && mine) {
+            float *lp = w.loc + (((size_t)item * w.HV + hv) * DK + k0) * DV + ch;
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) lp[(32 * i + j) * DV] = S[i][j];
+        }
+    } else if (warp < 8) {
         // total decay of the segment, in a fixed order; its largest decay
         float sum = 0.f, top = -INFINITY;
         for (int u = tid; u < w.L; u += 256) {
@@ -763,11 +800,10 @@ linear_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
         }
         named_sync(2, 256);
         named_arrive(1, 288);                   // the producer warp may look at them
-        const size_t slot = (size_t)item * w.HV + hv;
         if (tid == 0) {
             float all = 0.f;
             for (int i = 0; i < 8; ++i) all += ctl->red[i];
-            w.gam[slot] = ex2(all);
+            w.gam[(size_t)item * w.HV + hv] = ex2(all);
         }
         const int ch = tid & 127, half = tid >> 7;
         const bool mine = (ch & ~31) < DV;
@@ -782,20 +818,6 @@ linear_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
             if (mine) put_values<3>(smem + s * Cf::STAGE + Cf::KB, wa + s * kC, ch, 64 * half, a, a + 64, a + 128);
             tc_fence_before();
             mbar_arrive(&ctl->ready[n & 1]);
-        }
-        if (wt.warp(&ctl->last, 0, 37)) {
-            tc_fence_after();
-            if (mine) {                         // half of the key channels
-                float *lp = w.loc + slot * DK * DV + ch;
-#pragma unroll 1
-                for (int cb = half * (DK / 2); cb < (half + 1) * (DK / 2); cb += 32) {
-                    uint32_t x[32];
-                    tmem_ld32(tlane + cb, x);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) lp[(cb + j) * DV] = __uint_as_float(x[j]);
-                }
-            }
         }
     }
     tc_fence_before();

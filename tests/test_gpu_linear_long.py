@@ -65,3 +65,25 @@ def test_a_memory_kept_over_calls(kda):
         s = slice(t, t + 1024)
         h = kda.linear_chunk_fwd(q[:, s], k[:, s], v[:, s], g[:, s].contiguous(), h, check_device=True)[1]
     assert _rel(h, want) <= MEMORY
+
+
+@pytest.mark.parametrize("heads", [1, 3, 20, 40])
+@pytest.mark.parametrize("dims", [(64, 64), (64, 128), (128, 64), (128, 128)], ids=str)
+def test_a_memory_kept_throughout_segments(kda, dims, heads):
+    """A long sequence of few heads is cut, up to 64 chunks to a segment, whose local memories are added."""
+    import torch
+    q, k, v, _, h0, _ = _inputs(8192, heads, *dims)
+    want = h0.double() + torch.einsum("bthi,bthj->bhij", k.double(), v.double())
+    assert _rel(kda.linear_chunk_fwd(q, k, v, None, h0, check_device=True)[1], want) <= MEMORY
+
+
+def test_memories_kept_throughout_a_long_packed_sequence(kda):
+    """Packed sequences longer than an SM's share are cut as well."""
+    import torch
+    lens = [16384, 70, 3000]
+    q, k, v, _, _, _ = _inputs(sum(lens), 4, 64, 64)
+    cu = torch.tensor([0, 16384, 16454, 19454], dtype=torch.int32)
+    h = kda.linear_varlen_fwd(q, k, v, cu.cuda(), cu_seqlens_cpu=cu, check_device=True)[1]
+    for i, (a, b) in enumerate(zip(cu.tolist(), cu.tolist()[1:])):
+        want = torch.einsum("bthi,bthj->bhij", k[:, a:b].double(), v[:, a:b].double())
+        assert _rel(h[i:i + 1], want) <= MEMORY
