@@ -485,7 +485,7 @@ template <int DK, int DV>
 struct GradCfg {
     static constexpr int QB = kC * DK * 2, VB = kC * DV * 2, XB = DK * DV * 2;
     static constexpr int Q = 0, K = QB, V = 2 * QB, O = 2 * QB + VB, XH = 2 * QB + 2 * VB, XL = XH + XB;
-    static constexpr int ARR = XL + XB;         // G, E, w, then quarters of: r, c, q dots, k dots
+    static constexpr int ARR = XL + XB;         // G, E (what G's fp32 lost, where not mild), w, then quarters of: r, c, q dots, k dots
     static constexpr int CTL = ARR + 19 * kC * 4, SMEM = CTL + 256;
     static_assert(SMEM <= 232448, "shared memory");
 };
@@ -554,6 +554,30 @@ __device__ __noinline__ void scale_row(uint32_t taddr, float f) {
     for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(f * __uint_as_float(x[i]));
     tmem_st32(taddr, x);
     tmem_st_wait();
+}
+
+// Running sums of a lane's four log2 decays and all before them as sums of two floats, x + low.  A restart counts as -150,
+// so that a few of them leave fp32 no bits for the decays between: 2^-24 of 2000 is 1e-4 of a weight.
+struct Two {
+    float h, l;
+};
+__device__ __forceinline__ Two add(const Two &a, const Two &b) {
+    const float s = a.h + b.h, v = s - a.h, r = (a.h - (s - v)) + (b.h - v) + (a.l + b.l), h = s + r;   // exact sum, then both tails
+    return {h, r - (h - s)};
+}
+__device__ __noinline__ void running_sums(const float4 &d, int lane, float4 &x, float4 &low) {
+    const Two a = {d.x, 0.f}, b = add(a, {d.y, 0.f}), c = add(b, {d.z, 0.f}), e = add(c, {d.w, 0.f});
+    Two run = e;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const Two y = {__shfl_up_sync(0xffffffffu, run.h, off), __shfl_up_sync(0xffffffffu, run.l, off)};
+        if (lane >= off) run = add(y, run);
+    }
+    Two before = {__shfl_up_sync(0xffffffffu, run.h, 1), __shfl_up_sync(0xffffffffu, run.l, 1)};
+    if (lane == 0) before = {0.f, 0.f};
+    const Two p = add(before, a), q = add(before, b), r = add(before, c), s = add(before, e);
+    x = make_float4(p.h, q.h, r.h, s.h);
+    low = make_float4(p.l, q.l, r.l, s.l);
 }
 
 template <int DK, int DV>
@@ -752,7 +776,8 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             // ---- S (asked for at the end of the item before), the decays
             if (warp == 0) {
                 const float *gp = w.g.p ? w.g.p + b * w.g.b + hv : nullptr;
-                float4 x = load_decay(w.g, gp, u + 4 * lane, w.T);
+                const float4 d = load_decay(w.g, gp, u + 4 * lane, w.T);
+                float4 x = d;
                 x.y += x.x; x.z += x.y; x.w += x.z;
                 float up = x.w;
 #pragma unroll
@@ -766,17 +791,23 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                 const float end = __shfl_sync(0xffffffffu, x.w, 31);
                 const int strong = !__all_sync(0xffffffffu, is_mild(x, end));
                 if (lane == 0) ctl->strong = strong;
+                float4 e;
+                if (strong)
+                    running_sums(d, lane, x, e);
+                else
+                    e = make_float4(w.scale * ex2(x.x - end), w.scale * ex2(x.y - end), w.scale * ex2(x.z - end),
+                                    w.scale * ex2(x.w - end));
                 *reinterpret_cast<float4 *>(ga + 4 * lane) = x;
-                *reinterpret_cast<float4 *>(ae + 4 * lane) = make_float4(w.scale * ex2(x.x - end), w.scale * ex2(x.y - end),
-                                                                         w.scale * ex2(x.z - end), w.scale * ex2(x.w - end));
+                *reinterpret_cast<float4 *>(ae + 4 * lane) = e;
                 *reinterpret_cast<float4 *>(aw + 4 * lane) = make_float4(ex2(end - x.x), ex2(end - x.y), ex2(end - x.z), ex2(end - x.w));
             }
             if (!meet()) break;
             const float gr = ga[row], gc = ga[kC - 1];
             const bool strong = ctl->strong;
+            const float lr = strong ? ae[row] : 0.f, lc = strong ? ae[kC - 1] : 0.f;
             // row factors of dQ and of dK, dV at the end; of the first terms in place
             const float fq = strong ? 1.f : ae[row], fk = strong ? 1.f : aw[row];
-            const float iq = w.scale * ex2(gr), ik = ex2(gc - gr);
+            const float iq = w.scale * ex2(gr), ik = ex2((gc - gr) + (lc - lr));
             put_x(xs, strong ? 1.f : ex2(gc));
             fence_proxy_async();                 // here, where the products are waited for (1500 clocks before `go`)
             if (!wt.warp(&ctl->full_qk, it & 1, 58) || !done(53)) break;   // Q and K are read here too
@@ -800,7 +831,7 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                             *reinterpret_cast<float4 *>(e + j) = *reinterpret_cast<const float4 *>(ae + i0 + j);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) e[j] = w.scale * ex2(ga[i0 + j] - gr);
+                        for (int j = 0; j < 16; ++j) e[j] = w.scale * ex2((ga[i0 + j] - gr) + (ae[i0 + j] - lr));
                     }
                     if (part == quad) {          // nothing from before the row's own token, W not from it either
 #pragma unroll
@@ -842,7 +873,7 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                             *reinterpret_cast<float4 *>(e + j) = *reinterpret_cast<const float4 *>(aw + j0 + j);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) e[j] = w.scale * ex2(gr - ga[j0 + j]);
+                        for (int j = 0; j < 16; ++j) e[j] = w.scale * ex2((gr - ga[j0 + j]) + (lr - ae[j0 + j]));
                     }
                     if (part == quad) {
 #pragma unroll
