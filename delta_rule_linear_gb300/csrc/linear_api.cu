@@ -133,6 +133,7 @@ kda_status kda_linear_varlen_fwd(const void *q, const void *k, const void *v, co
     kda_status c = check_shape(N, 0, H, HV, dk, dv, dtype);
     if (c != KDA_OK) return c;
     if (total_T < 0) return KDA_ERR_SHAPE;
+    if (N == 0 && total_T > 0) return KDA_ERR_INDEX;      // tokens of no sequence: nobody would write their outputs
     if (N > 0 && !cu_seqlens) return KDA_ERR_NULL;
     if (!al(cu_seqlens, 4)) return KDA_ERR_ALIGN;
     LinFwd a{};

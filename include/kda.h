@@ -471,7 +471,8 @@ kda_status kda_linear_chunk_fwd(const void *q, const void *k, const void *v, con
                                 size_t ws_bytes, kda_stream_t stream);
 
 /* Packed sequences: token arrays [1,total_T,..], cu_seqlens / cu_seqlens_host as kda_varlen_fwd
- * (the host copy also tells how to split the work), one memory per sequence. */
+ * (the host copy also tells how to split the work), one memory per sequence.  Tokens of no sequence
+ * (N == 0, total_T > 0) are KDA_ERR_INDEX. */
 size_t kda_linear_varlen_fwd_workspace(int N, int total_T, int H, int HV, int dk, int dv,
                                        kda_dtype dtype);
 kda_status kda_linear_varlen_fwd(const void *q, const void *k, const void *v, const float *decay,

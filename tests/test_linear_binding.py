@@ -217,3 +217,14 @@ def test_outputs_are_no_broadcast_views(lib):
     assert not lib.launched
     kda.linear_chunk_fwd(x, x, x, out=_on_device(torch.zeros(2, 4, 3, 32)[:, :, :2]))
     assert len(lib.launched) == 1
+
+
+def test_tokens_of_no_sequence_are_refused():
+    """Packed tokens with an empty list of sequences: no kernel would write their outputs (dummy addresses, never read)."""
+    import ctypes
+    from delta_rule_linear_gb300 import build, _lib
+    build.build()
+    lib, p = _lib.load(), ctypes.c_void_p(0x1000)
+    call = lambda total: lib.kda_linear_varlen_fwd(p, p, p, p, 0, p, None, None, p, None, None, 0, total, 2, 2, 64, 64, 1,  # noqa: E731
+                                                   0.0, p, 1 << 40, None)
+    assert call(10) == 9 and call(0) == 0
