@@ -46,9 +46,10 @@ bool view(LinView &v, const void *p, const long long *strides, int i, long B, lo
 }
 
 // Whether the chunked tensor-core form takes this problem.  A chunk costs the same whatever it
-// holds; the token walk costs less for a few tokens.  Prefill on the device, walk and chunk: one sequence,
-// 4 heads of 64, 16 tokens 5.6 and 7.1 us, 32 tokens 7.5 and 7.1; 4 heads of 128, 16 tokens 8.5 and 8.9, 32 tokens
-// 11.2 and 8.9 (gradients 26 and 21, 29 and 21); 16 x 32 heads of 128 gain from 8 tokens on (76 and 33).
+// holds; the token walk costs less for a few tokens.  On the device, walk and chunk, 16 tokens: prefill of one
+// sequence, 4 heads of 64 5.0 and 7.8 us, of 128 7.1 and 9.6, of 16 x 32 heads of 128 56 and 35; gradients 8.7 and 15.2,
+// 9.2 and 21, 98 and 117.  32 tokens: prefill 7.0 and 7.9, 9.5 and 9.7, 77 and 35; gradients 10.8 and 15.0, 12.4 and 21,
+// 175 and 121.  One limit serves both; gradients of one sequence with few heads would gain by the walk up to 64 tokens.
 bool use_tc(int dk, int dv, kda_dtype dt, int max_len) {
     return linear_tc_supported(dk, dv, to_dtype(dt)) && max_len > 16;
 }

@@ -1,5 +1,5 @@
-// linear_ptx.cuh -- the tcgen05, TMA and ldmatrix forms that only the linear-attention kernels use (the shared
-// ones: tc_ptx.cuh).
+// linear_ptx.cuh -- the tcgen05, TMA, ldmatrix and register-split forms that only the linear-attention kernels use (the
+// shared ones: tc_ptx.cuh).
 #pragma once
 
 #include "tc_ptx.cuh"

@@ -835,12 +835,12 @@ linear_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
 }
 
 // ------------------------------------------------------------------------------ host
-// Chunks per segment.  In units of one chunk of the walk (3.6 us at d = 128, 2.6 at 64), a CTA costs about 3 to set up,
+// Chunks per segment.  In units of one chunk of the walk (3.7 us at d = 128, 2.6 at 64), a CTA costs about 3 to set up,
 // fill and drain, a chunk of the local kernel 0.5, its launch 1, a start state 0.2 per earlier segment; every
 // (sequence, head) that finds no SM waits for the next wave.  Equal lengths: the cut with the least of it, and
 // of cuts within 5 % the coarsest (a long segment's local memory stops early where decays are strong: B=1 T=32768
-// H=32 with softplus decays, 4 segments 0.31 ms, 9 segments 0.36 ms).  Of all cuts of nine shapes, 2048 to
-// 32,768 tokens, 1 to 128 heads, it picks the fastest or one within 2 %.  Packed sequences: whole ones while the
+// H=32, 4 segments 0.30 ms, 8 segments 0.36 ms).  Of all cuts of ten shapes, 2048 to 32,768 tokens, 1 to 128 heads, it
+// picks the fastest or one within 1 %, in one 9 % (8192 tokens, 4 heads of 128: 39.0 us for 35.9).  Packed sequences: whole ones while the
 // longest is no more than an SM's share of the work (taken longest first they then fill the SMs evenly),
 // else segments of half an SM's share.
 int plan_chunks(int nseq, int HV, long total, int max_len, bool varlen, int sms) {

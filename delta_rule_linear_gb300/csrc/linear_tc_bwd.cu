@@ -24,9 +24,9 @@
 //   the chunks, elementwise and in place.
 // A walk takes 1.4 to 2.1 us a chunk of d = 128 however many pairs fit the machine, the other way 0.11 us a
 // chunk and pair or, where a group has room for few pairs, the latency of the chains (costs in `walks` below).  All
-// gradients of 2 x 2048 tokens, 16 heads of 128: 96 us walked, 112 the other way; of 2048 tokens, 14 heads:
-// 60 and 50; of 2 x 2048 tokens, 16 heads of 64: 63 and 57; of 32,768 tokens, 16 heads of 128: 815 and 1209.  Of 22
-// shapes the choice is the faster one or within 6 % of it.
+// gradients of 2 x 2048 tokens, 16 heads of 128, on the device: 92 us walked, 107 the other way; of 2048 tokens, 14
+// heads: 55 and 46; of 2 x 2048 tokens, 16 heads of 64: 61 and 54; of 32,768 tokens, 16 heads of 128: 813 and 1252.  Of
+// 12 shapes the choice is the faster one, in one 7 % off it (8192 tokens, 14 heads: 203 for 189).
 // The contributions of a group stay within L2, where the chains read them: 2 x 64 KB a chunk at d = 128 and
 // at most kGroupChunks chunks.  A walk's memories are read back once, and a wider group fills the machine: kWalkChunks
 // of them (32,768 tokens, 16 heads: 814 us, with half as many 1187).  A larger problem is taken group by
@@ -478,7 +478,8 @@ linear_state_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
 //     dQ_i = E_i [dO (e^{G_C} S)^T + sum_j m_ij w_j k_j],   E_i = c e^{G_i - G_C},
 //     dK_j = w_j [V R^T + sum_i m_ij E_i q_i],   dV_j = w_j [K R + sum_i s_ij E_i do_i],   w_j = e^{G_C - G_j},
 // which takes one multiplication per element and no exponential, as long as the chunk is mild (is_mild); otherwise
-// every weight has its own exponent and the first terms are rescaled in place.
+// every weight has its own exponent and the first terms are rescaled in place (99 us instead of 92 with 2 x 2048 tokens).
+// 17 warps leave a thread 96 registers, of which 44 to 120 bytes spill.
 constexpr int kGradThreads = 17 * 32;
 
 template <int DK, int DV>

@@ -459,7 +459,8 @@ kda_status kda_gk_chunk_bwd(const void *q, const void *k, const void *v,
  * bf16 with dk, dv in {64, 128} runs by chunks of 128 tokens on the tensor cores (sequences of
  * more than 16 tokens); everything else runs token by token on CUDA cores.  The results do not
  * depend on which beyond rounding: memories and their sums are fp32 in both.  In the chunked form
- * an infinite or NaN v or k reaches the outputs of its whole chunk.
+ * an infinite or NaN v or k reaches the outputs of its whole chunk, and any infinite or NaN input of
+ * the gradients theirs.
  * B, N, T == 0 are allowed (final_state = initial_state, or zeros).  Without a sequence (B or N == 0)
  * nothing is touched, the workspace's header included: there is no error word to ask for.
  */
