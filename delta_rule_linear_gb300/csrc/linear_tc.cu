@@ -20,11 +20,11 @@
 // decayed values w v go in as the sum of three bf16s, which is w v as fp32 has it (two parts, 16
 // bits, leave 2.4e-6 in the memory), k is exact, and a chunk's product is added to S in fp32 registers, rounded to
 // nearest.  (Added up in the tensor cores' accumulator, S would be cut at each of the 24 steps of a chunk, always towards
-// 0: 3.8e-5 of a memory kept over 32,768 tokens, against 3e-7.  It costs 3 % at dk = 128, nothing at 64.)
+// 0: 3.8e-5 of a memory kept over 32,768 tokens, against 3e-7.  It costs 1 % at dk = 128, nothing at 64.)
 //
 // Bound: 2 (2 dk + 2 dv) bytes per token and head through HBM; per chunk of d = 128 that is 128 KB,
-// 5900 clocks of an SM's share at the measured 6.8 TB/s.  A chunk takes 6900 (8 x 4096 tokens, 19 heads: one CTA
-// per SM, 131 us, 4.8 TB/s), of d = 64 5100 (half the bytes).  What the CTA itself is short of is TMEM and
+// 5900 clocks of an SM's share at the measured 6.8 TB/s.  A chunk takes 6800 (8 x 4096 tokens, 19 heads: one CTA
+// per SM, 128 us, 5.0 TB/s), of d = 64 5100 (half the bytes).  What the CTA itself is short of is TMEM and
 // shared-memory bandwidth: beside the passes over values, memory and outputs a product's step of 16 takes 130 to
 // 230 clocks (64 alone), and the passes take longer beside the products; and instruction fetch.  So the two
 // products that can take their A operand from TMEM do, values are transposed by ldmatrix, products are issued from
@@ -122,15 +122,15 @@ struct WalkCfg {
     static constexpr int CTL = ARR + 2 * 2 * kC * 4;
     static constexpr int SMEM = CTL + 256;
     // TMEM columns: a chunk's product 4 [dv][dk] (first the start state), scores / P, O, the three parts of the decayed values.  At d = 128 there is
-    // room for two of them, and lo follows hi once that is used
-    static constexpr bool OWN_LO = DK + DV <= 192;
-    static constexpr int T_S = 0, T_P = DK, T_O = DK + 128, T_V = DK + 128 + DV, T_LO = OWN_LO ? T_V + 128 : T_V;
-    static_assert(T_V + (OWN_LO ? 192 : 128) <= 512, "TMEM");
+    // room for two of them, and hi follows lo once that is used
+    static constexpr bool OWN_HI = DK + DV <= 192;
+    static constexpr int T_S = 0, T_P = DK, T_O = DK + 128, T_V = DK + 128 + DV, T_HI = OWN_HI ? T_V + 128 : T_V;
+    static_assert(T_V + (OWN_HI ? 192 : 128) <= 512, "TMEM");
     static_assert(SMEM <= 232448, "shared memory");
 };
 
 struct WalkCtl {
-    uint64_t full[2], done[2], s_full, q_free, p_ready, r_ready, o_full, o_free, s_ready, v_ready, lo_ready, hi_done, kv_done, cleared, start, last;
+    uint64_t full[2], done[2], s_full, q_free, p_ready, r_ready, o_full, o_free, s_ready, v_ready, hi_ready, lo_done, kv_done, cleared, start, last;
     uint32_t tmem;
     int fail;
     int strong[2];   // the chunk is not mild
@@ -178,9 +178,9 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             mbar_init(&ctl->full[i], 1);
             mbar_init(&ctl->done[i], 1);
         }
-        for (uint64_t *x : {&ctl->s_full, &ctl->q_free, &ctl->o_full, &ctl->hi_done, &ctl->kv_done, &ctl->last}) mbar_init(x, 1);
+        for (uint64_t *x : {&ctl->s_full, &ctl->q_free, &ctl->o_full, &ctl->lo_done, &ctl->kv_done, &ctl->last}) mbar_init(x, 1);
         for (uint64_t *x : {&ctl->p_ready, &ctl->r_ready, &ctl->o_free}) mbar_init(x, 128);
-        for (uint64_t *x : {&ctl->s_ready, &ctl->v_ready, &ctl->lo_ready, &ctl->cleared}) mbar_init(x, 256);
+        for (uint64_t *x : {&ctl->s_ready, &ctl->v_ready, &ctl->hi_ready, &ctl->cleared}) mbar_init(x, 256);
         mbar_init(&ctl->start, 512);
         ctl->fail = 0;
         fence_mbar_init();
@@ -335,21 +335,21 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             tc_fence_after();
             if (lane == 0) {
                 product_ts<false>(tm + Cf::T_S, tm + Cf::T_V, dk, id4);
-                if (!Cf::OWN_LO) mma_commit(&ctl->hi_done);
+                if (!Cf::OWN_HI) mma_commit(&ctl->lo_done);
                 product_ts<true>(tm + Cf::T_S, tm + Cf::T_V + 64, dk, id4);
             }
             __syncwarp();
-            if (!Cf::OWN_LO) {                   // while lo is written over hi
+            if (!Cf::OWN_HI) {                   // while hi is written over lo
                 if (!outputs()) break;
-                if (!wt.warp(&ctl->lo_ready, ph, 7)) break;
+                if (!wt.warp(&ctl->hi_ready, ph, 7)) break;
                 tc_fence_after();
             }
             if (lane == 0) {
-                product_ts<true>(tm + Cf::T_S, tm + Cf::T_LO, dk, id4);
+                product_ts<true>(tm + Cf::T_S, tm + Cf::T_HI, dk, id4);
                 mma_commit(&ctl->kv_done);
             }
             __syncwarp();
-            if (Cf::OWN_LO && !outputs()) break;
+            if (Cf::OWN_HI && !outputs()) break;
             if (lane == 0) mma_commit(&ctl->done[ph]);
             __syncwarp();
             if (c + 1 < nch) ok = scores(c + 1);
@@ -561,15 +561,15 @@ linear_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
                 if (!wt.warp(&ctl->cleared, 0, 24)) break;
             }
             tc_fence_after();
-            if (mine) put_values<Cf::OWN_LO ? 3 : 1>(v, wa, ch, 64 * half, tlane + Cf::T_V, tlane + Cf::T_V + 64, tlane + Cf::T_LO);
+            if (mine) put_values<Cf::OWN_HI ? 3 : 1>(v, wa, ch, 64 * half, tlane + Cf::T_HI, tlane + Cf::T_V + 64, tlane + Cf::T_V);
             tc_fence_before();
             mbar_arrive(&ctl->v_ready);
-            if constexpr (Cf::OWN_LO) continue;
-            if (!wt.warp(&ctl->hi_done, c & 1, 23)) break;
+            if constexpr (Cf::OWN_HI) continue;
+            if (!wt.warp(&ctl->lo_done, c & 1, 23)) break;
             tc_fence_after();
-            if (mine) put_values<2>(v, wa, ch, 64 * half, 0, 0, tlane + Cf::T_LO);
+            if (mine) put_values<2>(v, wa, ch, 64 * half, tlane + Cf::T_HI, 0, 0);
             tc_fence_before();
-            mbar_arrive(&ctl->lo_ready);
+            mbar_arrive(&ctl->hi_ready);
         }
     }
     tc_fence_before();
@@ -732,9 +732,9 @@ linear_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
             const uint64_t dk = desc_mnmajor_sw128(smem_u32(smem + s * Cf::STAGE), kC, 0);
             const uint32_t a = tm + Cf::T_V + (n & 1) * 192;
             if (lane == 0) {
-                product_ts<false>(tm, a, dk, id);
+                product_ts<false>(tm, a + 128, dk, id);
                 product_ts<true>(tm, a + 64, dk, id);
-                product_ts<true>(tm, a + 128, dk, id);
+                product_ts<true>(tm, a, dk, id);
                 mma_commit(&ctl->used[n & 1]);
                 mma_commit(&ctl->empty[s]);
                 mma_commit(&ctl->d_full);

@@ -91,7 +91,9 @@ struct ShortWaits {
 };
 
 // A decayed value x = w v in fp32 goes in as the sum of three bf16s: each takes the top 8 bits of what is
-// left (a truncation, so the rest is exact), together x's 24.
+// left (a truncation, so the rest is exact), together x's 24.  Their products are added up from the smallest part on: the
+// accumulator cuts every step towards 0, by its own size, which is next to nothing until the large part comes (8 of
+// the 24 steps; the other way round a chunk's product lost three times as much).
 __device__ __forceinline__ uint32_t top2(float a, float b) {
     return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
@@ -101,7 +103,7 @@ __device__ __forceinline__ uint32_t piece(int rows, int r, int c) {
     return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 // The decayed values of the warp's 32 channels (from `ch`, its TMEM lanes), tokens t0 .. t0 + 63, as A-operand
-// words (two tokens each) into column t0 / 2 of each part.  PARTS: bit 0 hi and mid, bit 1 lo.  The tile is
+// words (two tokens each) into column t0 / 2 of each part.  PARTS: bit 0 mid and lo, bit 1 hi.  The tile is
 // token-major: ldmatrix transposes it into the layout that a 16x128b store takes (lane l holds channel l / 4,
 // tokens 2 (l % 4) and the next of each 8), 16 channels by 32 tokens a step.
 template <int PARTS>
@@ -122,17 +124,19 @@ __device__ __forceinline__ void put_values(const uint8_t *v, const float *wa, in
         for (int j = 0; j < 8; ++j) {
             const float2 w = *reinterpret_cast<const float2 *>(wa + t + (j >> 1) * 8);
             const float x = w.x * __uint_as_float(r[j] << 16), y = w.y * __uint_as_float(r[j] & 0xffff0000u);
-            h[j] = top2(x, y);
-            const float rx = rest(x), ry = rest(y);
-            m[j] = top2(rx, ry);
-            l[j] = top2(rest(rx), rest(ry));
+            if constexpr (PARTS & 2) h[j] = top2(x, y);
+            if constexpr (PARTS & 1) {
+                const float rx = rest(x), ry = rest(y);
+                m[j] = top2(rx, ry);
+                l[j] = top2(rest(rx), rest(ry));
+            }
         }
         const uint32_t to = ((uint32_t)(u & 1) << 20) + t / 2;  // 16 lanes on
         if constexpr (PARTS & 1) {
-            tmem_st_16x128(hi + to, h);
+            tmem_st_16x128(lo + to, l);
             tmem_st_16x128(mid + to, m);
         }
-        if constexpr (PARTS & 2) tmem_st_16x128(lo + to, l);
+        if constexpr (PARTS & 2) tmem_st_16x128(hi + to, h);
     }
     tmem_st_wait();
 }

@@ -185,9 +185,9 @@ linear_part_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             const uint64_t dk = desc_mnmajor_sw128(smem_u32(smem + s * Cf::STAGE), kC, 0);
             const uint32_t a = tm + Cf::T_V + (n & 1) * 192;
             if (lane == 0) {
-                product_ts<false>(tm, a, dk, id);
+                product_ts<false>(tm, a + 128, dk, id);
                 product_ts<true>(tm, a + 64, dk, id);
-                product_ts<true>(tm, a + 128, dk, id);
+                product_ts<true>(tm, a, dk, id);
                 mma_commit(&ctl->used[n & 1]);
                 mma_commit(&ctl->empty[s]);
                 mma_commit(&ctl->d_full);
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(256) linear_chain_kernel(BwdParams w, int cell
 // A CTA walks the chunks of one (direction, pair) for 64 key channels: the memory stays in fp32 registers, is stored
 // to each chunk's slot, decayed, and takes the chunk's contribution, a product of its own (24 steps of N = 64) in one of
 // two TMEM accumulators, rounded to nearest.  Added up in the accumulator itself it would be cut 24 times a chunk, always
-// towards 0: without decays that came to 1.2e-4 of the memory over 32,768 tokens.  The products wait for nothing of the
+// towards 0: without decays that came to 1.2e-4 of the memory over 32,768 tokens (3e-7 now).  The products wait for nothing of the
 // memory's, so what a chunk takes is the conversion of its weighted values: 14 instructions a pair of them, in either half
 // of a memory's CTAs.
 // Warps 0-7: weighted values; 8-11: the memory; 12: decays and TMA; 13: products.
@@ -384,9 +384,9 @@ linear_state_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             const uint64_t dk = desc_mnmajor_sw128(smem_u32(smem + s * Cf::STAGE), kC, 0);
             const uint32_t a = tm + Cf::T_V + (n & 1) * 192, d = tm + (n & 1) * 64;
             if (lane == 0) {
-                product_ts<false>(d, a, dk, id);
+                product_ts<false>(d, a + 128, dk, id);
                 product_ts<true>(d, a + 64, dk, id);
-                product_ts<true>(d, a + 128, dk, id);
+                product_ts<true>(d, a, dk, id);
                 mma_commit(&ctl->used[n & 1]);
                 mma_commit(&ctl->empty[s]);
                 mma_commit(&ctl->d_full[n & 1]);
@@ -653,10 +653,10 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         // token tile times token tile over D channels, both K-major
         auto gram_k = [&](uint32_t d, uint64_t a, uint64_t bb) { product_ss<DK / 16, kC, kC, false>(tm + d, a, bb, ida); };
         auto gram_v = [&](uint32_t d, uint64_t a, uint64_t bb) { product_ss<DV / 16, kC, kC, false>(tm + d, a, bb, ida); };
-        // token tile [., dv] times X^T
+        // token tile [., dv] times X^T, the small part first
         auto into = [&](uint64_t a, uint32_t d) {
-            product_ss<DV / 16, kC, DK, false>(tm + d, a, xh, idx);
-            product_ss<DV / 16, kC, DK, true>(tm + d, a, xl, idx);
+            product_ss<DV / 16, kC, DK, false>(tm + d, a, xl, idx);
+            product_ss<DV / 16, kC, DK, true>(tm + d, a, xh, idx);
         };
         // A in TMEM times a token tile
         auto spread = [&](uint32_t d, uint32_t a, uint64_t bb, uint32_t id) { product_ts<true, true>(tm + d, tm + a, bb, id); };

@@ -114,3 +114,17 @@ def test_packed_lengths(kda, dims):
         oo, hh = ref.forward(n["q"][:, a:b], n["k"][:, a:b], n["v"][:, a:b], n["decay"][:, a:b], _np(h0t[i:i + 1]))
         ro[:, a:b], rh[i] = oo, hh[0]
     assert ref.frob(_np(o), ro) <= OUT and ref.frob(_np(h), rh) <= MEMORY
+
+
+@pytest.mark.parametrize("heads", [4, 40])
+@pytest.mark.parametrize("dims", [(64, 64), (64, 128), (128, 64), (128, 128)], ids=str)
+def test_a_chunks_product_is_added_up_from_its_small_parts(kda, dims, heads):
+    """The accumulator cuts each step by half a unit of its own size: 8 steps of the large part are 8 2^-25 = 2.4e-7 of a
+    chunk's product (24, if that came first, 7e-7), beside 1.2e-7 of ex2 and some 2e-7 of exponents of mild decays: 6e-7.
+    (ddecay's terms through S or R err by their two-part operands, 2^-18 / sqrt(3) of an element, beside that.)"""
+    d, n = _make(2, 640, heads, 1, *dims, "bf16", seed=12)
+    h = kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], check_device=True)[1]
+    got = kda.linear_chunk_bwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], d["d_o"], d["dhT"], check_device=True)
+    want = ref.backward(n["q"], n["k"], n["v"], n["decay"], n["h0"], n["d_o"], n["dhT"])
+    err = (ref.frob(_np(h), ref.forward(n["q"], n["k"], n["v"], n["decay"], n["h0"])[1]), ref.frob(_np(got["dh0"]), want["dh0"]))
+    assert max(err) <= 6e-7, err
