@@ -23,7 +23,8 @@
 //              = <h_T, dh_T> + sum_{i >= t} (q_i . dq'_i - k_i . dk'_i)
 // where ' leaves out token i's own pair: both dots then hold just what crosses token t (a term
 // of token i's own pair would have to cancel between them, and under a strong decay it is far
-// larger than the result).  The last sum runs in fp64.
+// larger than the result).  The last sum runs in fp64.  A token that keeps nothing (a restart, the first one without an
+// initial memory) has 0.
 #include <algorithm>
 
 #include "linear_internal.cuh"
@@ -474,6 +475,8 @@ struct Dgate {
     const float *rq, *rk;        // row dots, n slices each
     int n;
     const float *hT, *dhT;       // final memory and its gradient (or nullptr)
+    LinDecay g;
+    int h0;                      // there is an initial memory
     float *dg;
     int T, HV, cells;
     long rows;
@@ -515,9 +518,12 @@ __device__ __forceinline__ void sum_dgate(const Dgate &d, int pair) {
     double acc = sum - mine;
 #pragma unroll
     for (int i = 0; i < kGradThreads / 32; ++i) acc += s_anchor[i] + (i > warp ? s_run[i] : 0.0);
+    const float *gp = d.g.p + b * d.g.b + hv;
     for (int t = t1 - 1; t >= t0; --t) {
         acc += at(t);
-        d.dg[((size_t)b * d.T + t) * d.HV + hv] = (float)acc;
+        // where nothing is kept the sum's terms cancel, all but their rounding
+        const bool kept = (t > 0 || d.h0) && !(gp[(long long)t * d.g.t] < kMinDecay);
+        d.dg[((size_t)b * d.T + t) * d.HV + hv] = kept ? (float)acc : 0.f;
     }
 }
 
@@ -701,7 +707,7 @@ cudaError_t launch_linear_scan_bwd(const LinBwd &a, cudaStream_t st) {
                                            : run_walks<float>(ws, a.dv, a.dk, a.T, st);
     if (e != cudaSuccess) return e;
     const bool fixed = a.g.t == 0;
-    Dgate d{rq, rk, a.dk / kCols, hT, a.dhT, fixed ? dgt : a.dg, a.T, a.HV, a.dk * a.dv, (long)a.B * a.T};
+    Dgate d{rq, rk, a.dk / kCols, hT, a.dhT, a.g, a.h0 != nullptr, fixed ? dgt : a.dg, a.T, a.HV, a.dk * a.dv, (long)a.B * a.T};
     Fold f{};
     if (m > 1) f = Fold{{fq, fk}, {a.dq, a.dk_}, (long)a.B * a.T * a.H * a.dk, a.T, a.H, m, a.dk};
     e = run_tail(d, want_g ? a.B * a.HV : 0, f, a.dtype, st);

@@ -982,12 +982,17 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                 if (lane == 31) behind = 0.f;
                 if (lane == 0) before = 0.f;
                 all *= ex2(gc);
+                // a token that keeps nothing has 0, not what the sums' rounding leaves (restarts are in chunks that are not mild)
+                float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (strong) d = load_decay(w.g, w.g.p + b * w.g.b + hv, u + 4 * lane, w.T);
+                const float *pd = &d.x;
                 float suf[4];
                 suf[3] = behind + f[3]; suf[2] = suf[3] + f[2]; suf[1] = suf[2] + f[1]; suf[0] = suf[1] + f[0];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int t = u + 4 * lane + i;
-                    if (t < w.T) w.dg[((long long)b * w.T + t) * w.HV + hv] = all + suf[i] + before;
+                    const bool kept = (t > 0 || w.h0) && pd[i] > kMinDecay * kLog2e;
+                    if (t < w.T) w.dg[((long long)b * w.T + t) * w.HV + hv] = kept || pd[i] != pd[i] ? all + suf[i] + before : 0.f;
                     before += kd[i];
                 }
             }

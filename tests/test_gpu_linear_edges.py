@@ -134,3 +134,26 @@ def test_decays_that_fall_and_grow_in_a_chunk(kda, first, size, D, heads):
         assert err.max() <= 4 * ref.U8, (x, err.max())
     assert ref.frob(_np(h), rh) <= ref.TC_STATE
     assert ref.frob(_np(got["dh0"]), want["dh0"]) <= ref.TC_STATE
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("T", [1, 2, 16, 17, 200, 500])
+def test_decays_that_keep_nothing_have_no_gradient(kda, T, D, dtype):
+    """ddecay_t = e^{decay_t} <h_{t-1}, D_t> is exactly 0 at a restart and, without an initial memory, at the first token: not
+    what rounding leaves of the sums that it is taken from.  With an initial memory the first token's is not."""
+    import torch
+    d, n = _make(2, T, 3, 1, D, D, dtype, seed=40)
+    g = n["decay"].copy()
+    if T > 2:
+        g[0, 1], g[1, T - 1], g[1, T // 2] = -np.inf, -200.0, -np.inf
+    d["decay"] = _t(g, torch.float32)
+    for h0 in (None, d["h0"]):
+        got = _np(kda.linear_chunk_bwd(d["q"], d["k"], d["v"], d["decay"], h0, d["d_o"], d["dhT"], check_device=True)["ddecay"])
+        want = ref.backward(n["q"], n["k"], n["v"], _np(d["decay"]), None if h0 is None else n["h0"], n["d_o"], n["dhT"])["ddecay"]
+        with np.errstate(under="ignore"):
+            nothing = np.exp(_np(d["decay"])) < 1e-45
+        if h0 is None:
+            nothing[:, 0] = True
+        assert (got[nothing] == 0).all() and (got[~nothing] != 0).all()
+        assert ref.frob(got, np.where(nothing, 0.0, want)) <= (2e-5 if T > 1 else 1e-5)
