@@ -1,8 +1,9 @@
 """Binding of linear attention with a decay per head and of the block norms (include/kda.h).
 
 Argument marshalling only, as ``_lib``: outputs and workspaces are torch tensors of the stream the
-call runs on, and the tensors of a call are all on the current device.  q, k, v and the other token arrays may be views with any batch, token and head strides
-(16-byte multiples, last dimension contiguous), e.g. slices of one projection's output.
+call runs on, and the tensors of a call are all on the current device.  q, k, v and the other token
+arrays may be views with any batch, token and head strides (16-byte multiples, last dimension
+contiguous), e.g. slices of one projection's output.
 """
 from __future__ import annotations
 

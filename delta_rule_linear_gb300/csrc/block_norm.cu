@@ -121,8 +121,8 @@ __device__ __forceinline__ float row_sum(float x, float *s, bool *any = nullptr)
 // s = 1 / (1 + e), e = 2^(-a log2 e): approximate operations that flush what is below 2^-126 (a sigmoid of -88 or
 // less), without the scaling that keeps subnormals, which every element would pay for.  An exponent p = a log2 e rounded
 // to fp32 is off by up to 2^-24 |p|, 3e-6 of e at |a| = 80: a bf16 result does not show that; for fp32 (T) what p lost,
-// which an FMA gives exactly, and what the constant lost, go in to the first order, 2^-d = 1 - d ln 2.  `rest`: 1 - s = e s, with all its bits where s is next to 1 (and 1
-// where e is infinite).
+// which an FMA gives exactly, and what the constant lost, go in to the first order, 2^-d = 1 - d ln 2.  `rest`: 1 - s =
+// e s, with all its bits where s is next to 1 (and 1 where e is infinite).
 template <typename T>
 __device__ __forceinline__ float sigmoid(float a, float &rest) {
     constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = 1.925963033e-8f, kLn2 = 0.6931471805599453f;

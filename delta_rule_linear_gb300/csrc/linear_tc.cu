@@ -121,8 +121,8 @@ struct WalkCfg {
     static constexpr int ARR = SB + DK * DV * 2;                // per chunk parity: G [128], w [128]
     static constexpr int CTL = ARR + 2 * 2 * kC * 4;
     static constexpr int SMEM = CTL + 256;
-    // TMEM columns: a chunk's product 4 [dv][dk] (first the start state), scores / P, O, the three parts of the decayed values.  At d = 128 there is
-    // room for two of them, and hi follows lo once that is used
+    // TMEM columns: a chunk's product 4 [dv][dk] (first the start state), scores / P, O, the three parts of the decayed
+    // values.  At d = 128 there is room for two of them, and hi follows lo once that is used
     static constexpr bool OWN_HI = DK + DV <= 192;
     static constexpr int T_S = 0, T_P = DK, T_O = DK + 128, T_V = DK + 128 + DV, T_HI = OWN_HI ? T_V + 128 : T_V;
     static_assert(T_V + (OWN_HI ? 192 : 128) <= 512, "TMEM");
@@ -130,7 +130,8 @@ struct WalkCfg {
 };
 
 struct WalkCtl {
-    uint64_t full[2], done[2], s_full, q_free, p_ready, r_ready, o_full, o_free, s_ready, v_ready, hi_ready, lo_done, kv_done, cleared, start, last;
+    uint64_t full[2], done[2], s_full, q_free, p_ready, r_ready, o_full, o_free, s_ready, v_ready, hi_ready, lo_done, kv_done,
+        cleared, start, last;
     uint32_t tmem;
     int fail;
     int strong[2];   // the chunk is not mild
@@ -840,7 +841,8 @@ linear_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
 // (sequence, head) that finds no SM waits for the next wave.  Equal lengths: the cut with the least of it, and
 // of cuts within 5 % the coarsest (a long segment's local memory stops early where decays are strong: B=1 T=32768
 // H=32, 4 segments 0.30 ms, 8 segments 0.36 ms).  Of all cuts of ten shapes, 2048 to 32,768 tokens, 1 to 128 heads, it
-// picks the fastest or one within 1 %, in one 9 % (8192 tokens, 4 heads of 128: 39.0 us for 35.9).  Packed sequences: whole ones while the
+// picks the fastest or one within 1 %, in one 9 % (8192 tokens, 4 heads of 128: 39.0 us for 35.9).
+// Packed sequences: whole ones while the
 // longest is no more than an SM's share of the work (taken longest first they then fill the SMs evenly),
 // else segments of half an SM's share.
 int plan_chunks(int nseq, int HV, long total, int max_len, bool varlen, int sms) {

@@ -486,7 +486,8 @@ template <int DK, int DV>
 struct GradCfg {
     static constexpr int QB = kC * DK * 2, VB = kC * DV * 2, XB = DK * DV * 2;
     static constexpr int Q = 0, K = QB, V = 2 * QB, O = 2 * QB + VB, XH = 2 * QB + 2 * VB, XL = XH + XB;
-    static constexpr int ARR = XL + XB;         // G, E (what G's fp32 lost, where not mild), w, then quarters of: r, c, q dots, k dots
+    // G, E (in chunks that are not mild: what G's fp32 lost), w, then quarters of: r, c, q dots, k dots
+    static constexpr int ARR = XL + XB;
     static constexpr int CTL = ARR + 19 * kC * 4, SMEM = CTL + 256;
     static_assert(SMEM <= 232448, "shared memory");
 };
@@ -563,7 +564,8 @@ struct Two {
     float h, l;
 };
 __device__ __forceinline__ Two add(const Two &a, const Two &b) {
-    const float s = a.h + b.h, v = s - a.h, r = (a.h - (s - v)) + (b.h - v) + (a.l + b.l), h = s + r;   // exact sum, then both tails
+    const float s = a.h + b.h, v = s - a.h, r = (a.h - (s - v)) + (b.h - v) + (a.l + b.l);   // what s lost, both tails
+    const float h = s + r;
     return {h, r - (h - s)};
 }
 __device__ __noinline__ void running_sums(const float4 &d, int lane, float4 &x, float4 &low) {
