@@ -35,7 +35,11 @@ EXPORTS = ("kda_status_string", "kda_version", "kda_chunk_fwd_workspace", "kda_c
            "kda_linear_chunk_fwd_workspace", "kda_linear_chunk_fwd", "kda_linear_varlen_fwd_workspace",
            "kda_linear_varlen_fwd", "kda_linear_decode_step", "kda_linear_chunk_bwd_workspace", "kda_linear_chunk_bwd",
            "kda_gated_norm_fwd", "kda_gated_norm_bwd_workspace", "kda_gated_norm_bwd",
-           "kda_residual_norm_fwd", "kda_residual_norm_bwd_workspace", "kda_residual_norm_bwd")
+           "kda_residual_norm_fwd", "kda_residual_norm_bwd_workspace", "kda_residual_norm_bwd",
+           "kda_conv_fwd", "kda_conv_varlen_fwd", "kda_conv_decode_step", "kda_conv_bwd_workspace", "kda_conv_bwd",
+           "kda_ssm_chunk_fwd_workspace", "kda_ssm_chunk_fwd", "kda_ssm_varlen_fwd_workspace", "kda_ssm_varlen_fwd",
+           "kda_ssm_decode_step", "kda_ssm_chunk_bwd_workspace", "kda_ssm_chunk_bwd",
+           "kda_beam_select_workspace", "kda_beam_select", "kda_beam_reorder")
 
 
 class KdaOptions(ctypes.Structure):
@@ -186,6 +190,36 @@ def load(path: str | None = None):
         lib.kda_residual_norm_bwd_workspace.restype = Z
         lib.kda_residual_norm_bwd.argtypes = [P, P, P, P, P, P, F, P, P, P, P, L, I, I, I, F, P, Z, P]
         lib.kda_residual_norm_bwd.restype = I
+        lib.kda_conv_fwd.argtypes = [P] * 7 + [I] * 6 + [P]
+        lib.kda_conv_fwd.restype = I
+        lib.kda_conv_varlen_fwd.argtypes = [P] * 9 + [I] * 6 + [P]
+        lib.kda_conv_varlen_fwd.restype = I
+        lib.kda_conv_decode_step.argtypes = [P] * 6 + [I] * 5 + [P]
+        lib.kda_conv_decode_step.restype = I
+        lib.kda_conv_bwd_workspace.argtypes = [I] * 2
+        lib.kda_conv_bwd_workspace.restype = Z
+        lib.kda_conv_bwd.argtypes = [P] * 12 + [I] * 6 + [P, Z, P]
+        lib.kda_conv_bwd.restype = I
+        lib.kda_ssm_chunk_fwd_workspace.argtypes = [I] * 6
+        lib.kda_ssm_chunk_fwd_workspace.restype = Z
+        lib.kda_ssm_chunk_fwd.argtypes = [P] * 12 + [I] * 7 + [P, Z, P]
+        lib.kda_ssm_chunk_fwd.restype = I
+        lib.kda_ssm_varlen_fwd_workspace.argtypes = [I] * 6
+        lib.kda_ssm_varlen_fwd_workspace.restype = Z
+        lib.kda_ssm_varlen_fwd.argtypes = [P] * 14 + [I] * 7 + [P, Z, P]
+        lib.kda_ssm_varlen_fwd.restype = I
+        lib.kda_ssm_decode_step.argtypes = [P] * 11 + [I] * 6 + [P]
+        lib.kda_ssm_decode_step.restype = I
+        lib.kda_ssm_chunk_bwd_workspace.argtypes = [I] * 7
+        lib.kda_ssm_chunk_bwd_workspace.restype = Z
+        lib.kda_ssm_chunk_bwd.argtypes = [P] * 22 + [I] * 7 + [P, Z, P]
+        lib.kda_ssm_chunk_bwd.restype = I
+        lib.kda_beam_select_workspace.argtypes = [I] * 4
+        lib.kda_beam_select_workspace.restype = Z
+        lib.kda_beam_select.argtypes = [P, P, P, P, I, P, P, P, I, I, I, I, I, P, Z, P]
+        lib.kda_beam_select.restype = I
+        lib.kda_beam_reorder.argtypes = [P, P, I, P, I, I, P]
+        lib.kda_beam_reorder.restype = I
         _lib = lib
         return lib
 

@@ -1,0 +1,391 @@
+// short_conv.cu -- the short causal convolution over tokens, one filter of K taps per channel.
+//
+//     p_t = bias + sum_j w_j x_{t-K+1+j},   y_t = act(p_t),   act = silu or none,
+// with the K - 1 tokens before a sequence from its window (zeros without one), and after it the last K - 1 tokens as the
+// next window.  Gradients, with q_t = dy_t act'(p_t) (p_t formed again):
+//     dx_t = sum_j w_j q_{t+K-1-j},   dw_j = sum_t q_t x_{t-K+1+j},   dbias = sum_t q_t,
+// where the last K - 1 tokens' dx takes the next window's gradient too, and dx of the tokens before the sequence is the
+// window's gradient.
+//
+// All are bound by HBM: a lane holds V channels (16 bytes), a warp 32 V of them, and walks a run of tokens of one
+// sequence with the K last rows in registers, so that every row is read once, but for the K - 1 rows that a run shares
+// with the next (L2 has them).  The sums are fp32 and rounded once.  The weights' gradients stay in registers over all
+// runs of a lane, are added up over a CTA's warps in shared memory and over the CTAs by a second kernel, in a fixed order.
+#include <algorithm>
+
+#include "conv_internal.cuh"
+#include "pack.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+
+template <typename T, int V> __device__ __forceinline__ void load_row(const T *p, bool live, float (&x)[V]) {
+    if (live) {
+        Pack<T, V>::load(p, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = 0.f;
+    }
+}
+
+// Taps of the lane's channels [c, c + V), and their biases.
+template <int V, int K> __device__ __forceinline__ void load_taps(const Conv &a, int c, bool live, float (&w)[K][V], float (&b)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        b[i] = live && a.bias ? a.bias[c + i] : 0.f;
+#pragma unroll
+        for (int j = 0; j < K; ++j) w[j][i] = live ? a.w[(long)(c + i) * K + j] : 0.f;
+    }
+}
+
+// Row t of the window before a sequence's tokens (t in [-(K - 1), -1]).
+template <typename T, int V, int K>
+__device__ __forceinline__ void load_window(const void *h0, int n, int t, int C, int c, bool live, float (&x)[V]) {
+    load_row<T, V>(static_cast<const T *>(h0) + ((long)n * (K - 1) + (t + K - 1)) * C + c, live && h0, x);
+}
+
+// The window after sequence n: rows len - (K - 1) .. len - 1, read before any is written (hT may be h0).
+template <typename T, int V, int K>
+__device__ __forceinline__ void next_window(const Conv &a, int n, long start, int len, int c) {
+    const T *xp = static_cast<const T *>(a.x.p) + (a.s.cu ? start * a.x.t : (long)n * a.x.b) + c;
+    typename Pack<T, V>::Raw r[K - 1];
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i) {
+        const int t = len - (K - 1) + i;
+        if (t >= 0)
+            r[i] = Pack<T, V>::get(xp + t * a.x.t);
+        else
+            r[i] = a.h0 ? Pack<T, V>::get(static_cast<const T *>(a.h0) + ((long)n * (K - 1) + (t + K - 1)) * a.C + c)
+                        : Pack<T, V>::zero();
+    }
+    T *hp = static_cast<T *>(a.hT) + (long)n * (K - 1) * a.C + c;
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i) {
+        if constexpr (V == 1) {
+            hp[(long)i * a.C] = r[i];
+        } else {
+            uint4 *to = reinterpret_cast<uint4 *>(hp + (long)i * a.C);
+#pragma unroll
+            for (int k = 0; k < Pack<T, V>::N; ++k) to[k] = r[i].w[k];
+        }
+    }
+}
+
+// The run `item`, with the rows a packed batch has (whatever its prefix array says, none outside them is touched).
+__device__ __forceinline__ bool conv_item(const Conv &a, long item, LinItem &it) {
+    if (item >= a.items || !lin_item(a.s, a.run, (int)item, it)) return false;
+    if (a.s.cu) {
+        it.start = min(max(it.start, 0L), a.total);
+        it.len = (int)min((long)max(it.len, 0), a.total - it.start);
+    }
+    return true;
+}
+
+// Warp = 32 V channels of one run.  The run that ends a sequence writes its next window (WINDOW_ONLY: nothing else).
+template <typename T, int V, int K, bool WINDOW_ONLY>
+__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(Conv a) {
+    const int group = blockIdx.x / a.blocks, c = ((blockIdx.x - group * a.blocks) * 32 + (threadIdx.x & 31)) * V;
+    const bool live = c < a.C;
+    LinItem it;
+    if (!conv_item(a, (long)group * kWarps + threadIdx.x / 32, it)) return;
+    const int t0 = it.p * a.run, t1 = min(it.len, t0 + a.run);
+    if (a.hT && it.p == it.nseg - 1 && live && (WINDOW_ONLY || a.hT != a.h0)) next_window<T, V, K>(a, it.n, it.start, it.len, c);
+    if (WINDOW_ONLY || !live || t0 >= t1) return;
+    float w[K][V], b[V], x[K][V];
+    load_taps<V, K>(a, c, live, w, b);
+    const T *xp = static_cast<const T *>(a.x.p) + (a.s.cu ? it.start * a.x.t : it.n * a.x.b) + c;
+    T *yp = static_cast<T *>(a.y.p) + (a.s.cu ? it.start * a.y.t : it.n * a.y.b) + c;
+#pragma unroll
+    for (int j = 1; j < K; ++j) {
+        const int t = t0 - K + j;
+        if (t >= 0)
+            load_row<T, V>(xp + t * a.x.t, true, x[j]);
+        else
+            load_window<T, V, K>(a.h0, it.n, t, a.C, c, true, x[j]);
+    }
+    // eight rows in flight
+    constexpr int U = 8;
+    for (int t = t0; t < t1; t += U) {
+        typename Pack<T, V>::Raw raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (t + u < t1) raw[u] = Pack<T, V>::get(xp + (t + u) * a.x.t);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (t + u >= t1) break;
+#pragma unroll
+            for (int j = 0; j + 1 < K; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[j][i] = x[j + 1][i];
+            Pack<T, V>::open(raw[u], x[K - 1]);
+            float y[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                y[i] = b[i];
+#pragma unroll
+                for (int j = 0; j < K; ++j) y[i] = fmaf(w[j][i], x[j][i], y[i]);
+                if (a.act) {
+                    float rest;
+                    y[i] *= sigmoid<T>(y[i], rest);
+                }
+            }
+            Pack<T, V>::store(yp + (t + u) * a.y.t, y);
+        }
+    }
+}
+
+// A warp's lanes go over the items warp, warp + warps, ...; q of K rows and x of K rows in registers.
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(Conv a) {
+    __shared__ float sum[kWarps / 2][32 * V + 1];
+    next_may_start();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int c = (blockIdx.x * 32 + lane) * V;
+    const bool live = c < a.C;
+    float w[K][V], b[V], dw[K][V], db[V];
+    load_taps<V, K>(a, c, live, w, b);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        db[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < K; ++j) dw[j][i] = 0.f;
+    }
+    for (long item = (long)blockIdx.y * kWarps + warp; item < a.items; item += (long)gridDim.y * kWarps) {
+        LinItem it;
+        if (!conv_item(a, item, it)) break;
+        if (!live || (it.p && it.p * a.run >= it.len)) continue;
+        const int t0 = it.p * a.run, t1 = min(it.len, t0 + a.run);
+        const T *xp = static_cast<const T *>(a.x.p) + (a.s.cu ? it.start * a.x.t : it.n * a.x.b) + c;
+        const T *gp = static_cast<const T *>(a.y.p) + (a.s.cu ? it.start * a.y.t : it.n * a.y.b) + c;
+        T *dp = static_cast<T *>(a.dx.p) + (a.s.cu ? it.start * a.dx.t : it.n * a.dx.b) + c;
+        const long win = (long)it.n * (K - 1) * a.C + c;      // row -(K - 1) of the window
+        float x[K][V], q[K][V];
+#pragma unroll
+        for (int j = 1; j < K; ++j) {
+            const int t = t0 - K + j;
+            if (t >= 0)
+                load_row<T, V>(xp + t * a.x.t, true, x[j]);
+            else
+                load_window<T, V, K>(a.h0, it.n, t, a.C, c, true, x[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) q[j][i] = 0.f;
+        // dx of row t - (K - 1) is whole once q_t is there; the first run goes on to the window's rows.  q of rows past
+        // the run is formed here too (its share of the weights' gradients belongs to the next run).
+        const int last = t1 + K - 1;
+        constexpr int U = 4;
+        for (int t = t0; t < last; t += U) {
+            typename Pack<T, V>::Raw xr[U], gr[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                xr[u] = gr[u] = Pack<T, V>::zero();
+                if (t + u < last && t + u < it.len) {
+                    xr[u] = Pack<T, V>::get(xp + (t + u) * a.x.t);
+                    gr[u] = Pack<T, V>::get(gp + (t + u) * a.y.t);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int tt = t + u;
+                if (tt >= last) break;
+#pragma unroll
+                for (int j = 0; j + 1 < K; ++j)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        x[j][i] = x[j + 1][i];
+                        q[j][i] = q[j + 1][i];
+                    }
+                Pack<T, V>::open(xr[u], x[K - 1]);
+                float g[V];
+                Pack<T, V>::open(gr[u], g);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    if (a.act) {
+                        float p = b[i], rest;
+#pragma unroll
+                        for (int j = 0; j < K; ++j) p = fmaf(w[j][i], x[j][i], p);
+                        const float s = sigmoid<T>(p, rest);
+                        g[i] *= fmaf(p * s, rest, s);
+                    }
+                    q[K - 1][i] = tt < it.len ? g[i] : 0.f;
+                }
+                if (tt < t1) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        db[i] += q[K - 1][i];
+#pragma unroll
+                        for (int j = 0; j < K; ++j) dw[j][i] = fmaf(q[K - 1][i], x[j][i], dw[j][i]);
+                    }
+                }
+                const int row = tt - (K - 1);
+                if (row >= t0 || (t0 == 0 && a.dh0)) {
+                    float d[V];
+                    const int tail = row - (it.len - (K - 1));        // its row of the next window
+                    load_row<T, V>(static_cast<const T *>(a.dhT) + win + (long)tail * a.C, a.dhT && tail >= 0, d);
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+#pragma unroll
+                        for (int j = 0; j < K; ++j) d[i] = fmaf(w[j][i], q[K - 1 - j][i], d[i]);
+                    Pack<T, V>::store(row >= 0 ? dp + row * a.dx.t : static_cast<T *>(a.dh0) + win + (long)(row + K - 1) * a.C, d);
+                }
+            }
+        }
+    }
+    // the CTA's sums, in the order of its warps: 4 + 4 (two rounds), then the partial row
+    const long row = (long)blockIdx.y * a.C * (K + 1);
+#pragma unroll
+    for (int j = 0; j <= K; ++j) {
+        float(&v)[V] = j < K ? dw[j < K ? j : 0] : db;
+        __syncthreads();
+        if (warp >= kWarps / 2)
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum[warp - kWarps / 2][lane * V + i] = v[i];
+        __syncthreads();
+        if (warp < kWarps / 2)
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum[warp][lane * V + i] += v[i];
+        __syncthreads();
+        for (int e = threadIdx.x; e < 32 * V; e += kThreads) {
+            const int ch = blockIdx.x * 32 * V + e;
+            if (ch < a.C) a.part[row + (long)j * a.C + ch] = (sum[0][e] + sum[1][e]) + (sum[2][e] + sum[3][e]);
+        }
+    }
+}
+
+// dw, dbias from the partial rows; a warp sums 32 consecutive columns' parts in order, eight warps share a column.
+__global__ void __launch_bounds__(kThreads) conv_fold_kernel(const float *part, int parts, int C, int K, float *dw, float *dbias) {
+    __shared__ float s[kWarps][33];
+    wait_for_previous();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const long col = (long)blockIdx.x * 32 + lane, cols = (long)C * (K + 1);
+    float v = 0.f;
+    if (col < cols)
+        for (int p = warp; p < parts; p += kWarps) v += part[p * cols + col];
+    s[warp][lane] = v;
+    __syncthreads();
+    if (warp || col >= cols) return;
+    v = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) v += s[k][lane];
+    const int j = (int)(col / C), c = (int)(col - (long)j * C);
+    if (j < K)
+        dw[(long)c * K + j] = v;
+    else if (dbias)
+        dbias[c] = v;
+}
+
+// One token of a request, V channels per lane.
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStep a) {
+    const int nv = a.C / V;
+    const long id = blockIdx.x * (long)kThreads + threadIdx.x;
+    if (id >= (long)nv * a.B) return;
+    const int n = (int)(id / nv), c = (int)(id - (long)n * nv) * V;
+    T *sp = static_cast<T *>(a.state) + (long)n * (K - 1) * a.C + c;
+    float x[K][V], y[V];
+    typename Pack<T, V>::Raw r[K];
+#pragma unroll
+    for (int j = 0; j + 1 < K; ++j) r[j] = Pack<T, V>::get(sp + (long)j * a.C);
+    r[K - 1] = Pack<T, V>::get(static_cast<const T *>(a.x) + n * a.xb + c);
+#pragma unroll
+    for (int j = 0; j < K; ++j) Pack<T, V>::open(r[j], x[j]);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        y[i] = a.bias ? a.bias[c + i] : 0.f;
+#pragma unroll
+        for (int j = 0; j < K; ++j) y[i] = fmaf(a.w[(long)(c + i) * K + j], x[j][i], y[i]);
+        if (a.act) {
+            float rest;
+            y[i] *= sigmoid<T>(y[i], rest);
+        }
+    }
+    Pack<T, V>::store(static_cast<T *>(a.y) + n * a.yb + c, y);
+#pragma unroll
+    for (int j = 0; j + 1 < K; ++j) Pack<T, V>::store(sp + (long)j * a.C, x[j + 1]);
+}
+
+template <typename T> bool vec_view(const ConvView &v) {
+    constexpr int V = 16 / sizeof(T);
+    return reinterpret_cast<uintptr_t>(v.p) % 16 == 0 && v.b % V == 0 && v.t % V == 0;
+}
+bool al16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Tokens of a run: long ones share few rows with the next, but the launch needs about a thousand lanes per SM.
+int pick_run(const Conv &a, int V, long rows, int lanes_per_sm) {
+    const long vecs = (a.C + V - 1) / V;
+    int run = 32;
+    while (run > 4 && rows * vecs / run < (long)lanes_per_sm * a.sms) run /= 2;
+    return run;
+}
+
+template <typename T, int V, int K> cudaError_t run_fwd(Conv a, cudaStream_t st) {
+    const long rows = a.s.cu ? a.total : (long)a.s.nseq * a.s.T;
+    a.run = pick_run(a, V, rows, 768);
+    a.items = lin_items(a.s.nseq, a.s.cu ? a.total : a.s.T, a.s.cu ? (int)a.total : a.s.T, a.s.cu != nullptr, a.run);
+    a.blocks = (a.C + 32 * V - 1) / (32 * V);
+    const long ctas = (a.items + kWarps - 1) / kWarps * a.blocks;
+    if (ctas > 0x7fffffffL) return cudaErrorInvalidValue;
+    const unsigned grid = (unsigned)ctas;
+    conv_fwd_kernel<T, V, K, false><<<grid, kThreads, 0, st>>>(a);
+    // the window is updated in place: after the tokens have been read
+    if (a.hT && a.hT == a.h0) conv_fwd_kernel<T, V, K, true><<<grid, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int V, int K> cudaError_t run_bwd(Conv a, cudaStream_t st) {
+    const long rows = a.s.cu ? a.total : (long)a.s.nseq * a.s.T;
+    a.run = pick_run(a, V, rows, 512);
+    a.items = lin_items(a.s.nseq, a.s.cu ? a.total : a.s.T, a.s.cu ? (int)a.total : a.s.T, a.s.cu != nullptr, a.run);
+    const unsigned cb = (a.C + 32 * V - 1) / (32 * V);
+    const long want = (long)std::max(1, std::min(conv_parts(a.C, a.sms), 2 * a.sms / (int)cb));
+    const unsigned parts = (unsigned)std::min((a.items + kWarps - 1) / kWarps, want);
+    conv_bwd_kernel<T, V, K><<<dim3(cb, parts), kThreads, 0, st>>>(a);
+    const long cols = (long)a.C * (K + 1);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_after(conv_fold_kernel, dim3((unsigned)((cols + 31) / 32)), kThreads, 0, st, (const float *)a.part, (int)parts,
+                        a.C, K, a.dw, a.dbias);
+}
+
+template <typename T, int K> cudaError_t go(const Conv &a, bool bwd, cudaStream_t st) {
+    constexpr int V = 16 / sizeof(T);
+    const bool vec = a.C % V == 0 && vec_view<T>(a.x) && vec_view<T>(a.y) && al16(a.h0) && al16(a.hT) &&
+                     (!bwd || (vec_view<T>(a.dx) && al16(a.dhT) && al16(a.dh0)));
+    if (bwd) return vec ? run_bwd<T, V, K>(a, st) : run_bwd<T, 1, K>(a, st);
+    return vec ? run_fwd<T, V, K>(a, st) : run_fwd<T, 1, K>(a, st);
+}
+template <typename T> cudaError_t taps(const Conv &a, bool bwd, cudaStream_t st) {
+    return a.K == 2 ? go<T, 2>(a, bwd, st) : a.K == 3 ? go<T, 3>(a, bwd, st) : go<T, 4>(a, bwd, st);
+}
+
+template <typename T, int V, int K> cudaError_t run_step(const ConvStep &a, cudaStream_t st) {
+    const long n = (long)(a.C / V) * a.B;
+    conv_step_kernel<T, V, K><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+template <typename T, int K> cudaError_t go_step(const ConvStep &a, cudaStream_t st) {
+    constexpr int V = 16 / sizeof(T);
+    const bool vec = a.C % V == 0 && al16(a.x) && al16(a.y) && al16(a.state) && (a.B == 1 || (a.xb % V == 0 && a.yb % V == 0));
+    return vec ? run_step<T, V, K>(a, st) : run_step<T, 1, K>(a, st);
+}
+template <typename T> cudaError_t taps_step(const ConvStep &a, cudaStream_t st) {
+    return a.K == 2 ? go_step<T, 2>(a, st) : a.K == 3 ? go_step<T, 3>(a, st) : go_step<T, 4>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_conv(const Conv &a, cudaStream_t st) {
+    return a.dtype == DType::BF16 ? taps<__nv_bfloat16>(a, false, st) : taps<float>(a, false, st);
+}
+cudaError_t launch_conv_bwd(const Conv &a, cudaStream_t st) {
+    return a.dtype == DType::BF16 ? taps<__nv_bfloat16>(a, true, st) : taps<float>(a, true, st);
+}
+cudaError_t launch_conv_step(const ConvStep &a, cudaStream_t st) {
+    return a.dtype == DType::BF16 ? taps_step<__nv_bfloat16>(a, st) : taps_step<float>(a, st);
+}
+
+}  // namespace kda

@@ -550,6 +550,136 @@ kda_status kda_residual_norm_bwd(const void *d_n, const void *d_x_out, const voi
                                  size_t ws_bytes, kda_stream_t stream);
 
 /*
+ * The short causal convolution that stands before a recurrent layer (its q, k, v, or the x of a state
+ * space scan): one filter of K taps per channel,
+ *
+ *     y_t = act(bias + sum_j weight[:, j] x_{t-K+1+j}),
+ *
+ * where tokens before the sequence come from its window, the last K - 1 tokens seen (zeros without one).
+ *
+ *   x, y    [B,T,C], KDA_F32 or KDA_BF16; weight [C,K] float32, 2 <= K <= 4; bias [C] float32 or NULL.
+ *   strides NULL: contiguous.  Otherwise four element strides (batch, token) of x, y, channels
+ *           contiguous; any alignment of the element type (16-byte multiples run faster).
+ *   initial_state, final_state   windows [B,K-1,C] of x's type, oldest token first, or NULL.  They may be
+ *           the same array, and must not overlap otherwise.
+ *   activation   0: none, 1: silu.
+ * B, N, T == 0 are allowed.
+ */
+kda_status kda_conv_fwd(const void *x, const float *weight, const float *bias, const void *initial_state,
+                        void *y, void *final_state, const long long *strides, int B, int T, int C, int K,
+                        kda_dtype dtype, int activation, kda_stream_t stream);
+/* Packed sequences [1,total_T,C] split by cu_seqlens [N+1] (device; cu_seqlens_host: its host copy, which
+ * is checked, or NULL), one window per sequence; rows outside all sequences are left as they are. */
+kda_status kda_conv_varlen_fwd(const void *x, const float *weight, const float *bias, const int *cu_seqlens,
+                               const int *cu_seqlens_host, const void *initial_state, void *y,
+                               void *final_state, const long long *strides, int N, int total_T, int C,
+                               int K, kda_dtype dtype, int activation, kda_stream_t stream);
+/* One token for each of B requests: x, y [B,C] (two strides of the request, or NULL), state [B,K-1,C]
+ * moved on by one token in place. */
+kda_status kda_conv_decode_step(const void *x, const float *weight, const float *bias, void *state, void *y,
+                                const long long *strides, int B, int C, int K, kda_dtype dtype,
+                                int activation, kda_stream_t stream);
+/* Gradients, given d_y and dfinal_state (the windows' gradient, x's type, or NULL): dx, dinitial_state (x's
+ * type; the latter may be NULL), dweight [C,K], dbias [C] float32 (may be NULL).  cu_seqlens NULL: N
+ * sequences of T tokens; otherwise N packed ones of T tokens in all (dx of rows outside them is not
+ * written).  strides: NULL or six (batch, token) of x, d_y, dx. */
+size_t kda_conv_bwd_workspace(int C, int K);
+kda_status kda_conv_bwd(const void *d_y, const void *x, const float *weight, const float *bias,
+                        const void *initial_state, const void *dfinal_state, void *dx, float *dweight,
+                        float *dbias, void *dinitial_state, const int *cu_seqlens,
+                        const long long *strides, int N, int T, int C, int K, kda_dtype dtype,
+                        int activation, void *ws, size_t ws_bytes, kda_stream_t stream);
+
+/*
+ * The state space scan: a memory h_t of N states for each channel, with a decay per channel and state
+ * whose time step depends on the token,
+ *
+ *     dt_t = softplus(dt_t + dt_bias),      h_t = exp(dt_t A) h_{t-1} + dt_t x_t B_t,
+ *     y_t  = (C_t . h_t + skip x_t) silu(gate_t).
+ *
+ *   x, dt, gate, y   [B,T,D], KDA_F32 or KDA_BF16; gate NULL: none.  softplus 0: dt + dt_bias is used as
+ *           it is.
+ *   B_in, C_in       [B,T,G,N], the same type: channel d reads group d / (D / G).  N in {8, 16, 32, 64}.
+ *   A [D,N], skip [D], dt_bias [D]   float32 (skip, dt_bias NULL: zeros); A finite, negative for a memory
+ *           that decays.
+ *   strides NULL: contiguous.  Otherwise eighteen element strides (batch, token, group) of x, dt, B_in,
+ *           C_in, gate, y, the last dimension contiguous (the group stride of x, dt, gate, y is not looked
+ *           at); any alignment of the element type (16-byte multiples run faster).
+ *   initial_state, final_state   [B,D,N] float32 or NULL.  They may be the same array (a long sequence is
+ *           then not split over the GPU), and must not overlap otherwise.
+ *   ws      at least the query's bytes, 16-byte aligned.
+ * Memories, their sums and exp are fp32 whatever the type.  B, nseq, T == 0 are allowed.  At most 65535
+ * sequences.
+ */
+size_t kda_ssm_chunk_fwd_workspace(int B, int T, int D, int G, int N, kda_dtype dtype);
+kda_status kda_ssm_chunk_fwd(const void *x, const void *dt, const float *A, const void *B_in,
+                             const void *C_in, const float *skip, const void *gate, const float *dt_bias,
+                             const float *initial_state, void *y, float *final_state,
+                             const long long *strides, int B, int T, int D, int G, int N, kda_dtype dtype,
+                             int softplus, void *ws, size_t ws_bytes, kda_stream_t stream);
+/* Packed sequences: token arrays [1,total_T,..], cu_seqlens and its host copy as kda_conv_varlen_fwd (the
+ * host copy also tells how to split the work), one memory per sequence. */
+size_t kda_ssm_varlen_fwd_workspace(int nseq, int total_T, int D, int G, int N, kda_dtype dtype);
+kda_status kda_ssm_varlen_fwd(const void *x, const void *dt, const float *A, const void *B_in,
+                              const void *C_in, const float *skip, const void *gate, const float *dt_bias,
+                              const int *cu_seqlens, const int *cu_seqlens_host,
+                              const float *initial_state, void *y, float *final_state,
+                              const long long *strides, int nseq, int total_T, int D, int G, int N,
+                              kda_dtype dtype, int softplus, void *ws, size_t ws_bytes,
+                              kda_stream_t stream);
+/* One token for each of B requests: x, dt, gate, y [B,D], B_in, C_in [B,G,N] (contiguous, or with eight
+ * element strides: x, dt (request), B_in, C_in (request, group), gate, y (request)); state [B,D,N] float32,
+ * updated in place. */
+kda_status kda_ssm_decode_step(const void *x, const void *dt, const float *A, const void *B_in,
+                               const void *C_in, const float *skip, const void *gate,
+                               const float *dt_bias, float *state, void *y, const long long *strides,
+                               int B, int D, int G, int N, kda_dtype dtype, int softplus,
+                               kda_stream_t stream);
+/* Gradients, given d_y (x's type) and dfinal_state (float32 or NULL): dx, ddt, dB, dC, dgate in x's type
+ * (contiguous; dB, dC summed over the group's channels in fp32), dA [D,N], dskip, ddt_bias [D] and
+ * dinitial_state [nseq,D,N] float32 (dskip, ddt_bias, dinitial_state may be NULL).  cu_seqlens NULL: nseq
+ * sequences of T tokens; otherwise nseq packed ones of T tokens in all (gradients of rows outside them
+ * are not written).  strides: NULL or eighteen, of x, dt, B_in, C_in, gate, d_y.  The results do not depend
+ * on the order in which the GPU works. */
+size_t kda_ssm_chunk_bwd_workspace(int nseq, int T, int packed, int D, int G, int N, kda_dtype dtype);
+kda_status kda_ssm_chunk_bwd(const void *d_y, const void *x, const void *dt, const float *A,
+                             const void *B_in, const void *C_in, const float *skip, const void *gate,
+                             const float *dt_bias, const float *initial_state, const float *dfinal_state,
+                             void *dx, void *ddt, float *dA, void *dB, void *dC, float *dskip, void *dgate,
+                             float *ddt_bias, float *dinitial_state, const int *cu_seqlens,
+                             const long long *strides, int nseq, int T, int D, int G, int N,
+                             kda_dtype dtype, int softplus, void *ws, size_t ws_bytes,
+                             kda_stream_t stream);
+
+/*
+ * Beam search: the k best continuations of each request's W beams,
+ *     total[w, v] = scores[w] + logits[w, v] - log sum_v' exp(logits[w, v']),
+ * in order, equal totals by the lowest w V + v: out_scores [B,k] float32, parents and tokens [B,k] int32
+ * (token v of beam parent).  Totals are formed and compared in 64 bits and rounded once.
+ *
+ *   logits   [B,W,V], KDA_F32 or KDA_BF16, contiguous or with two element strides (request, beam).
+ *   scores   [B,W] float32; -inf: a beam that does not count (on the first step, all but one).
+ *   finished [B,W] bytes or NULL: a nonzero beam has the one candidate `eos`, with its score as it is.
+ * W <= 128, k <= 32, k <= W V.  A beam whose logits hold NaN or +inf, or nothing but -inf, has no
+ * distribution: its candidates count as -inf.  out_scores may be scores (k == W).  ws: at least the
+ * query's bytes, 16-byte aligned.
+ */
+size_t kda_beam_select_workspace(int B, int W, int V, kda_dtype dtype);
+kda_status kda_beam_select(const void *logits, const long long *strides, const float *scores,
+                           const unsigned char *finished, int eos, float *out_scores, int *parents,
+                           int *tokens, int B, int W, int V, int k, kda_dtype dtype, void *ws,
+                           size_t ws_bytes, kda_stream_t stream);
+
+/*
+ * The recurrent memories follow the beams, in place: row (b, w) of each array becomes row
+ * (b, parents[b, w]).  states: `count` device pointers in a host array, each [B,W,row_bytes[i]] bytes,
+ * contiguous, of any type (memories, windows); arrays that overlap are KDA_ERR_INDEX.  parents [B,W]
+ * int32; a parent outside 0 .. W - 1 leaves its beam as it is.  W <= 32.
+ */
+kda_status kda_beam_reorder(void *const *states, const long long *row_bytes, int count, const int *parents,
+                            int B, int W, kda_stream_t stream);
+
+/*
  * Read the device error word that the kernels of the most recent kda_chunk_fwd /
  * kda_varlen_fwd call on `ws` recorded (KDA_OK if none), then clear it.  Each of
  * those calls clears the word on its stream before its kernels run.  ws == NULL reads
