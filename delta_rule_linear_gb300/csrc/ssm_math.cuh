@@ -39,4 +39,106 @@ __device__ __forceinline__ float softplus(float z) {
     return fmaf(q, e, fmaxf(z, 0.f)) + (z != z ? z : 0.f);     // fmaxf drops a NaN
 }
 
+// Two fp32 in one register pair: the packed operations do both in one instruction.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float a, float b) {
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void each(Two x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// N consecutive elements as words, unopened: one load where VEC (aligned to the smaller of 16 bytes and all of them), the
+// first `n` of them one by one otherwise.
+template <typename T, int N> struct Few {
+    static constexpr int W = N * (int)sizeof(T) / 4 ? N * (int)sizeof(T) / 4 : 1;
+    uint32_t w[W];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void set(int i, T x) {
+        if constexpr (sizeof(T) == 4)
+            w[i] = __float_as_uint(x);
+        else
+            w[i / 2] |= (uint32_t)__bfloat16_as_ushort(x) << 16 * (i & 1);
+    }
+    template <bool VEC> __device__ __forceinline__ void load(const T *p, int n) {
+        zero();
+        if (VEC) {
+            if (n <= 0) return;
+            if constexpr (W % 4 == 0) {
+#pragma unroll
+                for (int i = 0; i < W / 4; ++i) {
+                    const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+                    w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+                }
+            } else if constexpr (W == 2) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(p);
+                w[0] = v.x, w[1] = v.y;
+            } else if constexpr (N * sizeof(T) == 4) {
+                w[0] = *reinterpret_cast<const uint32_t *>(p);
+            } else {
+                set(0, p[0]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i < n) set(i, p[i]);
+        }
+    }
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(w[i]);
+        else
+            return __uint_as_float((i & 1) ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16));
+    }
+    template <bool VEC> static __device__ __forceinline__ void store(T *p, const float (&x)[N], int n) {
+        if (VEC) {
+            if (n <= 0) return;
+            Few r;
+            r.zero();
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) r.w[i] = __float_as_uint(x[i]);
+            } else if constexpr (N > 1) {
+#pragma unroll
+                for (int i = 0; i < N; i += 2) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(x[i], x[i + 1]);
+                    r.w[i / 2] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+            }
+            if constexpr (N == 1)
+                p[0] = from_f32<T>(x[0]);
+            else if constexpr (W % 4 == 0)
+#pragma unroll
+                for (int i = 0; i < W / 4; ++i)
+                    reinterpret_cast<uint4 *>(p)[i] = make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
+            else if constexpr (W == 2)
+                *reinterpret_cast<uint2 *>(p) = make_uint2(r.w[0], r.w[1]);
+            else
+                *reinterpret_cast<uint32_t *>(p) = r.w[0];
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i < n) p[i] = from_f32<T>(x[i]);
+        }
+    }
+};
+
 }  // namespace kda
