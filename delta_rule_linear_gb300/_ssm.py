@@ -30,8 +30,8 @@ def _raw(dev):
     return _linear._raw(dev)
 
 
-def _ws(query, sizes, t, stream, workspace):
-    return _linear._ws(query, sizes, t, stream, workspace)
+def _ws(query, sizes, t, stream, workspace, asked=False):
+    return _linear._ws(query, sizes, t, stream, workspace, asked)
 
 
 def _longs(*xs):
@@ -226,7 +226,7 @@ def _scan_strides(*ts):
     return _longs(*out)
 
 
-def _scan_call(x, dt, A, B, C, initial_state, skip, gate, dt_bias, softplus, out, final_state, workspace, cu, cu_cpu):
+def _scan_call(x, dt, A, B, C, initial_state, skip, gate, dt_bias, softplus, out, final_state, workspace, check, cu, cu_cpu):
     lib = load()
     if x.dim() != 3:
         raise ValueError("x must be [B, T, D]")
@@ -250,39 +250,44 @@ def _scan_call(x, dt, A, B, C, initial_state, skip, gate, dt_bias, softplus, out
     s = None if plain else _scan_strides(x, dt, B, C, gate, out)
     a = (x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(skip), _ptr(gate), _ptr(dt_bias))
     if cu is None:
-        ws, size = _ws("kda_ssm_chunk_fwd_workspace", (n, T, D, G, N, code), x, st, workspace)
+        ws, size = _ws("kda_ssm_chunk_fwd_workspace", (n, T, D, G, N, code), x, st, workspace, check)
         _ok(lib.kda_ssm_chunk_fwd(*a, _ptr(initial_state), out.data_ptr(), final_state.data_ptr(), s, n, T, D, G, N, code,
                                   int(softplus), ws.data_ptr(), size, st), "kda_ssm_chunk_fwd", lib)
     else:
-        ws, size = _ws("kda_ssm_varlen_fwd_workspace", (n, T, D, G, N, code), x, st, workspace)
+        ws, size = _ws("kda_ssm_varlen_fwd_workspace", (n, T, D, G, N, code), x, st, workspace, check)
         _ok(lib.kda_ssm_varlen_fwd(*a, cu.data_ptr(), _ptr(host), _ptr(initial_state), out.data_ptr(), final_state.data_ptr(), s,
                                    n, T, D, G, N, code, int(softplus), ws.data_ptr(), size, st), "kda_ssm_varlen_fwd", lib)
+    if check and n:        # an empty batch launches nothing and leaves the header as it is
+        _ok(_linear.query_device_error(ws), "state space scan (device)", lib)
     return out, final_state
 
 
 def ssm_chunk_fwd(x, dt, A, B, C, initial_state=None, *, skip=None, gate=None, dt_bias=None, softplus=True, out=None,
-                  final_state=None, workspace=None, stream=None):
+                  final_state=None, workspace=None, stream=None, check_device=False):
     """kda_ssm_chunk_fwd: the state space scan, dt_t = softplus(dt_t + dt_bias), h_t = exp(dt_t A) h_{t-1} + dt_t x_t B_t,
     y_t = (C_t . h_t + skip x_t) silu(gate_t), with N states for each of D channels.
 
     x, dt, gate [B,T,D]; B, C [B,T,G,N] or [B,T,N] (channel d reads group d // (D // G)), N in {8, 16, 32, 64}; A [D,N] (finite,
     negative for a decay), skip [D], dt_bias [D] fp32; initial_state [B,D,N] fp32; skip, gate, dt_bias, initial_state may
-    be None; softplus=False uses dt + dt_bias as it is.  Returns (y [B,T,D], final_state [B,D,N] fp32)."""
+    be None; softplus=False uses dt + dt_bias as it is.  Returns (y [B,T,D], final_state [B,D,N] fp32).  check_device as in
+    chunk_fwd."""
     if stream is not None:
         return _on(stream, ssm_chunk_fwd, x, dt, A, B, C, initial_state, skip=skip, gate=gate, dt_bias=dt_bias,
-                   softplus=softplus, out=out, final_state=final_state, workspace=workspace)
-    return _scan_call(x, dt, A, B, C, initial_state, skip, gate, dt_bias, softplus, out, final_state, workspace, None, None)
+                   softplus=softplus, out=out, final_state=final_state, workspace=workspace, check_device=check_device)
+    return _scan_call(x, dt, A, B, C, initial_state, skip, gate, dt_bias, softplus, out, final_state, workspace, check_device,
+                      None, None)
 
 
 def ssm_varlen_fwd(x, dt, A, B, C, cu_seqlens, initial_state=None, *, cu_seqlens_cpu=None, skip=None, gate=None, dt_bias=None,
-                   softplus=True, out=None, final_state=None, workspace=None, stream=None):
+                   softplus=True, out=None, final_state=None, workspace=None, stream=None, check_device=False):
     """kda_ssm_varlen_fwd: packed sequences [1,total,..] split by cu_seqlens [N+1] (int32, device); cu_seqlens_cpu, its host
     copy where there is one, is checked and tells how to split the work.  Returns (y [1,total,D], final_state [N,D,N])."""
     if stream is not None:
         return _on(stream, ssm_varlen_fwd, x, dt, A, B, C, cu_seqlens, initial_state, cu_seqlens_cpu=cu_seqlens_cpu, skip=skip,
-                   gate=gate, dt_bias=dt_bias, softplus=softplus, out=out, final_state=final_state, workspace=workspace)
-    return _scan_call(x, dt, A, B, C, initial_state, skip, gate, dt_bias, softplus, out, final_state, workspace, cu_seqlens,
-                      cu_seqlens_cpu)
+                   gate=gate, dt_bias=dt_bias, softplus=softplus, out=out, final_state=final_state, workspace=workspace,
+                   check_device=check_device)
+    return _scan_call(x, dt, A, B, C, initial_state, skip, gate, dt_bias, softplus, out, final_state, workspace, check_device,
+                      cu_seqlens, cu_seqlens_cpu)
 
 
 def ssm_decode_step(x, dt, A, B, C, state, *, skip=None, gate=None, dt_bias=None, softplus=True, out=None, stream=None):

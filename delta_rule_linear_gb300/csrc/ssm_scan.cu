@@ -2,55 +2,80 @@
 //
 //     dt_t = softplus(dt_t + bias),   h_t = exp(dt_t A) h_{t-1} + dt_t x_t B_t,   y_t = (C_t . h_t + skip x_t) silu(gate_t)
 //
-// The decay differs by channel and state, so nothing here is a matrix product: per (token, channel, state) there is one
+// The decay differs by channel and state, so the recurrence is no matrix product: per (token, channel, state) there is one
 // exp2 and four multiply-adds.  An SM does 32 exp2 and 128 fp32 operations a cycle, which are 32 such cells either way;
 // 152 SMs 9.3e12 a second.  With 16 states that is below the rate at which HBM brings x, dt, gate and takes y, so the
-// scan is bound by issue and arithmetic, and the kernel keeps everything else away from the warps that do it.
+// scan is bound by issue and arithmetic, and everything else is kept away from the warps that do it.
 //
-// A CTA walks 128 / L channels of one sequence (L = N / 4 lanes hold a channel, four states each), 32 tokens a tile, with
-// four warps that only scan and four that only serve them, one barrier a tile:
-//   serving warps load tile s (x, dt, B, C; the loads go out a tile ahead), apply softplus, and leave dt, dt x, B and C as
-//     fp32 in shared memory, tokens side by side; they add up the lanes' parts of tile s - 2, and store y after skip and gate;
-//   scanning warps read four tokens of dt, dt x, B, C at a time and work on packed pairs of tokens (exponents, inputs and
-//     outputs; the memory itself goes from token to token), and leave every lane's part of y in shared memory, since
-//     adding it up over the lanes by shuffles would cost them four times what storing it does.
+// What they would wait for is shared memory: a load delivers 128 bytes a cycle to an SM whatever is the same in them, and
+// B_t, C_t are wanted by every channel (8 bytes a cell: 40 cycles a token of 32 channels, where the arithmetic takes 17).  So
+// the tensor cores spread them: D = E X with E [128 lanes, 16] one-hot rows that pick a lane's states and X [16, columns]
+// the tokens' B and C as they lie in memory puts each lane's B and C into its TMEM row, as fp32 and exactly (one term
+// of the sum is not zero; fp32 inputs go in as three bf16 parts), and tcgen05.ld reads TMEM beside the shared memory.
+//
+// A group of eight warps walks 128 / L channels of one sequence (L = N / 4 lanes hold a channel, four states each), 32 tokens
+// a tile; four of its warps only scan and four only serve them, one barrier a tile:
+//   serving warps load tile s two tiles ahead, lay B and C out and issue their product, apply softplus, and leave dt and
+//     dt x as fp32 in shared memory, tokens side by side; they add up the lanes' parts of tile s - 2, and store y after skip
+//     and gate;
+//   scanning warps work on packed pairs of tokens (exponents, inputs, outputs; the memory itself goes from token to token)
+//     and leave every lane's part of y in shared memory: adding it up by shuffles would cost four times what storing does.
+// A CTA is one group, or two (over the same B and C) where there are more blocks of channels than SMs; it takes all of
+// TMEM (two tiles of 256 columns), so there is one to an SM.
 // Few channels and a long sequence: its parts ("segments") run side by side.  A first launch walks all but a sequence's last
 // segment from an empty memory and leaves the memory and the sum of dt; in the second, every CTA joins those before it,
 // h <- exp(A sum dt) h + local, which costs the walk of the memories (not of y) twice.
 #include <algorithm>
 
+#include "linear_tc.cuh"
 #include "ssm_internal.cuh"
 #include "ssm_math.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256, kServe = 128;     // threads of a CTA; of them, those that serve
+using lin::Waits;
+using namespace ptx;
+
+constexpr int kServe = 128;                     // threads of a group that serve (as many scan)
 constexpr int kTile = 32;                       // tokens
 constexpr int kPitch = kTile + 4;               // floats from row to row: rows start four banks apart
 
 // Layout of the shared memory, in floats.  Pads keep the rows that a warp's lanes touch at once in different banks.
-template <int L> struct Lay {
-    static constexpr int N = 4 * L, CH = 128 / L;               // states, channels of a CTA
+template <typename T, int L> struct Lay {
+    static constexpr int N = 4 * L, CH = 128 / L;               // states, channels of a group
     static constexpr int VC = CH >= 32 ? 8 : CH / 4;            // channels that a serving lane loads together
     static constexpr int NQ = CH / VC;
     static constexpr int QPAD = L == 2 ? 4 : L == 4 ? 8 : L == 8 ? 24 : 0;
     static constexpr int LPAD = L == 2 ? 16 : L == 4 ? 8 : 4;
-    static constexpr int ROWS = CH * kPitch + NQ * QPAD, HEADS = N * kPitch, PART = CH * kPitch + LPAD;
-    static constexpr int IN = 2 * ROWS + 2 * HEADS, OUT = L * PART;
-    static constexpr size_t bytes(bool local) { return (size_t)(2 * IN + (local ? 0 : 2 * OUT)) * 4; }
+    static constexpr int ROWS = CH * kPitch + NQ * QPAD, PART = CH * kPitch + LPAD;
+    static constexpr int IN = 2 * ROWS, OUT = L * PART;         // per group, two of each
     static __device__ __forceinline__ int row(int c) { return c * kPitch + c / VC * QPAD; }
     static constexpr int PC = L <= 4 ? 2 : 1;                   // channels that a serving lane finishes together
     static constexpr int IN_TASKS = kTile * NQ / kServe, BC_TASKS = L / 2;
     static constexpr int OUT_TASKS = CH / PC * (kTile / 4) > kServe ? CH / PC * (kTile / 4) / kServe : 1;
+    // The product's operands: rows of 128 bytes (K-major, 128-byte swizzle) whose four K steps of 16 hold tile buffer 0,
+    // buffer 1 and E, KS steps each; a block of rows more for every four steps.
+    static constexpr int PARTS = sizeof(T) == 2 ? 1 : 3, KS = (PARTS * L + 15) / 16, BLOCKS = (3 * KS + 3) / 4;
+    static constexpr int XROWS(bool local) { return local ? 128 : 256; }
+    static constexpr size_t bytes(int groups, bool local) {
+        return 1024 + (size_t)BLOCKS * XROWS(local) * 128 + (size_t)groups * (2 * IN + (local ? 0 : 2 * OUT)) * 4;
+    }
 };
 
 struct Walk {
     Ssm a;
-    int cpg, bpg, blocks;       // channels and CTAs of a group, CTAs of all
+    int cpg, bpg, blocks;       // channels and CTAs of a group of heads, CTAs of all
     int seg;                    // tokens of a segment
     long items;
     float *local, *sums;        // [items, D, N], [items, D]; nullptr where nothing is split
+    WsHeader *hdr;
+};
+
+struct Ctl {
+    uint64_t full[2];           // the tile's product is in TMEM
+    uint32_t tmem;
+    int fail;
 };
 
 // The segment `item`, with the rows a packed batch has (whatever its prefix array says, none outside them is touched).
@@ -63,28 +88,81 @@ __device__ __forceinline__ bool walk_item(const Walk &w, long item, LinItem &it)
     return true;
 }
 
+// Byte of K element k (16 a step) of row r, step `slot`, in the operands.
+__device__ __forceinline__ uint32_t op_byte(int rows, int r, int slot, int k) {
+    const int chunk = (slot & 3) * 2 + (k >> 3);
+    return (uint32_t)((slot >> 2) * rows * 128 + r * 128 + ((chunk ^ (r & 7)) << 4) + (k & 7) * 2);
+}
+__device__ __forceinline__ uint64_t op_desc(uint32_t base, int rows, int slot) {
+    return smem_desc(base + (uint32_t)((slot >> 2) * rows * 128 + (slot & 3) * 32), 16u, 1024u, kSwizzle128B);
+}
+
+// What a lane has asked of TMEM is there: nothing that uses it may come before.
+template <int N> __device__ __forceinline__ void landed(uint32_t (&r)[N]) {
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
 // VEC: rows and heads start on boundaries of what a lane loads, and groups hold whole loads.
-template <typename T, int L, bool VEC, bool LOCAL>
-__global__ void __launch_bounds__(kThreads, 2) ssm_scan_kernel(const __grid_constant__ Walk w) {
-    using Y = Lay<L>;
-    extern __shared__ __align__(16) float smem[];
+template <typename T, int L, bool VEC, bool LOCAL, int GROUPS>
+__global__ void __launch_bounds__(GROUPS * 256, 1) ssm_scan_kernel(const __grid_constant__ Walk w) {
+    using Y = Lay<T, L>;
+    constexpr int XR = Y::XROWS(LOCAL), W = LOCAL ? 4 : 8;      // columns of X: 4 W of every four tokens, W of a state
+    constexpr uint32_t COLS = LOCAL ? 256 : 512;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    __shared__ Ctl ctl;
     const Ssm &a = w.a;
     const long item = blockIdx.x / w.blocks;
-    const int cb = (int)(blockIdx.x - item * w.blocks), g = cb / w.bpg, c0 = (cb - g * w.bpg) * Y::CH;   // first channel in the group
-    if (LOCAL) next_may_start();
+    const int cb = (int)(blockIdx.x - item * w.blocks), g = cb / w.bpg, sub = threadIdx.x / 256;
+    const int c0 = ((cb - g * w.bpg) * GROUPS + sub) * Y::CH;           // the group's first channel among its heads'
+    const bool role = (threadIdx.x & 255) < 128;                        // scan
+    const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid / 32;
     LinItem it;
+    if (blockIdx.x == 0 && threadIdx.x == 0 && (LOCAL || !w.local)) w.hdr->error = 0;       // (no wait can run out this early)
     if (!walk_item(w, item, it) || (LOCAL && it.p == it.nseg - 1)) {
+        if (LOCAL) next_may_start();
         if (!LOCAL && w.local) wait_for_previous();
         return;
     }
+    const uint32_t x_base = (smem_u32(raw) + 1023u) & ~1023u;
+    uint8_t *xs = raw + (x_base - smem_u32(raw));
+    float *fl = reinterpret_cast<float *>(xs + Y::BLOCKS * XR * 128) + sub * (2 * Y::IN + (LOCAL ? 0 : 2 * Y::OUT));
+    float *in = fl, *out = fl + 2 * Y::IN;
+    if (threadIdx.x == 0) {
+        mbar_init(&ctl.full[0], 1);
+        mbar_init(&ctl.full[1], 1);
+        ctl.fail = 0;
+        fence_mbar_init();
+    }
+    for (int i = threadIdx.x; i < Y::BLOCKS * XR * 8; i += GROUPS * 256) reinterpret_cast<uint4 *>(xs)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async();
+    if (threadIdx.x >= 224 && threadIdx.x < 256) {
+        tmem_alloc(&ctl.tmem, COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (LOCAL) next_may_start();        // behind the allocation
+    const uint32_t tm = ctl.tmem;
+    if (threadIdx.x < 128) {            // E: lane m has state l of each quad, in all parts
+#pragma unroll
+        for (int p = 0; p < Y::PARTS; ++p) {
+            const int k = p * L + tid % L;
+            *reinterpret_cast<__nv_bfloat16 *>(xs + op_byte(XR, tid, 2 * Y::KS + k / 16, k & 15)) = __float2bfloat16_rn(1.f);
+        }
+        fence_proxy_async();
+    }
+    const Waits wt{&ctl.fail, w.hdr};
     const int t0 = min(it.p * w.seg, it.len), len = min(w.seg, it.len - t0), nt = (len + kTile - 1) / kTile;
-    const int d0 = g * w.cpg + c0, live = min(Y::CH, w.cpg - c0);      // channels d0 .. d0 + live
+    const int d0 = g * w.cpg + c0, live = min(Y::CH, w.cpg - c0);      // channels d0 .. d0 + live (none: live <= 0)
     const long b = a.s.cu ? 0 : it.n, row0 = (a.s.cu ? it.start : 0) + t0;
-    float *in = smem, *out = smem + 2 * Y::IN;
+    const int last = nt + (LOCAL ? 0 : 1);
 
-    if (threadIdx.x >= kServe) {        // ---------------------------------------------------------------- scan
-        const int tid = threadIdx.x - kServe, c = tid / L, l = tid % L;
-        const int d = d0 + min(c, live - 1);
+    if (role) {         // ------------------------------------------------------------------------------------- scan
+        const int c = tid / L, l = tid % L;
+        const int d = min(d0 + min(c, max(live - 1, 0)), a.D - 1);
         const long at = ((long)it.n * a.D + d) * Y::N + l;
         float h[4];
         Two A[4];
@@ -108,21 +186,37 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_scan_kernel(const __grid_cons
             }
         }
         Two sum = two(0.f, 0.f);
-        for (int s = 0; s <= nt + (LOCAL ? 0 : 1); ++s) {
+        const uint32_t mine = tm + ((uint32_t)(32 * warp) << 16);
+        for (int s = 0; s <= last; ++s) {
+            tc_fence_before();
             __syncthreads();
             if (s < 1 || s > nt) continue;
-            const float *base = in + ((s - 1) & 1) * Y::IN;
-            const float *dtp = base + Y::row(c), *dxp = dtp + Y::ROWS, *Bp = base + 2 * Y::ROWS + l * kPitch, *Cp = Bp + Y::HEADS;
-            float *op = out + ((s - 1) & 1) * Y::OUT + l * Y::PART + c * kPitch;
-#pragma unroll 4
-            for (int t = 0; t < kTile; t += 4) {
-                const ulonglong2 dt = *reinterpret_cast<const ulonglong2 *>(dtp + t), dx = *reinterpret_cast<const ulonglong2 *>(dxp + t);
+            const int k = s - 1;
+            const float *dtp = in + (k & 1) * Y::IN + Y::row(c), *dxp = dtp + Y::ROWS;
+            float *op = out + (k & 1) * Y::OUT + l * Y::PART + c * kPitch;
+            const uint32_t from = mine + (k & 1) * XR;
+            wt.warp(&ctl.full[k & 1], (k >> 1) & 1, 1);
+            tc_fence_after();
+            uint32_t bc[2][4 * W];
+            auto ask = [&](int t4, uint32_t (&r)[4 * W]) {
+                if constexpr (LOCAL)
+                    tmem_ld16(from + t4 * 16, r);
+                else
+                    tmem_ld32(from + t4 * 32, r);
+            };
+            ask(0, bc[0]);
+#pragma unroll
+            for (int t4 = 0; t4 < kTile / 4; ++t4) {
+                const ulonglong2 dt = *reinterpret_cast<const ulonglong2 *>(dtp + 4 * t4), dx = *reinterpret_cast<const ulonglong2 *>(dxp + 4 * t4);
+                uint32_t(&r)[4 * W] = bc[t4 & 1];
+                landed(r);
+                if (t4 + 1 < kTile / 4) ask(t4 + 1, bc[(t4 + 1) & 1]);
+                auto col = [&](int k0) { return two(__uint_as_float(r[k0]), __uint_as_float(r[k0 + 1])); };
                 if (LOCAL) sum = add2(sum, add2(dt.x, dt.y));
                 ulonglong2 y = make_ulonglong2(0, 0);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const ulonglong2 B = *reinterpret_cast<const ulonglong2 *>(Bp + L * i * kPitch + t);
-                    const Two p0 = mul2(dt.x, A[i]), p1 = mul2(dt.y, A[i]), u0 = mul2(dx.x, B.x), u1 = mul2(dx.y, B.y);
+                    const Two p0 = mul2(dt.x, A[i]), p1 = mul2(dt.y, A[i]), u0 = mul2(dx.x, col(W * i)), u1 = mul2(dx.y, col(W * i + 2));
                     float e0, e1, e2, e3, v0, v1, v2, v3;
                     each(p0, e0, e1);
                     each(p1, e2, e3);
@@ -130,157 +224,199 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_scan_kernel(const __grid_cons
                     each(u1, v2, v3);
                     const float h0 = fmaf(ex2(e0), h[i], v0), h1 = fmaf(ex2(e1), h0, v1), h2 = fmaf(ex2(e2), h1, v2);
                     h[i] = fmaf(ex2(e3), h2, v3);
-                    if (!LOCAL) {
-                        const ulonglong2 C = *reinterpret_cast<const ulonglong2 *>(Cp + L * i * kPitch + t);
-                        y.x = i ? fma2(two(h0, h1), C.x, y.x) : mul2(two(h0, h1), C.x);
-                        y.y = i ? fma2(two(h2, h[i]), C.y, y.y) : mul2(two(h2, h[i]), C.y);
+                    if constexpr (!LOCAL) {
+                        y.x = i ? fma2(two(h0, h1), col(W * i + 4), y.x) : mul2(two(h0, h1), col(W * i + 4));
+                        y.y = i ? fma2(two(h2, h[i]), col(W * i + 6), y.y) : mul2(two(h2, h[i]), col(W * i + 6));
                     }
                 }
-                if (!LOCAL) *reinterpret_cast<ulonglong2 *>(op + t) = y;
+                if (!LOCAL) *reinterpret_cast<ulonglong2 *>(op + 4 * t4) = y;
             }
         }
-        if (c >= live) return;
-        if (LOCAL) {
+        if (c < live) {
+            if (LOCAL) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w.local[(item * a.D + d) * Y::N + l + L * i] = h[i];
-            float s0, s1;
-            each(sum, s0, s1);
-            if (l == 0) w.sums[item * a.D + d] = s0 + s1;
-        } else if (a.hT && it.p == it.nseg - 1) {
+                for (int i = 0; i < 4; ++i) w.local[(item * a.D + d) * Y::N + l + L * i] = h[i];
+                float s0, s1;
+                each(sum, s0, s1);
+                if (l == 0) w.sums[item * a.D + d] = s0 + s1;
+            } else if (a.hT && it.p == it.nseg - 1) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a.hT[at + L * i] = h[i];
+                for (int i = 0; i < 4; ++i) a.hT[at + L * i] = h[i];
+            }
         }
-        return;
-    }
-
-    // ------------------------------------------------------------------------------------------------ serve
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
-    const int q = tid % Y::NQ, cq = q * Y::VC, tq = tid / Y::NQ;       // input: channels cq.., token tq (+ kServe / NQ)
-    float bias[Y::VC];
+    } else {            // ------------------------------------------------------------------------------------- serve
+        const int q = tid % Y::NQ, cq = q * Y::VC, tq = tid / Y::NQ;       // input: channels cq.., token tq (+ kServe / NQ)
+        float bias[Y::VC];
 #pragma unroll
-    for (int i = 0; i < Y::VC; ++i) bias[i] = a.bias && cq + i < live ? a.bias[d0 + cq + i] : 0.f;
-    const T *xp = static_cast<const T *>(a.x.p) + b * a.x.b + row0 * a.x.t + d0;
-    const T *dp = static_cast<const T *>(a.dt.p) + b * a.dt.b + row0 * a.dt.t + d0;
-    const T *zp = static_cast<const T *>(a.gate.p) + (a.gate.p ? b * a.gate.b + row0 * a.gate.t + d0 : 0);
-    const T *Bp = static_cast<const T *>(a.B.p) + b * a.B.b + row0 * a.B.t + g * a.B.g;
-    const T *Cp = static_cast<const T *>(a.C.p) + b * a.C.b + row0 * a.C.t + g * a.C.g;
-    T *yp = LOCAL ? nullptr : static_cast<T *>(a.y.p) + b * a.y.b + row0 * a.y.t + d0;
-    Few<T, Y::VC> rx[Y::IN_TASKS], rd[Y::IN_TASKS];
-    Few<T, 4> rh[Y::BC_TASKS];
-    auto fetch = [&](int s) {
+        for (int i = 0; i < Y::VC; ++i) bias[i] = a.bias && cq + i < live ? a.bias[d0 + cq + i] : 0.f;
+        const T *xp = static_cast<const T *>(a.x.p) + b * a.x.b + row0 * a.x.t + d0;
+        const T *dp = static_cast<const T *>(a.dt.p) + b * a.dt.b + row0 * a.dt.t + d0;
+        const T *zp = static_cast<const T *>(a.gate.p) + (a.gate.p ? b * a.gate.b + row0 * a.gate.t + d0 : 0);
+        const T *Bp = static_cast<const T *>(a.B.p) + b * a.B.b + row0 * a.B.t + g * a.B.g;
+        const T *Cp = static_cast<const T *>(a.C.p) + b * a.C.b + row0 * a.C.t + g * a.C.g;
+        T *yp = LOCAL ? nullptr : static_cast<T *>(a.y.p) + b * a.y.b + row0 * a.y.t + d0;
+        Few<T, Y::VC> rx[2][Y::IN_TASKS], rd[2][Y::IN_TASKS];
+        Few<T, 4> rh[2][Y::BC_TASKS];
+        auto fetch = [&](int s, Few<T, Y::VC> (&fx)[Y::IN_TASKS], Few<T, Y::VC> (&fd)[Y::IN_TASKS], Few<T, 4> (&fh)[Y::BC_TASKS]) {
 #pragma unroll
-        for (int j = 0; j < Y::IN_TASKS; ++j) {
-            const int t = s * kTile + tq + j * (kServe / Y::NQ), n = t < len ? live - cq : 0;
-            rx[j].template load<VEC>(xp + (long)t * a.x.t + cq, n);
-            rd[j].template load<VEC>(dp + (long)t * a.dt.t + cq, n);
+            for (int j = 0; j < Y::IN_TASKS; ++j) {
+                const int t = s * kTile + tq + j * (kServe / Y::NQ), n = t < len ? live - cq : 0;
+                fx[j].template load<VEC>(xp + (long)t * a.x.t + cq, n);
+                fd[j].template load<VEC>(dp + (long)t * a.dt.t + cq, n);
+            }
+            if (sub) return;
+#pragma unroll
+            for (int j = 0; j < Y::BC_TASKS; ++j) {      // token = lane; quad of states = the rest, B's then C's
+                const int k = warp + 4 * j, t = s * kTile + lane;
+                const bool isB = k < L;
+                if (LOCAL && !isB) continue;
+                fh[j].template load<VEC>(isB ? Bp + (long)t * a.B.t + 4 * k : Cp + (long)t * a.C.t + 4 * (k - L), t < len ? 4 : 0);
+            }
+        };
+        // output: PC channels from co on, tokens 4 to .. 4 to + 3 (of the task's)
+        int co, to;
+        if (L <= 4) {
+            co = 2 * ((lane & 3) | (lane >> 3) << 2);
+            to = (lane >> 2 & 1) | warp << 1;
+        } else if (L == 8) {
+            co = lane & 15;
+            to = lane >> 4 | warp << 1;
+        } else {
+            co = lane & 7;
+            to = lane >> 3 | warp << 2;
         }
-#pragma unroll
-        for (int j = 0; j < Y::BC_TASKS; ++j) {      // token = lane; quad of states = the rest, B's then C's
-            const int k = warp + 4 * j, t = s * kTile + lane;
-            const bool isB = k < L;
-            if (LOCAL && !isB) continue;
-            rh[j].template load<VEC>(isB ? Bp + (long)t * a.B.t + 4 * k : Cp + (long)t * a.C.t + 4 * (k - L), t < len ? 4 : 0);
-        }
-    };
-    // output: PC channels from co on, tokens 4 to .. 4 to + 3 (of the task's)
-    int co, to;
-    if (L <= 4) {
-        co = 2 * ((lane & 3) | (lane >> 3) << 2);
-        to = (lane >> 2 & 1) | warp << 1;
-    } else if (L == 8) {
-        co = lane & 15;
-        to = lane >> 4 | warp << 1;
-    } else {
-        co = lane & 7;
-        to = lane >> 3 | warp << 2;
-    }
-    const bool finishes = to < kTile / 4;
-    float skip[Y::OUT_TASKS][Y::PC];
-    Few<T, Y::PC> ox[Y::OUT_TASKS][4], oz[Y::OUT_TASKS][4];
-#pragma unroll
-    for (int j = 0; j < Y::OUT_TASKS; ++j)
-#pragma unroll
-        for (int i = 0; i < Y::PC; ++i) {
-            const int c = co + j * 32 + i;
-            skip[j][i] = a.skip && c < live ? a.skip[d0 + c] : 0.f;
-        }
-    auto fetch_out = [&](int s) {
+        const bool finishes = to < kTile / 4;
+        float skip[Y::OUT_TASKS][Y::PC];
+        Few<T, Y::PC> ox[2][Y::OUT_TASKS][4], oz[2][Y::OUT_TASKS][4];
 #pragma unroll
         for (int j = 0; j < Y::OUT_TASKS; ++j)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int t = s * kTile + 4 * to + k, c = co + j * 32, n = finishes && t < len ? live - c : 0;
-                ox[j][k].template load<VEC>(xp + (long)t * a.x.t + c, n);
-                if (a.gate.p) oz[j][k].template load<VEC>(zp + (long)t * a.gate.t + c, n);
+            for (int i = 0; i < Y::PC; ++i) {
+                const int c = co + j * 32 + i;
+                skip[j][i] = a.skip && c < live ? a.skip[d0 + c] : 0.f;
             }
-    };
-    fetch(0);
-    for (int s = 0; s <= nt + (LOCAL ? 0 : 1); ++s) {
-        __syncthreads();
-        if (s < nt) {
-            float *base = in + (s & 1) * Y::IN;
+        // one step of the pipeline; P = s & 1 names the registers that tiles of this parity go through
+        auto step = [&](int s, auto parity) {
+            constexpr int P = decltype(parity)::value;
+            __syncthreads();
+            if (s < nt) {
+                if (!sub) {             // B and C into the operand's rows (token, state, B or C), parts of L states side by side
 #pragma unroll
-            for (int j = 0; j < Y::IN_TASKS; ++j) {
-                const int tt = tq + j * (kServe / Y::NQ);
-                const bool there = s * kTile + tt < len;        // behind the last token the memory stays: dt = 0
+                    for (int j = 0; j < Y::BC_TASKS; ++j) {
+                        const int k = warp + 4 * j, quad = k < L ? k : k - L;
+                        if (LOCAL && k >= L) continue;
+                        const Few<T, 4> &f = rh[P][j];
+                        const int r0 = (lane >> 2) * 4 * W + (k < L ? 0 : 4) + (lane & 3);
 #pragma unroll
-                for (int i = 0; i < Y::VC; ++i) {
-                    float v = rd[j][i] + bias[i];
-                    if (a.softplus) v = softplus<T>(v);
-                    v = there ? v : 0.f;
-                    float *to_row = base + Y::row(cq + i) + tt;
-                    to_row[0] = v;
-                    to_row[Y::ROWS] = there ? v * rx[j][i] : 0.f;
-                }
-            }
+                        for (int e = 0; e < 4; e += 2) {        // states 4 quad + e and the next: column i, K element l
+                            const int n = 4 * quad + e, i = n / L, l = n % L;
+                            if constexpr (sizeof(T) == 2) {
+                                *reinterpret_cast<uint32_t *>(xs + op_byte(XR, r0 + i * W, P * Y::KS, l)) = f.w[e / 2];
+                            } else {
+                                float u = f[e], v = f[e + 1];
 #pragma unroll
-            for (int j = 0; j < Y::BC_TASKS; ++j) {
-                const int k = warp + 4 * j;
-                if (LOCAL && k >= L) continue;
-                float *to_row = base + 2 * Y::ROWS + (k < L ? 4 * k * kPitch : Y::HEADS + 4 * (k - L) * kPitch) + lane;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) to_row[i * kPitch] = rh[j][i];
-            }
-            if (s + 1 < nt) fetch(s + 1);
-        }
-        if (!LOCAL) {
-            if (s >= 2 && finishes) {
-                const float *base = out + (s & 1) * Y::OUT;
-#pragma unroll
-                for (int j = 0; j < Y::OUT_TASKS; ++j) {
-                    const int c = co + j * 32;
-                    Two y[Y::PC][2];
-#pragma unroll
-                    for (int i = 0; i < Y::PC; ++i) {
-                        y[i][0] = y[i][1] = two(0.f, 0.f);
-#pragma unroll
-                        for (int l = 0; l < L; ++l) {
-                            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(base + l * Y::PART + (c + i) * kPitch + 4 * to);
-                            y[i][0] = l ? add2(y[i][0], v.x) : v.x;
-                            y[i][1] = l ? add2(y[i][1], v.y) : v.y;
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int t = (s - 2) * kTile + 4 * to + k;
-                        float v[Y::PC];
-#pragma unroll
-                        for (int i = 0; i < Y::PC; ++i) {
-                            float v0, v1;
-                            each(y[i][k / 2], v0, v1);
-                            v[i] = fmaf(skip[j][i], ox[j][k][i], k & 1 ? v1 : v0);
-                            if (a.gate.p) {
-                                const float z = oz[j][k][i];
-                                float rest;
-                                v[i] *= z * sigmoid<T>(z, rest);
+                                for (int p = 0; p < Y::PARTS; ++p) {
+                                    const int kk = p * L + l;
+                                    *reinterpret_cast<uint32_t *>(xs + op_byte(XR, r0 + i * W, P * Y::KS + kk / 16, kk & 15)) = lin::top2(u, v);
+                                    u = lin::rest(u);
+                                    v = lin::rest(v);
+                                }
                             }
                         }
-                        Few<T, Y::PC>::template store<VEC>(yp + (long)t * a.y.t + c, v, t < len ? live - c : 0);
+                    }
+                    fence_proxy_async();
+                    lin::named_sync(1, kServe);
+                    if (tid == 0) {
+                        tc_fence_after();
+                        constexpr uint32_t id = idesc_bf16_f32(128, XR, false, false);
+#pragma unroll
+                        for (int p = 0; p < Y::KS; ++p) {
+                            const uint64_t e = op_desc(x_base, XR, 2 * Y::KS + p), x = op_desc(x_base, XR, P * Y::KS + p);
+                            if (p)
+                                mma_ss<1>(tm + P * XR, e, x, id);
+                            else
+                                mma_ss<0>(tm + P * XR, e, x, id);
+                        }
+                        mma_commit(&ctl.full[P]);
                     }
                 }
+                float *base = in + P * Y::IN;
+#pragma unroll
+                for (int j = 0; j < Y::IN_TASKS; ++j) {
+                    const int tt = tq + j * (kServe / Y::NQ);
+                    const bool there = s * kTile + tt < len;        // behind the last token the memory stays: dt = 0
+#pragma unroll
+                    for (int i = 0; i < Y::VC; ++i) {
+                        float v = rd[P][j][i] + bias[i];
+                        if (a.softplus) v = softplus<T>(v);
+                        v = there ? v : 0.f;
+                        float *to_row = base + Y::row(cq + i) + tt;
+                        to_row[0] = v;
+                        to_row[Y::ROWS] = there ? v * rx[P][j][i] : 0.f;
+                    }
+                }
+                if (s + 2 < nt) fetch(s + 2, rx[P], rd[P], rh[P]);
             }
-            if (s >= 1 && s <= nt) fetch_out(s - 1);
+            if constexpr (!LOCAL) {
+                if (s >= 2 && finishes) {
+                    const float *base = out + P * Y::OUT;
+#pragma unroll
+                    for (int j = 0; j < Y::OUT_TASKS; ++j) {
+                        const int c = co + j * 32;
+                        Two y[Y::PC][2];
+#pragma unroll
+                        for (int i = 0; i < Y::PC; ++i) {
+                            y[i][0] = y[i][1] = two(0.f, 0.f);
+#pragma unroll
+                            for (int l = 0; l < L; ++l) {
+                                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(base + l * Y::PART + (c + i) * kPitch + 4 * to);
+                                y[i][0] = l ? add2(y[i][0], v.x) : v.x;
+                                y[i][1] = l ? add2(y[i][1], v.y) : v.y;
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int t = (s - 2) * kTile + 4 * to + k;
+                            float v[Y::PC];
+#pragma unroll
+                            for (int i = 0; i < Y::PC; ++i) {
+                                float v0, v1;
+                                each(y[i][k / 2], v0, v1);
+                                v[i] = fmaf(skip[j][i], ox[P][j][k][i], k & 1 ? v1 : v0);
+                                if (a.gate.p) {
+                                    const float z = oz[P][j][k][i];
+                                    float rest;
+                                    v[i] *= z * sigmoid<T>(z, rest);
+                                }
+                            }
+                            Few<T, Y::PC>::template store<VEC>(yp + (long)t * a.y.t + c, v, t < len ? live - c : 0);
+                        }
+                    }
+                }
+                if (s < nt && finishes) {
+#pragma unroll
+                    for (int j = 0; j < Y::OUT_TASKS; ++j)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int t = s * kTile + 4 * to + k, c = co + j * 32, n = t < len ? live - c : 0;
+                            ox[P][j][k].template load<VEC>(xp + (long)t * a.x.t + c, n);
+                            if (a.gate.p) oz[P][j][k].template load<VEC>(zp + (long)t * a.gate.t + c, n);
+                        }
+                }
+            }
+        };
+        fetch(0, rx[0], rd[0], rh[0]);
+        if (nt > 1) fetch(1, rx[1], rd[1], rh[1]);
+        for (int s = 0; s <= last; s += 2) {
+            step(s, std::integral_constant<int, 0>());
+            if (s + 1 <= last) step(s + 1, std::integral_constant<int, 1>());
         }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x >= 224 && threadIdx.x < 256) {
+        tc_fence_after();
+        tmem_dealloc(tm, COLS);
     }
 }
 
@@ -334,42 +470,55 @@ long split_items(int nseq, long rows, int blocks, int sms) {      // of any segm
     return rows / seg + nseq;
 }
 
-template <int L> int blocks_of(int D, int G) { return (D / G + Lay<L>::CH - 1) / Lay<L>::CH * G; }
+template <int L> int blocks_of(int D, int G) { return (D / G + 128 / L - 1) / (128 / L) * G; }
 
-template <typename T, int L, bool VEC> cudaError_t launch(const Ssm &a, cudaStream_t st) {
-    using Y = Lay<L>;
-    Walk w{};
-    w.a = a;
-    w.cpg = a.D / a.G;
-    w.bpg = (w.cpg + Y::CH - 1) / Y::CH;
-    w.blocks = w.bpg * a.G;
-    const long rows = a.s.cu ? a.total : (long)a.s.nseq * a.s.T;
-    const int max_len = a.s.cu ? a.max_len : a.s.T;
-    w.seg = a.hT && a.hT == a.h0 ? 0 : pick_segment(a, rows, max_len, w.blocks);
-    const bool split = w.seg > 0;
-    if (!split) w.seg = std::max(max_len, 1);
-    w.items = lin_items(a.s.nseq, a.s.cu ? a.total : a.s.T, max_len, a.s.cu != nullptr, w.seg);
-    const long ctas = w.items * w.blocks;
-    if (ctas > 0x7fffffffL) return cudaErrorInvalidValue;
-    if (split) {
-        w.local = static_cast<float *>(a.ws);
-        w.sums = w.local + w.items * (long)a.D * a.N;
-        const auto first = ssm_scan_kernel<T, L, VEC, true>;
-        cudaError_t e = cudaFuncSetAttribute(first, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Y::bytes(true));
-        if (e != cudaSuccess) return e;
-        first<<<(unsigned)ctas, kThreads, Y::bytes(true), st>>>(w);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    const auto main = ssm_scan_kernel<T, L, VEC, false>;
-    cudaError_t e = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Y::bytes(false));
+template <typename T, int L, bool VEC, bool LOCAL, int GROUPS> cudaError_t start(const Walk &w, long ctas, bool after, cudaStream_t st) {
+    static lin::SmemOnce once;
+    constexpr size_t bytes = Lay<T, L>::bytes(GROUPS, LOCAL);
+    static_assert(bytes <= 232448 - 64, "shared memory");
+    const auto kernel = ssm_scan_kernel<T, L, VEC, LOCAL, GROUPS>;
+    const cudaError_t e = once(kernel, (int)bytes);
     if (e != cudaSuccess) return e;
-    if (split) return launch_after(main, dim3((unsigned)ctas), kThreads, Y::bytes(false), st, w);
-    main<<<(unsigned)ctas, kThreads, Y::bytes(false), st>>>(w);
+    if (after) return launch_after(kernel, dim3((unsigned)ctas), GROUPS * 256, bytes, st, w);
+    kernel<<<(unsigned)ctas, GROUPS * 256, bytes, st>>>(w);
     return cudaGetLastError();
 }
 
+template <typename T, int L, bool VEC> cudaError_t launch(const Ssm &a, cudaStream_t st) {
+    using Y = Lay<T, L>;
+    Walk w{};
+    w.a = a;
+    w.hdr = static_cast<WsHeader *>(a.ws);
+    w.cpg = a.D / a.G;
+    const long rows = a.s.cu ? a.total : (long)a.s.nseq * a.s.T;
+    const int max_len = a.s.cu ? a.max_len : a.s.T;
+    w.seg = a.hT && a.hT == a.h0 ? 0 : pick_segment(a, rows, max_len, blocks_of<L>(a.D, a.G));
+    const bool split = w.seg > 0;
+    if (!split) w.seg = std::max(max_len, 1);
+    w.items = lin_items(a.s.nseq, a.s.cu ? a.total : a.s.T, max_len, a.s.cu != nullptr, w.seg);
+    // two groups to a CTA where one would leave blocks waiting for an SM
+    constexpr bool two_groups = sizeof(T) == 2;      // fp32 groups' registers are more than half an SM's
+    const bool pair = two_groups && w.items * blocks_of<L>(a.D, a.G) > a.sms && w.cpg > Y::CH;
+    w.bpg = (w.cpg + Y::CH * (1 + pair) - 1) / (Y::CH * (1 + pair));
+    w.blocks = w.bpg * a.G;
+    const long ctas = w.items * w.blocks;
+    if (ctas > 0x7fffffffL) return cudaErrorInvalidValue;
+    if (split) {
+        w.local = reinterpret_cast<float *>(static_cast<char *>(a.ws) + sizeof(WsHeader));
+        w.sums = w.local + w.items * (long)a.D * a.N;
+        Walk one = w;       // one group to a CTA: two of these share an SM
+        one.bpg = (w.cpg + Y::CH - 1) / Y::CH;
+        one.blocks = one.bpg * a.G;
+        const cudaError_t e = start<T, L, VEC, true, 1>(one, one.items * one.blocks, false, st);
+        if (e != cudaSuccess) return e;
+    }
+    if constexpr (two_groups)
+        if (pair) return start<T, L, VEC, false, 2>(w, ctas, split, st);
+    return start<T, L, VEC, false, 1>(w, ctas, split, st);
+}
+
 template <typename T, int L> cudaError_t run(const Ssm &a, cudaStream_t st) {
-    using Y = Lay<L>;
+    using Y = Lay<T, L>;
     const int cpg = a.D / a.G;
     const bool vec = cpg % Y::VC == 0 && few_view<T>(a.x, Y::VC, false) && few_view<T>(a.dt, Y::VC, false) &&
                      few_view<T>(a.gate, Y::VC, false) && few_view<T>(a.y, Y::VC, false) && few_view<T>(a.B, 4, true) &&

@@ -607,8 +607,11 @@ kda_status kda_conv_bwd(const void *d_y, const void *x, const float *weight, con
  *           at); any alignment of the element type (16-byte multiples run faster).
  *   initial_state, final_state   [B,D,N] float32 or NULL.  They may be the same array (a long sequence is
  *           then not split over the GPU), and must not overlap otherwise.
- *   ws      at least the query's bytes, 16-byte aligned.
- * Memories, their sums and exp are fp32 whatever the type.  B, nseq, T == 0 are allowed.  At most 65535
+ *   ws      at least the query's bytes, 16-byte aligned; a kernel's bounded wait that runs out is recorded
+ *           in its header (kda_query_device_error).
+ * Memories, their sums and exp are fp32 whatever the type.  An infinite or NaN x, dt or gate stays in its
+ * channel; an infinite or NaN B_in or C_in reaches all channels of its group from its token on.
+ * B, nseq, T == 0 are allowed; without a sequence nothing is touched, the header included.  At most 65535
  * sequences.
  */
 size_t kda_ssm_chunk_fwd_workspace(int B, int T, int D, int G, int N, kda_dtype dtype);
