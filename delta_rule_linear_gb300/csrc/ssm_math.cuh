@@ -141,4 +141,59 @@ template <typename T, int N> struct Few {
     }
 };
 
+__device__ __forceinline__ uint32_t shared_at(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+// BYTES from global to shared memory behind the thread's back, zeros behind the first `have` of them.
+template <int BYTES> __device__ __forceinline__ void copy_async(void *to, const void *from, int have) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(shared_at(to)), "l"(from), "r"(have) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(shared_at(to)), "l"(from), "n"(BYTES), "r"(have) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory"); }
+
+// N elements of each of THREADS threads in shared memory, copied there and read again by the thread itself (no barrier):
+// 16-byte units of the threads side by side.
+template <typename T, int N, int THREADS> struct Own {
+    static constexpr int BYTES = N * (int)sizeof(T), UNIT = BYTES < 16 ? BYTES : 16, UNITS = BYTES / UNIT;
+    static constexpr int SIZE = BYTES * THREADS;
+    static constexpr int PER = UNIT / (int)sizeof(T);       // elements of a unit
+    // VEC: p is aligned to a unit and n is 0 or N; otherwise the first n elements, by twos where `pairs` (p aligned to two)
+    template <bool VEC> static __device__ __forceinline__ void fetch(uint8_t *slot, int tid, const T *p, int n, const T *some, bool pairs) {
+        uint8_t *to = slot + tid * UNIT;
+        if constexpr (VEC) {
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) copy_async<UNIT>(to + u * UNIT * THREADS, n > 0 ? p + u * PER : some, n > 0 ? UNIT : 0);
+        } else if (sizeof(T) == 4 || pairs) {
+            constexpr int E = 4 / (int)sizeof(T);
+#pragma unroll
+            for (int i = 0; i < N; i += E)
+                copy_async<4>(to + i / PER * UNIT * THREADS + i % PER * (int)sizeof(T), i < n ? p + i : some,
+                              i >= n ? 0 : i + E <= n ? 4 : 4 / E);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                *reinterpret_cast<T *>(to + i / PER * UNIT * THREADS + i % PER * (int)sizeof(T)) = i < n ? p[i] : from_f32<T>(0.f);
+        }
+    }
+    static __device__ __forceinline__ Few<T, N> read(const uint8_t *slot, int tid) {
+        Few<T, N> r;
+        const uint8_t *at = slot + tid * UNIT;
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            const uint8_t *q = at + u * UNIT * THREADS;
+            if constexpr (UNIT == 16) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(q);
+                r.w[4 * u] = v.x, r.w[4 * u + 1] = v.y, r.w[4 * u + 2] = v.z, r.w[4 * u + 3] = v.w;
+            } else if constexpr (UNIT == 8) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(q);
+                r.w[0] = v.x, r.w[1] = v.y;
+            } else {
+                r.w[0] = *reinterpret_cast<const uint32_t *>(q);
+            }
+        }
+        return r;
+    }
+};
+
 }  // namespace kda

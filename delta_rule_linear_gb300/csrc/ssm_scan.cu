@@ -15,7 +15,7 @@
 //
 // A group of eight warps walks 128 / L channels of one sequence (L = N / 4 lanes hold a channel, four states each), 32 tokens
 // a tile; four of its warps only scan and four only serve them, one barrier a tile:
-//   serving warps load tile s two tiles ahead, lay B and C out and issue their product, apply softplus, and leave dt and
+//   serving warps load tiles ahead into a ring, lay B and C out and issue their product, apply softplus, and leave dt and
 //     dt x as fp32 in shared memory, tokens side by side; they add up the lanes' parts of tile s - 2, and store y after skip
 //     and gate;
 //   scanning warps work on packed pairs of tokens (exponents, inputs, outputs; the memory itself goes from token to token)
@@ -48,18 +48,22 @@ template <typename T, int L> struct Lay {
     static constexpr int NQ = CH / VC;
     static constexpr int QPAD = L == 2 ? 4 : L == 4 ? 8 : L == 8 ? 24 : 0;
     static constexpr int LPAD = L == 2 ? 16 : L == 4 ? 8 : 4;
-    static constexpr int ROWS = CH * kPitch + NQ * QPAD, PART = CH * kPitch + LPAD;
+    static constexpr int ROWS = CH * kPitch + NQ * QPAD, PART = ROWS + LPAD;
     static constexpr int IN = 2 * ROWS, OUT = L * PART;         // per group, two of each
     static __device__ __forceinline__ int row(int c) { return c * kPitch + c / VC * QPAD; }
-    static constexpr int PC = L <= 4 ? 2 : 1;                   // channels that a serving lane finishes together
-    static constexpr int IN_TASKS = kTile * NQ / kServe, BC_TASKS = L / 2;
-    static constexpr int OUT_TASKS = CH / PC * (kTile / 4) > kServe ? CH / PC * (kTile / 4) / kServe : 1;
+    static constexpr int TASKS = kTile * NQ / kServe, BC_TASKS = L / 2;     // loads of a serving lane and tile
+    // What serving lanes have loaded, in a ring of tiles: x (from two tiles back on, for the output), dt, gate; B and C.
+    using Rows = Own<T, VC, kServe>;
+    using Quad = Own<T, 4, kServe>;
+    static constexpr int RING = sizeof(T) == 2 ? 5 : L == 2 || L == 16 ? 4 : 5, AHEAD = RING - 3;      // as many as fit
+    static constexpr int RAW = 3 * TASKS * Rows::SIZE, RAW_BC = BC_TASKS * Quad::SIZE;      // bytes of a tile
     // The product's operands: rows of 128 bytes (K-major, 128-byte swizzle) whose four K steps of 16 hold tile buffer 0,
     // buffer 1 and E, KS steps each; a block of rows more for every four steps.
     static constexpr int PARTS = sizeof(T) == 2 ? 1 : 3, KS = (PARTS * L + 15) / 16, BLOCKS = (3 * KS + 3) / 4;
     static constexpr int XROWS(bool local) { return local ? 128 : 256; }
     static constexpr size_t bytes(int groups, bool local) {
-        return 1024 + (size_t)BLOCKS * XROWS(local) * 128 + (size_t)groups * (2 * IN + (local ? 0 : 2 * OUT)) * 4;
+        return 1024 + (size_t)BLOCKS * XROWS(local) * 128 + (size_t)RING * RAW_BC +
+               (size_t)groups * ((2 * IN + (local ? 0 : 2 * OUT)) * 4 + RING * RAW);
     }
 };
 
@@ -67,6 +71,7 @@ struct Walk {
     Ssm a;
     int cpg, bpg, blocks;       // channels and CTAs of a group of heads, CTAs of all
     int seg;                    // tokens of a segment
+    int pairs;                  // every array can be read by two elements
     long items;
     float *local, *sums;        // [items, D, N], [items, D]; nullptr where nothing is split
     WsHeader *hdr;
@@ -127,8 +132,9 @@ __global__ void __launch_bounds__(GROUPS * 256, 1) ssm_scan_kernel(const __grid_
     }
     const uint32_t x_base = (smem_u32(raw) + 1023u) & ~1023u;
     uint8_t *xs = raw + (x_base - smem_u32(raw));
-    float *fl = reinterpret_cast<float *>(xs + Y::BLOCKS * XR * 128) + sub * (2 * Y::IN + (LOCAL ? 0 : 2 * Y::OUT));
-    float *in = fl, *out = fl + 2 * Y::IN;
+    constexpr int GROUP = (2 * Y::IN + (LOCAL ? 0 : 2 * Y::OUT)) * 4 + Y::RING * Y::RAW;
+    uint8_t *ring_bc = xs + Y::BLOCKS * XR * 128, *ring = ring_bc + Y::RING * Y::RAW_BC + sub * GROUP;
+    float *in = reinterpret_cast<float *>(ring + Y::RING * Y::RAW), *out = in + 2 * Y::IN;
     if (threadIdx.x == 0) {
         mbar_init(&ctl.full[0], 1);
         mbar_init(&ctl.full[1], 1);
@@ -193,7 +199,7 @@ __global__ void __launch_bounds__(GROUPS * 256, 1) ssm_scan_kernel(const __grid_
             if (s < 1 || s > nt) continue;
             const int k = s - 1;
             const float *dtp = in + (k & 1) * Y::IN + Y::row(c), *dxp = dtp + Y::ROWS;
-            float *op = out + (k & 1) * Y::OUT + l * Y::PART + c * kPitch;
+            float *op = out + (k & 1) * Y::OUT + l * Y::PART + Y::row(c);
             const uint32_t from = mine + (k & 1) * XR;
             wt.warp(&ctl.full[k & 1], (k >> 1) & 1, 1);
             tc_fence_after();
@@ -245,67 +251,59 @@ __global__ void __launch_bounds__(GROUPS * 256, 1) ssm_scan_kernel(const __grid_
             }
         }
     } else {            // ------------------------------------------------------------------------------------- serve
-        const int q = tid % Y::NQ, cq = q * Y::VC, tq = tid / Y::NQ;       // input: channels cq.., token tq (+ kServe / NQ)
-        float bias[Y::VC];
+        const int q = tid % Y::NQ, cq = q * Y::VC, tq = tid / Y::NQ;       // channels cq .. cq + VC, token tq (+ kServe / NQ)
+        float bias[Y::VC], skip[Y::VC];
 #pragma unroll
-        for (int i = 0; i < Y::VC; ++i) bias[i] = a.bias && cq + i < live ? a.bias[d0 + cq + i] : 0.f;
-        const T *xp = static_cast<const T *>(a.x.p) + b * a.x.b + row0 * a.x.t + d0;
-        const T *dp = static_cast<const T *>(a.dt.p) + b * a.dt.b + row0 * a.dt.t + d0;
-        const T *zp = static_cast<const T *>(a.gate.p) + (a.gate.p ? b * a.gate.b + row0 * a.gate.t + d0 : 0);
+        for (int i = 0; i < Y::VC; ++i) {
+            bias[i] = a.bias && cq + i < live ? a.bias[d0 + cq + i] : 0.f;
+            skip[i] = a.skip && cq + i < live ? a.skip[d0 + cq + i] : 0.f;
+        }
+        const T *xp = static_cast<const T *>(a.x.p) + b * a.x.b + row0 * a.x.t + d0 + cq;
+        const T *dp = static_cast<const T *>(a.dt.p) + b * a.dt.b + row0 * a.dt.t + d0 + cq;
+        const T *zp = a.gate.p ? static_cast<const T *>(a.gate.p) + b * a.gate.b + row0 * a.gate.t + d0 + cq : nullptr;
         const T *Bp = static_cast<const T *>(a.B.p) + b * a.B.b + row0 * a.B.t + g * a.B.g;
         const T *Cp = static_cast<const T *>(a.C.p) + b * a.C.b + row0 * a.C.t + g * a.C.g;
-        T *yp = LOCAL ? nullptr : static_cast<T *>(a.y.p) + b * a.y.b + row0 * a.y.t + d0;
-        Few<T, Y::VC> rx[2][Y::IN_TASKS], rd[2][Y::IN_TASKS];
-        Few<T, 4> rh[2][Y::BC_TASKS];
-        auto fetch = [&](int s, Few<T, Y::VC> (&fx)[Y::IN_TASKS], Few<T, Y::VC> (&fd)[Y::IN_TASKS], Few<T, 4> (&fh)[Y::BC_TASKS]) {
+        T *yp = LOCAL ? nullptr : static_cast<T *>(a.y.p) + b * a.y.b + row0 * a.y.t + d0 + cq;
+        const T *some = static_cast<const T *>(a.x.p);
+        using Rows = typename Y::Rows;
+        using Quad = typename Y::Quad;
+        auto fetch = [&](int s) {
+            if (s < nt) {
+                uint8_t *slot = ring + s % Y::RING * Y::RAW, *slot_bc = ring_bc + s % Y::RING * Y::RAW_BC;
 #pragma unroll
-            for (int j = 0; j < Y::IN_TASKS; ++j) {
-                const int t = s * kTile + tq + j * (kServe / Y::NQ), n = t < len ? live - cq : 0;
-                fx[j].template load<VEC>(xp + (long)t * a.x.t + cq, n);
-                fd[j].template load<VEC>(dp + (long)t * a.dt.t + cq, n);
-            }
-            if (sub) return;
+                for (int j = 0; j < Y::TASKS; ++j, slot += 3 * Rows::SIZE) {
+                    const int t = s * kTile + tq + j * (kServe / Y::NQ), n = t < len ? live - cq : 0;
+                    Rows::template fetch<VEC>(slot, tid, xp + (long)t * a.x.t, n, some, w.pairs);
+                    Rows::template fetch<VEC>(slot + Rows::SIZE, tid, dp + (long)t * a.dt.t, n, some, w.pairs);
+                    if (!LOCAL && zp) Rows::template fetch<VEC>(slot + 2 * Rows::SIZE, tid, zp + (long)t * a.gate.t, n, some, w.pairs);
+                }
+                if (!sub) {
 #pragma unroll
-            for (int j = 0; j < Y::BC_TASKS; ++j) {      // token = lane; quad of states = the rest, B's then C's
-                const int k = warp + 4 * j, t = s * kTile + lane;
-                const bool isB = k < L;
-                if (LOCAL && !isB) continue;
-                fh[j].template load<VEC>(isB ? Bp + (long)t * a.B.t + 4 * k : Cp + (long)t * a.C.t + 4 * (k - L), t < len ? 4 : 0);
+                    for (int j = 0; j < Y::BC_TASKS; ++j) {      // token = lane; quad of states = the rest, B's then C's
+                        const int k = warp + 4 * j, t = s * kTile + lane;
+                        const bool isB = k < L;
+                        if (LOCAL && !isB) continue;
+                        Quad::template fetch<VEC>(slot_bc + j * Quad::SIZE, tid, isB ? Bp + (long)t * a.B.t + 4 * k : Cp + (long)t * a.C.t + 4 * (k - L),
+                                                  t < len ? 4 : 0, some, w.pairs);
+                    }
+                }
             }
+            copies_commit();
         };
-        // output: PC channels from co on, tokens 4 to .. 4 to + 3 (of the task's)
-        int co, to;
-        if (L <= 4) {
-            co = 2 * ((lane & 3) | (lane >> 3) << 2);
-            to = (lane >> 2 & 1) | warp << 1;
-        } else if (L == 8) {
-            co = lane & 15;
-            to = lane >> 4 | warp << 1;
-        } else {
-            co = lane & 7;
-            to = lane >> 3 | warp << 2;
-        }
-        const bool finishes = to < kTile / 4;
-        float skip[Y::OUT_TASKS][Y::PC];
-        Few<T, Y::PC> ox[2][Y::OUT_TASKS][4], oz[2][Y::OUT_TASKS][4];
 #pragma unroll
-        for (int j = 0; j < Y::OUT_TASKS; ++j)
-#pragma unroll
-            for (int i = 0; i < Y::PC; ++i) {
-                const int c = co + j * 32 + i;
-                skip[j][i] = a.skip && c < live ? a.skip[d0 + c] : 0.f;
-            }
-        // one step of the pipeline; P = s & 1 names the registers that tiles of this parity go through
-        auto step = [&](int s, auto parity) {
-            constexpr int P = decltype(parity)::value;
+        for (int s = 0; s < Y::AHEAD; ++s) fetch(s);
+        for (int s = 0; s <= last; ++s) {
             __syncthreads();
+            copies_wait<Y::AHEAD - 1>();
+            const int P = s & 1;
             if (s < nt) {
                 if (!sub) {             // B and C into the operand's rows (token, state, B or C), parts of L states side by side
+                    const uint8_t *slot = ring_bc + s % Y::RING * Y::RAW_BC;
 #pragma unroll
                     for (int j = 0; j < Y::BC_TASKS; ++j) {
                         const int k = warp + 4 * j, quad = k < L ? k : k - L;
                         if (LOCAL && k >= L) continue;
-                        const Few<T, 4> &f = rh[P][j];
+                        const Few<T, 4> f = Quad::read(slot + j * Quad::SIZE, tid);
                         const int r0 = (lane >> 2) * 4 * W + (k < L ? 0 : 4) + (lane & 3);
 #pragma unroll
                         for (int e = 0; e < 4; e += 2) {        // states 4 quad + e and the next: column i, K element l
@@ -341,75 +339,49 @@ __global__ void __launch_bounds__(GROUPS * 256, 1) ssm_scan_kernel(const __grid_
                     }
                 }
                 float *base = in + P * Y::IN;
+                const uint8_t *slot = ring + s % Y::RING * Y::RAW;
 #pragma unroll
-                for (int j = 0; j < Y::IN_TASKS; ++j) {
+                for (int j = 0; j < Y::TASKS; ++j) {
                     const int tt = tq + j * (kServe / Y::NQ);
                     const bool there = s * kTile + tt < len;        // behind the last token the memory stays: dt = 0
+                    const Few<T, Y::VC> x = Rows::read(slot + 3 * j * Rows::SIZE, tid), d = Rows::read(slot + (3 * j + 1) * Rows::SIZE, tid);
 #pragma unroll
                     for (int i = 0; i < Y::VC; ++i) {
-                        float v = rd[P][j][i] + bias[i];
+                        float v = d[i] + bias[i];
                         if (a.softplus) v = softplus<T>(v);
                         v = there ? v : 0.f;
                         float *to_row = base + Y::row(cq + i) + tt;
                         to_row[0] = v;
-                        to_row[Y::ROWS] = there ? v * rx[P][j][i] : 0.f;
+                        to_row[Y::ROWS] = there ? v * x[i] : 0.f;
                     }
                 }
-                if (s + 2 < nt) fetch(s + 2, rx[P], rd[P], rh[P]);
             }
-            if constexpr (!LOCAL) {
-                if (s >= 2 && finishes) {
-                    const float *base = out + P * Y::OUT;
+            if (!LOCAL && s >= 2) {
+                const float *base = out + P * Y::OUT;
+                const uint8_t *slot = ring + (s - 2) % Y::RING * Y::RAW;
 #pragma unroll
-                    for (int j = 0; j < Y::OUT_TASKS; ++j) {
-                        const int c = co + j * 32;
-                        Two y[Y::PC][2];
+                for (int j = 0; j < Y::TASKS; ++j) {
+                    const int tt = tq + j * (kServe / Y::NQ), t = (s - 2) * kTile + tt;
+                    const Few<T, Y::VC> x = Rows::read(slot + 3 * j * Rows::SIZE, tid);
+                    Few<T, Y::VC> z;
+                    if (zp) z = Rows::read(slot + (3 * j + 2) * Rows::SIZE, tid);
+                    float v[Y::VC];
 #pragma unroll
-                        for (int i = 0; i < Y::PC; ++i) {
-                            y[i][0] = y[i][1] = two(0.f, 0.f);
+                    for (int i = 0; i < Y::VC; ++i) {
+                        const float *part = base + Y::row(cq + i) + tt;
+                        v[i] = part[0];
 #pragma unroll
-                            for (int l = 0; l < L; ++l) {
-                                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(base + l * Y::PART + (c + i) * kPitch + 4 * to);
-                                y[i][0] = l ? add2(y[i][0], v.x) : v.x;
-                                y[i][1] = l ? add2(y[i][1], v.y) : v.y;
-                            }
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int t = (s - 2) * kTile + 4 * to + k;
-                            float v[Y::PC];
-#pragma unroll
-                            for (int i = 0; i < Y::PC; ++i) {
-                                float v0, v1;
-                                each(y[i][k / 2], v0, v1);
-                                v[i] = fmaf(skip[j][i], ox[P][j][k][i], k & 1 ? v1 : v0);
-                                if (a.gate.p) {
-                                    const float z = oz[P][j][k][i];
-                                    float rest;
-                                    v[i] *= z * sigmoid<T>(z, rest);
-                                }
-                            }
-                            Few<T, Y::PC>::template store<VEC>(yp + (long)t * a.y.t + c, v, t < len ? live - c : 0);
+                        for (int l = 1; l < L; ++l) v[i] += part[l * Y::PART];
+                        v[i] = fmaf(skip[i], x[i], v[i]);
+                        if (zp) {
+                            float rest;
+                            v[i] *= z[i] * sigmoid<T>(z[i], rest);
                         }
                     }
-                }
-                if (s < nt && finishes) {
-#pragma unroll
-                    for (int j = 0; j < Y::OUT_TASKS; ++j)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int t = s * kTile + 4 * to + k, c = co + j * 32, n = t < len ? live - c : 0;
-                            ox[P][j][k].template load<VEC>(xp + (long)t * a.x.t + c, n);
-                            if (a.gate.p) oz[P][j][k].template load<VEC>(zp + (long)t * a.gate.t + c, n);
-                        }
+                    Few<T, Y::VC>::template store<VEC>(yp + (long)t * a.y.t, v, t < len ? live - cq : 0);
                 }
             }
-        };
-        fetch(0, rx[0], rd[0], rh[0]);
-        if (nt > 1) fetch(1, rx[1], rd[1], rh[1]);
-        for (int s = 0; s <= last; s += 2) {
-            step(s, std::integral_constant<int, 0>());
-            if (s + 1 <= last) step(s + 1, std::integral_constant<int, 1>());
+            fetch(s + Y::AHEAD);
         }
     }
     tc_fence_before();
@@ -487,6 +459,8 @@ template <typename T, int L, bool VEC, bool LOCAL, int GROUPS> cudaError_t start
 template <typename T, int L, bool VEC> cudaError_t launch(const Ssm &a, cudaStream_t st) {
     using Y = Lay<T, L>;
     Walk w{};
+    w.pairs = a.D / a.G % 2 == 0 && few_view<T>(a.x, 2, false) && few_view<T>(a.dt, 2, false) && few_view<T>(a.gate, 2, false) &&
+              few_view<T>(a.B, 2, true) && few_view<T>(a.C, 2, true);
     w.a = a;
     w.hdr = static_cast<WsHeader *>(a.ws);
     w.cpg = a.D / a.G;
@@ -497,7 +471,7 @@ template <typename T, int L, bool VEC> cudaError_t launch(const Ssm &a, cudaStre
     if (!split) w.seg = std::max(max_len, 1);
     w.items = lin_items(a.s.nseq, a.s.cu ? a.total : a.s.T, max_len, a.s.cu != nullptr, w.seg);
     // two groups to a CTA where one would leave blocks waiting for an SM
-    constexpr bool two_groups = sizeof(T) == 2;      // fp32 groups' registers are more than half an SM's
+    constexpr bool two_groups = sizeof(T) == 2 && L > 2;      // what two groups hold has to fit
     const bool pair = two_groups && w.items * blocks_of<L>(a.D, a.G) > a.sms && w.cpg > Y::CH;
     w.bpg = (w.cpg + Y::CH * (1 + pair) - 1) / (Y::CH * (1 + pair));
     w.blocks = w.bpg * a.G;
