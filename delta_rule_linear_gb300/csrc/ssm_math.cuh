@@ -13,32 +13,6 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// softplus(z) = max(z, 0) + log1p(e), e = exp(-|z|) in [0, 1].  A time step of 1e-3 needs log1p's relative accuracy, which
-// the logarithm of 1 + e has lost: log1p(e) / e is a polynomial of degree 9 (fitted to its values on [0, 1] with the
-// largest relative error least, 5e-9; evaluated in fp32 1.6e-7).  The product |z| log2 e is rounded to fp32, 2^-24 |p|
-// ln 2 of e: a bf16 z does not carry that, for fp32 (T) it goes in to the first order.
-template <typename T>
-__device__ __forceinline__ float softplus(float z) {
-    constexpr float kLow = 1.925963033e-8f, kLn2 = 0.6931471805599453f;
-    const float m = fabsf(z), p = kLog2eF * m;
-    float e = ex2(-p);
-    if constexpr (sizeof(T) == 4) {
-        const float low = fmaf(kLow, m, fmaf(kLog2eF, m, -p));
-        e = p < 126.f ? fmaf(e, -kLn2 * low, e) : e;
-    }
-    float q = -0.0032440253999084234f;
-    q = fmaf(q, e, 0.01985146477818489f);
-    q = fmaf(q, e, -0.056959543377161026f);
-    q = fmaf(q, e, 0.10603656619787216f);
-    q = fmaf(q, e, -0.15305593609809875f);
-    q = fmaf(q, e, 0.1967594027519226f);
-    q = fmaf(q, e, -0.24954134225845337f);
-    q = fmaf(q, e, 0.3332996368408203f);
-    q = fmaf(q, e, -0.4999990165233612f);
-    q = fmaf(q, e, 1.f);
-    return fmaf(q, e, fmaxf(z, 0.f)) + (z != z ? z : 0.f);     // fmaxf drops a NaN
-}
-
 // Two fp32 in one register pair: the packed operations do both in one instruction.
 using Two = unsigned long long;
 __device__ __forceinline__ Two two(float a, float b) {
@@ -61,6 +35,37 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
     Two r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
+}
+
+// softplus(z) = max(z, 0) + log1p(e), e = exp(-|z|) in [0, 1], of two.  A time step of 1e-3 needs log1p's relative accuracy,
+// which the logarithm of 1 + e has lost: log1p(e) / e is a polynomial of degree 9 (fitted to its values on [0, 1] with the
+// largest relative error least, 5e-9; evaluated in fp32 1.6e-7).  The product |z| log2 e is rounded to fp32, 2^-24 |p|
+// ln 2 of e: a bf16 z does not carry that, for fp32 (T) it goes in to the first order.  A NaN comes through e.
+template <typename T>
+__device__ __forceinline__ float softplus_e(float z) {
+    constexpr float kLow = 1.925963033e-8f, kLn2 = 0.6931471805599453f;
+    const float m = fabsf(z), p = kLog2eF * m;
+    float e = ex2(-p);
+    if constexpr (sizeof(T) == 4) {
+        const float low = fmaf(kLow, m, fmaf(kLog2eF, m, -p));
+        e = p < 126.f ? fmaf(e, -kLn2 * low, e) : e;
+    }
+    return e;
+}
+template <typename T>
+__device__ __forceinline__ void softplus(float &z0, float &z1) {
+    constexpr float c[10] = {-0.0032440253999084234f, 0.01985146477818489f, -0.056959543377161026f, 0.10603656619787216f, -0.15305593609809875f, 0.1967594027519226f, -0.24954134225845337f, 0.3332996368408203f, -0.4999990165233612f, 1.f};
+    const Two e = two(softplus_e<T>(z0), softplus_e<T>(z1));
+    Two q = two(c[0], c[0]);
+#pragma unroll
+    for (int i = 1; i < 10; ++i) q = fma2(q, e, two(c[i], c[i]));
+    each(fma2(q, e, two(fmaxf(z0, 0.f), fmaxf(z1, 0.f))), z0, z1);
+}
+template <typename T>
+__device__ __forceinline__ float softplus(float z) {
+    float other = 0.f;
+    softplus<T>(z, other);
+    return z;
 }
 
 // N consecutive elements as words, unopened: one load where VEC (aligned to the smaller of 16 bytes and all of them), the

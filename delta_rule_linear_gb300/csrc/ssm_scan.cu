@@ -104,24 +104,29 @@ __device__ __forceinline__ uint64_t op_desc(uint32_t base, int rows, int slot) {
 
 // What a lane has asked of TMEM is there: nothing that uses it may come before.
 template <int N> __device__ __forceinline__ void landed(uint32_t (&r)[N]) {
-    tmem_ld_wait();
+    asm volatile("tcgen05.wait::ld.sync.aligned;");
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// Threads of a CTA.  A lone group has few warps to change between: other warps store the outputs than bring the inputs.
+constexpr int threads_of(bool local, int groups) { return !local && groups == 1 ? 384 : 256 * groups; }
+
 // VEC: rows and heads start on boundaries of what a lane loads, and groups hold whole loads.
 template <typename T, int L, bool VEC, bool LOCAL, int GROUPS>
-__global__ void __launch_bounds__(GROUPS * 256, 1) ssm_scan_kernel(const __grid_constant__ Walk w) {
+__global__ void __launch_bounds__(threads_of(LOCAL, GROUPS), 1) ssm_scan_kernel(const __grid_constant__ Walk w) {
     using Y = Lay<T, L>;
+    constexpr int THREADS = threads_of(LOCAL, GROUPS), GT = THREADS / GROUPS;
+    constexpr bool SPLIT = GT == 384;           // the serving of inputs and of outputs by four warps each
     constexpr int XR = Y::XROWS(LOCAL), W = LOCAL ? 4 : 8;      // columns of X: 4 W of every four tokens, W of a state
     constexpr uint32_t COLS = LOCAL ? 256 : 512;
     extern __shared__ __align__(1024) uint8_t raw[];
     __shared__ Ctl ctl;
     const Ssm &a = w.a;
     const long item = blockIdx.x / w.blocks;
-    const int cb = (int)(blockIdx.x - item * w.blocks), g = cb / w.bpg, sub = threadIdx.x / 256;
+    const int cb = (int)(blockIdx.x - item * w.blocks), g = cb / w.bpg, sub = threadIdx.x / GT;
     const int c0 = ((cb - g * w.bpg) * GROUPS + sub) * Y::CH;           // the group's first channel among its heads'
-    const bool role = (threadIdx.x & 255) < 128;                        // scan
+    const int role = threadIdx.x % GT / 128;                            // 0 scan, 1 serve, 2 serve the outputs
     const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid / 32;
     LinItem it;
     if (blockIdx.x == 0 && threadIdx.x == 0 && (LOCAL || !w.local)) w.hdr->error = 0;       // (no wait can run out this early)
@@ -141,7 +146,7 @@ __global__ void __launch_bounds__(GROUPS * 256, 1) ssm_scan_kernel(const __grid_
         ctl.fail = 0;
         fence_mbar_init();
     }
-    for (int i = threadIdx.x; i < Y::BLOCKS * XR * 8; i += GROUPS * 256) reinterpret_cast<uint4 *>(xs)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < Y::BLOCKS * XR * 8; i += THREADS) reinterpret_cast<uint4 *>(xs)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async();
     if (threadIdx.x >= 224 && threadIdx.x < 256) {
         tmem_alloc(&ctl.tmem, COLS);
@@ -166,7 +171,7 @@ __global__ void __launch_bounds__(GROUPS * 256, 1) ssm_scan_kernel(const __grid_
     const long b = a.s.cu ? 0 : it.n, row0 = (a.s.cu ? it.start : 0) + t0;
     const int last = nt + (LOCAL ? 0 : 1);
 
-    if (role) {         // ------------------------------------------------------------------------------------- scan
+    if (role == 0) {    // ------------------------------------------------------------------------------------- scan
         const int c = tid / L, l = tid % L;
         const int d = min(d0 + min(c, max(live - 1, 0)), a.D - 1);
         const long at = ((long)it.n * a.D + d) * Y::N + l;
@@ -201,35 +206,52 @@ __global__ void __launch_bounds__(GROUPS * 256, 1) ssm_scan_kernel(const __grid_
             const float *dtp = in + (k & 1) * Y::IN + Y::row(c), *dxp = dtp + Y::ROWS;
             float *op = out + (k & 1) * Y::OUT + l * Y::PART + Y::row(c);
             const uint32_t from = mine + (k & 1) * XR;
+            // the factors of the next four tokens are formed beside the memories of these
+            uint32_t bc[2][4 * W];
+            float f[2][4][4];
+            Two dx[2][2];
+            auto ask = [&](int t4) {
+                if constexpr (LOCAL)
+                    tmem_ld16(from + t4 * 16, bc[t4 & 1]);
+                else
+                    tmem_ld32(from + t4 * 32, bc[t4 & 1]);
+            };
+            auto factors = [&](int t4) {
+                const ulonglong2 dt = *reinterpret_cast<const ulonglong2 *>(dtp + 4 * t4), u = *reinterpret_cast<const ulonglong2 *>(dxp + 4 * t4);
+                if (LOCAL) sum = add2(sum, add2(dt.x, dt.y));
+                dx[t4 & 1][0] = u.x;
+                dx[t4 & 1][1] = u.y;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float(&e)[4] = f[t4 & 1][i];
+                    each(mul2(dt.x, A[i]), e[0], e[1]);
+                    each(mul2(dt.y, A[i]), e[2], e[3]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) e[k] = ex2(e[k]);
+                }
+            };
+            factors(0);
             wt.warp(&ctl.full[k & 1], (k >> 1) & 1, 1);
             tc_fence_after();
-            uint32_t bc[2][4 * W];
-            auto ask = [&](int t4, uint32_t (&r)[4 * W]) {
-                if constexpr (LOCAL)
-                    tmem_ld16(from + t4 * 16, r);
-                else
-                    tmem_ld32(from + t4 * 32, r);
-            };
-            ask(0, bc[0]);
+            ask(0);
 #pragma unroll
             for (int t4 = 0; t4 < kTile / 4; ++t4) {
-                const ulonglong2 dt = *reinterpret_cast<const ulonglong2 *>(dtp + 4 * t4), dx = *reinterpret_cast<const ulonglong2 *>(dxp + 4 * t4);
                 uint32_t(&r)[4 * W] = bc[t4 & 1];
                 landed(r);
-                if (t4 + 1 < kTile / 4) ask(t4 + 1, bc[(t4 + 1) & 1]);
+                if (t4 + 1 < kTile / 4) {
+                    ask(t4 + 1);
+                    factors(t4 + 1);
+                }
                 auto col = [&](int k0) { return two(__uint_as_float(r[k0]), __uint_as_float(r[k0 + 1])); };
-                if (LOCAL) sum = add2(sum, add2(dt.x, dt.y));
                 ulonglong2 y = make_ulonglong2(0, 0);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const Two p0 = mul2(dt.x, A[i]), p1 = mul2(dt.y, A[i]), u0 = mul2(dx.x, col(W * i)), u1 = mul2(dx.y, col(W * i + 2));
-                    float e0, e1, e2, e3, v0, v1, v2, v3;
-                    each(p0, e0, e1);
-                    each(p1, e2, e3);
-                    each(u0, v0, v1);
-                    each(u1, v2, v3);
-                    const float h0 = fmaf(ex2(e0), h[i], v0), h1 = fmaf(ex2(e1), h0, v1), h2 = fmaf(ex2(e2), h1, v2);
-                    h[i] = fmaf(ex2(e3), h2, v3);
+                    const float(&e)[4] = f[t4 & 1][i];
+                    float v0, v1, v2, v3;
+                    each(mul2(dx[t4 & 1][0], col(W * i)), v0, v1);
+                    each(mul2(dx[t4 & 1][1], col(W * i + 2)), v2, v3);
+                    const float h0 = fmaf(e[0], h[i], v0), h1 = fmaf(e[1], h0, v1), h2 = fmaf(e[2], h1, v2);
+                    h[i] = fmaf(e[3], h2, v3);
                     if constexpr (!LOCAL) {
                         y.x = i ? fma2(two(h0, h1), col(W * i + 4), y.x) : mul2(two(h0, h1), col(W * i + 4));
                         y.y = i ? fma2(two(h2, h[i]), col(W * i + 6), y.y) : mul2(two(h2, h[i]), col(W * i + 6));
@@ -273,11 +295,13 @@ __global__ void __launch_bounds__(GROUPS * 256, 1) ssm_scan_kernel(const __grid_
 #pragma unroll
                 for (int j = 0; j < Y::TASKS; ++j, slot += 3 * Rows::SIZE) {
                     const int t = s * kTile + tq + j * (kServe / Y::NQ), n = t < len ? live - cq : 0;
-                    Rows::template fetch<VEC>(slot, tid, xp + (long)t * a.x.t, n, some, w.pairs);
-                    Rows::template fetch<VEC>(slot + Rows::SIZE, tid, dp + (long)t * a.dt.t, n, some, w.pairs);
-                    if (!LOCAL && zp) Rows::template fetch<VEC>(slot + 2 * Rows::SIZE, tid, zp + (long)t * a.gate.t, n, some, w.pairs);
+                    if (!SPLIT || role == 1) {
+                        Rows::template fetch<VEC>(slot, tid, xp + (long)t * a.x.t, n, some, w.pairs);
+                        Rows::template fetch<VEC>(slot + Rows::SIZE, tid, dp + (long)t * a.dt.t, n, some, w.pairs);
+                    }
+                    if (!LOCAL && zp && (!SPLIT || role == 2)) Rows::template fetch<VEC>(slot + 2 * Rows::SIZE, tid, zp + (long)t * a.gate.t, n, some, w.pairs);
                 }
-                if (!sub) {
+                if (!sub && role == 1) {
 #pragma unroll
                     for (int j = 0; j < Y::BC_TASKS; ++j) {      // token = lane; quad of states = the rest, B's then C's
                         const int k = warp + 4 * j, t = s * kTile + lane;
@@ -296,7 +320,7 @@ __global__ void __launch_bounds__(GROUPS * 256, 1) ssm_scan_kernel(const __grid_
             __syncthreads();
             copies_wait<Y::AHEAD - 1>();
             const int P = s & 1;
-            if (s < nt) {
+            if (s < nt && (!SPLIT || role == 1)) {
                 if (!sub) {             // B and C into the operand's rows (token, state, B or C), parts of L states side by side
                     const uint8_t *slot = ring_bc + s % Y::RING * Y::RAW_BC;
 #pragma unroll
@@ -346,17 +370,19 @@ __global__ void __launch_bounds__(GROUPS * 256, 1) ssm_scan_kernel(const __grid_
                     const bool there = s * kTile + tt < len;        // behind the last token the memory stays: dt = 0
                     const Few<T, Y::VC> x = Rows::read(slot + 3 * j * Rows::SIZE, tid), d = Rows::read(slot + (3 * j + 1) * Rows::SIZE, tid);
 #pragma unroll
-                    for (int i = 0; i < Y::VC; ++i) {
-                        float v = d[i] + bias[i];
-                        if (a.softplus) v = softplus<T>(v);
-                        v = there ? v : 0.f;
-                        float *to_row = base + Y::row(cq + i) + tt;
-                        to_row[0] = v;
-                        to_row[Y::ROWS] = there ? v * x[i] : 0.f;
+                    for (int i = 0; i < Y::VC; i += 2) {
+                        float v[2] = {d[i] + bias[i], d[i + 1] + bias[i + 1]};
+                        if (a.softplus) softplus<T>(v[0], v[1]);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float *to_row = base + Y::row(cq + i + k) + tt;
+                            to_row[0] = there ? v[k] : 0.f;
+                            to_row[Y::ROWS] = there ? v[k] * x[i + k] : 0.f;
+                        }
                     }
                 }
             }
-            if (!LOCAL && s >= 2) {
+            if (!LOCAL && s >= 2 && (!SPLIT || role == 2)) {
                 const float *base = out + P * Y::OUT;
                 const uint8_t *slot = ring + (s - 2) % Y::RING * Y::RAW;
 #pragma unroll
@@ -447,12 +473,13 @@ template <int L> int blocks_of(int D, int G) { return (D / G + 128 / L - 1) / (1
 template <typename T, int L, bool VEC, bool LOCAL, int GROUPS> cudaError_t start(const Walk &w, long ctas, bool after, cudaStream_t st) {
     static lin::SmemOnce once;
     constexpr size_t bytes = Lay<T, L>::bytes(GROUPS, LOCAL);
+    constexpr int threads = threads_of(LOCAL, GROUPS);
     static_assert(bytes <= 232448 - 64, "shared memory");
     const auto kernel = ssm_scan_kernel<T, L, VEC, LOCAL, GROUPS>;
     const cudaError_t e = once(kernel, (int)bytes);
     if (e != cudaSuccess) return e;
-    if (after) return launch_after(kernel, dim3((unsigned)ctas), GROUPS * 256, bytes, st, w);
-    kernel<<<(unsigned)ctas, GROUPS * 256, bytes, st>>>(w);
+    if (after) return launch_after(kernel, dim3((unsigned)ctas), threads, bytes, st, w);
+    kernel<<<(unsigned)ctas, threads, bytes, st>>>(w);
     return cudaGetLastError();
 }
 
