@@ -6,6 +6,20 @@
 //     s_t = g_t . B_t,   e_t = a_t g_t h_{t-1}
 //     dx_t = dt_t s_t + skip p_t,   ddt_t = (x_t s_t + sum_n e_t A) softplus'(dt_t),   dz_t = dy_t r_t silu'(z_t)
 //     dA = sum_t e_t dt_t,   dskip = sum p_t x_t,   dbias = sum ddt_t,   dh0 = a_1 g_1
+//
+// Chunks of 32 tokens are independent once the memory before a chunk and the gradient behind it are known, so:
+//   1. every chunk by itself, forwards: the memory it leaves from an empty one, what its outputs send to the memory before
+//      it, sum_t (a_1 .. a_t) C_t p_t, and the sum of its dt (its decay is exp(A sum dt));
+//   2. the two chains over the chunks, one thread per (sequence, channel, state) and direction;
+//   3. every chunk again: forwards from its memory, then backwards; dB and dC of up to 128 channels go out as partial sums;
+//   4. the partial sums, in a fixed order.
+// Per (token, channel, state) that is three exp2 and some 20 fp32 operations, in packed pairs of states, and the sums over
+// states and channels; arithmetic and issue bound it, at four times what HBM would take.
+//
+// A warp holds 64 / L channels (L = N / 4): a lane two channels and four states, so that sums over states meet over L lanes and
+// sums over channels over 32 / L, in shuffles that halve the values at every step (a lane ends with one token's sums, or
+// one state's).  Memories of a chunk do not fit in registers: every fourth is kept in shared memory, and four tokens at
+// a time are walked again from it.
 #include <algorithm>
 
 #include "ssm_internal.cuh"
@@ -14,167 +28,592 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kTile = 32;                   // tokens of a chunk
+constexpr float kLn2F = 0.6931471805599453f;
 
-template <typename T> __device__ __forceinline__ float at(const SsmView &v, long b, long t, long e) {
-    return to_f32(static_cast<const T *>(v.p)[b * v.b + t * v.t + e]);
+template <int L> struct Lay {
+    static constexpr int N = 4 * L, CL = 32 / L, CW = 2 * CL, CH = kWarps * CW;      // states; channel lanes, channels of a warp, of a CTA
+    // floats: B and C of the chunk; per warp dt, u, p (each twice, for both channels of a lane), kept memories, dB and dC
+    static constexpr int HEADS = 2 * kTile * N, ROWS = kTile * CL * 12, KEPT = kTile / 4 * 256, SUMS = kTile * 2 * N;
+    static constexpr size_t bytes(bool local) { return (size_t)(HEADS + kWarps * (ROWS + (local ? 0 : KEPT + SUMS))) * 4; }
+};
+
+struct Bwd {
+    Ssm a;
+    int cpg, bpg, blocks;       // channels and CTAs of a group of heads, CTAs of all
+    long chunks;                // (a bound for packed sequences)
+    int slots;                  // CTAs that share a block of channels
+    long rows;
+    int pairs;                  // arrays can be read and written by two channels at a time
+    float *h, *g, *sums;        // [chunks, D, N] twice, [chunks, D]
+    float *bc;                  // [bpg, rows, G, 2 N]
+    float *pA, *pd;             // [slots, D, N], [slots, 2, D]
+};
+
+__device__ __forceinline__ bool chunk_item(const Bwd &w, long item, LinItem &it) {
+    if (!lin_item(w.a.s, kTile, (int)item, it)) return false;
+    if (w.a.s.cu) {
+        it.start = min(max(it.start, 0L), w.a.total);
+        it.len = (int)min((long)max(it.len, 0), w.a.total - it.start);
+    }
+    return true;
 }
-template <typename T> __device__ __forceinline__ void put(const SsmView &v, long b, long t, long e, float x) {
-    static_cast<T *>(v.p)[b * v.b + t * v.t + e] = from_f32<T>(x);
+
+// Sums over GRP lanes (STRIDE apart) of CNT values each: a step sends one half and keeps the other, so that a lane ends with
+// the sums of CNT / GRP values (of one, if there are fewer than lanes: neighbours have the same), from index first() on.
+template <int CNT, int GRP, int STRIDE> struct Meet {
+    static constexpr int LEFT = CNT > GRP ? CNT / GRP : 1;
+    static __device__ __forceinline__ void sum(float (&v)[CNT]) {
+        const int lane = threadIdx.x & 31;
+        int n = CNT;
+#pragma unroll
+        for (int off = GRP / 2; off; off >>= 1) {
+            if (n > 1) {
+                n /= 2;
+                const bool up = lane & (off * STRIDE);
+#pragma unroll
+                for (int i = 0; i < CNT / 2; ++i) {
+                    if (i >= n) break;
+                    const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off * STRIDE);
+                }
+            } else {
+                v[0] += __shfl_xor_sync(0xffffffffu, v[0], off * STRIDE);
+            }
+        }
+    }
+    static constexpr int SAME = CNT < GRP ? GRP / CNT : 1;
+    static __device__ __forceinline__ int first(int i) { return i / SAME * LEFT; }
+    static __device__ __forceinline__ bool lead(int i) { return i % SAME == 0; }      // of the neighbours
+};
+
+// Two channels' elements at p (n of them are there).
+template <typename T> __device__ __forceinline__ void get2(const T *p, int n, bool pairs, float &x, float &y) {
+    x = y = 0.f;
+    if (pairs) {
+        if (n <= 0) return;
+        if constexpr (sizeof(T) == 4) {
+            const float2 v = *reinterpret_cast<const float2 *>(p);
+            x = v.x, y = v.y;
+        } else {
+            const uint32_t v = *reinterpret_cast<const uint32_t *>(p);
+            x = __uint_as_float(v << 16), y = __uint_as_float(v & 0xffff0000u);
+        }
+    } else {
+        if (n > 0) x = to_f32(p[0]);
+        if (n > 1) y = to_f32(p[1]);
+    }
+}
+template <typename T> __device__ __forceinline__ void put2(T *p, int n, bool pairs, float x, float y) {
+    if (pairs) {
+        if (n <= 0) return;
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float2 *>(p) = make_float2(x, y);
+        } else {
+            *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
+        }
+    } else {
+        if (n > 0) p[0] = from_f32<T>(x);
+        if (n > 1) p[1] = from_f32<T>(y);
+    }
+}
+
+// Where a chunk lies in the arrays.
+struct At {
+    long b, row;        // batch entry, its first token
+    int len;            // tokens of the chunk
+};
+template <typename T> __device__ __forceinline__ T *rows_at(const SsmView &v, const At &at, int t, long e) {
+    return static_cast<T *>(v.p) + at.b * v.b + (at.row + t) * v.t + e;
+}
+
+// What both walks read: B and C (all warps together), and the warp's dt, u, p.
+template <typename T, int L>
+__device__ __forceinline__ void bring(const Bwd &w, const At &at, int g, int d0, int live, float *heads, float *rows) {
+    using Y = Lay<L>;
+    const Ssm &a = w.a;
+    const int lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < 2 * kTile * L; i += kThreads) {       // four states of a token
+        const int q = i % L, t = i / L % kTile;
+        const bool isB = i < kTile * L;
+        const SsmView &v = isB ? a.B : a.C;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < at.len) {
+            const T *p = rows_at<const T>(v, at, t, (long)g * v.g + 4 * q);
+            get2<T>(p, 2, w.pairs, x.x, x.y);
+            get2<T>(p + 2, 2, w.pairs, x.z, x.w);
+        }
+        reinterpret_cast<float4 *>(heads)[(isB ? 0 : kTile * L) + t * L + q] = x;
+    }
+    const int cp = lane % Y::CL, n = live - 2 * cp;
+    const long d = d0 + 2 * cp;
+    float bias[2] = {0.f, 0.f};
+    if (a.bias) {
+        if (n > 0) bias[0] = a.bias[d];
+        if (n > 1) bias[1] = a.bias[d + 1];
+    }
+#pragma unroll 4
+    for (int t = lane / Y::CL; t < kTile; t += L) {
+        const int m = t < at.len ? n : 0;
+        float dt[2], x[2], p[2];
+        get2<T>(rows_at<const T>(a.dt, at, t, d), m, w.pairs, dt[0], dt[1]);
+        get2<T>(rows_at<const T>(a.x, at, t, d), m, w.pairs, x[0], x[1]);
+        get2<T>(rows_at<const T>(a.y, at, t, d), m, w.pairs, p[0], p[1]);
+        dt[0] += bias[0];
+        dt[1] += bias[1];
+        if (a.softplus) softplus<T>(dt[0], dt[1]);
+        if (a.gate.p) {
+            float z[2], rest;
+            get2<T>(rows_at<const T>(a.gate, at, t, d), m, w.pairs, z[0], z[1]);
+            p[0] *= z[0] * sigmoid<T>(z[0], rest);
+            p[1] *= z[1] * sigmoid<T>(z[1], rest);
+        }
+        // behind the last token, and in channels that are not there, nothing happens: dt = u = p = 0
+        const bool a0 = m > 0, a1 = m > 1;
+        dt[0] = a0 ? dt[0] : 0.f, dt[1] = a1 ? dt[1] : 0.f;
+        x[0] = a0 ? dt[0] * x[0] : 0.f, x[1] = a1 ? dt[1] * x[1] : 0.f;
+        p[0] = a0 ? p[0] : 0.f, p[1] = a1 ? p[1] : 0.f;
+        float4 *to = reinterpret_cast<float4 *>(rows) + (t * Y::CL + cp) * 3;
+        to[0] = make_float4(dt[0], dt[0], dt[1], dt[1]);
+        to[1] = make_float4(x[0], x[0], x[1], x[1]);
+        to[2] = make_float4(p[0], p[0], p[1], p[1]);
+    }
+}
+
+__device__ __forceinline__ Two pair_at(const float *p) { return *reinterpret_cast<const Two *>(p); }
+__device__ __forceinline__ Two ex2_2(Two x) {
+    float a, b;
+    each(x, a, b);
+    return two(ex2(a), ex2(b));
+}
+__device__ __forceinline__ float both(Two x) {
+    float a, b;
+    each(x, a, b);
+    return a + b;
+}
+
+// CTA = one chunk, kWarps warps' channels.
+template <typename T, int L>
+__global__ void __launch_bounds__(kThreads, 4) ssm_bwd_local_kernel(const __grid_constant__ Bwd w) {
+    using Y = Lay<L>;
+    extern __shared__ __align__(16) float smem[];
+    const Ssm &a = w.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, l = lane % L, cl = lane / L;
+    const long item = blockIdx.x / w.blocks;
+    const int cb = (int)(blockIdx.x - item * w.blocks), g = cb / w.bpg, c0 = (cb - g * w.bpg) * Y::CH + warp * Y::CW;
+    LinItem it;
+    if (!chunk_item(w, item, it)) return;
+    const int t0 = min(it.p * kTile, it.len);
+    const At at{a.s.cu ? 0L : it.n, (a.s.cu ? it.start : 0L) + t0, min(kTile, it.len - t0)};
+    const int d0 = g * w.cpg + c0, live = w.cpg - c0;
+    float *rows = smem + Y::HEADS + warp * Y::ROWS;
+    bring<T, L>(w, at, g, d0, live, smem, rows);
+    __syncthreads();
+    Two A[2][2], h[2][2], P[2][2], G[2][2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const long d = min(d0 + 2 * cl + c, a.D - 1);
+        const float4 x = *reinterpret_cast<const float4 *>(a.A + d * Y::N + 4 * l);
+        A[c][0] = two(x.x * kLog2eF, x.y * kLog2eF);
+        A[c][1] = two(x.z * kLog2eF, x.w * kLog2eF);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            h[c][k] = G[c][k] = two(0.f, 0.f);
+            P[c][k] = two(1.f, 1.f);
+        }
+    }
+    float sum[2] = {0.f, 0.f};
+#pragma unroll 4
+    for (int t = 0; t < kTile; ++t) {
+        const float *Bp = smem + t * Y::N + 4 * l, *Cp = Bp + kTile * Y::N, *rp = rows + (t * Y::CL + cl) * 12;
+        const Two B[2] = {pair_at(Bp), pair_at(Bp + 2)}, C[2] = {pair_at(Cp), pair_at(Cp + 2)};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const Two dt = pair_at(rp + 2 * c), u = pair_at(rp + 4 + 2 * c), p = pair_at(rp + 8 + 2 * c);
+            sum[c] += rp[2 * c];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const Two f = ex2_2(mul2(dt, A[c][k]));
+                h[c][k] = fma2(f, h[c][k], mul2(u, B[k]));
+                P[c][k] = mul2(P[c][k], f);
+                G[c][k] = fma2(P[c][k], mul2(p, C[k]), G[c][k]);
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        if (2 * cl + c >= live) continue;
+        const long d = d0 + 2 * cl + c, to = (item * a.D + d) * Y::N + 4 * l;
+        *reinterpret_cast<ulonglong2 *>(w.h + to) = make_ulonglong2(h[c][0], h[c][1]);
+        *reinterpret_cast<ulonglong2 *>(w.g + to) = make_ulonglong2(G[c][0], G[c][1]);
+        if (l == 0) w.sums[item * a.D + d] = sum[c];
+    }
+}
+
+// One thread per (sequence, channel, state) and direction (blockIdx.y): what a chunk left by itself becomes the memory before
+// it, or the gradient behind it.
+template <int N> __global__ void __launch_bounds__(256) ssm_bwd_chain_kernel(const __grid_constant__ Bwd w, int seq_blocks) {
+    const Ssm &a = w.a;
+    const int n = blockIdx.x / seq_blocks;
+    const long e = (long)(blockIdx.x - n * seq_blocks) * 256 + threadIdx.x, DN = (long)a.D * N;
+    // the sequence's chunks
+    long first;
+    int cnt;
+    if (a.s.cu) {
+        __shared__ long s_first;
+        __shared__ int s_cnt;
+        if (threadIdx.x < 32) {
+            long before = 0;
+            int mine = 0;
+            for (int k = threadIdx.x; k <= n; k += 32) {
+                const int len = a.s.cu[k + 1] - a.s.cu[k], c = len > kTile ? (len + kTile - 1) / kTile : 1;
+                if (k < n) before += c;
+                else mine = c;
+            }
+#pragma unroll
+            for (int off = 16; off; off >>= 1) {
+                before += __shfl_xor_sync(0xffffffffu, before, off);
+                mine += __shfl_xor_sync(0xffffffffu, mine, off);
+            }
+            if (threadIdx.x == 0) s_first = before, s_cnt = mine;
+        }
+        __syncthreads();
+        first = s_first;
+        cnt = s_cnt;
+        if (first >= w.chunks) return;
+        cnt = (int)min((long)cnt, w.chunks - first);
+    } else {
+        cnt = a.s.T > kTile ? (a.s.T + kTile - 1) / kTile : 1;
+        first = (long)n * cnt;
+    }
+    if (e >= DN) return;
+    const bool back = blockIdx.y;
+    const float A = a.A[e] * kLog2eF;
+    const long d = e / N;
+    const float *start = back ? a.dhT : a.h0;
+    float v = start ? start[n * DN + e] : 0.f;
+    float *arr = (back ? w.g : w.h) + e;
+    constexpr int U = 8;
+    for (int i0 = 0; i0 < cnt; i0 += U) {
+        float x[U], s[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = min(i0 + u, cnt - 1);
+            const long k = first + (back ? cnt - 1 - i : i);
+            x[u] = arr[k * DN];
+            s[u] = w.sums[k * a.D + d];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i0 + u >= cnt) break;
+            const long k = first + (back ? cnt - 1 - (i0 + u) : i0 + u);
+            arr[k * DN] = v;
+            v = fmaf(ex2(s[u] * A), v, x[u]);
+        }
+    }
+    if (back && a.dh0) a.dh0[n * DN + e] = v;
 }
 
 template <typename T, int L>
-__global__ void __launch_bounds__(kThreads) ssm_bwd_walk_kernel(Ssm a, int cpg, int bpg, long rows, float *kept, float *part,
-                                                                float *pA, float *pd) {
-    const int CH = kThreads / L, N = 4 * L;
-    const int g = blockIdx.x / bpg, cb = blockIdx.x - g * bpg, cg = cb * CH + threadIdx.x / L, l = threadIdx.x % L;
-    const bool live = cg < cpg;
-    const int d = g * cpg + (live ? cg : 0), n = blockIdx.y;
-    long start = 0, len = a.s.T, b = n, row0 = (long)n * a.s.T;
-    if (a.s.cu) {
-        start = min(max((long)a.s.cu[n], 0L), a.total);
-        len = min(max((long)a.s.cu[n + 1] - a.s.cu[n], 0L), a.total - start);
-        b = 0;
-        row0 = 0;
+__global__ void __launch_bounds__(kThreads, 2) ssm_bwd_grad_kernel(const __grid_constant__ Bwd w) {
+    using Y = Lay<L>;
+    extern __shared__ __align__(16) float smem[];
+    const Ssm &a = w.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, l = lane % L, cl = lane / L;
+    const int slot = blockIdx.x / w.blocks, cb = blockIdx.x - slot * w.blocks, g = cb / w.bpg, cg = cb - g * w.bpg;
+    const int c0 = cg * Y::CH + warp * Y::CW, d0 = g * w.cpg + c0, live = w.cpg - c0;
+    float *rows = smem + Y::HEADS + warp * (Y::ROWS + Y::KEPT + Y::SUMS), *kept = rows + Y::ROWS, *sums = kept + Y::KEPT;
+    Two A[2][2], dA[2][2];
+    float skip[2], bias[2], dskip[2] = {0.f, 0.f}, dbias[2] = {0.f, 0.f};
+    const int n = live - 2 * cl;            // of the lane's two channels those that are there
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const long d = min(d0 + 2 * cl + c, a.D - 1);
+        const float4 x = *reinterpret_cast<const float4 *>(a.A + d * Y::N + 4 * l);
+        A[c][0] = two(x.x * kLog2eF, x.y * kLog2eF);
+        A[c][1] = two(x.z * kLog2eF, x.w * kLog2eF);
+        dA[c][0] = dA[c][1] = two(0.f, 0.f);
+        skip[c] = a.skip && c < n ? a.skip[d] : 0.f;
+        bias[c] = a.bias && c < n ? a.bias[d] : 0.f;
     }
-    float A[4], A2[4], h[4], G[4], dA[4];
-    for (int i = 0; i < 4; ++i) {
-        A[i] = a.A[(long)d * N + l + L * i];
-        A2[i] = A[i] * kLog2eF;
-        dA[i] = 0.f;
-        h[i] = a.h0 ? a.h0[((long)n * a.D + d) * N + l + L * i] : 0.f;
-        G[i] = a.dhT ? a.dhT[((long)n * a.D + d) * N + l + L * i] : 0.f;
-    }
-    const float bias = a.bias ? a.bias[d] : 0.f, skip = a.skip ? a.skip[d] : 0.f;
-    auto step = [&](long t, float &raw) {
-        raw = at<T>(a.dt, b, t, d) + bias;
-        return a.softplus ? softplus<T>(raw) : raw;
-    };
-    auto keep = [&](long t, int i) -> float & { return kept[((row0 + t) * a.D + d) * N + l + L * i]; };
-    for (long t = start; t < start + len; ++t) {
-        float raw;
-        const float dt = step(t, raw), u = dt * at<T>(a.x, b, t, d);
-        for (int i = 0; i < 4; ++i) {
-            if (live) keep(t, i) = h[i];
-            h[i] = fmaf(ex2(dt * A2[i]), h[i], u * at<T>(a.B, b, t, g * a.B.g + l + L * i));
+    for (long item = slot; item < w.chunks; item += w.slots) {
+        LinItem it;
+        if (!chunk_item(w, item, it)) break;
+        const int t0 = min(it.p * kTile, it.len);
+        const At at{a.s.cu ? 0L : it.n, (a.s.cu ? it.start : 0L) + t0, min(kTile, it.len - t0)};
+        if (at.len == 0) continue;
+        __syncthreads();        // the chunk before has been read
+        bring<T, L>(w, at, g, d0, live, smem, rows);
+        Two h[2][2], G[2][2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const long from = (item * a.D + min(d0 + 2 * cl + c, a.D - 1)) * Y::N + 4 * l;
+            ulonglong2 x = make_ulonglong2(0, 0), y = x;
+            if (c < n) x = *reinterpret_cast<const ulonglong2 *>(w.h + from), y = *reinterpret_cast<const ulonglong2 *>(w.g + from);
+            h[c][0] = x.x, h[c][1] = x.y;
+            G[c][0] = y.x, G[c][1] = y.y;
+        }
+        __syncthreads();
+        auto heads = [&](int t, Two (&B)[2]) {
+            const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(smem + t * Y::N + 4 * l);
+            B[0] = x.x, B[1] = x.y;
+        };
+        auto row = [&](int t, int k) { return *reinterpret_cast<const ulonglong2 *>(rows + ((t * Y::CL + cl) * 3 + k) * 4); };
+        // forwards, every fourth memory kept
+        for (int q = 0; q < kTile / 4; ++q) {
+            ulonglong2 *to = reinterpret_cast<ulonglong2 *>(kept) + q * 64 + lane;
+            to[0] = make_ulonglong2(h[0][0], h[0][1]);
+            to[32] = make_ulonglong2(h[1][0], h[1][1]);
+            if (q + 1 == kTile / 4) break;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int t = 4 * q + k;
+                Two B[2];
+                heads(t, B);
+                const ulonglong2 dt = row(t, 0), u = row(t, 1);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    h[0][s] = fma2(ex2_2(mul2(dt.x, A[0][s])), h[0][s], mul2(u.x, B[s]));
+                    h[1][s] = fma2(ex2_2(mul2(dt.y, A[1][s])), h[1][s], mul2(u.y, B[s]));
+                }
+            }
+        }
+        // backwards, four tokens at a time
+#pragma unroll 1
+        for (int q = kTile / 4 - 1; q >= 0; --q) {
+            if (4 * q >= at.len) continue;          // nothing happens there
+            Two was[5][2][2], f[4][2][2];
+            {
+                const ulonglong2 *from = reinterpret_cast<const ulonglong2 *>(kept) + q * 64 + lane;
+                const ulonglong2 x = from[0], y = from[32];
+                was[0][0][0] = x.x, was[0][0][1] = x.y, was[0][1][0] = y.x, was[0][1][1] = y.y;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int t = 4 * q + k;
+                Two B[2];
+                heads(t, B);
+                const ulonglong2 dt = row(t, 0), u = row(t, 1);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    f[k][0][s] = ex2_2(mul2(dt.x, A[0][s]));
+                    f[k][1][s] = ex2_2(mul2(dt.y, A[1][s]));
+                    was[k + 1][0][s] = fma2(f[k][0][s], was[k][0][s], mul2(u.x, B[s]));
+                    was[k + 1][1][s] = fma2(f[k][1][s], was[k][1][s], mul2(u.y, B[s]));
+                }
+            }
+            float r[8], sB[8], sA[8];       // token, channel
+#pragma unroll
+            for (int k = 3; k >= 0; --k) {
+                const int t = 4 * q + k;
+                Two B[2], C[2];
+                heads(t, B);
+                heads(t + kTile, C);
+                const ulonglong2 dt2 = row(t, 0), u2 = row(t, 1), p2 = row(t, 2);
+                const Two dt[2] = {dt2.x, dt2.y}, u[2] = {u2.x, u2.y}, p[2] = {p2.x, p2.y};
+                Two dB[2], dC[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    Two rr, ss, sa;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const Two now = was[k + 1][c][s];
+                        rr = s ? fma2(now, C[s], rr) : mul2(now, C[s]);
+                        dC[s] = c ? fma2(now, p[c], dC[s]) : mul2(now, p[c]);
+                        G[c][s] = fma2(C[s], p[c], G[c][s]);
+                        dB[s] = c ? fma2(G[c][s], u[c], dB[s]) : mul2(G[c][s], u[c]);
+                        ss = s ? fma2(G[c][s], B[s], ss) : mul2(G[c][s], B[s]);
+                        G[c][s] = mul2(G[c][s], f[k][c][s]);
+                        const Two e = mul2(G[c][s], was[k][c][s]);
+                        sa = s ? fma2(e, A[c][s], sa) : mul2(e, A[c][s]);
+                        dA[c][s] = fma2(e, dt[c], dA[c][s]);
+                    }
+                    r[2 * k + c] = both(rr);
+                    sB[2 * k + c] = both(ss);
+                    sA[2 * k + c] = both(sa);
+                }
+                float v[8];
+                each(dB[0], v[0], v[1]);
+                each(dB[1], v[2], v[3]);
+                each(dC[0], v[4], v[5]);
+                each(dC[1], v[6], v[7]);
+                using M = Meet<8, Y::CL, L>;
+                M::sum(v);
+                if (M::lead(cl)) {          // value j: B or C (j / 4), state 4 l + j % 4
+#pragma unroll
+                    for (int i = 0; i < M::LEFT; ++i) {
+                        const int j = M::first(cl) + i;
+                        sums[t * 2 * Y::N + (j >> 2) * Y::N + 4 * l + (j & 3)] = v[i];
+                    }
+                }
+            }
+            using M = Meet<8, L, 1>;
+            M::sum(r);
+            M::sum(sB);
+            M::sum(sA);
+            // the lane's tokens: two channels of one or two of them, or one channel
+            if (M::lead(l)) {
+                constexpr int CNT = M::LEFT;
+#pragma unroll
+                for (int i = 0; i < CNT; i += 2) {
+                    const int j = M::first(l) + i, t = 4 * q + (j >> 1), c1 = CNT == 1 ? (j & 1) : 0;
+                    const long d = d0 + 2 * cl + c1;
+                    const int m = t < at.len ? (CNT == 1 ? min(n - c1, 1) : n) : 0;
+                    const bool two_at_once = CNT > 1 && w.pairs;
+                    float x[2], raw[2], dy[2], z[2], dx[2], ddt[2], dz[2];
+                    get2<T>(rows_at<const T>(a.x, at, t, d), m, two_at_once, x[0], x[1]);
+                    get2<T>(rows_at<const T>(a.dt, at, t, d), m, two_at_once, raw[0], raw[1]);
+                    if (a.gate.p) {
+                        get2<T>(rows_at<const T>(a.y, at, t, d), m, two_at_once, dy[0], dy[1]);
+                        get2<T>(rows_at<const T>(a.gate, at, t, d), m, two_at_once, z[0], z[1]);
+                    }
+#pragma unroll
+                    for (int c = 0; c < (CNT > 1 ? 2 : 1); ++c) {
+                        const int ch = CNT == 1 ? c1 : c;
+                        const float sk = ch ? skip[1] : skip[0], bi = ch ? bias[1] : bias[0];
+                        const float *rp = rows + (t * Y::CL + cl) * 12 + 2 * ch;
+                        const float dt = rp[0], p = rp[8];
+                        float rest = 0.f, slope = 1.f;
+                        if (a.softplus) slope = sigmoid<T>(raw[c] + bi, rest);
+                        dx[c] = fmaf(dt, sB[i + c], sk * p);
+                        ddt[c] = fmaf(x[c], sB[i + c], kLn2F * sA[i + c]) * slope;
+                        if (a.gate.p) {
+                            const float sg = sigmoid<T>(z[c], rest), rr = fmaf(sk, x[c], r[i + c]);
+                            dz[c] = dy[c] * rr * fmaf(z[c] * sg, rest, sg);
+                        }
+                        if (c < m) {
+                            if (ch) {
+                                dskip[1] = fmaf(p, x[c], dskip[1]);
+                                dbias[1] += ddt[c];
+                            } else {
+                                dskip[0] = fmaf(p, x[c], dskip[0]);
+                                dbias[0] += ddt[c];
+                            }
+                        }
+                    }
+                    put2<T>(rows_at<T>(a.dx, at, t, d), m, two_at_once, dx[0], dx[1]);
+                    put2<T>(rows_at<T>(a.ddt, at, t, d), m, two_at_once, ddt[0], ddt[1]);
+                    if (a.gate.p) put2<T>(rows_at<T>(a.dgate, at, t, d), m, two_at_once, dz[0], dz[1]);
+                }
+            }
+        }
+        __syncthreads();
+        const long row0 = a.s.cu ? at.row : at.b * a.s.T + at.row;
+        for (int i = threadIdx.x; i < at.len * 2 * Y::N; i += kThreads) {
+            const float *from = smem + Y::HEADS + Y::ROWS + Y::KEPT + i;
+            constexpr int step = Y::ROWS + Y::KEPT + Y::SUMS;
+            const float v = (from[0] + from[step]) + (from[2 * step] + from[3 * step]);
+            const int t = i / (2 * Y::N), k = i % (2 * Y::N);
+            w.bc[(((long)cg * w.rows + row0 + t) * a.G + g) * 2 * Y::N + k] = v;
         }
     }
-    float dskip = 0.f, dbias = 0.f;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = bpg * (kThreads / 32);
-    for (long t = start + len - 1; t >= start; --t) {
-        float raw;
-        const float dt = step(t, raw), x = at<T>(a.x, b, t, d), u = dt * x, dy = live ? at<T>(a.y, b, t, d) : 0.f;
-        float p = dy, z = 0.f, sg = 1.f, rest = 0.f;
-        if (a.gate.p) {
-            z = at<T>(a.gate, b, t, d);
-            sg = sigmoid<T>(z, rest);
-            p *= z * sg;
+    // the lanes' sums over tokens
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int off = 1; off < L; off <<= 1) {
+            dskip[c] += __shfl_xor_sync(0xffffffffu, dskip[c], off);
+            dbias[c] += __shfl_xor_sync(0xffffffffu, dbias[c], off);
         }
-        float r = 0.f, s = 0.f, sA = 0.f, bc[8];
-        for (int i = 0; i < 4; ++i) {
-            const float Bn = at<T>(a.B, b, t, g * a.B.g + l + L * i), Cn = at<T>(a.C, b, t, g * a.C.g + l + L * i);
-            const float was = live ? keep(t, i) : 0.f, al = ex2(dt * A2[i]), now = fmaf(al, was, u * Bn);
-            r = fmaf(now, Cn, r);
-            G[i] = fmaf(Cn, p, G[i]);
-            bc[i] = live ? u * G[i] : 0.f;
-            bc[4 + i] = live ? p * now : 0.f;
-            s = fmaf(G[i], Bn, s);
-            G[i] *= al;
-            const float e = G[i] * was;
-            sA = fmaf(e, A[i], sA);
-            dA[i] = fmaf(e, dt, dA[i]);
+        if (c >= n) continue;
+        const long d = d0 + 2 * cl + c;
+        *reinterpret_cast<ulonglong2 *>(w.pA + ((long)slot * a.D + d) * Y::N + 4 * l) = make_ulonglong2(dA[c][0], dA[c][1]);
+        if (l == 0) {
+            w.pd[(long)slot * 2 * a.D + d] = dskip[c];
+            w.pd[((long)slot * 2 + 1) * a.D + d] = dbias[c];
         }
-        for (int off = L / 2; off; off >>= 1) {
-            r += __shfl_xor_sync(0xffffffffu, r, off);
-            s += __shfl_xor_sync(0xffffffffu, s, off);
-            sA += __shfl_xor_sync(0xffffffffu, sA, off);
-        }
-        r = fmaf(skip, x, r);
-        float ddt = fmaf(x, s, sA), other;
-        if (a.softplus) ddt *= sigmoid<T>(raw, other);
-        dskip = fmaf(p, x, dskip);
-        dbias += ddt;
-        if (live && l == 0) {
-            put<T>(a.dx, b, t, d, fmaf(dt, s, skip * p));
-            put<T>(a.ddt, b, t, d, ddt);
-            if (a.gate.p) put<T>(a.dgate, b, t, d, dy * r * fmaf(z * sg, rest, sg));
-        }
-        for (int k = 0; k < 8; ++k)
-            for (int off = 16; off >= L; off >>= 1) bc[k] += __shfl_xor_sync(0xffffffffu, bc[k], off);
-        if (lane < L)
-            for (int k = 0; k < 8; ++k)
-                part[(((long)(cb * (kThreads / 32) + warp) * rows + row0 + t) * a.G + g) * 2 * N + (k / 4) * N + l + L * (k % 4)] = bc[k];
-    }
-    (void)warps;
-    if (!live) return;
-    for (int i = 0; i < 4; ++i) {
-        if (a.dh0) a.dh0[((long)n * a.D + d) * N + l + L * i] = G[i];
-        pA[((long)n * a.D + d) * N + l + L * i] = dA[i];
-    }
-    if (l == 0) {
-        pd[((long)n * 2) * a.D + d] = dskip;
-        pd[((long)n * 2 + 1) * a.D + d] = dbias;
     }
 }
 
-// dB, dC of row blockIdx.x from the warps' parts; the last blocks: dA, dskip, dbias from the sequences'
+// dB and dC from the blocks' sums (a thread per value of a token), and the parameters' gradients from the slots'.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) ssm_fold_bc_kernel(Ssm a, long rows, int warps, const float *part) {
-    const long row = blockIdx.x;
-    const int n2 = a.G * 2 * a.N;
-    if (a.s.cu && (row < a.s.cu[0] || row >= a.s.cu[a.s.nseq])) return;
-    for (int e = threadIdx.x; e < n2; e += kThreads) {
+__global__ void __launch_bounds__(256) ssm_bwd_fold_kernel(const __grid_constant__ Bwd w, long bc_blocks) {
+    const Ssm &a = w.a;
+    if (blockIdx.x < bc_blocks) {
+        const long id = (long)blockIdx.x * 256 + threadIdx.x, n2 = (long)a.G * 2 * a.N, all = w.rows * n2;
+        if (id >= all) return;
+        const long row = id / n2;
+        const int e = (int)(id - row * n2);
+        if (a.s.cu && (row < a.s.cu[0] || row >= a.s.cu[a.s.nseq])) return;
         float v = 0.f;
-        for (int w = 0; w < warps; ++w) v += part[((long)w * rows + row) * n2 + e];
+        for (int k = 0; k < w.bpg; ++k) v += w.bc[k * all + id];
         const int g = e / (2 * a.N), k = e % (2 * a.N);
-        const long b = a.s.cu ? 0 : row / a.s.T, t = a.s.cu ? row : row % a.s.T;
+        const long b = a.s.cu ? 0 : row / a.s.T, t = a.s.cu ? row : row - b * a.s.T;
         const SsmView &o = k < a.N ? a.dB : a.dC;
         static_cast<T *>(o.p)[b * o.b + t * o.t + g * o.g + k % a.N] = from_f32<T>(v);
+        return;
     }
-}
-__global__ void __launch_bounds__(kThreads) ssm_fold_par_kernel(Ssm a, const float *pA, const float *pd) {
-    const long id = blockIdx.x * (long)kThreads + threadIdx.x, nA = (long)a.D * a.N;
+    const long id = (blockIdx.x - bc_blocks) * 256 + threadIdx.x, nA = (long)a.D * a.N;
+    if (id >= nA + 2 * a.D) return;
+    const float *from = id < nA ? w.pA + id : w.pd + (id - nA);
+    const long step = id < nA ? nA : 2L * a.D;
     float v = 0.f;
-    if (id < nA) {
-        for (int n = 0; n < a.s.nseq; ++n) v += pA[n * nA + id];
+    for (int s = 0; s < w.slots; ++s) v += from[s * step];
+    if (id < nA)
         a.dA[id] = v;
-    } else if (id < nA + 2 * a.D) {
-        const long k = id - nA;
-        for (int n = 0; n < a.s.nseq; ++n) v += pd[(long)n * 2 * a.D + k];
-        if (k < a.D) {
-            if (a.dskip) a.dskip[k] = v;
-        } else if (a.dbias) {
-            a.dbias[k - a.D] = v;
-        }
+    else if (id < nA + a.D) {
+        if (a.dskip) a.dskip[id - nA] = v;
+    } else if (a.dbias) {
+        a.dbias[id - nA - a.D] = v;
     }
 }
 
+// Sizes and places of the scratch.
 struct Plan {
-    long rows;
-    int cpg, bpg, warps;
-    size_t kept, part, pA, pd;
+    long rows, chunks;
+    int cpg, bpg, blocks, slots;
+    size_t mem, sums, bc, pA, pd;
 };
-Plan plan(int nseq, long rows, int D, int G, int N) {
+Plan plan(int nseq, long total, int max_len, bool varlen, int D, int G, int N, int sms) {
     Plan p{};
-    const int L = N / 4, CH = kThreads / L;
-    p.rows = rows;
+    const int CH = kWarps * 64 / (N / 4);
+    p.rows = varlen ? total : (long)nseq * max_len;
+    p.chunks = lin_items(nseq, total, max_len, varlen, kTile);
     p.cpg = D / G;
     p.bpg = (p.cpg + CH - 1) / CH;
-    p.warps = p.bpg * (kThreads / 32);
-    p.kept = (size_t)rows * D * N;
-    p.part = (size_t)p.warps * rows * G * 2 * N;
-    p.pA = (size_t)nseq * D * N;
-    p.pd = (size_t)nseq * 2 * D;
+    p.blocks = p.bpg * G;
+    // four rounds of two CTAs per SM: ends meet, and the parameters' partial sums stay few
+    p.slots = (int)std::max(1L, std::min(p.chunks, (8L * sms + p.blocks - 1) / p.blocks));
+    p.mem = (size_t)p.chunks * D * N;
+    p.sums = ((size_t)p.chunks * D + 3) / 4 * 4;
+    p.bc = (size_t)p.bpg * p.rows * G * 2 * N;
+    p.pA = (size_t)p.slots * D * N;
+    p.pd = (size_t)p.slots * 2 * D;
     return p;
 }
 
+template <typename T> bool even(const SsmView &v, bool heads) {
+    return !v.p || (reinterpret_cast<uintptr_t>(v.p) % (2 * sizeof(T)) == 0 && v.b % 2 == 0 && v.t % 2 == 0 && (!heads || v.g % 2 == 0));
+}
+
 template <typename T, int L> cudaError_t run(const Ssm &a, cudaStream_t st) {
-    const long rows = a.s.cu ? a.total : (long)a.s.nseq * a.s.T;
-    const Plan p = plan(a.s.nseq, rows, a.D, a.G, a.N);
-    float *kept = static_cast<float *>(a.ws), *part = kept + p.kept, *pA = part + p.part, *pd = pA + p.pA;
-    ssm_bwd_walk_kernel<T, L><<<dim3(p.bpg * a.G, a.s.nseq), kThreads, 0, st>>>(a, p.cpg, p.bpg, rows, kept, part, pA, pd);
-    if (rows > 0) ssm_fold_bc_kernel<T><<<(unsigned)rows, kThreads, 0, st>>>(a, rows, p.warps, part);
-    ssm_fold_par_kernel<<<(unsigned)(((long)a.D * (a.N + 2) + kThreads - 1) / kThreads), kThreads, 0, st>>>(a, pA, pd);
+    using Y = Lay<L>;
+    const bool varlen = a.s.cu != nullptr;
+    const Plan p = plan(a.s.nseq, a.total, varlen ? (int)a.total : a.s.T, varlen, a.D, a.G, a.N, a.sms);
+    Bwd w{};
+    w.a = a;
+    w.cpg = p.cpg, w.bpg = p.bpg, w.blocks = p.blocks, w.chunks = p.chunks, w.slots = p.slots, w.rows = p.rows;
+    w.pairs = p.cpg % 2 == 0 && even<T>(a.x, false) && even<T>(a.dt, false) && even<T>(a.gate, false) && even<T>(a.y, false) &&
+              even<T>(a.B, true) && even<T>(a.C, true) && even<T>(a.dx, false) && even<T>(a.ddt, false) && even<T>(a.dgate, false);
+    w.h = reinterpret_cast<float *>(static_cast<char *>(a.ws) + sizeof(WsHeader));
+    w.g = w.h + p.mem;
+    w.pA = w.g + p.mem;
+    w.bc = w.pA + p.pA;
+    w.sums = w.bc + p.bc;
+    w.pd = w.sums + p.sums;
+    const long ctas = p.chunks * p.blocks;
+    const int seq_blocks = (int)(((long)a.D * a.N + 255) / 256);
+    if (ctas > 0x7fffffffL || (long)a.s.nseq * seq_blocks > 0x7fffffffL) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(ssm_bwd_local_kernel<T, L>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Y::bytes(true));
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(ssm_bwd_grad_kernel<T, L>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Y::bytes(false));
+    if (e != cudaSuccess) return e;
+    ssm_bwd_local_kernel<T, L><<<(unsigned)ctas, kThreads, Y::bytes(true), st>>>(w);
+    ssm_bwd_chain_kernel<4 * L><<<dim3((unsigned)(a.s.nseq * seq_blocks), 2), 256, 0, st>>>(w, seq_blocks);
+    ssm_bwd_grad_kernel<T, L><<<(unsigned)(p.slots * p.blocks), kThreads, Y::bytes(false), st>>>(w);
+    const long bc_blocks = (p.rows * a.G * 2 * a.N + 255) / 256, par_blocks = ((long)a.D * (a.N + 2) + 255) / 256;
+    ssm_bwd_fold_kernel<T><<<(unsigned)(bc_blocks + par_blocks), 256, 0, st>>>(w, bc_blocks);
     return cudaGetLastError();
 }
 template <typename T> cudaError_t go(const Ssm &a, cudaStream_t st) {
@@ -183,9 +622,9 @@ template <typename T> cudaError_t go(const Ssm &a, cudaStream_t st) {
 
 }  // namespace
 
-size_t ssm_bwd_scratch_bytes(int nseq, long total, int max_len, bool varlen, int D, int G, int N, int) {
-    const Plan p = plan(nseq, varlen ? total : (long)nseq * max_len, D, G, N);
-    return 4 * (p.kept + p.part + p.pA + p.pd);
+size_t ssm_bwd_scratch_bytes(int nseq, long total, int max_len, bool varlen, int D, int G, int N, int sms) {
+    const Plan p = plan(nseq, total, max_len, varlen, D, G, N, sms);
+    return 4 * (2 * p.mem + p.sums + p.bc + p.pA + p.pd);
 }
 cudaError_t launch_ssm_bwd(const Ssm &a, cudaStream_t st) {
     return a.dtype == DType::BF16 ? go<__nv_bfloat16>(a, st) : go<float>(a, st);

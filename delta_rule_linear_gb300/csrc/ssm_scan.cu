@@ -206,50 +206,48 @@ __global__ void __launch_bounds__(threads_of(LOCAL, GROUPS), 1) ssm_scan_kernel(
             const float *dtp = in + (k & 1) * Y::IN + Y::row(c), *dxp = dtp + Y::ROWS;
             float *op = out + (k & 1) * Y::OUT + l * Y::PART + Y::row(c);
             const uint32_t from = mine + (k & 1) * XR;
-            // the factors of the next four tokens are formed beside the memories of these
+            // The factors of the next four tokens are formed beside the memories of these, state by state: four exp2 hold their
+            // unit for 16 cycles, as long as the chain of four multiply-adds takes.
             uint32_t bc[2][4 * W];
             float f[2][4][4];
-            Two dx[2][2];
             auto ask = [&](int t4) {
                 if constexpr (LOCAL)
                     tmem_ld16(from + t4 * 16, bc[t4 & 1]);
                 else
                     tmem_ld32(from + t4 * 32, bc[t4 & 1]);
             };
-            auto factors = [&](int t4) {
-                const ulonglong2 dt = *reinterpret_cast<const ulonglong2 *>(dtp + 4 * t4), u = *reinterpret_cast<const ulonglong2 *>(dxp + 4 * t4);
-                if (LOCAL) sum = add2(sum, add2(dt.x, dt.y));
-                dx[t4 & 1][0] = u.x;
-                dx[t4 & 1][1] = u.y;
+            auto factors = [&](const ulonglong2 &dt, int i, float (&e)[4]) {
+                each(mul2(dt.x, A[i]), e[0], e[1]);
+                each(mul2(dt.y, A[i]), e[2], e[3]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float(&e)[4] = f[t4 & 1][i];
-                    each(mul2(dt.x, A[i]), e[0], e[1]);
-                    each(mul2(dt.y, A[i]), e[2], e[3]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) e[k] = ex2(e[k]);
-                }
+                for (int k = 0; k < 4; ++k) e[k] = ex2(e[k]);
             };
-            factors(0);
+            ulonglong2 dt = *reinterpret_cast<const ulonglong2 *>(dtp), dx = *reinterpret_cast<const ulonglong2 *>(dxp), dx_next = dx;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) factors(dt, i, f[0][i]);
             wt.warp(&ctl.full[k & 1], (k >> 1) & 1, 1);
             tc_fence_after();
             ask(0);
 #pragma unroll
             for (int t4 = 0; t4 < kTile / 4; ++t4) {
+                const bool more = t4 + 1 < kTile / 4;
+                if (LOCAL) sum = add2(sum, add2(dt.x, dt.y));
+                if (more) {
+                    dt = *reinterpret_cast<const ulonglong2 *>(dtp + 4 * t4 + 4);
+                    dx_next = *reinterpret_cast<const ulonglong2 *>(dxp + 4 * t4 + 4);
+                }
                 uint32_t(&r)[4 * W] = bc[t4 & 1];
                 landed(r);
-                if (t4 + 1 < kTile / 4) {
-                    ask(t4 + 1);
-                    factors(t4 + 1);
-                }
+                if (more) ask(t4 + 1);
                 auto col = [&](int k0) { return two(__uint_as_float(r[k0]), __uint_as_float(r[k0 + 1])); };
                 ulonglong2 y = make_ulonglong2(0, 0);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float(&e)[4] = f[t4 & 1][i];
                     float v0, v1, v2, v3;
-                    each(mul2(dx[t4 & 1][0], col(W * i)), v0, v1);
-                    each(mul2(dx[t4 & 1][1], col(W * i + 2)), v2, v3);
+                    each(mul2(dx.x, col(W * i)), v0, v1);
+                    each(mul2(dx.y, col(W * i + 2)), v2, v3);
+                    if (more) factors(dt, i, f[(t4 + 1) & 1][i]);
                     const float h0 = fmaf(e[0], h[i], v0), h1 = fmaf(e[1], h0, v1), h2 = fmaf(e[2], h1, v2);
                     h[i] = fmaf(e[3], h2, v3);
                     if constexpr (!LOCAL) {
@@ -258,6 +256,7 @@ __global__ void __launch_bounds__(threads_of(LOCAL, GROUPS), 1) ssm_scan_kernel(
                     }
                 }
                 if (!LOCAL) *reinterpret_cast<ulonglong2 *>(op + 4 * t4) = y;
+                dx = dx_next;
             }
         }
         if (c < live) {
