@@ -5,8 +5,8 @@
 // and adds up exp(x - M) against the running maximum M of its chunks.  An element among the k best lies in one of the k
 // chunks that come first when chunks are ordered by (maximum, position): every chunk before its own holds an element that
 // comes before it.  So the second kernel, a CTA per request, orders the chunks' maxima and looks at k chunks only.
-// Totals are formed and compared in 64 bits (candidates of different beams may be closer than an fp32 total's rounding);
-// sums of exp are fp32 over a lane's few hundred terms and 64-bit from there on.
+// Totals are formed and compared as pairs of fp32, 48 bits (candidates of different beams may be closer than an fp32 total's
+// rounding); sums of exp are fp32 over a warp's terms and 64-bit from there on.
 //
 // Reordering in place: a thread holds one 16-byte column of all W beams of a request, reads what the moved beams take
 // and then writes it, so no beam is overwritten before it has been read and nothing is copied aside.
@@ -141,73 +141,121 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(BeamSelect a) {
     }
 }
 
+// A total as the sum of two fp32 (48 bits), which orders it by whole numbers; fp64 is 64 times slower here.
+__device__ __forceinline__ unsigned ordered(float x) {
+    const unsigned u = __float_as_uint(x + 0.f);        // -0 is 0
+    return u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(unsigned u) { return __uint_as_float(u >> 31 ? u ^ 0x80000000u : ~u); }
+struct Off {                // score - lse; hi = -inf: the beam's candidates are all -inf
+    float hi, lo;
+};
+__device__ __forceinline__ unsigned long long key_of(float hi, float lo) { return (unsigned long long)ordered(hi) << 32 | ordered(lo); }
+__device__ __forceinline__ unsigned long long key_of(const Off &o, float x) {
+    const float s = o.hi + x;
+    if (!(fabsf(s) < INFINITY)) return key_of(s != s ? -INFINITY : s, 0.f);
+    const float b = s - o.hi, e = ((o.hi - (s - b)) + (x - b)) + o.lo, hi = s + e;      // s + the sum's error, exactly
+    return key_of(hi, (s - hi) + e);
+}
+
+// log of a sum of exp (1 <= s < 2^40), 2^-44: s = 2^n f, log f = 2 artanh((f - 1) / (f + 1)) by its series, |r| < 0.172.
+__device__ __forceinline__ double log_sum(double s) {
+    int n = (int)((unsigned long long)__double_as_longlong(s) >> 52) - 1023;
+    double f = __longlong_as_double((__double_as_longlong(s) & 0xfffffffffffffll) | 0x3ff0000000000000ll);
+    if (f > 1.4142135623730951) {
+        f *= 0.5;
+        ++n;
+    }
+    const double d = f + 1.0;
+    double q = 1.0f / (float)d;
+    q = q * (2.0 - d * q);
+    q = q * (2.0 - d * q);
+    const double r = (f - 1.0) * q, r2 = r * r;
+    double p = 1.0 / 15;
+    p = p * r2 + 1.0 / 13;
+    p = p * r2 + 1.0 / 11;
+    p = p * r2 + 1.0 / 9;
+    p = p * r2 + 1.0 / 7;
+    p = p * r2 + 1.0 / 5;
+    p = p * r2 + 1.0 / 3;
+    p = p * r2 + 1.0;
+    return 2.0 * r * p + n * 0.69314718055994530942;
+}
+
 // A candidate's place in the order: larger totals first, then lower indices.
 struct Cand {
-    unsigned long long key;     // of the total: larger is larger
+    unsigned long long key;     // of the total: larger is larger (0: none)
     unsigned at;                // w V + v, or a chunk's number
 };
 __device__ __forceinline__ bool before(const Cand &a, const Cand &b) { return a.key > b.key || (a.key == b.key && a.at < b.at); }
-__device__ __forceinline__ unsigned long long key_of(double x) {
-    const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);    // -0 is 0
-    return u >> 63 ? ~u : u | 0x8000000000000000ull;
-}
-__device__ __forceinline__ double total_of(unsigned long long key) {
-    return __longlong_as_double((long long)(key >> 63 ? key & 0x7fffffffffffffffull : ~key));
+__device__ __forceinline__ Cand shuffled(const Cand &c, int from) {
+    return {__shfl_sync(0xffffffffu, c.key, from), __shfl_sync(0xffffffffu, c.at, from)};
 }
 
-// The best of what a warp has seen, in order over its lanes.
+// The best 32 of what a warp has seen, in order over its lanes.
 struct WarpList {
     Cand c;
-    __device__ __forceinline__ void clear() { c = {0, 0xffffffffu}; }
+    // lane pairs `stride` apart: the better one to the lower lane (up: to the upper)
+    __device__ __forceinline__ void trade(int stride, bool up) {
+        const Cand y = shuffled(c, (threadIdx.x & 31) ^ stride);
+        const bool lower = !(threadIdx.x & stride);
+        if (before(y, c) == (lower != up)) c = y;
+    }
+    // a first batch, one candidate of each lane
+    __device__ __forceinline__ void start(Cand x) {
+        c = x;
+#pragma unroll
+        for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+            for (int stride = size / 2; stride; stride /= 2) trade(stride, size < 32 && (threadIdx.x & size));
+    }
     // lanes with `some` bring a candidate each; k: how many are wanted
     __device__ __forceinline__ void take(bool some, Cand x, int k) {
         const int lane = threadIdx.x & 31;
         for (;;) {
-            Cand worst;
-            worst.key = __shfl_sync(0xffffffffu, c.key, k - 1);
-            worst.at = __shfl_sync(0xffffffffu, c.at, k - 1);
+            const Cand worst = shuffled(c, k - 1);      // by the whole warp, whatever its lanes bring
             some = some && before(x, worst);
             const unsigned who = __ballot_sync(0xffffffffu, some);
             if (!who) return;
             const int src = __ffs(who) - 1;
-            Cand y;
-            y.key = __shfl_sync(0xffffffffu, x.key, src);
-            y.at = __shfl_sync(0xffffffffu, x.at, src);
+            const Cand y = shuffled(x, src);
             if (lane == src) some = false;
             const int pos = __popc(__ballot_sync(0xffffffffu, before(c, y)));     // the list is in order
-            const unsigned long long uk = __shfl_up_sync(0xffffffffu, c.key, 1);
-            const unsigned ua = __shfl_up_sync(0xffffffffu, c.at, 1);
+            const Cand up = shuffled(c, lane ? lane - 1 : 0);
             if (lane == pos) c = y;
-            if (lane > pos) c = {uk, ua};
+            if (lane > pos) c = up;
         }
     }
 };
 
-// The k first of all warps' lists, in order, at out[0 .. k): every entry counts those before it.
-__device__ __forceinline__ void join(WarpList &l, Cand *all, Cand *out, int k) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, n = kPickWarps * k;
-    __syncthreads();
-    if (lane < k) all[warp * k + lane] = l.c;
-    __syncthreads();
-    if ((int)threadIdx.x < n) {
-        const Cand x = all[threadIdx.x];
-        int rank = 0;
-        for (int i = 0; i < n; ++i) rank += i != (int)threadIdx.x && (before(all[i], x) || (!before(x, all[i]) && i < (int)threadIdx.x));
-        if (rank < k) out[rank] = x;
+// The best 32 of all warps' lists, in order, in warp 0's (two lists, one of them turned round, hold their best 32 in the
+// better of each place, and five trades put those in order).
+__device__ __forceinline__ void join(WarpList &l, Cand *other) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+#pragma unroll 1
+    for (int half = kPickWarps / 2; half; half /= 2) {
+        __syncthreads();
+        if (warp >= half && warp < 2 * half) other[(warp - half) * 32 + lane] = l.c;
+        __syncthreads();
+        if (warp < half) {
+            const Cand y = other[warp * 32 + 31 - lane];
+            if (before(y, l.c)) l.c = y;
+#pragma unroll
+            for (int stride = 16; stride; stride /= 2) l.trade(stride, false);
+        }
     }
-    __syncthreads();
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(BeamSelect a) {
-    __shared__ double off[kBeamsIn];        // score - lse; -inf: the beam's candidates are all -inf
-    __shared__ Cand all[kPickWarps * kBeamMax], top[kBeamMax];
+    __shared__ Off off[kBeamsIn];
+    __shared__ Cand other[kPickWarps / 2 * 32], top[kBeamMax];
     const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x / 32, k = a.k;
     wait_for_previous();
     for (int w = warp; w < a.W; w += kPickWarps) {
         const long row = (long)b * a.W + w;
-        const double score = a.scores[row];
-        double o = score;
+        const float score = a.scores[row];
+        Off o{score, 0.f};
         if (!(a.finished && a.finished[row])) {
             const BeamSum *s = a.sums + row * a.splits;
             float m = -INFINITY;
@@ -216,69 +264,72 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(BeamSelect a) {
             for (int q = 16; q; q >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, q));
             double sum = 0.0;
             for (int i = lane; i < a.splits; i += 32)      // a part of -inf alone has a sum of 0
-                sum += s[i].max == m || s[i].max == -INFINITY ? s[i].sum : s[i].sum * exp((double)s[i].max - (double)m);
+                sum += s[i].max == m || s[i].max == -INFINITY ? s[i].sum : s[i].sum * (double)exp2f((s[i].max - m) * 1.4426950408889634f);
 #pragma unroll
             for (int q = 16; q; q >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, q);
-            o = score - ((double)m + log(sum));
-            if (!(m > -INFINITY && m < INFINITY && sum < INFINITY)) o = -INFINITY;       // no distribution
+            o.hi = -INFINITY;
+            if (m > -INFINITY && m < INFINITY && sum < INFINITY && score > -INFINITY && score < INFINITY) {
+                const double t = (double)score - ((double)m + log_sum(sum));
+                o.hi = (float)t;
+                o.lo = (float)(t - (double)o.hi);
+            }
         }
-        if (!(o == o)) o = -INFINITY;
+        if (!(o.hi == o.hi)) o.hi = -INFINITY;
         if (lane == 0) off[w] = o;
     }
     __syncthreads();
-    auto dead = [&](double o) { return o == -INFINITY; };
+    const unsigned long long none = key_of(-INFINITY, 0.f);
     auto done = [&](int w) { return a.finished && a.finished[(long)b * a.W + w]; };
     // the k first chunks
     WarpList l;
-    l.clear();
     const int nall = a.W * a.nc;
-    for (int i0 = warp * 32; i0 < nall; i0 += kPickThreads) {
+    for (int i0 = warp * 32; i0 < nall || i0 == warp * 32; i0 += kPickThreads) {
         const int i = i0 + lane;
-        const bool some = i < nall;
-        Cand x{0, (unsigned)i};
-        if (some) {
+        Cand x{0, 0xffffffffu};
+        if (i < nall) {
             const int w = i / a.nc, j = i - w * a.nc;
-            double t = -INFINITY;
+            x.at = i;
+            x.key = none;
             if (done(w))
-                t = a.eos / kBeamChunk == j ? off[w] : t;
-            else if (!dead(off[w]))
-                t = off[w] + (double)a.cmax[((long)b * a.W + w) * a.nc + j];
-            x.key = key_of(t);
+                x.key = a.eos / kBeamChunk == j ? key_of(off[w].hi, off[w].lo) : none;
+            else if (off[w].hi > -INFINITY)
+                x.key = key_of(off[w], a.cmax[((long)b * a.W + w) * a.nc + j]);
         }
-        l.take(some, x, k);
+        if (i0 == warp * 32)
+            l.start(x);
+        else
+            l.take(x.key != 0, x, k);
     }
-    join(l, all, top, k);
-    // their elements: those that reach the k-th chunk's maximum are looked at in 64 bits
-    const unsigned long long least = top[k - 1].at == 0xffffffffu ? 0 : top[k - 1].key;
-    const double reach = total_of(least ? least : key_of(-INFINITY));
-    l.clear();
+    join(l, other);
+    if (threadIdx.x < k) top[threadIdx.x] = l.c;
+    __syncthreads();
+    // their elements, those that reach the k-th chunk's maximum
+    const unsigned long long least = top[k - 1].key;
+    l.c = {0, 0xffffffffu};
     constexpr int parts = kBeamChunk / 32;
+#pragma unroll 4
     for (int i = warp; i < k * parts; i += kPickWarps) {
         const unsigned chunk = top[i / parts].at;
         if (chunk == 0xffffffffu) break;         // fewer chunks than k
         const int w = chunk / a.nc, j = chunk - w * a.nc;
-        const T *p = row_of<T>(a, b, w);
-        const long e = (long)j * kBeamChunk + (i % parts) * 32 + lane;
-        bool some = e < a.V;
-        Cand x{0, (unsigned)(w * (long)a.V + e)};
-        if (some) {
-            double t = -INFINITY;
+        const int e = j * kBeamChunk + (i % parts) * 32 + lane;
+        Cand x{0, 0xffffffffu};
+        if (e < a.V) {
+            x.at = (unsigned)(w * (long)a.V + e);
+            x.key = none;
             if (done(w))
-                t = e == a.eos ? off[w] : t;
-            else if (!dead(off[w]))
-                t = off[w] + (double)to_f32(p[e]);
-            x.key = key_of(t);
-            some = t >= reach;
+                x.key = e == a.eos ? key_of(off[w].hi, off[w].lo) : none;
+            else if (off[w].hi > -INFINITY)
+                x.key = key_of(off[w], to_f32(row_of<T>(a, b, w)[e]));
         }
-        l.take(some, x, k);
+        l.take(x.key != 0 && x.key >= least, x, k);
     }
-    join(l, all, top, k);
+    join(l, other);
     if (threadIdx.x < k) {
-        const Cand x = top[threadIdx.x];
         const long o = (long)b * k + threadIdx.x;
-        a.out[o] = (float)total_of(x.key);
-        a.parents[o] = (int)(x.at / (unsigned)a.V);
-        a.tokens[o] = (int)(x.at % (unsigned)a.V);
+        a.out[o] = unordered((unsigned)(l.c.key >> 32));
+        a.parents[o] = (int)(l.c.at / (unsigned)a.V);
+        a.tokens[o] = (int)(l.c.at % (unsigned)a.V);
     }
 }
 

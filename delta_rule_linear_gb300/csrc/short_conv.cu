@@ -85,7 +85,7 @@ __device__ __forceinline__ bool conv_item(const Conv &a, long item, LinItem &it)
 
 // Warp = 32 V channels of one run.  The run that ends a sequence writes its next window (WINDOW_ONLY: nothing else).
 template <typename T, int V, int K, bool WINDOW_ONLY>
-__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(Conv a) {
+__global__ void __launch_bounds__(kThreads, 2) conv_fwd_kernel(Conv a) {
     const int group = blockIdx.x / a.blocks, c = ((blockIdx.x - group * a.blocks) * 32 + (threadIdx.x & 31)) * V;
     const bool live = c < a.C;
     LinItem it;
@@ -105,35 +105,35 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(Conv a) {
         else
             load_window<T, V, K>(a.h0, it.n, t, a.C, c, true, x[j]);
     }
-    // eight rows in flight
-    constexpr int U = 8;
-    for (int t = t0; t < t1; t += U) {
+    auto one = [&](int t, const typename Pack<T, V>::Raw &raw) {
+#pragma unroll
+        for (int j = 0; j + 1 < K; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[j][i] = x[j + 1][i];
+        Pack<T, V>::open(raw, x[K - 1]);
+        float y[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            y[i] = b[i];
+#pragma unroll
+            for (int j = 0; j < K; ++j) y[i] = fmaf(w[j][i], x[j][i], y[i]);
+            if (a.act) {
+                float rest;
+                y[i] *= sigmoid<T>(y[i], rest);
+            }
+        }
+        Pack<T, V>::store(yp + t * a.y.t, y);
+    };
+    constexpr int U = 4;                // rows in flight
+    int t = t0;
+    for (; t + U <= t1; t += U) {
         typename Pack<T, V>::Raw raw[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t + u < t1) raw[u] = Pack<T, V>::get(xp + (t + u) * a.x.t);
+        for (int u = 0; u < U; ++u) raw[u] = Pack<T, V>::get(xp + (t + u) * a.x.t);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (t + u >= t1) break;
-#pragma unroll
-            for (int j = 0; j + 1 < K; ++j)
-#pragma unroll
-                for (int i = 0; i < V; ++i) x[j][i] = x[j + 1][i];
-            Pack<T, V>::open(raw[u], x[K - 1]);
-            float y[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                y[i] = b[i];
-#pragma unroll
-                for (int j = 0; j < K; ++j) y[i] = fmaf(w[j][i], x[j][i], y[i]);
-                if (a.act) {
-                    float rest;
-                    y[i] *= sigmoid<T>(y[i], rest);
-                }
-            }
-            Pack<T, V>::store(yp + (t + u) * a.y.t, y);
-        }
+        for (int u = 0; u < U; ++u) one(t + u, raw[u]);
     }
+    for (; t < t1; ++t) one(t, Pack<T, V>::get(xp + t * a.x.t));
 }
 
 // A warp's lanes go over the items warp, warp + warps, ...; q of K rows and x of K rows in registers.
@@ -177,62 +177,63 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(Conv a) {
         // dx of row t - (K - 1) is whole once q_t is there; the first run goes on to the window's rows.  q of rows past
         // the run is formed here too (its share of the weights' gradients belongs to the next run).
         const int last = t1 + K - 1;
-        constexpr int U = 4;
-        for (int t = t0; t < last; t += U) {
+        auto one = [&](int tt, const typename Pack<T, V>::Raw &xr, const typename Pack<T, V>::Raw &gr) {
+#pragma unroll
+            for (int j = 0; j + 1 < K; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    x[j][i] = x[j + 1][i];
+                    q[j][i] = q[j + 1][i];
+                }
+            Pack<T, V>::open(xr, x[K - 1]);
+            float g[V];
+            Pack<T, V>::open(gr, g);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (a.act) {
+                    float p = b[i], rest;
+#pragma unroll
+                    for (int j = 0; j < K; ++j) p = fmaf(w[j][i], x[j][i], p);
+                    const float s = sigmoid<T>(p, rest);
+                    g[i] *= fmaf(p * s, rest, s);
+                }
+                q[K - 1][i] = tt < it.len ? g[i] : 0.f;
+            }
+            if (tt < t1) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    db[i] += q[K - 1][i];
+#pragma unroll
+                    for (int j = 0; j < K; ++j) dw[j][i] = fmaf(q[K - 1][i], x[j][i], dw[j][i]);
+                }
+            }
+            const int row = tt - (K - 1);
+            if (row >= t0 || (t0 == 0 && a.dh0)) {
+                float d[V];
+                const int tail = row - (it.len - (K - 1));        // its row of the next window
+                load_row<T, V>(static_cast<const T *>(a.dhT) + win + (long)tail * a.C, a.dhT && tail >= 0, d);
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int j = 0; j < K; ++j) d[i] = fmaf(w[j][i], q[K - 1 - j][i], d[i]);
+                Pack<T, V>::store(row >= 0 ? dp + row * a.dx.t : static_cast<T *>(a.dh0) + win + (long)(row + K - 1) * a.C, d);
+            }
+        };
+        constexpr int U = 4;            // rows of x and d_y in flight
+        int t = t0;
+        for (const int whole = min(last, it.len); t + U <= whole; t += U) {
             typename Pack<T, V>::Raw xr[U], gr[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                xr[u] = gr[u] = Pack<T, V>::zero();
-                if (t + u < last && t + u < it.len) {
-                    xr[u] = Pack<T, V>::get(xp + (t + u) * a.x.t);
-                    gr[u] = Pack<T, V>::get(gp + (t + u) * a.y.t);
-                }
+                xr[u] = Pack<T, V>::get(xp + (t + u) * a.x.t);
+                gr[u] = Pack<T, V>::get(gp + (t + u) * a.y.t);
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int tt = t + u;
-                if (tt >= last) break;
-#pragma unroll
-                for (int j = 0; j + 1 < K; ++j)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        x[j][i] = x[j + 1][i];
-                        q[j][i] = q[j + 1][i];
-                    }
-                Pack<T, V>::open(xr[u], x[K - 1]);
-                float g[V];
-                Pack<T, V>::open(gr[u], g);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    if (a.act) {
-                        float p = b[i], rest;
-#pragma unroll
-                        for (int j = 0; j < K; ++j) p = fmaf(w[j][i], x[j][i], p);
-                        const float s = sigmoid<T>(p, rest);
-                        g[i] *= fmaf(p * s, rest, s);
-                    }
-                    q[K - 1][i] = tt < it.len ? g[i] : 0.f;
-                }
-                if (tt < t1) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        db[i] += q[K - 1][i];
-#pragma unroll
-                        for (int j = 0; j < K; ++j) dw[j][i] = fmaf(q[K - 1][i], x[j][i], dw[j][i]);
-                    }
-                }
-                const int row = tt - (K - 1);
-                if (row >= t0 || (t0 == 0 && a.dh0)) {
-                    float d[V];
-                    const int tail = row - (it.len - (K - 1));        // its row of the next window
-                    load_row<T, V>(static_cast<const T *>(a.dhT) + win + (long)tail * a.C, a.dhT && tail >= 0, d);
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-#pragma unroll
-                        for (int j = 0; j < K; ++j) d[i] = fmaf(w[j][i], q[K - 1 - j][i], d[i]);
-                    Pack<T, V>::store(row >= 0 ? dp + row * a.dx.t : static_cast<T *>(a.dh0) + win + (long)(row + K - 1) * a.C, d);
-                }
-            }
+            for (int u = 0; u < U; ++u) one(t + u, xr[u], gr[u]);
+        }
+        for (; t < last; ++t) {
+            const bool there = t < it.len;
+            one(t, there ? Pack<T, V>::get(xp + t * a.x.t) : Pack<T, V>::zero(), there ? Pack<T, V>::get(gp + t * a.y.t) : Pack<T, V>::zero());
         }
     }
     // the CTA's sums, in the order of its warps: 4 + 4 (two rounds), then the partial row

@@ -32,11 +32,14 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTile = 32;                   // tokens of a chunk
 constexpr float kLn2F = 0.6931471805599453f;
 
-template <int L> struct Lay {
+template <typename T, int L> struct Lay {
     static constexpr int N = 4 * L, CL = 32 / L, CW = 2 * CL, CH = kWarps * CW;      // states; channel lanes, channels of a warp, of a CTA
-    // floats: B and C of the chunk; per warp dt, u, p (each twice, for both channels of a lane), kept memories, dB and dC
-    static constexpr int HEADS = 2 * kTile * N, ROWS = kTile * CL * 12, KEPT = kTile / 4 * 256, SUMS = kTile * 2 * N;
-    static constexpr size_t bytes(bool local) { return (size_t)(HEADS + kWarps * (ROWS + (local ? 0 : KEPT + SUMS))) * 4; }
+    // floats: B and C of the chunk; per warp dt, u, p (each twice, for both channels of a lane), x, dt, dy, z as they came
+    // (two channels each), memories kept (but the first), dB and dC
+    static constexpr int HEADS = 2 * kTile * N, ROWS = kTile * CL * 12, RAW = kTile * CL * 2 * (int)sizeof(T),
+                         KEPT = (kTile / 4 - 1) * 256, SUMS = kTile * 2 * N;
+    static constexpr int WARP = ROWS + RAW + KEPT + SUMS;
+    static constexpr size_t bytes(bool local) { return (size_t)(HEADS + kWarps * (local ? ROWS : WARP)) * 4; }
 };
 
 struct Bwd {
@@ -45,7 +48,6 @@ struct Bwd {
     long chunks;                // (a bound for packed sequences)
     int slots;                  // CTAs that share a block of channels
     long rows;
-    int pairs;                  // arrays can be read and written by two channels at a time
     float *h, *g, *sums;        // [chunks, D, N] twice, [chunks, D]
     float *bc;                  // [bpg, rows, G, 2 N]
     float *pA, *pd;             // [slots, D, N], [slots, 2, D]
@@ -88,25 +90,40 @@ template <int CNT, int GRP, int STRIDE> struct Meet {
     static __device__ __forceinline__ bool lead(int i) { return i % SAME == 0; }      // of the neighbours
 };
 
-// Two channels' elements at p (n of them are there).
-template <typename T> __device__ __forceinline__ void get2(const T *p, int n, bool pairs, float &x, float &y) {
-    x = y = 0.f;
-    if (pairs) {
-        if (n <= 0) return;
-        if constexpr (sizeof(T) == 4) {
-            const float2 v = *reinterpret_cast<const float2 *>(p);
-            x = v.x, y = v.y;
-        } else {
-            const uint32_t v = *reinterpret_cast<const uint32_t *>(p);
-            x = __uint_as_float(v << 16), y = __uint_as_float(v & 0xffff0000u);
-        }
-    } else {
-        if (n > 0) x = to_f32(p[0]);
-        if (n > 1) y = to_f32(p[1]);
+// Two channels' elements as they lie in memory (n of them are there).  PAIRS: by one access.
+template <typename T> struct Raw2 {
+    uint32_t w[sizeof(T) / 2];
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(w[i]);
+        else
+            return __uint_as_float(i ? w[0] & 0xffff0000u : w[0] << 16);
     }
+};
+template <bool PAIRS, typename T> __device__ __forceinline__ Raw2<T> get2(const T *p, int n) {
+    Raw2<T> r{};
+    if constexpr (PAIRS) {
+        if (n > 0) {
+            if constexpr (sizeof(T) == 4) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(p);
+                r.w[0] = v.x, r.w[1] = v.y;
+            } else {
+                r.w[0] = *reinterpret_cast<const uint32_t *>(p);
+            }
+        }
+    } else if constexpr (sizeof(T) == 4) {
+        if (n > 0) r.w[0] = __float_as_uint(p[0]);
+        if (n > 1) r.w[1] = __float_as_uint(p[1]);
+    } else {
+        uint32_t x = 0, y = 0;
+        if (n > 0) x = __bfloat16_as_ushort(p[0]);
+        if (n > 1) y = __bfloat16_as_ushort(p[1]);
+        r.w[0] = x | y << 16;
+    }
+    return r;
 }
-template <typename T> __device__ __forceinline__ void put2(T *p, int n, bool pairs, float x, float y) {
-    if (pairs) {
+template <bool PAIRS, typename T> __device__ __forceinline__ void put2(T *p, int n, float x, float y) {
+    if constexpr (PAIRS) {
         if (n <= 0) return;
         if constexpr (sizeof(T) == 4) {
             *reinterpret_cast<float2 *>(p) = make_float2(x, y);
@@ -128,57 +145,72 @@ template <typename T> __device__ __forceinline__ T *rows_at(const SsmView &v, co
     return static_cast<T *>(v.p) + at.b * v.b + (at.row + t) * v.t + e;
 }
 
-// What both walks read: B and C (all warps together), and the warp's dt, u, p.
-template <typename T, int L>
-__device__ __forceinline__ void bring(const Bwd &w, const At &at, int g, int d0, int live, float *heads, float *rows) {
-    using Y = Lay<L>;
+// What both walks read: B and C (all warps together), and the warp's dt, u, p; KEEP: and its rows as they came.  All loads of
+// a part go out before the first is used.
+template <typename T, int L, bool PAIRS, bool KEEP>
+__device__ __forceinline__ void bring(const Bwd &w, const At &at, int g, int d0, int live, float *heads, float *rows, float *raw) {
+    using Y = Lay<T, L>;
     const Ssm &a = w.a;
     const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < 2 * kTile * L; i += kThreads) {       // four states of a token
-        const int q = i % L, t = i / L % kTile;
-        const bool isB = i < kTile * L;
-        const SsmView &v = isB ? a.B : a.C;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t < at.len) {
-            const T *p = rows_at<const T>(v, at, t, (long)g * v.g + 4 * q);
-            get2<T>(p, 2, w.pairs, x.x, x.y);
-            get2<T>(p + 2, 2, w.pairs, x.z, x.w);
-        }
-        reinterpret_cast<float4 *>(heads)[(isB ? 0 : kTile * L) + t * L + q] = x;
-    }
-    const int cp = lane % Y::CL, n = live - 2 * cp;
+    const int cp = lane % Y::CL, n = live - 2 * cp, tl = lane / Y::CL;
     const long d = d0 + 2 * cp;
+    constexpr int U = 32 / L < 8 ? 32 / L : 8;         // tokens of a lane and part
+    constexpr int HT = 2 * kTile * L / kThreads;        // quads of states of a thread
+    Raw2<T> hq[HT][2];
+#pragma unroll
+    for (int j = 0; j < HT; ++j) {
+        const int i = threadIdx.x + j * kThreads, q = i % L, t = i / L % kTile;
+        const SsmView &v = i < kTile * L ? a.B : a.C;
+        const T *p = rows_at<const T>(v, at, t, (long)g * v.g + 4 * q);
+        hq[j][0] = get2<PAIRS, T>(p, t < at.len ? 2 : 0);
+        hq[j][1] = get2<PAIRS, T>(p + 2, t < at.len ? 2 : 0);
+    }
     float bias[2] = {0.f, 0.f};
     if (a.bias) {
         if (n > 0) bias[0] = a.bias[d];
         if (n > 1) bias[1] = a.bias[d + 1];
     }
-#pragma unroll 4
-    for (int t = lane / Y::CL; t < kTile; t += L) {
-        const int m = t < at.len ? n : 0;
-        float dt[2], x[2], p[2];
-        get2<T>(rows_at<const T>(a.dt, at, t, d), m, w.pairs, dt[0], dt[1]);
-        get2<T>(rows_at<const T>(a.x, at, t, d), m, w.pairs, x[0], x[1]);
-        get2<T>(rows_at<const T>(a.y, at, t, d), m, w.pairs, p[0], p[1]);
-        dt[0] += bias[0];
-        dt[1] += bias[1];
-        if (a.softplus) softplus<T>(dt[0], dt[1]);
-        if (a.gate.p) {
-            float z[2], rest;
-            get2<T>(rows_at<const T>(a.gate, at, t, d), m, w.pairs, z[0], z[1]);
-            p[0] *= z[0] * sigmoid<T>(z[0], rest);
-            p[1] *= z[1] * sigmoid<T>(z[1], rest);
+#pragma unroll 1
+    for (int t0 = 0; t0 < kTile; t0 += U * L) {
+        Raw2<T> dt2[U], x2[U], y2[U], z2[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = t0 + u * L + tl, m = t < at.len ? n : 0;
+            dt2[u] = get2<PAIRS, T>(rows_at<const T>(a.dt, at, t, d), m);
+            x2[u] = get2<PAIRS, T>(rows_at<const T>(a.x, at, t, d), m);
+            y2[u] = get2<PAIRS, T>(rows_at<const T>(a.y, at, t, d), m);
+            z2[u] = get2<PAIRS, T>(rows_at<const T>(a.gate, at, t, d), a.gate.p ? m : 0);
         }
-        // behind the last token, and in channels that are not there, nothing happens: dt = u = p = 0
-        const bool a0 = m > 0, a1 = m > 1;
-        dt[0] = a0 ? dt[0] : 0.f, dt[1] = a1 ? dt[1] : 0.f;
-        x[0] = a0 ? dt[0] * x[0] : 0.f, x[1] = a1 ? dt[1] * x[1] : 0.f;
-        p[0] = a0 ? p[0] : 0.f, p[1] = a1 ? p[1] : 0.f;
-        float4 *to = reinterpret_cast<float4 *>(rows) + (t * Y::CL + cp) * 3;
-        to[0] = make_float4(dt[0], dt[0], dt[1], dt[1]);
-        to[1] = make_float4(x[0], x[0], x[1], x[1]);
-        to[2] = make_float4(p[0], p[0], p[1], p[1]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = t0 + u * L + tl, m = t < at.len ? n : 0;
+            float dt[2] = {dt2[u][0] + bias[0], dt2[u][1] + bias[1]}, p[2] = {y2[u][0], y2[u][1]}, rest;
+            if (a.softplus) softplus<T>(dt[0], dt[1]);
+            if (a.gate.p) {
+                p[0] *= z2[u][0] * sigmoid<T>(z2[u][0], rest);
+                p[1] *= z2[u][1] * sigmoid<T>(z2[u][1], rest);
+            }
+            // behind the last token, and in channels that are not there, nothing happens: dt = u = p = 0
+            dt[0] = m > 0 ? dt[0] : 0.f, dt[1] = m > 1 ? dt[1] : 0.f;
+            const float u0 = m > 0 ? dt[0] * x2[u][0] : 0.f, u1 = m > 1 ? dt[1] * x2[u][1] : 0.f;
+            float4 *to = reinterpret_cast<float4 *>(rows) + (t * Y::CL + cp) * 3;
+            to[0] = make_float4(dt[0], dt[0], dt[1], dt[1]);
+            to[1] = make_float4(u0, u0, u1, u1);
+            to[2] = make_float4(p[0], p[0], p[1], p[1]);
+            if constexpr (KEEP) {
+                Raw2<T> *r = reinterpret_cast<Raw2<T> *>(raw) + (t * Y::CL + cp) * 4;
+                if constexpr (sizeof(T) == 2) {
+                    *reinterpret_cast<uint4 *>(r) = make_uint4(x2[u].w[0], dt2[u].w[0], y2[u].w[0], z2[u].w[0]);
+                } else {
+                    reinterpret_cast<uint4 *>(r)[0] = make_uint4(x2[u].w[0], x2[u].w[1], dt2[u].w[0], dt2[u].w[1]);
+                    reinterpret_cast<uint4 *>(r)[1] = make_uint4(y2[u].w[0], y2[u].w[1], z2[u].w[0], z2[u].w[1]);
+                }
+            }
+        }
     }
+#pragma unroll
+    for (int j = 0; j < HT; ++j)        // B's quads, then C's, token by token: the order of the threads
+        reinterpret_cast<float4 *>(heads)[threadIdx.x + j * kThreads] = make_float4(hq[j][0][0], hq[j][0][1], hq[j][1][0], hq[j][1][1]);
 }
 
 __device__ __forceinline__ Two pair_at(const float *p) { return *reinterpret_cast<const Two *>(p); }
@@ -194,9 +226,9 @@ __device__ __forceinline__ float both(Two x) {
 }
 
 // CTA = one chunk, kWarps warps' channels.
-template <typename T, int L>
+template <typename T, int L, bool PAIRS>
 __global__ void __launch_bounds__(kThreads, 4) ssm_bwd_local_kernel(const __grid_constant__ Bwd w) {
-    using Y = Lay<L>;
+    using Y = Lay<T, L>;
     extern __shared__ __align__(16) float smem[];
     const Ssm &a = w.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, l = lane % L, cl = lane / L;
@@ -208,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_bwd_local_kernel(const __grid
     const At at{a.s.cu ? 0L : it.n, (a.s.cu ? it.start : 0L) + t0, min(kTile, it.len - t0)};
     const int d0 = g * w.cpg + c0, live = w.cpg - c0;
     float *rows = smem + Y::HEADS + warp * Y::ROWS;
-    bring<T, L>(w, at, g, d0, live, smem, rows);
+    bring<T, L, PAIRS, false>(w, at, g, d0, live, smem, rows, nullptr);
     __syncthreads();
     Two A[2][2], h[2][2], P[2][2], G[2][2];
 #pragma unroll
@@ -315,15 +347,15 @@ template <int N> __global__ void __launch_bounds__(256) ssm_bwd_chain_kernel(con
     if (back && a.dh0) a.dh0[n * DN + e] = v;
 }
 
-template <typename T, int L>
+template <typename T, int L, bool PAIRS>
 __global__ void __launch_bounds__(kThreads, 2) ssm_bwd_grad_kernel(const __grid_constant__ Bwd w) {
-    using Y = Lay<L>;
+    using Y = Lay<T, L>;
     extern __shared__ __align__(16) float smem[];
     const Ssm &a = w.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, l = lane % L, cl = lane / L;
     const int slot = blockIdx.x / w.blocks, cb = blockIdx.x - slot * w.blocks, g = cb / w.bpg, cg = cb - g * w.bpg;
     const int c0 = cg * Y::CH + warp * Y::CW, d0 = g * w.cpg + c0, live = w.cpg - c0;
-    float *rows = smem + Y::HEADS + warp * (Y::ROWS + Y::KEPT + Y::SUMS), *kept = rows + Y::ROWS, *sums = kept + Y::KEPT;
+    float *rows = smem + Y::HEADS + warp * Y::WARP, *raw = rows + Y::ROWS, *kept = raw + Y::RAW, *sums = kept + Y::KEPT;
     Two A[2][2], dA[2][2];
     float skip[2], bias[2], dskip[2] = {0.f, 0.f}, dbias[2] = {0.f, 0.f};
     const int n = live - 2 * cl;            // of the lane's two channels those that are there
@@ -344,14 +376,14 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_bwd_grad_kernel(const __grid_
         const At at{a.s.cu ? 0L : it.n, (a.s.cu ? it.start : 0L) + t0, min(kTile, it.len - t0)};
         if (at.len == 0) continue;
         __syncthreads();        // the chunk before has been read
-        bring<T, L>(w, at, g, d0, live, smem, rows);
-        Two h[2][2], G[2][2];
+        bring<T, L, PAIRS, true>(w, at, g, d0, live, smem, rows, raw);
+        Two h[2][2], G[2][2], start[2][2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const long from = (item * a.D + min(d0 + 2 * cl + c, a.D - 1)) * Y::N + 4 * l;
             ulonglong2 x = make_ulonglong2(0, 0), y = x;
             if (c < n) x = *reinterpret_cast<const ulonglong2 *>(w.h + from), y = *reinterpret_cast<const ulonglong2 *>(w.g + from);
-            h[c][0] = x.x, h[c][1] = x.y;
+            start[c][0] = h[c][0] = x.x, start[c][1] = h[c][1] = x.y;
             G[c][0] = y.x, G[c][1] = y.y;
         }
         __syncthreads();
@@ -361,11 +393,7 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_bwd_grad_kernel(const __grid_
         };
         auto row = [&](int t, int k) { return *reinterpret_cast<const ulonglong2 *>(rows + ((t * Y::CL + cl) * 3 + k) * 4); };
         // forwards, every fourth memory kept
-        for (int q = 0; q < kTile / 4; ++q) {
-            ulonglong2 *to = reinterpret_cast<ulonglong2 *>(kept) + q * 64 + lane;
-            to[0] = make_ulonglong2(h[0][0], h[0][1]);
-            to[32] = make_ulonglong2(h[1][0], h[1][1]);
-            if (q + 1 == kTile / 4) break;
+        for (int q = 0; q < kTile / 4 - 1; ++q) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int t = 4 * q + k;
@@ -378,14 +406,18 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_bwd_grad_kernel(const __grid_
                     h[1][s] = fma2(ex2_2(mul2(dt.y, A[1][s])), h[1][s], mul2(u.y, B[s]));
                 }
             }
+            ulonglong2 *to = reinterpret_cast<ulonglong2 *>(kept) + q * 64 + lane;
+            to[0] = make_ulonglong2(h[0][0], h[0][1]);
+            to[32] = make_ulonglong2(h[1][0], h[1][1]);
         }
         // backwards, four tokens at a time
 #pragma unroll 1
         for (int q = kTile / 4 - 1; q >= 0; --q) {
             if (4 * q >= at.len) continue;          // nothing happens there
             Two was[5][2][2], f[4][2][2];
-            {
-                const ulonglong2 *from = reinterpret_cast<const ulonglong2 *>(kept) + q * 64 + lane;
+            was[0][0][0] = start[0][0], was[0][0][1] = start[0][1], was[0][1][0] = start[1][0], was[0][1][1] = start[1][1];
+            if (q) {
+                const ulonglong2 *from = reinterpret_cast<const ulonglong2 *>(kept) + (q - 1) * 64 + lane;
                 const ulonglong2 x = from[0], y = from[32];
                 was[0][0][0] = x.x, was[0][0][1] = x.y, was[0][1][0] = y.x, was[0][1][1] = y.y;
             }
@@ -460,49 +492,44 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_bwd_grad_kernel(const __grid_
                     const int j = M::first(l) + i, t = 4 * q + (j >> 1), c1 = CNT == 1 ? (j & 1) : 0;
                     const long d = d0 + 2 * cl + c1;
                     const int m = t < at.len ? (CNT == 1 ? min(n - c1, 1) : n) : 0;
-                    const bool two_at_once = CNT > 1 && w.pairs;
-                    float x[2], raw[2], dy[2], z[2], dx[2], ddt[2], dz[2];
-                    get2<T>(rows_at<const T>(a.x, at, t, d), m, two_at_once, x[0], x[1]);
-                    get2<T>(rows_at<const T>(a.dt, at, t, d), m, two_at_once, raw[0], raw[1]);
-                    if (a.gate.p) {
-                        get2<T>(rows_at<const T>(a.y, at, t, d), m, two_at_once, dy[0], dy[1]);
-                        get2<T>(rows_at<const T>(a.gate, at, t, d), m, two_at_once, z[0], z[1]);
-                    }
+                    const Raw2<T> *rw = reinterpret_cast<const Raw2<T> *>(raw) + (t * Y::CL + cl) * 4;
+                    const Raw2<T> x2 = rw[0], dt2 = rw[1], y2 = rw[2], z2 = rw[3];
+                    float dx[2], ddt[2], dz[2];
 #pragma unroll
                     for (int c = 0; c < (CNT > 1 ? 2 : 1); ++c) {
                         const int ch = CNT == 1 ? c1 : c;
                         const float sk = ch ? skip[1] : skip[0], bi = ch ? bias[1] : bias[0];
                         const float *rp = rows + (t * Y::CL + cl) * 12 + 2 * ch;
-                        const float dt = rp[0], p = rp[8];
+                        const float dt = rp[0], p = rp[8], x = ch ? x2[1] : x2[0];
                         float rest = 0.f, slope = 1.f;
-                        if (a.softplus) slope = sigmoid<T>(raw[c] + bi, rest);
+                        if (a.softplus) slope = sigmoid<T>((ch ? dt2[1] : dt2[0]) + bi, rest);
                         dx[c] = fmaf(dt, sB[i + c], sk * p);
-                        ddt[c] = fmaf(x[c], sB[i + c], kLn2F * sA[i + c]) * slope;
+                        ddt[c] = fmaf(x, sB[i + c], kLn2F * sA[i + c]) * slope;
                         if (a.gate.p) {
-                            const float sg = sigmoid<T>(z[c], rest), rr = fmaf(sk, x[c], r[i + c]);
-                            dz[c] = dy[c] * rr * fmaf(z[c] * sg, rest, sg);
+                            const float z = ch ? z2[1] : z2[0], sg = sigmoid<T>(z, rest), rr = fmaf(sk, x, r[i + c]);
+                            dz[c] = (ch ? y2[1] : y2[0]) * rr * fmaf(z * sg, rest, sg);
                         }
                         if (c < m) {
                             if (ch) {
-                                dskip[1] = fmaf(p, x[c], dskip[1]);
+                                dskip[1] = fmaf(p, x, dskip[1]);
                                 dbias[1] += ddt[c];
                             } else {
-                                dskip[0] = fmaf(p, x[c], dskip[0]);
+                                dskip[0] = fmaf(p, x, dskip[0]);
                                 dbias[0] += ddt[c];
                             }
                         }
                     }
-                    put2<T>(rows_at<T>(a.dx, at, t, d), m, two_at_once, dx[0], dx[1]);
-                    put2<T>(rows_at<T>(a.ddt, at, t, d), m, two_at_once, ddt[0], ddt[1]);
-                    if (a.gate.p) put2<T>(rows_at<T>(a.dgate, at, t, d), m, two_at_once, dz[0], dz[1]);
+                    put2<PAIRS && (CNT > 1), T>(rows_at<T>(a.dx, at, t, d), m, dx[0], dx[1]);
+                    put2<PAIRS && (CNT > 1), T>(rows_at<T>(a.ddt, at, t, d), m, ddt[0], ddt[1]);
+                    if (a.gate.p) put2<PAIRS && (CNT > 1), T>(rows_at<T>(a.dgate, at, t, d), m, dz[0], dz[1]);
                 }
             }
         }
         __syncthreads();
         const long row0 = a.s.cu ? at.row : at.b * a.s.T + at.row;
         for (int i = threadIdx.x; i < at.len * 2 * Y::N; i += kThreads) {
-            const float *from = smem + Y::HEADS + Y::ROWS + Y::KEPT + i;
-            constexpr int step = Y::ROWS + Y::KEPT + Y::SUMS;
+            const float *from = smem + Y::HEADS + Y::WARP - Y::SUMS + i;
+            constexpr int step = Y::WARP;
             const float v = (from[0] + from[step]) + (from[2 * step] + from[3 * step]);
             const int t = i / (2 * Y::N), k = i % (2 * Y::N);
             w.bc[(((long)cg * w.rows + row0 + t) * a.G + g) * 2 * Y::N + k] = v;
@@ -587,15 +614,11 @@ template <typename T> bool even(const SsmView &v, bool heads) {
     return !v.p || (reinterpret_cast<uintptr_t>(v.p) % (2 * sizeof(T)) == 0 && v.b % 2 == 0 && v.t % 2 == 0 && (!heads || v.g % 2 == 0));
 }
 
-template <typename T, int L> cudaError_t run(const Ssm &a, cudaStream_t st) {
-    using Y = Lay<L>;
-    const bool varlen = a.s.cu != nullptr;
-    const Plan p = plan(a.s.nseq, a.total, varlen ? (int)a.total : a.s.T, varlen, a.D, a.G, a.N, a.sms);
+template <typename T, int L, bool PAIRS> cudaError_t run(const Ssm &a, const Plan &p, cudaStream_t st) {
+    using Y = Lay<T, L>;
     Bwd w{};
     w.a = a;
     w.cpg = p.cpg, w.bpg = p.bpg, w.blocks = p.blocks, w.chunks = p.chunks, w.slots = p.slots, w.rows = p.rows;
-    w.pairs = p.cpg % 2 == 0 && even<T>(a.x, false) && even<T>(a.dt, false) && even<T>(a.gate, false) && even<T>(a.y, false) &&
-              even<T>(a.B, true) && even<T>(a.C, true) && even<T>(a.dx, false) && even<T>(a.ddt, false) && even<T>(a.dgate, false);
     w.h = reinterpret_cast<float *>(static_cast<char *>(a.ws) + sizeof(WsHeader));
     w.g = w.h + p.mem;
     w.pA = w.g + p.mem;
@@ -605,16 +628,23 @@ template <typename T, int L> cudaError_t run(const Ssm &a, cudaStream_t st) {
     const long ctas = p.chunks * p.blocks;
     const int seq_blocks = (int)(((long)a.D * a.N + 255) / 256);
     if (ctas > 0x7fffffffL || (long)a.s.nseq * seq_blocks > 0x7fffffffL) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(ssm_bwd_local_kernel<T, L>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Y::bytes(true));
+    cudaError_t e = cudaFuncSetAttribute(ssm_bwd_local_kernel<T, L, PAIRS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Y::bytes(true));
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(ssm_bwd_grad_kernel<T, L>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Y::bytes(false));
+    e = cudaFuncSetAttribute(ssm_bwd_grad_kernel<T, L, PAIRS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Y::bytes(false));
     if (e != cudaSuccess) return e;
-    ssm_bwd_local_kernel<T, L><<<(unsigned)ctas, kThreads, Y::bytes(true), st>>>(w);
+    ssm_bwd_local_kernel<T, L, PAIRS><<<(unsigned)ctas, kThreads, Y::bytes(true), st>>>(w);
     ssm_bwd_chain_kernel<4 * L><<<dim3((unsigned)(a.s.nseq * seq_blocks), 2), 256, 0, st>>>(w, seq_blocks);
-    ssm_bwd_grad_kernel<T, L><<<(unsigned)(p.slots * p.blocks), kThreads, Y::bytes(false), st>>>(w);
+    ssm_bwd_grad_kernel<T, L, PAIRS><<<(unsigned)(p.slots * p.blocks), kThreads, Y::bytes(false), st>>>(w);
     const long bc_blocks = (p.rows * a.G * 2 * a.N + 255) / 256, par_blocks = ((long)a.D * (a.N + 2) + 255) / 256;
     ssm_bwd_fold_kernel<T><<<(unsigned)(bc_blocks + par_blocks), 256, 0, st>>>(w, bc_blocks);
     return cudaGetLastError();
+}
+template <typename T, int L> cudaError_t run(const Ssm &a, cudaStream_t st) {
+    const bool varlen = a.s.cu != nullptr;
+    const Plan p = plan(a.s.nseq, a.total, varlen ? (int)a.total : a.s.T, varlen, a.D, a.G, a.N, a.sms);
+    const bool pairs = p.cpg % 2 == 0 && even<T>(a.x, false) && even<T>(a.dt, false) && even<T>(a.gate, false) && even<T>(a.y, false) &&
+                       even<T>(a.B, true) && even<T>(a.C, true) && even<T>(a.dx, false) && even<T>(a.ddt, false) && even<T>(a.dgate, false);
+    return pairs ? run<T, L, true>(a, p, st) : run<T, L, false>(a, p, st);
 }
 template <typename T> cudaError_t go(const Ssm &a, cudaStream_t st) {
     return a.N == 8 ? run<T, 2>(a, st) : a.N == 16 ? run<T, 4>(a, st) : a.N == 32 ? run<T, 8>(a, st) : run<T, 16>(a, st);

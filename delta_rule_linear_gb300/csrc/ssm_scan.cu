@@ -419,34 +419,58 @@ __global__ void __launch_bounds__(threads_of(LOCAL, GROUPS), 1) ssm_scan_kernel(
 
 constexpr int kStepThreads = 128;
 
+// One token: a lane has four states of a channel, for kStepReqs requests at a time (A, skip and bias are read once, all
+// their loads are in flight together).
+constexpr int kStepReqs = 4;
 template <typename T, int L>
 __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(SsmStep a) {
-    const int CH = kStepThreads / L, N = 4 * L;
-    const int d0 = blockIdx.x * CH + threadIdx.x / L, l = threadIdx.x % L, n = blockIdx.y;
+    constexpr int CH = kStepThreads / L, N = 4 * L, R = kStepReqs;
+    const int d0 = blockIdx.x * CH + threadIdx.x / L, l = threadIdx.x % L;
     const bool live = d0 < a.D;
-    const int d = live ? d0 : 0, g = d / (a.D / a.G);
+    const int d = live ? d0 : 0, g = a.G == 1 ? 0 : d / (a.D / a.G);
     auto val = [](const void *p, long i) { return to_f32(static_cast<const T *>(p)[i]); };
-    float dt = val(a.dt, n * a.dtb + d) + (a.bias ? a.bias[d] : 0.f);
-    if (a.softplus) dt = softplus<T>(dt);
-    const float x = val(a.x, n * a.xb + d), u = dt * x;
-    float *sp = a.state + ((long)n * a.D + d) * N + 4 * l;
-    const float4 s = *reinterpret_cast<const float4 *>(sp);
+    float4 s[R];
+    float dt[R], x[R], z[R], B[R][4], C[R][4];
+    const int n0 = blockIdx.y * R;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int n = min(n0 + r, a.nb - 1);
+        s[r] = *reinterpret_cast<const float4 *>(a.state + ((long)n * a.D + d) * N + 4 * l);
+        dt[r] = val(a.dt, n * a.dtb + d);
+        x[r] = val(a.x, n * a.xb + d);
+        z[r] = a.gate ? val(a.gate, n * a.gb + d) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            B[r][i] = val(a.B, n * a.Bb + g * a.Bg + 4 * l + i);
+            C[r][i] = val(a.C, n * a.Cb + g * a.Cg + 4 * l + i);
+        }
+    }
     const float4 A = *reinterpret_cast<const float4 *>(a.A + (long)d * N + 4 * l);
-    float h[4] = {s.x, s.y, s.z, s.w}, y = 0.f;
-    const float Av[4] = {A.x, A.y, A.z, A.w};
-    for (int i = 0; i < 4; ++i) {
-        h[i] = fmaf(ex2(dt * (Av[i] * kLog2eF)), h[i], u * val(a.B, n * a.Bb + g * a.Bg + 4 * l + i));
-        y = fmaf(h[i], val(a.C, n * a.Cb + g * a.Cg + 4 * l + i), y);
+    const float Av[4] = {A.x * kLog2eF, A.y * kLog2eF, A.z * kLog2eF, A.w * kLog2eF};
+    const float bias = a.bias ? a.bias[d] : 0.f, skip = a.skip ? a.skip[d] : 0.f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (n0 + r >= a.nb) break;
+        float t = dt[r] + bias;
+        if (a.softplus) t = softplus<T>(t);
+        const float u = t * x[r];
+        float h[4] = {s[r].x, s[r].y, s[r].z, s[r].w}, y = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[i] = fmaf(ex2(t * Av[i]), h[i], u * B[r][i]);
+            y = fmaf(h[i], C[r][i], y);
+        }
+#pragma unroll
+        for (int off = L / 2; off; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
+        if (!live) continue;
+        *reinterpret_cast<float4 *>(a.state + ((long)(n0 + r) * a.D + d) * N + 4 * l) = make_float4(h[0], h[1], h[2], h[3]);
+        y = fmaf(skip, x[r], y);
+        if (a.gate) {
+            float rest;
+            y *= z[r] * sigmoid<T>(z[r], rest);
+        }
+        if (l == 0) static_cast<T *>(a.y)[(n0 + r) * a.yb + d] = from_f32<T>(y);
     }
-    for (int off = L / 2; off; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
-    if (!live) return;
-    *reinterpret_cast<float4 *>(sp) = make_float4(h[0], h[1], h[2], h[3]);
-    y = fmaf(a.skip ? a.skip[d] : 0.f, x, y);
-    if (a.gate) {
-        float z = val(a.gate, n * a.gb + d), rest;
-        y *= z * sigmoid<T>(z, rest);
-    }
-    if (l == 0) static_cast<T *>(a.y)[n * a.yb + d] = from_f32<T>(y);
 }
 
 template <typename T> bool few_view(const SsmView &v, int n, bool heads) {      // rows start where n elements may be loaded at once
@@ -526,7 +550,7 @@ template <typename T, int L> cudaError_t run(const Ssm &a, cudaStream_t st) {
     return vec ? launch<T, L, true>(a, st) : launch<T, L, false>(a, st);
 }
 template <typename T, int L> cudaError_t run_step(const SsmStep &a, cudaStream_t st) {
-    ssm_step_kernel<T, L><<<dim3((a.D * L + kStepThreads - 1) / kStepThreads, a.nb), kStepThreads, 0, st>>>(a);
+    ssm_step_kernel<T, L><<<dim3((unsigned)(((long)a.D * L + kStepThreads - 1) / kStepThreads), (a.nb + kStepReqs - 1) / kStepReqs), kStepThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 template <typename T> cudaError_t go(const Ssm &a, cudaStream_t st) {

@@ -658,7 +658,7 @@ kda_status kda_ssm_chunk_bwd(const void *d_y, const void *x, const void *dt, con
  * Beam search: the k best continuations of each request's W beams,
  *     total[w, v] = scores[w] + logits[w, v] - log sum_v' exp(logits[w, v']),
  * in order, equal totals by the lowest w V + v: out_scores [B,k] float32, parents and tokens [B,k] int32
- * (token v of beam parent).  Totals are formed and compared in 64 bits and rounded once.
+ * (token v of beam parent).  Totals are formed and compared with 48 bits and rounded once.
  *
  *   logits   [B,W,V], KDA_F32 or KDA_BF16, contiguous or with two element strides (request, beam).
  *   scores   [B,W] float32; -inf: a beam that does not count (on the first step, all but one).
