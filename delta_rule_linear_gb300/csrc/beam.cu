@@ -306,23 +306,30 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(BeamSelect a) {
     // their elements, those that reach the k-th chunk's maximum
     const unsigned long long least = top[k - 1].key;
     l.c = {0, 0xffffffffu};
-    constexpr int parts = kBeamChunk / 32;
-#pragma unroll 4
+    constexpr int U = 8, parts = kBeamChunk / (32 * U);         // eight rows of 32 elements at a time, loaded together
     for (int i = warp; i < k * parts; i += kPickWarps) {
         const unsigned chunk = top[i / parts].at;
         if (chunk == 0xffffffffu) break;         // fewer chunks than k
-        const int w = chunk / a.nc, j = chunk - w * a.nc;
-        const int e = j * kBeamChunk + (i % parts) * 32 + lane;
-        Cand x{0, 0xffffffffu};
-        if (e < a.V) {
-            x.at = (unsigned)(w * (long)a.V + e);
-            x.key = none;
-            if (done(w))
-                x.key = e == a.eos ? key_of(off[w].hi, off[w].lo) : none;
-            else if (off[w].hi > -INFINITY)
-                x.key = key_of(off[w], to_f32(row_of<T>(a, b, w)[e]));
+        const int w = chunk / a.nc, e0 = (int)(chunk - w * a.nc) * kBeamChunk + i % parts * (32 * U) + lane;
+        const Off o = off[w];
+        const T *p = row_of<T>(a, b, w);
+        T x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = e0 + 32 * u < a.V ? p[e0 + 32 * u] : from_f32<T>(0.f);
+        const bool over = done(w);
+#pragma unroll 1
+        for (int u = 0; u < U; ++u) {
+            T v = x[0];
+#pragma unroll
+            for (int q = 0; q + 1 < U; ++q) x[q] = x[q + 1];
+            const int e = e0 + 32 * u;
+            Cand c{0, (unsigned)(w * (long)a.V + e)};
+            if (over)
+                c.key = e == a.eos ? key_of(o.hi, o.lo) : none;
+            else
+                c.key = o.hi > -INFINITY ? key_of(o, to_f32(v)) : none;
+            l.take(e < a.V && c.key >= least, c, k);
         }
-        l.take(x.key != 0 && x.key >= least, x, k);
     }
     join(l, other);
     if (threadIdx.x < k) {

@@ -29,10 +29,10 @@ struct Conv {
     int sms;
 };
 
-// Partial sums of the weights' gradients at most (rows of `part`): two CTAs per SM, of up to 256 channels.
+// Partial sums of the weights' gradients at most (rows of `part`): four CTAs per SM, of up to 128 channels.
 inline int conv_parts(int C, int sms) {
-    const int blocks = C / 256 + (C % 256 != 0);
-    return 2 * sms > blocks ? 2 * sms / blocks : 1;
+    const int blocks = C / 128 + (C % 128 != 0);
+    return 4 * sms > blocks ? 4 * sms / blocks : 1;
 }
 
 cudaError_t launch_conv(const Conv &a, cudaStream_t st);

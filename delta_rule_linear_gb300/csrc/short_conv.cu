@@ -7,36 +7,52 @@
 // where the last K - 1 tokens' dx takes the next window's gradient too, and dx of the tokens before the sequence is the
 // window's gradient.
 //
-// All are bound by HBM: a lane holds V channels (16 bytes), a warp 32 V of them, and walks a run of tokens of one
+// All are bound by HBM: a lane holds V = 4 channels (wider lanes run out of registers before
+// enough rows are in flight: 8 channels took 34 us where 4 take @@), a warp 32 V of them, and walks a run of tokens of one
 // sequence with the K last rows in registers, so that every row is read once, but for the K - 1 rows that a run shares
 // with the next (L2 has them).  The sums are fp32 and rounded once.  The weights' gradients stay in registers over all
 // runs of a lane, are added up over a CTA's warps in shared memory and over the CTAs by a second kernel, in a fixed order.
 #include <algorithm>
 
 #include "conv_internal.cuh"
-#include "pack.cuh"
+#include "ssm_math.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
-template <typename T, int V> __device__ __forceinline__ void load_row(const T *p, bool live, float (&x)[V]) {
-    if (live) {
-        Pack<T, V>::load(p, x);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = 0.f;
-    }
+template <typename T, int V> __device__ __forceinline__ Few<T, V> get(const T *p, bool live = true) {
+    Few<T, V> r;
+    r.template load<true>(p, live ? V : 0);
+    return r;
 }
+template <typename T, int V> __device__ __forceinline__ void open(const Few<T, V> &r, float (&x)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = r[i];
+}
+template <typename T, int V> __device__ __forceinline__ void put(T *p, const float (&x)[V]) { Few<T, V>::template store<true>(p, x, V); }
+template <typename T, int V> __device__ __forceinline__ void load_row(const T *p, bool live, float (&x)[V]) { open<T, V>(get<T, V>(p, live), x); }
 
 // Taps of the lane's channels [c, c + V), and their biases.
-template <int V, int K> __device__ __forceinline__ void load_taps(const Conv &a, int c, bool live, float (&w)[K][V], float (&b)[V]) {
+template <int V, int K, typename A> __device__ __forceinline__ void load_taps(const A &a, int c, bool live, float (&w)[K][V], float (&b)[V]) {
+    if constexpr (V == 4) {        // K 16-byte pieces (the launcher has seen to the alignment)
+        float t[4 * K];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        b[i] = live && a.bias ? a.bias[c + i] : 0.f;
+        for (int j = 0; j < K; ++j) {
+            const float4 v = live ? reinterpret_cast<const float4 *>(a.w + (long)c * K)[j] : make_float4(0.f, 0.f, 0.f, 0.f);
+            t[4 * j] = v.x, t[4 * j + 1] = v.y, t[4 * j + 2] = v.z, t[4 * j + 3] = v.w;
+        }
+        const float4 v = live && a.bias ? *reinterpret_cast<const float4 *>(a.bias + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
 #pragma unroll
-        for (int j = 0; j < K; ++j) w[j][i] = live ? a.w[(long)(c + i) * K + j] : 0.f;
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < K; ++j) w[j][i] = t[i * K + j];
+    } else {
+        b[0] = live && a.bias ? a.bias[c] : 0.f;
+#pragma unroll
+        for (int j = 0; j < K; ++j) w[j][0] = live ? a.w[(long)c * K + j] : 0.f;
     }
 }
 
@@ -50,27 +66,18 @@ __device__ __forceinline__ void load_window(const void *h0, int n, int t, int C,
 template <typename T, int V, int K>
 __device__ __forceinline__ void next_window(const Conv &a, int n, long start, int len, int c) {
     const T *xp = static_cast<const T *>(a.x.p) + (a.s.cu ? start * a.x.t : (long)n * a.x.b) + c;
-    typename Pack<T, V>::Raw r[K - 1];
+    Few<T, V> r[K - 1];
 #pragma unroll
     for (int i = 0; i < K - 1; ++i) {
         const int t = len - (K - 1) + i;
         if (t >= 0)
-            r[i] = Pack<T, V>::get(xp + t * a.x.t);
+            r[i] = get<T, V>(xp + t * a.x.t);
         else
-            r[i] = a.h0 ? Pack<T, V>::get(static_cast<const T *>(a.h0) + ((long)n * (K - 1) + (t + K - 1)) * a.C + c)
-                        : Pack<T, V>::zero();
+            r[i] = get<T, V>(static_cast<const T *>(a.h0) + ((long)n * (K - 1) + (t + K - 1)) * a.C + c, a.h0 != nullptr);
     }
     T *hp = static_cast<T *>(a.hT) + (long)n * (K - 1) * a.C + c;
 #pragma unroll
-    for (int i = 0; i < K - 1; ++i) {
-        if constexpr (V == 1) {
-            hp[(long)i * a.C] = r[i];
-        } else {
-            uint4 *to = reinterpret_cast<uint4 *>(hp + (long)i * a.C);
-#pragma unroll
-            for (int k = 0; k < Pack<T, V>::N; ++k) to[k] = r[i].w[k];
-        }
-    }
+    for (int i = 0; i < K - 1; ++i) r[i].keep(hp + (long)i * a.C);
 }
 
 // The run `item`, with the rows a packed batch has (whatever its prefix array says, none outside them is touched).
@@ -85,7 +92,7 @@ __device__ __forceinline__ bool conv_item(const Conv &a, long item, LinItem &it)
 
 // Warp = 32 V channels of one run.  The run that ends a sequence writes its next window (WINDOW_ONLY: nothing else).
 template <typename T, int V, int K, bool WINDOW_ONLY>
-__global__ void __launch_bounds__(kThreads, 2) conv_fwd_kernel(Conv a) {
+__global__ void __launch_bounds__(kThreads, 3) conv_fwd_kernel(Conv a) {
     const int group = blockIdx.x / a.blocks, c = ((blockIdx.x - group * a.blocks) * 32 + (threadIdx.x & 31)) * V;
     const bool live = c < a.C;
     LinItem it;
@@ -105,12 +112,12 @@ __global__ void __launch_bounds__(kThreads, 2) conv_fwd_kernel(Conv a) {
         else
             load_window<T, V, K>(a.h0, it.n, t, a.C, c, true, x[j]);
     }
-    auto one = [&](int t, const typename Pack<T, V>::Raw &raw) {
+    auto one = [&](int t, const Few<T, V> &raw) {
 #pragma unroll
         for (int j = 0; j + 1 < K; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) x[j][i] = x[j + 1][i];
-        Pack<T, V>::open(raw, x[K - 1]);
+        open<T, V>(raw, x[K - 1]);
         float y[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -122,23 +129,29 @@ __global__ void __launch_bounds__(kThreads, 2) conv_fwd_kernel(Conv a) {
                 y[i] *= sigmoid<T>(y[i], rest);
             }
         }
-        Pack<T, V>::store(yp + t * a.y.t, y);
+        put<T, V>(yp + t * a.y.t, y);
     };
-    constexpr int U = 4;                // rows in flight
+    constexpr int U = 4;                // rows ahead of those at work
     int t = t0;
+    Few<T, V> now[U], next[U];
+    auto fetch = [&](int t, Few<T, V> (&r)[U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) r[u] = get<T, V>(xp + (t + u) * a.x.t);
+    };
+    if (t + U <= t1) fetch(t, now);
     for (; t + U <= t1; t += U) {
-        typename Pack<T, V>::Raw raw[U];
+        if (t + 2 * U <= t1) fetch(t + U, next);
 #pragma unroll
-        for (int u = 0; u < U; ++u) raw[u] = Pack<T, V>::get(xp + (t + u) * a.x.t);
+        for (int u = 0; u < U; ++u) one(t + u, now[u]);
 #pragma unroll
-        for (int u = 0; u < U; ++u) one(t + u, raw[u]);
+        for (int u = 0; u < U; ++u) now[u] = next[u];
     }
-    for (; t < t1; ++t) one(t, Pack<T, V>::get(xp + t * a.x.t));
+    for (; t < t1; ++t) one(t, get<T, V>(xp + t * a.x.t));
 }
 
 // A warp's lanes go over the items warp, warp + warps, ...; q of K rows and x of K rows in registers.
 template <typename T, int V, int K>
-__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(Conv a) {
+__global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(Conv a) {
     __shared__ float sum[kWarps / 2][32 * V + 1];
     next_may_start();
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
@@ -177,7 +190,7 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(Conv a) {
         // dx of row t - (K - 1) is whole once q_t is there; the first run goes on to the window's rows.  q of rows past
         // the run is formed here too (its share of the weights' gradients belongs to the next run).
         const int last = t1 + K - 1;
-        auto one = [&](int tt, const typename Pack<T, V>::Raw &xr, const typename Pack<T, V>::Raw &gr) {
+        auto one = [&](int tt, const Few<T, V> &xr, const Few<T, V> &gr) {
 #pragma unroll
             for (int j = 0; j + 1 < K; ++j)
 #pragma unroll
@@ -185,9 +198,9 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(Conv a) {
                     x[j][i] = x[j + 1][i];
                     q[j][i] = q[j + 1][i];
                 }
-            Pack<T, V>::open(xr, x[K - 1]);
+            open<T, V>(xr, x[K - 1]);
             float g[V];
-            Pack<T, V>::open(gr, g);
+            open<T, V>(gr, g);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 if (a.act) {
@@ -216,25 +229,22 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(Conv a) {
                 for (int i = 0; i < V; ++i)
 #pragma unroll
                     for (int j = 0; j < K; ++j) d[i] = fmaf(w[j][i], q[K - 1 - j][i], d[i]);
-                Pack<T, V>::store(row >= 0 ? dp + row * a.dx.t : static_cast<T *>(a.dh0) + win + (long)(row + K - 1) * a.C, d);
+                put<T, V>(row >= 0 ? dp + row * a.dx.t : static_cast<T *>(a.dh0) + win + (long)(row + K - 1) * a.C, d);
             }
         };
         constexpr int U = 4;            // rows of x and d_y in flight
         int t = t0;
         for (const int whole = min(last, it.len); t + U <= whole; t += U) {
-            typename Pack<T, V>::Raw xr[U], gr[U];
+            Few<T, V> xr[U], gr[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                xr[u] = Pack<T, V>::get(xp + (t + u) * a.x.t);
-                gr[u] = Pack<T, V>::get(gp + (t + u) * a.y.t);
+                xr[u] = get<T, V>(xp + (t + u) * a.x.t);
+                gr[u] = get<T, V>(gp + (t + u) * a.y.t);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) one(t + u, xr[u], gr[u]);
         }
-        for (; t < last; ++t) {
-            const bool there = t < it.len;
-            one(t, there ? Pack<T, V>::get(xp + t * a.x.t) : Pack<T, V>::zero(), there ? Pack<T, V>::get(gp + t * a.y.t) : Pack<T, V>::zero());
-        }
+        for (; t < last; ++t) one(t, get<T, V>(xp + t * a.x.t, t < it.len), get<T, V>(gp + t * a.y.t, t < it.len));
     }
     // the CTA's sums, in the order of its warps: 4 + 4 (two rounds), then the partial row
     const long row = (long)blockIdx.y * a.C * (K + 1);
@@ -287,33 +297,32 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStep a) {
     if (id >= (long)nv * a.B) return;
     const int n = (int)(id / nv), c = (int)(id - (long)n * nv) * V;
     T *sp = static_cast<T *>(a.state) + (long)n * (K - 1) * a.C + c;
-    float x[K][V], y[V];
-    typename Pack<T, V>::Raw r[K];
+    float x[K][V], w[K][V], b[V], y[V];
+    Few<T, V> r[K];
 #pragma unroll
-    for (int j = 0; j + 1 < K; ++j) r[j] = Pack<T, V>::get(sp + (long)j * a.C);
-    r[K - 1] = Pack<T, V>::get(static_cast<const T *>(a.x) + n * a.xb + c);
+    for (int j = 0; j + 1 < K; ++j) r[j] = get<T, V>(sp + (long)j * a.C);
+    r[K - 1] = get<T, V>(static_cast<const T *>(a.x) + n * a.xb + c);
+    load_taps<V, K>(a, c, true, w, b);
 #pragma unroll
-    for (int j = 0; j < K; ++j) Pack<T, V>::open(r[j], x[j]);
+    for (int j = 0; j < K; ++j) open<T, V>(r[j], x[j]);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        y[i] = a.bias ? a.bias[c + i] : 0.f;
+        y[i] = b[i];
 #pragma unroll
-        for (int j = 0; j < K; ++j) y[i] = fmaf(a.w[(long)(c + i) * K + j], x[j][i], y[i]);
+        for (int j = 0; j < K; ++j) y[i] = fmaf(w[j][i], x[j][i], y[i]);
         if (a.act) {
             float rest;
             y[i] *= sigmoid<T>(y[i], rest);
         }
     }
-    Pack<T, V>::store(static_cast<T *>(a.y) + n * a.yb + c, y);
+    put<T, V>(static_cast<T *>(a.y) + n * a.yb + c, y);
 #pragma unroll
-    for (int j = 0; j + 1 < K; ++j) Pack<T, V>::store(sp + (long)j * a.C, x[j + 1]);
+    for (int j = 0; j + 1 < K; ++j) r[j + 1].keep(sp + (long)j * a.C);
 }
 
-template <typename T> bool vec_view(const ConvView &v) {
-    constexpr int V = 16 / sizeof(T);
-    return reinterpret_cast<uintptr_t>(v.p) % 16 == 0 && v.b % V == 0 && v.t % V == 0;
-}
-bool al16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+constexpr int kLane = 4;            // channels of a lane where everything is aligned to them
+template <typename T> bool by4(const void *p) { return reinterpret_cast<uintptr_t>(p) % (kLane * sizeof(T)) == 0; }
+template <typename T> bool vec_view(const ConvView &v) { return by4<T>(v.p) && v.b % kLane == 0 && v.t % kLane == 0; }
 
 // Tokens of a run: long ones share few rows with the next, but the launch needs about a thousand lanes per SM.
 int pick_run(const Conv &a, int V, long rows, int lanes_per_sm) {
@@ -342,7 +351,7 @@ template <typename T, int V, int K> cudaError_t run_bwd(Conv a, cudaStream_t st)
     a.run = pick_run(a, V, rows, 512);
     a.items = lin_items(a.s.nseq, a.s.cu ? a.total : a.s.T, a.s.cu ? (int)a.total : a.s.T, a.s.cu != nullptr, a.run);
     const unsigned cb = (a.C + 32 * V - 1) / (32 * V);
-    const long want = (long)std::max(1, std::min(conv_parts(a.C, a.sms), 2 * a.sms / (int)cb));
+    const long want = (long)std::max(1, std::min(conv_parts(a.C, a.sms), 4 * a.sms / (int)cb));
     const unsigned parts = (unsigned)std::min((a.items + kWarps - 1) / kWarps, want);
     conv_bwd_kernel<T, V, K><<<dim3(cb, parts), kThreads, 0, st>>>(a);
     const long cols = (long)a.C * (K + 1);
@@ -353,9 +362,9 @@ template <typename T, int V, int K> cudaError_t run_bwd(Conv a, cudaStream_t st)
 }
 
 template <typename T, int K> cudaError_t go(const Conv &a, bool bwd, cudaStream_t st) {
-    constexpr int V = 16 / sizeof(T);
-    const bool vec = a.C % V == 0 && vec_view<T>(a.x) && vec_view<T>(a.y) && al16(a.h0) && al16(a.hT) &&
-                     (!bwd || (vec_view<T>(a.dx) && al16(a.dhT) && al16(a.dh0)));
+    constexpr int V = kLane;
+    const bool vec = a.C % V == 0 && by4<float>(a.w) && by4<float>(a.bias) && vec_view<T>(a.x) && vec_view<T>(a.y) && by4<T>(a.h0) &&
+                     by4<T>(a.hT) && (!bwd || (vec_view<T>(a.dx) && by4<T>(a.dhT) && by4<T>(a.dh0)));
     if (bwd) return vec ? run_bwd<T, V, K>(a, st) : run_bwd<T, 1, K>(a, st);
     return vec ? run_fwd<T, V, K>(a, st) : run_fwd<T, 1, K>(a, st);
 }
@@ -369,8 +378,9 @@ template <typename T, int V, int K> cudaError_t run_step(const ConvStep &a, cuda
     return cudaGetLastError();
 }
 template <typename T, int K> cudaError_t go_step(const ConvStep &a, cudaStream_t st) {
-    constexpr int V = 16 / sizeof(T);
-    const bool vec = a.C % V == 0 && al16(a.x) && al16(a.y) && al16(a.state) && (a.B == 1 || (a.xb % V == 0 && a.yb % V == 0));
+    constexpr int V = kLane;
+    const bool vec = a.C % V == 0 && by4<float>(a.w) && by4<float>(a.bias) && by4<T>(a.x) && by4<T>(a.y) && by4<T>(a.state) &&
+                     (a.B == 1 || (a.xb % V == 0 && a.yb % V == 0));
     return vec ? run_step<T, V, K>(a, st) : run_step<T, 1, K>(a, st);
 }
 template <typename T> cudaError_t taps_step(const ConvStep &a, cudaStream_t st) {

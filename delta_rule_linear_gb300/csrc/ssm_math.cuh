@@ -113,6 +113,22 @@ template <typename T, int N> struct Few {
         else
             return __uint_as_float((i & 1) ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16));
     }
+    // as they are, to an aligned place
+    __device__ __forceinline__ void keep(T *p) const {
+        if constexpr (N == 1) {
+            if constexpr (sizeof(T) == 4)
+                p[0] = __uint_as_float(w[0]);
+            else
+                p[0] = __ushort_as_bfloat16((unsigned short)w[0]);
+        } else if constexpr (W % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        } else if constexpr (W == 2) {
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        } else {
+            *reinterpret_cast<uint32_t *>(p) = w[0];
+        }
+    }
     template <bool VEC> static __device__ __forceinline__ void store(T *p, const float (&x)[N], int n) {
         if (VEC) {
             if (n <= 0) return;

@@ -422,7 +422,7 @@ constexpr int kStepThreads = 128;
 // One token: a lane has four states of a channel, for kStepReqs requests at a time (A, skip and bias are read once, all
 // their loads are in flight together).
 constexpr int kStepReqs = 4;
-template <typename T, int L>
+template <typename T, int L, bool VEC>
 __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(SsmStep a) {
     constexpr int CH = kStepThreads / L, N = 4 * L, R = kStepReqs;
     const int d0 = blockIdx.x * CH + threadIdx.x / L, l = threadIdx.x % L;
@@ -430,7 +430,8 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(SsmStep a) {
     const int d = live ? d0 : 0, g = a.G == 1 ? 0 : d / (a.D / a.G);
     auto val = [](const void *p, long i) { return to_f32(static_cast<const T *>(p)[i]); };
     float4 s[R];
-    float dt[R], x[R], z[R], B[R][4], C[R][4];
+    float dt[R], x[R], z[R];
+    Few<T, 4> B[R], C[R];
     const int n0 = blockIdx.y * R;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -439,11 +440,8 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(SsmStep a) {
         dt[r] = val(a.dt, n * a.dtb + d);
         x[r] = val(a.x, n * a.xb + d);
         z[r] = a.gate ? val(a.gate, n * a.gb + d) : 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            B[r][i] = val(a.B, n * a.Bb + g * a.Bg + 4 * l + i);
-            C[r][i] = val(a.C, n * a.Cb + g * a.Cg + 4 * l + i);
-        }
+        B[r].template load<VEC>(static_cast<const T *>(a.B) + n * a.Bb + g * a.Bg + 4 * l, 4);
+        C[r].template load<VEC>(static_cast<const T *>(a.C) + n * a.Cb + g * a.Cg + 4 * l, 4);
     }
     const float4 A = *reinterpret_cast<const float4 *>(a.A + (long)d * N + 4 * l);
     const float Av[4] = {A.x * kLog2eF, A.y * kLog2eF, A.z * kLog2eF, A.w * kLog2eF};
@@ -550,7 +548,12 @@ template <typename T, int L> cudaError_t run(const Ssm &a, cudaStream_t st) {
     return vec ? launch<T, L, true>(a, st) : launch<T, L, false>(a, st);
 }
 template <typename T, int L> cudaError_t run_step(const SsmStep &a, cudaStream_t st) {
-    ssm_step_kernel<T, L><<<dim3((unsigned)(((long)a.D * L + kStepThreads - 1) / kStepThreads), (a.nb + kStepReqs - 1) / kStepReqs), kStepThreads, 0, st>>>(a);
+    const dim3 grid((unsigned)(((long)a.D * L + kStepThreads - 1) / kStepThreads), (a.nb + kStepReqs - 1) / kStepReqs);
+    const auto by4 = [](const void *p, long long b, long long g) { return reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0 && b % 4 == 0 && g % 4 == 0; };
+    if (by4(a.B, a.Bb, a.Bg) && by4(a.C, a.Cb, a.Cg))
+        ssm_step_kernel<T, L, true><<<grid, kStepThreads, 0, st>>>(a);
+    else
+        ssm_step_kernel<T, L, false><<<grid, kStepThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 template <typename T> cudaError_t go(const Ssm &a, cudaStream_t st) {
