@@ -7,9 +7,8 @@
 // where the last K - 1 tokens' dx takes the next window's gradient too, and dx of the tokens before the sequence is the
 // window's gradient.
 //
-// All are bound by HBM: a lane holds V = 4 channels (wider lanes run out of registers before
-// enough rows are in flight: 8 channels took 34 us where 4 take @@), a warp 32 V of them, and walks a run of tokens of one
-// sequence with the K last rows in registers, so that every row is read once, but for the K - 1 rows that a run shares
+// All are bound by HBM: a lane holds V = 4 channels in packed pairs (8 of them left registers for too few rows in flight: 34 us
+// where 4 take 19), a warp 32 V of them, and walks a run of tokens of one sequence with the K last rows in registers, so that every row is read once, but for the K - 1 rows that a run shares
 // with the next (L2 has them).  The sums are fp32 and rounded once.  The weights' gradients stay in registers over all
 // runs of a lane, are added up over a CTA's warps in shared memory and over the CTAs by a second kernel, in a fixed order.
 #include <algorithm>
@@ -22,20 +21,58 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
+// V channels' values, in packed pairs where there are any.
+template <int V> struct Ch {
+    static constexpr int P = V / 2;
+    Two p[P];
+    __device__ __forceinline__ void set(const float (&x)[V]) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) p[i] = two(x[2 * i], x[2 * i + 1]);
+    }
+    __device__ __forceinline__ void get(float (&x)[V]) const {
+#pragma unroll
+        for (int i = 0; i < P; ++i) each(p[i], x[2 * i], x[2 * i + 1]);
+    }
+    __device__ __forceinline__ void add(const Ch &a) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) p[i] = add2(p[i], a.p[i]);
+    }
+    __device__ __forceinline__ void fma(const Ch &a, const Ch &b) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) p[i] = fma2(a.p[i], b.p[i], p[i]);
+    }
+};
+template <> struct Ch<1> {
+    float p;
+    __device__ __forceinline__ void set(const float (&x)[1]) { p = x[0]; }
+    __device__ __forceinline__ void get(float (&x)[1]) const { x[0] = p; }
+    __device__ __forceinline__ void add(const Ch &a) { p += a.p; }
+    __device__ __forceinline__ void fma(const Ch &a, const Ch &b) { p = fmaf(a.p, b.p, p); }
+};
+
 template <typename T, int V> __device__ __forceinline__ Few<T, V> get(const T *p, bool live = true) {
     Few<T, V> r;
     r.template load<true>(p, live ? V : 0);
     return r;
 }
-template <typename T, int V> __device__ __forceinline__ void open(const Few<T, V> &r, float (&x)[V]) {
+template <typename T, int V> __device__ __forceinline__ Ch<V> open(const Few<T, V> &r) {
+    float x[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) x[i] = r[i];
+    Ch<V> c;
+    c.set(x);
+    return c;
 }
 template <typename T, int V> __device__ __forceinline__ void put(T *p, const float (&x)[V]) { Few<T, V>::template store<true>(p, x, V); }
-template <typename T, int V> __device__ __forceinline__ void load_row(const T *p, bool live, float (&x)[V]) { open<T, V>(get<T, V>(p, live), x); }
+template <int V> __device__ __forceinline__ Ch<V> zeros() {
+    float x[V] = {};
+    Ch<V> c;
+    c.set(x);
+    return c;
+}
 
 // Taps of the lane's channels [c, c + V), and their biases.
-template <int V, int K, typename A> __device__ __forceinline__ void load_taps(const A &a, int c, bool live, float (&w)[K][V], float (&b)[V]) {
+template <int V, int K, typename A> __device__ __forceinline__ void load_taps(const A &a, int c, bool live, Ch<V> (&w)[K], Ch<V> &b) {
     if constexpr (V == 4) {        // K 16-byte pieces (the launcher has seen to the alignment)
         float t[4 * K];
 #pragma unroll
@@ -44,22 +81,20 @@ template <int V, int K, typename A> __device__ __forceinline__ void load_taps(co
             t[4 * j] = v.x, t[4 * j + 1] = v.y, t[4 * j + 2] = v.z, t[4 * j + 3] = v.w;
         }
         const float4 v = live && a.bias ? *reinterpret_cast<const float4 *>(a.bias + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-        b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+        b.set({v.x, v.y, v.z, v.w});
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int j = 0; j < K; ++j) w[j][i] = t[i * K + j];
+        for (int j = 0; j < K; ++j) w[j].set({t[j], t[K + j], t[2 * K + j], t[3 * K + j]});
     } else {
-        b[0] = live && a.bias ? a.bias[c] : 0.f;
+        b.set({live && a.bias ? a.bias[c] : 0.f});
 #pragma unroll
-        for (int j = 0; j < K; ++j) w[j][0] = live ? a.w[(long)c * K + j] : 0.f;
+        for (int j = 0; j < K; ++j) w[j].set({live ? a.w[(long)c * K + j] : 0.f});
     }
 }
 
 // Row t of the window before a sequence's tokens (t in [-(K - 1), -1]).
 template <typename T, int V, int K>
-__device__ __forceinline__ void load_window(const void *h0, int n, int t, int C, int c, bool live, float (&x)[V]) {
-    load_row<T, V>(static_cast<const T *>(h0) + ((long)n * (K - 1) + (t + K - 1)) * C + c, live && h0, x);
+__device__ __forceinline__ Ch<V> load_window(const void *h0, int n, int t, int C, int c) {
+    return open<T, V>(get<T, V>(static_cast<const T *>(h0) + ((long)n * (K - 1) + (t + K - 1)) * C + c, h0 != nullptr));
 }
 
 // The window after sequence n: rows len - (K - 1) .. len - 1, read before any is written (hT may be h0).
@@ -92,7 +127,7 @@ __device__ __forceinline__ bool conv_item(const Conv &a, long item, LinItem &it)
 
 // Warp = 32 V channels of one run.  The run that ends a sequence writes its next window (WINDOW_ONLY: nothing else).
 template <typename T, int V, int K, bool WINDOW_ONLY>
-__global__ void __launch_bounds__(kThreads, 3) conv_fwd_kernel(Conv a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) conv_fwd_kernel(Conv a) {
     const int group = blockIdx.x / a.blocks, c = ((blockIdx.x - group * a.blocks) * 32 + (threadIdx.x & 31)) * V;
     const bool live = c < a.C;
     LinItem it;
@@ -100,31 +135,27 @@ __global__ void __launch_bounds__(kThreads, 3) conv_fwd_kernel(Conv a) {
     const int t0 = it.p * a.run, t1 = min(it.len, t0 + a.run);
     if (a.hT && it.p == it.nseg - 1 && live && (WINDOW_ONLY || a.hT != a.h0)) next_window<T, V, K>(a, it.n, it.start, it.len, c);
     if (WINDOW_ONLY || !live || t0 >= t1) return;
-    float w[K][V], b[V], x[K][V];
+    Ch<V> w[K], b, x[K];
     load_taps<V, K>(a, c, live, w, b);
     const T *xp = static_cast<const T *>(a.x.p) + (a.s.cu ? it.start * a.x.t : it.n * a.x.b) + c;
     T *yp = static_cast<T *>(a.y.p) + (a.s.cu ? it.start * a.y.t : it.n * a.y.b) + c;
 #pragma unroll
     for (int j = 1; j < K; ++j) {
         const int t = t0 - K + j;
-        if (t >= 0)
-            load_row<T, V>(xp + t * a.x.t, true, x[j]);
-        else
-            load_window<T, V, K>(a.h0, it.n, t, a.C, c, true, x[j]);
+        x[j] = t >= 0 ? open<T, V>(get<T, V>(xp + t * a.x.t)) : load_window<T, V, K>(a.h0, it.n, t, a.C, c);
     }
     auto one = [&](int t, const Few<T, V> &raw) {
 #pragma unroll
-        for (int j = 0; j + 1 < K; ++j)
+        for (int j = 0; j + 1 < K; ++j) x[j] = x[j + 1];
+        x[K - 1] = open<T, V>(raw);
+        Ch<V> p = b;
 #pragma unroll
-            for (int i = 0; i < V; ++i) x[j][i] = x[j + 1][i];
-        open<T, V>(raw, x[K - 1]);
+        for (int j = 0; j < K; ++j) p.fma(w[j], x[j]);
         float y[V];
+        p.get(y);
+        if (a.act) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            y[i] = b[i];
-#pragma unroll
-            for (int j = 0; j < K; ++j) y[i] = fmaf(w[j][i], x[j][i], y[i]);
-            if (a.act) {
+            for (int i = 0; i < V; ++i) {
                 float rest;
                 y[i] *= sigmoid<T>(y[i], rest);
             }
@@ -157,14 +188,10 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(Conv a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const int c = (blockIdx.x * 32 + lane) * V;
     const bool live = c < a.C;
-    float w[K][V], b[V], dw[K][V], db[V];
+    Ch<V> w[K], b, dw[K], db = zeros<V>();
     load_taps<V, K>(a, c, live, w, b);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        db[i] = 0.f;
-#pragma unroll
-        for (int j = 0; j < K; ++j) dw[j][i] = 0.f;
-    }
+    for (int j = 0; j < K; ++j) dw[j] = db;
     for (long item = (long)blockIdx.y * kWarps + warp; item < a.items; item += (long)gridDim.y * kWarps) {
         LinItem it;
         if (!conv_item(a, item, it)) break;
@@ -174,65 +201,59 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(Conv a) {
         const T *gp = static_cast<const T *>(a.y.p) + (a.s.cu ? it.start * a.y.t : it.n * a.y.b) + c;
         T *dp = static_cast<T *>(a.dx.p) + (a.s.cu ? it.start * a.dx.t : it.n * a.dx.b) + c;
         const long win = (long)it.n * (K - 1) * a.C + c;      // row -(K - 1) of the window
-        float x[K][V], q[K][V];
+        Ch<V> x[K], q[K];
 #pragma unroll
         for (int j = 1; j < K; ++j) {
             const int t = t0 - K + j;
-            if (t >= 0)
-                load_row<T, V>(xp + t * a.x.t, true, x[j]);
-            else
-                load_window<T, V, K>(a.h0, it.n, t, a.C, c, true, x[j]);
+            x[j] = t >= 0 ? open<T, V>(get<T, V>(xp + t * a.x.t)) : load_window<T, V, K>(a.h0, it.n, t, a.C, c);
         }
 #pragma unroll
-        for (int j = 0; j < K; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) q[j][i] = 0.f;
+        for (int j = 0; j < K; ++j) q[j] = zeros<V>();
         // dx of row t - (K - 1) is whole once q_t is there; the first run goes on to the window's rows.  q of rows past
         // the run is formed here too (its share of the weights' gradients belongs to the next run).
         const int last = t1 + K - 1;
         auto one = [&](int tt, const Few<T, V> &xr, const Few<T, V> &gr) {
 #pragma unroll
-            for (int j = 0; j + 1 < K; ++j)
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    x[j][i] = x[j + 1][i];
-                    q[j][i] = q[j + 1][i];
-                }
-            open<T, V>(xr, x[K - 1]);
-            float g[V];
-            open<T, V>(gr, g);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                if (a.act) {
-                    float p = b[i], rest;
-#pragma unroll
-                    for (int j = 0; j < K; ++j) p = fmaf(w[j][i], x[j][i], p);
-                    const float s = sigmoid<T>(p, rest);
-                    g[i] *= fmaf(p * s, rest, s);
-                }
-                q[K - 1][i] = tt < it.len ? g[i] : 0.f;
+            for (int j = 0; j + 1 < K; ++j) {
+                x[j] = x[j + 1];
+                q[j] = q[j + 1];
             }
-            if (tt < t1) {
+            x[K - 1] = open<T, V>(xr);
+            float g[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) g[i] = gr[i];
+            if (a.act) {
+                Ch<V> pre = b;
+#pragma unroll
+                for (int j = 0; j < K; ++j) pre.fma(w[j], x[j]);
+                float p[V], rest;
+                pre.get(p);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    db[i] += q[K - 1][i];
-#pragma unroll
-                    for (int j = 0; j < K; ++j) dw[j][i] = fmaf(q[K - 1][i], x[j][i], dw[j][i]);
+                    const float s = sigmoid<T>(p[i], rest);
+                    g[i] *= fmaf(p[i] * s, rest, s);
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) g[i] = tt < it.len ? g[i] : 0.f;
+            q[K - 1].set(g);
+            if (tt < t1) {
+                db.add(q[K - 1]);
+#pragma unroll
+                for (int j = 0; j < K; ++j) dw[j].fma(q[K - 1], x[j]);
             }
             const int row = tt - (K - 1);
             if (row >= t0 || (t0 == 0 && a.dh0)) {
-                float d[V];
                 const int tail = row - (it.len - (K - 1));        // its row of the next window
-                load_row<T, V>(static_cast<const T *>(a.dhT) + win + (long)tail * a.C, a.dhT && tail >= 0, d);
+                Ch<V> d = open<T, V>(get<T, V>(static_cast<const T *>(a.dhT) + win + (long)tail * a.C, a.dhT && tail >= 0));
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-#pragma unroll
-                    for (int j = 0; j < K; ++j) d[i] = fmaf(w[j][i], q[K - 1 - j][i], d[i]);
-                put<T, V>(row >= 0 ? dp + row * a.dx.t : static_cast<T *>(a.dh0) + win + (long)(row + K - 1) * a.C, d);
+                for (int j = 0; j < K; ++j) d.fma(w[j], q[K - 1 - j]);
+                float o[V];
+                d.get(o);
+                put<T, V>(row >= 0 ? dp + row * a.dx.t : static_cast<T *>(a.dh0) + win + (long)(row + K - 1) * a.C, o);
             }
         };
-        constexpr int U = 4;            // rows of x and d_y in flight
+        constexpr int U = sizeof(T) == 2 ? 8 : 4;       // rows of x and d_y in flight
         int t = t0;
         for (const int whole = min(last, it.len); t + U <= whole; t += U) {
             Few<T, V> xr[U], gr[U];
@@ -250,7 +271,8 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(Conv a) {
     const long row = (long)blockIdx.y * a.C * (K + 1);
 #pragma unroll
     for (int j = 0; j <= K; ++j) {
-        float(&v)[V] = j < K ? dw[j < K ? j : 0] : db;
+        float v[V];
+        (j < K ? dw[j < K ? j : 0] : db).get(v);
         __syncthreads();
         if (warp >= kWarps / 2)
 #pragma unroll
@@ -297,20 +319,19 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStep a) {
     if (id >= (long)nv * a.B) return;
     const int n = (int)(id / nv), c = (int)(id - (long)n * nv) * V;
     T *sp = static_cast<T *>(a.state) + (long)n * (K - 1) * a.C + c;
-    float x[K][V], w[K][V], b[V], y[V];
+    Ch<V> w[K], b;
     Few<T, V> r[K];
 #pragma unroll
     for (int j = 0; j + 1 < K; ++j) r[j] = get<T, V>(sp + (long)j * a.C);
     r[K - 1] = get<T, V>(static_cast<const T *>(a.x) + n * a.xb + c);
     load_taps<V, K>(a, c, true, w, b);
 #pragma unroll
-    for (int j = 0; j < K; ++j) open<T, V>(r[j], x[j]);
+    for (int j = 0; j < K; ++j) b.fma(w[j], open<T, V>(r[j]));
+    float y[V];
+    b.get(y);
+    if (a.act) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        y[i] = b[i];
-#pragma unroll
-        for (int j = 0; j < K; ++j) y[i] = fmaf(w[j][i], x[j][i], y[i]);
-        if (a.act) {
+        for (int i = 0; i < V; ++i) {
             float rest;
             y[i] *= sigmoid<T>(y[i], rest);
         }
@@ -334,7 +355,7 @@ int pick_run(const Conv &a, int V, long rows, int lanes_per_sm) {
 
 template <typename T, int V, int K> cudaError_t run_fwd(Conv a, cudaStream_t st) {
     const long rows = a.s.cu ? a.total : (long)a.s.nseq * a.s.T;
-    a.run = pick_run(a, V, rows, 768);
+    a.run = pick_run(a, V, rows, 1536);
     a.items = lin_items(a.s.nseq, a.s.cu ? a.total : a.s.T, a.s.cu ? (int)a.total : a.s.T, a.s.cu != nullptr, a.run);
     a.blocks = (a.C + 32 * V - 1) / (32 * V);
     const long ctas = (a.items + kWarps - 1) / kWarps * a.blocks;

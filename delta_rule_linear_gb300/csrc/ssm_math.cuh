@@ -179,17 +179,18 @@ template <typename T, int N, int THREADS> struct Own {
     static constexpr int BYTES = N * (int)sizeof(T), UNIT = BYTES < 16 ? BYTES : 16, UNITS = BYTES / UNIT;
     static constexpr int SIZE = BYTES * THREADS;
     static constexpr int PER = UNIT / (int)sizeof(T);       // elements of a unit
-    // VEC: p is aligned to a unit and n is 0 or N; otherwise the first n elements, by twos where `pairs` (p aligned to two)
-    template <bool VEC> static __device__ __forceinline__ void fetch(uint8_t *slot, int tid, const T *p, int n, const T *some, bool pairs) {
+    // VEC: p is aligned to a unit and n is 0 or N; otherwise the first n elements, by twos where `pairs` (p aligned to two).
+    // What is not there is not touched.
+    template <bool VEC> static __device__ __forceinline__ void fetch(uint8_t *slot, int tid, const T *p, int n, bool pairs) {
         uint8_t *to = slot + tid * UNIT;
         if constexpr (VEC) {
 #pragma unroll
-            for (int u = 0; u < UNITS; ++u) copy_async<UNIT>(to + u * UNIT * THREADS, n > 0 ? p + u * PER : some, n > 0 ? UNIT : 0);
+            for (int u = 0; u < UNITS; ++u) copy_async<UNIT>(to + u * UNIT * THREADS, p + u * PER, n > 0 ? UNIT : 0);
         } else if (sizeof(T) == 4 || pairs) {
             constexpr int E = 4 / (int)sizeof(T);
 #pragma unroll
             for (int i = 0; i < N; i += E)
-                copy_async<4>(to + i / PER * UNIT * THREADS + i % PER * (int)sizeof(T), i < n ? p + i : some,
+                copy_async<4>(to + i / PER * UNIT * THREADS + i % PER * (int)sizeof(T), p + i,
                               i >= n ? 0 : i + E <= n ? 4 : 4 / E);
         } else {
 #pragma unroll

@@ -279,49 +279,67 @@ __global__ void __launch_bounds__(threads_of(LOCAL, GROUPS), 1) ssm_scan_kernel(
             bias[i] = a.bias && cq + i < live ? a.bias[d0 + cq + i] : 0.f;
             skip[i] = a.skip && cq + i < live ? a.skip[d0 + cq + i] : 0.f;
         }
-        const T *xp = static_cast<const T *>(a.x.p) + b * a.x.b + row0 * a.x.t + d0 + cq;
-        const T *dp = static_cast<const T *>(a.dt.p) + b * a.dt.b + row0 * a.dt.t + d0 + cq;
-        const T *zp = a.gate.p ? static_cast<const T *>(a.gate.p) + b * a.gate.b + row0 * a.gate.t + d0 + cq : nullptr;
-        const T *Bp = static_cast<const T *>(a.B.p) + b * a.B.b + row0 * a.B.t + g * a.B.g;
-        const T *Cp = static_cast<const T *>(a.C.p) + b * a.C.b + row0 * a.C.t + g * a.C.g;
-        T *yp = LOCAL ? nullptr : static_cast<T *>(a.y.p) + b * a.y.b + row0 * a.y.t + d0 + cq;
-        const T *some = static_cast<const T *>(a.x.p);
         using Rows = typename Y::Rows;
         using Quad = typename Y::Quad;
-        auto fetch = [&](int s) {
-            if (s < nt) {
-                uint8_t *slot = ring + s % Y::RING * Y::RAW, *slot_bc = ring_bc + s % Y::RING * Y::RAW_BC;
+        constexpr int NEXT = kServe / Y::NQ;        // tokens from a lane's load to its next
+        // the lane's places in the tile that is fetched next, and in the one that is finished next
+        const T *xp = static_cast<const T *>(a.x.p) + b * a.x.b + (row0 + tq) * a.x.t + d0 + cq;
+        const T *dp = static_cast<const T *>(a.dt.p) + b * a.dt.b + (row0 + tq) * a.dt.t + d0 + cq;
+        const T *zp = a.gate.p ? static_cast<const T *>(a.gate.p) + b * a.gate.b + (row0 + tq) * a.gate.t + d0 + cq : nullptr;
+        const T *hp[Y::BC_TASKS];       // B and C: token = lane; quad of states = the rest, B's then C's
+#pragma unroll
+        for (int j = 0; j < Y::BC_TASKS; ++j) {
+            const int k = warp + 4 * j;
+            const SsmView &v = k < L ? a.B : a.C;
+            hp[j] = static_cast<const T *>(v.p) + b * v.b + (row0 + lane) * v.t + g * v.g + 4 * (k < L ? k : k - L);
+        }
+        T *yp = LOCAL ? nullptr : static_cast<T *>(a.y.p) + b * a.y.b + (row0 + tq) * a.y.t + d0 + cq;
+        const bool gated = zp != nullptr;
+        int to_fetch = 0;               // tokens of the tiles fetched so far
+        uint8_t *slot_in = ring, *slot_bc = ring_bc;
+        auto fetch = [&]() {
+            if (to_fetch < len) {
+                uint8_t *slot = slot_in;
 #pragma unroll
                 for (int j = 0; j < Y::TASKS; ++j, slot += 3 * Rows::SIZE) {
-                    const int t = s * kTile + tq + j * (kServe / Y::NQ), n = t < len ? live - cq : 0;
+                    const int n = to_fetch + tq + j * NEXT < len ? live - cq : 0;
                     if (!SPLIT || role == 1) {
-                        Rows::template fetch<VEC>(slot, tid, xp + (long)t * a.x.t, n, some, w.pairs);
-                        Rows::template fetch<VEC>(slot + Rows::SIZE, tid, dp + (long)t * a.dt.t, n, some, w.pairs);
+                        Rows::template fetch<VEC>(slot, tid, xp + (long)(j * NEXT) * a.x.t, n, w.pairs);
+                        Rows::template fetch<VEC>(slot + Rows::SIZE, tid, dp + (long)(j * NEXT) * a.dt.t, n, w.pairs);
                     }
-                    if (!LOCAL && zp && (!SPLIT || role == 2)) Rows::template fetch<VEC>(slot + 2 * Rows::SIZE, tid, zp + (long)t * a.gate.t, n, some, w.pairs);
+                    if (!LOCAL && gated && (!SPLIT || role == 2)) Rows::template fetch<VEC>(slot + 2 * Rows::SIZE, tid, zp + (long)(j * NEXT) * a.gate.t, n, w.pairs);
                 }
                 if (!sub && role == 1) {
 #pragma unroll
-                    for (int j = 0; j < Y::BC_TASKS; ++j) {      // token = lane; quad of states = the rest, B's then C's
-                        const int k = warp + 4 * j, t = s * kTile + lane;
-                        const bool isB = k < L;
+                    for (int j = 0; j < Y::BC_TASKS; ++j) {
+                        const bool isB = warp + 4 * j < L;
                         if (LOCAL && !isB) continue;
-                        Quad::template fetch<VEC>(slot_bc + j * Quad::SIZE, tid, isB ? Bp + (long)t * a.B.t + 4 * k : Cp + (long)t * a.C.t + 4 * (k - L),
-                                                  t < len ? 4 : 0, some, w.pairs);
+                        Quad::template fetch<VEC>(slot_bc + j * Quad::SIZE, tid, hp[j], to_fetch + lane < len ? 4 : 0, w.pairs);
+                        hp[j] += (long)kTile * (isB ? a.B.t : a.C.t);
                     }
                 }
+                to_fetch += kTile;
+                xp += kTile * a.x.t;
+                dp += kTile * a.dt.t;
+                if (gated) zp += kTile * a.gate.t;
+                const bool round = slot_in == ring + (Y::RING - 1) * Y::RAW;
+                slot_in = round ? ring : slot_in + Y::RAW;
+                slot_bc = round ? ring_bc : slot_bc + Y::RAW_BC;
             }
             copies_commit();
         };
+        const uint8_t *slot_s = ring, *slot_s_bc = ring_bc, *slot_out = ring;      // of tile s, and of tile s - 2
+        auto on = [&](const uint8_t *&slot, const uint8_t *first, int size) { slot = slot == first + (Y::RING - 1) * size ? first : slot + size; };
 #pragma unroll
-        for (int s = 0; s < Y::AHEAD; ++s) fetch(s);
+        for (int s = 0; s < Y::AHEAD; ++s) fetch();
         for (int s = 0; s <= last; ++s) {
             __syncthreads();
             copies_wait<Y::AHEAD - 1>();
             const int P = s & 1;
             if (s < nt && (!SPLIT || role == 1)) {
                 if (!sub) {             // B and C into the operand's rows (token, state, B or C), parts of L states side by side
-                    const uint8_t *slot = ring_bc + s % Y::RING * Y::RAW_BC;
+                    const uint8_t *slot = slot_s_bc;
+                    on(slot_s_bc, ring_bc, Y::RAW_BC);
 #pragma unroll
                     for (int j = 0; j < Y::BC_TASKS; ++j) {
                         const int k = warp + 4 * j, quad = k < L ? k : k - L;
@@ -362,34 +380,42 @@ __global__ void __launch_bounds__(threads_of(LOCAL, GROUPS), 1) ssm_scan_kernel(
                     }
                 }
                 float *base = in + P * Y::IN;
-                const uint8_t *slot = ring + s % Y::RING * Y::RAW;
+                const uint8_t *slot = slot_s;
+                on(slot_s, ring, Y::RAW);
+                const bool whole = (s + 1) * kTile <= len;
 #pragma unroll
                 for (int j = 0; j < Y::TASKS; ++j) {
-                    const int tt = tq + j * (kServe / Y::NQ);
-                    const bool there = s * kTile + tt < len;        // behind the last token the memory stays: dt = 0
+                    const int tt = tq + j * NEXT;
+                    const bool there = whole || s * kTile + tt < len;       // behind the last token the memory stays: dt = 0
                     const Few<T, Y::VC> x = Rows::read(slot + 3 * j * Rows::SIZE, tid), d = Rows::read(slot + (3 * j + 1) * Rows::SIZE, tid);
 #pragma unroll
                     for (int i = 0; i < Y::VC; i += 2) {
                         float v[2] = {d[i] + bias[i], d[i + 1] + bias[i + 1]};
                         if (a.softplus) softplus<T>(v[0], v[1]);
+                        float u[2] = {v[0] * x[i], v[1] * x[i + 1]};
+                        if (!whole) {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) v[k] = there ? v[k] : 0.f, u[k] = there ? u[k] : 0.f;
+                        }
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             float *to_row = base + Y::row(cq + i + k) + tt;
-                            to_row[0] = there ? v[k] : 0.f;
-                            to_row[Y::ROWS] = there ? v[k] * x[i + k] : 0.f;
+                            to_row[0] = v[k];
+                            to_row[Y::ROWS] = u[k];
                         }
                     }
                 }
             }
             if (!LOCAL && s >= 2 && (!SPLIT || role == 2)) {
                 const float *base = out + P * Y::OUT;
-                const uint8_t *slot = ring + (s - 2) % Y::RING * Y::RAW;
+                const uint8_t *slot = slot_out;
+                on(slot_out, ring, Y::RAW);
 #pragma unroll
                 for (int j = 0; j < Y::TASKS; ++j) {
-                    const int tt = tq + j * (kServe / Y::NQ), t = (s - 2) * kTile + tt;
+                    const int tt = tq + j * NEXT, t = (s - 2) * kTile + tt;
                     const Few<T, Y::VC> x = Rows::read(slot + 3 * j * Rows::SIZE, tid);
                     Few<T, Y::VC> z;
-                    if (zp) z = Rows::read(slot + (3 * j + 2) * Rows::SIZE, tid);
+                    if (gated) z = Rows::read(slot + (3 * j + 2) * Rows::SIZE, tid);
                     float v[Y::VC];
 #pragma unroll
                     for (int i = 0; i < Y::VC; ++i) {
@@ -398,15 +424,16 @@ __global__ void __launch_bounds__(threads_of(LOCAL, GROUPS), 1) ssm_scan_kernel(
 #pragma unroll
                         for (int l = 1; l < L; ++l) v[i] += part[l * Y::PART];
                         v[i] = fmaf(skip[i], x[i], v[i]);
-                        if (zp) {
+                        if (gated) {
                             float rest;
                             v[i] *= z[i] * sigmoid<T>(z[i], rest);
                         }
                     }
-                    Few<T, Y::VC>::template store<VEC>(yp + (long)t * a.y.t, v, t < len ? live - cq : 0);
+                    Few<T, Y::VC>::template store<VEC>(yp + (long)(j * NEXT) * a.y.t, v, t < len ? live - cq : 0);
                 }
+                yp += kTile * a.y.t;
             }
-            fetch(s + Y::AHEAD);
+            fetch();
         }
     }
     tc_fence_before();
