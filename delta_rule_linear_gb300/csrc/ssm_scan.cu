@@ -109,15 +109,17 @@ template <int N> __device__ __forceinline__ void landed(uint32_t (&r)[N]) {
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// Threads of a CTA.  A lone group has few warps to change between: other warps store the outputs than bring the inputs.
-constexpr int threads_of(bool local, int groups) { return !local && groups == 1 ? 384 : 256 * groups; }
+// Threads of a CTA.  A lone group has few warps to change between, so what serves is split: four warps each for x and dt, for
+// the outputs, and for B and C.
+constexpr int threads_of(bool local, int groups) { return !local && groups == 1 ? 512 : 256 * groups; }
 
 // VEC: rows and heads start on boundaries of what a lane loads, and groups hold whole loads.
 template <typename T, int L, bool VEC, bool LOCAL, int GROUPS>
 __global__ void __launch_bounds__(threads_of(LOCAL, GROUPS), 1) ssm_scan_kernel(const __grid_constant__ Walk w) {
     using Y = Lay<T, L>;
     constexpr int THREADS = threads_of(LOCAL, GROUPS), GT = THREADS / GROUPS;
-    constexpr bool SPLIT = GT == 384;           // the serving of inputs and of outputs by four warps each
+    constexpr bool SPLIT = GT == 512;
+    constexpr int HEADS = SPLIT ? 3 : 1;        // the role that brings B and C
     constexpr int XR = Y::XROWS(LOCAL), W = LOCAL ? 4 : 8;      // columns of X: 4 W of every four tokens, W of a state
     constexpr uint32_t COLS = LOCAL ? 256 : 512;
     extern __shared__ __align__(1024) uint8_t raw[];
@@ -126,7 +128,7 @@ __global__ void __launch_bounds__(threads_of(LOCAL, GROUPS), 1) ssm_scan_kernel(
     const long item = blockIdx.x / w.blocks;
     const int cb = (int)(blockIdx.x - item * w.blocks), g = cb / w.bpg, sub = threadIdx.x / GT;
     const int c0 = ((cb - g * w.bpg) * GROUPS + sub) * Y::CH;           // the group's first channel among its heads'
-    const int role = threadIdx.x % GT / 128;                            // 0 scan, 1 serve, 2 serve the outputs
+    const int role = threadIdx.x % GT / 128;                            // 0 scan, 1 serve (SPLIT: x and dt), 2 the outputs, 3 B and C
     const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid / 32;
     LinItem it;
     if (blockIdx.x == 0 && threadIdx.x == 0 && (LOCAL || !w.local)) w.hdr->error = 0;       // (no wait can run out this early)
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(threads_of(LOCAL, GROUPS), 1) ssm_scan_kernel(
                     }
                     if (!LOCAL && gated && (!SPLIT || role == 2)) Rows::template fetch<VEC>(slot + 2 * Rows::SIZE, tid, zp + (long)(j * NEXT) * a.gate.t, n, w.pairs);
                 }
-                if (!sub && role == 1) {
+                if (!sub && role == HEADS) {
 #pragma unroll
                     for (int j = 0; j < Y::BC_TASKS; ++j) {
                         const bool isB = warp + 4 * j < L;
@@ -336,8 +338,8 @@ __global__ void __launch_bounds__(threads_of(LOCAL, GROUPS), 1) ssm_scan_kernel(
             __syncthreads();
             copies_wait<Y::AHEAD - 1>();
             const int P = s & 1;
-            if (s < nt && (!SPLIT || role == 1)) {
-                if (!sub) {             // B and C into the operand's rows (token, state, B or C), parts of L states side by side
+            if (s < nt) {
+                if (!sub && role == HEADS) {        // B and C into the operand's rows (token, state, B or C), parts of L states side by side
                     const uint8_t *slot = slot_s_bc;
                     on(slot_s_bc, ring_bc, Y::RAW_BC);
 #pragma unroll
@@ -379,6 +381,8 @@ __global__ void __launch_bounds__(threads_of(LOCAL, GROUPS), 1) ssm_scan_kernel(
                         mma_commit(&ctl.full[P]);
                     }
                 }
+            }
+            if (s < nt && role == 1) {
                 float *base = in + P * Y::IN;
                 const uint8_t *slot = slot_s;
                 on(slot_s, ring, Y::RAW);
