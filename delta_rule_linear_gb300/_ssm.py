@@ -11,7 +11,7 @@ import ctypes
 import torch
 
 from . import _linear
-from ._linear import _F32, _code, _dense, _empty, _into, _like, _need, _ok, _on, _ptr, _view
+from ._linear import _F32, _code, _dense, _empty, _into, _like, _need, _ok, _on, _ptr, _view  # noqa: F401
 
 _CONV_ACT = {None: 0, "silu": 1}
 _I32 = torch.int32
@@ -85,11 +85,11 @@ def _conv_call(x, weight, bias, initial_state, activation, out, final_state, cu,
     if initial_state is not None:
         _dense(initial_state, "initial_state", x.dtype, window, dev)
     if out is None:
-        out = _like(x) if plain else _empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _like(x) if plain else x.new_empty(x.shape)
     else:
         plain &= _into(out, "out", x.dtype, x.shape, dev)
     if final_state is None:
-        final_state = _empty(window, dtype=x.dtype, device=x.device)
+        final_state = x.new_empty(window) if initial_state is None else _like(initial_state)
     else:
         _dense(final_state, "final_state", x.dtype, window, dev)
     s = None if plain else _longs(x.stride(0), x.stride(1), out.stride(0), out.stride(1))
@@ -133,7 +133,7 @@ def conv_decode_step(x, weight, state, bias=None, *, activation="silu", out=None
     B = x.shape[0]
     _dense(state, "state", x.dtype, (B, K - 1, C), dev)
     if out is None:
-        out = _like(x) if plain else _empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _like(x) if plain else x.new_empty(x.shape)
     else:
         plain &= _into(out, "out", x.dtype, x.shape, dev)
     s = None if plain else _longs(x.stride(0), out.stride(0))
@@ -165,7 +165,7 @@ def conv_bwd(d_y, x, weight, bias=None, initial_state=None, dfinal_state=None, *
         _dense(initial_state, "initial_state", x.dtype, window, dev)
     if dfinal_state is not None:
         _dense(dfinal_state, "dfinal_state", x.dtype, window, dev)
-    dx, dw = _empty(x.shape, dtype=x.dtype, device=x.device), _like(weight)
+    dx, dw = _like(x) if plain else x.new_empty(x.shape), _like(weight)
     out = dict(dx=dx, dw=dw)
     db = dh = None
     if bias is not None:
@@ -239,11 +239,11 @@ def _scan_call(x, dt, A, B, C, initial_state, skip, gate, dt_bias, softplus, out
     if initial_state is not None:
         _dense(initial_state, "initial_state", _F32, (n, D, N), dev)
     if out is None:
-        out = _like(x) if plain else _empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _like(x) if plain else x.new_empty(x.shape)
     else:
         plain &= _into(out, "out", x.dtype, x.shape, dev)
     if final_state is None:
-        final_state = _empty((n, D, N), dtype=_F32, device=x.device)
+        final_state = A.new_empty((n, D, N)) if initial_state is None else _like(initial_state)
     else:
         _dense(final_state, "final_state", _F32, (n, D, N), dev)
     st = _raw(dev)
@@ -304,7 +304,7 @@ def ssm_decode_step(x, dt, A, B, C, state, *, skip=None, gate=None, dt_bias=None
     nb = x.shape[0]
     _dense(state, "state", _F32, (nb, D, N), dev)
     if out is None:
-        out = _like(x) if plain else _empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _like(x) if plain else x.new_empty(x.shape)
     else:
         plain &= _into(out, "out", x.dtype, x.shape, dev)
     s = None
@@ -340,12 +340,13 @@ def ssm_chunk_bwd(d_y, x, dt, A, B, C, initial_state=None, dfinal_state=None, *,
         _dense(initial_state, "initial_state", _F32, (n, D, N), dev)
     if dfinal_state is not None:
         _dense(dfinal_state, "dfinal_state", _F32, (n, D, N), dev)
-    rows = lambda t: _empty(t.shape, dtype=x.dtype, device=x.device)  # noqa: E731
-    out = dict(dx=rows(x), ddt=rows(x), dA=_like(A), dB=rows(B), dC=rows(C))
+    rows = _like if plain else lambda t: t.new_empty(t.shape)
+    dx, dB = rows(x), rows(B)
+    out = dict(dx=dx, ddt=_like(dx), dA=_like(A), dB=dB, dC=_like(dB))
     if skip is not None:
         out["dskip"] = _like(skip)
     if gate is not None:
-        out["dgate"] = rows(x)
+        out["dgate"] = _like(dx)
     if dt_bias is not None:
         out["ddt_bias"] = _like(dt_bias)
     if initial_state is not None:
@@ -384,8 +385,8 @@ def beam_select(logits, scores, k=None, *, finished=None, eos=None, out=None, wo
             raise ValueError("finished beams need the token they go on with: eos")
     k = W if k is None else k
     if out is None:
-        out = (_empty((B, k), dtype=_F32, device=logits.device), _empty((B, k), dtype=_I32, device=logits.device),
-               _empty((B, k), dtype=_I32, device=logits.device))
+        tokens = _empty((B, k), dtype=_I32, device=logits.device)
+        out = (_like(scores) if k == W else scores.new_empty((B, k)), _like(tokens), tokens)
     else:
         for t, name, dtype in zip(out, ("out scores", "out parents", "out tokens"), (_F32, _I32, _I32)):
             _dense(t, name, dtype, (B, k), dev)
@@ -411,14 +412,15 @@ def beam_reorder(states, parents, *, stream=None):
     dev = _device(parents, "parents")
     _dense(parents, "parents", _I32, (B, W), dev)
     arrays = [states] if isinstance(states, torch.Tensor) else list(states)
-    n = len(arrays)
-    ptrs, sizes = (ctypes.c_void_p * n)(), (ctypes.c_longlong * n)()
+    n, rows, ptrs, sizes = len(arrays), B * W, [], []
     for i, t in enumerate(arrays):
         if not (t.is_contiguous() and t.get_device() == dev):
             _need(t, f"states[{i}]", t.dtype, t.shape, dev)
-        if not (t.dim() and (t.shape[0] == B * W or tuple(t.shape[:2]) == (B, W))):
-            raise ValueError(f"states[{i}] has shape {tuple(t.shape)}, expected [{B * W}, ...] or [{B}, {W}, ...]")
-        ptrs[i] = t.data_ptr()
-        sizes[i] = t.numel() // max(1, B * W) * t.element_size()
+        shape = t.shape
+        if not (shape and (shape[0] == rows or tuple(shape[:2]) == (B, W))):
+            raise ValueError(f"states[{i}] has shape {tuple(shape)}, expected [{rows}, ...] or [{B}, {W}, ...]")
+        ptrs.append(t.data_ptr())
+        sizes.append(t.nbytes // rows if rows else 0)
+    ptrs, sizes = (ctypes.c_void_p * n)(*ptrs), (ctypes.c_longlong * n)(*sizes)
     _ok(lib.kda_beam_reorder(ptrs, sizes, n, parents.data_ptr(), B, W, _raw(dev)), "kda_beam_reorder", lib)
     return states

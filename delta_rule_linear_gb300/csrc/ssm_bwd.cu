@@ -22,6 +22,7 @@
 // a time are walked again from it.
 #include <algorithm>
 
+#include "linear_tc.cuh"
 #include "ssm_internal.cuh"
 #include "ssm_math.cuh"
 
@@ -31,6 +32,7 @@ namespace {
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTile = 32;                   // tokens of a chunk
 constexpr float kLn2F = 0.6931471805599453f;
+constexpr int kPartC = 128;                 // floats from a part's dB to its dC
 
 template <typename T, int L> struct Lay {
     static constexpr int N = 4 * L, CL = 32 / L, CW = 2 * CL, CH = kWarps * CW;      // states; channel lanes, channels of a warp, of a CTA
@@ -213,7 +215,6 @@ __device__ __forceinline__ void bring(const Bwd &w, const At &at, int g, int d0,
         reinterpret_cast<float4 *>(heads)[threadIdx.x + j * kThreads] = make_float4(hq[j][0][0], hq[j][0][1], hq[j][1][0], hq[j][1][1]);
 }
 
-__device__ __forceinline__ Two pair_at(const float *p) { return *reinterpret_cast<const Two *>(p); }
 __device__ __forceinline__ Two ex2_2(Two x) {
     float a, b;
     each(x, a, b);
@@ -258,18 +259,22 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_bwd_local_kernel(const __grid
     float sum[2] = {0.f, 0.f};
 #pragma unroll 4
     for (int t = 0; t < kTile; ++t) {
-        const float *Bp = smem + t * Y::N + 4 * l, *Cp = Bp + kTile * Y::N, *rp = rows + (t * Y::CL + cl) * 12;
-        const Two B[2] = {pair_at(Bp), pair_at(Bp + 2)}, C[2] = {pair_at(Cp), pair_at(Cp + 2)};
+        const ulonglong2 B2 = *reinterpret_cast<const ulonglong2 *>(smem + t * Y::N + 4 * l);
+        const ulonglong2 C2 = *reinterpret_cast<const ulonglong2 *>(smem + (t + kTile) * Y::N + 4 * l);
+        const ulonglong2 *rp = reinterpret_cast<const ulonglong2 *>(rows) + (t * Y::CL + cl) * 3;
+        const ulonglong2 dt2 = rp[0], u2 = rp[1], p2 = rp[2];
+        const Two B[2] = {B2.x, B2.y}, C[2] = {C2.x, C2.y}, dt[2] = {dt2.x, dt2.y}, u[2] = {u2.x, u2.y}, p[2] = {p2.x, p2.y};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const Two dt = pair_at(rp + 2 * c), u = pair_at(rp + 4 + 2 * c), p = pair_at(rp + 8 + 2 * c);
-            sum[c] += rp[2 * c];
+            float d0, d1;
+            each(dt[c], d0, d1);
+            sum[c] += d0;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const Two f = ex2_2(mul2(dt, A[c][k]));
-                h[c][k] = fma2(f, h[c][k], mul2(u, B[k]));
+                const Two f = ex2_2(mul2(dt[c], A[c][k]));
+                h[c][k] = fma2(f, h[c][k], mul2(u[c], B[k]));
                 P[c][k] = mul2(P[c][k], f);
-                G[c][k] = fma2(P[c][k], mul2(p, C[k]), G[c][k]);
+                G[c][k] = fma2(P[c][k], mul2(p[c], C[k]), G[c][k]);
             }
         }
     }
@@ -435,6 +440,8 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_bwd_grad_kernel(const __grid_
                     was[k + 1][1][s] = fma2(f[k][1][s], was[k][1][s], mul2(u.y, B[s]));
                 }
             }
+            float *part = kept + max(q - 1, 0) * 256;       // 2 x 32 lanes x 4 values
+            __syncwarp();
             float r[8], sB[8], sA[8];       // token, channel
 #pragma unroll
             for (int k = 3; k >= 0; --k) {
@@ -465,20 +472,29 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_bwd_grad_kernel(const __grid_
                     sB[2 * k + c] = both(ss);
                     sA[2 * k + c] = both(sa);
                 }
-                float v[8];
-                each(dB[0], v[0], v[1]);
-                each(dB[1], v[2], v[3]);
-                each(dC[0], v[4], v[5]);
-                each(dC[1], v[6], v[7]);
-                using M = Meet<8, Y::CL, L>;
-                M::sum(v);
-                if (M::lead(cl)) {          // value j: B or C (j / 4), state 4 l + j % 4
+                // over the channels: every lane leaves its eight values, and takes a column of them (the memory that was kept
+                // for this part has been read)
+                ulonglong2 *to = reinterpret_cast<ulonglong2 *>(part) + lane;
+                to[0] = make_ulonglong2(dB[0], dB[1]);
+                to[kPartC / 4] = make_ulonglong2(dC[0], dC[1]);
+                __syncwarp();
+                constexpr int COLS = 8 * L;         // of the warp: B or C, state
 #pragma unroll
-                    for (int i = 0; i < M::LEFT; ++i) {
-                        const int j = M::first(cl) + i;
-                        sums[t * 2 * Y::N + (j >> 2) * Y::N + 4 * l + (j & 3)] = v[i];
+                for (int j = 0; j < (COLS + 31) / 32; ++j) {
+                    const int col = lane + 32 * j, n = col % Y::N;
+                    if (COLS >= 32 || col < COLS) {
+                        const float *from = part + col / Y::N * kPartC + n;
+                        float v[Y::CL];
+#pragma unroll
+                        for (int i = 0; i < Y::CL; ++i) v[i] = from[(i ^ col / Y::N) * 4 * L];     // dC's in another order: other banks
+#pragma unroll
+                        for (int half = Y::CL / 2; half; half /= 2)
+#pragma unroll
+                            for (int i = 0; i < half; ++i) v[i] += v[i + half];
+                        sums[t * 2 * Y::N + col] = v[0];
                     }
                 }
+                __syncwarp();
             }
             using M = Meet<8, L, 1>;
             M::sum(r);
@@ -628,9 +644,10 @@ template <typename T, int L, bool PAIRS> cudaError_t run(const Ssm &a, const Pla
     const long ctas = p.chunks * p.blocks;
     const int seq_blocks = (int)(((long)a.D * a.N + 255) / 256);
     if (ctas > 0x7fffffffL || (long)a.s.nseq * seq_blocks > 0x7fffffffL) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(ssm_bwd_local_kernel<T, L, PAIRS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Y::bytes(true));
+    static lin::SmemOnce local_once, grad_once;
+    cudaError_t e = local_once(ssm_bwd_local_kernel<T, L, PAIRS>, (int)Y::bytes(true));
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(ssm_bwd_grad_kernel<T, L, PAIRS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Y::bytes(false));
+    e = grad_once(ssm_bwd_grad_kernel<T, L, PAIRS>, (int)Y::bytes(false));
     if (e != cudaSuccess) return e;
     ssm_bwd_local_kernel<T, L, PAIRS><<<(unsigned)ctas, kThreads, Y::bytes(true), st>>>(w);
     ssm_bwd_chain_kernel<4 * L><<<dim3((unsigned)(a.s.nseq * seq_blocks), 2), 256, 0, st>>>(w, seq_blocks);
