@@ -52,6 +52,7 @@ ConvView conv_view(const void *p, const long long *s, int i, long N, long T, int
 kda_status conv_fwd(const void *x, const float *w, const float *bias, const void *h0, void *y, void *hT, const long long *strides,
                     const int *cu, int N, int T, long rows, int C, int K, kda_dtype dtype, int act, cudaStream_t st) {
     if (!w || (rows > 0 && (!x || !y))) return KDA_ERR_NULL;
+    if (rows > 0 && y == x) return KDA_ERR_UNSUPPORTED;     // rows are read by more runs than the one that writes them
     const unsigned e = size_of(dtype);
     if (!al(x, e) || !al(y, e) || !al(h0, e) || !al(hT, e) || !al(w, 4) || !al(bias, 4)) return KDA_ERR_ALIGN;
     if (N == 0) return KDA_OK;
@@ -88,6 +89,8 @@ struct SsmIn {
     const void *x, *dt, *B, *C, *gate;
     const float *A, *skip, *bias, *h0;
 };
+// An output in place of an input: a split sequence is read by two launches, of which the second writes.
+bool in_place(const void *y, const SsmIn &p, long rows) { return rows > 0 && (y == p.x || y == p.dt || (p.gate && y == p.gate)); }
 // The arrays that every call has; strides in the order x, dt, B, C, gate.
 kda_status ssm_in(Ssm &a, const SsmIn &p, const long long *s, const int *cu, int N, int T, long rows, int D, int G, int S,
                   kda_dtype dtype, int softplus) {
@@ -213,6 +216,7 @@ kda_status kda_ssm_chunk_fwd(const void *x, const void *dt, const float *A, cons
                softplus);
     if (c != KDA_OK) return c;
     if ((long)B * T > 0 && !y) return KDA_ERR_NULL;
+    if (in_place(y, {x, dt, B_in, C_in, gate, A, skip, dt_bias, initial_state}, (long)B * T)) return KDA_ERR_UNSUPPORTED;
     if (!al(y, size_of(dtype)) || !al(final_state, 16)) return KDA_ERR_ALIGN;
     if (!ws || ws_bytes < kda_ssm_chunk_fwd_workspace(B, T, D, G, N, dtype)) return KDA_ERR_WORKSPACE;
     if (!al(ws, 16)) return KDA_ERR_ALIGN;
@@ -239,6 +243,7 @@ kda_status kda_ssm_varlen_fwd(const void *x, const void *dt, const float *A, con
                dtype, softplus);
     if (c != KDA_OK) return c;
     if (total_T > 0 && !y) return KDA_ERR_NULL;
+    if (in_place(y, {x, dt, B_in, C_in, gate, A, skip, dt_bias, initial_state}, total_T)) return KDA_ERR_UNSUPPORTED;
     if (!al(y, size_of(dtype)) || !al(final_state, 16)) return KDA_ERR_ALIGN;
     if (!ws || ws_bytes < kda_ssm_varlen_fwd_workspace(nseq, total_T, D, G, N, dtype)) return KDA_ERR_WORKSPACE;
     if (!al(ws, 16)) return KDA_ERR_ALIGN;

@@ -558,6 +558,7 @@ kda_status kda_residual_norm_bwd(const void *d_n, const void *d_x_out, const voi
  * where tokens before the sequence come from its window, the last K - 1 tokens seen (zeros without one).
  *
  *   x, y    [B,T,C], KDA_F32 or KDA_BF16; weight [C,K] float32, 2 <= K <= 4; bias [C] float32 or NULL.
+ *           y must not overlap x (KDA_ERR_UNSUPPORTED where it is x).
  *   strides NULL: contiguous.  Otherwise four element strides (batch, token) of x, y, channels
  *           contiguous; any alignment of the element type (16-byte multiples run faster).
  *   initial_state, final_state   windows [B,K-1,C] of x's type, oldest token first, or NULL.  They may be
@@ -598,7 +599,7 @@ kda_status kda_conv_bwd(const void *d_y, const void *x, const float *weight, con
  *     y_t  = (C_t . h_t + skip x_t) silu(gate_t).
  *
  *   x, dt, gate, y   [B,T,D], KDA_F32 or KDA_BF16; gate NULL: none.  softplus 0: dt + dt_bias is used as
- *           it is.
+ *           it is.  y must not overlap the inputs (KDA_ERR_UNSUPPORTED where it is one of them).
  *   B_in, C_in       [B,T,G,N], the same type: channel d reads group d / (D / G).  N in {8, 16, 32, 64}.
  *   A [D,N], skip [D], dt_bias [D]   float32 (skip, dt_bias NULL: zeros); A finite, negative for a memory
  *           that decays.

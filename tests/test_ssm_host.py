@@ -99,18 +99,19 @@ P = lambda a=0x1000: ctypes.c_void_p(a)  # noqa: E731
 
 
 def test_conv_refusals(lib):
-    def f(x=P(), w=P(), b=None, h=None, y=P(), hT=None, B=2, T=5, C=6, K=4, dt=1, act=1):
+    def f(x=P(), w=P(), b=None, h=None, y=P(0x9000), hT=None, B=2, T=5, C=6, K=4, dt=1, act=1):
         return lib.kda_conv_fwd(x, w, b, h, y, hT, None, B, T, C, K, dt, act, None)
     assert f(x=None) == 1 and f(w=None) == 1 and f(y=None) == 1
     assert f(B=-1) == 2 and f(T=-1) == 2 and f(C=0) == 2 and f(K=0) == 2 and f(B=1 << 16, T=1 << 16) == 2
     assert f(dt=2) == 3
     assert f(K=5) == 4 and f(K=1) == 4 and f(act=2) == 4 and f(act=-1) == 4
     assert f(x=P(0x1001)) == 5 and f(w=P(0x1002)) == 5 and f(h=P(0x1001)) == 5 and f(b=P(0x1001)) == 5
+    assert f(y=P()) == 4                # in place
     assert f(B=0) == 0
 
     def v(host, N=3, total=10, cu=P()):
         hs = ctypes.cast((ctypes.c_int * len(host))(*host), ctypes.c_void_p)
-        return lib.kda_conv_varlen_fwd(P(), P(), None, cu, hs, None, P(), None, None, N, total, 6, 4, 1, 1, None)
+        return lib.kda_conv_varlen_fwd(P(), P(), None, cu, hs, None, P(0x9000), None, None, N, total, 6, 4, 1, 1, None)
     assert v([0, 4, 3, 10]) == 9 and v([1, 4, 6, 10]) == 9 and v([0, 4, 6, 9]) == 9 and v([0], N=0) == 9
     assert v([0, 4, 6, 10], cu=None) == 1 and v([0, 4, 6, 10], cu=P(0x1002)) == 5
 
@@ -128,7 +129,7 @@ def test_conv_refusals(lib):
 
 
 def test_ssm_refusals(lib):
-    base = dict(x=P(), dt=P(), A=P(), B=P(), C=P(), skip=None, gate=None, bias=None, h0=None, y=P(), hT=None, nb=2, T=5, D=12,
+    base = dict(x=P(), dt=P(), A=P(), B=P(), C=P(), skip=None, gate=None, bias=None, h0=None, y=P(0x9000), hT=None, nb=2, T=5, D=12,
                 G=2, N=16, code=1, ws=P(), n=1 << 50)
 
     def f(**kw):
@@ -143,11 +144,12 @@ def test_ssm_refusals(lib):
     assert f(x=P(0x1001)) == 5 and f(A=P(0x1008)) == 5 and f(h0=P(0x1004)) == 5 and f(hT=P(0x1008)) == 5 and f(ws=P(0x1008)) == 5
     assert f(gate=P(0x1001)) == 5 and f(skip=P(0x1002)) == 5
     assert f(ws=None) == 6 and f(n=8) == 6
+    assert f(y=P()) == 4 and f(gate=P(0x9000)) == 4         # in place
     assert f(nb=0) == 0
 
     def v(host, nseq=3, total=10, cu=P(), N=16):
         hs = ctypes.cast((ctypes.c_int * len(host))(*host), ctypes.c_void_p)
-        return lib.kda_ssm_varlen_fwd(P(), P(), P(), P(), P(), None, None, None, cu, hs, None, P(), None, None, nseq, total, 12, 2,
+        return lib.kda_ssm_varlen_fwd(P(), P(), P(), P(), P(), None, None, None, cu, hs, None, P(0x9000), None, None, nseq, total, 12, 2,
                                       N, 1, 1, P(), 1 << 50, None)
     assert v([0, 4, 3, 10]) == 9 and v([0, 4, 6, 9]) == 9 and v([0], nseq=0) == 9 and v([0, 4, 6, 10], cu=None) == 1
     assert v([0, 4, 6, 10], N=24) == 4
