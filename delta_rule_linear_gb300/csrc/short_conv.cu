@@ -177,7 +177,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) conv_fwd_ker
 #pragma unroll
         for (int u = 0; u < U; ++u) now[u] = next[u];
     }
-    for (; t < t1; ++t) one(t, get<T, V>(xp + t * a.x.t));
+    if (t < t1) {                       // what is left of the run, loaded together
+#pragma unroll
+        for (int u = 0; u < U - 1; ++u) now[u] = get<T, V>(xp + (t + u) * a.x.t, t + u < t1);
+#pragma unroll
+        for (int u = 0; u < U - 1; ++u)
+            if (t + u < t1) one(t + u, now[u]);
+    }
 }
 
 // A warp's lanes go over the items warp, warp + warps, ...; q of K rows and x of K rows in registers.
@@ -212,7 +218,9 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(Conv a) {
         // dx of row t - (K - 1) is whole once q_t is there; the first run goes on to the window's rows.  q of rows past
         // the run is formed here too (its share of the weights' gradients belongs to the next run).
         const int last = t1 + K - 1;
-        auto one = [&](int tt, const Few<T, V> &xr, const Few<T, V> &gr) {
+        // INNER: a row of the run whose dx row is of the run too, which needs no condition
+        auto one = [&](int tt, const Few<T, V> &xr, const Few<T, V> &gr, auto inner) {
+            constexpr bool INNER = decltype(inner)::value;
 #pragma unroll
             for (int j = 0; j + 1 < K; ++j) {
                 x[j] = x[j + 1];
@@ -234,38 +242,53 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(Conv a) {
                     g[i] *= fmaf(p[i] * s, rest, s);
                 }
             }
+            if (!INNER) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) g[i] = tt < it.len ? g[i] : 0.f;
+                for (int i = 0; i < V; ++i) g[i] = tt < it.len ? g[i] : 0.f;
+            }
             q[K - 1].set(g);
-            if (tt < t1) {
+            if (INNER || tt < t1) {
                 db.add(q[K - 1]);
 #pragma unroll
                 for (int j = 0; j < K; ++j) dw[j].fma(q[K - 1], x[j]);
             }
             const int row = tt - (K - 1);
-            if (row >= t0 || (t0 == 0 && a.dh0)) {
-                const int tail = row - (it.len - (K - 1));        // its row of the next window
-                Ch<V> d = open<T, V>(get<T, V>(static_cast<const T *>(a.dhT) + win + (long)tail * a.C, a.dhT && tail >= 0));
+            if (INNER || row >= t0 || (t0 == 0 && a.dh0)) {
+                Ch<V> d = zeros<V>();
+                if (!INNER && a.dhT && tt >= it.len)        // a row of the next window
+                    d = open<T, V>(get<T, V>(static_cast<const T *>(a.dhT) + win + (long)(tt - it.len) * a.C));
 #pragma unroll
                 for (int j = 0; j < K; ++j) d.fma(w[j], q[K - 1 - j]);
                 float o[V];
                 d.get(o);
-                put<T, V>(row >= 0 ? dp + row * a.dx.t : static_cast<T *>(a.dh0) + win + (long)(row + K - 1) * a.C, o);
+                put<T, V>(INNER || row >= 0 ? dp + row * a.dx.t : static_cast<T *>(a.dh0) + win + (long)(row + K - 1) * a.C, o);
             }
         };
-        constexpr int U = sizeof(T) == 2 ? 8 : 4;       // rows of x and d_y in flight
-        int t = t0;
-        for (const int whole = min(last, it.len); t + U <= whole; t += U) {
-            Few<T, V> xr[U], gr[U];
+        // n rows from t on, loaded together
+        constexpr int U = sizeof(T) == 2 ? 6 : 4;
+        auto some = [&](int t, int n, auto most, auto inner) {
+            constexpr int MOST = decltype(most)::value;
+            Few<T, V> xr[MOST], gr[MOST];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                xr[u] = get<T, V>(xp + (t + u) * a.x.t);
-                gr[u] = get<T, V>(gp + (t + u) * a.y.t);
+            for (int u = 0; u < MOST; ++u) {
+                const bool there = u < n && (decltype(inner)::value || t + u < it.len);
+                xr[u] = get<T, V>(xp + (t + u) * a.x.t, there);
+                gr[u] = get<T, V>(gp + (t + u) * a.y.t, there);
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) one(t + u, xr[u], gr[u]);
-        }
-        for (; t < last; ++t) one(t, get<T, V>(xp + t * a.x.t, t < it.len), get<T, V>(gp + t * a.y.t, t < it.len));
+            for (int u = 0; u < MOST; ++u)
+                if (u < n) one(t + u, xr[u], gr[u], inner);
+        };
+        const std::true_type inner;
+        const std::false_type edge;
+        const std::integral_constant<int, K - 1> few;
+        const std::integral_constant<int, U> many;
+        some(t0, K - 1, few, edge);             // (of a short run: rows behind it)
+        int t = t0 + K - 1;
+        for (; t + U <= t1; t += U) some(t, U, many, inner);
+        if (t < t1) some(t, t1 - t, many, inner);
+        t = max(t1, t0 + K - 1);
+        some(t, last - t, few, edge);
     }
     // the CTA's sums, in the order of its warps: 4 + 4 (two rounds), then the partial row
     const long row = (long)blockIdx.y * a.C * (K + 1);
@@ -345,17 +368,21 @@ constexpr int kLane = 4;            // channels of a lane where everything is al
 template <typename T> bool by4(const void *p) { return reinterpret_cast<uintptr_t>(p) % (kLane * sizeof(T)) == 0; }
 template <typename T> bool vec_view(const ConvView &v) { return by4<T>(v.p) && v.b % kLane == 0 && v.t % kLane == 0; }
 
-// Tokens of a run: long ones share few rows with the next, but the launch needs about a thousand lanes per SM.
-int pick_run(const Conv &a, int V, long rows, int lanes_per_sm) {
-    const long vecs = (a.C + V - 1) / V;
-    int run = 32;
-    while (run > 4 && rows * vecs / run < (long)lanes_per_sm * a.sms) run /= 2;
-    return run;
+// Tokens of a run: so many that the warps that stay resident (ctas to an SM) have one each, or the same number of them where
+// they would pass 64 tokens; a last round of few warps would take as long as a full one (2 x 2048 tokens of 4096 channels in runs
+// of 16 and 32: forwards 17.0, backwards 41 us; in runs of 27 and 57: @F and @B).
+int pick_run(const Conv &a, int V, long rows, int ctas) {
+    const long blocks = (a.C + 32 * V - 1) / (32 * V), warps = std::max(1L, (long)ctas * a.sms / blocks) * kWarps;
+    const long most = warps * ((rows + warps * 64 - 1) / (warps * 64));         // runs
+    long run = std::max(8L, most ? (rows + most - 1) / most : 0);
+    if (!a.s.cu)
+        while (run < 64 && a.s.nseq * ((a.s.T + run - 1) / run) > most) ++run;   // sequences end in runs of their own
+    return (int)run;
 }
 
 template <typename T, int V, int K> cudaError_t run_fwd(Conv a, cudaStream_t st) {
     const long rows = a.s.cu ? a.total : (long)a.s.nseq * a.s.T;
-    a.run = pick_run(a, V, rows, 1536);
+    a.run = pick_run(a, V, rows, sizeof(T) == 2 ? 4 : 3);
     a.items = lin_items(a.s.nseq, a.s.cu ? a.total : a.s.T, a.s.cu ? (int)a.total : a.s.T, a.s.cu != nullptr, a.run);
     a.blocks = (a.C + 32 * V - 1) / (32 * V);
     const long ctas = (a.items + kWarps - 1) / kWarps * a.blocks;
@@ -369,7 +396,7 @@ template <typename T, int V, int K> cudaError_t run_fwd(Conv a, cudaStream_t st)
 
 template <typename T, int V, int K> cudaError_t run_bwd(Conv a, cudaStream_t st) {
     const long rows = a.s.cu ? a.total : (long)a.s.nseq * a.s.T;
-    a.run = pick_run(a, V, rows, 512);
+    a.run = pick_run(a, V, rows, 2);
     a.items = lin_items(a.s.nseq, a.s.cu ? a.total : a.s.T, a.s.cu ? (int)a.total : a.s.T, a.s.cu != nullptr, a.run);
     const unsigned cb = (a.C + 32 * V - 1) / (32 * V);
     const long want = (long)std::max(1, std::min(conv_parts(a.C, a.sms), 4 * a.sms / (int)cb));
