@@ -168,18 +168,11 @@ __device__ __forceinline__ double log_sum(double s) {
     }
     const double d = f + 1.0;
     double q = 1.0f / (float)d;
-    q = q * (2.0 - d * q);
-    q = q * (2.0 - d * q);
-    const double r = (f - 1.0) * q, r2 = r * r;
-    double p = 1.0 / 15;
-    p = p * r2 + 1.0 / 13;
-    p = p * r2 + 1.0 / 11;
-    p = p * r2 + 1.0 / 9;
-    p = p * r2 + 1.0 / 7;
-    p = p * r2 + 1.0 / 5;
-    p = p * r2 + 1.0 / 3;
-    p = p * r2 + 1.0;
-    return 2.0 * r * p + n * 0.69314718055994530942;
+    q = q * (2.0 - d * q);                  // 2^-46
+    const double r = (f - 1.0) * q, r2 = r * r, r4 = r2 * r2;
+    // the series in pairs: every operation of the chain takes as long as dozens in fp32
+    const double p = (1.0 + r2 * (1.0 / 3)) + r4 * ((1.0 / 5 + r2 * (1.0 / 7)) + r4 * ((1.0 / 9 + r2 * (1.0 / 11)) + r4 * (1.0 / 13 + r2 * (1.0 / 15))));
+    return (r + r) * p + n * 0.69314718055994530942;
 }
 
 // A candidate's place in the order: larger totals first, then lower indices.
@@ -265,8 +258,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(BeamSelect a) {
             double sum = 0.0;
             for (int i = lane; i < a.splits; i += 32)      // a part of -inf alone has a sum of 0
                 sum += s[i].max == m || s[i].max == -INFINITY ? s[i].sum : s[i].sum * (double)exp2f((s[i].max - m) * 1.4426950408889634f);
-#pragma unroll
-            for (int q = 16; q; q >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, q);
+            for (int q = 1; q < 32 && q < a.splits; q <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, q);
             o.hi = -INFINITY;
             if (m > -INFINITY && m < INFINITY && sum < INFINITY && score > -INFINITY && score < INFINITY) {
                 const double t = (double)score - ((double)m + log_sum(sum));

@@ -331,7 +331,7 @@ template <int N> __global__ void __launch_bounds__(256) ssm_bwd_chain_kernel(con
     const float *start = back ? a.dhT : a.h0;
     float v = start ? start[n * DN + e] : 0.f;
     float *arr = (back ? w.g : w.h) + e;
-    constexpr int U = 8;
+    constexpr int U = 16;
     for (int i0 = 0; i0 < cnt; i0 += U) {
         float x[U], s[U];
 #pragma unroll
