@@ -1,8 +1,8 @@
 // beam.cu -- beam search: the k best continuations of a request's W beams, and the recurrent memories that follow them.
 //
 // Selection: total[w, v] = score_w + x_w[v] - lse_w, lse_w = log sum_v exp(x_w[v]); the k largest over all (w, v), ties to
-// the lowest w V + v.  The logits are read once: a warp takes a chunk of 1024 consecutive ones, keeps the chunk's maximum
-// and adds up exp(x - M) against the running maximum M of its chunks.  An element among the k best lies in one of the k
+// the lowest w V + v.  The logits are read once: a warp takes 1024 consecutive ones at a time, keeps the maxima of their
+// two chunks of 512 and adds up exp(x - M) against the running maximum M of its chunks.  An element among the k best lies in one of the k
 // chunks that come first when chunks are ordered by (maximum, position): every chunk before its own holds an element that
 // comes before it.  So the second kernel, a CTA per request, orders the chunks' maxima and looks at k chunks only.
 // Totals are formed and compared as pairs of fp32, 48 bits (candidates of different beams may be closer than an fp32 total's
@@ -56,12 +56,12 @@ __device__ __forceinline__ uint4 from_byte(uint4 lo, uint4 hi, int bytes) {
                       __funnelshift_r(w[3], w[4], bits));
 }
 
-// Chunk j of a row, 16 bytes per lane and i: elements j 1024 + (32 i + lane) V on, whatever the row's address is, so that
+// 1024 elements of a row, 16 bytes per lane and i: elements j 1024 + (32 i + lane) V on, whatever the row's address is, so that
 // equal rows give equal sums.  A row off the 16-byte boundary is read from the boundary before it and shifted, with the
 // next lane's bytes.
 template <typename T, int V, int NI> __device__ __forceinline__ void get_chunk(const T *p, int j, int n, typename Pack<T, V>::Raw (&r)[NI]) {
     const int lane = threadIdx.x & 31, off = (int)(reinterpret_cast<uintptr_t>(p) % 16);
-    const long e = (long)j * kBeamChunk - off / (int)sizeof(T) + lane * V;
+    const long e = (long)j * kBeamTake - off / (int)sizeof(T) + lane * V;
 #pragma unroll
     for (int i = 0; i < NI; ++i) r[i].w[0] = get_some<T, V>(p, e + i * 32 * V, n);
     if (!off) return;
@@ -83,7 +83,7 @@ template <typename T, int V, int NI> __device__ __forceinline__ void get_chunk(c
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) beam_scan_kernel(BeamSelect a) {
-    constexpr int V = 16 / sizeof(T), NI = kBeamChunk / (32 * V);
+    constexpr int V = 16 / sizeof(T), NI = kBeamTake / (32 * V);
     constexpr float kLog2e = 1.4426950408889634f;
     __shared__ float sm[kWarps], ss[kWarps];
     next_may_start();
@@ -92,19 +92,24 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(BeamSelect a) {
     if (a.finished && a.finished[row]) return;
     const T *p = row_of<T>(a, b, w);
     float M = -INFINITY, S = 0.f;
-    for (int j = split * kWarps + warp; j < a.nc; j += a.splits * kWarps) {
+    const int takes = (a.V + kBeamTake - 1) / kBeamTake;
+    for (int j = split * kWarps + warp; j < takes; j += a.splits * kWarps) {
         typename Pack<T, V>::Raw r[NI];
         get_chunk<T, V, NI>(p, j, a.V, r);
-        float m = -INFINITY, x[V];
+        float half[2] = {-INFINITY, -INFINITY}, x[V];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             Pack<T, V>::open(r[i], x);
 #pragma unroll
-            for (int k = 0; k < V; ++k) m = fmaxf(m, x[k]);
+            for (int k = 0; k < V; ++k) half[2 * i / NI] = fmaxf(half[2 * i / NI], x[k]);
         }
+        // lanes of the upper half go on with the second chunk's maximum
+        const bool up = lane & 16;
+        float m = fmaxf(up ? half[1] : half[0], __shfl_xor_sync(0xffffffffu, up ? half[0] : half[1], 16));
 #pragma unroll
-        for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        if (lane == 0) a.cmax[(long)row * a.nc + j] = m;
+        for (int off = 8; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        if ((lane & 15) == 0) a.cmax[(long)row * a.nc + 2 * j + (lane >> 4)] = m;
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
         const float now = fmaxf(M, m), ref = now == -INFINITY ? 0.f : now;    // nothing but -inf so far: sums of 0
         float add = 0.f;
 #pragma unroll
@@ -245,20 +250,22 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(BeamSelect a) {
     __shared__ Cand other[kPickWarps / 2 * 32], top[kBeamMax];
     const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x / 32, k = a.k;
     wait_for_previous();
-    for (int w = warp; w < a.W; w += kPickWarps) {
+    if ((int)threadIdx.x < a.W) {           // a beam each
+        const int w = threadIdx.x;
         const long row = (long)b * a.W + w;
         const float score = a.scores[row];
         Off o{score, 0.f};
         if (!(a.finished && a.finished[row])) {
             const BeamSum *s = a.sums + row * a.splits;
             float m = -INFINITY;
-            for (int i = lane; i < a.splits; i += 32) m = fmaxf(m, s[i].max);
-#pragma unroll
-            for (int q = 16; q; q >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, q));
+#pragma unroll 4
+            for (int i = 0; i < a.splits; ++i) m = fmaxf(m, s[i].max);
             double sum = 0.0;
-            for (int i = lane; i < a.splits; i += 32)      // a part of -inf alone has a sum of 0
-                sum += s[i].max == m || s[i].max == -INFINITY ? s[i].sum : s[i].sum * (double)exp2f((s[i].max - m) * 1.4426950408889634f);
-            for (int q = 1; q < 32 && q < a.splits; q <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, q);
+#pragma unroll 4
+            for (int i = 0; i < a.splits; ++i) {        // a part of -inf alone has a sum of 0
+                const float part = s[i].max;
+                sum += part == m || part == -INFINITY ? s[i].sum : s[i].sum * (double)exp2f((part - m) * 1.4426950408889634f);
+            }
             o.hi = -INFINITY;
             if (m > -INFINITY && m < INFINITY && sum < INFINITY && score > -INFINITY && score < INFINITY) {
                 const double t = (double)score - ((double)m + log_sum(sum));
@@ -267,7 +274,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(BeamSelect a) {
             }
         }
         if (!(o.hi == o.hi)) o.hi = -INFINITY;
-        if (lane == 0) off[w] = o;
+        off[w] = o;
     }
     __syncthreads();
     const unsigned long long none = key_of(-INFINITY, 0.f);
@@ -275,22 +282,46 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(BeamSelect a) {
     // the k first chunks
     WarpList l;
     const int nall = a.W * a.nc;
-    for (int i0 = warp * 32; i0 < nall || i0 == warp * 32; i0 += kPickThreads) {
-        const int i = i0 + lane;
-        Cand x{0, 0xffffffffu};
-        if (i < nall) {
-            const int w = i / a.nc, j = i - w * a.nc;
-            x.at = i;
-            x.key = none;
+    constexpr int AT_ONCE = 4;              // maxima of a lane, loaded together
+    bool first = true;
+    for (int i0 = warp * 32; first || i0 < nall; i0 += AT_ONCE * kPickThreads) {
+        Cand x[AT_ONCE];
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+            const int i = i0 + u * kPickThreads + lane, w = i / a.nc, j = i - w * a.nc;
+            x[u] = {0, 0xffffffffu};
+            if (i >= nall || j * kBeamChunk >= a.V) continue;       // (a row's last chunk may hold nothing)
+            x[u].at = i;
             if (done(w))
-                x.key = a.eos / kBeamChunk == j ? key_of(off[w].hi, off[w].lo) : none;
-            else if (off[w].hi > -INFINITY)
-                x.key = key_of(off[w], a.cmax[((long)b * a.W + w) * a.nc + j]);
+                x[u].key = a.eos / kBeamChunk == j ? key_of(off[w].hi, off[w].lo) : none;
+            else
+                x[u].key = off[w].hi > -INFINITY ? key_of(off[w], a.cmax[((long)b * a.W + w) * a.nc + j]) : none;
         }
-        if (i0 == warp * 32)
-            l.start(x);
+        // a lane's best first: what comes after the lanes' best ones is seldom wanted
+        auto order = [&](Cand &p, Cand &q) {
+            if (before(q, p)) {
+                const Cand t = p;
+                p = q;
+                q = t;
+            }
+        };
+        order(x[0], x[1]);
+        order(x[2], x[3]);
+        order(x[0], x[2]);
+        order(x[1], x[3]);
+        order(x[1], x[2]);
+        if (first)
+            l.start(x[0]);
         else
-            l.take(x.key != 0, x, k);
+            l.take(x[0].key != 0, x[0], k);
+        first = false;
+#pragma unroll 1
+        for (int u = 1; u < AT_ONCE; ++u) {
+            x[0] = x[1];
+#pragma unroll
+            for (int q = 1; q + 1 < AT_ONCE; ++q) x[q] = x[q + 1];
+            l.take(x[0].key != 0, x[0], k);
+        }
     }
     join(l, other);
     if (threadIdx.x < k) top[threadIdx.x] = l.c;

@@ -8,7 +8,8 @@ namespace kda {
 
 constexpr int kBeamMax = 32;        // beams kept (k) and beams reordered at most
 constexpr int kBeamsIn = 128;       // beams selected from at most
-constexpr int kBeamChunk = 1024;    // logits of a chunk (one warp at a time)
+constexpr int kBeamChunk = 512;     // logits of a chunk
+constexpr int kBeamTake = 1024;     // logits that a warp takes at a time: two chunks
 constexpr int kBeamStates = 32;     // arrays of a reordering launch
 
 // Part of a row: its largest logit and the sum of exp(x - max).
@@ -32,8 +33,9 @@ struct BeamSelect {
     int nc, splits;
     int sms;
 };
-inline int beam_chunks(int V) { return (int)(((long)V + kBeamChunk - 1) / kBeamChunk); }
-int beam_splits(long rows, int nc, int sms);
+inline int beam_takes(int V) { return (int)(((long)V + kBeamTake - 1) / kBeamTake); }
+inline int beam_chunks(int V) { return beam_takes(V) * (kBeamTake / kBeamChunk); }      // (the last may be empty)
+int beam_splits(long rows, int takes, int sms);
 cudaError_t launch_beam_select(const BeamSelect &a, cudaStream_t st);
 
 struct BeamReorder {

@@ -336,7 +336,7 @@ size_t kda_beam_select_workspace(int B, int W, int V, kda_dtype dtype) {
     if (beam_shape(B, W, V, 1, dtype) != KDA_OK) return 0;
     const long rows = (long)B * W;
     const int nc = beam_chunks(V);
-    return kLeast + rows * beam_splits(rows, nc, kSms) * sizeof(BeamSum) + (size_t)rows * nc * 4;
+    return kLeast + rows * beam_splits(rows, beam_takes(V), kSms) * sizeof(BeamSum) + (size_t)rows * nc * 4;
 }
 
 kda_status kda_beam_select(const void *logits, const long long *strides, const float *scores, const unsigned char *finished,
@@ -358,7 +358,7 @@ kda_status kda_beam_select(const void *logits, const long long *strides, const f
     a.B = B; a.W = W; a.V = V; a.k = k; a.eos = eos; a.dtype = to_dtype(dtype); a.sms = kSms;
     const long rows = (long)B * W;
     a.nc = beam_chunks(V);
-    a.splits = beam_splits(rows, a.nc, kSms);
+    a.splits = beam_splits(rows, beam_takes(V), kSms);
     a.sums = static_cast<BeamSum *>(ws);
     a.cmax = reinterpret_cast<float *>(a.sums + rows * a.splits);
     return done(launch_beam_select(a, reinterpret_cast<cudaStream_t>(stream)));

@@ -220,3 +220,13 @@ def test_reorder_refusals(kda):
         kda.beam_select(torch.zeros(1, 1, 4, device="cuda"), torch.zeros(1, 1, device="cuda"), 5)
     with pytest.raises(ValueError):
         kda.beam_select(torch.zeros(1, 1, 4, device="cuda"), torch.zeros(1, 1, device="cuda"), finished=torch.zeros(1, 1, dtype=torch.bool, device="cuda"))
+
+
+@pytest.mark.parametrize("V", [1, 3, 512, 513, 1025])
+def test_many_beams_that_do_not_count(kda, V):
+    """Nothing but -inf, or a few beams that count: the lowest indices follow, also where a row's last chunk is empty."""
+    import torch
+    x, s = _logits(2, 64, V, "f32")
+    s[0] = float("-inf")
+    s[1, 5:] = float("-inf")
+    _compare(kda, x, s, 32)
