@@ -17,21 +17,9 @@ _CONV_ACT = {None: 0, "silu": 1}
 _I32 = torch.int32
 
 
-# The library, the current device and stream and a call's workspace, as _linear finds them.
-def load():
-    return _linear.load()
-
-
-def _device(t, name):
-    return _linear._device(t, name)
-
-
-def _raw(dev):
-    return _linear._raw(dev)
-
-
-def _ws(query, sizes, t, stream, workspace, asked=False):
-    return _linear._ws(query, sizes, t, stream, workspace, asked)
+# The calls below cost the GPU a few microseconds where inputs are small, so what they check on the way is a handful of
+# comparisons; what fails one goes through _need, which finds the words.  The library, the current device and stream and
+# a call's workspace are _linear's.
 
 
 def _longs(*xs):
@@ -63,8 +51,8 @@ def _conv_args(x, weight, bias, activation):
     if act is None:
         raise ValueError("a convolution's activation must be 'silu' or None")
     C, K = x.shape[-1], weight.shape[-1]
-    dt, dev = _code(x, "x"), _device(x, "x")
-    plain = _view(x, "x", x.dtype, x.shape, dev)
+    dt, dev = _code(x, "x"), _linear._device(x, "x")
+    plain = x.is_contiguous() or _view(x, "x", x.dtype, x.shape, dev)
     _dense(weight, "weight", _F32, (C, K), dev)
     if bias is not None:
         _dense(bias, "bias", _F32, (C,), dev)
@@ -72,7 +60,7 @@ def _conv_args(x, weight, bias, activation):
 
 
 def _conv_call(x, weight, bias, initial_state, activation, out, final_state, cu, cu_cpu):
-    lib = load()
+    lib = _linear.load()
     if x.dim() != 3:
         raise ValueError("x must be [B, T, C]")
     act, dt, dev, plain, C, K = _conv_args(x, weight, bias, activation)
@@ -95,9 +83,9 @@ def _conv_call(x, weight, bias, initial_state, activation, out, final_state, cu,
     s = None if plain else _longs(x.stride(0), x.stride(1), out.stride(0), out.stride(1))
     a, z = (x.data_ptr(), weight.data_ptr(), _ptr(bias)), (_ptr(initial_state), out.data_ptr(), final_state.data_ptr(), s)
     if cu is None:
-        _ok(lib.kda_conv_fwd(*a, *z, B, T, C, K, dt, act, _raw(dev)), "kda_conv_fwd", lib)
+        _ok(lib.kda_conv_fwd(*a, *z, B, T, C, K, dt, act, _linear._raw(dev)), "kda_conv_fwd", lib)
     else:
-        _ok(lib.kda_conv_varlen_fwd(*a, cu.data_ptr(), _ptr(host), *z, n, T, C, K, dt, act, _raw(dev)), "kda_conv_varlen_fwd", lib)
+        _ok(lib.kda_conv_varlen_fwd(*a, cu.data_ptr(), _ptr(host), *z, n, T, C, K, dt, act, _linear._raw(dev)), "kda_conv_varlen_fwd", lib)
     return out, final_state
 
 
@@ -126,7 +114,7 @@ def conv_decode_step(x, weight, state, bias=None, *, activation="silu", out=None
     in place.  x [B,C] or [B,1,C].  Returns y with x's shape."""
     if stream is not None:
         return _on(stream, conv_decode_step, x, weight, state, bias, activation=activation, out=out)
-    lib = load()
+    lib = _linear.load()
     if x.dim() not in (2, 3) or (x.dim() == 3 and x.shape[1] != 1):
         raise ValueError("x must be [B, C] or [B, 1, C]")
     act, dt, dev, plain, C, K = _conv_args(x, weight, bias, activation)
@@ -138,7 +126,7 @@ def conv_decode_step(x, weight, state, bias=None, *, activation="silu", out=None
         plain &= _into(out, "out", x.dtype, x.shape, dev)
     s = None if plain else _longs(x.stride(0), out.stride(0))
     _ok(lib.kda_conv_decode_step(x.data_ptr(), weight.data_ptr(), _ptr(bias), state.data_ptr(), out.data_ptr(), s, B, C, K, dt,
-                                 act, _raw(dev)), "kda_conv_decode_step", lib)
+                                 act, _linear._raw(dev)), "kda_conv_decode_step", lib)
     return out
 
 
@@ -150,7 +138,7 @@ def conv_bwd(d_y, x, weight, bias=None, initial_state=None, dfinal_state=None, *
     if stream is not None:
         return _on(stream, conv_bwd, d_y, x, weight, bias, initial_state, dfinal_state, cu_seqlens=cu_seqlens,
                    activation=activation, workspace=workspace)
-    lib = load()
+    lib = _linear.load()
     if x.dim() != 3:
         raise ValueError("x must be [B, T, C]")
     act, dt, dev, plain, C, K = _conv_args(x, weight, bias, activation)
@@ -172,8 +160,8 @@ def conv_bwd(d_y, x, weight, bias=None, initial_state=None, dfinal_state=None, *
         db = out["dbias"] = _like(bias)
     if initial_state is not None:
         dh = out["dstate"] = _like(initial_state)
-    st = _raw(dev)
-    ws, size = _ws("kda_conv_bwd_workspace", (C, K), x, st, workspace)
+    st = _linear._raw(dev)
+    ws, size = _linear._ws("kda_conv_bwd_workspace", (C, K), x, st, workspace)
     s = None if plain else _longs(x.stride(0), x.stride(1), d_y.stride(0), d_y.stride(1), T * C, C)
     _ok(lib.kda_conv_bwd(d_y.data_ptr(), x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(initial_state), _ptr(dfinal_state),
                          dx.data_ptr(), dw.data_ptr(), _ptr(db), _ptr(dh), _ptr(cu_seqlens), s, n, T, C, K, dt, act,
@@ -194,22 +182,30 @@ def _heads(t, name, dtype, lead, dev, N):
 
 def _scan_args(x, dt, A, B, C, skip, gate, dt_bias, dev):
     """Checks what every scan call has; (D, G, N, whether all is contiguous)."""
-    lead, D, dtype = x.shape[:-1], x.shape[-1], x.dtype
+    shape, dtype = x.shape, x.dtype
+    D = shape[-1]
     if A.dim() != 2:
         raise ValueError("A must be [D, N]")
     N = A.shape[1]
-    plain = _view(x, "x", dtype, x.shape, dev) & _view(dt, "dt", dtype, x.shape, dev)
+    heads = B.shape
+    G = heads[-2] if len(heads) == len(shape) + 1 else 1
+    plain = (x.is_contiguous() and dt.is_contiguous() and B.is_contiguous() and C.is_contiguous() and dt.dtype is dtype and
+             B.dtype is dtype and C.dtype is dtype and dt.get_device() == dev and B.get_device() == dev and C.get_device() == dev and
+             dt.shape == shape and C.shape == heads and heads[-1] == N and heads[:-1] == (shape[:-1] if G == 1 and len(heads) == len(shape)
+                                                                                          else (*shape[:-1], G)))
+    if not plain:
+        plain = _view(x, "x", dtype, shape, dev) & _view(dt, "dt", dtype, shape, dev)
+        G, p = _heads(B, "B", dtype, shape[:-1], dev, N)
+        plain &= p
+        G2, p = _heads(C, "C", dtype, shape[:-1], dev, N)
+        plain &= p
+        if G2 != G or B.dim() != C.dim():
+            raise ValueError(f"C has shape {tuple(C.shape)}, expected B's {tuple(B.shape)}")
     _dense(A, "A", _F32, (D, N), dev)
-    G, p = _heads(B, "B", dtype, lead, dev, N)
-    plain &= p
-    G2, p = _heads(C, "C", dtype, lead, dev, N)
-    plain &= p
-    if G2 != G or B.dim() != C.dim():
-        raise ValueError(f"C has shape {tuple(C.shape)}, expected B's {tuple(B.shape)}")
     if G == 0 or D % G:
         raise ValueError(f"the channels ({D}) must be a multiple of the groups ({G})")
     if gate is not None:
-        plain &= _view(gate, "gate", dtype, x.shape, dev)
+        plain &= _view(gate, "gate", dtype, shape, dev)
     if skip is not None:
         _dense(skip, "skip", _F32, (D,), dev)
     if dt_bias is not None:
@@ -227,10 +223,10 @@ def _scan_strides(*ts):
 
 
 def _scan_call(x, dt, A, B, C, initial_state, skip, gate, dt_bias, softplus, out, final_state, workspace, check, cu, cu_cpu):
-    lib = load()
+    lib = _linear.load()
     if x.dim() != 3:
         raise ValueError("x must be [B, T, D]")
-    code, dev = _code(x, "x"), _device(x, "x")
+    code, dev = _code(x, "x"), _linear._device(x, "x")
     D, G, N, plain = _scan_args(x, dt, A, B, C, skip, gate, dt_bias, dev)
     n, T, host = x.shape[0], x.shape[1], None
     if cu is not None:
@@ -246,15 +242,15 @@ def _scan_call(x, dt, A, B, C, initial_state, skip, gate, dt_bias, softplus, out
         final_state = A.new_empty((n, D, N)) if initial_state is None else _like(initial_state)
     else:
         _dense(final_state, "final_state", _F32, (n, D, N), dev)
-    st = _raw(dev)
+    st = _linear._raw(dev)
     s = None if plain else _scan_strides(x, dt, B, C, gate, out)
     a = (x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(skip), _ptr(gate), _ptr(dt_bias))
     if cu is None:
-        ws, size = _ws("kda_ssm_chunk_fwd_workspace", (n, T, D, G, N, code), x, st, workspace, check)
+        ws, size = _linear._ws("kda_ssm_chunk_fwd_workspace", (n, T, D, G, N, code), x, st, workspace, check)
         _ok(lib.kda_ssm_chunk_fwd(*a, _ptr(initial_state), out.data_ptr(), final_state.data_ptr(), s, n, T, D, G, N, code,
                                   int(softplus), ws.data_ptr(), size, st), "kda_ssm_chunk_fwd", lib)
     else:
-        ws, size = _ws("kda_ssm_varlen_fwd_workspace", (n, T, D, G, N, code), x, st, workspace, check)
+        ws, size = _linear._ws("kda_ssm_varlen_fwd_workspace", (n, T, D, G, N, code), x, st, workspace, check)
         _ok(lib.kda_ssm_varlen_fwd(*a, cu.data_ptr(), _ptr(host), _ptr(initial_state), out.data_ptr(), final_state.data_ptr(), s,
                                    n, T, D, G, N, code, int(softplus), ws.data_ptr(), size, st), "kda_ssm_varlen_fwd", lib)
     if check and n:        # an empty batch launches nothing and leaves the header as it is
@@ -296,10 +292,10 @@ def ssm_decode_step(x, dt, A, B, C, state, *, skip=None, gate=None, dt_bias=None
     if stream is not None:
         return _on(stream, ssm_decode_step, x, dt, A, B, C, state, skip=skip, gate=gate, dt_bias=dt_bias, softplus=softplus,
                    out=out)
-    lib = load()
+    lib = _linear.load()
     if x.dim() not in (2, 3) or (x.dim() == 3 and x.shape[1] != 1):
         raise ValueError("x must be [B, D] or [B, 1, D]")
-    code, dev = _code(x, "x"), _device(x, "x")
+    code, dev = _code(x, "x"), _linear._device(x, "x")
     D, G, N, plain = _scan_args(x, dt, A, B, C, skip, gate, dt_bias, dev)
     nb = x.shape[0]
     _dense(state, "state", _F32, (nb, D, N), dev)
@@ -313,7 +309,7 @@ def ssm_decode_step(x, dt, A, B, C, state, *, skip=None, gate=None, dt_bias=None
         s = _longs(x.stride(0), dt.stride(0), B.stride(0), group(B), C.stride(0), group(C),
                    (x if gate is None else gate).stride(0), out.stride(0))
     _ok(lib.kda_ssm_decode_step(x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(skip), _ptr(gate),
-                                _ptr(dt_bias), state.data_ptr(), out.data_ptr(), s, nb, D, G, N, code, int(softplus), _raw(dev)),
+                                _ptr(dt_bias), state.data_ptr(), out.data_ptr(), s, nb, D, G, N, code, int(softplus), _linear._raw(dev)),
         "kda_ssm_decode_step", lib)
     return out
 
@@ -326,10 +322,10 @@ def ssm_chunk_bwd(d_y, x, dt, A, B, C, initial_state=None, dfinal_state=None, *,
     if stream is not None:
         return _on(stream, ssm_chunk_bwd, d_y, x, dt, A, B, C, initial_state, dfinal_state, skip=skip, gate=gate,
                    dt_bias=dt_bias, softplus=softplus, cu_seqlens=cu_seqlens, workspace=workspace)
-    lib = load()
+    lib = _linear.load()
     if x.dim() != 3:
         raise ValueError("x must be [B, T, D]")
-    code, dev = _code(x, "x"), _device(x, "x")
+    code, dev = _code(x, "x"), _linear._device(x, "x")
     D, G, N, plain = _scan_args(x, dt, A, B, C, skip, gate, dt_bias, dev)
     plain &= _view(d_y, "d_y", x.dtype, x.shape, dev)
     n, T = x.shape[:2]
@@ -351,8 +347,8 @@ def ssm_chunk_bwd(d_y, x, dt, A, B, C, initial_state=None, dfinal_state=None, *,
         out["ddt_bias"] = _like(dt_bias)
     if initial_state is not None:
         out["dh0"] = _like(initial_state)
-    st = _raw(dev)
-    ws, size = _ws("kda_ssm_chunk_bwd_workspace", (n, T, int(cu_seqlens is not None), D, G, N, code), x, st, workspace)
+    st = _linear._raw(dev)
+    ws, size = _linear._ws("kda_ssm_chunk_bwd_workspace", (n, T, int(cu_seqlens is not None), D, G, N, code), x, st, workspace)
     g = lambda name: _ptr(out.get(name))  # noqa: E731
     _ok(lib.kda_ssm_chunk_bwd(d_y.data_ptr(), x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(skip),
                               _ptr(gate), _ptr(dt_bias), _ptr(initial_state), _ptr(dfinal_state), g("dx"), g("ddt"), g("dA"),
@@ -372,12 +368,12 @@ def beam_select(logits, scores, k=None, *, finished=None, eos=None, out=None, wo
     fp32, parents [B,k] int32, tokens [B,k] int32)."""
     if stream is not None:
         return _on(stream, beam_select, logits, scores, k, finished=finished, eos=eos, out=out, workspace=workspace)
-    lib = load()
+    lib = _linear.load()
     if logits.dim() != 3:
         raise ValueError("logits must be [B, W, V]")
     B, W, V = logits.shape
-    code, dev = _code(logits, "logits"), _device(logits, "logits")
-    plain = _view(logits, "logits", logits.dtype, logits.shape, dev)
+    code, dev = _code(logits, "logits"), _linear._device(logits, "logits")
+    plain = logits.is_contiguous() or _view(logits, "logits", logits.dtype, logits.shape, dev)
     _dense(scores, "scores", _F32, (B, W), dev)
     if finished is not None:
         _dense(finished, "finished", torch.bool, (B, W), dev)
@@ -390,8 +386,8 @@ def beam_select(logits, scores, k=None, *, finished=None, eos=None, out=None, wo
     else:
         for t, name, dtype in zip(out, ("out scores", "out parents", "out tokens"), (_F32, _I32, _I32)):
             _dense(t, name, dtype, (B, k), dev)
-    st = _raw(dev)
-    ws, size = _ws("kda_beam_select_workspace", (B, W, V, code), logits, st, workspace)
+    st = _linear._raw(dev)
+    ws, size = _linear._ws("kda_beam_select_workspace", (B, W, V, code), logits, st, workspace)
     _ok(lib.kda_beam_select(logits.data_ptr(), None if plain else _longs(logits.stride(0), logits.stride(1)), scores.data_ptr(),
                             _ptr(finished), eos or 0, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), B, W, V, k, code,
                             ws.data_ptr(), size, st), "kda_beam_select", lib)
@@ -405,11 +401,11 @@ def beam_reorder(states, parents, *, stream=None):
     W <= 32 (a parent outside 0 .. W - 1 leaves its beam as it is).  Returns states."""
     if stream is not None:
         return _on(stream, beam_reorder, states, parents)
-    lib = load()
+    lib = _linear.load()
     if parents.dim() != 2:
         raise ValueError("parents must be [B, W]")
     B, W = parents.shape
-    dev = _device(parents, "parents")
+    dev = _linear._device(parents, "parents")
     _dense(parents, "parents", _I32, (B, W), dev)
     arrays = [states] if isinstance(states, torch.Tensor) else list(states)
     n, rows, ptrs, sizes = len(arrays), B * W, [], []
@@ -422,5 +418,5 @@ def beam_reorder(states, parents, *, stream=None):
         ptrs.append(t.data_ptr())
         sizes.append(t.nbytes // rows if rows else 0)
     ptrs, sizes = (ctypes.c_void_p * n)(*ptrs), (ctypes.c_longlong * n)(*sizes)
-    _ok(lib.kda_beam_reorder(ptrs, sizes, n, parents.data_ptr(), B, W, _raw(dev)), "kda_beam_reorder", lib)
+    _ok(lib.kda_beam_reorder(ptrs, sizes, n, parents.data_ptr(), B, W, _linear._raw(dev)), "kda_beam_reorder", lib)
     return states
