@@ -14,11 +14,12 @@
 //   3. every chunk again: forwards from its memory, then backwards; dB and dC of up to 128 channels go out as partial sums;
 //   4. the partial sums, in a fixed order.
 // Per (token, channel, state) that is three exp2 and some 20 fp32 operations, in packed pairs of states, and the sums over
-// states and channels; arithmetic and issue bound it, at four times what HBM would take.
+// states and channels; arithmetic and issue bound it.  Measured, bf16, 2 x 2048 tokens of 4096 channels of 16 states, gated: 112 + 30 +
+// 385 + 11 us (237 MB, 35 us at the copy rate).
 //
-// A warp holds 64 / L channels (L = N / 4): a lane two channels and four states, so that sums over states meet over L lanes and
-// sums over channels over 32 / L, in shuffles that halve the values at every step (a lane ends with one token's sums, or
-// one state's).  Memories of a chunk do not fit in registers: every fourth is kept in shared memory, and four tokens at
+// A warp holds 64 / L channels (L = N / 4): a lane two channels and four states, so that sums over states meet over L lanes, in
+// shuffles that halve the values at every step (a lane ends with one token's sums), and sums over channels over 32 / L, by columns
+// through shared memory (half the instructions of such shuffles).  Memories of a chunk do not fit in registers: every fourth is kept in shared memory, and four tokens at
 // a time are walked again from it.
 #include <algorithm>
 
@@ -32,7 +33,7 @@ namespace {
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTile = 32;                   // tokens of a chunk
 constexpr float kLn2F = 0.6931471805599453f;
-constexpr int kPartC = 128;                 // floats from a part's dB to its dC
+constexpr int kPartC = 128;                 // floats from the lanes' dB to their dC
 
 template <typename T, int L> struct Lay {
     static constexpr int N = 4 * L, CL = 32 / L, CW = 2 * CL, CH = kWarps * CW;      // states; channel lanes, channels of a warp, of a CTA
