@@ -8,14 +8,14 @@
 // window's gradient.
 //
 // A lane holds V = 4 channels in packed pairs (8 of them left registers for too few rows in flight: forwards 34 us at 2 x 2048 tokens
-// of 4096 channels where 4 take 15), a warp 32 V of them, and walks a run of tokens of one sequence with the K last rows in
+// of 4096 channels where 4 took 23), a warp 32 V of them, and walks a run of tokens of one sequence with the K last rows in
 // registers, so that every row is read once, but for the K - 1 rows that a run shares with the next (L2 has them).  The
 // sums are fp32 and rounded once.  The weights' gradients stay in registers over all runs of a lane, are added up over a
 // CTA's warps in shared memory and over the CTAs by a second kernel, in a fixed order.
 //
-// Measured, bf16: forwards 15 us at that shape (67 MB, 9.9 us at the copy rate; some 70 instructions a row of four channels are
-// the other bound), 16 packed prompts of 40,000 tokens in all and 2048 channels 59 us, 5.4 TB/s; gradients 31 us (101 MB, 14.9 us; 128
-// registers, 16 warps an SM) and 4 us for the second kernel.
+// Measured, bf16: forwards 15 us at that shape (67 MB, 9.9 us at the copy rate; 66 instructions a row and warp are
+// the other bound), 16 packed prompts of 40,000 tokens in all and 2048 channels 61 us, 5.3 TB/s; gradients 31 us (101 MB, 14.9 us; 128
+// registers, 16 warps an SM), the second kernel among it.
 #include <algorithm>
 
 #include "conv_internal.cuh"

@@ -14,12 +14,12 @@
 //   3. every chunk again: forwards from its memory, then backwards; dB and dC of up to 128 channels go out as partial sums;
 //   4. the partial sums, in a fixed order.
 // Per (token, channel, state) that is three exp2 and some 20 fp32 operations, in packed pairs of states, and the sums over
-// states and channels; arithmetic and issue bound it.  Measured, bf16, 2 x 2048 tokens of 4096 channels of 16 states, gated: 112 + 30 +
+// states and channels; arithmetic and issue bound it.  Measured, bf16, 2 x 2048 tokens of 4096 channels of 16 states, gated: 113 + 32 +
 // 385 + 11 us (237 MB, 35 us at the copy rate).
 //
 // A warp holds 64 / L channels (L = N / 4): a lane two channels and four states, so that sums over states meet over L lanes, in
 // shuffles that halve the values at every step (a lane ends with one token's sums), and sums over channels over 32 / L, by columns
-// through shared memory (half the instructions of such shuffles).  Memories of a chunk do not fit in registers: every fourth is kept in shared memory, and four tokens at
+// through shared memory.  Memories of a chunk do not fit in registers: every fourth is kept in shared memory, and four tokens at
 // a time are walked again from it.
 #include <algorithm>
 

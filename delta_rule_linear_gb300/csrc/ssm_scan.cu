@@ -26,9 +26,9 @@
 // segment from an empty memory and leaves the memory and the sum of dt; in the second, every CTA joins those before it,
 // h <- exp(A sum dt) h + local, which costs the walk of the memories (not of y) twice.
 //
-// Measured, bf16, 16 states, gated: 2 x 2048 tokens of 4096 channels 103 us (the cells alone 29 us, HBM 20; with B and C from
-// shared memory 156), 32,768 tokens 931 us (230 and 158); 0.65 of the issue slots in the former.  Per tile the scanning warps alone
-// take 0.58 us, with what serves them 0.91.
+// Measured, bf16, 16 states, gated: 2 x 2048 tokens of 4096 channels 103 us (the cells alone 29 us, HBM 20; an earlier form with
+// B and C from shared memory 156), 32,768 tokens 932 us (230 and 158); 0.65 of the issue slots in the former.  Per tile of the latter
+// the scanning warps alone take 0.58 us, with what serves them 0.91.
 #include <algorithm>
 
 #include "linear_tc.cuh"
