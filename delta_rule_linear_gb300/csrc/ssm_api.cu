@@ -381,6 +381,10 @@ kda_status kda_beam_reorder(void *const *states, const long long *row_bytes, int
     if (B == 0 || count == 0 || W == 1) return KDA_OK;
     if (!parents) return KDA_ERR_NULL;
     if (!al(parents, 4)) return KDA_ERR_ALIGN;
+    for (int i = 0; i < count; ++i) {       // every CTA reads them, others have written by then
+        const uintptr_t p = reinterpret_cast<uintptr_t>(states[i]), q = reinterpret_cast<uintptr_t>(parents);
+        if (p < q + 4 * (uintptr_t)B * W && q < p + (uintptr_t)row_bytes[i] * B * W) return KDA_ERR_INDEX;
+    }
     for (int i0 = 0; i0 < count; i0 += kBeamStates) {
         BeamReorder a{};
         a.count = count - i0 < kBeamStates ? count - i0 : kBeamStates;

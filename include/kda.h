@@ -677,8 +677,8 @@ kda_status kda_beam_select(const void *logits, const long long *strides, const f
 /*
  * The recurrent memories follow the beams, in place: row (b, w) of each array becomes row
  * (b, parents[b, w]).  states: `count` device pointers in a host array, each [B,W,row_bytes[i]] bytes,
- * contiguous, of any type (memories, windows); arrays that overlap are KDA_ERR_INDEX.  parents [B,W]
- * int32; a parent outside 0 .. W - 1 leaves its beam as it is.  W <= 32.
+ * contiguous, of any type (memories, windows); arrays that overlap, or hold the parents, are KDA_ERR_INDEX.
+ * parents [B,W] int32; a parent outside 0 .. W - 1 leaves its beam as it is.  W <= 32.
  */
 kda_status kda_beam_reorder(void *const *states, const long long *row_bytes, int count, const int *parents,
                             int B, int W, kda_stream_t stream);

@@ -194,6 +194,17 @@ def test_beam_refusals(lib):
     assert r(B=0) == 0 and r(W=1) == 0 and r(ptrs=(), sizes=()) == 0
 
 
+def test_reorder_refuses_parents_among_the_arrays(lib):
+    """B W parents of four bytes: moved rows would be read as parents by CTAs that have not begun."""
+    def r(par, sizes=(64, 64), B=2, W=3):
+        a, n = (ctypes.c_void_p * 2)(0x1000, 0x9000), (ctypes.c_longlong * 2)(*sizes)
+        return lib.kda_beam_reorder(a, n, 2, P(par), B, W, None)
+    last = 64 * 6
+    for at in (0x1000, 0x1000 + last - 4, 0x1000 - 4 * 6 + 4, 0x9000, 0x9000 + 8):
+        assert r(at) == 9, hex(at)
+    assert r(0x1000, B=0) == 0 and r(0x1000, W=1) == 0
+
+
 # ------------------------------------------------------------------ refusals of the binding
 def test_binding_refuses_host_tensors_and_bad_arguments():
     import torch
