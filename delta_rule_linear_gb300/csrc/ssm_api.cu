@@ -178,6 +178,9 @@ kda_status kda_conv_bwd(const void *d_y, const void *x, const float *weight, con
     if (!al(weight, 4) || !al(bias, 4) || !al(dweight, 4) || !al(dbias, 4) || !al(cu_seqlens, 4)) return KDA_ERR_ALIGN;
     if (!ws || ws_bytes < kda_conv_bwd_workspace(C, K)) return KDA_ERR_WORKSPACE;
     if (!al(ws, 16)) return KDA_ERR_ALIGN;
+    // rows and windows are read by other runs than the one that writes them
+    if (rows > 0 && (dx == x || dx == d_y)) return KDA_ERR_UNSUPPORTED;
+    if (N > 0 && dinitial_state && (dinitial_state == initial_state || dinitial_state == dfinal_state)) return KDA_ERR_UNSUPPORTED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (N == 0) {
         if (cudaMemsetAsync(dweight, 0, (size_t)C * K * 4, st) != cudaSuccess) return KDA_ERR_CUDA;

@@ -583,7 +583,7 @@ kda_status kda_conv_decode_step(const void *x, const float *weight, const float 
 /* Gradients, given d_y and dfinal_state (the windows' gradient, x's type, or NULL): dx, dinitial_state (x's
  * type; the latter may be NULL), dweight [C,K], dbias [C] float32 (may be NULL).  cu_seqlens NULL: N
  * sequences of T tokens; otherwise N packed ones of T tokens in all (dx of rows outside them is not
- * written).  strides: NULL or six (batch, token) of x, d_y, dx. */
+ * written).  No output overlaps an input (KDA_ERR_UNSUPPORTED where one is it).  strides: NULL or six (batch, token) of x, d_y, dx. */
 size_t kda_conv_bwd_workspace(int C, int K);
 kda_status kda_conv_bwd(const void *d_y, const void *x, const float *weight, const float *bias,
                         const void *initial_state, const void *dfinal_state, void *dx, float *dweight,
@@ -643,7 +643,8 @@ kda_status kda_ssm_decode_step(const void *x, const void *dt, const float *A, co
  * (contiguous; dB, dC summed over the group's channels in fp32), dA [D,N], dskip, ddt_bias [D] and
  * dinitial_state [nseq,D,N] float32 (dskip, ddt_bias, dinitial_state may be NULL).  cu_seqlens NULL: nseq
  * sequences of T tokens; otherwise nseq packed ones of T tokens in all (gradients of rows outside them
- * are not written).  strides: NULL or eighteen, of x, dt, B_in, C_in, gate, d_y.  The results do not depend
+ * are not written).  No output overlaps an input.  strides: NULL or eighteen, of x, dt, B_in, C_in, gate,
+ * d_y.  The results do not depend
  * on the order in which the GPU works. */
 size_t kda_ssm_chunk_bwd_workspace(int nseq, int T, int packed, int D, int G, int N, kda_dtype dtype);
 kda_status kda_ssm_chunk_bwd(const void *d_y, const void *x, const void *dt, const float *A,

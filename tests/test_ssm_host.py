@@ -205,6 +205,15 @@ def test_reorder_refuses_parents_among_the_arrays(lib):
     assert r(0x1000, B=0) == 0 and r(0x1000, W=1) == 0
 
 
+def test_conv_gradients_refuse_outputs_in_place_of_inputs(lib):
+    """A run reads rows that its neighbours write, and the first run writes the window that the last one reads."""
+    def b(dy=0x1000, x=0x2000, dx=0x3000, h0=0x4000, dhT=0x5000, dh0=0x6000):
+        return lib.kda_conv_bwd(P(dy), P(x), P(), None, P(h0), P(dhT), P(dx), P(), None, P(dh0), None, None, 2, 5, 6, 4, 1, 1, P(),
+                                1 << 40, None)
+    assert b(dx=0x1000) == 4 and b(dx=0x2000) == 4
+    assert b(dh0=0x4000) == 4 and b(dh0=0x5000) == 4
+
+
 # ------------------------------------------------------------------ refusals of the binding
 def test_binding_refuses_host_tensors_and_bad_arguments():
     import torch
