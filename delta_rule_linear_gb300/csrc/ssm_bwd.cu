@@ -305,7 +305,7 @@ template <int N> __global__ void __launch_bounds__(256) ssm_bwd_chain_kernel(con
             long before = 0;
             int mine = 0;
             for (int k = threadIdx.x; k <= n; k += 32) {
-                const int len = a.s.cu[k + 1] - a.s.cu[k], c = len > kTile ? (len + kTile - 1) / kTile : 1;
+                const int len = (int)min((long)a.s.cu[k + 1] - a.s.cu[k], a.total), c = len > kTile ? (len + kTile - 1) / kTile : 1;
                 if (k < n) before += c;
                 else mine = c;
             }
