@@ -583,7 +583,8 @@ kda_status kda_conv_decode_step(const void *x, const float *weight, const float 
 /* Gradients, given d_y and dfinal_state (the windows' gradient, x's type, or NULL): dx, dinitial_state (x's
  * type; the latter may be NULL), dweight [C,K], dbias [C] float32 (may be NULL).  cu_seqlens NULL: N
  * sequences of T tokens; otherwise N packed ones of T tokens in all (dx of rows outside them is not
- * written).  No output overlaps an input (KDA_ERR_UNSUPPORTED where one is it).  strides: NULL or six (batch, token) of x, d_y, dx. */
+ * written).  No output overlaps an input (KDA_ERR_UNSUPPORTED where one is it).  strides: NULL or six
+ * (batch, token) of x, d_y, dx. */
 size_t kda_conv_bwd_workspace(int C, int K);
 kda_status kda_conv_bwd(const void *d_y, const void *x, const float *weight, const float *bias,
                         const void *initial_state, const void *dfinal_state, void *dx, float *dweight,
