@@ -89,8 +89,15 @@ struct SsmIn {
     const void *x, *dt, *B, *C, *gate;
     const float *A, *skip, *bias, *h0;
 };
-// An output in place of an input: a split sequence is read by two launches, of which the second writes.
-bool in_place(const void *y, const SsmIn &p, long rows) { return rows > 0 && (y == p.x || y == p.dt || (p.gate && y == p.gate)); }
+// Whether y is one of the inputs: a split sequence is read by two launches, of which the second writes; the rows of B and C
+// are read by all CTAs of a group, the other arrays by all that have a channel.
+bool in_place(const void *y, const SsmIn &p, const int *cu, long rows) {
+    if (rows == 0) return false;
+    for (const void *q : {p.x, p.dt, p.B, p.C, p.gate, (const void *)p.A, (const void *)p.skip, (const void *)p.bias,
+                          (const void *)p.h0, (const void *)cu})
+        if (q == y) return true;
+    return false;
+}
 // The arrays that every call has; strides in the order x, dt, B, C, gate.
 kda_status ssm_in(Ssm &a, const SsmIn &p, const long long *s, const int *cu, int N, int T, long rows, int D, int G, int S,
                   kda_dtype dtype, int softplus) {
@@ -219,7 +226,7 @@ kda_status kda_ssm_chunk_fwd(const void *x, const void *dt, const float *A, cons
                softplus);
     if (c != KDA_OK) return c;
     if ((long)B * T > 0 && !y) return KDA_ERR_NULL;
-    if (in_place(y, {x, dt, B_in, C_in, gate, A, skip, dt_bias, initial_state}, (long)B * T)) return KDA_ERR_UNSUPPORTED;
+    if (in_place(y, {x, dt, B_in, C_in, gate, A, skip, dt_bias, initial_state}, nullptr, (long)B * T)) return KDA_ERR_UNSUPPORTED;
     if (!al(y, size_of(dtype)) || !al(final_state, 16)) return KDA_ERR_ALIGN;
     if (!ws || ws_bytes < kda_ssm_chunk_fwd_workspace(B, T, D, G, N, dtype)) return KDA_ERR_WORKSPACE;
     if (!al(ws, 16)) return KDA_ERR_ALIGN;
@@ -246,7 +253,7 @@ kda_status kda_ssm_varlen_fwd(const void *x, const void *dt, const float *A, con
                dtype, softplus);
     if (c != KDA_OK) return c;
     if (total_T > 0 && !y) return KDA_ERR_NULL;
-    if (in_place(y, {x, dt, B_in, C_in, gate, A, skip, dt_bias, initial_state}, total_T)) return KDA_ERR_UNSUPPORTED;
+    if (in_place(y, {x, dt, B_in, C_in, gate, A, skip, dt_bias, initial_state}, cu_seqlens, total_T)) return KDA_ERR_UNSUPPORTED;
     if (!al(y, size_of(dtype)) || !al(final_state, 16)) return KDA_ERR_ALIGN;
     if (!ws || ws_bytes < kda_ssm_varlen_fwd_workspace(nseq, total_T, D, G, N, dtype)) return KDA_ERR_WORKSPACE;
     if (!al(ws, 16)) return KDA_ERR_ALIGN;

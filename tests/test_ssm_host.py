@@ -229,3 +229,23 @@ def test_binding_refuses_host_tensors_and_bad_arguments():
                  lambda: kda.beam_reorder(h, torch.zeros(2, 1, dtype=torch.int32))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_scan_refuses_outputs_in_place_of_any_input(lib):
+    """CTAs of a group read the same B and C rows, and every CTA reads A, skip, dt_bias and the prefix array, while others
+    write y already.  An empty call writes nothing: nothing is refused."""
+    at = dict(x=0x1000, dt=0x2000, A=0x3000, B=0x4000, C=0x5000, skip=0x6000, gate=0x7000, bias=0x8000, h0=0x9000, cu=0xa000)
+
+    def chunk(y, T=5, nb=2):
+        p = {k: P(v) for k, v in at.items()}
+        return lib.kda_ssm_chunk_fwd(p["x"], p["dt"], p["A"], p["B"], p["C"], p["skip"], p["gate"], p["bias"], p["h0"], P(y), P(0xb000),
+                                     None, nb, T, 32, 2, 16, 1, 1, P(0xc000), 1 << 50, None)
+
+    def packed(y):
+        p = {k: P(v) for k, v in at.items()}
+        return lib.kda_ssm_varlen_fwd(p["x"], p["dt"], p["A"], p["B"], p["C"], p["skip"], p["gate"], p["bias"], p["cu"], None, p["h0"],
+                                      P(y), P(0xb000), None, 2, 10, 32, 2, 16, 1, 1, P(0xc000), 1 << 50, None)
+    for name, y in at.items():
+        assert packed(y) == 4, name
+        assert name == "cu" or chunk(y) == 4, name
+    assert chunk(0x4000, nb=0) == 0
