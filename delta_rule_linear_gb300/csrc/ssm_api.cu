@@ -1,5 +1,7 @@
 // ssm_api.cu -- the C ABI of the short convolution, the state space scan and beam search: argument checks, workspace
 // carving, dispatch.  Nothing here allocates device memory.
+#include <initializer_list>
+
 #include "../../include/kda.h"
 #include "beam_internal.cuh"
 #include "conv_internal.cuh"
@@ -15,6 +17,13 @@ bool al(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n
 bool dtype_ok(kda_dtype d) { return d == KDA_F32 || d == KDA_BF16; }
 unsigned size_of(kda_dtype d) { return d == KDA_BF16 ? 2 : 4; }
 DType to_dtype(kda_dtype d) { return d == KDA_BF16 ? DType::BF16 : DType::F32; }
+// Whether one of the outputs is one of the inputs (nullptr: not there).
+bool any_in_place(std::initializer_list<const void *> outputs, std::initializer_list<const void *> inputs) {
+    for (const void *o : outputs)
+        for (const void *i : inputs)
+            if (o && o == i) return true;
+    return false;
+}
 kda_status done(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
 // Packed sequences: the device array, and the host copy where there is one (max_len: bound on the longest).
@@ -92,11 +101,7 @@ struct SsmIn {
 // Whether y is one of the inputs: a split sequence is read by two launches, of which the second writes; the rows of B and C
 // are read by all CTAs of a group, the other arrays by all that have a channel.
 bool in_place(const void *y, const SsmIn &p, const int *cu, long rows) {
-    if (rows == 0) return false;
-    for (const void *q : {p.x, p.dt, p.B, p.C, p.gate, (const void *)p.A, (const void *)p.skip, (const void *)p.bias,
-                          (const void *)p.h0, (const void *)cu})
-        if (q == y) return true;
-    return false;
+    return rows > 0 && any_in_place({y}, {p.x, p.dt, p.B, p.C, p.gate, p.A, p.skip, p.bias, p.h0, cu});
 }
 // The arrays that every call has; strides in the order x, dt, B, C, gate.
 kda_status ssm_in(Ssm &a, const SsmIn &p, const long long *s, const int *cu, int N, int T, long rows, int D, int G, int S,
@@ -315,6 +320,13 @@ kda_status kda_ssm_chunk_bwd(const void *d_y, const void *x, const void *dt, con
         return KDA_ERR_ALIGN;
     if (!ws || ws_bytes < kda_ssm_chunk_bwd_workspace(nseq, T, cu_seqlens != nullptr, D, G, N, dtype)) return KDA_ERR_WORKSPACE;
     if (!al(ws, 16)) return KDA_ERR_ALIGN;
+    // arrays without rows have no address that counts
+    const auto tok = [&](const void *p) { return rows > 0 ? p : nullptr; };
+    const auto seq = [&](const void *p) { return nseq > 0 ? p : nullptr; };
+    if (any_in_place({tok(dx), tok(ddt), tok(dB), tok(dC), gate ? tok(dgate) : nullptr, dA, dskip, ddt_bias, seq(dinitial_state)},
+                     {tok(d_y), tok(x), tok(dt), tok(B_in), tok(C_in), tok(gate), A, skip, dt_bias, seq(initial_state),
+                      seq(dfinal_state), cu_seqlens}))
+        return KDA_ERR_UNSUPPORTED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (nseq == 0) {
         if (cudaMemsetAsync(dA, 0, (size_t)D * N * 4, st) != cudaSuccess) return KDA_ERR_CUDA;

@@ -644,9 +644,8 @@ kda_status kda_ssm_decode_step(const void *x, const void *dt, const float *A, co
  * (contiguous; dB, dC summed over the group's channels in fp32), dA [D,N], dskip, ddt_bias [D] and
  * dinitial_state [nseq,D,N] float32 (dskip, ddt_bias, dinitial_state may be NULL).  cu_seqlens NULL: nseq
  * sequences of T tokens; otherwise nseq packed ones of T tokens in all (gradients of rows outside them
- * are not written).  No output overlaps an input.  strides: NULL or eighteen, of x, dt, B_in, C_in, gate,
- * d_y.  The results do not depend
- * on the order in which the GPU works. */
+ * are not written).  No output overlaps an input (KDA_ERR_UNSUPPORTED where one is it).  strides: NULL or
+ * eighteen, of x, dt, B_in, C_in, gate, d_y.  The results do not depend on the order in which the GPU works. */
 size_t kda_ssm_chunk_bwd_workspace(int nseq, int T, int packed, int D, int G, int N, kda_dtype dtype);
 kda_status kda_ssm_chunk_bwd(const void *d_y, const void *x, const void *dt, const float *A,
                              const void *B_in, const void *C_in, const float *skip, const void *gate,

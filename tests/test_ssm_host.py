@@ -249,3 +249,21 @@ def test_scan_refuses_outputs_in_place_of_any_input(lib):
         assert packed(y) == 4, name
         assert name == "cu" or chunk(y) == 4, name
     assert chunk(0x4000, nb=0) == 0
+
+
+def test_scan_gradients_refuse_outputs_in_place_of_inputs(lib):
+    """The chain of the gradients writes dinitial_state beside the chain of the memories, which reads initial_state; the last
+    launch writes what CTAs of the same or an earlier one read.  The smallest call of each kind is refused too."""
+    ins = ("dy", "x", "dt", "A", "B", "C", "skip", "gate", "bias", "h0", "dhT")
+    outs = ("dx", "ddt", "dA", "dB", "dC", "dskip", "dgate", "dbias", "dh0")
+    at = {k: 0x1000 * (i + 1) for i, k in enumerate(ins + outs)}
+
+    def b(nseq=2, T=5, cu=None, **kw):
+        p = {k: P(v) if v else None for k, v in dict(at, **kw).items()}
+        return lib.kda_ssm_chunk_bwd(*(p[k] for k in ins), *(p[k] for k in outs), cu, None, nseq, T, 32, 2, 16, 1, 1, P(0x100000),
+                                     1 << 50, None)
+    for o in outs:
+        for i in ins:
+            assert b(**{o: at[i]}) == 4, (o, i)
+    assert b(dB=0x200000, cu=P(0x200000)) == 4
+    assert b(T=0, dh0=at["h0"]) == 4 and b(nseq=1, T=1, dA=at["A"]) == 4
