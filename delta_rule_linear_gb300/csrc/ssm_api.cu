@@ -191,8 +191,11 @@ kda_status kda_conv_bwd(const void *d_y, const void *x, const float *weight, con
     if (!ws || ws_bytes < kda_conv_bwd_workspace(C, K)) return KDA_ERR_WORKSPACE;
     if (!al(ws, 16)) return KDA_ERR_ALIGN;
     // rows and windows are read by other runs than the one that writes them
-    if (rows > 0 && (dx == x || dx == d_y)) return KDA_ERR_UNSUPPORTED;
-    if (N > 0 && dinitial_state && (dinitial_state == initial_state || dinitial_state == dfinal_state)) return KDA_ERR_UNSUPPORTED;
+    const auto tok = [&](const void *p) { return rows > 0 ? p : nullptr; };
+    const auto seq = [&](const void *p) { return N > 0 ? p : nullptr; };
+    if (any_in_place({tok(dx), dweight, dbias, seq(dinitial_state)},
+                     {tok(d_y), tok(x), weight, bias, seq(initial_state), seq(dfinal_state), cu_seqlens}))
+        return KDA_ERR_UNSUPPORTED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (N == 0) {
         if (cudaMemsetAsync(dweight, 0, (size_t)C * K * 4, st) != cudaSuccess) return KDA_ERR_CUDA;

@@ -267,3 +267,18 @@ def test_scan_gradients_refuse_outputs_in_place_of_inputs(lib):
             assert b(**{o: at[i]}) == 4, (o, i)
     assert b(dB=0x200000, cu=P(0x200000)) == 4
     assert b(T=0, dh0=at["h0"]) == 4 and b(nseq=1, T=1, dA=at["A"]) == 4
+
+
+def test_conv_gradients_refuse_any_output_that_is_an_input(lib):
+    """The weights and biases are inputs too: without a sequence their gradients are set to zero before anything is read."""
+    ins, outs = ("dy", "x", "w", "b", "h0", "dhT"), ("dx", "dw", "db", "dh0")
+    at = {k: 0x1000 * (i + 1) for i, k in enumerate(ins + outs)}
+
+    def f(N=2, T=5, cu=None, **kw):
+        p = {k: P(v) for k, v in dict(at, **kw).items()}
+        return lib.kda_conv_bwd(*(p[k] for k in ins), *(p[k] for k in outs), cu, None, N, T, 8, 4, 1, 1, P(0x100000), 1 << 40, None)
+    for o in outs:
+        for i in ins:
+            assert f(**{o: at[i]}) == 4, (o, i)
+    assert f(dw=0x200000, cu=P(0x200000)) == 4
+    assert f(N=0, dw=at["w"]) == 4 and f(T=0, db=at["b"]) == 4
