@@ -400,7 +400,7 @@ kda_status kda_beam_reorder(void *const *states, const long long *row_bytes, int
         const uintptr_t p = reinterpret_cast<uintptr_t>(states[i]), n = (uintptr_t)row_bytes[i] * B * W;
         for (int j = 0; j < i; ++j) {       // an array that is there twice would be moved twice
             const uintptr_t q = reinterpret_cast<uintptr_t>(states[j]), m = (uintptr_t)row_bytes[j] * B * W;
-            if (p < q + m && q < p + n) return KDA_ERR_INDEX;
+            if (n && m && p < q + m && q < p + n) return KDA_ERR_INDEX;
         }
     }
     if (B == 0 || count == 0 || W == 1) return KDA_OK;
@@ -408,7 +408,7 @@ kda_status kda_beam_reorder(void *const *states, const long long *row_bytes, int
     if (!al(parents, 4)) return KDA_ERR_ALIGN;
     for (int i = 0; i < count; ++i) {       // every CTA reads them, others have written by then
         const uintptr_t p = reinterpret_cast<uintptr_t>(states[i]), q = reinterpret_cast<uintptr_t>(parents);
-        if (p < q + 4 * (uintptr_t)B * W && q < p + (uintptr_t)row_bytes[i] * B * W) return KDA_ERR_INDEX;
+        if (row_bytes[i] && p < q + 4 * (uintptr_t)B * W && q < p + (uintptr_t)row_bytes[i] * B * W) return KDA_ERR_INDEX;
     }
     for (int i0 = 0; i0 < count; i0 += kBeamStates) {
         BeamReorder a{};

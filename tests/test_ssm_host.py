@@ -282,3 +282,12 @@ def test_conv_gradients_refuse_any_output_that_is_an_input(lib):
             assert f(**{o: at[i]}) == 4, (o, i)
     assert f(dw=0x200000, cu=P(0x200000)) == 4
     assert f(N=0, dw=at["w"]) == 4 and f(T=0, db=at["b"]) == 4
+
+
+def test_reorder_takes_empty_arrays_wherever_they_lie(lib):
+    """Rows of no bytes overlap nothing (one beam: the call ends before a launch, after these checks)."""
+    def r(ptrs, sizes):
+        a, n = (ctypes.c_void_p * len(ptrs))(*ptrs), (ctypes.c_longlong * len(sizes))(*sizes)
+        return lib.kda_beam_reorder(a, n, len(ptrs), P(), 2, 1, None)
+    assert r((0x1000, 0x1040), (64, 0)) == 0 and r((0x1040, 0x1000), (0, 64)) == 0
+    assert r((0x1000, 0x1040), (64, 1)) == 9
