@@ -176,3 +176,67 @@ def test_an_infinite_token_stays_where_it_is(kda):
     want = torch.zeros_like(bad)
     want[10:14, 5] = True
     assert torch.equal(bad, want)
+
+
+def _packed64(x, w, b, s0, cu):
+    """Packed sequences in fp64 without a loop over them: x [total,C] and windows [N,K-1,C] (both with a gradient), y [total,C]."""
+    import torch
+    K, total = w.shape[1], x.shape[0]
+    lens = (cu[1:] - cu[:-1]).long()
+    seq = torch.repeat_interleave(torch.arange(len(lens), device="cuda"), lens)
+    t = torch.arange(total, device="cuda") - cu.long()[seq]             # the token's place in its sequence
+    flat = torch.cat([s0.flatten(0, 1), x])
+    p = b.expand(total, -1)
+    for j in range(K):
+        back = t - (K - 1) + j
+        at = torch.where(back >= 0, len(s0) * (K - 1) + cu.long()[seq] + back, seq * (K - 1) + back + K - 1)
+        p = p + w[:, j] * flat[at]
+    return p * torch.sigmoid(p)
+
+
+@pytest.mark.parametrize("N,most,C", [(31, 60, 40), (512, 30, 36), (513, 30, 37), (1100, 9, 256), (33000, 1, 24), (40000, 3, 32)])
+def test_packed_sequences_of_any_number(kda, N, most, C):
+    """A warp finds its run's sequence among any number of them: lengths from none on, a run's length and its multiples among
+    them.  Tolerances: CONV; sums over up to 60,000 rows err like sqrt(n) 2^-24, 1.5e-5."""
+    import torch
+    g, K = _gen(N), 4
+    lens = torch.randint(0, most + 1, (N,), generator=torch.Generator().manual_seed(N))
+    lens[::5] = lens[::5] // 8 * 8
+    lens[1::7] = 0
+    cu = torch.cat([lens.new_zeros(1), lens.cumsum(0)]).int()
+    cud, total = cu.cuda(), int(cu[-1])
+    x, w, b, s0 = _rn(g, 1, total, C), _rn(g, C, K), _rn(g, C), _rn(g, N, K - 1, C)
+    y, s = kda.conv_varlen_fwd(x, w, cud, b, s0, cu_seqlens_cpu=cu)
+    leaf = [t.double().requires_grad_(True) for t in (x[0], w, b, s0)]
+    want = _packed64(*leaf, cud)
+    _check("y", y[0], to_np(want.detach()), ref.CONV)
+    rows = cud[1:].long()[:, None] - (K - 1) + torch.arange(K - 1, device="cuda")
+    back = (cud[1:] - cud[:-1]).long()[:, None] - (K - 1) + torch.arange(K - 1, device="cuda")
+    old = s0.gather(1, (back + K - 1).clamp(0, K - 2)[..., None].expand(-1, -1, C))
+    assert torch.equal(s, torch.where((back >= 0)[..., None], x[0][rows.clamp(min=0)], old))
+    dy = _rn(g, 1, total, C)
+    got = kda.conv_bwd(dy, x, w, b, s0, None, cu_seqlens=cud)
+    grads = torch.autograd.grad(want, leaf, dy[0].double())
+    for k, v, tol in zip(("dx", "dw", "dbias", "dstate"), grads, (ref.CONV, 1.5e-5, 1.5e-5, ref.CONV)):
+        _check(k, got[k].reshape(v.shape), to_np(v), tol)
+
+
+def test_many_short_sequences_cost_what_their_tokens_do(kda):
+    """A token for each of 200,000 sequences: packed it is the same work as a batch of that many (a search whose time grows with
+    the number of sequences, for each of them, takes a thousand times as long; ten are allowed)."""
+    import torch
+    g, N, C = _gen(1), 200000, 128
+    x, w, s0 = _rn(g, N, 1, C, dt=torch.bfloat16), _rn(g, C, 4), _rn(g, N, 3, C, dt=torch.bfloat16)
+    cu = torch.arange(N + 1, dtype=torch.int32, device="cuda")
+    want = kda.conv_fwd(x, w, None, s0)
+    got = kda.conv_varlen_fwd(x.view(1, N, C), w, cu, None, s0)
+    assert torch.equal(got[0].view_as(want[0]), want[0]) and torch.equal(got[1], want[1])
+
+    def us(call):
+        ev = [torch.cuda.Event(enable_timing=True) for _ in range(6)]
+        for e in ev:
+            e.record()
+            call()
+        torch.cuda.synchronize()
+        return min(a.elapsed_time(b) for a, b in zip(ev, ev[1:]))
+    assert us(lambda: kda.conv_varlen_fwd(x.view(1, N, C), w, cu, None, s0)) <= 10 * us(lambda: kda.conv_fwd(x, w, None, s0))
