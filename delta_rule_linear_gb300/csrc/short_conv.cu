@@ -19,6 +19,7 @@
 #include <algorithm>
 
 #include "conv_internal.cuh"
+#include "run_item.cuh"
 #include "ssm_math.cuh"
 
 namespace kda {
@@ -120,13 +121,8 @@ __device__ __forceinline__ void next_window(const Conv &a, int n, long start, in
     for (int i = 0; i < K - 1; ++i) r[i].keep(hp + (long)i * a.C);
 }
 
-// Run `item` of the launch; false: there is none.  (Whatever a prefix array says, no row outside the batch is touched.)
-// Few sequences' runs are counted one after another, which a warp does for 32 sequences at a time; of many that would take the
-// square of their number.  There sequence n has its runs from number cu[n] / run + n on: the numbers rise with n and leave each
-// sequence enough of them (some stay empty), so that its sequence is found 32 places at a time.  40,000 tokens of 2048 channels,
-// counted and searched: 16 sequences 62.5 and 67.6 us (runs without rows stand between the others), 512 sequences 89 and 85 (gradients
-// 200 both), 1024 128 and 99, 16,384 3826 and 317.
-constexpr int kCounted = 512;
+// Run `item` of the launch; false: there is none.  (What run_item does, written out: called, 16 packed prompts of 40,000 tokens take
+// 69.6 us instead of 63.4, with the same registers; the search is not what they go through.)
 __device__ __forceinline__ bool conv_item(const Conv &a, long item, LinItem &it) {
     if (item >= a.items) return false;
     if (!a.s.cu) return lin_item(a.s, a.run, (int)item, it);
@@ -157,7 +153,6 @@ __device__ __forceinline__ bool conv_item(const Conv &a, long item, LinItem &it)
     it.nseg = it.len > a.run ? (it.len + a.run - 1) / a.run : 1;
     return it.p < it.nseg;
 }
-inline long conv_items(const Conv &a) { return a.s.cu ? a.total / a.run + a.s.nseq : lin_items(a.s.nseq, a.s.T, a.s.T, false, a.run); }
 
 // Warp = 32 V channels of one run.  The run that ends a sequence writes its next window (WINDOW_ONLY: nothing else).
 template <typename T, int V, int K, bool WINDOW_ONLY>
@@ -416,7 +411,7 @@ int pick_run(const Conv &a, int V, long rows, int ctas) {
 template <typename T, int V, int K> cudaError_t run_fwd(Conv a, cudaStream_t st) {
     const long rows = a.s.cu ? a.total : (long)a.s.nseq * a.s.T;
     a.run = pick_run(a, V, rows, sizeof(T) == 2 ? 4 : 3);
-    a.items = conv_items(a);
+    a.items = run_items(a.s, a.total, a.run);
     a.blocks = (a.C + 32 * V - 1) / (32 * V);
     const long ctas = (a.items + kWarps - 1) / kWarps * a.blocks;
     if (ctas > 0x7fffffffL) return cudaErrorInvalidValue;
@@ -430,7 +425,7 @@ template <typename T, int V, int K> cudaError_t run_fwd(Conv a, cudaStream_t st)
 template <typename T, int V, int K> cudaError_t run_bwd(Conv a, cudaStream_t st) {
     const long rows = a.s.cu ? a.total : (long)a.s.nseq * a.s.T;
     a.run = pick_run(a, V, rows, 2);
-    a.items = conv_items(a);
+    a.items = run_items(a.s, a.total, a.run);
     const unsigned cb = (a.C + 32 * V - 1) / (32 * V);
     const long want = (long)std::max(1, std::min(conv_parts(a.C, a.sms), 4 * a.sms / (int)cb));
     const unsigned parts = (unsigned)std::min((a.items + kWarps - 1) / kWarps, want);

@@ -24,6 +24,7 @@
 #include <algorithm>
 
 #include "linear_tc.cuh"
+#include "run_item.cuh"
 #include "ssm_internal.cuh"
 #include "ssm_math.cuh"
 
@@ -57,12 +58,7 @@ struct Bwd {
 };
 
 __device__ __forceinline__ bool chunk_item(const Bwd &w, long item, LinItem &it) {
-    if (!lin_item(w.a.s, kTile, (int)item, it)) return false;
-    if (w.a.s.cu) {
-        it.start = min(max(it.start, 0L), w.a.total);
-        it.len = (int)min((long)max(it.len, 0), w.a.total - it.start);
-    }
-    return true;
+    return run_item(w.a.s, w.a.total, kTile, item, it);
 }
 
 // Sums over GRP lanes (STRIDE apart) of CNT values each: a step sends one half and keeps the other, so that a lane ends with
@@ -299,26 +295,25 @@ template <int N> __global__ void __launch_bounds__(256) ssm_bwd_chain_kernel(con
     long first;
     int cnt;
     if (a.s.cu) {
-        __shared__ long s_first;
-        __shared__ int s_cnt;
-        if (threadIdx.x < 32) {
-            long before = 0;
-            int mine = 0;
-            for (int k = threadIdx.x; k <= n; k += 32) {
-                const int len = (int)min((long)a.s.cu[k + 1] - a.s.cu[k], a.total), c = len > kTile ? (len + kTile - 1) / kTile : 1;
-                if (k < n) before += c;
-                else mine = c;
-            }
+        const int start = min(max(a.s.cu[n], 0), (int)a.total), len = min(a.s.cu[n + 1], (int)a.total) - start;
+        cnt = len > kTile ? (len + kTile - 1) / kTile : 1;
+        if (a.s.nseq <= kCounted) {
+            __shared__ long s_first;
+            if (threadIdx.x < 32) {
+                long before = 0;
+                for (int k = threadIdx.x; k < n; k += 32) {
+                    const int len = (int)min((long)a.s.cu[k + 1] - a.s.cu[k], a.total);
+                    before += len > kTile ? (len + kTile - 1) / kTile : 1;
+                }
 #pragma unroll
-            for (int off = 16; off; off >>= 1) {
-                before += __shfl_xor_sync(0xffffffffu, before, off);
-                mine += __shfl_xor_sync(0xffffffffu, mine, off);
+                for (int off = 16; off; off >>= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
+                if (threadIdx.x == 0) s_first = before;
             }
-            if (threadIdx.x == 0) s_first = before, s_cnt = mine;
+            __syncthreads();
+            first = s_first;
+        } else {
+            first = first_of_many(a.s, a.total, kTile, n);
         }
-        __syncthreads();
-        first = s_first;
-        cnt = s_cnt;
         if (first >= w.chunks) return;
         cnt = (int)min((long)cnt, w.chunks - first);
     } else {
@@ -377,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_bwd_grad_kernel(const __grid_
     }
     for (long item = slot; item < w.chunks; item += w.slots) {
         LinItem it;
-        if (!chunk_item(w, item, it)) break;
+        if (!chunk_item(w, item, it)) continue;
         const int t0 = min(it.p * kTile, it.len);
         const At at{a.s.cu ? 0L : it.n, (a.s.cu ? it.start : 0L) + t0, min(kTile, it.len - t0)};
         if (at.len == 0) continue;
@@ -613,7 +608,7 @@ Plan plan(int nseq, long total, int max_len, bool varlen, int D, int G, int N, i
     Plan p{};
     const int CH = kWarps * 64 / (N / 4);
     p.rows = varlen ? total : (long)nseq * max_len;
-    p.chunks = lin_items(nseq, total, max_len, varlen, kTile);
+    p.chunks = varlen ? total / kTile + nseq : lin_items(nseq, max_len, max_len, false, kTile);      // as run_items
     p.cpg = D / G;
     p.bpg = (p.cpg + CH - 1) / CH;
     p.blocks = p.bpg * G;

@@ -32,6 +32,7 @@
 #include <algorithm>
 
 #include "linear_tc.cuh"
+#include "run_item.cuh"
 #include "ssm_internal.cuh"
 #include "ssm_math.cuh"
 
@@ -74,7 +75,7 @@ template <typename T, int L> struct Lay {
 struct Walk {
     Ssm a;
     int cpg, bpg, blocks;       // channels and CTAs of a group of heads, CTAs of all
-    int seg;                    // tokens of a segment
+    int seg;                    // tokens of a segment (of any number where nothing is split)
     int pairs;                  // every array can be read by two elements
     long items;
     float *local, *sums;        // [items, D, N], [items, D]; nullptr where nothing is split
@@ -87,13 +88,15 @@ struct Ctl {
     int fail;
 };
 
-// The segment `item`, with the rows a packed batch has (whatever its prefix array says, none outside them is touched).
+// The segment `item`; where nothing is split, the sequence.  (Whatever a prefix array says, no row outside the batch is touched.)
 __device__ __forceinline__ bool walk_item(const Walk &w, long item, LinItem &it) {
-    if (!lin_item(w.a.s, w.seg, (int)item, it)) return false;
-    if (w.a.s.cu) {
-        it.start = min(max(it.start, 0L), w.a.total);
-        it.len = (int)min((long)max(it.len, 0), w.a.total - it.start);
-    }
+    const LinSeqs &s = w.a.s;
+    if (w.local) return run_item(s, w.a.total, w.seg, item, it);
+    it.n = it.first = (int)item;
+    it.p = 0;
+    it.nseg = 1;
+    it.start = s.cu ? min(max((long)s.cu[it.n], 0L), w.a.total) : (long)it.n * s.T;
+    it.len = s.cu ? (int)max(min((long)s.cu[it.n + 1], w.a.total) - it.start, 0L) : s.T;
     return true;
 }
 
@@ -551,8 +554,8 @@ template <typename T, int L, bool VEC> cudaError_t launch(const Ssm &a, cudaStre
     const int max_len = a.s.cu ? a.max_len : a.s.T;
     w.seg = a.hT && a.hT == a.h0 ? 0 : pick_segment(a, rows, max_len, blocks_of<L>(a.D, a.G));
     const bool split = w.seg > 0;
-    if (!split) w.seg = std::max(max_len, 1);
-    w.items = lin_items(a.s.nseq, a.s.cu ? a.total : a.s.T, max_len, a.s.cu != nullptr, w.seg);
+    if (!split) w.seg = 0x7fffffff;
+    w.items = split ? run_items(a.s, a.total, w.seg) : a.s.nseq;
     // two groups to a CTA where one would leave blocks waiting for an SM
     constexpr bool two_groups = sizeof(T) == 2 && L > 2;      // what two groups hold has to fit
     const bool pair = two_groups && w.items * blocks_of<L>(a.D, a.G) > a.sms && w.cpg > Y::CH;

@@ -338,3 +338,100 @@ def test_totals_that_fp32_cannot_tell_apart_keep_their_order(kda):
     assert float(got[0][0, 2]) == float(got[0][0, 3])
     got = kda.beam_select(x, s.flip(1).contiguous(), 4)
     assert got[1].tolist() == [[0, 1, 0, 1]]
+
+
+# ------------------------------------------------------------------ packed batches of many sequences
+def _scan64(x, dt, A, B, C, h, skip, gate, bias, cu):
+    """Packed sequences in fp64, side by side: rows [total,..] of one group, h [N,D,S]; (y [total,D], the memories after)."""
+    import torch
+    lens = (cu[1:] - cu[:-1]).long()
+    y, places = [], []
+    for t in range(int(lens.max())):
+        live = torch.nonzero(lens > t)[:, 0]
+        r = cu[:-1].long()[live] + t
+        step = torch.nn.functional.softplus(dt[r] + bias, threshold=50.0)
+        new = torch.exp(step[..., None] * A) * h[live] + (step * x[r])[..., None] * B[r][:, None]
+        h = h.index_copy(0, live, new)
+        out = ((new * C[r][:, None]).sum(-1) + skip * x[r]) * gate[r] * torch.sigmoid(gate[r])
+        y.append(out)
+        places.append(r)
+    order = torch.cat(places).argsort()
+    return torch.cat(y)[order], h
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,most,D,S", [(512, 40, 24, 16), (513, 40, 24, 16), (1100, 9, 24, 16), (600, 300, 33, 8), (33000, 1, 24, 8),
+                                        (2000, 3, 700, 16)])
+def test_packed_batches_of_many_sequences(kda, dtype, N, most, D, S):
+    """A sequence or its part is found among any number of them: lengths from none on, multiples of a chunk and of a segment among
+    them, split into segments (no host copy, few channels) and not."""
+    import torch
+    lens = torch.randint(0, most + 1, (N,), generator=torch.Generator().manual_seed(N))
+    lens[::5] = lens[::5] // 32 * 32
+    lens[1::7] = 0
+    lens[3] = min(128, 32 * most)
+    lens[-1] = 0
+    cu = torch.cat([lens.new_zeros(1), lens.cumsum(0)]).int()
+    cud, total, T = cu.cuda(), int(cu[-1]), int(lens.max())
+    a, kw, h0, dy, dh = _inputs(dtype, 1, total, D, 1, S, seqs=N)
+    leaf = dict(dx=a["x"][0], ddt=a["dt"][0], dA=a["A"], dB=a["B"][0, :, 0], dC=a["C"][0, :, 0], dh0=h0, dskip=kw["skip"], dgate=kw["gate"][0],
+                ddt_bias=kw["dt_bias"])
+    leaf = {k: v.double().requires_grad_(True) for k, v in leaf.items()}
+    wy, wh = _scan64(*leaf.values(), cud)
+    for host in (None, cu):
+        y, h = kda.ssm_varlen_fwd(*a.values(), cud, h0, cu_seqlens_cpu=host, **kw)
+        _check_rows("y", y[0], to_np(wy.detach()), dtype, tight(T))
+        _check32("h", h, to_np(wh.detach()), tight(T))
+    got = kda.ssm_chunk_bwd(dy, *a.values(), h0, dh, cu_seqlens=cud, **kw)
+    want = torch.autograd.grad([wy, wh], list(leaf.values()), [dy[0].double(), dh.double()])
+    assert set(got) == set(leaf)
+    for k, v in zip(leaf, want):
+        if k in ROWS:
+            _check_rows(k, got[k].reshape(v.shape), to_np(v), dtype, 2 * tight(T))
+        else:
+            _check32(k, got[k], to_np(v), 2 * tight(T))
+
+
+@gpu
+def test_packed_batch_of_a_chunks_rows(kda):
+    """32 rows of 600 sequences: the empty ones behind them have their chunks too."""
+    import torch
+    cu = torch.full((601,), 32, dtype=torch.int32, device="cuda")
+    cu[0] = 0
+    a, kw, h0, dy, dh = _inputs("f32", 1, 32, 24, 1, 16, seqs=600)
+    _, h = kda.ssm_varlen_fwd(*a.values(), cu, h0, **kw)
+    assert torch.equal(h[1:], h0[1:])
+    one = kda.ssm_chunk_bwd(dy, *a.values(), h0[:1], dh[:1], **kw)
+    got = kda.ssm_chunk_bwd(dy, *a.values(), h0, dh, cu_seqlens=cu, **kw)
+    assert torch.equal(got["dh0"][1:], dh[1:]) and torch.equal(got["dh0"][:1], one["dh0"])
+    assert torch.equal(got["dx"], one["dx"]) and torch.equal(got["dB"], one["dB"])
+
+
+@gpu
+def test_many_short_sequences_cost_what_their_tokens_do(kda):
+    """A token for each of 40,000 sequences: packed it is the work of a batch of that many, gradients too (counting all the sequences
+    before one's own, for each of them, takes some fifty times as long; four are allowed)."""
+    import torch
+    N = 40000
+    a, kw, _, dy, _ = _inputs("bf16", N, 1, 128, 1, 16, h0=False)
+    p = {k: (v if k == "A" else v.transpose(0, 1)) for k, v in a.items()}
+    pw = dict(kw, gate=kw["gate"].transpose(0, 1))
+    cu = torch.arange(N + 1, dtype=torch.int32, device="cuda")
+    calls = [(lambda: kda.ssm_varlen_fwd(*p.values(), cu, **pw), lambda: kda.ssm_chunk_fwd(*a.values(), **kw)),
+             (lambda: kda.ssm_chunk_bwd(dy.transpose(0, 1), *p.values(), cu_seqlens=cu, **pw), lambda: kda.ssm_chunk_bwd(dy, *a.values(), **kw))]
+
+    def ms(call):
+        call()
+        ev = [torch.cuda.Event(enable_timing=True) for _ in range(5)]
+        for e in ev:
+            e.record()
+            call()
+        torch.cuda.synchronize()
+        return min(a.elapsed_time(b) for a, b in zip(ev, ev[1:]))
+    for packed, batch in calls:
+        t = ms(packed), ms(batch)
+        assert t[0] <= 4 * t[1], t
+    y, h = calls[0][0]()
+    wy, wh = calls[0][1]()
+    assert torch.equal(y[0], wy[:, 0]) and torch.equal(h, wh)
