@@ -5,8 +5,9 @@
 // two chunks of 512 and adds up exp(x - M) against the running maximum M of its chunks.  An element among the k best lies in one of the k
 // chunks that come first when chunks are ordered by (maximum, position): every chunk before its own holds an element that
 // comes before it.  So the second kernel, a CTA per request, orders the chunks' maxima and looks at k chunks only.
-// Totals are formed and compared as pairs of fp32, 48 bits (candidates of different beams may be closer than an fp32 total's
-// rounding); sums of exp are fp32 over a warp's terms and 64-bit from there on.
+// Totals are compared as pairs of fp32, 48 bits: tokens of a beam, and of beams with equal rows, may be closer than an fp32 total's
+// rounding.  Sums of exp are fp32 over a warp's terms (approximate exp2 of exponents rounded to fp32) and 64-bit from there on:
+// lse is good to some 3e-7 (131,072 normal logits), so far are other beams told apart.
 //
 // Measured: 64 requests of 8 beams over 131,072 bf16 logits 23 us (134 MB, 19.8 us at the copy rate) and 15 us for the second kernel, whose
 // small steps wait for one another; 35 us together.

@@ -13,9 +13,9 @@
 // sums are fp32 and rounded once.  The weights' gradients stay in registers over all runs of a lane, are added up over a
 // CTA's warps in shared memory and over the CTAs by a second kernel, in a fixed order.
 //
-// Measured, bf16: forwards 15 us at that shape (67 MB, 9.9 us at the copy rate; 66 instructions a row and warp are
-// the other bound), 16 packed prompts of 40,000 tokens in all and 2048 channels 61 us, 5.3 TB/s; gradients 31 us (101 MB, 14.9 us; 128
-// registers, 16 warps an SM), the second kernel among it.
+// Measured, bf16: forwards 15 us at that shape (67 MB, 9.9 us at the copy rate; 66 instructions a row and warp take 0.57 of the
+// issue slots, and warps wait for their loads), 16 packed prompts of 40,000 tokens in all and 2048 channels 61 to 64 us, 5.3 to
+// 5.1 TB/s; gradients 31 us (101 MB, 14.9 us; 128 registers, 16 warps an SM), the second kernel among it; in fp32 44 us (29.7).
 #include <algorithm>
 
 #include "conv_internal.cuh"

@@ -612,7 +612,8 @@ kda_status kda_conv_bwd(const void *d_y, const void *x, const float *weight, con
  *   ws      at least the query's bytes, 16-byte aligned; a kernel's bounded wait that runs out is recorded
  *           in its header (kda_query_device_error).
  * Memories, their sums and exp are fp32 whatever the type.  An infinite or NaN x, dt or gate stays in its
- * channel; an infinite or NaN B_in or C_in reaches all channels of its group from its token on.
+ * channel; an infinite or NaN B_in reaches all channels of its group from its token on, a C_in those of its
+ * token.
  * B, nseq, T == 0 are allowed; without a sequence nothing is touched, the header included.  At most 65535
  * sequences.
  */
@@ -660,14 +661,16 @@ kda_status kda_ssm_chunk_bwd(const void *d_y, const void *x, const void *dt, con
  * Beam search: the k best continuations of each request's W beams,
  *     total[w, v] = scores[w] + logits[w, v] - log sum_v' exp(logits[w, v']),
  * in order, equal totals by the lowest w V + v: out_scores [B,k] float32, parents and tokens [B,k] int32
- * (token v of beam parent).  Totals are formed and compared with 48 bits and rounded once.
+ * (token v of beam parent).  The logarithm of the sum is good to some 3e-7 (sums of exp in fp32) and the same
+ * for equal rows of a call; its last bits depend on B W.  Totals are formed from it, compared with 48 bits and
+ * rounded once: tokens of a beam, and beams with equal rows, are told apart that far, other beams to 3e-7.
  *
  *   logits   [B,W,V], KDA_F32 or KDA_BF16, contiguous or with two element strides (request, beam).
  *   scores   [B,W] float32; -inf: a beam that does not count (on the first step, all but one).
  *   finished [B,W] bytes or NULL: a nonzero beam has the one candidate `eos`, with its score as it is.
  * W <= 128, k <= 32, k <= W V.  A beam whose logits hold NaN or +inf, or nothing but -inf, has no
- * distribution: its candidates count as -inf.  out_scores may be scores (k == W).  ws: at least the
- * query's bytes, 16-byte aligned.
+ * distribution: its candidates count as -inf, as those of a beam do whose score is NaN, or +inf and not
+ * finished.  out_scores may be scores (k == W).  ws: at least the query's bytes, 16-byte aligned.
  */
 size_t kda_beam_select_workspace(int B, int W, int V, kda_dtype dtype);
 kda_status kda_beam_select(const void *logits, const long long *strides, const float *scores,

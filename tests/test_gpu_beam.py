@@ -230,3 +230,17 @@ def test_many_beams_that_do_not_count(kda, V):
     s[0] = float("-inf")
     s[1, 5:] = float("-inf")
     _compare(kda, x, s, 32)
+
+
+def test_scores_without_a_value(kda):
+    """A beam whose score is NaN, or +inf and not finished, has no candidates; a finished one keeps +inf."""
+    import torch
+    x, _ = _logits(1, 4, 700, "f32")
+    s = torch.tensor([[float("nan"), -1.0, float("inf"), -2.0]], device="cuda")
+    got = kda.beam_select(x, s, 8)
+    assert set(got[1][0].tolist()) <= {1, 3} and bool(torch.isfinite(got[0]).all())
+    want = kda.beam_select(x[:, 1::2].contiguous(), s[:, 1::2].contiguous(), 8)
+    assert torch.equal(got[1], 2 * want[1] + 1) and torch.equal(got[2], want[2])
+    f = torch.tensor([[True, False, True, False]], device="cuda")
+    got = kda.beam_select(x, s, 4, finished=f, eos=9)
+    assert float(got[0][0, 0]) == float("inf") and int(got[1][0, 0]) == 2 and int(got[2][0, 0]) == 9 and 0 not in got[1][0].tolist()
